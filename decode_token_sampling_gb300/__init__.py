@@ -5,14 +5,19 @@ The work runs in hand-written sm_103a CUDA kernels behind the C ABI declared in
 include/kps.h (libkps.so, built in-tree).  This module only marshals torch
 tensors into that ABI; there is no fallback of any kind: if the library is
 missing or the tensors are not on a CUDA device, calls raise.
+
+Beside the step: top_logits (a row's top logits and log-sum-exps, for
+log-probabilities and for teachers) and distill_loss, distill_loss_grad (the
+distillation loss of a student against a teacher's top logits).
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -72,6 +77,14 @@ def load_library() -> ctypes.CDLL:
     lib.kps_last_launch_count.argtypes = []
     lib.kps_last_cluster_size.restype = I32
     lib.kps_last_cluster_size.argtypes = []
+    lib.kps_top_logits.restype = I32
+    lib.kps_top_logits.argtypes = [P, I32, I64, I64, I64, I64, F32, P, P, P, P, P, P, P]
+    lib.kps_distill_forward.restype = I32
+    lib.kps_distill_forward.argtypes = [P, I32, I64, I64, I64, P, P, I32, I64, P, P, F32, P, P, P]
+    lib.kps_distill_backward.restype = I32
+    lib.kps_distill_backward.argtypes = [P, I32, I64, I64, I64, P, P, I32, I64, P, P, F32, P, P, P, I64, P]
+    lib.kps_distill_loss_grad.restype = I32
+    lib.kps_distill_loss_grad.argtypes = [P, I32, I64, I64, I64, P, P, I32, I64, P, P, F32, P, P, I64, P]
     lib.kps_query_launch.restype = I32
     lib.kps_query_launch.argtypes = [I64, I64, I32, ctypes.POINTER(I32), ctypes.POINTER(I64),
                                      ctypes.POINTER(ctypes.c_size_t)]
@@ -270,3 +283,198 @@ def last_device_status(workspace: torch.Tensor, stream: Optional[torch.cuda.Stre
     if st != 0:
         raise KpsError(st, "kps_last_device_status")
     return out.value
+
+
+# ---- rows of logits beside the sampling step --------------------------------------------------
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    """Checks a [rows, V] matrix of logits and returns the elements between its rows' starts."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, V]")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    N, V = t.shape
+    if V < 1:
+        raise ValueError(f"{name} has no columns")
+    if V > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows (stride 1 along the vocabulary)")
+    if N < 2:
+        return V
+    if t.stride(0) < V:
+        raise ValueError(f"{name} has overlapping rows (row stride {t.stride(0)}, {V} columns)")
+    return t.stride(0)
+
+
+@contextlib.contextmanager
+def _queued_on(device: torch.device, stream: Optional[torch.cuda.Stream], *inputs: Optional[torch.Tensor]):
+    """Makes `device` and `stream` current (so that outputs are allocated for that stream) and keeps
+    the inputs' memory from reuse before the stream is done with it; yields the stream's handle."""
+    with contextlib.ExitStack() as stack:
+        if device.index is not None and device.index != torch.cuda.current_device():
+            stack.enter_context(torch.cuda.device(device))
+        current = torch.cuda.current_stream(device)
+        if stream is not None and stream != current:
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the logits on {device}")
+            stack.enter_context(torch.cuda.stream(stream))
+            for t in inputs:
+                if t is not None:
+                    t.record_stream(stream)
+            current = stream
+        yield ctypes.c_void_p(current.cuda_stream)
+
+
+class TopLogits(NamedTuple):
+    """What top_logits returns (kps_top_logits in include/kps.h)."""
+    ids: torch.Tensor  # int32 [B, n]
+    values: torch.Tensor  # float32 [B, n]
+    lse: torch.Tensor  # float32 [B]
+    rest: torch.Tensor  # float32 [B]
+    logprob: Optional[torch.Tensor]  # float32 [B], with tokens
+
+
+def top_logits(logits: torch.Tensor, n: int, *, temperature: float = 1.0, tokens: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> TopLogits:
+    """The top n logits of every row (value descending, lower index first among equals) with the
+    row's log-sum-exp at `temperature`, that of everything outside the top n and, for tokens
+    (int64 [B]), their log-probabilities (asynchronous on `stream`).
+
+    values - lse[:, None] are log-probabilities at temperature 1 (values are the raw logits);
+    (ids, values, rest) is what distill_loss takes of a teacher.  Rows may lie apart
+    (logits.stride(0) >= V).
+    """
+    lib = load_library()
+    ld = _rows(logits, "logits")
+    dt = _dtype_code(logits)
+    B, V = logits.shape
+    dev = logits.device
+    n = int(n)
+    if not 0 <= n <= min(V, 1024):
+        raise ValueError(f"n must be in 0..min(V, 1024), got {n}")
+    if tokens is not None:
+        _check(tokens, "tokens", torch.int64, (B,), dev)
+    with _queued_on(dev, stream, logits, tokens) as handle:
+        ids = torch.empty(B, n, dtype=torch.int32, device=dev)
+        values = torch.empty(B, n, dtype=torch.float32, device=dev)
+        sums = torch.empty(3, B, dtype=torch.float32, device=dev)
+        lse, rest, logprob = sums.unbind(0)
+        st = lib.kps_top_logits(_ptr(logits), dt, B, V, ld, n, float(temperature), _ptr(tokens), _ptr(ids),
+                                _ptr(values), _ptr(lse), _ptr(rest), None if tokens is None else _ptr(logprob), handle)
+    if st != 0:
+        raise KpsError(st, "kps_top_logits")
+    return TopLogits(ids, values, lse, rest, None if tokens is None else logprob)
+
+
+def _distill_args(student, ids, values, rest, weight, temperature):
+    """Checks the arguments the distillation calls share; returns the leading ABI arguments."""
+    ld = _rows(student, "student")
+    dt = _dtype_code(student)
+    N, V = student.shape
+    if ids.dim() != 2 or ids.shape[0] != N or not 1 <= ids.shape[1] <= 1024:
+        raise ValueError(f"ids must be [{N}, K] with K in 1..1024, got {tuple(ids.shape)}")
+    K = ids.shape[1]
+    _check(ids, "ids", torch.int32, (N, K), student.device)
+    if values.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"values must be float32 or bfloat16, got {values.dtype}")
+    _check(values, "values", values.dtype, (N, K), student.device)
+    _check(rest, "rest", torch.float32, (N,), student.device)
+    _check(weight, "weight", torch.float32, (N,), student.device)
+    return (_ptr(student), dt, N, V, ld, _ptr(ids), _ptr(values), _dtype_code(values), K, _ptr(rest), _ptr(weight),
+            float(temperature))
+
+
+def _grad_like(student: torch.Tensor) -> torch.Tensor:
+    """An uninitialised gradient whose rows lie on the same 16-byte phase as the student's."""
+    N, V = student.shape
+    ld = student.stride(0) if N > 1 else V
+    return torch.empty(N, ld, dtype=student.dtype, device=student.device)[:, :V]
+
+
+def distill_forward(student: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, *, temperature: float = 1.0,
+                    rest: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The distillation loss of every row and the statistics [N, 4] that distill_backward takes
+    (kps_distill_forward in include/kps.h); no autograd."""
+    lib = load_library()
+    args = _distill_args(student, ids, values, rest, weight, temperature)
+    N, dev = student.shape[0], student.device
+    with _queued_on(dev, stream, student, ids, values, rest, weight) as handle:
+        loss = torch.empty(N, dtype=torch.float32, device=dev)
+        stats = torch.empty(N, 4, dtype=torch.float32, device=dev)
+        st = lib.kps_distill_forward(*args, _ptr(loss), _ptr(stats), handle)
+    if st != 0:
+        raise KpsError(st, "kps_distill_forward")
+    return loss, stats
+
+
+def distill_backward(grad_loss: Optional[torch.Tensor], student: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
+                     stats: torch.Tensor, *, temperature: float = 1.0, rest: Optional[torch.Tensor] = None,
+                     weight: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The gradient of the student's logits, in their type, for the rows' upstream gradients
+    grad_loss (float32 [N], None: 1) and the statistics of distill_forward on the same arguments."""
+    lib = load_library()
+    args = _distill_args(student, ids, values, rest, weight, temperature)
+    N, dev = student.shape[0], student.device
+    _check(grad_loss, "grad_loss", torch.float32, (N,), dev)
+    _check(stats, "stats", torch.float32, (N, 4), dev)
+    with _queued_on(dev, stream, student, ids, values, rest, weight, grad_loss, stats) as handle:
+        grad = _grad_like(student)
+        st = lib.kps_distill_backward(*args, _ptr(grad_loss), _ptr(stats), _ptr(grad), grad.stride(0), handle)
+    if st != 0:
+        raise KpsError(st, "kps_distill_backward")
+    return grad
+
+
+def distill_loss_grad(student: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, *, temperature: float = 1.0,
+                      rest: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The distillation loss of every row and its gradient in one launch (kps_distill_loss_grad in
+    include/kps.h): for training loops that know every factor of the loss, given in `weight`.  No
+    autograd; it may be captured into a CUDA graph."""
+    lib = load_library()
+    args = _distill_args(student, ids, values, rest, weight, temperature)
+    N, dev = student.shape[0], student.device
+    with _queued_on(dev, stream, student, ids, values, rest, weight) as handle:
+        loss = torch.empty(N, dtype=torch.float32, device=dev)
+        grad = _grad_like(student)
+        st = lib.kps_distill_loss_grad(*args, _ptr(loss), _ptr(grad), grad.stride(0), handle)
+    if st != 0:
+        raise KpsError(st, "kps_distill_loss_grad")
+    return loss, grad
+
+
+class _DistillLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, student, ids, values, rest, weight, temperature):
+        loss, stats = distill_forward(student, ids, values, temperature=temperature, rest=rest, weight=weight)
+        ctx.save_for_backward(student, ids, values, rest, weight, stats)
+        ctx.temperature = temperature
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_loss):
+        student, ids, values, rest, weight, stats = ctx.saved_tensors
+        grad = distill_backward(grad_loss.contiguous(), student, ids, values, stats, temperature=ctx.temperature,
+                                rest=rest, weight=weight)
+        return grad, None, None, None, None, None
+
+
+def distill_loss(student: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, *, temperature: float = 1.0,
+                 rest: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The distillation loss of every row of the student's logits [N, V] against a teacher's top
+    logits, float32 [N], differentiable with respect to the student (include/kps.h has the formula).
+
+    ids, values: the teacher's slots [N, K], int32 and float32 or bfloat16 (an id outside [0, V) or
+    a value of -inf: an empty slot); rest: float32 [N], the log-sum-exp of what the list leaves out
+    at the same temperature (None: nothing); weight: float32 [N] (None: 1; rows of weight 0 are not
+    read).  The teacher's side and the weights get no gradient: tensors of theirs that require one
+    are refused.  Runs on the current stream.
+    """
+    for name, t in (("values", values), ("rest", rest), ("weight", weight)):
+        if t is not None and t.requires_grad:
+            raise ValueError(f"{name} requires a gradient, but distill_loss has one for the student only")
+    if not (torch.is_grad_enabled() and student.requires_grad):
+        return distill_forward(student, ids, values, temperature=temperature, rest=rest, weight=weight)[0]
+    return _DistillLoss.apply(student, ids, values, rest, weight, temperature)

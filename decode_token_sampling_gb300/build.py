@@ -1,8 +1,9 @@
 """Builds the in-tree CUDA library libkps.so for GB300 (sm_103a) with nvcc.
 
-One translation unit, one -gencode, compiled in seconds; the product is
-decode_token_sampling_gb300/libkps.so (git-ignored).  No torch extension
-machinery is involved: the library exports a plain C ABI (include/kps.h).
+One -gencode, the translation units compiled in parallel and linked, in under a
+minute; the product is decode_token_sampling_gb300/libkps.so (git-ignored).  No
+torch extension machinery is involved: the library exports a plain C ABI
+(include/kps.h).
 """
 
 from __future__ import annotations
@@ -13,14 +14,15 @@ import subprocess
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "kps.cu")
+SRCS = [os.path.join(PKG, "csrc", f) for f in ("kps.cu", "kps_top.cu", "kps_distill.cu")]
+SRC = SRCS[0]
 HDR = os.path.join(ROOT, "include", "kps.h")
 LIB = os.path.join(PKG, "libkps.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
     "--expt-relaxed-constexpr",
 ]
 
@@ -41,10 +43,24 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     if not force and os.path.exists(out) and all(os.path.getmtime(out) >= os.path.getmtime(s) for s in srcs):
         return out
     tmp = out + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, *(extra_flags or []), "-I", os.path.join(ROOT, "include"), "-o", tmp, SRC]
+    objs = [f"{tmp}.{i}.o" for i in range(len(SRCS))]
+    flags = [nvcc(), *NVCC_FLAGS]
+    cmds = [[*flags, *(extra_flags or []), "-I", os.path.join(ROOT, "include"), "-c", "-o", obj, src]
+            for obj, src in zip(objs, SRCS)]
+    link = [*flags, "-shared", "-o", tmp, *objs]
     if verbose:
-        print(" ".join(cmd))
-    subprocess.check_call(cmd)
+        print("\n".join(" ".join(c) for c in [*cmds, link]))
+    try:
+        jobs = [subprocess.Popen(c) for c in cmds]
+        codes = [job.wait() for job in jobs]
+        for code, c in zip(codes, cmds):
+            if code != 0:
+                raise subprocess.CalledProcessError(code, c)
+        subprocess.check_call(link)
+    finally:
+        for obj in objs:
+            if os.path.exists(obj):
+                os.remove(obj)
     os.replace(tmp, out)
     return out
 

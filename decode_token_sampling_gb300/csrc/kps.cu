@@ -55,11 +55,11 @@
 #include "kps_fixed.h"
 #include "kps_div.h"
 #include "kps_weights.cuh"
+#include "kps_host.h"
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cooperative_groups.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <climits>
 #include <cmath>
@@ -2115,17 +2115,6 @@ static kps_status lookup_shape(kps_dtype dt, int64_t V, CachedShape* out) {
   return KPS_OK;
 }
 
-}  // namespace kps
-
-namespace kps {
-// An NVTX range around each public sampling call: it names the call in a profiler's timeline
-// (Nsight Systems, ncu's NVTX filters) and costs a pointer check when no tool is attached.
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
 }  // namespace kps
 
 // ------------------------------------------------------------------------------------------

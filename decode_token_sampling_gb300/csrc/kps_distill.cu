@@ -1,0 +1,601 @@
+// kps_distill.cu — the distillation loss of a student's rows of logits against the top logits
+// of a teacher, and its gradient.
+//
+// Per row, with tau the temperature, (id_k, t_k) the teacher's slots and, optionally, r the
+// log-sum-exp of everything the teacher's list leaves out:
+//
+//   p   = softmax([t_k / tau ..., r])                        over the valid slots and the rest
+//   L   = ln sum_v exp(s_v / tau)                            over the student's whole row
+//   R   = ln sum_{v not in the list} exp(s_v / tau)
+//   loss = w tau^2 (sum_k p_k (ln p_k - s_{id_k} / tau + L) + p_r (ln p_r - R + L))
+//   d loss / d s_v = w tau (exp(s_v / tau - L) - sum_{k: id_k = v} p_k)        v in the list
+//                    w tau (exp(s_v / tau - L) - p_r exp(s_v / tau - R))       else
+//
+// The work is one pass over the student's row for the loss (V elements read) and one more for
+// the gradient (V read, V written): both are bound by memory.  Every exponential is taken of a
+// difference to a reference logit, and the loss is assembled from quantities relative to the
+// largest student logit among the list's tokens and to the teacher's largest value, so nothing
+// of the size of L itself is ever subtracted.
+
+#include "kps.h"
+#include "kps_host.h"
+#include "kps_stream.cuh"
+
+#include <cooperative_groups.h>
+
+#include <climits>
+#include <cmath>
+
+namespace cg = cooperative_groups;
+
+namespace kps {
+namespace distill {
+
+using namespace stream;
+
+constexpr int kNT = 256;  // threads per CTA
+constexpr int kNW = kNT / 32;
+constexpr int kU = 4;         // 16-byte loads each thread keeps in flight
+constexpr int kMaxK = 1024;   // teacher slots a row may have (the framework's top-k limit)
+constexpr int64_t kMaxV = 1 << 20;
+constexpr int kMaxCS = 8;     // widest cluster (the portable limit)
+constexpr int kStats = 4;     // floats of statistics per row
+
+enum Mode { kForward = 0, kBackward = 1, kBoth = 2 };
+
+struct Params {
+  const void* student;
+  int64_t N, ld;
+  int V, K;
+  const int32_t* ids;
+  const void* values;
+  int values_bf16;
+  const float* rest;     // or nullptr
+  const float* weight;   // or nullptr: 1
+  float tau, c;          // c = log2(e) / tau
+  const float* upstream; // gradient modes: the loss's gradient per row, or nullptr: 1
+  float* loss;           // [N] (kForward, kBoth)
+  float* stats;          // [N, kStats]: written by kForward (may be nullptr), read by kBackward
+  void* grad;
+  int64_t ld_grad;
+};
+
+// Shared memory: the teacher's slots, the exchange slots, the hash table of the list's ids
+// (gradient modes) and the bitmap of the list's tokens in this CTA's part of the row (rest).
+struct Layout {
+  size_t id, e, v, hash, bits, total;
+  int hash_size;
+};
+__host__ __device__ inline Layout make_layout(int K, int64_t chunk, bool grad, bool rest) {
+  Layout L;
+  size_t off = 0;
+  const size_t k4 = (static_cast<size_t>(K) * 4 + 15) / 16 * 16;
+  L.id = off; off += k4;
+  L.e = off;  off += k4;
+  L.v = off;  off += k4;
+  L.hash_size = 32;
+  while (L.hash_size < 2 * K) L.hash_size *= 2;
+  L.hash = off;
+  if (grad) off += static_cast<size_t>(L.hash_size) * 4;
+  L.bits = off;
+  if (rest) off += (static_cast<size_t>(chunk) + 31) / 32 * 4 / 16 * 16 + 32;
+  L.total = off;
+  return L;
+}
+
+// Block reductions over kNT threads; every thread gets the result.
+__device__ __forceinline__ void block_max2(float& a, float& b, float (*red)[2]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  a = warp_max(a);
+  b = warp_max(b);
+  __syncthreads();
+  if (lane == 0) {
+    red[warp][0] = a;
+    red[warp][1] = b;
+  }
+  __syncthreads();
+  a = warp_max(red[lane & (kNW - 1)][0]);
+  b = warp_max(red[lane & (kNW - 1)][1]);
+}
+__device__ __forceinline__ void block_sum2(float& a, float& b, float (*red)[2]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  a = warp_sum(a);
+  b = warp_sum(b);
+  __syncthreads();
+  if (lane == 0) {
+    red[warp][0] = a;
+    red[warp][1] = b;
+  }
+  __syncthreads();
+  a = warp_sum(lane < kNW ? red[lane][0] : 0.0f);
+  b = warp_sum(lane < kNW ? red[lane][1] : 0.0f);
+}
+__device__ __forceinline__ Sum2 block_merge(Sum2 v, float c, float (*red)[2]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = warp_merge(v, c);
+  __syncthreads();
+  if (lane == 0) {
+    red[warp][0] = v.ref;
+    red[warp][1] = v.s;
+  }
+  __syncthreads();
+  v.ref = red[lane & (kNW - 1)][0];
+  v.s = lane < kNW ? red[lane][1] : 0.0f;
+  return warp_merge(v, c);
+}
+
+__device__ __forceinline__ void add_one(Sum2& sum, float x, float c) {
+  if (x > sum.ref + kRaise / c) sum.raise(clamp_ref(x), c);
+  sum.s += ex2((x - sum.ref) * c);
+}
+
+// log2(1 + 2^z).
+__device__ __forceinline__ float log2_1p_ex2(float z) { return z > 24.0f ? z : kLog2e * log1pf(ex2(z)); }
+
+template <bool kBF16, bool kRest, int kMode>
+__global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
+  constexpr int G = kBF16 ? 8 : 4;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float red[kNW][2];
+  __shared__ float part[2 * kMaxCS][2];  // the partial sums of the cluster's CTAs (list, rest)
+  const int CS = static_cast<int>(cg::this_cluster().num_blocks());
+  const int rank = static_cast<int>(cg::this_cluster().block_rank());
+  const int64_t row = blockIdx.x / CS;
+  // every CTA of the cluster runs before any writes into another's shared memory
+  constexpr bool kShare = kMode != kBackward;  // the cluster's CTAs exchange their partial sums
+  if (kShare && CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  const int V = P.V, K = P.K;
+  const float c = P.c;
+
+  const RowView<kBF16> x(P.student, row * P.ld, V);
+  const int g0 = static_cast<int>(static_cast<int64_t>(x.nv) * rank / CS);
+  const int g1 = static_cast<int>(static_cast<int64_t>(x.nv) * (rank + 1) / CS);
+  const Layout lay = make_layout(K, (V + CS - 1) / CS + 4 * G, kMode != kForward, kRest);
+  int32_t* s_id = reinterpret_cast<int32_t*>(smem + lay.id);
+  float* s_e = reinterpret_cast<float*>(smem + lay.e);
+  float* s_v = reinterpret_cast<float*>(smem + lay.v);
+  int32_t* s_hash = reinterpret_cast<int32_t*>(smem + lay.hash);
+  uint32_t* s_bits = reinterpret_cast<uint32_t*>(smem + lay.bits);
+  // bit of element v: its distance from the first element of vector g0, plus G (the head's
+  // elements come before the first vector)
+  const int bit0 = x.head + g0 * G - G;
+  const int nbits = (g1 - g0 + 3) * G;
+
+  const float w = P.weight ? P.weight[row] : 1.0f;
+  float scale = w;  // of the gradient
+  if (kMode != kForward && P.upstream) scale *= P.upstream[row];
+  scale *= P.tau;
+
+  // ---- the teacher's slots ------------------------------------------------------------
+  float tmax = -INFINITY, smax = -INFINITY;
+  bool any = false;
+  if (w != 0.0f) {
+    if (kRest && kMode != kBackward)
+      for (int i = threadIdx.x; i < (nbits + 31) / 32; i += kNT) s_bits[i] = 0u;
+    if (kMode != kForward)
+      for (int i = threadIdx.x; i < lay.hash_size; i += kNT) s_hash[i] = -1;
+    for (int k = threadIdx.x; k < K; k += kNT) {
+      int32_t id = P.ids[row * K + k];
+      const float t = P.values_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(P.values)[row * K + k])
+                                    : static_cast<const float*>(P.values)[row * K + k];
+      float s = 0.0f;
+      if (id < 0 || id >= V || t == -INFINITY) {
+        id = -1;
+      } else {
+        s = x.at(id);
+        any = true;
+        tmax = fmaxf(tmax, t);
+        smax = fmaxf(smax, s);
+      }
+      s_id[k] = id;
+      s_e[k] = t;
+      s_v[k] = s;
+    }
+  }
+  any = __syncthreads_or(any);
+  if (kShare && CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  const bool dead = !any || (kMode == kBackward && scale == 0.0f);
+  if (dead) {  // no loss: zeros, and the student's row is not looked at (the same in every CTA of the row)
+    if (rank == 0 && threadIdx.x == 0) {
+      if (kMode != kBackward) P.loss[row] = 0.0f;
+      if (kMode == kForward && P.stats)
+        for (int i = 0; i < kStats; ++i) P.stats[row * kStats + i] = 0.0f;
+    }
+    if (kMode != kForward) {
+      const RowView<kBF16> o(P.grad, row * P.ld_grad, V);
+      const int o0 = static_cast<int>(static_cast<int64_t>(o.nv) * rank / CS);
+      const int o1 = static_cast<int>(static_cast<int64_t>(o.nv) * (rank + 1) / CS);
+      uint4* ov = const_cast<uint4*>(o.vec);
+      for (int g = o0 + static_cast<int>(threadIdx.x); g < o1; g += kNT) __stcs(ov + g, make_uint4(0u, 0u, 0u, 0u));
+      if (rank == 0 && static_cast<int>(threadIdx.x) < o.loose()) {
+        const int v = o.loose_at(threadIdx.x);
+        if (kBF16) reinterpret_cast<__nv_bfloat16*>(const_cast<unsigned char*>(o.base))[v] = __float2bfloat16(0.0f);
+        else reinterpret_cast<float*>(const_cast<unsigned char*>(o.base))[v] = 0.0f;
+      }
+    }
+    return;
+  }
+  block_max2(tmax, smax, red);
+  // the teacher's reference: its largest class, the rest (in nats at tau) included
+  const float r = kRest ? P.rest[row] : -INFINITY;
+  const float tref = clamp_ref(fmaxf(tmax, r * P.tau));
+  // the student's sums: over the whole row, and over the tokens outside the list
+  Sum2 all, rest;
+  if (kMode == kBackward) {
+    all = Sum2{P.stats[row * kStats], P.stats[row * kStats + 1]};
+    rest = Sum2{P.stats[row * kStats + 2], P.stats[row * kStats + 3]};
+  }
+  const float ref = kMode == kBackward ? all.ref : clamp_ref(smax);
+  // e_k = 2^(u_k), u_k = (t_k - tref) c; v_k = (s_k - ref) c; E = sum e_k, W = sum e_k (u_k - v_k)
+  float E = 0.0f, W = 0.0f;
+  bool twice = false;
+  for (int k = threadIdx.x; k < K; k += kNT) {
+    const int32_t id = s_id[k];
+    float e = 0.0f, v = 0.0f;
+    if (id >= 0) {
+      const float u = (s_e[k] - tref) * c;
+      v = (s_v[k] - ref) * c;
+      e = ex2(u);
+      E += e;
+      if (e != 0.0f) W += e * (u - v);  // NaN stays (e is NaN then)
+      if (kRest && kMode != kBackward) {
+        const int b = id - bit0;
+        if (b >= 0 && b < nbits) atomicOr(&s_bits[b >> 5], 1u << (b & 31));
+      }
+      if (kMode != kForward) {
+        // the list's distinct ids: a second slot of the same token marks the row
+        uint32_t h = (static_cast<uint32_t>(id) * 2654435761u) & (lay.hash_size - 1);
+        for (;;) {
+          const int32_t old = atomicCAS(&s_hash[h], -1, id);
+          if (old == -1) break;
+          if (old == id) {
+            twice = true;
+            break;
+          }
+          h = (h + 1) & (lay.hash_size - 1);  // at most K of the 2K places are taken
+        }
+      }
+    }
+    s_e[k] = e;
+    s_v[k] = v;
+  }
+  block_sum2(E, W, red);  // its barriers also publish the bitmap and the slots
+  const float ur = (r * P.tau - tref) * c;
+  const float er = kRest ? ex2(ur) : 0.0f;  // the rest class (0 when there is none)
+
+  // ---- the student's sums -------------------------------------------------------------
+  if (kMode != kBackward) {
+    // without kRest every token counts in `rest`; its reference is a value of the thread's own
+    Sum2 list{ref, 0.0f};
+    rest = Sum2{-FLT_MAX, 0.0f};
+    const float lift = kRaise / c;
+    const unsigned char* bytes = reinterpret_cast<const unsigned char*>(s_bits);
+    for (int base = g0; base < g1; base += kNT * kU) {
+      uint4 v[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int g = base + u * kNT + static_cast<int>(threadIdx.x);
+        v[u] = g < g1 ? ld_stream(x.vec + g) : neg_inf_vec<kBF16>();
+      }
+      if (kRest) {
+        // the list's tokens go to their own sum and leave the vector
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int g = base + u * kNT + static_cast<int>(threadIdx.x);
+          const int b = (g - g0 + 1) * G;
+          uint32_t m = g < g1 ? bytes[b >> 3] : 0u;
+          if (!kBF16) m = (m >> (b & 4)) & 15u;
+          if (m) {
+            uint32_t word[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+            for (int e = 0; e < G; ++e) {
+              if (!((m >> e) & 1u)) continue;
+              if (kBF16) {
+                const uint32_t h = (e & 1) ? (word[e / 2] & 0xFFFF0000u) : (word[e / 2] << 16);
+                add_one(list, __uint_as_float(h), c);
+                word[e / 2] = (e & 1) ? (word[e / 2] & 0x0000FFFFu) | 0xFF800000u : (word[e / 2] & 0xFFFF0000u) | 0x0000FF80u;
+              } else {
+                add_one(list, __uint_as_float(word[e]), c);
+                word[e] = 0xFF800000u;
+              }
+            }
+            v[u] = make_uint4(word[0], word[1], word[2], word[3]);
+          }
+        }
+      }
+      float m = vec_max<kBF16>(v[0]);
+#pragma unroll
+      for (int u = 1; u < kU; ++u) m = fmaxf(m, vec_max<kBF16>(v[u]));
+      if (m > rest.ref + lift) rest.raise(clamp_ref(m), c);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) add_vec<kBF16>(rest, v[u], c);
+    }
+    // the elements outside the vectors: the head with rank 0, the tail with the last rank
+    if (static_cast<int>(threadIdx.x) < x.loose()) {
+      const int v = x.loose_at(threadIdx.x);
+      if ((v < x.head) ? rank == 0 : rank == CS - 1) {
+        const int b = v - bit0;
+        const bool in = kRest && ((s_bits[b >> 5] >> (b & 31)) & 1u);
+        add_one(in ? list : rest, x.at(v), c);
+      }
+    }
+    rest = block_merge(rest, c, red);
+    if (kRest) list = block_merge(list, c, red);
+    if (CS > 1) {
+      cg::cluster_group cl = cg::this_cluster();
+      if (static_cast<int>(threadIdx.x) < CS) {
+        float* to = cl.map_shared_rank(&part[0][0], threadIdx.x);
+        to[2 * rank] = rest.ref;
+        to[2 * rank + 1] = rest.s;
+        to[2 * (kMaxCS + rank)] = list.ref;
+        to[2 * (kMaxCS + rank) + 1] = list.s;
+      }
+      cl.sync();  // every CTA holds every part
+      rest = Sum2{part[0][0], part[0][1]};
+      list = Sum2{part[kMaxCS][0], part[kMaxCS][1]};
+      for (int q = 1; q < CS; ++q) {
+        rest = merge(rest, Sum2{part[q][0], part[q][1]}, c);
+        list = merge(list, Sum2{part[kMaxCS + q][0], part[kMaxCS + q][1]}, c);
+      }
+    }
+    all = kRest ? merge(list, rest, c) : rest;
+    if (rank == 0 && threadIdx.x == 0) {
+      // in base 2: ls = log2 S and lr = log2 SR against ref
+      const float ls = log2f(all.s) + (all.ref - ref) * c;
+      float kl = W / E - log2f(E) + ls;  // without a rest class
+      if constexpr (kRest) {
+        const float Et = E + er, pr = er / Et;
+        const float lr = log2f(rest.s) + (rest.ref - ref) * c;
+        if (er != 0.0f && rest.s == 0.0f) {
+          kl = INFINITY;  // the teacher's rest has mass, the student's none
+        } else if (pr >= 0.5f) {
+          // most mass is the rest's: ln p_r and ln q_r from what they leave, so that two
+          // numbers near zero are not differences of large ones
+          const float q = list.s > 0.0f ? log2_1p_ex2(log2f(list.s / rest.s) + (list.ref - rest.ref) * c) : 0.0f;
+          kl = W / Et - E / Et * (ur - lr) - kLog2e * log1pf(E / er) + q;
+        } else if (er != 0.0f) {
+          kl = (W + er * (ur - lr)) / Et - log2f(Et) + ls;
+        }
+      }
+      const bool ok = all.s > 0.0f && all.s < INFINITY;
+      P.loss[row] = ok ? w * P.tau * P.tau * (kl * kLn2) : NAN;
+      if (kMode == kForward && P.stats) {
+        P.stats[row * kStats] = all.ref;
+        P.stats[row * kStats + 1] = all.s;
+        P.stats[row * kStats + 2] = rest.ref;
+        P.stats[row * kStats + 3] = rest.s;
+      }
+    }
+    if (kMode == kForward) return;
+  }
+
+  // ---- the gradient -------------------------------------------------------------------
+  if (kMode != kForward) {
+    // d_v = scale (q_v - p_v): q_v = 2^((s_v - all.ref) c) / all.s; a token outside the list has
+    // p_v = p_r 2^((s_v - rest.ref) c) / rest.s, so one factor of one exponential covers both
+    // unless the two references lie too far apart for fp32
+    const float invE = 1.0f / (E + er);
+    const float A = all.s > 0.0f && all.s < INFINITY ? scale / all.s : NAN;
+    const float B = er != 0.0f ? scale * (er * invE) / rest.s : 0.0f;
+    const float apart = (all.ref - rest.ref) * c;
+    const bool one = er == 0.0f || apart < 80.0f;
+    const float C = er == 0.0f ? A : A - B * ex2(apart);
+    auto outside = [&](float s) {  // d of a token outside the list
+      const float a = ex2((s - all.ref) * c);
+      return one ? C * a : A * a - B * ex2((s - rest.ref) * c);
+    };
+    const RowView<kBF16> o(P.grad, row * P.ld_grad, V);
+    unsigned char* obase = const_cast<unsigned char*>(o.base);
+    auto put = [&](int v, float d) {
+      if (kBF16) reinterpret_cast<__nv_bfloat16*>(obase)[v] = __float2bfloat16_rn(d);
+      else reinterpret_cast<float*>(obase)[v] = d;
+    };
+    if (one && o.head == x.head) {
+      const f32x2 nref = pack2(-all.ref, -all.ref), c2 = pack2(c, c), C2 = pack2(C, C);
+      uint4* ov = const_cast<uint4*>(o.vec);
+      for (int base = g0; base < g1; base += kNT * kU) {
+        uint4 v[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int g = base + u * kNT + static_cast<int>(threadIdx.x);
+          v[u] = g < g1 ? ld_stream(x.vec + g) : neg_inf_vec<kBF16>();
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int g = base + u * kNT + static_cast<int>(threadIdx.x);
+          uint32_t out[4];
+#pragma unroll
+          for (int i = 0; i < G / 2; ++i) {
+            float a, b;
+            unpack2(mul2(add2(pair_of<kBF16>(v[u], i), nref), c2), a, b);
+            unpack2(mul2(pack2(ex2(a), ex2(b)), C2), a, b);
+            if (kBF16) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);  // the gradient's one rounding
+              out[i] = reinterpret_cast<const uint32_t&>(h);
+            } else {
+              out[2 * i] = __float_as_uint(a);
+              out[2 * i + 1] = __float_as_uint(b);
+            }
+          }
+          if (g < g1) __stcs(ov + g, make_uint4(out[0], out[1], out[2], out[3]));
+        }
+      }
+      if (static_cast<int>(threadIdx.x) < x.loose()) {
+        const int v = x.loose_at(threadIdx.x);
+        if ((v < x.head) ? rank == 0 : rank == CS - 1) put(v, outside(x.at(v)));
+      }
+    } else {
+      // the two rows do not share their 16-byte boundaries: one element at a time
+      const int v0 = rank == 0 ? 0 : x.head + g0 * G;
+      const int v1 = rank == CS - 1 ? V : x.head + g1 * G;
+      for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kNT) put(v, outside(x.at(v)));
+    }
+    // the list's tokens in this CTA's part, over what the pass above wrote
+    const bool dup = __syncthreads_or(twice);
+    const int v0 = rank == 0 ? 0 : x.head + g0 * G;
+    const int v1 = rank == CS - 1 ? V : x.head + g1 * G;
+    for (int k = threadIdx.x; k < K; k += kNT) {
+      const int32_t id = s_id[k];
+      if (id < v0 || id >= v1) continue;  // empty slots are -1
+      float e = s_e[k];
+      if (dup) {
+        // the token's first slot takes the sum over its slots, in slot order
+        e = 0.0f;
+        bool first = true;
+        for (int j = 0; j < K; ++j) {
+          if (s_id[j] != id) continue;
+          first = first && j >= k;
+          e += s_e[j];
+        }
+        if (!first) continue;
+      }
+      put(id, A * ex2(s_v[k] + (ref - all.ref) * c) - scale * (e * invE));
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// Host side
+// ------------------------------------------------------------------------------------------
+static int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  return n;
+}
+
+template <bool kBF16, bool kRest, int kMode>
+static kps_status launch_t(const Params& P, cudaStream_t stream) {
+  const int sms = sm_count();
+  if (!sms) return KPS_ERR_CUDA;
+  // few rows: a cluster shares each, as wide as leaves every CTA a full round of loads
+  int cs = 1;
+  const int64_t round = static_cast<int64_t>(kNT) * kU * (kBF16 ? 8 : 4);
+  while (cs < kMaxCS && P.N * cs * 2 <= 2 * sms && P.V >= 2 * cs * round) cs *= 2;
+  const Layout lay = make_layout(P.K, (P.V + cs - 1) / cs + 4 * (kBF16 ? 8 : 4), kMode != kForward, kRest);
+  if (lay.total > 48 * 1024 &&
+      cudaFuncSetAttribute(distill_kernel<kBF16, kRest, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(lay.total)) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return KPS_ERR_CUDA;
+  }
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(static_cast<unsigned>(P.N * cs));
+  lc.blockDim = dim3(kNT);
+  lc.dynamicSmemBytes = lay.total;
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  if (cudaLaunchKernelEx(&lc, distill_kernel<kBF16, kRest, kMode>, P) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return KPS_ERR_CUDA;
+  }
+  return KPS_OK;
+}
+
+template <int kMode>
+static kps_status launch(const Params& P, kps_dtype dt, cudaStream_t stream) {
+  if (dt == KPS_BF16) return P.rest ? launch_t<true, true, kMode>(P, stream) : launch_t<true, false, kMode>(P, stream);
+  return P.rest ? launch_t<false, true, kMode>(P, stream) : launch_t<false, false, kMode>(P, stream);
+}
+
+// The checks every entry point shares; fills P.  *empty: nothing to do.
+static kps_status check(const void* student, kps_dtype dt, int64_t N, int64_t V, int64_t ld, const int32_t* ids,
+                        const void* values, kps_dtype values_dt, int64_t K, const float* rest, const float* weight,
+                        float temperature, Params* P) {
+  if ((dt != KPS_F32 && dt != KPS_BF16) || (values_dt != KPS_F32 && values_dt != KPS_BF16)) return KPS_ERR_INVALID_ARG;
+  if (N < 0 || V < 1 || K < 1 || K > kMaxK) return KPS_ERR_INVALID_ARG;
+  if (N > 1 && ld < V) return KPS_ERR_INVALID_ARG;
+  if (!(temperature > 0.0f) || std::isinf(temperature) || std::isinf(stream::kLog2e / temperature)) return KPS_ERR_INVALID_ARG;
+  if (V > kMaxV || N > INT32_MAX / kMaxCS) return KPS_ERR_UNSUPPORTED;
+  if (N == 0) return KPS_OK;
+  if (!student || !ids || !values) return KPS_ERR_INVALID_ARG;
+  const uintptr_t esize = dt == KPS_BF16 ? 2 : 4, vsize = values_dt == KPS_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(student) % esize || reinterpret_cast<uintptr_t>(values) % vsize ||
+      reinterpret_cast<uintptr_t>(ids) % 4 || reinterpret_cast<uintptr_t>(rest) % 4 || reinterpret_cast<uintptr_t>(weight) % 4)
+    return KPS_ERR_INVALID_ARG;
+  P->student = student;
+  P->N = N;
+  P->ld = ld;
+  P->V = static_cast<int>(V);
+  P->K = static_cast<int>(K);
+  P->ids = ids;
+  P->values = values;
+  P->values_bf16 = values_dt == KPS_BF16;
+  P->rest = rest;
+  P->weight = weight;
+  P->tau = temperature;
+  P->c = stream::kLog2e / temperature;
+  return KPS_OK;
+}
+
+// A gradient buffer of its own: rows of at least V elements, sharing no byte with the student's rows.
+static kps_status check_grad(const Params& P, kps_dtype dt, void* grad, int64_t ld_grad) {
+  const uintptr_t esize = dt == KPS_BF16 ? 2 : 4;
+  if (!grad || reinterpret_cast<uintptr_t>(grad) % esize || (P.N > 1 && ld_grad < P.V)) return KPS_ERR_INVALID_ARG;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(P.student), b = reinterpret_cast<uintptr_t>(grad);
+  const uintptr_t an = ((P.N - 1) * P.ld + P.V) * esize, bn = ((P.N - 1) * ld_grad + P.V) * esize;
+  if (a < b + bn && b < a + an) return KPS_ERR_INVALID_ARG;
+  return KPS_OK;
+}
+
+}  // namespace distill
+}  // namespace kps
+
+extern "C" {
+
+kps_status kps_distill_forward(const void* student, kps_dtype dt, int64_t N, int64_t V, int64_t ld,
+                               const int32_t* ids, const void* values, kps_dtype values_dt, int64_t K,
+                               const float* rest, const float* weight, float temperature, float* out_loss,
+                               float* out_stats, cudaStream_t stream) {
+  const kps::NvtxRange range("kps_distill_forward");
+  kps::distill::Params P = {};
+  const kps_status st = kps::distill::check(student, dt, N, V, ld, ids, values, values_dt, K, rest, weight, temperature, &P);
+  if (st != KPS_OK || N == 0) return st;
+  if (!out_loss) return KPS_ERR_INVALID_ARG;
+  P.loss = out_loss;
+  P.stats = out_stats;
+  return kps::distill::launch<kps::distill::kForward>(P, dt, stream);
+}
+
+kps_status kps_distill_backward(const void* student, kps_dtype dt, int64_t N, int64_t V, int64_t ld,
+                                const int32_t* ids, const void* values, kps_dtype values_dt, int64_t K,
+                                const float* rest, const float* weight, float temperature, const float* grad_loss,
+                                const float* stats, void* out_grad, int64_t ld_grad, cudaStream_t stream) {
+  const kps::NvtxRange range("kps_distill_backward");
+  kps::distill::Params P = {};
+  kps_status st = kps::distill::check(student, dt, N, V, ld, ids, values, values_dt, K, rest, weight, temperature, &P);
+  if (st != KPS_OK || N == 0) return st;
+  if (!stats) return KPS_ERR_INVALID_ARG;
+  if ((st = kps::distill::check_grad(P, dt, out_grad, ld_grad)) != KPS_OK) return st;
+  P.upstream = grad_loss;
+  P.stats = const_cast<float*>(stats);
+  P.grad = out_grad;
+  P.ld_grad = ld_grad;
+  return kps::distill::launch<kps::distill::kBackward>(P, dt, stream);
+}
+
+kps_status kps_distill_loss_grad(const void* student, kps_dtype dt, int64_t N, int64_t V, int64_t ld,
+                                 const int32_t* ids, const void* values, kps_dtype values_dt, int64_t K,
+                                 const float* rest, const float* weight, float temperature, float* out_loss,
+                                 void* out_grad, int64_t ld_grad, cudaStream_t stream) {
+  const kps::NvtxRange range("kps_distill_loss_grad");
+  kps::distill::Params P = {};
+  kps_status st = kps::distill::check(student, dt, N, V, ld, ids, values, values_dt, K, rest, weight, temperature, &P);
+  if (st != KPS_OK || N == 0) return st;
+  if (!out_loss) return KPS_ERR_INVALID_ARG;
+  if ((st = kps::distill::check_grad(P, dt, out_grad, ld_grad)) != KPS_OK) return st;
+  P.loss = out_loss;
+  P.grad = out_grad;
+  P.ld_grad = ld_grad;
+  return kps::distill::launch<kps::distill::kBoth>(P, dt, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,178 @@
+// kps_stream.cuh — streaming one row of logits through a thread block: the row's 16-byte
+// vectors, packed fp32 arithmetic, base-2 sums of exponentials and their reductions.  Shared
+// by the kernels that read whole rows of [rows, vocab] logits (the top logits, distillation).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cfloat>
+#include <cstdint>
+
+namespace kps {
+namespace stream {
+
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.693147180559945309f;
+// The vectors of one row: `head` elements before the first 16-byte boundary, `nv` vectors of G
+// elements, then the tail.
+template <bool kBF16>
+struct RowView {
+  static constexpr int G = kBF16 ? 8 : 4;
+  const unsigned char* base;  // element 0
+  const uint4* vec;           // the first vector
+  int V, head, nv;
+
+  __device__ __forceinline__ RowView(const void* p, int64_t offset, int V_) {
+    base = static_cast<const unsigned char*>(p) + offset * (kBF16 ? 2 : 4);
+    V = V_;
+    const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(base) & 15u);
+    head = mis ? (16 - mis) / (kBF16 ? 2 : 4) : 0;
+    if (head > V) head = V;
+    nv = (V - head) / G;
+    vec = reinterpret_cast<const uint4*>(base + head * (kBF16 ? 2 : 4));
+  }
+  __device__ __forceinline__ float at(int v) const {
+    return kBF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(base)[v])
+                 : reinterpret_cast<const float*>(base)[v];
+  }
+  // Elements outside the vectors: i in [0, loose()) -> their index.
+  __device__ __forceinline__ int loose() const { return V - nv * G; }
+  __device__ __forceinline__ int loose_at(int i) const { return i < head ? i : i + nv * G; }
+};
+
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
+template <bool kBF16>
+__device__ __forceinline__ uint4 neg_inf_vec() {
+  const uint32_t w = kBF16 ? 0xFF80FF80u : 0xFF800000u;
+  return make_uint4(w, w, w, w);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Two fp32 values in one 64-bit register pair (one instruction for both on sm_100 and later).
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Elements 2i and 2i + 1 of a vector (i < G / 2), as fp32.
+template <bool kBF16>
+__device__ __forceinline__ f32x2 pair_of(const uint4& w, int i) {
+  if (kBF16) {
+    const uint32_t x = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+    return pack2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+  }
+  return i == 0 ? pack2(__uint_as_float(w.x), __uint_as_float(w.y)) : pack2(__uint_as_float(w.z), __uint_as_float(w.w));
+}
+
+// The largest element of a vector (NaN ignored).
+template <bool kBF16>
+__device__ __forceinline__ float vec_max(const uint4& w) {
+  if (kBF16) {
+    const __nv_bfloat162 a = __hmax2(reinterpret_cast<const __nv_bfloat162&>(w.x), reinterpret_cast<const __nv_bfloat162&>(w.y));
+    const __nv_bfloat162 b = __hmax2(reinterpret_cast<const __nv_bfloat162&>(w.z), reinterpret_cast<const __nv_bfloat162&>(w.w));
+    const __nv_bfloat162 m = __hmax2(a, b);
+    const uint32_t u = reinterpret_cast<const uint32_t&>(m);
+    return fmaxf(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+  }
+  return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+
+// A sum of exp(x_v / temperature) in fp32 against a reference logit: s = sum 2^((x_v - ref) c)
+// with c = log2(e) / temperature.  The difference is taken before the product, so it is as
+// exact at |x| = 1e9 as at 10.  The reference starts where the caller puts it and moves up only
+// when a value lies more than 2^64 above it, so a row's threads normally share one reference and
+// no element pays for a running maximum.
+struct Sum2 {
+  float ref, s;
+  __device__ __forceinline__ void raise(float to, float c) {  // to > ref
+    s *= ex2((ref - to) * c);
+    ref = to;
+  }
+};
+constexpr float kRaise = 64.0f;
+
+// The sum of two sums, against the larger reference of those that hold anything.
+__device__ __forceinline__ Sum2 merge(const Sum2& a, const Sum2& b, float c) {
+  if (b.s == 0.0f) return a;
+  if (a.s == 0.0f) return b;
+  if (a.ref == b.ref) return Sum2{a.ref, a.s + b.s};
+  const float m = fmaxf(a.ref, b.ref);
+  return Sum2{m, a.s * ex2((a.ref - m) * c) + b.s * ex2((b.ref - m) * c)};
+}
+
+__device__ __forceinline__ Sum2 warp_merge(Sum2 v, float c) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    Sum2 t;
+    t.ref = __shfl_xor_sync(0xffffffffu, v.ref, o);
+    t.s = __shfl_xor_sync(0xffffffffu, v.s, o);
+    // the same operand order in both lanes, so that both hold the same bits
+    v = (threadIdx.x & o) ? merge(t, v, c) : merge(v, t, c);
+  }
+  return v;
+}
+// Adds the elements of a vector to a sum whose reference is high enough for them.
+template <bool kBF16>
+__device__ __forceinline__ void add_vec(Sum2& sum, const uint4& w, float c) {
+  constexpr int G = kBF16 ? 8 : 4;
+  const f32x2 nref = pack2(-sum.ref, -sum.ref), c2 = pack2(c, c);
+  f32x2 acc = 0ull;  // two zeros
+#pragma unroll
+  for (int i = 0; i < G / 2; ++i) {
+    float a, b;
+    unpack2(mul2(add2(pair_of<kBF16>(w, i), nref), c2), a, b);
+    acc = add2(acc, pack2(ex2(a), ex2(b)));
+  }
+  float a, b;
+  unpack2(acc, a, b);
+  sum.s += a + b;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// A finite reference: differences to it are never inf - inf.
+__device__ __forceinline__ float clamp_ref(float x) { return fminf(fmaxf(x, -FLT_MAX), FLT_MAX); }
+
+}  // namespace stream
+}  // namespace kps

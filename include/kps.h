@@ -245,6 +245,96 @@ kps_status kps_sample_noalloc(const void* logits, kps_dtype dt, int64_t B, int64
                               int64_t* out_idx, float* out_filtered, cudaStream_t stream);
 
 
+/*
+ * Rows of logits beside the sampling step.  The three operators below read
+ * [rows, V] logits whose rows start ld elements apart (ld >= V when there is
+ * more than one row; what lies between a row's end and the next row's start is
+ * neither read nor written).  They take V <= 1048576, allocate nothing, need no
+ * workspace and keep nothing between calls; calls are independent of each
+ * other, on one stream or several, and may be captured into CUDA graphs.  The
+ * device of the pointers must be current.  Pointers must be aligned to their
+ * element type; rows on 16-byte boundaries are read fastest, any others work.
+ * Errors are as for kps_sample: KPS_ERR_INVALID_ARG, KPS_ERR_UNSUPPORTED (a
+ * vocabulary or a row count too large), KPS_ERR_CUDA.
+ */
+
+/*
+ * kps_top_logits — the top logits of every row and the log-sum-exps that make
+ * them log-probabilities.  With the order of kps_sample (value descending,
+ * index ascending; NaN counts as -inf) and a = x / temperature:
+ *
+ *   out_ids, out_values [B, n]   the first n elements of the order and their
+ *                                logits x, as fp32 (-0 as +0); 0 <= n <=
+ *                                min(V, 1024); NULL allowed for n == 0
+ *   out_lse      [B]  ln sum over the row of exp(a), or NULL
+ *   out_rest     [B]  ln sum over the row without its top n of exp(a): -inf
+ *                     when nothing is left, or NULL
+ *   out_logprob  [B]  a[tokens[b]] - out_lse[b]: -inf for a token outside
+ *                     [0, V), or NULL.  tokens [B] int64, as kps_sample
+ *                     writes them; needed only for out_logprob.
+ *
+ * temperature is finite and > 0.  A row with +inf has an lse of +inf; in a row
+ * of -inf alone lse and rest are -inf.  Log-probabilities of such rows follow
+ * IEEE arithmetic.  Results do not depend on the launch shape or on repetition.
+ */
+kps_status kps_top_logits(const void* logits, kps_dtype dt, int64_t B, int64_t V, int64_t ld, int64_t n,
+                          float temperature, const int64_t* tokens, int32_t* out_ids, float* out_values,
+                          float* out_lse, float* out_rest, float* out_logprob, cudaStream_t stream);
+
+/*
+ * kps_distill_forward, kps_distill_backward, kps_distill_loss_grad — the
+ * distillation loss of a student's rows against the top logits of a teacher
+ * (as kps_top_logits gives them), and its gradient.
+ *
+ *   student  [N, V] logits s (dt), rows ld apart
+ *   ids, values [N, K]  the teacher's slots, contiguous, 1 <= K <= 1024: token
+ *            ids and logits t (values_dt).  An id outside [0, V) or a value of
+ *            -inf marks an empty slot.  A token may fill several slots; their
+ *            masses add.
+ *   rest     [N] ln sum of exp(t / temperature) over everything the teacher's
+ *            list leaves out (kps_top_logits' out_rest at the same
+ *            temperature), or NULL: the list is all there is.
+ *   weight   [N] or NULL (1): of each row's loss.  A row of weight 0, or
+ *            without a filled slot, has loss 0 and gradient 0, and the
+ *            student's logits in it are not looked at.
+ *
+ * With tau = temperature, p = softmax([t / tau ..., rest]) over the filled
+ * slots and the rest, L = ln sum_v exp(s_v / tau) and R the same over the
+ * tokens outside the row's list:
+ *
+ *   loss = weight tau^2 (sum_k p_k (ln p_k - s_{id_k} / tau + L)
+ *                        + p_rest (ln p_rest - R + L))
+ *   d loss / d s_v = weight tau (exp(s_v / tau - L) - sum_{k: id_k = v} p_k)
+ *                                                        for v in the list,
+ *                    weight tau (exp(s_v / tau - L) - p_rest exp(s_v / tau - R))
+ *                                                        for every other v
+ *
+ * (the Kullback-Leibler divergence of the student from the teacher, everything
+ * outside the list as one class).  A student row holding NaN or +inf, or
+ * nothing above -inf, has a loss and a gradient of NaN; a student that gives
+ * no mass to a token or a rest that the teacher gives some has a loss of +inf.
+ *
+ * kps_distill_forward writes out_loss [N] and, unless NULL, out_stats [N, 4],
+ * which kps_distill_backward takes with the same other arguments: it writes
+ * out_grad [N, V] (dt, rows ld_grad apart), the gradient times grad_loss [N]
+ * (NULL: 1; a row of grad_loss 0 gets zeros).  kps_distill_loss_grad does both
+ * in one launch, for programs that have all factors in weight.  out_grad must
+ * not overlap the student's rows.  Gradients are computed in fp32 and rounded
+ * once.
+ */
+kps_status kps_distill_forward(const void* student, kps_dtype dt, int64_t N, int64_t V, int64_t ld,
+                               const int32_t* ids, const void* values, kps_dtype values_dt, int64_t K,
+                               const float* rest, const float* weight, float temperature, float* out_loss,
+                               float* out_stats, cudaStream_t stream);
+kps_status kps_distill_backward(const void* student, kps_dtype dt, int64_t N, int64_t V, int64_t ld,
+                                const int32_t* ids, const void* values, kps_dtype values_dt, int64_t K,
+                                const float* rest, const float* weight, float temperature, const float* grad_loss,
+                                const float* stats, void* out_grad, int64_t ld_grad, cudaStream_t stream);
+kps_status kps_distill_loss_grad(const void* student, kps_dtype dt, int64_t N, int64_t V, int64_t ld,
+                                 const int32_t* ids, const void* values, kps_dtype values_dt, int64_t K,
+                                 const float* rest, const float* weight, float temperature, float* out_loss,
+                                 void* out_grad, int64_t ld_grad, cudaStream_t stream);
+
 /* Which kernel the most recent kps_sample call of the calling host thread
  * that launched one used: 1 = the cluster kernel (kps_sample_kernel),
  * 2 = the row kernel (kps_row_kernel, possibly after its pre-pass
