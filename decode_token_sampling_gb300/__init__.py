@@ -71,6 +71,9 @@ def load_library() -> ctypes.CDLL:
     lib.kps_sample_step.restype = I32
     lib.kps_sample_step.argtypes = [P, I32, I64, I64, P, P, P, P, P, P, ctypes.POINTER(StepOpts), ctypes.c_float,
                                     I32, P, P, P, ctypes.c_size_t, P]
+    lib.kps_sample_min_p.restype = I32
+    lib.kps_sample_min_p.argtypes = [P, I32, I64, I64, P, P, P, P, P, P, P, ctypes.POINTER(StepOpts), ctypes.c_float,
+                                     I32, P, P, P, ctypes.c_size_t, P]
     lib.kps_last_kernel.restype = I32
     lib.kps_last_kernel.argtypes = []
     lib.kps_last_launch_count.restype = I32
@@ -183,7 +186,7 @@ def sample(logits: torch.Tensor, top_k: torch.Tensor, top_p: torch.Tensor, tempe
            workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
            seed: Optional[int] = None, step: int = 0, finished: Optional[torch.Tensor] = None,
            eos_id: int = 0, unfinished: Optional[torch.Tensor] = None, seen_bits: Optional[torch.Tensor] = None,
-           update_seen: bool = False, kernel: Optional[int] = None):
+           update_seen: bool = False, kernel: Optional[int] = None, min_p: Optional[torch.Tensor] = None):
     """One fused sampling step on the GPU (asynchronous on `stream`).
 
     q: the race's Exp(1) draws [B, V] fp32, or None to sample off (each row's index is
@@ -195,6 +198,8 @@ def sample(logits: torch.Tensor, top_k: torch.Tensor, top_p: torch.Tensor, tempe
     seen_bits (int32 [B, ceil(V/32)], bit v % 32 of word v // 32 = token v seen): the
     seen set in place of seen_indptr/seen_ids; update_seen sets each row's emitted
     token in it after the step (kps_sample_step).
+    min_p: float32 [B]: after top-p, keep the tokens with at least min_p times the largest
+    probability (kps_sample_min_p); values <= 0 skip the stage for their row.
     kernel: the kernel policy of this call (KERNEL_*; default: this thread's
     set_kernel_policy choice, else automatic).
     Returns (out_idx int64[B], out_filtered float32[B,V] or None).
@@ -242,7 +247,8 @@ def sample(logits: torch.Tensor, top_k: torch.Tensor, top_p: torch.Tensor, tempe
         workspace = new_workspace(B, V, logits.dtype, dev)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     policy = get_kernel_policy() if kernel is None else int(kernel)
-    step_call = finished is not None or seen_bits is not None or policy != KERNEL_AUTO
+    step_call = finished is not None or seen_bits is not None or policy != KERNEL_AUTO or min_p is not None
+    _check(min_p, "min_p", torch.float32, (B,), dev)
     if step_call:
         if finished is not None:
             _check(finished, "finished", torch.uint8, (B,), dev)
@@ -253,10 +259,13 @@ def sample(logits: torch.Tensor, top_k: torch.Tensor, top_p: torch.Tensor, tempe
         opts = StepOpts(_ptr(q) if seed is None else None, 0 if seed is None else 1,
                         0 if seed is None else int(seed) & (2**64 - 1), int(step) & (2**64 - 1), _ptr(finished),
                         int(eos_id), _ptr(unfinished), _ptr(seen_bits), 1 if update_seen else 0, policy)
-        st = lib.kps_sample_step(_ptr(logits), dt, B, V, _ptr(top_k), _ptr(top_p), _ptr(temperature),
-                                 _ptr(seen_indptr), _ptr(seen_ids), _ptr(penalty), ctypes.byref(opts), float(eps),
-                                 1 if need_logits else 0, _ptr(out_idx), _ptr(out_filtered), _ptr(workspace),
-                                 workspace.numel(), ctypes.c_void_p(s.cuda_stream))
+        tail = (_ptr(temperature), _ptr(seen_indptr), _ptr(seen_ids), _ptr(penalty), ctypes.byref(opts), float(eps),
+                1 if need_logits else 0, _ptr(out_idx), _ptr(out_filtered), _ptr(workspace), workspace.numel(),
+                ctypes.c_void_p(s.cuda_stream))
+        if min_p is not None:
+            st = lib.kps_sample_min_p(_ptr(logits), dt, B, V, _ptr(top_k), _ptr(top_p), _ptr(min_p), *tail)
+        else:
+            st = lib.kps_sample_step(_ptr(logits), dt, B, V, _ptr(top_k), _ptr(top_p), *tail)
     elif seed is not None:
         st = lib.kps_sample_seeded(_ptr(logits), dt, B, V, _ptr(top_k), _ptr(top_p), _ptr(temperature),
                                    _ptr(seen_indptr), _ptr(seen_ids), _ptr(penalty), int(seed) & (2**64 - 1),
@@ -269,7 +278,7 @@ def sample(logits: torch.Tensor, top_k: torch.Tensor, top_p: torch.Tensor, tempe
                             1 if need_logits else 0, _ptr(out_idx), _ptr(out_filtered), _ptr(workspace),
                             workspace.numel(), ctypes.c_void_p(s.cuda_stream))
     if st != 0:
-        raise KpsError(st, "kps_sample_step" if step_call else
+        raise KpsError(st, "kps_sample_min_p" if min_p is not None else "kps_sample_step" if step_call else
                        "kps_sample_seeded" if seed is not None else "kps_sample")
     return out_idx, out_filtered
 

@@ -29,6 +29,8 @@
 //        linear bins of (M - x), then a finer one inside the boundary bin,
 //        locates the boundary, resolved exactly as above; the race and the
 //        filtered-logit write are one fused pass.
+//   min-p (kps_sample_min_p): the cut that top-k and top-p left is raised to
+//        the smallest value not below M + ln(min_p).
 //   Any overflow of the small candidate structures falls back to an exact
 //   radix select over the whole resident row.
 //
@@ -111,6 +113,7 @@ struct Params {
   const int32_t* top_k;
   const float* top_p;
   const float* temperature;
+  const float* min_p;  // [B] (nullptr: the stage is off)
   const int32_t* seen_indptr;
   const int32_t* seen_ids;
   const float* penalty;
@@ -148,15 +151,22 @@ __device__ __forceinline__ uint32_t seen_word_at(const uint32_t* row_bits, int64
 
 constexpr int kMaxRowList = 256;  // rows one worker (CTA or cluster) may own in a filtered launch
 
-// True for rows of the one-pass top-k path: top-k active, or a single element kept
-// (greedy temperature, top_p <= 0, or k == 1).  Every kernel and worker agrees on it.
+// The row's min-p in (0, 1], or 0 where the stage is off (min_p <= 0 or NaN, or no min_p).
+__device__ __forceinline__ float row_min_p(const Params& P, int64_t row) {
+  if (!P.min_p) return 0.0f;
+  const float m = P.min_p[row];
+  return m > 0.0f ? fminf(m, 1.0f) : 0.0f;
+}
+
+// True for rows of the one-pass list paths: top-k active, a single element kept (greedy
+// temperature, top_p <= 0, or k == 1), or min-p active.  Every kernel and worker agrees on it.
 __device__ __forceinline__ bool row_is_kmode(const Params& P, int64_t row) {
   const int32_t k = P.top_k[row];
   const float p = P.top_p[row];
   const float T = P.temperature[row];
   const bool greedyT = !(T > 0.0f) || isinf(T);
   const bool topk_on = k >= 1 && static_cast<int64_t>(k) <= (P.V < 1024 ? P.V : 1024);
-  return topk_on || greedyT || (!isnan(p) && p <= 0.0f);
+  return topk_on || greedyT || (!isnan(p) && p <= 0.0f) || row_min_p(P, row) > 0.0f;
 }
 
 // Rows worker w of nw owns in a filtered launch: the matching rows whose rank among
@@ -305,6 +315,25 @@ __device__ __forceinline__ long long eos_epilogue(const Params& P, int64_t row, 
 __device__ __forceinline__ void seen_append(const Params& P, int64_t row, long long tok) {
   if (!P.update_seen || tok < 0 || tok >= P.V) return;
   atomicOr(P.seen_bits + row * seen_words(P.V) + (tok >> 5), 1u << (tok & 31));
+}
+
+// ---- min-p ------------------------------------------------------------------------------
+//
+// An element y is kept when exp(y - M) >= min_p, that is y >= M + ln(min_p).  ln(min_p) is
+// taken in 64 bits by one thread and carried as two floats hi + lo; the bound is the smallest
+// float that is not below M + hi + lo, so the comparison of keys decides as 64 bits would.
+__device__ __forceinline__ float2 ln_min_p(float mp) {
+  const double l = log(static_cast<double>(mp));
+  const float hi = static_cast<float>(l);
+  return make_float2(hi, static_cast<float>(l - static_cast<double>(hi)));
+}
+// The key of that bound below the maximum M.
+__device__ __forceinline__ uint32_t min_p_key(float2 ln, float M) {
+  if (isinf(M)) return fkey(M);
+  const float s = __fadd_rn(M, ln.x);
+  const float b = __fsub_rn(s, M);
+  const float e = __fadd_rn(__fsub_rn(M, __fsub_rn(s, b)), __fsub_rn(ln.x, b));  // s + e = M + hi
+  return fkey(__fadd_rn(__fadd_ru(s, __fadd_rn(e, ln.y)), 0.0f));
 }
 
 __device__ __forceinline__ unsigned long long fixed_mass(float w) {
@@ -567,6 +596,13 @@ struct Thresh {
 
 // Element sources for the fallback radix select.  for_each calls
 // f(valid, key, index, value) with the whole warp converged.
+// The tighter of th and the min-p bound: both keep prefixes of the order that hold its first
+// element.
+__device__ __forceinline__ Thresh with_min_p(Thresh th, float2 ln, float M) {
+  const uint32_t k = min_p_key(ln, M);
+  return k > th.key ? Thresh{k, INT_MAX} : th;
+}
+
 struct SrcData {  // the CTA's resident chunk (transformed values)
   const float* xs;
   int n4;
@@ -1122,6 +1158,9 @@ __global__ void __launch_bounds__(kThreads, 2) kps_sample_kernel(const Params P)
     const bool p_nan = isnan(p);
     const bool single = greedyT || (!p_nan && p <= 0.0f) || (topk_on && k == 1);
     const bool topp_on = !single && !p_nan && p > 0.0f && p < 1.0f;
+    const float mp = single ? 0.0f : row_min_p(P, row);
+    // one thread takes the logarithm while the chunk is in flight (read after the barriers below)
+    if (mp > 0.0f && threadIdx.x == kThreads - 1) *reinterpret_cast<float2*>(c.misc + 11) = ln_min_p(mp);
     // top-k bound: split the 128-element groups until there are at least k of them
     // (while the gathered maxima still fit kGallCap)
     int gsh = 0;
@@ -1705,6 +1744,7 @@ __global__ void __launch_bounds__(kThreads, 2) kps_sample_kernel(const Params P)
     } else {
       transform_in_place();  // top-k and top-p both skipped: every element is kept
     }
+    if (mp > 0.0f) th = with_min_p(th, *reinterpret_cast<const float2*>(c.misc + 11), M);
 
     // ---- exponential race over the kept set, and the filtered-logit write --------------
     const float* qrow = P.q ? P.q + row * V : nullptr;  // none: sampling off or generated draws
@@ -2200,7 +2240,7 @@ static kps_status sample_impl(const void* logits, kps_dtype dt, int64_t B, int64
                               size_t workspace_bytes, cudaStream_t stream, int gen, unsigned long long seed,
                               unsigned long long step, unsigned char* finished = nullptr, long long eos = 0,
                               int* unfinished = nullptr, uint32_t* seen_bits = nullptr, int update_seen = 0,
-                              int policy = 0) {
+                              int policy = 0, const float* min_p = nullptr) {
   if (dt != KPS_F32 && dt != KPS_BF16) return KPS_ERR_INVALID_ARG;
   if (V < 1 || V > INT32_MAX || B < 0) return KPS_ERR_INVALID_ARG;
   if (!(eps >= 0.0f) || std::isinf(eps)) return KPS_ERR_INVALID_ARG;
@@ -2241,6 +2281,7 @@ static kps_status sample_impl(const void* logits, kps_dtype dt, int64_t B, int64
   P.top_k = top_k;
   P.top_p = top_p;
   P.temperature = temperature;
+  P.min_p = min_p;
   P.seen_indptr = pen && !seen_bits ? seen_indptr : nullptr;
   P.seen_ids = pen && !seen_bits ? seen_ids : nullptr;
   P.penalty = pen ? penalty : nullptr;
@@ -2366,12 +2407,12 @@ kps_status kps_sample_seeded(const void* logits, kps_dtype dt, int64_t B, int64_
                      need_logits, out_idx, out_filtered, workspace, workspace_bytes, stream, 1, seed, step);
 }
 
-kps_status kps_sample_step(const void* logits, kps_dtype dt, int64_t B, int64_t V, const int32_t* top_k,
-                           const float* top_p, const float* temperature, const int32_t* seen_indptr,
-                           const int32_t* seen_ids, const float* penalty, const kps_step_opts* opts, float eps,
-                           int need_logits, int64_t* out_idx, float* out_filtered, void* workspace,
-                           size_t workspace_bytes, cudaStream_t stream) {
-  const kps::NvtxRange range("kps_sample_step");
+// kps_sample_step, with min_p NULL, and kps_sample_min_p.
+static kps_status step_impl(const void* logits, kps_dtype dt, int64_t B, int64_t V, const int32_t* top_k,
+                            const float* top_p, const float* min_p, const float* temperature,
+                            const int32_t* seen_indptr, const int32_t* seen_ids, const float* penalty,
+                            const kps_step_opts* opts, float eps, int need_logits, int64_t* out_idx,
+                            float* out_filtered, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   if (!opts) return KPS_ERR_INVALID_ARG;
   if (opts->unfinished && !opts->finished) return KPS_ERR_INVALID_ARG;
   if (opts->kernel_policy < 0 || opts->kernel_policy > 3) return KPS_ERR_INVALID_ARG;
@@ -2379,7 +2420,28 @@ kps_status kps_sample_step(const void* logits, kps_dtype dt, int64_t B, int64_t 
                      opts->generate ? nullptr : opts->q, eps, need_logits, out_idx, out_filtered, workspace,
                      workspace_bytes, stream, opts->generate ? 1 : 0, opts->seed, opts->step, opts->finished,
                      static_cast<long long>(opts->eos_id), opts->unfinished, opts->seen_bits, opts->update_seen,
-                     opts->kernel_policy);
+                     opts->kernel_policy, min_p);
+}
+
+kps_status kps_sample_step(const void* logits, kps_dtype dt, int64_t B, int64_t V, const int32_t* top_k,
+                           const float* top_p, const float* temperature, const int32_t* seen_indptr,
+                           const int32_t* seen_ids, const float* penalty, const kps_step_opts* opts, float eps,
+                           int need_logits, int64_t* out_idx, float* out_filtered, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream) {
+  const kps::NvtxRange range("kps_sample_step");
+  return step_impl(logits, dt, B, V, top_k, top_p, nullptr, temperature, seen_indptr, seen_ids, penalty, opts, eps,
+                   need_logits, out_idx, out_filtered, workspace, workspace_bytes, stream);
+}
+
+kps_status kps_sample_min_p(const void* logits, kps_dtype dt, int64_t B, int64_t V, const int32_t* top_k,
+                            const float* top_p, const float* min_p, const float* temperature,
+                            const int32_t* seen_indptr, const int32_t* seen_ids, const float* penalty,
+                            const kps_step_opts* opts, float eps, int need_logits, int64_t* out_idx,
+                            float* out_filtered, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  const kps::NvtxRange range("kps_sample_min_p");
+  if (B > 0 && (!min_p || (reinterpret_cast<uintptr_t>(min_p) & 3u) != 0)) return KPS_ERR_INVALID_ARG;
+  return step_impl(logits, dt, B, V, top_k, top_p, min_p, temperature, seen_indptr, seen_ids, penalty, opts, eps,
+                   need_logits, out_idx, out_filtered, workspace, workspace_bytes, stream);
 }
 
 int kps_last_kernel(void) { return kps::t_last_kernel; }

@@ -23,6 +23,10 @@
 //     mass S, races and writes every element above the band and collects the band,
 //     which is sorted and cut exactly.  Pass A keeps the row in L2 for pass B.
 //   keep-all rows (no top-k, p >= 1): a maximum pass, then the race and write.
+//   min-p rows without top-k: what can be kept lies above the sample maximum plus
+//     ln(min_p), so one streaming pass lists it, as for top-k rows; with top-p the pass
+//     also sums the softmax mass of everything below.  Top-k rows raise their cut to the
+//     min-p bound at the end.
 //
 // The method is the one of the Ascend "torch_npu.npu_top_k_top_p_sample" page
 // (topK valid range, topP rule, Sample formulas), MiniMind "Chapter 10: inference
@@ -77,6 +81,7 @@ enum RMisc {
   kMFound = 4,                         // int32: index found by the tie scan
   kMBin = 8, kMAbove = 9, kMHit = 10,  // bin searches
   kMCut = 11, kMBlo = 12, kMBhi = 13,  // list cut, band bounds
+  kMLnMinP = 14,                       // float2: ln(min_p) of the row
   kMCnt = 16,                          // uint32 counter
   kMSeg = 20,                          // uint32[kRW]: per-warp segment counts (8 slots)
   kMPush = 32,                         // [8][kRMaxTeam]: values pushed by the CTAs sharing a row
@@ -809,10 +814,14 @@ __device__ __noinline__ uint32_t rsample_rank(const uint32_t* samp, uint32_t r, 
 // The streaming pass: the -inf background of the filtered row, and every element whose
 // penalised raw value is >= tau_raw (NaN: nothing passes) appended, as (raw key, index),
 // to this warp's segment seg[0..kRSeg).  keep_all: NaN counts as -inf and everything
-// passes.  Returns the warp's count (above kRSeg: the segment overflowed).
-template <bool kBF16>
+// passes.  Returns the warp's count (above kRSeg: the segment overflowed).  kSum: *below gets
+// the thread's sum of exp((x - below_ref) / T) over what did not pass (NaN counts as -inf);
+// the exponent's factor log2(e) / T is carried as two floats, for its rounding would scale
+// every exponent of the row alike.
+template <bool kBF16, bool kSum = false>
 __device__ __forceinline__ uint32_t rk_stream(const RowCtx& rc, float tau_raw, bool keep_all, unsigned long long* seg,
-                                              unsigned long long pol) {
+                                              unsigned long long pol, float below_ref = 0.0f, float2 cs = float2{},
+                                              float* below = nullptr) {
   constexpr int G = kBF16 ? 8 : 4;
   const int lane = threadIdx.x & 31;
   const unsigned lt = (1u << lane) - 1u;
@@ -824,6 +833,7 @@ __device__ __forceinline__ uint32_t rk_stream(const RowCtx& rc, float tau_raw, b
   const float pen = rc.pen;
   const float4 ninf = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
   uint32_t wcnt = 0;
+  float total = 0.0f;
   for (int base = rc.g0; base < g1; base += kRT * kRU) {
     uint4 w[kRU];
 #pragma unroll
@@ -859,6 +869,16 @@ __device__ __forceinline__ uint32_t rk_stream(const RowCtx& rc, float tau_raw, b
         pass[e] = in && v[e] >= tau_raw;
         any |= pass[e];
       }
+      if (kSum && in) {
+        float part = 0.0f;
+#pragma unroll
+        for (int e = 0; e < G; ++e) {
+          const float d = __fsub_rn(v[e], below_ref);
+          const float z = fmaxf(__fmaf_rn(d, cs.x, __fmul_rn(d, cs.y)), -200.0f);  // NaN: 2^-200
+          part += pass[e] ? 0.0f : rex2(z);
+        }
+        total += part;
+      }
       if (__any_sync(kFull, any)) {
 #pragma unroll
         for (int e = 0; e < G; ++e) {
@@ -872,6 +892,7 @@ __device__ __forceinline__ uint32_t rk_stream(const RowCtx& rc, float tau_raw, b
       }
     }
   }
+  if (kSum) *below = total;
   return wcnt;
 }
 
@@ -944,9 +965,11 @@ __device__ __noinline__ int rlist_topp_cut(const unsigned long long* kl, int n, 
 // Top-p over the survivors kl[0..n) (1 < n <= 1024, maximum M): a fixed-point mass
 // histogram over linear bins of [smallest value, M] finds the bin holding the boundary
 // and that bin's entries are ranked pairwise; a large bin is sorted instead.  Returns
-// the last kept entry.  scratch: 2 * kRRank + 1024 u64.
-__device__ __noinline__ Thresh rk_topp(unsigned long long* kl, int n, float M, float p, uint32_t* hist,
-                                       unsigned long long* scratch, unsigned long long* red,
+// the last kept entry.  S_row: the mass that p is a share of where the survivors do not hold
+// all of it (0: their own sum); every survivor is kept when they do not reach the target.
+// scratch: 2 * kRRank + 1024 u64.
+__device__ __noinline__ Thresh rk_topp(unsigned long long* kl, int n, float M, float p, unsigned long long S_row,
+                                       uint32_t* hist, unsigned long long* scratch, unsigned long long* red,
                                        unsigned long long* misc) {
   uint32_t& s_cnt = *reinterpret_cast<uint32_t*>(misc + kMCnt);
   unsigned long long* mass = scratch + 2 * kRRank;
@@ -967,8 +990,9 @@ __device__ __noinline__ Thresh rk_topp(unsigned long long* kl, int n, float M, f
     s_cnt = 0u;
   }
   rblock_sum_max2(part, nmn, dummy, red);
-  const unsigned long long S = part;
+  const unsigned long long S = S_row ? S_row : part;
   const unsigned long long tq = rtopp_target(p, S);
+  if (tq > part) return Thresh{1u, -1};  // only with S_row
   const float lo = kfloat(~static_cast<uint32_t>(nmn));
   const float span = __fsub_rn(M, lo);
   const float s = (span > 0.0f && span < INFINITY) ? __fdiv_rn(static_cast<float>(kRSurvBins), span) : 0.0f;
@@ -1075,7 +1099,6 @@ struct RowSmem {
 
 constexpr Thresh kKeepAll{1u, -1};  // kept_by(any real key) holds; empty slots (key 0) fail
 
-// Top-k and one-element rows; returns the chosen index.
 // The CTAs that work on one row.  C == 1: this CTA alone (barriers are __syncthreads);
 // C > 1: the C CTAs of the thread-block cluster, each on its own part of the row,
 // exchanging partial results through distributed shared memory.
@@ -1120,9 +1143,37 @@ struct Team {
   }
 };
 
+// A team streamed the parts of one row against the same threshold (every member samples the
+// same elements): rank 0 appends the others' warp segments behind its own (a segment that would
+// overflow marks the buffer overflowed) and goes on alone; false for the other members, which
+// leave the row.
+__device__ __forceinline__ bool rk_gather_team(const RowSmem& sm, const Team& tm) {
+  if (tm.C == 1) return true;
+  uint32_t* segcnt = reinterpret_cast<uint32_t*>(sm.misc + kMSeg);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  tm.sync();
+  if (tm.rank == 0) {
+    uint32_t own = segcnt[warp];
+    for (int r = 1; r < tm.C; ++r) {
+      const uint32_t other = *tm.remote(segcnt + warp, r);
+      const unsigned long long* src = tm.remote(sm.cw + warp * kRSeg, r);
+      const bool fits = own <= static_cast<uint32_t>(kRSeg) && other <= static_cast<uint32_t>(kRSeg) &&
+                        own + other <= static_cast<uint32_t>(kRSeg);
+      if (fits)
+        for (uint32_t i = lane; i < other; i += 32) sm.cw[warp * kRSeg + own + i] = src[i];
+      own = fits ? own + other : static_cast<uint32_t>(kRSeg) + 1u;
+    }
+    __syncwarp();
+    if (lane == 0) segcnt[warp] = own;
+  }
+  tm.sync();  // the other members' segments are read
+  return tm.rank == 0;
+}
+
+// Top-k and one-element rows; returns the chosen index.
 template <bool kBF16>
 __device__ __noinline__ int32_t rk_row(const RowCtx& rc, const RowSmem& sm, const Team& tm, uint32_t keff, bool single,
-                                       bool topp_on, float p, float eps, bool exact, bool sampled) {
+                                       bool topp_on, float p, float mp, float eps, bool exact, bool sampled) {
   uint32_t& s_cnt = *reinterpret_cast<uint32_t*>(sm.misc + kMCnt);
   uint32_t* segcnt = reinterpret_cast<uint32_t*>(sm.misc + kMSeg);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1148,31 +1199,11 @@ __device__ __noinline__ int32_t rk_row(const RowCtx& rc, const RowSmem& sm, cons
     // a threshold at or below -inf would take the whole row: go to the exact select
     tau_raw = (tau_key > kKeyNegInf && !isnan(tv)) ? raw_floor(tv, rc.T, rc.identity) : __int_as_float(0x7fffffff);
   }
+  if (mp > 0.0f && threadIdx.x == kRT - 1) *reinterpret_cast<float2*>(sm.misc + kMLnMinP) = ln_min_p(mp);
   const uint32_t wc = rk_stream<kBF16>(rc, tau_raw, keep_all, sm.cw + warp * kRSeg, l2_policy_first());
   if (lane == 0) segcnt[warp] = wc;
   __syncthreads();
-  if (tm.C > 1) {
-    // a team streamed the parts of one row against the same threshold (every member
-    // samples the same elements): rank 0 appends the others' warp segments behind its own
-    // (a segment that would overflow marks the buffer overflowed), then goes on alone
-    tm.sync();
-    if (tm.rank == 0) {
-      uint32_t own = segcnt[warp];
-      for (int r = 1; r < tm.C; ++r) {
-        const uint32_t other = *tm.remote(segcnt + warp, r);
-        const unsigned long long* src = tm.remote(sm.cw + warp * kRSeg, r);
-        const bool fits = own <= static_cast<uint32_t>(kRSeg) && other <= static_cast<uint32_t>(kRSeg) &&
-                          own + other <= static_cast<uint32_t>(kRSeg);
-        if (fits)
-          for (uint32_t i = lane; i < other; i += 32) sm.cw[warp * kRSeg + own + i] = src[i];
-        own = fits ? own + other : static_cast<uint32_t>(kRSeg) + 1u;
-      }
-      __syncwarp();
-      if (lane == 0) segcnt[warp] = own;
-    }
-    tm.sync();  // the other members' segments are read; they leave the row
-    if (tm.rank != 0) return -1;
-  }
+  if (!rk_gather_team(sm, tm)) return -1;
   bool over = false;
 #pragma unroll
   for (int w = 0; w < kRW; ++w) over |= segcnt[w] > static_cast<uint32_t>(kRSeg);
@@ -1212,7 +1243,8 @@ __device__ __noinline__ int32_t rk_row(const RowCtx& rc, const RowSmem& sm, cons
   const Thresh tk = n > keff ? rbuf_kth(sm.cw, kRCap, keff, mx, mn, sm.hist, sm.wbuf, sm.red, sm.misc) : kKeepAll;
   const int ns = rbuf_gather(sm.cw, kRCap, tk, sm.wbuf, kTopKMax, sm.red);  // the k survivors
   Thresh th = kKeepAll;
-  if (topp_on && ns > 1) th = rk_topp(sm.wbuf, ns, M, p, sm.hist, sm.cw, sm.red, sm.misc);
+  if (topp_on && ns > 1) th = rk_topp(sm.wbuf, ns, M, p, 0ull, sm.hist, sm.cw, sm.red, sm.misc);
+  if (mp > 0.0f) th = with_min_p(th, *reinterpret_cast<const float2*>(sm.misc + kMLnMinP), M);
   unsigned long long rb = 0, first = 0;
   rlist_race(sm.wbuf, ns, th, M, rc, eps, rb, first);
   rblock_max2(rb, first, sm.red);
@@ -1333,6 +1365,139 @@ __device__ __noinline__ int32_t rrow_first_max(const RowCtx& rc, float M, unsign
   });
   rblock_max2(best, dummy, red);
   return static_cast<int32_t>(~static_cast<uint32_t>(best));
+}
+
+// The exact selection over a whole row without top-k, by one CTA: top-p (topp), then min-p
+// (mp > 0), the race and the write.
+template <bool kBF16>
+__device__ __noinline__ int32_t rexact_row(const RowCtx& whole, const RowSmem& sm, bool topp, float p, float mp,
+                                           float eps) {
+  if (mp > 0.0f && threadIdx.x == kRT - 1) *reinterpret_cast<float2*>(sm.misc + kMLnMinP) = ln_min_p(mp);
+  const float M = rmax_transformed(rrow_max_key<kBF16>(whole, l2_policy_last(), sm.red), whole);
+  Thresh th{0u, INT_MAX};
+  if (topp) {
+    unsigned long long part = 0;
+    rrow_pass<kBF16>(whole, l2_policy_normal(), [&](bool valid, float y, uint32_t, int) {
+      if (valid) part += fixed_mass(softmax_weight(y, M));
+    });
+    const unsigned long long tq = rtopp_target(p, rblock_sum_u64(part, sm.red));
+    th = rrow_select<kBF16, true>(whole, tq, M, sm.hist, sm.red, sm.misc);
+  }
+  if (mp > 0.0f) th = with_min_p(th, *reinterpret_cast<const float2*>(sm.misc + kMLnMinP), M);
+  unsigned long long rb, first;
+  rrow_race_write<kBF16>(whole, th, M, eps, l2_policy_normal(), sm.red, &rb, &first);
+  return static_cast<int32_t>(~static_cast<uint32_t>(rb ? rb : first));
+}
+
+// ---- min-p rows without top-k ----------------------------------------------------------------
+
+// exp(below_ref / T - M) for the raw value below_ref: the quotient carried as two floats.
+__device__ __forceinline__ float rscale_to_max(float below_ref, float T, float M) {
+  const float q = __fdiv_rn(below_ref, T);
+  const float ql = __fdiv_rn(__fmaf_rn(-q, T, below_ref), T);
+  const float s = __fsub_rn(q, M);
+  const float b = __fsub_rn(s, q);
+  const float lo = __fadd_rn(__fadd_rn(__fsub_rn(q, __fsub_rn(s, b)), __fsub_rn(-M, b)), ql);
+  const float e = expf(s);
+  return __fmaf_rn(e, lo, e);
+}
+
+// A row whose top-k is off and whose min-p is on (mp in (0, 1]); returns the chosen index.
+// Everything that can be kept is at least M + ln(mp), and M is at least the sample's maximum:
+// one streaming pass lists what reaches that (the true maximum is always among it).  With top-p
+// the pass also sums the mass of everything it does not list, for p is a share of the whole row's.
+template <bool kBF16>
+__device__ __noinline__ int32_t rm_row(const RowCtx& rc, const RowSmem& sm, const Team& tm, bool topp_on, float p,
+                                       float mp, float eps, bool exact, bool sampled) {
+  uint32_t* segcnt = reinterpret_cast<uint32_t*>(sm.misc + kMSeg);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  RowCtx whole = rc;
+  whole.g0 = 0;
+  whole.g1 = rc.nv;
+  if (exact) return tm.rank == 0 ? rexact_row<kBF16>(whole, sm, topp_on, p, mp, eps) : -1;
+  const bool keep_all = rc.V <= kRKeepAllV;
+  float tau_raw = -INFINITY, below_ref = 0.0f;
+  if (!keep_all) {
+    uint32_t* samp = reinterpret_cast<uint32_t*>(sm.wbuf);
+    if (!sampled) rsample_load<kBF16>(whole, samp);
+    unsigned long long a = 0, b = 0;
+    for (int i = threadIdx.x; i < kRSamp; i += kRT) a = samp[i] > a ? samp[i] : a;
+    rblock_max2(a, b, sm.red);
+    const float ms = kfloat(static_cast<uint32_t>(a));
+    // a lower bound of ms + ln(mp): logf is within 2^-22 relative and 2^-22
+    const float l = logf(mp);
+    const float tv = __fadd_rd(ms, __fsub_rd(l, __fmaf_rn(fabsf(l), 0x1p-20f, 0x1p-20f)));
+    tau_raw = tv > -INFINITY ? raw_floor(tv, rc.T, rc.identity) : __int_as_float(0x7fffffff);
+    below_ref = __fmul_rn(ms, rc.T);
+  }
+  if (threadIdx.x == kRT - 1) *reinterpret_cast<float2*>(sm.misc + kMLnMinP) = ln_min_p(mp);
+  uint32_t wc;
+  unsigned long long below = 0;  // in units of 2^-32 of exp(below_ref / T)
+  if (topp_on) {
+    constexpr float kLog2eHi = 1.44269502162933349609f, kLog2eLo = 1.92596299112661746887e-8f;
+    const float hi = __fdiv_rn(kLog2eHi, rc.T);
+    const float lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-hi, rc.T, kLog2eHi), kLog2eLo), rc.T);
+    float part;
+    wc = rk_stream<kBF16, true>(rc, tau_raw, keep_all, sm.cw + warp * kRSeg, l2_policy_first(), below_ref,
+                                make_float2(hi, lo), &part);
+    below = rblock_sum_u64(__float2ull_rn(__fmul_rn(part, 4294967296.0f)), sm.red);
+    tm.push(sm.misc, 0, below);
+  } else {
+    wc = rk_stream<kBF16>(rc, tau_raw, keep_all, sm.cw + warp * kRSeg, l2_policy_first());
+  }
+  if (lane == 0) segcnt[warp] = wc;
+  __syncthreads();
+  if (!rk_gather_team(sm, tm)) return -1;
+  if (topp_on) below = tm.sum_of(sm.misc, 0);
+  bool over = false;
+#pragma unroll
+  for (int w = 0; w < kRW; ++w) over |= segcnt[w] > static_cast<uint32_t>(kRSeg);
+  unsigned long long top;
+  uint32_t mn;
+  const uint32_t n = rk_normalize(sm.cw, segcnt, 0u, rc.div, rc.identity, sm.red, &top, &mn);
+  // the list overflowed, or the sample says nothing (all -inf): the exact selection
+  if (over || n == 0u) return rexact_row<kBF16>(whole, sm, topp_on, p, mp, eps);
+  const float M = kfloat(static_cast<uint32_t>(top >> 32));
+  Thresh th = with_min_p(kKeepAll, *reinterpret_cast<const float2*>(sm.misc + kMLnMinP), M);
+  const unsigned long long* list = sm.cw;
+  int len = kRCap;
+  if (topp_on) {
+    unsigned long long S = 0;
+    for (int i = threadIdx.x; i < kRCap; i += kRT) {
+      const uint32_t key = static_cast<uint32_t>(sm.cw[i] >> 32);
+      if (key) S += fixed_mass(softmax_weight(kfloat(key), M));
+    }
+    S = rblock_sum_u64(S, sm.red);
+    if (!keep_all && below) {
+      const unsigned long long f = fixed_mass(fminf(rscale_to_max(below_ref, rc.T, M), 1.0f));
+      S += (__umul64hi(below, f) << 32) | ((below * f) >> 32);
+    }
+    const int ns = rbuf_gather(sm.cw, kRCap, th, sm.wbuf, kTopKMax, sm.red);
+    if (ns < kTopKMax) {
+      th = rk_topp(sm.wbuf, ns, M, p, S, sm.hist, sm.cw, sm.red, sm.misc);
+      list = sm.wbuf;
+      len = ns;
+    } else {
+      // more survivors than rk_topp takes: sorted whole
+      for (int i = threadIdx.x; i < kRCap; i += kRT) {
+        const unsigned long long w = sm.cw[i];
+        if (!kept_by(static_cast<uint32_t>(w >> 32), static_cast<int32_t>(~static_cast<uint32_t>(w)), th.key, th.idx))
+          sm.cw[i] = 0ull;
+      }
+      const int nk = rcompact_nonzero(sm.cw, sm.red);
+      if (nk > kRSortMax) return rexact_row<kBF16>(whole, sm, topp_on, p, mp, eps);
+      int N = 1;
+      while (N < nk) N <<= 1;
+      rbitonic_desc(sm.cw, N);
+      const int L = rlist_topp_cut(sm.cw, nk, M, 0ull, rtopp_target(p, S), sm.red, sm.misc);
+      if (L > 0) th = Thresh{static_cast<uint32_t>(sm.cw[L - 1] >> 32), static_cast<int32_t>(~static_cast<uint32_t>(sm.cw[L - 1]))};
+      len = nk;
+    }
+  }
+  unsigned long long rb = 0, first = 0;
+  rlist_race(list, len, th, M, rc, eps, rb, first);
+  rblock_max2(rb, first, sm.red);
+  return static_cast<int32_t>(~static_cast<uint32_t>(rb ? rb : first));
 }
 
 // ---- top-p-only rows: pass A (histogram), pass B (race, write, band) -------------------
@@ -1643,21 +1808,7 @@ __device__ __noinline__ int32_t rwide_row(const RowCtx& rc, const RowSmem& sm, c
   whole.g0 = 0;
   whole.g1 = rc.nv;
   // the exact whole-row selection, by rank 0 alone (the other members leave the row)
-  auto exact_row = [&]() -> int32_t {
-    const float M = rmax_transformed(rrow_max_key<kBF16>(whole, l2_policy_last(), sm.red), whole);
-    Thresh th{0u, INT_MAX};
-    if (topp) {
-      unsigned long long part = 0;
-      rrow_pass<kBF16>(whole, l2_policy_normal(), [&](bool valid, float y, uint32_t, int) {
-        if (valid) part += fixed_mass(softmax_weight(y, M));
-      });
-      const unsigned long long tq = rtopp_target(p, rblock_sum_u64(part, sm.red));
-      th = rrow_select<kBF16, true>(whole, tq, M, sm.hist, sm.red, sm.misc);
-    }
-    unsigned long long rb, first;
-    rrow_race_write<kBF16>(whole, th, M, eps, l2_policy_normal(), sm.red, &rb, &first);
-    return static_cast<int32_t>(~static_cast<uint32_t>(rb ? rb : first));
-  };
+  auto exact_row = [&]() -> int32_t { return rexact_row<kBF16>(whole, sm, topp, p, 0.0f, eps); };
   if (exact) return tm.rank == 0 ? exact_row() : -1;
   if (!topp) {
     // keep-all: the maximum, then the race and the write of every part
@@ -2223,7 +2374,8 @@ __device__ __forceinline__ void rseen_copy(const uint32_t* src, int V, uint32_t*
 struct RowFlags {
   int32_t k;
   float p;
-  bool pen_on, single, topp_on;
+  bool pen_on, single, topk_on, topp_on;
+  float mp;        // min-p in (0, 1], or 0: off
   int32_t b0, b1;  // the row's seen ids
 };
 template <bool kBF16>
@@ -2240,7 +2392,9 @@ __device__ __forceinline__ RowFlags row_setup(const Params& P, int64_t row, cons
   f.pen_on = ((P.seen_indptr && P.seen_ids) || P.seen_bits) && P.penalty && (P.penalty[row] > 0.0f);
   const bool topk_on = f.k >= 1 && static_cast<int64_t>(f.k) <= (P.V < kTopKMax ? P.V : kTopKMax);
   const bool p_nan = isnan(f.p);
+  f.topk_on = topk_on;
   f.single = greedyT || (!p_nan && f.p <= 0.0f) || (topk_on && f.k == 1);
+  f.mp = f.single ? 0.0f : row_min_p(P, row);
   f.topp_on = !f.single && !p_nan && f.p > 0.0f && f.p < 1.0f;
   RowCtx& rc = *rcp;
   rc.x = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(P.logits) + row * P.V * esize);
@@ -2418,9 +2572,11 @@ __global__ void __launch_bounds__(kRT, 2) kps_row_kernel(const Params P) {
     const bool sample = !wide && !P.exact && P.V > kRKeepAllV;
     const RowFlags f = row_setup<kBF16>(P, row, sm, tm.rank, tm.C, &rc, sample);
     int32_t chosen;
-    if (!wide) {
-      chosen = rk_row<kBF16>(rc, sm, tm, f.single ? 1u : static_cast<uint32_t>(f.k), f.single, f.topp_on, f.p, P.eps,
-                             P.exact != 0, sample);
+    if (!wide && f.mp > 0.0f && !f.topk_on) {
+      chosen = rm_row<kBF16>(rc, sm, tm, f.topp_on, f.p, f.mp, P.eps, P.exact != 0, sample);
+    } else if (!wide) {
+      chosen = rk_row<kBF16>(rc, sm, tm, f.single ? 1u : static_cast<uint32_t>(f.k), f.single, f.topp_on, f.p, f.mp,
+                             P.eps, P.exact != 0, sample);
     } else {
       PRec rec;
       if (!shared_rows && P.pre && row_prepass(P, row)) {

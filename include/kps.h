@@ -211,6 +211,30 @@ kps_status kps_sample_step(const void* logits, kps_dtype dt, int64_t B, int64_t 
                            int need_logits, int64_t* out_idx, float* out_filtered,
                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * kps_sample_min_p — kps_sample_step with one more stage, after top-p:
+ *
+ *   min-p: keep the elements whose softmax probability is at least min_p[b]
+ *          times the row's largest, exp(y - max) >= min_p[b] with y the
+ *          penalised value over the temperature (elements equal to the largest
+ *          weigh 1; the order's first is always kept).
+ *
+ * min_p [B] fp32: a value <= 0 or NaN skips the stage for that row, a value
+ * above 1 counts as 1 (every element equal to the maximum is kept).  The
+ * condition is on the value, so what is kept is still a prefix of the order,
+ * the shorter of the top-p one and the min-p one; top-p's share stays that of
+ * the set top-k left.  The comparison decides as 64-bit arithmetic on the fp32
+ * values y would.  The race, the sampling-off choice, the filtered logits and
+ * every option of opts (required) work over the kept set as in kps_sample_step.
+ * (The method's pages have no min-p.)
+ */
+kps_status kps_sample_min_p(const void* logits, kps_dtype dt, int64_t B, int64_t V,
+                            const int32_t* top_k, const float* top_p, const float* min_p,
+                            const float* temperature, const int32_t* seen_indptr,
+                            const int32_t* seen_ids, const float* penalty, const kps_step_opts* opts,
+                            float eps, int need_logits, int64_t* out_idx, float* out_filtered,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Reads (and clears) the device status word of a workspace: waits for the
  * stream, stores KPS_OK or the first device-side error code in *out. */
 kps_status kps_last_device_status(void* workspace, cudaStream_t stream, int* out);
