@@ -14,7 +14,7 @@ import subprocess
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRCS = [os.path.join(PKG, "csrc", f) for f in ("kps.cu", "kps_top.cu", "kps_distill.cu")]
+SRCS = [os.path.join(PKG, "csrc", f) for f in ("kps.cu", "kps_min_p.cu", "kps_top.cu", "kps_distill.cu")]
 SRC = SRCS[0]
 HDR = os.path.join(ROOT, "include", "kps.h")
 LIB = os.path.join(PKG, "libkps.so")

@@ -14,4 +14,11 @@ struct NvtxRange {
   NvtxRange& operator=(const NvtxRange&) = delete;
 };
 
+// What the calling thread's last sampling call launched: the kernel (1 cluster, 2 row), how many
+// kernels, and the CTAs per cluster; zeros before the first.
+struct LastCall {
+  int kernel, launches, cluster;
+};
+LastCall& last_call();
+
 }  // namespace kps

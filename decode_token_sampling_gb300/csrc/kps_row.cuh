@@ -1,4 +1,4 @@
-// kps_row.cuh — the one-CTA-per-row kernel (included by kps.cu inside namespace kps).
+// kps_row.cuh — the one-CTA-per-row kernel (included by kps_sampler.cuh inside namespace kps).
 //
 // For batches that fill the GPU every CTA takes whole rows on its own: the row is
 // read straight from global memory with 16-byte loads (several in flight per
@@ -34,7 +34,7 @@
 // of seen ids).  The kernel never waits on another CTA or on memory it does not
 // load itself, so it has no timeouts.
 
-static_assert(kThreads == 512, "the block helpers of kps.cu assume 512 threads");
+static_assert(kThreads == 512, "the block helpers of kps_sampler.cuh assume 512 threads");
 
 constexpr int kRT = kThreads;           // threads per CTA
 constexpr int kRW = kRT / 32;
@@ -82,6 +82,8 @@ enum RMisc {
   kMBin = 8, kMAbove = 9, kMHit = 10,  // bin searches
   kMCut = 11, kMBlo = 12, kMBhi = 13,  // list cut, band bounds
   kMLnMinP = 14,                       // float2: ln(min_p) of the row
+  kMMinP = 15,                         // float: the row's min-p (0: off)
+  kMRowMass = 17,                      // the whole row's mass (min-p rows with top-p)
   kMCnt = 16,                          // uint32 counter
   kMSeg = 20,                          // uint32[kRW]: per-warp segment counts (8 slots)
   kMPush = 32,                         // [8][kRMaxTeam]: values pushed by the CTAs sharing a row
@@ -965,11 +967,11 @@ __device__ __noinline__ int rlist_topp_cut(const unsigned long long* kl, int n, 
 // Top-p over the survivors kl[0..n) (1 < n <= 1024, maximum M): a fixed-point mass
 // histogram over linear bins of [smallest value, M] finds the bin holding the boundary
 // and that bin's entries are ranked pairwise; a large bin is sorted instead.  Returns
-// the last kept entry.  S_row: the mass that p is a share of where the survivors do not hold
-// all of it (0: their own sum); every survivor is kept when they do not reach the target.
-// scratch: 2 * kRRank + 1024 u64.
-__device__ __noinline__ Thresh rk_topp(unsigned long long* kl, int n, float M, float p, unsigned long long S_row,
-                                       uint32_t* hist, unsigned long long* scratch, unsigned long long* red,
+// the last kept entry.  kRow: p is a share of misc[kMRowMass] instead of the survivors' own
+// sum; every survivor is kept when they do not reach the target.  scratch: 2 * kRRank + 1024 u64.
+template <bool kRow = false>
+__device__ __noinline__ Thresh rk_topp(unsigned long long* kl, int n, float M, float p, uint32_t* hist,
+                                       unsigned long long* scratch, unsigned long long* red,
                                        unsigned long long* misc) {
   uint32_t& s_cnt = *reinterpret_cast<uint32_t*>(misc + kMCnt);
   unsigned long long* mass = scratch + 2 * kRRank;
@@ -990,9 +992,9 @@ __device__ __noinline__ Thresh rk_topp(unsigned long long* kl, int n, float M, f
     s_cnt = 0u;
   }
   rblock_sum_max2(part, nmn, dummy, red);
-  const unsigned long long S = S_row ? S_row : part;
+  const unsigned long long S = kRow ? misc[kMRowMass] : part;
   const unsigned long long tq = rtopp_target(p, S);
-  if (tq > part) return Thresh{1u, -1};  // only with S_row
+  if (kRow && tq > part) return Thresh{1u, -1};
   const float lo = kfloat(~static_cast<uint32_t>(nmn));
   const float span = __fsub_rn(M, lo);
   const float s = (span > 0.0f && span < INFINITY) ? __fdiv_rn(static_cast<float>(kRSurvBins), span) : 0.0f;
@@ -1173,7 +1175,8 @@ __device__ __forceinline__ bool rk_gather_team(const RowSmem& sm, const Team& tm
 // Top-k and one-element rows; returns the chosen index.
 template <bool kBF16>
 __device__ __noinline__ int32_t rk_row(const RowCtx& rc, const RowSmem& sm, const Team& tm, uint32_t keff, bool single,
-                                       bool topp_on, float p, float mp, float eps, bool exact, bool sampled) {
+                                       bool topp_on, float p, float eps, bool exact, bool sampled) {
+  const float mp = kMinP ? *reinterpret_cast<const float*>(sm.misc + kMMinP) : 0.0f;
   uint32_t& s_cnt = *reinterpret_cast<uint32_t*>(sm.misc + kMCnt);
   uint32_t* segcnt = reinterpret_cast<uint32_t*>(sm.misc + kMSeg);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1243,7 +1246,7 @@ __device__ __noinline__ int32_t rk_row(const RowCtx& rc, const RowSmem& sm, cons
   const Thresh tk = n > keff ? rbuf_kth(sm.cw, kRCap, keff, mx, mn, sm.hist, sm.wbuf, sm.red, sm.misc) : kKeepAll;
   const int ns = rbuf_gather(sm.cw, kRCap, tk, sm.wbuf, kTopKMax, sm.red);  // the k survivors
   Thresh th = kKeepAll;
-  if (topp_on && ns > 1) th = rk_topp(sm.wbuf, ns, M, p, 0ull, sm.hist, sm.cw, sm.red, sm.misc);
+  if (topp_on && ns > 1) th = rk_topp(sm.wbuf, ns, M, p, sm.hist, sm.cw, sm.red, sm.misc);
   if (mp > 0.0f) th = with_min_p(th, *reinterpret_cast<const float2*>(sm.misc + kMLnMinP), M);
   unsigned long long rb = 0, first = 0;
   rlist_race(sm.wbuf, ns, th, M, rc, eps, rb, first);
@@ -1370,7 +1373,7 @@ __device__ __noinline__ int32_t rrow_first_max(const RowCtx& rc, float M, unsign
 // The exact selection over a whole row without top-k, by one CTA: top-p (topp), then min-p
 // (mp > 0), the race and the write.
 template <bool kBF16>
-__device__ __noinline__ int32_t rexact_row(const RowCtx& whole, const RowSmem& sm, bool topp, float p, float mp,
+__device__ __forceinline__ int32_t rexact_row(const RowCtx& whole, const RowSmem& sm, bool topp, float p, float mp,
                                            float eps) {
   if (mp > 0.0f && threadIdx.x == kRT - 1) *reinterpret_cast<float2*>(sm.misc + kMLnMinP) = ln_min_p(mp);
   const float M = rmax_transformed(rrow_max_key<kBF16>(whole, l2_policy_last(), sm.red), whole);
@@ -1402,19 +1405,27 @@ __device__ __forceinline__ float rscale_to_max(float below_ref, float T, float M
   return __fmaf_rn(e, lo, e);
 }
 
+// The same out of line: the fallback of the min-p rows.
+template <bool kBF16>
+__device__ __noinline__ int32_t rexact_min_p_row(const RowCtx& whole, const RowSmem& sm, bool topp, float p, float mp,
+                                                 float eps) {
+  return rexact_row<kBF16>(whole, sm, topp, p, mp, eps);
+}
+
 // A row whose top-k is off and whose min-p is on (mp in (0, 1]); returns the chosen index.
 // Everything that can be kept is at least M + ln(mp), and M is at least the sample's maximum:
 // one streaming pass lists what reaches that (the true maximum is always among it).  With top-p
 // the pass also sums the mass of everything it does not list, for p is a share of the whole row's.
 template <bool kBF16>
 __device__ __noinline__ int32_t rm_row(const RowCtx& rc, const RowSmem& sm, const Team& tm, bool topp_on, float p,
-                                       float mp, float eps, bool exact, bool sampled) {
+                                       float eps, bool exact, bool sampled) {
+  const float mp = *reinterpret_cast<const float*>(sm.misc + kMMinP);
   uint32_t* segcnt = reinterpret_cast<uint32_t*>(sm.misc + kMSeg);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   RowCtx whole = rc;
   whole.g0 = 0;
   whole.g1 = rc.nv;
-  if (exact) return tm.rank == 0 ? rexact_row<kBF16>(whole, sm, topp_on, p, mp, eps) : -1;
+  if (exact) return tm.rank == 0 ? rexact_min_p_row<kBF16>(whole, sm, topp_on, p, mp, eps) : -1;
   const bool keep_all = rc.V <= kRKeepAllV;
   float tau_raw = -INFINITY, below_ref = 0.0f;
   if (!keep_all) {
@@ -1456,7 +1467,7 @@ __device__ __noinline__ int32_t rm_row(const RowCtx& rc, const RowSmem& sm, cons
   uint32_t mn;
   const uint32_t n = rk_normalize(sm.cw, segcnt, 0u, rc.div, rc.identity, sm.red, &top, &mn);
   // the list overflowed, or the sample says nothing (all -inf): the exact selection
-  if (over || n == 0u) return rexact_row<kBF16>(whole, sm, topp_on, p, mp, eps);
+  if (over || n == 0u) return rexact_min_p_row<kBF16>(whole, sm, topp_on, p, mp, eps);
   const float M = kfloat(static_cast<uint32_t>(top >> 32));
   Thresh th = with_min_p(kKeepAll, *reinterpret_cast<const float2*>(sm.misc + kMLnMinP), M);
   const unsigned long long* list = sm.cw;
@@ -1472,9 +1483,10 @@ __device__ __noinline__ int32_t rm_row(const RowCtx& rc, const RowSmem& sm, cons
       const unsigned long long f = fixed_mass(fminf(rscale_to_max(below_ref, rc.T, M), 1.0f));
       S += (__umul64hi(below, f) << 32) | ((below * f) >> 32);
     }
+    if (threadIdx.x == 0) sm.misc[kMRowMass] = S;  // published by the gather's barriers
     const int ns = rbuf_gather(sm.cw, kRCap, th, sm.wbuf, kTopKMax, sm.red);
     if (ns < kTopKMax) {
-      th = rk_topp(sm.wbuf, ns, M, p, S, sm.hist, sm.cw, sm.red, sm.misc);
+      th = rk_topp<true>(sm.wbuf, ns, M, p, sm.hist, sm.cw, sm.red, sm.misc);
       list = sm.wbuf;
       len = ns;
     } else {
@@ -1485,7 +1497,7 @@ __device__ __noinline__ int32_t rm_row(const RowCtx& rc, const RowSmem& sm, cons
           sm.cw[i] = 0ull;
       }
       const int nk = rcompact_nonzero(sm.cw, sm.red);
-      if (nk > kRSortMax) return rexact_row<kBF16>(whole, sm, topp_on, p, mp, eps);
+      if (nk > kRSortMax) return rexact_min_p_row<kBF16>(whole, sm, topp_on, p, mp, eps);
       int N = 1;
       while (N < nk) N <<= 1;
       rbitonic_desc(sm.cw, N);
@@ -2394,7 +2406,8 @@ __device__ __forceinline__ RowFlags row_setup(const Params& P, int64_t row, cons
   const bool p_nan = isnan(f.p);
   f.topk_on = topk_on;
   f.single = greedyT || (!p_nan && f.p <= 0.0f) || (topk_on && f.k == 1);
-  f.mp = f.single ? 0.0f : row_min_p(P, row);
+  f.mp = kMinP && !f.single ? row_min_p(P, row) : 0.0f;
+  if (kMinP && threadIdx.x == 0) *reinterpret_cast<float*>(sm.misc + kMMinP) = f.mp;  // read after the barriers below
   f.topp_on = !f.single && !p_nan && f.p > 0.0f && f.p < 1.0f;
   RowCtx& rc = *rcp;
   rc.x = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(P.logits) + row * P.V * esize);
@@ -2572,11 +2585,11 @@ __global__ void __launch_bounds__(kRT, 2) kps_row_kernel(const Params P) {
     const bool sample = !wide && !P.exact && P.V > kRKeepAllV;
     const RowFlags f = row_setup<kBF16>(P, row, sm, tm.rank, tm.C, &rc, sample);
     int32_t chosen;
-    if (!wide && f.mp > 0.0f && !f.topk_on) {
-      chosen = rm_row<kBF16>(rc, sm, tm, f.topp_on, f.p, f.mp, P.eps, P.exact != 0, sample);
+    if (kMinP && !wide && f.mp > 0.0f && !f.topk_on) {
+      chosen = rm_row<kBF16>(rc, sm, tm, f.topp_on, f.p, P.eps, P.exact != 0, sample);
     } else if (!wide) {
-      chosen = rk_row<kBF16>(rc, sm, tm, f.single ? 1u : static_cast<uint32_t>(f.k), f.single, f.topp_on, f.p, f.mp,
-                             P.eps, P.exact != 0, sample);
+      chosen = rk_row<kBF16>(rc, sm, tm, f.single ? 1u : static_cast<uint32_t>(f.k), f.single, f.topp_on, f.p, P.eps,
+                             P.exact != 0, sample);
     } else {
       PRec rec;
       if (!shared_rows && P.pre && row_prepass(P, row)) {
