@@ -23,10 +23,10 @@
 //     mass S, races and writes every element above the band and collects the band,
 //     which is sorted and cut exactly.  Pass A keeps the row in L2 for pass B.
 //   keep-all rows (no top-k, p >= 1): a maximum pass, then the race and write.
-//   min-p rows without top-k: what can be kept lies above the sample maximum plus
-//     ln(min_p), so one streaming pass lists it, as for top-k rows; with top-p the pass
-//     also sums the softmax mass of everything below.  Top-k rows raise their cut to the
-//     min-p bound at the end.
+//   min-p rows without top-k: what can be kept lies above the largest value seen so
+//     far plus T ln(min_p), so one streaming pass lists it, thinning the list as that
+//     value grows; with top-p the pass also sums the softmax mass of everything else.
+//     Top-k rows raise their cut to the min-p bound at the end.
 //
 // The method is the one of the Ascend "torch_npu.npu_top_k_top_p_sample" page
 // (topK valid range, topP rule, Sample formulas), MiniMind "Chapter 10: inference
@@ -84,6 +84,7 @@ enum RMisc {
   kMLnMinP = 14,                       // float2: ln(min_p) of the row
   kMMinP = 15,                         // float: the row's min-p (0: off)
   kMRowMass = 17,                      // the whole row's mass (min-p rows with top-p)
+  kMRunMax = 18,                       // uint32: key of the largest raw value so far (min-p rows)
   kMCnt = 16,                          // uint32 counter
   kMSeg = 20,                          // uint32[kRW]: per-warp segment counts (8 slots)
   kMPush = 32,                         // [8][kRMaxTeam]: values pushed by the CTAs sharing a row
@@ -816,14 +817,10 @@ __device__ __noinline__ uint32_t rsample_rank(const uint32_t* samp, uint32_t r, 
 // The streaming pass: the -inf background of the filtered row, and every element whose
 // penalised raw value is >= tau_raw (NaN: nothing passes) appended, as (raw key, index),
 // to this warp's segment seg[0..kRSeg).  keep_all: NaN counts as -inf and everything
-// passes.  Returns the warp's count (above kRSeg: the segment overflowed).  kSum: *below gets
-// the thread's sum of exp((x - below_ref) / T) over what did not pass (NaN counts as -inf);
-// the exponent's factor log2(e) / T is carried as two floats, for its rounding would scale
-// every exponent of the row alike.
-template <bool kBF16, bool kSum = false>
+// passes.  Returns the warp's count (above kRSeg: the segment overflowed).
+template <bool kBF16>
 __device__ __forceinline__ uint32_t rk_stream(const RowCtx& rc, float tau_raw, bool keep_all, unsigned long long* seg,
-                                              unsigned long long pol, float below_ref = 0.0f, float2 cs = float2{},
-                                              float* below = nullptr) {
+                                              unsigned long long pol) {
   constexpr int G = kBF16 ? 8 : 4;
   const int lane = threadIdx.x & 31;
   const unsigned lt = (1u << lane) - 1u;
@@ -835,7 +832,6 @@ __device__ __forceinline__ uint32_t rk_stream(const RowCtx& rc, float tau_raw, b
   const float pen = rc.pen;
   const float4 ninf = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
   uint32_t wcnt = 0;
-  float total = 0.0f;
   for (int base = rc.g0; base < g1; base += kRT * kRU) {
     uint4 w[kRU];
 #pragma unroll
@@ -871,16 +867,6 @@ __device__ __forceinline__ uint32_t rk_stream(const RowCtx& rc, float tau_raw, b
         pass[e] = in && v[e] >= tau_raw;
         any |= pass[e];
       }
-      if (kSum && in) {
-        float part = 0.0f;
-#pragma unroll
-        for (int e = 0; e < G; ++e) {
-          const float d = __fsub_rn(v[e], below_ref);
-          const float z = fmaxf(__fmaf_rn(d, cs.x, __fmul_rn(d, cs.y)), -200.0f);  // NaN: 2^-200
-          part += pass[e] ? 0.0f : rex2(z);
-        }
-        total += part;
-      }
       if (__any_sync(kFull, any)) {
 #pragma unroll
         for (int e = 0; e < G; ++e) {
@@ -894,7 +880,6 @@ __device__ __forceinline__ uint32_t rk_stream(const RowCtx& rc, float tau_raw, b
       }
     }
   }
-  if (kSum) *below = total;
   return wcnt;
 }
 
@@ -1394,10 +1379,10 @@ __device__ __forceinline__ int32_t rexact_row(const RowCtx& whole, const RowSmem
 
 // ---- min-p rows without top-k ----------------------------------------------------------------
 
-// exp(below_ref / T - M) for the raw value below_ref: the quotient carried as two floats.
-__device__ __forceinline__ float rscale_to_max(float below_ref, float T, float M) {
-  const float q = __fdiv_rn(below_ref, T);
-  const float ql = __fdiv_rn(__fmaf_rn(-q, T, below_ref), T);
+// exp(x / T - M) for a raw value x near the maximum: the quotient carried as two floats.
+__device__ __forceinline__ float rscale_to_max(float x, float T, float M) {
+  const float q = __fdiv_rn(x, T);
+  const float ql = __fdiv_rn(__fmaf_rn(-q, T, x), T);
   const float s = __fsub_rn(q, M);
   const float b = __fsub_rn(s, q);
   const float lo = __fadd_rn(__fadd_rn(__fsub_rn(q, __fsub_rn(s, b)), __fsub_rn(-M, b)), ql);
@@ -1405,7 +1390,162 @@ __device__ __forceinline__ float rscale_to_max(float below_ref, float T, float M
   return __fmaf_rn(e, lo, e);
 }
 
-// The same out of line: the fallback of the min-p rows.
+// What the warps of a min-p row's pass work with.
+struct MinPScan {
+  float reach;   // T ln(min_p): how far under the maximum a kept raw value can lie
+  float tiny;    // 1e-30 T: magnitudes whose quotients by T have room above the subnormals
+  float2 c;      // log2(e) / T as two floats: its rounding would scale every exponent of the row alike
+  // A raw value below which nothing can be kept once xm has been seen (penalised raw values).
+  // The roundings of both quotients and of reach come to less than 2^-20 of |xm| + |reach|.
+  __device__ __forceinline__ float floor(float xm) const {
+    const float m = fabsf(xm) + fabsf(reach);
+    return m >= tiny ? __fsub_rd(__fadd_rd(xm, reach), m * 0x1p-20f) : -INFINITY;
+  }
+  // exp((x - ref) / T) for x <= ref; 0 for NaN and -inf.
+  __device__ __forceinline__ float weight(float x, float ref) const {
+    const float d = __fsub_rn(x, ref);
+    return rex2(fmaxf(__fmaf_rn(d, c.x, __fmul_rn(d, c.y)), -200.0f));
+  }
+};
+
+// Drops the entries of seg[0..n) below t, keeping their order; the dropped ones' weights go to
+// *total (kSum).  One warp; returns the count left.
+template <bool kSum>
+__device__ __forceinline__ uint32_t rm_thin(unsigned long long* seg, uint32_t n, float t, float ref, const MinPScan& sc,
+                                            float* total) {
+  const int lane = threadIdx.x & 31;
+  const unsigned lt = (1u << lane) - 1u;
+  uint32_t kept = 0;
+  __syncwarp();
+  for (uint32_t i = 0; i < n; i += 32) {
+    const bool in = i + lane < n;
+    const unsigned long long w = in ? seg[i + lane] : 0ull;
+    const float x = kfloat(static_cast<uint32_t>(w >> 32));
+    const bool keep = in && x >= t;
+    if (kSum && in && !keep) *total += sc.weight(x, ref);
+    const unsigned m = __ballot_sync(kFull, keep);  // every lane has read its entry
+    if (keep) seg[kept + __popc(m & lt)] = w;       // at or before the entries read
+    kept += __popc(m);
+  }
+  __syncwarp();
+  return kept;
+}
+
+// The pass of a min-p row: the -inf background of the filtered row, and everything that can
+// still be kept, as (raw key, index), in this warp's segment.  The bound follows the largest
+// value that any warp of the block has seen; a segment that fills up is thinned with the bound
+// as it then stands.  *total: the thread's weights of what is not listed, relative to *cur, the
+// warp's largest value (kSum).  Returns the warp's count (above kRSeg: it overflowed).
+template <bool kBF16, bool kSum>
+__device__ __forceinline__ uint32_t rm_stream(const RowCtx& rc, const MinPScan& sc, unsigned long long* seg,
+                                              uint32_t* run_max, unsigned long long pol, float* cur_out, float* total_out) {
+  constexpr int G = kBF16 ? 8 : 4;
+  const int lane = threadIdx.x & 31;
+  const unsigned lt = (1u << lane) - 1u;
+  const uint4* xr = rc.x;
+  float* out = rc.out;
+  const int g1 = rc.g1;
+  const uint32_t* bitmap = rc.bitmap;
+  const bool pen_on = rc.pen_on;
+  const float pen = rc.pen;
+  const float4 ninf = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+  uint32_t wcnt = 0;
+  bool over = false;
+  float cur = -INFINITY, t = -INFINITY, total = 0.0f;
+  for (int base = rc.g0; base < g1; base += kRT * kRU) {
+    uint4 w[kRU];
+#pragma unroll
+    for (int u = 0; u < kRU; ++u) {
+      const int g = base + u * kRT + static_cast<int>(threadIdx.x);
+      w[u] = g < g1 ? ld_row16(xr + g, pol) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    {
+      // what the other warps have seen (NaN before the first)
+      const float top = kfloat(__shfl_sync(kFull, *reinterpret_cast<volatile uint32_t*>(run_max), 0));
+      if (top > cur) {
+        if (kSum) total *= sc.weight(cur, top);
+        cur = top;
+        t = sc.floor(cur);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRU; ++u) {
+      const int g = base + u * kRT + static_cast<int>(threadIdx.x);
+      const bool in = g < g1;
+      if (out != nullptr && in) {
+        float4* o = reinterpret_cast<float4*>(out) + g * (G / 4);
+#pragma unroll
+        for (int h = 0; h < G / 4; ++h) __stcs(o + h, ninf);
+      }
+      float v[G];
+      unpack16<kBF16>(w[u], v);
+      const uint32_t bits = in ? rseen_bits<G>(bitmap, pen_on, g) : 0u;
+      if (__any_sync(kFull, bits != 0u)) {
+#pragma unroll
+        for (int e = 0; e < G; ++e)
+          if ((bits >> e) & 1u) v[e] = rpenal(v[e], pen);
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < G; ++e) mx = fmaxf(mx, v[e]);  // NaN is ignored (it counts as -inf)
+      if (!in) mx = -INFINITY;
+      if (__any_sync(kFull, mx > cur)) {
+        // a new largest value: what the block has seen by now, this vector included
+        const uint32_t key = __reduce_max_sync(kFull, fkey(mx));
+        uint32_t seen = 0;
+        if (lane == 0) seen = atomicMax(run_max, key);
+        seen = __shfl_sync(kFull, seen, 0);
+        const float top = kfloat(seen > key ? seen : key);
+        if (kSum) total *= sc.weight(cur, top);
+        cur = top;
+        t = sc.floor(cur);
+      }
+      bool pass[G];
+      bool any = false;
+#pragma unroll
+      for (int e = 0; e < G; ++e) {
+        pass[e] = in && v[e] >= t;
+        any |= pass[e];
+      }
+      if (kSum && in) {
+        float part = 0.0f;
+#pragma unroll
+        for (int e = 0; e < G; ++e) part += pass[e] ? 0.0f : sc.weight(v[e], cur);
+        total += part;
+      }
+      if (__any_sync(kFull, any) && !over) {
+        unsigned m[G];
+        uint32_t n = 0;
+#pragma unroll
+        for (int e = 0; e < G; ++e) {
+          m[e] = __ballot_sync(kFull, pass[e]);
+          n += __popc(m[e]);
+        }
+        if (wcnt + n > static_cast<uint32_t>(kRSeg)) {
+          // thin with the bound of the whole block; a segment that stays full is given up
+          const float top = fmaxf(cur, kfloat(__shfl_sync(kFull, *reinterpret_cast<volatile uint32_t*>(run_max), 0)));
+          if (kSum) total *= sc.weight(cur, top);
+          cur = top;
+          t = sc.floor(cur);
+          wcnt = rm_thin<kSum>(seg, wcnt, t, cur, sc, &total);
+          over = wcnt > static_cast<uint32_t>(kRSeg * 3 / 4) || wcnt + n > static_cast<uint32_t>(kRSeg);
+        }
+        if (!over) {
+#pragma unroll
+          for (int e = 0; e < G; ++e) {
+            if (pass[e]) seg[wcnt + __popc(m[e] & lt)] = order_word(fkey(v[e]), g * G + e);
+            wcnt += __popc(m[e]);
+          }
+        }
+      }
+    }
+  }
+  *cur_out = cur;
+  *total_out = total;
+  return over ? static_cast<uint32_t>(kRSeg) + 1u : wcnt;
+}
+
+// The exact selection out of line: the fallback of the min-p rows.
 template <bool kBF16>
 __device__ __noinline__ int32_t rexact_min_p_row(const RowCtx& whole, const RowSmem& sm, bool topp, float p, float mp,
                                                  float eps) {
@@ -1413,62 +1553,62 @@ __device__ __noinline__ int32_t rexact_min_p_row(const RowCtx& whole, const RowS
 }
 
 // A row whose top-k is off and whose min-p is on (mp in (0, 1]); returns the chosen index.
-// Everything that can be kept is at least M + ln(mp), and M is at least the sample's maximum:
-// one streaming pass lists what reaches that (the true maximum is always among it).  With top-p
-// the pass also sums the mass of everything it does not list, for p is a share of the whole row's.
+// Everything that can be kept is at least M + ln(mp): one streaming pass lists what reaches that
+// for the largest value seen so far (the true maximum is always among it).  With top-p the pass
+// also sums the mass of everything it does not list, for p is a share of the whole row's.
 template <bool kBF16>
 __device__ __noinline__ int32_t rm_row(const RowCtx& rc, const RowSmem& sm, const Team& tm, bool topp_on, float p,
-                                       float eps, bool exact, bool sampled) {
+                                       float eps, bool exact) {
   const float mp = *reinterpret_cast<const float*>(sm.misc + kMMinP);
   uint32_t* segcnt = reinterpret_cast<uint32_t*>(sm.misc + kMSeg);
+  uint32_t* run_max = reinterpret_cast<uint32_t*>(sm.misc + kMRunMax);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   RowCtx whole = rc;
   whole.g0 = 0;
   whole.g1 = rc.nv;
   if (exact) return tm.rank == 0 ? rexact_min_p_row<kBF16>(whole, sm, topp_on, p, mp, eps) : -1;
-  const bool keep_all = rc.V <= kRKeepAllV;
-  float tau_raw = -INFINITY, below_ref = 0.0f;
-  if (!keep_all) {
-    uint32_t* samp = reinterpret_cast<uint32_t*>(sm.wbuf);
-    if (!sampled) rsample_load<kBF16>(whole, samp);
-    unsigned long long a = 0, b = 0;
-    for (int i = threadIdx.x; i < kRSamp; i += kRT) a = samp[i] > a ? samp[i] : a;
-    rblock_max2(a, b, sm.red);
-    const float ms = kfloat(static_cast<uint32_t>(a));
-    // a lower bound of ms + ln(mp): logf is within 2^-22 relative and 2^-22
-    const float l = logf(mp);
-    const float tv = __fadd_rd(ms, __fsub_rd(l, __fmaf_rn(fabsf(l), 0x1p-20f, 0x1p-20f)));
-    tau_raw = tv > -INFINITY ? raw_floor(tv, rc.T, rc.identity) : __int_as_float(0x7fffffff);
-    below_ref = __fmul_rn(ms, rc.T);
-  }
-  if (threadIdx.x == kRT - 1) *reinterpret_cast<float2*>(sm.misc + kMLnMinP) = ln_min_p(mp);
-  uint32_t wc;
-  unsigned long long below = 0;  // in units of 2^-32 of exp(below_ref / T)
-  if (topp_on) {
+  if (threadIdx.x == 0) *run_max = 0u;
+  MinPScan sc;
+  {
+    sc.reach = __fmul_rn(logf(mp), rc.T);
+    sc.tiny = 1e-30f * rc.T;
     constexpr float kLog2eHi = 1.44269502162933349609f, kLog2eLo = 1.92596299112661746887e-8f;
     const float hi = __fdiv_rn(kLog2eHi, rc.T);
-    const float lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-hi, rc.T, kLog2eHi), kLog2eLo), rc.T);
-    float part;
-    wc = rk_stream<kBF16, true>(rc, tau_raw, keep_all, sm.cw + warp * kRSeg, l2_policy_first(), below_ref,
-                                make_float2(hi, lo), &part);
-    below = rblock_sum_u64(__float2ull_rn(__fmul_rn(part, 4294967296.0f)), sm.red);
-    tm.push(sm.misc, 0, below);
-  } else {
-    wc = rk_stream<kBF16>(rc, tau_raw, keep_all, sm.cw + warp * kRSeg, l2_policy_first());
+    sc.c = make_float2(hi, __fdiv_rn(__fadd_rn(__fmaf_rn(-hi, rc.T, kLog2eHi), kLog2eLo), rc.T));
+  }
+  __syncthreads();
+  if (threadIdx.x == kRT - 1) *reinterpret_cast<float2*>(sm.misc + kMLnMinP) = ln_min_p(mp);
+  float cur, total;
+  unsigned long long* seg = sm.cw + warp * kRSeg;
+  uint32_t wc = topp_on ? rm_stream<kBF16, true>(rc, sc, seg, run_max, l2_policy_first(), &cur, &total)
+                        : rm_stream<kBF16, false>(rc, sc, seg, run_max, l2_policy_first(), &cur, &total);
+  __syncthreads();
+  // the row's largest value, over every member's part; then every segment against it
+  tm.push(sm.misc, 0, *run_max);
+  tm.sync();
+  const float top_raw = kfloat(static_cast<uint32_t>(tm.max_of(sm.misc, 0)));
+  const float M = rmax_transformed(fkey(top_raw), rc);
+  if (topp_on) total *= sc.weight(cur, top_raw);
+  if (wc <= static_cast<uint32_t>(kRSeg))
+    wc = topp_on ? rm_thin<true>(seg, wc, sc.floor(top_raw), top_raw, sc, &total)
+                 : rm_thin<false>(seg, wc, sc.floor(top_raw), top_raw, sc, &total);
+  unsigned long long below = 0;  // the mass of what is not listed, against M
+  if (topp_on) {
+    below = rblock_sum_u64(fixed_mass(__fmul_rn(total, rscale_to_max(top_raw, rc.T, M))), sm.red);
+    tm.push(sm.misc, 1, below);
   }
   if (lane == 0) segcnt[warp] = wc;
   __syncthreads();
   if (!rk_gather_team(sm, tm)) return -1;
-  if (topp_on) below = tm.sum_of(sm.misc, 0);
+  if (topp_on) below = tm.sum_of(sm.misc, 1);
   bool over = false;
 #pragma unroll
   for (int w = 0; w < kRW; ++w) over |= segcnt[w] > static_cast<uint32_t>(kRSeg);
   unsigned long long top;
   uint32_t mn;
   const uint32_t n = rk_normalize(sm.cw, segcnt, 0u, rc.div, rc.identity, sm.red, &top, &mn);
-  // the list overflowed, or the sample says nothing (all -inf): the exact selection
-  if (over || n == 0u) return rexact_min_p_row<kBF16>(whole, sm, topp_on, p, mp, eps);
-  const float M = kfloat(static_cast<uint32_t>(top >> 32));
+  // a list overflowed, or nothing has a distance to the maximum: the exact selection
+  if (over || n == 0u || isinf(M)) return rexact_min_p_row<kBF16>(whole, sm, topp_on, p, mp, eps);
   Thresh th = with_min_p(kKeepAll, *reinterpret_cast<const float2*>(sm.misc + kMLnMinP), M);
   const unsigned long long* list = sm.cw;
   int len = kRCap;
@@ -1478,11 +1618,7 @@ __device__ __noinline__ int32_t rm_row(const RowCtx& rc, const RowSmem& sm, cons
       const uint32_t key = static_cast<uint32_t>(sm.cw[i] >> 32);
       if (key) S += fixed_mass(softmax_weight(kfloat(key), M));
     }
-    S = rblock_sum_u64(S, sm.red);
-    if (!keep_all && below) {
-      const unsigned long long f = fixed_mass(fminf(rscale_to_max(below_ref, rc.T, M), 1.0f));
-      S += (__umul64hi(below, f) << 32) | ((below * f) >> 32);
-    }
+    S = rblock_sum_u64(S, sm.red) + below;
     if (threadIdx.x == 0) sm.misc[kMRowMass] = S;  // published by the gather's barriers
     const int ns = rbuf_gather(sm.cw, kRCap, th, sm.wbuf, kTopKMax, sm.red);
     if (ns < kTopKMax) {
@@ -2386,8 +2522,7 @@ __device__ __forceinline__ void rseen_copy(const uint32_t* src, int V, uint32_t*
 struct RowFlags {
   int32_t k;
   float p;
-  bool pen_on, single, topk_on, topp_on;
-  float mp;        // min-p in (0, 1], or 0: off
+  bool pen_on, single, topp_on;
   int32_t b0, b1;  // the row's seen ids
 };
 template <bool kBF16>
@@ -2404,10 +2539,9 @@ __device__ __forceinline__ RowFlags row_setup(const Params& P, int64_t row, cons
   f.pen_on = ((P.seen_indptr && P.seen_ids) || P.seen_bits) && P.penalty && (P.penalty[row] > 0.0f);
   const bool topk_on = f.k >= 1 && static_cast<int64_t>(f.k) <= (P.V < kTopKMax ? P.V : kTopKMax);
   const bool p_nan = isnan(f.p);
-  f.topk_on = topk_on;
   f.single = greedyT || (!p_nan && f.p <= 0.0f) || (topk_on && f.k == 1);
-  f.mp = kMinP && !f.single ? row_min_p(P, row) : 0.0f;
-  if (kMinP && threadIdx.x == 0) *reinterpret_cast<float*>(sm.misc + kMMinP) = f.mp;  // read after the barriers below
+  if (kMinP && threadIdx.x == 0)  // read after the barriers below
+    *reinterpret_cast<float*>(sm.misc + kMMinP) = f.single ? 0.0f : row_min_p(P, row);
   f.topp_on = !f.single && !p_nan && f.p > 0.0f && f.p < 1.0f;
   RowCtx& rc = *rcp;
   rc.x = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(P.logits) + row * P.V * esize);
@@ -2582,11 +2716,11 @@ __global__ void __launch_bounds__(kRT, 2) kps_row_kernel(const Params P) {
     const bool kteam = !wide && shared_rows && P.B <= nclusters && P.V > kRKeepAllV;
     const Team& tm = (wide || kteam) ? team : alone;
     RowCtx rc;
-    const bool sample = !wide && !P.exact && P.V > kRKeepAllV;
+    const bool sample = !wide && !P.exact && P.V > kRKeepAllV && !(kMinP && row_min_p_alone(P, row));
     const RowFlags f = row_setup<kBF16>(P, row, sm, tm.rank, tm.C, &rc, sample);
     int32_t chosen;
-    if (kMinP && !wide && f.mp > 0.0f && !f.topk_on) {
-      chosen = rm_row<kBF16>(rc, sm, tm, f.topp_on, f.p, P.eps, P.exact != 0, sample);
+    if (kMinP && row_min_p_alone(P, row)) {
+      chosen = rm_row<kBF16>(rc, sm, tm, f.topp_on, f.p, P.eps, P.exact != 0);
     } else if (!wide) {
       chosen = rk_row<kBF16>(rc, sm, tm, f.single ? 1u : static_cast<uint32_t>(f.k), f.single, f.topp_on, f.p, P.eps,
                              P.exact != 0, sample);

@@ -195,6 +195,14 @@ __device__ __forceinline__ bool row_is_kmode(const Params& P, int64_t row) {
   return topk_on || greedyT || (!isnan(p) && p <= 0.0f) || (kMinP && row_min_p(P, row) > 0.0f);
 }
 
+// Rows with min-p and without top-k (and not greedy): the row kernel lists what min-p can keep.
+__device__ __forceinline__ bool row_min_p_alone(const Params& P, int64_t row) {
+  const int32_t k = P.top_k[row];
+  const float p = P.top_p[row], T = P.temperature[row];
+  const bool topk_on = k >= 1 && static_cast<int64_t>(k) <= (P.V < 1024 ? P.V : 1024);
+  return !topk_on && T > 0.0f && !isinf(T) && !(p <= 0.0f) && row_min_p(P, row) > 0.0f;
+}
+
 // Rows worker w of nw owns in a filtered launch: the matching rows whose rank among
 // matching rows is w mod nw, in row order, written to list; returns how many.
 template <int NT>
