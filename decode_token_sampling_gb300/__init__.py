@@ -13,7 +13,6 @@ distillation loss of a student against a teacher's top logits).
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -108,7 +107,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _check(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: Tuple[int, ...], device) -> None:
-    if t is None:
+    if t is None or (t.dtype is dtype and t.is_cuda and t.shape == shape and t.device == device and t.is_contiguous()):
         return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -315,23 +314,26 @@ def _rows(t: torch.Tensor, name: str) -> int:
     return t.stride(0)
 
 
-@contextlib.contextmanager
-def _queued_on(device: torch.device, stream: Optional[torch.cuda.Stream], *inputs: Optional[torch.Tensor]):
-    """Makes `device` and `stream` current (so that outputs are allocated for that stream) and keeps
-    the inputs' memory from reuse before the stream is done with it; yields the stream's handle."""
-    with contextlib.ExitStack() as stack:
-        if device.index is not None and device.index != torch.cuda.current_device():
-            stack.enter_context(torch.cuda.device(device))
-        current = torch.cuda.current_stream(device)
-        if stream is not None and stream != current:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the logits on {device}")
-            stack.enter_context(torch.cuda.stream(stream))
+def _queue(device: torch.device, stream: Optional[torch.cuda.Stream], inputs, call):
+    """call(handle of the stream) with `device` and `stream` current, so that what it allocates belongs to
+    them; the inputs' memory is kept from reuse before another stream than the current one is done with it."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(torch._C._cuda_getCurrentRawStream(device.index))  # torch.cuda.current_stream() costs 3 us more
+    with torch.cuda.device(device):
+        current = torch.cuda.current_stream()
+        if stream is None or stream == current:
+            return call(current.cuda_stream)
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the logits on {device}")
+        with torch.cuda.stream(stream):
             for t in inputs:
                 if t is not None:
                     t.record_stream(stream)
-            current = stream
-        yield ctypes.c_void_p(current.cuda_stream)
+            return call(stream.cuda_stream)
+
+
+def _addr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 class TopLogits(NamedTuple):
@@ -363,16 +365,20 @@ def top_logits(logits: torch.Tensor, n: int, *, temperature: float = 1.0, tokens
         raise ValueError(f"n must be in 0..min(V, 1024), got {n}")
     if tokens is not None:
         _check(tokens, "tokens", torch.int64, (B,), dev)
-    with _queued_on(dev, stream, logits, tokens) as handle:
-        ids = torch.empty(B, n, dtype=torch.int32, device=dev)
-        values = torch.empty(B, n, dtype=torch.float32, device=dev)
-        sums = torch.empty(3, B, dtype=torch.float32, device=dev)
+
+    def call(handle):
+        ids = torch.empty((B, n), dtype=torch.int32, device=dev)
+        values = torch.empty((B, n), dtype=torch.float32, device=dev)
+        sums = torch.empty((3, B), dtype=torch.float32, device=dev)
+        at = sums.data_ptr()
+        st = lib.kps_top_logits(logits.data_ptr(), dt, B, V, ld, n, temperature, _addr(tokens), ids.data_ptr(),
+                                values.data_ptr(), at, at + 4 * B, None if tokens is None else at + 8 * B, handle)
+        if st != 0:
+            raise KpsError(st, "kps_top_logits")
         lse, rest, logprob = sums.unbind(0)
-        st = lib.kps_top_logits(_ptr(logits), dt, B, V, ld, n, float(temperature), _ptr(tokens), _ptr(ids),
-                                _ptr(values), _ptr(lse), _ptr(rest), None if tokens is None else _ptr(logprob), handle)
-    if st != 0:
-        raise KpsError(st, "kps_top_logits")
-    return TopLogits(ids, values, lse, rest, None if tokens is None else logprob)
+        return TopLogits(ids, values, lse, rest, None if tokens is None else logprob)
+
+    return _queue(dev, stream, (logits, tokens), call)
 
 
 def _distill_args(student, ids, values, rest, weight, temperature):
@@ -389,15 +395,32 @@ def _distill_args(student, ids, values, rest, weight, temperature):
     _check(values, "values", values.dtype, (N, K), student.device)
     _check(rest, "rest", torch.float32, (N,), student.device)
     _check(weight, "weight", torch.float32, (N,), student.device)
-    return (_ptr(student), dt, N, V, ld, _ptr(ids), _ptr(values), _dtype_code(values), K, _ptr(rest), _ptr(weight),
-            float(temperature))
+    return (student.data_ptr(), dt, N, V, ld, ids.data_ptr(), values.data_ptr(), _dtype_code(values), K, _addr(rest),
+            _addr(weight), temperature)
 
 
 def _grad_like(student: torch.Tensor) -> torch.Tensor:
     """An uninitialised gradient whose rows lie on the same 16-byte phase as the student's."""
     N, V = student.shape
     ld = student.stride(0) if N > 1 else V
-    return torch.empty(N, ld, dtype=student.dtype, device=student.device)[:, :V]
+    grad = torch.empty((N, ld), dtype=student.dtype, device=student.device)
+    return grad if ld == V else grad[:, :V]
+
+
+def _distill_forward(student, ids, values, temperature, rest, weight, stream, want_stats):
+    lib = load_library()
+    args = _distill_args(student, ids, values, rest, weight, temperature)
+    N, dev = student.shape[0], student.device
+
+    def call(handle):
+        loss = torch.empty((N,), dtype=torch.float32, device=dev)
+        stats = torch.empty((N, 4), dtype=torch.float32, device=dev) if want_stats else None
+        st = lib.kps_distill_forward(*args, loss.data_ptr(), _addr(stats), handle)
+        if st != 0:
+            raise KpsError(st, "kps_distill_forward")
+        return loss, stats
+
+    return _queue(dev, stream, (student, ids, values, rest, weight), call)
 
 
 def distill_forward(student: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, *, temperature: float = 1.0,
@@ -405,16 +428,7 @@ def distill_forward(student: torch.Tensor, ids: torch.Tensor, values: torch.Tens
                     stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The distillation loss of every row and the statistics [N, 4] that distill_backward takes
     (kps_distill_forward in include/kps.h); no autograd."""
-    lib = load_library()
-    args = _distill_args(student, ids, values, rest, weight, temperature)
-    N, dev = student.shape[0], student.device
-    with _queued_on(dev, stream, student, ids, values, rest, weight) as handle:
-        loss = torch.empty(N, dtype=torch.float32, device=dev)
-        stats = torch.empty(N, 4, dtype=torch.float32, device=dev)
-        st = lib.kps_distill_forward(*args, _ptr(loss), _ptr(stats), handle)
-    if st != 0:
-        raise KpsError(st, "kps_distill_forward")
-    return loss, stats
+    return _distill_forward(student, ids, values, temperature, rest, weight, stream, True)
 
 
 def distill_backward(grad_loss: Optional[torch.Tensor], student: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
@@ -427,12 +441,15 @@ def distill_backward(grad_loss: Optional[torch.Tensor], student: torch.Tensor, i
     N, dev = student.shape[0], student.device
     _check(grad_loss, "grad_loss", torch.float32, (N,), dev)
     _check(stats, "stats", torch.float32, (N, 4), dev)
-    with _queued_on(dev, stream, student, ids, values, rest, weight, grad_loss, stats) as handle:
+
+    def call(handle):
         grad = _grad_like(student)
-        st = lib.kps_distill_backward(*args, _ptr(grad_loss), _ptr(stats), _ptr(grad), grad.stride(0), handle)
-    if st != 0:
-        raise KpsError(st, "kps_distill_backward")
-    return grad
+        st = lib.kps_distill_backward(*args, _addr(grad_loss), stats.data_ptr(), grad.data_ptr(), grad.stride(0), handle)
+        if st != 0:
+            raise KpsError(st, "kps_distill_backward")
+        return grad
+
+    return _queue(dev, stream, (student, ids, values, rest, weight, grad_loss, stats), call)
 
 
 def distill_loss_grad(student: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, *, temperature: float = 1.0,
@@ -444,19 +461,22 @@ def distill_loss_grad(student: torch.Tensor, ids: torch.Tensor, values: torch.Te
     lib = load_library()
     args = _distill_args(student, ids, values, rest, weight, temperature)
     N, dev = student.shape[0], student.device
-    with _queued_on(dev, stream, student, ids, values, rest, weight) as handle:
-        loss = torch.empty(N, dtype=torch.float32, device=dev)
+
+    def call(handle):
+        loss = torch.empty((N,), dtype=torch.float32, device=dev)
         grad = _grad_like(student)
-        st = lib.kps_distill_loss_grad(*args, _ptr(loss), _ptr(grad), grad.stride(0), handle)
-    if st != 0:
-        raise KpsError(st, "kps_distill_loss_grad")
-    return loss, grad
+        st = lib.kps_distill_loss_grad(*args, loss.data_ptr(), grad.data_ptr(), grad.stride(0), handle)
+        if st != 0:
+            raise KpsError(st, "kps_distill_loss_grad")
+        return loss, grad
+
+    return _queue(dev, stream, (student, ids, values, rest, weight), call)
 
 
 class _DistillLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, student, ids, values, rest, weight, temperature):
-        loss, stats = distill_forward(student, ids, values, temperature=temperature, rest=rest, weight=weight)
+        loss, stats = _distill_forward(student, ids, values, temperature, rest, weight, None, True)
         ctx.save_for_backward(student, ids, values, rest, weight, stats)
         ctx.temperature = temperature
         return loss
@@ -485,5 +505,5 @@ def distill_loss(student: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
         if t is not None and t.requires_grad:
             raise ValueError(f"{name} requires a gradient, but distill_loss has one for the student only")
     if not (torch.is_grad_enabled() and student.requires_grad):
-        return distill_forward(student, ids, values, temperature=temperature, rest=rest, weight=weight)[0]
+        return _distill_forward(student, ids, values, temperature, rest, weight, None, False)[0]
     return _DistillLoss.apply(student, ids, values, rest, weight, temperature)

@@ -7,12 +7,14 @@
 //   ids, values = the first n elements of the order       lse  = ln sum_v exp(a_v)
 //   rest = ln sum_{v not among them} exp(a_v)             logprob = a_token - lse
 //
-// One pass over the row.  A threshold from a sample of 2048 elements is reached by a few times n
-// elements; those go to a list in shared memory, all others into a running sum of exponentials.
-// The list is sorted, its first n are the top, and what is left of it joins the sum: the rest is
-// a sum of its own, never a difference of two large ones.  A list that came out too short or too
-// long (the sample misjudged the row, or ties crowd the threshold) sends the row to an exact
-// selection by digits.
+// One pass over the row, at best as fast as memory delivers it.  A threshold from a sample of
+// the row is reached by a few times n elements.  A 16-byte vector holding one of those goes to a
+// list in shared memory whole (one ballot and two stores; taking single elements out of the
+// vector cost four times the instructions of the sum itself), all others into a running sum of
+// exponentials.  Then digits of the listed keys, counted, cut the list to little more than n
+// elements, which are ranked; everything else in the list joins the sum.  So the rest is a sum of
+// its own, never a difference of two large ones.  A list that came out too short or too long (the
+// sample misjudged the row, or ties crowd the threshold) sends the row to an exact selection.
 
 #include "kps.h"
 #include "kps_host.h"
@@ -36,10 +38,21 @@ constexpr int kU = 4;          // 16-byte loads each thread keeps in flight
 constexpr int kMaxN = 1024;    // the framework's top-k limit
 constexpr int64_t kMaxV = 1 << 20;
 constexpr int kMaxCS = 8;      // widest cluster (the portable limit)
-constexpr int kCap = 4096;     // list entries
-constexpr int kPer = 8;        // sampled elements per thread
-constexpr int kSamp = kNT * kPer;
+constexpr int kAllV = 4096;    // rows this short are listed whole
+constexpr int kMaxPer = 16;    // sampled places per thread, at most
+constexpr int kMaxRank = 96;   // rank of the threshold among the threads' sample maxima, at most
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
+constexpr int kPairwise = 256;  // survivors ranked pairwise; more are sorted
+
+// Capacities: listed vectors (an equal part for each warp) and ranked survivors.  The small
+// form lets six CTAs share an SM; a list of 128 fills about 630 vectors of a long row.
+constexpr int kSmallN = 128;
+template <bool kSmall>
+struct Caps {
+  static constexpr int list = kSmall ? 1536 : 4096;
+  static constexpr int words = kSmall ? 512 : 2048;
+  static constexpr int seg = list / kNW;
+};
 
 struct Params {
   const void* x;
@@ -69,53 +82,43 @@ __device__ __forceinline__ unsigned long long word_of(uint32_t key, int v) {
 __device__ __forceinline__ float word_value(unsigned long long w) { return kfloat(static_cast<uint32_t>(w >> 32)); }
 __device__ __forceinline__ int word_index(unsigned long long w) { return static_cast<int>(~static_cast<uint32_t>(w)); }
 
+template <bool kSmall>
 struct Smem {
-  unsigned long long list[kCap];
+  unsigned long long words[Caps<kSmall>::words];  // the survivors
+  uint4 vec[Caps<kSmall>::list];                  // the listed vectors, by warp
+  int32_t at[Caps<kSmall>::list];                 // index of each one's first element (~: its only one)
   uint32_t hist[256];
-  float red[kNW][2];
-  float part[kMaxCS][2];     // the sums of the cluster's CTAs
-  uint32_t count[kMaxCS];    // their list lengths
-  uint32_t n_list;
-  uint32_t found;
-  int nan;
+  float red[kNW][4];
+  float part[kMaxCS][2];  // the sums of the cluster's CTAs
+  uint32_t seg[kNW];      // vectors each warp listed
+  uint32_t top_key;       // of the listed elements
+  uint32_t n_words;
+  uint32_t bin, above, inside;
 };
 
-__device__ __forceinline__ Sum2 block_merge(Sum2 v, float c, float (*red)[2]) {
+// Two sums merged over the block; every thread gets the results.
+__device__ __forceinline__ void block_merge2(Sum2& a, Sum2& b, float c, float (*red)[4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  v = warp_merge(v, c);
+  a = warp_merge(a, c);
+  b = warp_merge(b, c);
   __syncthreads();
   if (lane == 0) {
-    red[warp][0] = v.ref;
-    red[warp][1] = v.s;
+    red[warp][0] = a.ref;
+    red[warp][1] = a.s;
+    red[warp][2] = b.ref;
+    red[warp][3] = b.s;
   }
   __syncthreads();
-  v.ref = red[lane & (kNW - 1)][0];
-  v.s = lane < kNW ? red[lane][1] : 0.0f;
-  return warp_merge(v, c);
+  const float* r = red[lane & (kNW - 1)];
+  a = warp_merge(Sum2{r[0], lane < kNW ? r[1] : 0.0f}, c);
+  b = warp_merge(Sum2{r[2], lane < kNW ? r[3] : 0.0f}, c);
 }
 __device__ __forceinline__ void add_one(Sum2& sum, float x, float c) {
   if (x > sum.ref + kRaise / c) sum.raise(clamp_ref(x), c);
   sum.s += ex2((x - sum.ref) * c);
 }
 
-// The largest key (its low 16 bits zero) that at least r of the block's sampled keys reach.
-__device__ __forceinline__ uint32_t sample_threshold(const uint32_t (&key)[kPer], uint32_t r, Smem& sm) {
-  uint32_t t = 0;
-  for (int bit = 31; bit >= 16; --bit) {
-    const uint32_t mid = t | (1u << bit);
-    uint32_t n = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) n += key[i] >= mid ? 1u : 0u;
-    n = __reduce_add_sync(0xffffffffu, n);
-    uint32_t* slot = &sm.hist[bit];  // one counter per round, zeroed beforehand
-    if ((threadIdx.x & 31) == 0) atomicAdd(slot, n);
-    __syncthreads();
-    if (*slot >= r) t = mid;
-  }
-  return t;
-}
-
-// Descending bitonic sort of list[0..N), N a power of two.
+// Descending bitonic sort of a[0..N), N a power of two.
 __device__ __forceinline__ void sort_desc(unsigned long long* a, int N) {
   for (int k = 2; k <= N; k <<= 1) {
     for (int j = k >> 1; j > 0; j >>= 1) {
@@ -132,6 +135,41 @@ __device__ __forceinline__ void sort_desc(unsigned long long* a, int N) {
   }
 }
 
+// Finds in hist (256 counts) the bin, from the top, where the running count reaches need:
+// sm.bin, sm.above (the count over it) and sm.inside (its own).  Starts and ends with a barrier.
+template <class S>
+__device__ __forceinline__ void find_bin(S& sm, uint32_t need) {
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    uint32_t n[8], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      n[i] = sm.hist[255 - 8 * lane - i];
+      sum += n[i];
+    }
+    uint32_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    uint32_t acc = incl - sum;
+    if (acc < need && need <= incl) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (acc < need && need <= acc + n[i]) {
+          sm.bin = 255 - 8 * lane - i;
+          sm.above = acc;
+          sm.inside = n[i];
+        }
+        acc += n[i];
+      }
+    }
+  }
+  __syncthreads();
+}
+
 // One element at a time over the row: f(value with NaN -> -inf, index).
 template <bool kBF16, class F>
 __device__ __forceinline__ void each(const RowView<kBF16>& x, F&& f) {
@@ -139,14 +177,15 @@ __device__ __forceinline__ void each(const RowView<kBF16>& x, F&& f) {
 }
 
 // The exact selection, by one CTA: the n-th element of the order by 8-bit digits of its key and,
-// among equal keys, of its index; then the list of the n elements and the sum of all others.
-template <bool kBF16>
-__device__ __noinline__ Sum2 exact_select(const RowView<kBF16>& x, int n, float c, Smem& sm) {
+// among equal keys, of its index; then the n elements as survivors and the thread's sum of all others.
+template <bool kBF16, class S>
+__device__ __noinline__ Sum2 exact_select(const RowView<kBF16>& x, int n, float c, S& sm) {
   uint32_t need = static_cast<uint32_t>(n);
   unsigned long long at = 0;  // the digits found so far, from the top of the 64-bit word
+  __syncthreads();            // everything before is done with what is written below
   if (n > 0) {
     for (int shift = 56; shift >= 0; shift -= 8) {
-      if (shift == 24) {  // indexes are below 2^20, their complements share the top 12 bits
+      if (shift == 24) {  // indexes are below 2^20: the top 8 bits of their complements are ones
         at |= 0xFFull << 24;
         continue;
       }
@@ -156,38 +195,42 @@ __device__ __noinline__ Sum2 exact_select(const RowView<kBF16>& x, int n, float 
         const unsigned long long w = word_of(fkey(y), v);
         if (shift == 56 || (w >> (shift + 8)) == (at >> (shift + 8))) atomicAdd(&sm.hist[(w >> shift) & 255u], 1u);
       });
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        uint32_t above = 0, d = 255;
-        while (d > 0 && above + sm.hist[d] < need) above += sm.hist[d--];
-        sm.found = d;
-        sm.n_list = above;
-      }
-      __syncthreads();
-      at |= static_cast<unsigned long long>(sm.found) << shift;
-      need -= sm.n_list;
+      find_bin(sm, need);
+      at |= static_cast<unsigned long long>(sm.bin) << shift;
+      need -= sm.above;
       __syncthreads();
     }
   }
-  if (threadIdx.x == 0) sm.n_list = 0u;
+  if (threadIdx.x == 0) sm.n_words = 0u;
   __syncthreads();
   Sum2 sum{-FLT_MAX, 0.0f};
   each<kBF16>(x, [&](float y, int v) {
     const unsigned long long w = word_of(fkey(y), v);
     if (n > 0 && w >= at) {
-      sm.list[atomicAdd(&sm.n_list, 1u)] = w;  // n of them
+      sm.words[atomicAdd(&sm.n_words, 1u)] = w;  // n of them
     } else {
       add_one(sum, y, c);
     }
   });
-  return block_merge(sum, c, sm.red);
+  return sum;
 }
 
+// Element e of a vector as fp32.
 template <bool kBF16>
+__device__ __forceinline__ float elem(const uint4& w, int e) {
+  const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+  if (kBF16) return __uint_as_float((e & 1) ? (word[e / 2] & 0xFFFF0000u) : (word[e / 2] << 16));
+  return __uint_as_float(word[e]);
+}
+
+template <bool kBF16, bool kSmall>
 __global__ void __launch_bounds__(kNT) top_kernel(const Params P) {
   constexpr int G = kBF16 ? 8 : 4;
+  constexpr int kSeg = Caps<kSmall>::seg, kWords = Caps<kSmall>::words;
   extern __shared__ __align__(16) unsigned char smem[];
-  Smem& sm = *reinterpret_cast<Smem*>(smem);
+  Smem<kSmall>& sm = *reinterpret_cast<Smem<kSmall>*>(smem);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned lt = (1u << lane) - 1u;
   const int CS = static_cast<int>(cg::this_cluster().num_blocks());
   const int rank = static_cast<int>(cg::this_cluster().block_rank());
   const int64_t row = blockIdx.x / CS;
@@ -198,52 +241,63 @@ __global__ void __launch_bounds__(kNT) top_kernel(const Params P) {
   const int g1 = static_cast<int>(static_cast<int64_t>(x.nv) * (rank + 1) / CS);
   // every CTA of the cluster runs before any writes into another's shared memory
   if (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (threadIdx.x == 0) {
+    sm.top_key = 0u;
+    sm.n_words = 0u;
+  }
 
   // ---- the threshold: every CTA of the row takes the same sample --------------------------
-  float thr = INFINITY;  // n == 0: nothing is listed
-  if (n > 0) {
-    // kSamp places spread over the row (all of it when it is that short), each the largest of
-    // `m` elements for the longest rows
+  float thr = n > 0 ? -INFINITY : INFINITY;  // n == 0: only +inf is listed
+  if (n > 0 && P.V > kAllV) {
+    // kNT * per places in runs of 32 consecutive elements spread over the row, each the largest
+    // of m elements for the longest rows.  The rank-th largest of the threads' maxima is reached
+    // by about rank * one elements of the row, give or take sqrt(rank) * one: four of these and
+    // six ranks on the safe side of n.
     const int m = (P.V + (1 << 18) - 1) >> 18;
-    uint32_t key[kPer];
-    float y[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    int per = kMaxPer;
+    float one, r;
+    for (;; per >>= 1) {
+      one = fmaxf(1.0f, static_cast<float>(P.V) / static_cast<float>(kNT * per * m));
+      r = static_cast<float>(n) / one;
+      r += 4.0f * sqrtf(r) + 6.0f;
+      if (r <= static_cast<float>(kMaxRank) || per == 1) break;
+    }
+    float y = -INFINITY;
+    const int runs = kNT / 32 * per;
+#pragma unroll 4
+    for (int i = 0; i < per; ++i) {
       const int s = i * kNT + static_cast<int>(threadIdx.x);
-      // runs of 32 consecutive elements
-      const int64_t v = P.V <= kSamp ? s : static_cast<int64_t>(s >> 5) * (P.V - 32 * m) / (kSamp / 32 - 1) + (s & 31);
-      y[i] = v < P.V ? x.at(static_cast<int>(v)) : -INFINITY;
-      for (int j = 1; j < m; ++j) y[i] = fmaxf(y[i], x.at(static_cast<int>(v) + 32 * j));
+      const int64_t v = static_cast<int64_t>(s >> 5) * (P.V - 32 * m) / (runs - 1) + (s & 31);
+      for (int j = 0; j < m; ++j) y = fmaxf(y, x.at(static_cast<int>(v) + 32 * j));  // NaN is ignored
     }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) key[i] = fkey(clean(y[i]));
-    for (int i = threadIdx.x; i < 256; i += kNT) sm.hist[i] = 0u;
-    if (threadIdx.x == 0) {
-      sm.n_list = 0u;
-      sm.nan = 0;
+    const uint32_t key = fkey(y + 0.0f);
+    uint32_t t = 0;  // the largest key, its low 16 bits zero, that `rank` maxima reach
+    for (int bit = 31; bit >= 16; --bit) {
+      const uint32_t mid = t | (1u << bit);
+      if (__syncthreads_count(key >= mid) >= static_cast<int>(r)) t = mid;
     }
-    __syncthreads();
-    // the number of row elements that reach the r-th largest of the sample is about r times
-    // `one`, give or take sqrt(r) times `one`: four of these on the safe side
-    const float one = fmaxf(1.0f, static_cast<float>(P.V) / static_cast<float>(kSamp * m));
-    const float r = static_cast<float>(n) / one;
-    const uint32_t want = static_cast<uint32_t>(r + (P.V <= kSamp ? 0.0f : 4.0f * sqrtf(r) + 6.0f));
-    const uint32_t t = want >= static_cast<uint32_t>(kSamp) ? 0u : sample_threshold(key, want < 1u ? 1u : want, sm);
-    thr = t <= kKeyNegInf ? -INFINITY : kfloat(t);
-  } else {
-    if (threadIdx.x == 0) {
-      sm.n_list = 0u;
-      sm.nan = 0;
-    }
-    __syncthreads();
+    if (t > kKeyNegInf) thr = kfloat(t);
   }
+  __syncthreads();
 
   // ---- the pass -----------------------------------------------------------------------------
   Sum2 sum{-FLT_MAX, 0.0f};
   const float lift = kRaise / c;
-  auto put = [&](float y, int v) {
-    const uint32_t pos = atomicAdd(&sm.n_list, 1u);
-    if (pos < static_cast<uint32_t>(kCap)) sm.list[pos] = word_of(fkey(y + 0.0f), v);
+  uint32_t listed = 0;  // this warp's
+  uint4* const seg_vec = sm.vec + warp * kSeg;
+  int32_t* const seg_at = sm.at + warp * kSeg;
+  float mx = -INFINITY;  // of the listed vectors
+  auto list = [&](bool hit, const uint4& w, int first, float m) {
+    const unsigned who = __ballot_sync(0xffffffffu, hit);
+    const uint32_t pos = listed + __popc(who & lt);
+    if (hit) {
+      if (pos < static_cast<uint32_t>(kSeg)) {
+        seg_vec[pos] = w;
+        seg_at[pos] = first;
+      }
+      mx = fmaxf(mx, m);
+    }
+    listed += __popc(who);
   };
   for (int base = g0; base < g1; base += kNT * kU) {
     uint4 w[kU];
@@ -252,98 +306,181 @@ __global__ void __launch_bounds__(kNT) top_kernel(const Params P) {
       const int g = base + u * kNT + static_cast<int>(threadIdx.x);
       w[u] = g < g1 ? ld_stream(x.vec + g) : neg_inf_vec<kBF16>();
     }
-    float mx = -INFINITY;
+    float top = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int g = base + u * kNT + static_cast<int>(threadIdx.x);
       float m = vec_max<kBF16>(w[u]);
-      if (m >= thr && g < g1) {
-        uint32_t word[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-        const int v0 = x.head + g * G;
-#pragma unroll
-        for (int e = 0; e < G; ++e) {
-          const float y = kBF16 ? __uint_as_float((e & 1) ? (word[e / 2] & 0xFFFF0000u) : (word[e / 2] << 16))
-                                : __uint_as_float(word[e]);
-          if (y >= thr) {
-            put(y, v0 + e);
-            if (kBF16) word[e / 2] = (e & 1) ? (word[e / 2] & 0x0000FFFFu) | 0xFF800000u : (word[e / 2] & 0xFFFF0000u) | 0x0000FF80u;
-            else word[e] = 0xFF800000u;
-          }
+      const bool hit = m >= thr && g < g1;
+      if (__any_sync(0xffffffffu, hit)) {
+        list(hit, w[u], x.head + g * G, m);
+        if (hit) {
+          w[u] = neg_inf_vec<kBF16>();
+          m = -INFINITY;
         }
-        w[u] = make_uint4(word[0], word[1], word[2], word[3]);
-        m = vec_max<kBF16>(w[u]);
       }
-      mx = fmaxf(mx, m);
+      top = fmaxf(top, m);
     }
-    if (mx > sum.ref + lift) sum.raise(clamp_ref(mx), c);
+    if (top > sum.ref + lift) sum.raise(clamp_ref(top), c);
 #pragma unroll
     for (int u = 0; u < kU; ++u) add_vec<kBF16>(sum, w[u], c);
   }
-  // the elements outside the vectors: the head with rank 0, the tail with the last rank
-  if (static_cast<int>(threadIdx.x) < x.loose()) {
-    const int v = x.loose_at(threadIdx.x);
-    if ((v < x.head) ? rank == 0 : rank == CS - 1) {
-      const float y = x.at(v);
-      if (y >= thr) put(y, v);
-      else add_one(sum, y, c);
+  // the elements outside the vectors, each as the first of a vector of its own (its index
+  // complemented): the head with rank 0, the tail with the last rank
+  if (warp == 0) {
+    const bool in = lane < x.loose() && ((x.loose_at(lane) < x.head) ? rank == 0 : rank == CS - 1);
+    const float y = in ? x.at(x.loose_at(lane)) : -INFINITY;
+    const bool hit = in && y >= thr;
+    uint4 w = neg_inf_vec<kBF16>();
+    w.x = kBF16 ? (0xFF800000u | (__float_as_uint(y) >> 16)) : __float_as_uint(y);
+    list(hit, w, ~x.loose_at(lane), y);
+    if (in && !hit) add_one(sum, y, c);
+  }
+  {
+    const uint32_t k = __reduce_max_sync(0xffffffffu, fkey(mx + 0.0f));
+    if (lane == 0) {
+      sm.seg[warp] = listed;
+      atomicMax(&sm.top_key, k);
     }
   }
-  sum = block_merge(sum, c, sm.red);  // its barriers publish the list
+  for (int i = threadIdx.x; i < 256; i += kNT) sm.hist[i] = 0u;
 
   // ---- rank 0 gathers the lists and the sums --------------------------------------------------
-  uint32_t count = sm.n_list;
   if (CS > 1) {
+    Sum2 none{-FLT_MAX, 0.0f};
+    block_merge2(sum, none, c, sm.red);
     cg::cluster_group cl = cg::this_cluster();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (threadIdx.x == 0) {
       float* to = cl.map_shared_rank(&sm.part[rank][0], 0);
       to[0] = sum.ref;
       to[1] = sum.s;
-      *cl.map_shared_rank(&sm.count[rank], 0) = count;
+      if (rank != 0) atomicMax(cl.map_shared_rank(&sm.top_key, 0), sm.top_key);
     }
     cl.sync();
     if (rank == 0) {
-      count = 0;
-      for (int q = 0; q < CS; ++q) {
-        const uint32_t nq = sm.count[q];
-        if (q > 0) {
-          sum = merge(sum, Sum2{sm.part[q][0], sm.part[q][1]}, c);
-          const unsigned long long* from = cl.map_shared_rank(&sm.list[0], q);
-          if (count + nq <= static_cast<uint32_t>(kCap))
-            for (uint32_t i = threadIdx.x; i < nq; i += kNT) sm.list[count + i] = from[i];
+      // each warp appends the other CTAs' parts to its own (one that does not fit marks the list)
+      for (int q = 1; q < CS; ++q) {
+        const uint32_t other = *cl.map_shared_rank(&sm.seg[warp], q);
+        if (listed + other <= static_cast<uint32_t>(kSeg)) {
+          const uint4* fv = cl.map_shared_rank(seg_vec, q);
+          const int32_t* fa = cl.map_shared_rank(seg_at, q);
+          for (uint32_t i = lane; i < other; i += 32) {
+            seg_vec[listed + i] = fv[i];
+            seg_at[listed + i] = fa[i];
+          }
         }
-        count = nq > static_cast<uint32_t>(kCap) || count > static_cast<uint32_t>(kCap) ? kCap + 1u : count + nq;
+        listed += other;
       }
+      if (lane == 0) sm.seg[warp] = listed;
+      // the merged sum goes on as thread 0's
+      if (threadIdx.x != 0) sum = Sum2{-FLT_MAX, 0.0f};
+      else
+        for (int q = 1; q < CS; ++q) sum = merge(sum, Sum2{sm.part[q][0], sm.part[q][1]}, c);
     }
     cl.sync();  // the other CTAs' lists are read
     if (rank != 0) return;
   }
 
-  // a NaN anywhere in the sum, or a list of the wrong length: the exact selection
-  if (isnan(sum.s) || count < static_cast<uint32_t>(n) || count > static_cast<uint32_t>(kCap)) {
-    sum = exact_select<kBF16>(x, n, c, sm);
-    count = static_cast<uint32_t>(n);
-  }
-  int N = 2;
-  while (N < static_cast<int>(count)) N <<= 1;
-  for (int i = static_cast<int>(count + threadIdx.x); i < N; i += kNT) sm.list[i] = 0ull;  // below every word
-  __syncthreads();
-  if (n > 0) sort_desc(sm.list, N);
-
-  // ---- the outputs ----------------------------------------------------------------------------
-  Sum2 lead{-FLT_MAX, 0.0f}, left{-FLT_MAX, 0.0f};  // of the top, and of the list behind it
-  for (int i = threadIdx.x; i < static_cast<int>(count); i += kNT) {
-    const unsigned long long w = sm.list[i];
-    const float y = word_value(w);
-    add_one(i < n ? lead : left, y, c);
-    if (i < n) {
-      P.ids[row * n + i] = word_index(w);
-      P.values[row * n + i] = y;
+  // ---- the listed elements: cut to the n-th largest key's digit --------------------------------
+  const bool over = __syncthreads_or(listed > static_cast<uint32_t>(kSeg));
+  const bool nan = __syncthreads_or(isnan(sum.s));
+  bool exact = over || nan;
+  uint32_t cut = 0xFFFFFFFFu;  // keys from here on survive
+  const uint32_t tkey = thr == -INFINITY ? kKeyNegInf : fkey(thr + 0.0f);
+  auto elements = [&](auto&& f) {  // f(value, index) for every element of this warp's listed vectors
+    for (uint32_t i = lane; i < listed; i += 32) {
+      const uint4 w = seg_vec[i];
+      const int v0 = seg_at[i];
+#pragma unroll
+      for (int e = 0; e < G; ++e) {
+        if (v0 >= 0) f(clean(elem<kBF16>(w, e)), v0 + e);
+        else if (e == 0) f(clean(elem<kBF16>(w, e)), ~v0);
+      }
+    }
+  };
+  if (!exact && n > 0) {
+    uint32_t lo = tkey, hi = sm.top_key, need = static_cast<uint32_t>(n), above = 0;
+    for (;;) {
+      const uint32_t span = hi - lo;
+      const int shift = span >> 8 ? 24 - __clz(span) : 0;  // 256 bins over [lo, hi]
+      elements([&](float y, int) {
+        const uint32_t k = fkey(y);
+        if (k >= lo && k <= hi) atomicAdd(&sm.hist[(k - lo) >> shift], 1u);
+      });
+      if (threadIdx.x == 0) sm.bin = ~0u;
+      find_bin(sm, need);
+      if (sm.bin == ~0u) {  // fewer than n listed elements
+        exact = true;
+        break;
+      }
+      above += sm.above;
+      need -= sm.above;
+      lo += sm.bin << shift;
+      const uint32_t inside = sm.inside;
+      if (above + inside <= static_cast<uint32_t>(kWords)) {
+        cut = lo;
+        break;
+      }
+      if (shift == 0) {  // more equal keys than there is room for
+        exact = true;
+        break;
+      }
+      hi = lo + (1u << shift) - 1u;
+      __syncthreads();
+      for (int i = threadIdx.x; i < 256; i += kNT) sm.hist[i] = 0u;
+      __syncthreads();
     }
   }
-  left = block_merge(left, c, sm.red);
-  sum = merge(sum, left, c);
-  lead = block_merge(lead, c, sm.red);
+  if (exact) {
+    sum = exact_select<kBF16>(x, n, c, sm);
+  } else {
+    elements([&](float y, int v) {
+      const uint32_t k = fkey(y);
+      if (k >= cut) {
+        sm.words[atomicAdd(&sm.n_words, 1u)] = word_of(k, v);
+      } else if (y > -INFINITY) {
+        add_one(sum, y, c);
+      }
+    });
+  }
+  __syncthreads();
+  const int count = static_cast<int>(sm.n_words);
+
+  // ---- ranks and outputs ------------------------------------------------------------------------
+  Sum2 lead{-FLT_MAX, 0.0f};
+  auto out = [&](unsigned long long w, int i) {
+    const float y = word_value(w);
+    if (i < n) {
+      add_one(lead, y, c);
+      P.ids[row * n + i] = word_index(w);
+      P.values[row * n + i] = y;
+    } else {
+      add_one(sum, y, c);
+    }
+  };
+  if (count <= kPairwise) {
+    if (static_cast<int>(threadIdx.x) < count) {
+      const unsigned long long w = sm.words[threadIdx.x];
+      int r = 0;
+      for (int j = 0; j < count; ++j) r += sm.words[j] > w ? 1 : 0;
+      sm.vec[r].x = static_cast<uint32_t>(w);  // in rank order, so that the sums do not depend on the list's
+      sm.vec[r].y = static_cast<uint32_t>(w >> 32);
+    }
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < count) {
+      const uint4 w = sm.vec[threadIdx.x];
+      out((static_cast<unsigned long long>(w.y) << 32) | w.x, threadIdx.x);
+    }
+  } else {
+    int N = 2 * kPairwise;
+    while (N < count) N <<= 1;
+    for (int i = count + static_cast<int>(threadIdx.x); i < N; i += kNT) sm.words[i] = 0ull;  // below every word
+    __syncthreads();
+    sort_desc(sm.words, N);
+    for (int i = threadIdx.x; i < count; i += kNT) out(sm.words[i], i);
+  }
+  block_merge2(sum, lead, c, sm.red);
   if (threadIdx.x == 0) {
     const Sum2 all = merge(lead, sum, c);
     // a sum of nothing is -inf; a sum with +inf in it is +inf
@@ -367,10 +504,13 @@ __global__ void __launch_bounds__(kNT) top_kernel(const Params P) {
 // ------------------------------------------------------------------------------------------
 // Host side
 // ------------------------------------------------------------------------------------------
-template <bool kBF16>
-static kps_status launch(const Params& P, cudaStream_t stream) {
+template <bool kBF16, bool kSmall>
+static kps_status launch_t(const Params& P, cudaStream_t stream) {
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      (sizeof(Smem<kSmall>) > 48 * 1024 &&
+       cudaFuncSetAttribute(top_kernel<kBF16, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem<kSmall>)) !=
+           cudaSuccess)) {
     (void)cudaGetLastError();
     return KPS_ERR_CUDA;
   }
@@ -381,7 +521,7 @@ static kps_status launch(const Params& P, cudaStream_t stream) {
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(static_cast<unsigned>(P.B * cs));
   lc.blockDim = dim3(kNT);
-  lc.dynamicSmemBytes = sizeof(Smem);
+  lc.dynamicSmemBytes = sizeof(Smem<kSmall>);
   lc.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -390,11 +530,15 @@ static kps_status launch(const Params& P, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  if (cudaLaunchKernelEx(&lc, top_kernel<kBF16>, P) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&lc, top_kernel<kBF16, kSmall>, P) != cudaSuccess) {
     (void)cudaGetLastError();
     return KPS_ERR_CUDA;
   }
   return KPS_OK;
+}
+template <bool kBF16>
+static kps_status launch(const Params& P, cudaStream_t stream) {
+  return P.n <= kSmallN ? launch_t<kBF16, true>(P, stream) : launch_t<kBF16, false>(P, stream);
 }
 
 }  // namespace top
