@@ -160,6 +160,42 @@ __device__ __forceinline__ void add_vec(Sum2& sum, const uint4& w, float c) {
   sum.s += a + b;
 }
 
+// A sum against one reference that no element exceeds by much, for the inner loops: a pair of
+// partial sums for each pair of a vector, so that a vector adds one term to each.  The exponent
+// is one multiply-add, x c - rc with rc the rounded product of the reference and c: what rc's
+// rounding left out is put right once, in total().  Only for |rc| <= kFastRef.
+constexpr float kFastRef = 0x1p28f;
+template <bool kBF16>
+struct FastSum {
+  static constexpr int kPairs = kBF16 ? 4 : 2;
+  f32x2 acc[kPairs], c2, nrc2;
+  __device__ __forceinline__ FastSum(float ref, float c) {
+    const float rc = ref * c;
+    c2 = pack2(c, c);
+    nrc2 = pack2(-rc, -rc);
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) acc[i] = 0ull;
+  }
+  __device__ __forceinline__ void add(const uint4& w) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      float a, b;
+      unpack2(fma2(pair_of<kBF16>(w, i), c2, nrc2), a, b);
+      acc[i] = add2(acc[i], pack2(ex2(a), ex2(b)));
+    }
+  }
+  // The sum of 2^((x - ref) c).
+  __device__ __forceinline__ float total(float ref, float c) const {
+    f32x2 t = acc[0];
+#pragma unroll
+    for (int i = 1; i < kPairs; ++i) t = add2(t, acc[i]);
+    float a, b, rc, unused;
+    unpack2(t, a, b);
+    unpack2(nrc2, rc, unused);
+    return (a + b) * ex2(-fmaf(ref, c, rc));
+  }
+};
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));

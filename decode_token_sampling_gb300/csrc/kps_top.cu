@@ -224,7 +224,7 @@ __device__ __forceinline__ float elem(const uint4& w, int e) {
 }
 
 template <bool kBF16, bool kSmall>
-__global__ void __launch_bounds__(kNT) top_kernel(const Params P) {
+__global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P) {
   constexpr int G = kBF16 ? 8 : 4;
   constexpr int kSeg = Caps<kSmall>::seg, kWords = Caps<kSmall>::words;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -248,13 +248,14 @@ __global__ void __launch_bounds__(kNT) top_kernel(const Params P) {
 
   // ---- the threshold: every CTA of the row takes the same sample --------------------------
   float thr = n > 0 ? -INFINITY : INFINITY;  // n == 0: only +inf is listed
-  if (n > 0 && P.V > kAllV) {
+  float ref = 0.0f;                          // of the sum: the threshold; n == 0: the largest of the sample
+  if (P.V > kAllV || n == 0) {
     // kNT * per places in runs of 32 consecutive elements spread over the row, each the largest
     // of m elements for the longest rows.  The rank-th largest of the threads' maxima is reached
     // by about rank * one elements of the row, give or take sqrt(rank) * one: four of these and
     // six ranks on the safe side of n.
     const int m = (P.V + (1 << 18) - 1) >> 18;
-    int per = kMaxPer;
+    int per = P.V > kAllV ? kMaxPer : 1;
     float one, r;
     for (;; per >>= 1) {
       one = fmaxf(1.0f, static_cast<float>(P.V) / static_cast<float>(kNT * per * m));
@@ -263,26 +264,32 @@ __global__ void __launch_bounds__(kNT) top_kernel(const Params P) {
       if (r <= static_cast<float>(kMaxRank) || per == 1) break;
     }
     float y = -INFINITY;
-    const int runs = kNT / 32 * per;
+    const int step = P.V >= 32 * m ? (P.V - 32 * m) / (kNW * per - 1) : 0;
 #pragma unroll 4
     for (int i = 0; i < per; ++i) {
-      const int s = i * kNT + static_cast<int>(threadIdx.x);
-      const int64_t v = static_cast<int64_t>(s >> 5) * (P.V - 32 * m) / (runs - 1) + (s & 31);
-      for (int j = 0; j < m; ++j) y = fmaxf(y, x.at(static_cast<int>(v) + 32 * j));  // NaN is ignored
+      const int v = (i * kNW + warp) * step + lane;
+      for (int j = 0; j < m; ++j)
+        if (v + 32 * j < P.V) y = fmaxf(y, x.at(v + 32 * j));  // NaN is ignored
     }
     const uint32_t key = fkey(y + 0.0f);
-    uint32_t t = 0;  // the largest key, its low 16 bits zero, that `rank` maxima reach
+    const int want = n > 0 ? static_cast<int>(r) : 1;
+    uint32_t t = 0;  // the largest key, its low 16 bits zero, that `want` maxima reach
     for (int bit = 31; bit >= 16; --bit) {
       const uint32_t mid = t | (1u << bit);
-      if (__syncthreads_count(key >= mid) >= static_cast<int>(r)) t = mid;
+      if (__syncthreads_count(key >= mid) >= want) t = mid;
     }
-    if (t > kKeyNegInf) thr = kfloat(t);
+    if (t > kKeyNegInf) {
+      ref = kfloat(t);
+      if (n > 0) thr = ref;
+    } else if (n > 0) {
+      thr = -FLT_MAX;  // a row of -inf but for a few: everything finite
+    }
   }
   __syncthreads();
 
   // ---- the pass -----------------------------------------------------------------------------
-  Sum2 sum{-FLT_MAX, 0.0f};
-  const float lift = kRaise / c;
+  // everything summed here is below the threshold, the sum's reference
+  FastSum<kBF16> fast(ref, c);
   uint32_t listed = 0;  // this warp's
   uint4* const seg_vec = sm.vec + warp * kSeg;
   int32_t* const seg_at = sm.at + warp * kSeg;
@@ -306,25 +313,19 @@ __global__ void __launch_bounds__(kNT) top_kernel(const Params P) {
       const int g = base + u * kNT + static_cast<int>(threadIdx.x);
       w[u] = g < g1 ? ld_stream(x.vec + g) : neg_inf_vec<kBF16>();
     }
-    float top = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int g = base + u * kNT + static_cast<int>(threadIdx.x);
-      float m = vec_max<kBF16>(w[u]);
+      const float m = vec_max<kBF16>(w[u]);
       const bool hit = m >= thr && g < g1;
       if (__any_sync(0xffffffffu, hit)) {
         list(hit, w[u], x.head + g * G, m);
-        if (hit) {
-          w[u] = neg_inf_vec<kBF16>();
-          m = -INFINITY;
-        }
+        if (hit) w[u] = neg_inf_vec<kBF16>();
       }
-      top = fmaxf(top, m);
+      fast.add(w[u]);
     }
-    if (top > sum.ref + lift) sum.raise(clamp_ref(top), c);
-#pragma unroll
-    for (int u = 0; u < kU; ++u) add_vec<kBF16>(sum, w[u], c);
   }
+  Sum2 sum{ref, fast.total(ref, c)};
   // the elements outside the vectors, each as the first of a vector of its own (its index
   // complemented): the head with rank 0, the tail with the last rank
   if (warp == 0) {
@@ -383,9 +384,11 @@ __global__ void __launch_bounds__(kNT) top_kernel(const Params P) {
   }
 
   // ---- the listed elements: cut to the n-th largest key's digit --------------------------------
-  const bool over = __syncthreads_or(listed > static_cast<uint32_t>(kSeg));
-  const bool nan = __syncthreads_or(isnan(sum.s));
-  bool exact = over || nan;
+  // the sum is good when it is well inside fp32's range; when nothing comes near the threshold
+  // (or its product with c is large, or there is a NaN) the row is taken element by element
+  const bool bad = listed > static_cast<uint32_t>(kSeg) || !(sum.s < 0x1p100f) || fabsf(ref * c) > kFastRef;
+  bool exact = __syncthreads_or(bad);
+  if (thr > -FLT_MAX) exact = !__syncthreads_or(sum.s >= 0x1p-60f) || exact;
   uint32_t cut = 0xFFFFFFFFu;  // keys from here on survive
   const uint32_t tkey = thr == -INFINITY ? kKeyNegInf : fkey(thr + 0.0f);
   auto elements = [&](auto&& f) {  // f(value, index) for every element of this warp's listed vectors
