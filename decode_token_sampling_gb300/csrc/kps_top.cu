@@ -44,14 +44,14 @@ constexpr int kMaxRank = 96;   // rank of the threshold among the threads' sampl
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
 constexpr int kPairwise = 256;  // survivors ranked pairwise; more are sorted
 
-// Capacities: listed vectors (an equal part for each warp) and ranked survivors.  The small
-// form lets six CTAs share an SM; a list of 128 fills about 630 vectors of a long row.
+// Capacities: listed vectors (an equal segment for each warp that reads the row) and ranked
+// survivors.  The small form lets five CTAs share an SM; the top 128 of a long row list about
+// 550 vectors.
 constexpr int kSmallN = 128;
 template <bool kSmall>
 struct Caps {
   static constexpr int list = kSmall ? 1536 : 4096;
   static constexpr int words = kSmall ? 512 : 2048;
-  static constexpr int seg = list / kNW;
 };
 
 struct Params {
@@ -89,9 +89,9 @@ struct Smem {
   int32_t at[Caps<kSmall>::list];                 // index of each one's first element (~: its only one)
   uint32_t hist[256];
   float red[kNW][4];
-  float part[kMaxCS][2];  // the sums of the cluster's CTAs
-  uint32_t seg[kNW];      // vectors each warp listed
-  uint32_t top_key;       // of the listed elements
+  float part[kMaxCS * kNW];    // the sums of the cluster's warps
+  uint32_t seg[kMaxCS * kNW];  // vectors each warp listed
+  uint32_t top_key;            // of the listed elements
   uint32_t n_words;
   uint32_t bin, above, inside;
 };
@@ -118,21 +118,53 @@ __device__ __forceinline__ void add_one(Sum2& sum, float x, float c) {
   sum.s += ex2((x - sum.ref) * c);
 }
 
-// Descending bitonic sort of a[0..N), N a power of two.
-__device__ __forceinline__ void sort_desc(unsigned long long* a, int N) {
-  for (int k = 2; k <= N; k <<= 1) {
+// Descending bitonic sort of a[0 .. kNT * E): thread t holds entries E t .. E t + E - 1 in
+// registers, so partners are in the thread, across the warp, or, for the widest strides alone
+// (6 of 55 steps at 1024 entries), in shared memory.  Starts and ends with a barrier.
+template <int E>
+__device__ __noinline__ void sort_desc(unsigned long long* a) {
+  const int t0 = static_cast<int>(threadIdx.x) * E;
+  unsigned long long v[E];
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = a[t0 + e];
+  for (int k = 2; k <= kNT * E; k <<= 1) {
     for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int t = threadIdx.x; t < N / 2; t += kNT) {
-        const int i = 2 * t - (t & (j - 1)), l = i + j;
-        const unsigned long long p = a[i], q = a[l];
-        if (((i & k) == 0) ? p < q : p > q) {
-          a[i] = q;
-          a[l] = p;
+      if (j >= 32 * E) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < E; ++e) a[t0 + e] = v[e];
+        __syncthreads();
+      }
+      if (j < E) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+#pragma unroll
+          for (int o = 1; o < E; o <<= 1) {  // the stride as a constant, for the registers' sake
+            if (o != j || (e & o)) continue;
+            const bool desc = ((t0 + e) & k) == 0;
+            const unsigned long long p = v[e], q = v[e | o];
+            const bool swap = desc ? p < q : p > q;
+            v[e] = swap ? q : p;
+            v[e | o] = swap ? p : q;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int i = t0 + e;
+          const unsigned long long q = j >= 32 * E ? a[i ^ j] : __shfl_xor_sync(0xffffffffu, v[e], j / E);
+          // the lower index of the pair keeps the larger when descending
+          const bool larger = ((i & j) == 0) == ((i & k) == 0);
+          v[e] = larger ? (q > v[e] ? q : v[e]) : (q < v[e] ? q : v[e]);
         }
       }
-      __syncthreads();
     }
   }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < E; ++e) a[t0 + e] = v[e];
+  __syncthreads();
 }
 
 // Finds in hist (256 counts) the bin, from the top, where the running count reaches need:
@@ -226,7 +258,7 @@ __device__ __forceinline__ float elem(const uint4& w, int e) {
 template <bool kBF16, bool kSmall>
 __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P) {
   constexpr int G = kBF16 ? 8 : 4;
-  constexpr int kSeg = Caps<kSmall>::seg, kWords = Caps<kSmall>::words;
+  constexpr int kWords = Caps<kSmall>::words;
   extern __shared__ __align__(16) unsigned char smem[];
   Smem<kSmall>& sm = *reinterpret_cast<Smem<kSmall>*>(smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -239,11 +271,18 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
   const RowView<kBF16> x(P.x, row * P.ld, P.V);
   const int g0 = static_cast<int>(static_cast<int64_t>(x.nv) * rank / CS);
   const int g1 = static_cast<int>(static_cast<int64_t>(x.nv) * (rank + 1) / CS);
-  // every CTA of the cluster runs before any writes into another's shared memory
-  if (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  float token_logit = -INFINITY;
   if (threadIdx.x == 0) {
     sm.top_key = 0u;
     sm.n_words = 0u;
+  }
+  // every CTA of the cluster runs, and has set these, before any writes into another's shared memory
+  if (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (threadIdx.x == 0) {
+    if (P.logprob && rank == 0) {
+      const int64_t t = P.tokens[row];
+      token_logit = t >= 0 && t < P.V ? clean(x.at(static_cast<int>(t))) : NAN;  // NaN: no such token
+    }
   }
 
   // ---- the threshold: every CTA of the row takes the same sample --------------------------
@@ -251,26 +290,31 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
   float ref = 0.0f;                          // of the sum: the threshold; n == 0: the largest of the sample
   if (P.V > kAllV || n == 0) {
     // kNT * per places in runs of 32 consecutive elements spread over the row, each the largest
-    // of m elements for the longest rows.  The rank-th largest of the threads' maxima is reached
-    // by about rank * one elements of the row, give or take sqrt(rank) * one: four of these and
-    // six ranks on the safe side of n.
+    // of m elements for the longest rows, and a maximum of them per thread.  One element of the
+    // row in `one` is looked at, so of the row's first n about n / one are: fewer than `want`
+    // but for one row in 10^5 (a Poisson tail), so the want-th largest maximum is at most the
+    // n-th largest of the row.
     const int m = (P.V + (1 << 18) - 1) >> 18;
     int per = P.V > kAllV ? kMaxPer : 1;
     float one, r;
     for (;; per >>= 1) {
       one = fmaxf(1.0f, static_cast<float>(P.V) / static_cast<float>(kNT * per * m));
       r = static_cast<float>(n) / one;
-      r += 4.0f * sqrtf(r) + 6.0f;
+      r += 4.0f * sqrtf(r) + 3.5f;
       if (r <= static_cast<float>(kMaxRank) || per == 1) break;
     }
-    float y = -INFINITY;
     const int step = P.V >= 32 * m ? (P.V - 32 * m) / (kNW * per - 1) : 0;
-#pragma unroll 4
-    for (int i = 0; i < per; ++i) {
+    float place[kMaxPer];  // all loads in flight together
+#pragma unroll
+    for (int i = 0; i < kMaxPer; ++i) {
       const int v = (i * kNW + warp) * step + lane;
-      for (int j = 0; j < m; ++j)
-        if (v + 32 * j < P.V) y = fmaxf(y, x.at(v + 32 * j));  // NaN is ignored
+      place[i] = i < per && v < P.V ? x.at(v) : -INFINITY;
     }
+    float y = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kMaxPer; ++i) y = fmaxf(y, place[i]);  // NaN is ignored
+    for (int j = 1; j < m; ++j)
+      for (int i = 0; i < per; ++i) y = fmaxf(y, x.at((i * kNW + warp) * step + lane + 32 * j));
     const uint32_t key = fkey(y + 0.0f);
     const int want = n > 0 ? static_cast<int>(r) : 1;
     uint32_t t = 0;  // the largest key, its low 16 bits zero, that `want` maxima reach
@@ -286,19 +330,25 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
     }
   }
   __syncthreads();
+  if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 
   // ---- the pass -----------------------------------------------------------------------------
   // everything summed here is below the threshold, the sum's reference
   FastSum<kBF16> fast(ref, c);
+  // the list lives with rank 0: every warp of the cluster writes to a segment of its own there
+  cg::cluster_group cl = cg::this_cluster();
+  Smem<kSmall>& home = CS > 1 ? *cl.map_shared_rank(&sm, 0) : sm;
+  const uint32_t seg_cap = static_cast<uint32_t>(Caps<kSmall>::list / (kNW * CS));
+  const int seg = rank * kNW + warp;
   uint32_t listed = 0;  // this warp's
-  uint4* const seg_vec = sm.vec + warp * kSeg;
-  int32_t* const seg_at = sm.at + warp * kSeg;
+  uint4* const seg_vec = home.vec + seg * seg_cap;
+  int32_t* const seg_at = home.at + seg * seg_cap;
   float mx = -INFINITY;  // of the listed vectors
   auto list = [&](bool hit, const uint4& w, int first, float m) {
     const unsigned who = __ballot_sync(0xffffffffu, hit);
     const uint32_t pos = listed + __popc(who & lt);
     if (hit) {
-      if (pos < static_cast<uint32_t>(kSeg)) {
+      if (pos < seg_cap) {
         seg_vec[pos] = w;
         seg_at[pos] = first;
       }
@@ -325,7 +375,7 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
       fast.add(w[u]);
     }
   }
-  Sum2 sum{ref, fast.total(ref, c)};
+  Sum2 sum{ref, fast.total(ref, c)};  // one reference for all of them
   // the elements outside the vectors, each as the first of a vector of its own (its index
   // complemented): the head with rank 0, the tail with the last rank
   if (warp == 0) {
@@ -335,70 +385,44 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
     uint4 w = neg_inf_vec<kBF16>();
     w.x = kBF16 ? (0xFF800000u | (__float_as_uint(y) >> 16)) : __float_as_uint(y);
     list(hit, w, ~x.loose_at(lane), y);
-    if (in && !hit) add_one(sum, y, c);
+    if (in && !hit) sum.s += ex2((y - ref) * c);
   }
   {
     const uint32_t k = __reduce_max_sync(0xffffffffu, fkey(mx + 0.0f));
     if (lane == 0) {
-      sm.seg[warp] = listed;
-      atomicMax(&sm.top_key, k);
+      home.seg[seg] = listed;
+      atomicMax(&home.top_key, k);
     }
   }
-  for (int i = threadIdx.x; i < 256; i += kNT) sm.hist[i] = 0u;
-
-  // ---- rank 0 gathers the lists and the sums --------------------------------------------------
   if (CS > 1) {
-    Sum2 none{-FLT_MAX, 0.0f};
-    block_merge2(sum, none, c, sm.red);
-    cg::cluster_group cl = cg::this_cluster();
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (threadIdx.x == 0) {
-      float* to = cl.map_shared_rank(&sm.part[rank][0], 0);
-      to[0] = sum.ref;
-      to[1] = sum.s;
-      if (rank != 0) atomicMax(cl.map_shared_rank(&sm.top_key, 0), sm.top_key);
-    }
-    cl.sync();
-    if (rank == 0) {
-      // each warp appends the other CTAs' parts to its own (one that does not fit marks the list)
-      for (int q = 1; q < CS; ++q) {
-        const uint32_t other = *cl.map_shared_rank(&sm.seg[warp], q);
-        if (listed + other <= static_cast<uint32_t>(kSeg)) {
-          const uint4* fv = cl.map_shared_rank(seg_vec, q);
-          const int32_t* fa = cl.map_shared_rank(seg_at, q);
-          for (uint32_t i = lane; i < other; i += 32) {
-            seg_vec[listed + i] = fv[i];
-            seg_at[listed + i] = fa[i];
-          }
-        }
-        listed += other;
-      }
-      if (lane == 0) sm.seg[warp] = listed;
-      // the merged sum goes on as thread 0's
-      if (threadIdx.x != 0) sum = Sum2{-FLT_MAX, 0.0f};
-      else
-        for (int q = 1; q < CS; ++q) sum = merge(sum, Sum2{sm.part[q][0], sm.part[q][1]}, c);
-    }
-    cl.sync();  // the other CTAs' lists are read
+    const float s = warp_sum(sum.s);
+    if (lane == 0) home.part[seg] = s;
+  }
+  for (int i = threadIdx.x; i < 256; i += kNT) sm.hist[i] = 0u;
+  if (CS > 1) {
+    cl.sync();  // rank 0 holds everything
     if (rank != 0) return;
+    sum.s = static_cast<int>(threadIdx.x) < kNW * CS ? sm.part[threadIdx.x] : 0.0f;
+  } else {
+    __syncthreads();
   }
 
   // ---- the listed elements: cut to the n-th largest key's digit --------------------------------
+  const int nseg = kNW * CS;
+  const uint32_t most = static_cast<int>(threadIdx.x) < nseg ? sm.seg[threadIdx.x] : 0u;
   // the sum is good when it is well inside fp32's range; when nothing comes near the threshold
   // (or its product with c is large, or there is a NaN) the row is taken element by element
-  const bool bad = listed > static_cast<uint32_t>(kSeg) || !(sum.s < 0x1p100f) || fabsf(ref * c) > kFastRef;
+  const bool bad = most > seg_cap || !(sum.s < 0x1p100f) || fabsf(ref * c) > kFastRef;
   bool exact = __syncthreads_or(bad);
   if (thr > -FLT_MAX) exact = !__syncthreads_or(sum.s >= 0x1p-60f) || exact;
   uint32_t cut = 0xFFFFFFFFu;  // keys from here on survive
   const uint32_t tkey = thr == -INFINITY ? kKeyNegInf : fkey(thr + 0.0f);
-  auto elements = [&](auto&& f) {  // f(value, index) for every element of this warp's listed vectors
-    for (uint32_t i = lane; i < listed; i += 32) {
-      const uint4 w = seg_vec[i];
-      const int v0 = seg_at[i];
-#pragma unroll
-      for (int e = 0; e < G; ++e) {
-        if (v0 >= 0) f(clean(elem<kBF16>(w, e)), v0 + e);
-        else if (e == 0) f(clean(elem<kBF16>(w, e)), ~v0);
+  auto vectors = [&](auto&& f) {  // f(vector, index of its first element, elements) for the listed ones
+    for (int q = warp; q < nseg; q += kNW) {
+      const uint32_t count = sm.seg[q];
+      for (uint32_t i = lane; i < count; i += 32) {
+        const int v0 = sm.at[q * seg_cap + i];
+        f(sm.vec[q * seg_cap + i], v0 < 0 ? ~v0 : v0, v0 < 0 ? 1 : G);
       }
     }
   };
@@ -407,9 +431,12 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
     for (;;) {
       const uint32_t span = hi - lo;
       const int shift = span >> 8 ? 24 - __clz(span) : 0;  // 256 bins over [lo, hi]
-      elements([&](float y, int) {
-        const uint32_t k = fkey(y);
-        if (k >= lo && k <= hi) atomicAdd(&sm.hist[(k - lo) >> shift], 1u);
+      vectors([&](const uint4& w, int, int elems) {
+#pragma unroll
+        for (int e = 0; e < G; ++e) {
+          const uint32_t k = fkey(clean(elem<kBF16>(w, e)));
+          if (k >= lo && k <= hi && e < elems) atomicAdd(&sm.hist[(k - lo) >> shift], 1u);
+        }
       });
       if (threadIdx.x == 0) sm.bin = ~0u;
       find_bin(sm, need);
@@ -438,13 +465,22 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
   if (exact) {
     sum = exact_select<kBF16>(x, n, c, sm);
   } else {
-    elements([&](float y, int v) {
-      const uint32_t k = fkey(y);
-      if (k >= cut) {
-        sm.words[atomicAdd(&sm.n_words, 1u)] = word_of(k, v);
-      } else if (y > -INFINITY) {
-        add_one(sum, y, c);
+    vectors([&](const uint4& w, int v0, int elems) {
+      float y[G];
+      float m = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < G; ++e) {
+        y[e] = clean(elem<kBF16>(w, e));
+        const uint32_t k = fkey(y[e]);
+        if (k >= cut && e < elems) {
+          sm.words[atomicAdd(&sm.n_words, 1u)] = word_of(k, v0 + e);
+          y[e] = -INFINITY;
+        }
+        m = fmaxf(m, y[e]);
       }
+      if (m > sum.ref + kRaise / c) sum.raise(clamp_ref(m), c);
+#pragma unroll
+      for (int e = 0; e < G; ++e) sum.s += ex2((y[e] - sum.ref) * c);
     });
   }
   __syncthreads();
@@ -476,11 +512,10 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
       out((static_cast<unsigned long long>(w.y) << 32) | w.x, threadIdx.x);
     }
   } else {
-    int N = 2 * kPairwise;
-    while (N < count) N <<= 1;
-    for (int i = count + static_cast<int>(threadIdx.x); i < N; i += kNT) sm.words[i] = 0ull;  // below every word
-    __syncthreads();
-    sort_desc(sm.words, N);
+    for (int i = count + static_cast<int>(threadIdx.x); i < kWords; i += kNT) sm.words[i] = 0ull;  // below every word
+    if (count <= 2 * kNT || kWords == 2 * kNT) sort_desc<2>(sm.words);
+    else if (count <= 4 * kNT) sort_desc<4>(sm.words);
+    else sort_desc<8>(sm.words);
     for (int i = threadIdx.x; i < count; i += kNT) out(sm.words[i], i);
   }
   block_merge2(sum, lead, c, sm.red);
@@ -492,13 +527,10 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
     if (P.lse) P.lse[row] = lse;
     if (P.rest) P.rest[row] = ln(sum);
     if (P.logprob) {
-      const int64_t t = P.tokens[row];
       // relative to the sum's reference: lse and the token's logit are both large
-      float lp = -INFINITY;
-      if (t >= 0 && t < P.V) {
-        const float y = clean(x.at(static_cast<int>(t)));
-        lp = isinf(lse) ? y / P.tau - lse : (y - all.ref) / P.tau - logf(all.s);
-      }
+      const float y = token_logit;
+      float lp = isinf(lse) ? y / P.tau - lse : (y - all.ref) / P.tau - logf(all.s);
+      if (isnan(y)) lp = -INFINITY;
       P.logprob[row] = lp;
     }
   }
