@@ -132,17 +132,18 @@ __device__ __forceinline__ Sum2 merge(const Sum2& a, const Sum2& b, float c) {
   return Sum2{m, a.s * ex2((a.ref - m) * c) + b.s * ex2((b.ref - m) * c)};
 }
 
+// The warp's sums against the largest reference of those that hold anything; every lane gets the
+// same bits (no branch: a butterfly of merge() took ten times as long).
 __device__ __forceinline__ Sum2 warp_merge(Sum2 v, float c) {
+  float m = v.s == 0.0f ? -FLT_MAX : v.ref;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    Sum2 t;
-    t.ref = __shfl_xor_sync(0xffffffffu, v.ref, o);
-    t.s = __shfl_xor_sync(0xffffffffu, v.s, o);
-    // the same operand order in both lanes, so that both hold the same bits
-    v = (threadIdx.x & o) ? merge(t, v, c) : merge(v, t, c);
-  }
-  return v;
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float s = v.s == 0.0f ? 0.0f : v.s * ex2((v.ref - m) * c);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return Sum2{m, s};
 }
+
 // Adds the elements of a vector to a sum whose reference is high enough for them.
 template <bool kBF16>
 __device__ __forceinline__ void add_vec(Sum2& sum, const uint4& w, float c) {

@@ -12,7 +12,8 @@
 // list in shared memory whole (one ballot and two stores; taking single elements out of the
 // vector cost four times the instructions of the sum itself), all others into a running sum of
 // exponentials.  Then digits of the listed keys, counted, cut the list to little more than n
-// elements, which are ranked; everything else in the list joins the sum.  So the rest is a sum of
+// elements, which the first digit's counts also put in order but for the few that share one: these
+// are ranked pairwise.  Everything else in the list joins the sum.  So the rest is a sum of
 // its own, never a difference of two large ones.  A list that came out too short or too long (the
 // sample misjudged the row, or ties crowd the threshold) sends the row to an exact selection.
 
@@ -42,7 +43,6 @@ constexpr int kAllV = 4096;    // rows this short are listed whole
 constexpr int kMaxPer = 16;    // sampled places per thread, at most
 constexpr int kMaxRank = 96;   // rank of the threshold among the threads' sample maxima, at most
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
-constexpr int kPairwise = 256;  // survivors ranked pairwise; more are sorted
 
 // Capacities: listed vectors (an equal segment for each warp that reads the row) and ranked
 // survivors.  The small form lets five CTAs share an SM; the top 128 of a long row list about
@@ -88,6 +88,7 @@ struct Smem {
   uint4 vec[Caps<kSmall>::list];                  // the listed vectors, by warp
   int32_t at[Caps<kSmall>::list];                 // index of each one's first element (~: its only one)
   uint32_t hist[256];
+  uint32_t offset[256], filled[256];  // by first digit: survivors with a larger one, and with it
   float red[kNW][4];
   float part[kMaxCS * kNW];    // the sums of the cluster's warps
   uint32_t seg[kMaxCS * kNW];  // vectors each warp listed
@@ -114,63 +115,15 @@ __device__ __forceinline__ void block_merge2(Sum2& a, Sum2& b, float c, float (*
   b = warp_merge(Sum2{r[2], lane < kNW ? r[3] : 0.0f}, c);
 }
 __device__ __forceinline__ void add_one(Sum2& sum, float x, float c) {
-  if (x > sum.ref + kRaise / c) sum.raise(clamp_ref(x), c);
+  if ((x - sum.ref) * c > kRaise) sum.raise(clamp_ref(x), c);
   sum.s += ex2((x - sum.ref) * c);
 }
 
-// Descending bitonic sort of a[0 .. kNT * E): thread t holds entries E t .. E t + E - 1 in
-// registers, so partners are in the thread, across the warp, or, for the widest strides alone
-// (6 of 55 steps at 1024 entries), in shared memory.  Starts and ends with a barrier.
-template <int E>
-__device__ __noinline__ void sort_desc(unsigned long long* a) {
-  const int t0 = static_cast<int>(threadIdx.x) * E;
-  unsigned long long v[E];
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = a[t0 + e];
-  for (int k = 2; k <= kNT * E; k <<= 1) {
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      if (j >= 32 * E) {
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < E; ++e) a[t0 + e] = v[e];
-        __syncthreads();
-      }
-      if (j < E) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-#pragma unroll
-          for (int o = 1; o < E; o <<= 1) {  // the stride as a constant, for the registers' sake
-            if (o != j || (e & o)) continue;
-            const bool desc = ((t0 + e) & k) == 0;
-            const unsigned long long p = v[e], q = v[e | o];
-            const bool swap = desc ? p < q : p > q;
-            v[e] = swap ? q : p;
-            v[e | o] = swap ? p : q;
-          }
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int i = t0 + e;
-          const unsigned long long q = j >= 32 * E ? a[i ^ j] : __shfl_xor_sync(0xffffffffu, v[e], j / E);
-          // the lower index of the pair keeps the larger when descending
-          const bool larger = ((i & j) == 0) == ((i & k) == 0);
-          v[e] = larger ? (q > v[e] ? q : v[e]) : (q < v[e] ? q : v[e]);
-        }
-      }
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < E; ++e) a[t0 + e] = v[e];
-  __syncthreads();
-}
-
 // Finds in hist (256 counts) the bin, from the top, where the running count reaches need:
-// sm.bin, sm.above (the count over it) and sm.inside (its own).  Starts and ends with a barrier.
+// sm.bin, sm.above (the count over it) and sm.inside (its own).  With offsets, also every bin's
+// count over it.  Starts and ends with a barrier.
 template <class S>
-__device__ __forceinline__ void find_bin(S& sm, uint32_t need) {
+__device__ __forceinline__ void find_bin(S& sm, uint32_t need, bool offsets = false) {
   __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
@@ -187,6 +140,14 @@ __device__ __forceinline__ void find_bin(S& sm, uint32_t need) {
       if (lane >= o) incl += t;
     }
     uint32_t acc = incl - sum;
+    if (offsets) {
+      uint32_t o = acc;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sm.offset[255 - 8 * lane - i] = o;
+        o += n[i];
+      }
+    }
     if (acc < need && need <= incl) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -398,7 +359,10 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
     const float s = warp_sum(sum.s);
     if (lane == 0) home.part[seg] = s;
   }
-  for (int i = threadIdx.x; i < 256; i += kNT) sm.hist[i] = 0u;
+  for (int i = threadIdx.x; i < 256; i += kNT) {
+    sm.hist[i] = 0u;
+    sm.filled[i] = 0u;
+  }
   if (CS > 1) {
     cl.sync();  // rank 0 holds everything
     if (rank != 0) return;
@@ -416,11 +380,14 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
   bool exact = __syncthreads_or(bad);
   if (thr > -FLT_MAX) exact = !__syncthreads_or(sum.s >= 0x1p-60f) || exact;
   uint32_t cut = 0xFFFFFFFFu;  // keys from here on survive
+  int count = 0, digit = 0;    // the survivors, and the shift of their first digit
   const uint32_t tkey = thr == -INFINITY ? kKeyNegInf : fkey(thr + 0.0f);
   auto vectors = [&](auto&& f) {  // f(vector, index of its first element, elements) for the listed ones
-    for (int q = warp; q < nseg; q += kNW) {
+    // a warp for each segment, or for as many of a cluster's shorter ones as it has CTAs (at most four)
+    const int each = CS < 4 ? CS : 4, wide = 32 / each;
+    for (int q = warp * each + lane / wide; q < nseg; q += kNW * each) {
       const uint32_t count = sm.seg[q];
-      for (uint32_t i = lane; i < count; i += 32) {
+      for (uint32_t i = lane & (wide - 1); i < count; i += wide) {
         const int v0 = sm.at[q * seg_cap + i];
         f(sm.vec[q * seg_cap + i], v0 < 0 ? ~v0 : v0, v0 < 0 ? 1 : G);
       }
@@ -428,9 +395,10 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
   };
   if (!exact && n > 0) {
     uint32_t lo = tkey, hi = sm.top_key, need = static_cast<uint32_t>(n), above = 0;
-    for (;;) {
+    for (bool first = true;; first = false) {
       const uint32_t span = hi - lo;
       const int shift = span >> 8 ? 24 - __clz(span) : 0;  // 256 bins over [lo, hi]
+      if (first) digit = shift;
       vectors([&](const uint4& w, int, int elems) {
 #pragma unroll
         for (int e = 0; e < G; ++e) {
@@ -439,7 +407,7 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
         }
       });
       if (threadIdx.x == 0) sm.bin = ~0u;
-      find_bin(sm, need);
+      find_bin(sm, need, first);
       if (sm.bin == ~0u) {  // fewer than n listed elements
         exact = true;
         break;
@@ -450,6 +418,7 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
       const uint32_t inside = sm.inside;
       if (above + inside <= static_cast<uint32_t>(kWords)) {
         cut = lo;
+        count = static_cast<int>(above + inside);
         break;
       }
       if (shift == 0) {  // more equal keys than there is room for
@@ -464,6 +433,7 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
   }
   if (exact) {
     sum = exact_select<kBF16>(x, n, c, sm);
+    count = n;
   } else {
     vectors([&](const uint4& w, int v0, int elems) {
       float y[G];
@@ -473,50 +443,46 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
         y[e] = clean(elem<kBF16>(w, e));
         const uint32_t k = fkey(y[e]);
         if (k >= cut && e < elems) {
-          sm.words[atomicAdd(&sm.n_words, 1u)] = word_of(k, v0 + e);
+          const uint32_t d = (k - tkey) >> digit;
+          sm.words[sm.offset[d] + atomicAdd(&sm.filled[d], 1u)] = word_of(k, v0 + e);
           y[e] = -INFINITY;
         }
         m = fmaxf(m, y[e]);
       }
-      if (m > sum.ref + kRaise / c) sum.raise(clamp_ref(m), c);
+      if ((m - sum.ref) * c > kRaise) sum.raise(clamp_ref(m), c);
 #pragma unroll
       for (int e = 0; e < G; ++e) sum.s += ex2((y[e] - sum.ref) * c);
     });
   }
   __syncthreads();
-  const int count = static_cast<int>(sm.n_words);
 
   // ---- ranks and outputs ------------------------------------------------------------------------
+  unsigned long long* sorted = reinterpret_cast<unsigned long long*>(sm.vec);  // the list is done with
+  static_assert(sizeof(sm.vec) >= sizeof(sm.words), "the survivors in order take the list's place");
+  for (int i = threadIdx.x; i < count; i += kNT) {
+    const unsigned long long w = sm.words[i];
+    int first = 0, end = count;  // those that share the first digit
+    if (!exact) {
+      const uint32_t d = (static_cast<uint32_t>(w >> 32) - tkey) >> digit;
+      first = static_cast<int>(sm.offset[d]);
+      end = first + static_cast<int>(sm.filled[d]);
+    }
+    int r = first;
+    for (int j = first; j < end; ++j) r += sm.words[j] > w ? 1 : 0;
+    sorted[r] = w;
+  }
+  __syncthreads();
   Sum2 lead{-FLT_MAX, 0.0f};
-  auto out = [&](unsigned long long w, int i) {
+  for (int i = threadIdx.x; i < count; i += kNT) {
+    const unsigned long long w = sorted[i];
     const float y = word_value(w);
     if (i < n) {
-      add_one(lead, y, c);
       P.ids[row * n + i] = word_index(w);
       P.values[row * n + i] = y;
+      add_one(lead, y, c);
     } else {
       add_one(sum, y, c);
     }
-  };
-  if (count <= kPairwise) {
-    if (static_cast<int>(threadIdx.x) < count) {
-      const unsigned long long w = sm.words[threadIdx.x];
-      int r = 0;
-      for (int j = 0; j < count; ++j) r += sm.words[j] > w ? 1 : 0;
-      sm.vec[r].x = static_cast<uint32_t>(w);  // in rank order, so that the sums do not depend on the list's
-      sm.vec[r].y = static_cast<uint32_t>(w >> 32);
-    }
-    __syncthreads();
-    if (static_cast<int>(threadIdx.x) < count) {
-      const uint4 w = sm.vec[threadIdx.x];
-      out((static_cast<unsigned long long>(w.y) << 32) | w.x, threadIdx.x);
-    }
-  } else {
-    for (int i = count + static_cast<int>(threadIdx.x); i < kWords; i += kNT) sm.words[i] = 0ull;  // below every word
-    if (count <= 2 * kNT || kWords == 2 * kNT) sort_desc<2>(sm.words);
-    else if (count <= 4 * kNT) sort_desc<4>(sm.words);
-    else sort_desc<8>(sm.words);
-    for (int i = threadIdx.x; i < count; i += kNT) out(sm.words[i], i);
   }
   block_merge2(sum, lead, c, sm.red);
   if (threadIdx.x == 0) {
