@@ -35,7 +35,10 @@ using namespace stream;
 
 constexpr int kNT = 256;  // threads per CTA
 constexpr int kNW = kNT / 32;
-constexpr int kU = 4;          // 16-byte loads each thread keeps in flight
+// 16-byte loads each thread keeps in flight.  Six with four CTAs an SM (64 registers) took 133 us
+// for 2048 rows of 151936 bf16 and 24.8 us for 256; four with five CTAs 139 and 28.5 us, eight with
+// four 133 and 27.0 us.
+constexpr int kU = 6;
 constexpr int kMaxN = 1024;    // the framework's top-k limit
 constexpr int64_t kMaxV = 1 << 20;
 constexpr int kMaxCS = 8;      // widest cluster (the portable limit)
@@ -45,8 +48,8 @@ constexpr int kMaxRank = 96;   // rank of the threshold among the threads' sampl
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
 
 // Capacities: listed vectors (an equal segment for each warp that reads the row) and ranked
-// survivors.  The small form lets five CTAs share an SM; the top 128 of a long row list about
-// 550 vectors.
+// survivors.  The small form lets four CTAs share an SM with room left for their loads in flight
+// (lines of the first-level cache); the top 128 of a long row list about 550 vectors.
 constexpr int kSmallN = 128;
 template <bool kSmall>
 struct Caps {
@@ -163,51 +166,6 @@ __device__ __forceinline__ void find_bin(S& sm, uint32_t need, bool offsets = fa
   __syncthreads();
 }
 
-// One element at a time over the row: f(value with NaN -> -inf, index).
-template <bool kBF16, class F>
-__device__ __forceinline__ void each(const RowView<kBF16>& x, F&& f) {
-  for (int v = threadIdx.x; v < x.V; v += kNT) f(clean(x.at(v)), v);
-}
-
-// The exact selection, by one CTA: the n-th element of the order by 8-bit digits of its key and,
-// among equal keys, of its index; then the n elements as survivors and the thread's sum of all others.
-template <bool kBF16, class S>
-__device__ __noinline__ Sum2 exact_select(const RowView<kBF16>& x, int n, float c, S& sm) {
-  uint32_t need = static_cast<uint32_t>(n);
-  unsigned long long at = 0;  // the digits found so far, from the top of the 64-bit word
-  __syncthreads();            // everything before is done with what is written below
-  if (n > 0) {
-    for (int shift = 56; shift >= 0; shift -= 8) {
-      if (shift == 24) {  // indexes are below 2^20: the top 8 bits of their complements are ones
-        at |= 0xFFull << 24;
-        continue;
-      }
-      for (int i = threadIdx.x; i < 256; i += kNT) sm.hist[i] = 0u;
-      __syncthreads();
-      each<kBF16>(x, [&](float y, int v) {
-        const unsigned long long w = word_of(fkey(y), v);
-        if (shift == 56 || (w >> (shift + 8)) == (at >> (shift + 8))) atomicAdd(&sm.hist[(w >> shift) & 255u], 1u);
-      });
-      find_bin(sm, need);
-      at |= static_cast<unsigned long long>(sm.bin) << shift;
-      need -= sm.above;
-      __syncthreads();
-    }
-  }
-  if (threadIdx.x == 0) sm.n_words = 0u;
-  __syncthreads();
-  Sum2 sum{-FLT_MAX, 0.0f};
-  each<kBF16>(x, [&](float y, int v) {
-    const unsigned long long w = word_of(fkey(y), v);
-    if (n > 0 && w >= at) {
-      sm.words[atomicAdd(&sm.n_words, 1u)] = w;  // n of them
-    } else {
-      add_one(sum, y, c);
-    }
-  });
-  return sum;
-}
-
 // Element e of a vector as fp32.
 template <bool kBF16>
 __device__ __forceinline__ float elem(const uint4& w, int e) {
@@ -216,8 +174,90 @@ __device__ __forceinline__ float elem(const uint4& w, int e) {
   return __uint_as_float(word[e]);
 }
 
+// Every element of the row, with the warp converged: f(valid, value with NaN -> -inf, index).
+template <bool kBF16, class F>
+__device__ __forceinline__ void each(const RowView<kBF16>& x, F&& f) {
+  constexpr int G = kBF16 ? 8 : 4;
+  for (int base = 0; base < x.nv; base += kNT * kU) {
+    uint4 w[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int g = base + u * kNT + static_cast<int>(threadIdx.x);
+      w[u] = g < x.nv ? ld_stream(x.vec + g) : neg_inf_vec<kBF16>();
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int g = base + u * kNT + static_cast<int>(threadIdx.x);
+#pragma unroll
+      for (int e = 0; e < G; ++e) f(g < x.nv, clean(elem<kBF16>(w[u], e)), x.head + g * G + e);
+    }
+  }
+  const bool in = static_cast<int>(threadIdx.x) < x.loose();
+  const int v = in ? x.loose_at(threadIdx.x) : 0;
+  f(in, in ? clean(x.at(v)) : -INFINITY, v);
+}
+
+// The exact selection, by one CTA, for rows whose list came out too short or too long: the n-th
+// element of the order by 8-bit digits of its key and, among equal keys, of its index; then the n
+// elements as survivors and the thread's sum of all others.  At least n elements have a key of
+// floor or more.
+template <bool kBF16, class S>
+__device__ __noinline__ Sum2 exact_select(const RowView<kBF16>& x, int n, uint32_t floor, float c, S& sm) {
+  uint32_t need = static_cast<uint32_t>(n);
+  unsigned long long at = 0;  // the digits found so far, from the top of the 64-bit word
+  __syncthreads();            // everything before is done with what is written below
+  if (n > 0) {
+    for (int shift = 56; shift >= 0; shift -= 8) {
+      if (kBF16 && shift == 40) {  // a bf16 key's low half follows from its sign
+        at |= (at >> 63) ? 0ull : 0xFFFFull << 32;
+        shift = 32;
+        if (sm.inside == need) break;
+        continue;
+      }
+      if (shift == 24) {  // indexes are below 2^20: the top 8 bits of their complements are ones
+        at |= 0xFFull << 24;
+        continue;
+      }
+      for (int i = threadIdx.x; i < 256; i += kNT) sm.hist[i] = 0u;
+      __syncthreads();
+      each<kBF16>(x, [&](bool valid, float y, int v) {
+        const unsigned long long w = word_of(fkey(y), v);
+        const bool ok = valid && (w >> 32) >= floor && (shift == 56 || (w >> (shift + 8)) == (at >> (shift + 8)));
+        const int d = static_cast<int>((w >> shift) & 255u);
+        const unsigned who = __ballot_sync(0xffffffffu, ok);
+        if (who == 0u) return;
+        // one add for a warp that agrees (equal values side by side would otherwise queue up)
+        const int d0 = __shfl_sync(0xffffffffu, d, __ffs(who) - 1);
+        if (__all_sync(0xffffffffu, !ok || d == d0)) {
+          if ((threadIdx.x & 31) == 0) atomicAdd(&sm.hist[d0], static_cast<uint32_t>(__popc(who)));
+        } else if (ok) {
+          atomicAdd(&sm.hist[d], 1u);
+        }
+      });
+      find_bin(sm, need);
+      at |= static_cast<unsigned long long>(sm.bin) << shift;
+      need -= sm.above;
+      if (shift == 32 && sm.inside == need) break;  // every element equal to the n-th belongs
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) sm.n_words = 0u;
+  __syncthreads();
+  Sum2 sum{-FLT_MAX, 0.0f};
+  each<kBF16>(x, [&](bool valid, float y, int v) {
+    const unsigned long long w = word_of(fkey(y), v);
+    if (valid && n > 0 && w >= at) {
+      sm.words[atomicAdd(&sm.n_words, 1u)] = w;  // n of them
+    } else if (valid) {
+      add_one(sum, y, c);
+    }
+  });
+  return sum;
+}
+
 template <bool kBF16, bool kSmall>
-__global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P) {
+__global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P) {
   constexpr int G = kBF16 ? 8 : 4;
   constexpr int kWords = Caps<kSmall>::words;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -279,13 +319,22 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
     const uint32_t key = fkey(y + 0.0f);
     const int want = n > 0 ? static_cast<int>(r) : 1;
     uint32_t t = 0;  // the largest key, its low 16 bits zero, that `want` maxima reach
+    int reach = kNT;
     for (int bit = 31; bit >= 16; --bit) {
       const uint32_t mid = t | (1u << bit);
-      if (__syncthreads_count(key >= mid) >= want) t = mid;
+      const int k = __syncthreads_count(key >= mid);
+      if (k >= want) {
+        t = mid;
+        reach = k;
+      }
     }
+    // half of the sample shares the threshold's digits: a mask's value, as in a row that allows
+    // some tokens only.  What the row can offer lies above it (if not, the list is too short).
+    if (n > 0 && reach >= kNT / 2 && t > kKeyNegInf && t < 0xFF000000u) t += 0x10000u;
     if (t > kKeyNegInf) {
       ref = kfloat(t);
       if (n > 0) thr = ref;
+      if (fabsf(ref * c) > kFastRef) ref = 0.0f;  // far below zero: what is not listed weighs nothing against it
     } else if (n > 0) {
       thr = -FLT_MAX;  // a row of -inf but for a few: everything finite
     }
@@ -374,11 +423,12 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
   // ---- the listed elements: cut to the n-th largest key's digit --------------------------------
   const int nseg = kNW * CS;
   const uint32_t most = static_cast<int>(threadIdx.x) < nseg ? sm.seg[threadIdx.x] : 0u;
-  // the sum is good when it is well inside fp32's range; when nothing comes near the threshold
-  // (or its product with c is large, or there is a NaN) the row is taken element by element
-  const bool bad = most > seg_cap || !(sum.s < 0x1p100f) || fabsf(ref * c) > kFastRef;
+  // a list that overflowed, a NaN, a sum past fp32's range: the exact selection.  A sum that
+  // nothing near its reference holds up is taken again against what there is.
+  const bool over = __syncthreads_or(most > seg_cap);
+  const bool bad = over || !(sum.s < 0x1p100f);
   bool exact = __syncthreads_or(bad);
-  if (thr > -FLT_MAX) exact = !__syncthreads_or(sum.s >= 0x1p-60f) || exact;
+  const bool weak = !__syncthreads_or(sum.s >= 0x1p-60f) && thr > -FLT_MAX;
   uint32_t cut = 0xFFFFFFFFu;  // keys from here on survive
   int count = 0, digit = 0;    // the survivors, and the shift of their first digit
   const uint32_t tkey = thr == -INFINITY ? kKeyNegInf : fkey(thr + 0.0f);
@@ -432,7 +482,8 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
     }
   }
   if (exact) {
-    sum = exact_select<kBF16>(x, n, c, sm);
+    // (an overflown segment holds more than its capacity of vectors that reach the threshold)
+    sum = exact_select<kBF16>(x, n, over && seg_cap >= static_cast<uint32_t>(n) ? tkey : 0u, c, sm);
     count = n;
   } else {
     vectors([&](const uint4& w, int v0, int elems) {
@@ -453,6 +504,12 @@ __global__ void __launch_bounds__(kNT, kSmall ? 5 : 2) top_kernel(const Params P
 #pragma unroll
       for (int e = 0; e < G; ++e) sum.s += ex2((y[e] - sum.ref) * c);
     });
+    if (weak) {
+      sum = Sum2{-FLT_MAX, 0.0f};
+      each<kBF16>(x, [&](bool valid, float y, int) {
+        if (valid && fkey(y) < cut) add_one(sum, y, c);
+      });
+    }
   }
   __syncthreads();
 
