@@ -23,6 +23,7 @@
 
 #include <cooperative_groups.h>
 
+#include <atomic>
 #include <climits>
 #include <cmath>
 
@@ -39,6 +40,7 @@ constexpr int kU = 4;         // 16-byte loads each thread keeps in flight
 constexpr int kMaxK = 1024;   // teacher slots a row may have (the framework's top-k limit)
 constexpr int64_t kMaxV = 1 << 20;
 constexpr int kMaxCS = 8;     // widest cluster (the portable limit)
+constexpr int kMaxDevices = 64;
 constexpr int kStats = 4;     // floats of statistics per row
 
 enum Mode { kForward = 0, kBackward = 1, kBoth = 2 };
@@ -125,12 +127,141 @@ __device__ __forceinline__ Sum2 block_merge(Sum2 v, float c, float (*red)[2]) {
 }
 
 __device__ __forceinline__ void add_one(Sum2& sum, float x, float c) {
-  if (x > sum.ref + kRaise / c) sum.raise(clamp_ref(x), c);
+  if ((x - sum.ref) * c > kRaise) sum.raise(clamp_ref(x), c);
   sum.s += ex2((x - sum.ref) * c);
 }
 
 // log2(1 + 2^z).
 __device__ __forceinline__ float log2_1p_ex2(float z) { return z > 24.0f ? z : kLog2e * log1pf(ex2(z)); }
+
+// The divergence in base 2, from the teacher's E = sum 2^(u_k), W = sum 2^(u_k) (u_k - v_k) over
+// the list and er = 2^(ur) of the rest, and the student's sums.
+template <bool kRest>
+__device__ __forceinline__ float divergence(float E, float W, float er, float ur, float ref, const Sum2& list,
+                                            const Sum2& rest, const Sum2& all, float c) {
+  // ls = log2 S and lr = log2 SR against ref
+  const float ls = log2f(all.s) + (all.ref - ref) * c;
+  if (!kRest || er == 0.0f) return W / E - log2f(E) + ls;
+  if (rest.s == 0.0f) return INFINITY;  // the teacher's rest has mass, the student's none
+  const float Et = E + er, pr = er / Et;
+  const float lr = log2f(rest.s) + (rest.ref - ref) * c;
+  if (!(pr >= 0.5f)) return (W + er * (ur - lr)) / Et - log2f(Et) + ls;
+  // most mass is the rest's: ln p_r and ln q_r from what they leave, so that two numbers near
+  // zero are not differences of large ones
+  const float q = list.s > 0.0f ? log2_1p_ex2(log2f(list.s / rest.s) + (list.ref - rest.ref) * c) : 0.0f;
+  return W / Et - E / Et * (ur - lr) - kLog2e * log1pf(E / er) + q;
+}
+
+// Writes zeros to this CTA's part of a row of the gradient.
+template <bool kBF16>
+__device__ __forceinline__ void zero_row(void* grad, int64_t offset, int V, int rank, int CS) {
+  const RowView<kBF16> o(grad, offset, V);
+  const int o0 = static_cast<int>(static_cast<int64_t>(o.nv) * rank / CS);
+  const int o1 = static_cast<int>(static_cast<int64_t>(o.nv) * (rank + 1) / CS);
+  uint4* ov = const_cast<uint4*>(o.vec);
+  for (int g = o0 + static_cast<int>(threadIdx.x); g < o1; g += kNT) __stcs(ov + g, make_uint4(0u, 0u, 0u, 0u));
+  if (rank == 0 && static_cast<int>(threadIdx.x) < o.loose()) {
+    const int v = o.loose_at(threadIdx.x);
+    if (kBF16) reinterpret_cast<__nv_bfloat16*>(const_cast<unsigned char*>(o.base))[v] = __float2bfloat16(0.0f);
+    else reinterpret_cast<float*>(const_cast<unsigned char*>(o.base))[v] = 0.0f;
+  }
+}
+
+// Takes the list's tokens (bits m) out of a vector into their own sum.
+template <bool kBF16>
+__device__ __forceinline__ void take_listed(uint4& v, uint32_t m, Sum2& list, float c) {
+  constexpr int G = kBF16 ? 8 : 4;
+  uint32_t word[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < G; ++e) {
+    if (!((m >> e) & 1u)) continue;
+    if (kBF16) {
+      const uint32_t h = (e & 1) ? (word[e / 2] & 0xFFFF0000u) : (word[e / 2] << 16);
+      add_one(list, __uint_as_float(h), c);
+      word[e / 2] = (e & 1) ? (word[e / 2] & 0x0000FFFFu) | 0xFF800000u : (word[e / 2] & 0xFFFF0000u) | 0x0000FF80u;
+    } else {
+      add_one(list, __uint_as_float(word[e]), c);
+      word[e] = 0xFF800000u;
+    }
+  }
+  v = make_uint4(word[0], word[1], word[2], word[3]);
+}
+
+// Inserts a token of the list into a table of its distinct tokens; true when it was there already.
+__device__ __forceinline__ bool insert_token(int32_t* hash, int size, int32_t id) {
+  uint32_t h = (static_cast<uint32_t>(id) * 2654435761u) & (size - 1);
+  for (;;) {
+    const int32_t old = atomicCAS(&hash[h], -1, id);
+    if (old == -1) return false;
+    if (old == id) return true;
+    h = (h + 1) & (size - 1);  // at most K of the 2K places are taken
+  }
+}
+
+// The gradient's factors: d_v = A 2^((s_v - all.ref) c) - p_v for a token of the list, less
+// B 2^((s_v - rest.ref) c) for any other; C covers both terms of the latter with one exponential
+// unless the two references lie too far apart for fp32 (one false).
+struct Factors {
+  float A, B, C;
+  bool one;
+  __device__ __forceinline__ Factors(float scale, float er, float invE, const Sum2& all, const Sum2& rest, float c) {
+    A = all.s > 0.0f && all.s < INFINITY ? scale / all.s : NAN;
+    B = er != 0.0f ? scale * (er * invE) / rest.s : 0.0f;
+    const float apart = (all.ref - rest.ref) * c;
+    one = er == 0.0f || apart < 80.0f;
+    C = er == 0.0f ? A : A - B * ex2(apart);
+  }
+  __device__ __forceinline__ float outside(float s, const Sum2& all, const Sum2& rest, float c) const {
+    const float a = ex2((s - all.ref) * c);
+    return one ? C * a : A * a - B * ex2((s - rest.ref) * c);
+  }
+};
+template <bool kBF16>
+__device__ __forceinline__ void put_grad(unsigned char* base, int v, float d) {
+  if (kBF16) reinterpret_cast<__nv_bfloat16*>(base)[v] = __float2bfloat16_rn(d);
+  else reinterpret_cast<float*>(base)[v] = d;
+}
+// The gradient of a vector's tokens: C 2^(x c - rc).
+template <bool kBF16>
+__device__ __forceinline__ uint4 grad_vec(const uint4& w, f32x2 c2, f32x2 nrc2, f32x2 C2) {
+  uint32_t out[4];
+#pragma unroll
+  for (int i = 0; i < (kBF16 ? 4 : 2); ++i) {
+    float a, b;
+    unpack2(fma2(pair_of<kBF16>(w, i), c2, nrc2), a, b);
+    unpack2(mul2(pack2(ex2(a), ex2(b)), C2), a, b);
+    if (kBF16) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);  // the gradient's one rounding
+      out[i] = reinterpret_cast<const uint32_t&>(h);
+    } else {
+      out[2 * i] = __float_as_uint(a);
+      out[2 * i + 1] = __float_as_uint(b);
+    }
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+// The gradient of the list's tokens in [v0, v1), over what is there.  A token of several slots
+// (dup: there are some) takes the sum of their masses in slot order, at its first slot.
+template <bool kBF16>
+__device__ __forceinline__ void put_listed(unsigned char* base, int v0, int v1, bool dup, int K, const int32_t* s_id,
+                                           const float* s_e, const float* s_v, float shift, float A, float unit) {
+  for (int k = threadIdx.x; k < K; k += kNT) {
+    const int32_t id = s_id[k];
+    if (id < v0 || id >= v1) continue;  // empty slots are -1
+    float e = s_e[k];
+    if (dup) {
+      e = 0.0f;
+      bool first = true;
+      for (int j = 0; j < K; ++j) {
+        if (s_id[j] != id) continue;
+        first = first && j >= k;
+        e += s_e[j];
+      }
+      if (!first) continue;
+    }
+    put_grad<kBF16>(base, id, A * ex2(s_v[k] + shift) - unit * e);
+  }
+}
 
 template <bool kBF16, bool kRest, int kMode>
 __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
@@ -202,16 +333,7 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
         for (int i = 0; i < kStats; ++i) P.stats[row * kStats + i] = 0.0f;
     }
     if (kMode != kForward) {
-      const RowView<kBF16> o(P.grad, row * P.ld_grad, V);
-      const int o0 = static_cast<int>(static_cast<int64_t>(o.nv) * rank / CS);
-      const int o1 = static_cast<int>(static_cast<int64_t>(o.nv) * (rank + 1) / CS);
-      uint4* ov = const_cast<uint4*>(o.vec);
-      for (int g = o0 + static_cast<int>(threadIdx.x); g < o1; g += kNT) __stcs(ov + g, make_uint4(0u, 0u, 0u, 0u));
-      if (rank == 0 && static_cast<int>(threadIdx.x) < o.loose()) {
-        const int v = o.loose_at(threadIdx.x);
-        if (kBF16) reinterpret_cast<__nv_bfloat16*>(const_cast<unsigned char*>(o.base))[v] = __float2bfloat16(0.0f);
-        else reinterpret_cast<float*>(const_cast<unsigned char*>(o.base))[v] = 0.0f;
-      }
+      zero_row<kBF16>(P.grad, row * P.ld_grad, V, rank, CS);
     }
     return;
   }
@@ -243,17 +365,7 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
         if (b >= 0 && b < nbits) atomicOr(&s_bits[b >> 5], 1u << (b & 31));
       }
       if (kMode != kForward) {
-        // the list's distinct ids: a second slot of the same token marks the row
-        uint32_t h = (static_cast<uint32_t>(id) * 2654435761u) & (lay.hash_size - 1);
-        for (;;) {
-          const int32_t old = atomicCAS(&s_hash[h], -1, id);
-          if (old == -1) break;
-          if (old == id) {
-            twice = true;
-            break;
-          }
-          h = (h + 1) & (lay.hash_size - 1);  // at most K of the 2K places are taken
-        }
+        twice |= insert_token(s_hash, lay.hash_size, id);
       }
     }
     s_e[k] = e;
@@ -285,22 +397,7 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
           const int b = (g - g0 + 1) * G;
           uint32_t m = g < g1 ? bytes[b >> 3] : 0u;
           if (!kBF16) m = (m >> (b & 4)) & 15u;
-          if (m) {
-            uint32_t word[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-            for (int e = 0; e < G; ++e) {
-              if (!((m >> e) & 1u)) continue;
-              if (kBF16) {
-                const uint32_t h = (e & 1) ? (word[e / 2] & 0xFFFF0000u) : (word[e / 2] << 16);
-                add_one(list, __uint_as_float(h), c);
-                word[e / 2] = (e & 1) ? (word[e / 2] & 0x0000FFFFu) | 0xFF800000u : (word[e / 2] & 0xFFFF0000u) | 0x0000FF80u;
-              } else {
-                add_one(list, __uint_as_float(word[e]), c);
-                word[e] = 0xFF800000u;
-              }
-            }
-            v[u] = make_uint4(word[0], word[1], word[2], word[3]);
-          }
+          if (m) take_listed<kBF16>(v[u], m, list, c);
         }
       }
       float m = vec_max<kBF16>(v[0]);
@@ -340,23 +437,7 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
     }
     all = kRest ? merge(list, rest, c) : rest;
     if (rank == 0 && threadIdx.x == 0) {
-      // in base 2: ls = log2 S and lr = log2 SR against ref
-      const float ls = log2f(all.s) + (all.ref - ref) * c;
-      float kl = W / E - log2f(E) + ls;  // without a rest class
-      if constexpr (kRest) {
-        const float Et = E + er, pr = er / Et;
-        const float lr = log2f(rest.s) + (rest.ref - ref) * c;
-        if (er != 0.0f && rest.s == 0.0f) {
-          kl = INFINITY;  // the teacher's rest has mass, the student's none
-        } else if (pr >= 0.5f) {
-          // most mass is the rest's: ln p_r and ln q_r from what they leave, so that two
-          // numbers near zero are not differences of large ones
-          const float q = list.s > 0.0f ? log2_1p_ex2(log2f(list.s / rest.s) + (list.ref - rest.ref) * c) : 0.0f;
-          kl = W / Et - E / Et * (ur - lr) - kLog2e * log1pf(E / er) + q;
-        } else if (er != 0.0f) {
-          kl = (W + er * (ur - lr)) / Et - log2f(Et) + ls;
-        }
-      }
+      const float kl = divergence<kRest>(E, W, er, ur, ref, list, rest, all, c);
       const bool ok = all.s > 0.0f && all.s < INFINITY;
       P.loss[row] = ok ? w * P.tau * P.tau * (kl * kLn2) : NAN;
       if (kMode == kForward && P.stats) {
@@ -371,27 +452,14 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
 
   // ---- the gradient -------------------------------------------------------------------
   if (kMode != kForward) {
-    // d_v = scale (q_v - p_v): q_v = 2^((s_v - all.ref) c) / all.s; a token outside the list has
-    // p_v = p_r 2^((s_v - rest.ref) c) / rest.s, so one factor of one exponential covers both
-    // unless the two references lie too far apart for fp32
     const float invE = 1.0f / (E + er);
-    const float A = all.s > 0.0f && all.s < INFINITY ? scale / all.s : NAN;
-    const float B = er != 0.0f ? scale * (er * invE) / rest.s : 0.0f;
-    const float apart = (all.ref - rest.ref) * c;
-    const bool one = er == 0.0f || apart < 80.0f;
-    const float C = er == 0.0f ? A : A - B * ex2(apart);
-    auto outside = [&](float s) {  // d of a token outside the list
-      const float a = ex2((s - all.ref) * c);
-      return one ? C * a : A * a - B * ex2((s - rest.ref) * c);
-    };
+    const Factors F(scale, er, invE, all, rest, c);
     const RowView<kBF16> o(P.grad, row * P.ld_grad, V);
     unsigned char* obase = const_cast<unsigned char*>(o.base);
-    auto put = [&](int v, float d) {
-      if (kBF16) reinterpret_cast<__nv_bfloat16*>(obase)[v] = __float2bfloat16_rn(d);
-      else reinterpret_cast<float*>(obase)[v] = d;
-    };
-    if (one && o.head == x.head) {
-      const f32x2 nref = pack2(-all.ref, -all.ref), c2 = pack2(c, c), C2 = pack2(C, C);
+    const float rc = all.ref * c;
+    if (F.one && o.head == x.head && fabsf(rc) <= kFastRef) {
+      const float fix = ex2(-fmaf(all.ref, c, -rc));  // what rc's rounding left out
+      const f32x2 nrc2 = pack2(-rc, -rc), c2 = pack2(c, c), C2 = pack2(F.C * fix, F.C * fix);
       uint4* ov = const_cast<uint4*>(o.vec);
       for (int base = g0; base < g1; base += kNT * kU) {
         uint4 v[kU];
@@ -403,55 +471,281 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const int g = base + u * kNT + static_cast<int>(threadIdx.x);
-          uint32_t out[4];
-#pragma unroll
-          for (int i = 0; i < G / 2; ++i) {
-            float a, b;
-            unpack2(mul2(add2(pair_of<kBF16>(v[u], i), nref), c2), a, b);
-            unpack2(mul2(pack2(ex2(a), ex2(b)), C2), a, b);
-            if (kBF16) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);  // the gradient's one rounding
-              out[i] = reinterpret_cast<const uint32_t&>(h);
-            } else {
-              out[2 * i] = __float_as_uint(a);
-              out[2 * i + 1] = __float_as_uint(b);
-            }
-          }
-          if (g < g1) __stcs(ov + g, make_uint4(out[0], out[1], out[2], out[3]));
+          if (g < g1) __stcs(ov + g, grad_vec<kBF16>(v[u], c2, nrc2, C2));
         }
       }
       if (static_cast<int>(threadIdx.x) < x.loose()) {
         const int v = x.loose_at(threadIdx.x);
-        if ((v < x.head) ? rank == 0 : rank == CS - 1) put(v, outside(x.at(v)));
+        if ((v < x.head) ? rank == 0 : rank == CS - 1) put_grad<kBF16>(obase, v, F.outside(x.at(v), all, rest, c));
       }
     } else {
-      // the two rows do not share their 16-byte boundaries: one element at a time
+      // the two rows do not share their 16-byte boundaries, or the numbers are extreme: one
+      // element at a time
       const int v0 = rank == 0 ? 0 : x.head + g0 * G;
       const int v1 = rank == CS - 1 ? V : x.head + g1 * G;
-      for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kNT) put(v, outside(x.at(v)));
+      for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kNT)
+        put_grad<kBF16>(obase, v, F.outside(x.at(v), all, rest, c));
     }
     // the list's tokens in this CTA's part, over what the pass above wrote
     const bool dup = __syncthreads_or(twice);
-    const int v0 = rank == 0 ? 0 : x.head + g0 * G;
-    const int v1 = rank == CS - 1 ? V : x.head + g1 * G;
-    for (int k = threadIdx.x; k < K; k += kNT) {
-      const int32_t id = s_id[k];
-      if (id < v0 || id >= v1) continue;  // empty slots are -1
-      float e = s_e[k];
-      if (dup) {
-        // the token's first slot takes the sum over its slots, in slot order
-        e = 0.0f;
-        bool first = true;
-        for (int j = 0; j < K; ++j) {
-          if (s_id[j] != id) continue;
-          first = first && j >= k;
-          e += s_e[j];
-        }
-        if (!first) continue;
+    put_listed<kBF16>(obase, rank == 0 ? 0 : x.head + g0 * G, rank == CS - 1 ? V : x.head + g1 * G, dup, K, s_id, s_e, s_v,
+                      (ref - all.ref) * c, F.A, scale * invE);
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// The loss and the gradient with the row in shared memory
+// ------------------------------------------------------------------------------------------
+//
+// Memory bounds the pair: the row is read once, copied asynchronously into the shared memory of
+// a cluster's CTAs (a copy needs no register and every thread reads back only what it copied, so
+// no barrier either), summed as its parts arrive, and turned into the gradient from there.  Read
+// again from global memory it came from DRAM once more (an SM's rows in flight, times 152, are
+// more than the second-level cache holds): 495 us for 4096 rows of 151936 bf16 with a quarter
+// masked, three transfers of the matrix, whatever the number of rows in flight.
+constexpr int kGroups = 4;             // parts of a thread's copies that are waited for in turn
+constexpr int kChunkBytes = 40 * 1024; // of a row per CTA, where the cluster allows: five CTAs an SM
+constexpr int kMaxChunkBytes = 200 * 1024;
+
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+template <bool kBF16, bool kRest>
+__global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, int vecs) {
+  constexpr int G = kBF16 ? 8 : 4;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float4 part[kMaxCS * kNW];  // per warp of the cluster: rest.ref, rest.s, list.ref, list.s
+  __shared__ float teacher[4];           // E, W, the teacher's and the student's references
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int CS = static_cast<int>(cg::this_cluster().num_blocks());
+  const int rank = static_cast<int>(cg::this_cluster().block_rank());
+  const int64_t row = blockIdx.x / CS;
+  const int V = P.V, K = P.K;
+  const float c = P.c;
+  // every CTA of the cluster runs before any writes into another's shared memory
+  if (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  const float w = P.weight ? P.weight[row] : 1.0f;
+  const float scale = w * P.tau;
+
+  const RowView<kBF16> x(P.student, row * P.ld, V);
+  const int g0 = static_cast<int>(static_cast<int64_t>(x.nv) * rank / CS);
+  const int g1 = static_cast<int>(static_cast<int64_t>(x.nv) * (rank + 1) / CS);
+  uint4* const mine = reinterpret_cast<uint4*>(smem) + threadIdx.x;  // vector g0 + i kNT + threadIdx.x at mine[i kNT]
+  const Layout lay = make_layout(K, (V + CS - 1) / CS + 4 * G, true, kRest);
+  unsigned char* small = smem + static_cast<size_t>(vecs) * 16;
+  int32_t* s_id = reinterpret_cast<int32_t*>(small + lay.id);
+  float* s_e = reinterpret_cast<float*>(small + lay.e);
+  float* s_v = reinterpret_cast<float*>(small + lay.v);
+  int32_t* s_hash = reinterpret_cast<int32_t*>(small + lay.hash);
+  uint32_t* s_bits = reinterpret_cast<uint32_t*>(small + lay.bits);
+  const int bit0 = x.head + g0 * G - G;  // as in distill_kernel
+  const int nbits = (g1 - g0 + 3) * G;
+  const int per = (g1 - g0 + kNT - 1) / kNT, q = (per + kGroups - 1) / kGroups;  // a thread's vectors, and a group's
+
+  bool any = false;
+  if (w != 0.0f) {
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j) {
+      for (int i = j * q; i < (j + 1) * q && i < per; ++i) {
+        const int g = g0 + i * kNT + static_cast<int>(threadIdx.x);
+        if (g < g1) copy_async16(mine + i * kNT, x.vec + g);
       }
-      put(id, A * ex2(s_v[k] + (ref - all.ref) * c) - scale * (e * invE));
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    if (kRest)
+      for (int i = threadIdx.x; i < (nbits + 31) / 32; i += kNT) s_bits[i] = 0u;
+    for (int i = threadIdx.x; i < lay.hash_size; i += kNT) s_hash[i] = -1;
+    for (int k = threadIdx.x; k < K; k += kNT) {
+      int32_t id = P.ids[row * K + k];
+      const float t = P.values_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(P.values)[row * K + k])
+                                    : static_cast<const float*>(P.values)[row * K + k];
+      float s = 0.0f;
+      if (id < 0 || id >= V || t == -INFINITY) {
+        id = -1;
+      } else {
+        s = x.at(id);
+        any = true;
+      }
+      s_id[k] = id;
+      s_e[k] = t;
+      s_v[k] = s;
     }
   }
+  any = __syncthreads_or(any);
+  if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (!any) {  // no loss: zeros (the same in every CTA of the row)
+    wait_copies<0>();
+    if (rank == 0 && threadIdx.x == 0) P.loss[row] = 0.0f;
+    zero_row<kBF16>(P.grad, row * P.ld_grad, V, rank, CS);
+    return;
+  }
+  const float r = kRest ? P.rest[row] : -INFINITY;
+  bool twice = false;
+  for (int k = threadIdx.x; k < K; k += kNT) {
+    const int32_t id = s_id[k];
+    if (id < 0) continue;
+    twice |= insert_token(s_hash, lay.hash_size, id);
+    const int b = id - bit0;
+    if (kRest && b >= 0 && b < nbits) atomicOr(&s_bits[b >> 5], 1u << (b & 31));
+  }
+  const bool dup = __syncthreads_or(twice);
+  if (warp == 0) {
+    // the teacher's side, by one warp while the others wait for their copies
+    float tmax = -INFINITY, smax = -INFINITY;
+    for (int k = lane; k < K; k += 32) {
+      if (s_id[k] < 0) continue;
+      tmax = fmaxf(tmax, s_e[k]);
+      smax = fmaxf(smax, s_v[k]);
+    }
+    const float tref = clamp_ref(fmaxf(warp_max(tmax), r * P.tau)), ref = clamp_ref(warp_max(smax));
+    float E = 0.0f, W = 0.0f;
+    for (int k = lane; k < K; k += 32) {
+      float e = 0.0f, v = 0.0f;
+      if (s_id[k] >= 0) {
+        const float u = (s_e[k] - tref) * c;
+        v = (s_v[k] - ref) * c;
+        e = ex2(u);
+        E += e;
+        if (e != 0.0f) W += e * (u - v);
+      }
+      s_e[k] = e;
+      s_v[k] = v;
+    }
+    E = warp_sum(E);
+    W = warp_sum(W);
+    if (lane == 0) {
+      teacher[0] = E;
+      teacher[1] = W;
+      teacher[2] = tref;
+      teacher[3] = ref;
+    }
+  }
+
+  // ---- the student's sums, as the copies arrive -------------------------------------------------
+  // A thread's sum has its first vector's largest value as the reference; one that leaves fp32's
+  // range all the same (or has nothing to refer to) is taken again with a moving reference.
+  Sum2 list{-FLT_MAX, 0.0f}, rest;
+  const unsigned char* bytes = reinterpret_cast<const unsigned char*>(s_bits);
+  auto listed_bits = [&](int i) -> uint32_t {
+    const int b = (i * kNT + static_cast<int>(threadIdx.x) + 1) * G;
+    return kBF16 ? bytes[b >> 3] : (bytes[b >> 3] >> (b & 4)) & 15u;
+  };
+  auto vector = [&](int i, Sum2& l) {  // without the list's tokens, which go to l
+    uint4 v = mine[i * kNT];
+    if (kRest) {
+      const uint32_t m = listed_bits(i);
+      if (m) take_listed<kBF16>(v, m, l, c);
+    }
+    return v;
+  };
+  const int count = g0 + static_cast<int>(threadIdx.x) < g1 ? (g1 - g0 - 1 - static_cast<int>(threadIdx.x)) / kNT + 1 : 0;
+  wait_copies<kGroups - 1>();
+  {
+    float first = 0.0f;
+    uint4 v0 = neg_inf_vec<kBF16>();
+    if (count > 0) {
+      v0 = vector(0, list);
+      const float m = vec_max<kBF16>(v0);
+      if (fabsf(m * c) <= kFastRef) first = m;
+    }
+    FastSum<kBF16> fast(first, c);
+    fast.add(v0);
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j) {
+      if (j == 1) wait_copies<2>();
+      if (j == 2) wait_copies<1>();
+      if (j == 3) wait_copies<0>();
+      const int end = (j + 1) * q < count ? (j + 1) * q : count;
+      for (int i = j == 0 ? 1 : j * q; i < end; ++i) fast.add(vector(i, list));
+    }
+    rest = Sum2{first, fast.total(first, c)};
+  }
+  if (!(rest.s >= 0x1p-60f && rest.s <= 0x1p100f)) {
+    rest = Sum2{-FLT_MAX, 0.0f};
+    Sum2 again{-FLT_MAX, 0.0f};
+    for (int i = 0; i < count; ++i) {
+      const uint4 v = vector(i, again);
+      const float m = vec_max<kBF16>(v);
+      if ((m - rest.ref) * c > kRaise) rest.raise(clamp_ref(m), c);
+      add_vec<kBF16>(rest, v, c);
+    }
+    list = again;
+  }
+  // the elements outside the vectors: the head with rank 0, the tail with the last rank
+  const bool has_loose = static_cast<int>(threadIdx.x) < x.loose() &&
+                         ((x.loose_at(threadIdx.x) < x.head) ? rank == 0 : rank == CS - 1);
+  const int loose_v = has_loose ? x.loose_at(threadIdx.x) : 0;
+  const float loose_s = has_loose ? x.at(loose_v) : -INFINITY;
+  if (has_loose) {
+    const int b = loose_v - bit0;
+    const bool in = kRest && ((s_bits[b >> 5] >> (b & 31)) & 1u);
+    add_one(in ? list : rest, loose_s, c);
+  }
+  rest = warp_merge(rest, c);
+  if (kRest) list = warp_merge(list, c);
+  const float4 sums = make_float4(rest.ref, rest.s, list.ref, list.s);
+  if (CS > 1) {
+    cg::cluster_group cl = cg::this_cluster();
+    if (lane < CS) *cl.map_shared_rank(&part[rank * kNW + warp], lane) = sums;
+    cl.sync();  // every CTA holds every part
+  } else {
+    if (lane == 0) part[warp] = sums;
+    __syncthreads();
+  }
+  rest = Sum2{0.0f, 0.0f};
+  list = rest;
+  for (int i = lane; i < kNW * CS; i += 32) {
+    const float4 p = part[i];
+    rest = merge(rest, Sum2{p.x, p.y}, c);
+    if (kRest) list = merge(list, Sum2{p.z, p.w}, c);
+  }
+  rest = warp_merge(rest, c);
+  if (kRest) list = warp_merge(list, c);
+  const Sum2 all = kRest ? merge(list, rest, c) : rest;
+  const float E = teacher[0], W = teacher[1], tref = teacher[2], ref = teacher[3];
+  const float ur = (r * P.tau - tref) * c;
+  const float er = kRest ? ex2(ur) : 0.0f;  // the rest class (0 when there is none)
+  if (rank == 0 && threadIdx.x == 0) {
+    const float kl = divergence<kRest>(E, W, er, ur, ref, list, rest, all, c);
+    const bool ok = all.s > 0.0f && all.s < INFINITY;
+    P.loss[row] = ok ? w * P.tau * P.tau * (kl * kLn2) : NAN;
+  }
+
+  // ---- the gradient ------------------------------------------------------------------------------
+  const float invE = 1.0f / (E + er);
+  const Factors F(scale, er, invE, all, rest, c);
+  const RowView<kBF16> o(P.grad, row * P.ld_grad, V);
+  unsigned char* obase = const_cast<unsigned char*>(o.base);
+  const float rc = all.ref * c;
+  if (F.one && o.head == x.head && fabsf(rc) <= kFastRef) {
+    const float fix = ex2(-fmaf(all.ref, c, -rc));  // what rc's rounding left out
+    const f32x2 nrc2 = pack2(-rc, -rc), c2 = pack2(c, c), C2 = pack2(F.C * fix, F.C * fix);
+    uint4* ov = const_cast<uint4*>(o.vec) + g0 + threadIdx.x;
+#pragma unroll 2
+    for (int i = 0; i < count; ++i) __stcs(ov + i * kNT, grad_vec<kBF16>(mine[i * kNT], c2, nrc2, C2));
+  } else {
+    for (int i = 0; i < count; ++i) {
+      const uint4 v = mine[i * kNT];
+      const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < G; ++e) {
+        const float s = kBF16 ? __uint_as_float((e & 1) ? (word[e / 2] & 0xFFFF0000u) : (word[e / 2] << 16))
+                              : __uint_as_float(word[e]);
+        put_grad<kBF16>(obase, x.head + (g0 + i * kNT + static_cast<int>(threadIdx.x)) * G + e, F.outside(s, all, rest, c));
+      }
+    }
+  }
+  if (has_loose) put_grad<kBF16>(obase, loose_v, F.outside(loose_s, all, rest, c));
+  __syncthreads();
+  put_listed<kBF16>(obase, rank == 0 ? 0 : x.head + g0 * G, rank == CS - 1 ? V : x.head + g1 * G, dup, K, s_id, s_e, s_v,
+                    (ref - all.ref) * c, F.A, scale * invE);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -466,6 +760,19 @@ static int sm_count() {
   return n;
 }
 
+// Lets a kernel take as much dynamic shared memory as a block can have: the same for every call,
+// so that calls side by side do not undo each other's; once for each device.
+constexpr int kMaxDynamic = 224 * 1024;
+template <class Kernel>
+static bool allow_shared(Kernel* kernel, std::atomic<bool>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  if (done[dev].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic) != cudaSuccess) return false;
+  done[dev].store(true, std::memory_order_release);
+  return true;
+}
+
 template <bool kBF16, bool kRest, int kMode>
 static kps_status launch_t(const Params& P, cudaStream_t stream) {
   const int sms = sm_count();
@@ -475,9 +782,8 @@ static kps_status launch_t(const Params& P, cudaStream_t stream) {
   const int64_t round = static_cast<int64_t>(kNT) * kU * (kBF16 ? 8 : 4);
   while (cs < kMaxCS && P.N * cs * 2 <= 2 * sms && P.V >= 2 * cs * round) cs *= 2;
   const Layout lay = make_layout(P.K, (P.V + cs - 1) / cs + 4 * (kBF16 ? 8 : 4), kMode != kForward, kRest);
-  if (lay.total > 48 * 1024 &&
-      cudaFuncSetAttribute(distill_kernel<kBF16, kRest, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(lay.total)) != cudaSuccess) {
+  static std::atomic<bool> done[kMaxDevices];
+  if (!allow_shared(distill_kernel<kBF16, kRest, kMode>, done)) {
     (void)cudaGetLastError();
     return KPS_ERR_CUDA;
   }
@@ -500,8 +806,51 @@ static kps_status launch_t(const Params& P, cudaStream_t stream) {
   return KPS_OK;
 }
 
+// The loss and the gradient: with the row in shared memory where a cluster's holds it.
+template <bool kBF16, bool kRest>
+static kps_status launch_both(const Params& P, cudaStream_t stream) {
+  const int sms = sm_count();
+  if (!sms) return KPS_ERR_CUDA;
+  constexpr int G = kBF16 ? 8 : 4;
+  const int64_t bytes = static_cast<int64_t>(P.V) * (kBF16 ? 2 : 4);
+  int cs = 1;
+  while (cs < kMaxCS && bytes > static_cast<int64_t>(kChunkBytes) * cs) cs *= 2;
+  if (bytes > static_cast<int64_t>(kMaxChunkBytes) * cs) return launch_t<kBF16, kRest, kBoth>(P, stream);
+  // few rows: wider clusters, while every thread keeps a group's worth of vectors
+  while (cs < kMaxCS && P.N * cs * 2 <= 2 * sms && P.V >= 2 * cs * kNT * kGroups * G) cs *= 2;
+  const int vecs = (static_cast<int>((P.V / G + cs - 1) / cs) + 1 + kNT - 1) / kNT * kNT;  // a whole round for every thread
+  const size_t total = static_cast<size_t>(vecs) * 16 + make_layout(P.K, (P.V + cs - 1) / cs + 4 * G, true, kRest).total;
+  auto* kernel = distill_resident_kernel<kBF16, kRest>;
+  static std::atomic<bool> done[kMaxDevices];
+  if (!allow_shared(kernel, done)) {
+    (void)cudaGetLastError();
+    return KPS_ERR_CUDA;
+  }
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(static_cast<unsigned>(P.N * cs));
+  lc.blockDim = dim3(kNT);
+  lc.dynamicSmemBytes = total;
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  if (cudaLaunchKernelEx(&lc, kernel, P, vecs) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return KPS_ERR_CUDA;
+  }
+  return KPS_OK;
+}
+
 template <int kMode>
 static kps_status launch(const Params& P, kps_dtype dt, cudaStream_t stream) {
+  if (kMode == kBoth) {
+    if (dt == KPS_BF16) return P.rest ? launch_both<true, true>(P, stream) : launch_both<true, false>(P, stream);
+    return P.rest ? launch_both<false, true>(P, stream) : launch_both<false, false>(P, stream);
+  }
   if (dt == KPS_BF16) return P.rest ? launch_t<true, true, kMode>(P, stream) : launch_t<true, false, kMode>(P, stream);
   return P.rest ? launch_t<false, true, kMode>(P, stream) : launch_t<false, false, kMode>(P, stream);
 }
