@@ -517,12 +517,22 @@ __device__ __forceinline__ void wait_copies() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
+// Keys of floats that order as they do, for maxima by integer atomics (NaN excluded).
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
 template <bool kBF16, bool kRest>
 __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, int vecs) {
   constexpr int G = kBF16 ? 8 : 4;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float4 part[kMaxCS * kNW];  // per warp of the cluster: rest.ref, rest.s, list.ref, list.s
-  __shared__ float teacher[4];           // E, W, the teacher's and the student's references
+  __shared__ float2 part[kMaxCS * kNW];  // per warp of the cluster: the sums outside the list and in it
+  __shared__ float2 teacher[kNW];        // per warp: E and W
+  __shared__ uint32_t top[2];            // keys of the largest teacher's value and student's logit in the list
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int CS = static_cast<int>(cg::this_cluster().num_blocks());
   const int rank = static_cast<int>(cg::this_cluster().block_rank());
@@ -537,7 +547,10 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, i
   const RowView<kBF16> x(P.student, row * P.ld, V);
   const int g0 = static_cast<int>(static_cast<int64_t>(x.nv) * rank / CS);
   const int g1 = static_cast<int>(static_cast<int64_t>(x.nv) * (rank + 1) / CS);
-  uint4* const mine = reinterpret_cast<uint4*>(smem) + threadIdx.x;  // vector g0 + i kNT + threadIdx.x at mine[i kNT]
+  const int g = g0 + static_cast<int>(threadIdx.x);                  // the thread's vectors: g + i kNT, i < count,
+  uint4* const mine = reinterpret_cast<uint4*>(smem) + threadIdx.x;  // kept at mine[i kNT]
+  const int count = g < g1 ? (g1 - g - 1) / kNT + 1 : 0;
+  const int group = ((g1 - g0 + kNT - 1) / kNT + kGroups - 1) / kGroups;  // vectors waited for together
   const Layout lay = make_layout(K, (V + CS - 1) / CS + 4 * G, true, kRest);
   unsigned char* small = smem + static_cast<size_t>(vecs) * 16;
   int32_t* s_id = reinterpret_cast<int32_t*>(small + lay.id);
@@ -547,18 +560,20 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, i
   uint32_t* s_bits = reinterpret_cast<uint32_t*>(small + lay.bits);
   const int bit0 = x.head + g0 * G - G;  // as in distill_kernel
   const int nbits = (g1 - g0 + 3) * G;
-  const int per = (g1 - g0 + kNT - 1) / kNT, q = (per + kGroups - 1) / kGroups;  // a thread's vectors, and a group's
 
+  // ---- the copies, and the teacher's slots while they are under way -----------------------------
   bool any = false;
   if (w != 0.0f) {
+    const uint4* from = x.vec + g;
+    uint4* to = mine;
 #pragma unroll
-    for (int j = 0; j < kGroups; ++j) {
-      for (int i = j * q; i < (j + 1) * q && i < per; ++i) {
-        const int g = g0 + i * kNT + static_cast<int>(threadIdx.x);
-        if (g < g1) copy_async16(mine + i * kNT, x.vec + g);
-      }
+    for (int j = 0, i = 0; j < kGroups; ++j) {
+      const int end = count < (j + 1) * group ? count : (j + 1) * group;
+#pragma unroll 4
+      for (; i < end; ++i, from += kNT, to += kNT) copy_async16(to, from);
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
+    if (threadIdx.x < 2) top[threadIdx.x] = 0u;
     if (kRest)
       for (int i = threadIdx.x; i < (nbits + 31) / 32; i += kNT) s_bits[i] = 0u;
     for (int i = threadIdx.x; i < lay.hash_size; i += kNT) s_hash[i] = -1;
@@ -579,34 +594,41 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, i
     }
   }
   any = __syncthreads_or(any);
-  if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (!any) {  // no loss: zeros (the same in every CTA of the row)
     wait_copies<0>();
+    if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (rank == 0 && threadIdx.x == 0) P.loss[row] = 0.0f;
     zero_row<kBF16>(P.grad, row * P.ld_grad, V, rank, CS);
     return;
   }
-  const float r = kRest ? P.rest[row] : -INFINITY;
   bool twice = false;
-  for (int k = threadIdx.x; k < K; k += kNT) {
-    const int32_t id = s_id[k];
-    if (id < 0) continue;
-    twice |= insert_token(s_hash, lay.hash_size, id);
-    const int b = id - bit0;
-    if (kRest && b >= 0 && b < nbits) atomicOr(&s_bits[b >> 5], 1u << (b & 31));
+  if (warp * 32 < K) {  // (a warp's slots: all of them are its own threads')
+    uint32_t t = 0, sm = 0;
+    for (int k = threadIdx.x; k < K; k += kNT) {
+      const int32_t id = s_id[k];
+      if (id < 0) continue;
+      const float tk = s_e[k], sk = s_v[k];
+      if (!isnan(tk)) t = max(t, order_key(tk));
+      if (!isnan(sk)) sm = max(sm, order_key(sk));
+      twice |= insert_token(s_hash, lay.hash_size, id);
+      const int b = id - bit0;
+      if (kRest && b >= 0 && b < nbits) atomicOr(&s_bits[b >> 5], 1u << (b & 31));
+    }
+    __syncwarp();
+    t = __reduce_max_sync(0xffffffffu, t);
+    sm = __reduce_max_sync(0xffffffffu, sm);
+    if (lane == 0) {
+      atomicMax(&top[0], t);
+      atomicMax(&top[1], sm);
+    }
   }
   const bool dup = __syncthreads_or(twice);
-  if (warp == 0) {
-    // the teacher's side, by one warp while the others wait for their copies
-    float tmax = -INFINITY, smax = -INFINITY;
-    for (int k = lane; k < K; k += 32) {
-      if (s_id[k] < 0) continue;
-      tmax = fmaxf(tmax, s_e[k]);
-      smax = fmaxf(smax, s_v[k]);
-    }
-    const float tref = clamp_ref(fmaxf(warp_max(tmax), r * P.tau)), ref = clamp_ref(warp_max(smax));
+  const float r = kRest ? P.rest[row] : -INFINITY;
+  const float tref = clamp_ref(fmaxf(top[0] ? order_value(top[0]) : -INFINITY, r * P.tau));
+  const float ref = clamp_ref(top[1] ? order_value(top[1]) : -INFINITY);  // of the student's sums too
+  if (warp * 32 < K) {
     float E = 0.0f, W = 0.0f;
-    for (int k = lane; k < K; k += 32) {
+    for (int k = threadIdx.x; k < K; k += kNT) {
       float e = 0.0f, v = 0.0f;
       if (s_id[k] >= 0) {
         const float u = (s_e[k] - tref) * c;
@@ -620,96 +642,133 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, i
     }
     E = warp_sum(E);
     W = warp_sum(W);
-    if (lane == 0) {
-      teacher[0] = E;
-      teacher[1] = W;
-      teacher[2] = tref;
-      teacher[3] = ref;
-    }
+    if (lane == 0) teacher[warp] = make_float2(E, W);
+  } else if (lane == 0) {
+    teacher[warp] = make_float2(0.0f, 0.0f);
   }
 
   // ---- the student's sums, as the copies arrive -------------------------------------------------
-  // A thread's sum has its first vector's largest value as the reference; one that leaves fp32's
-  // range all the same (or has nothing to refer to) is taken again with a moving reference.
-  Sum2 list{-FLT_MAX, 0.0f}, rest;
-  const unsigned char* bytes = reinterpret_cast<const unsigned char*>(s_bits);
-  auto listed_bits = [&](int i) -> uint32_t {
-    const int b = (i * kNT + static_cast<int>(threadIdx.x) + 1) * G;
-    return kBF16 ? bytes[b >> 3] : (bytes[b >> 3] >> (b & 4)) & 15u;
-  };
-  auto vector = [&](int i, Sum2& l) {  // without the list's tokens, which go to l
-    uint4 v = mine[i * kNT];
-    if (kRest) {
-      const uint32_t m = listed_bits(i);
-      if (m) take_listed<kBF16>(v, m, l, c);
-    }
-    return v;
-  };
-  const int count = g0 + static_cast<int>(threadIdx.x) < g1 ? (g1 - g0 - 1 - static_cast<int>(threadIdx.x)) / kNT + 1 : 0;
-  wait_copies<kGroups - 1>();
+  // Against the list's largest student logit, one reference for the whole row, so that the parts
+  // simply add up.  Sums that leave fp32's range (the list far from everything else) are taken
+  // again below, with moving references.
+  float s_list = 0.0f, s_rest;
+  const unsigned char* bytes = reinterpret_cast<const unsigned char*>(s_bits) + (kBF16 ? threadIdx.x + 1 : (threadIdx.x + 1) / 2);
+  const int nibble = kBF16 ? 0 : ((threadIdx.x + 1) & 1) * 4;  // a vector's bits: a byte, or half of one
+  auto listed_bits = [&](int i) -> uint32_t { return kBF16 ? bytes[i * kNT] : (bytes[i * (kNT / 2)] >> nibble) & 15u; };
   {
-    float first = 0.0f;
-    uint4 v0 = neg_inf_vec<kBF16>();
-    if (count > 0) {
-      v0 = vector(0, list);
-      const float m = vec_max<kBF16>(v0);
-      if (fabsf(m * c) <= kFastRef) first = m;
-    }
-    FastSum<kBF16> fast(first, c);
-    fast.add(v0);
+    FastSum<kBF16> fast(fabsf(ref * c) <= kFastRef ? ref : 0.0f, c);
 #pragma unroll
-    for (int j = 0; j < kGroups; ++j) {
+    for (int j = 0, i = 0; j < kGroups; ++j) {
+      if (j == 0) wait_copies<3>();
       if (j == 1) wait_copies<2>();
       if (j == 2) wait_copies<1>();
       if (j == 3) wait_copies<0>();
-      const int end = (j + 1) * q < count ? (j + 1) * q : count;
-      for (int i = j == 0 ? 1 : j * q; i < end; ++i) fast.add(vector(i, list));
+      const int end = count < (j + 1) * group ? count : (j + 1) * group;
+#pragma unroll 2
+      for (; i < end; ++i) {
+        uint4 v = mine[i * kNT];
+        if (kRest) {
+          const uint32_t m = listed_bits(i);
+          if (m) {
+            Sum2 l{ref, 0.0f};
+            take_listed<kBF16>(v, m, l, c);
+            s_list += l.s;
+          }
+        }
+        fast.add(v);
+      }
     }
-    rest = Sum2{first, fast.total(first, c)};
-  }
-  if (!(rest.s >= 0x1p-60f && rest.s <= 0x1p100f)) {
-    rest = Sum2{-FLT_MAX, 0.0f};
-    Sum2 again{-FLT_MAX, 0.0f};
-    for (int i = 0; i < count; ++i) {
-      const uint4 v = vector(i, again);
-      const float m = vec_max<kBF16>(v);
-      if ((m - rest.ref) * c > kRaise) rest.raise(clamp_ref(m), c);
-      add_vec<kBF16>(rest, v, c);
-    }
-    list = again;
+    s_rest = fast.total(ref, c);
   }
   // the elements outside the vectors: the head with rank 0, the tail with the last rank
   const bool has_loose = static_cast<int>(threadIdx.x) < x.loose() &&
                          ((x.loose_at(threadIdx.x) < x.head) ? rank == 0 : rank == CS - 1);
   const int loose_v = has_loose ? x.loose_at(threadIdx.x) : 0;
   const float loose_s = has_loose ? x.at(loose_v) : -INFINITY;
-  if (has_loose) {
-    const int b = loose_v - bit0;
-    const bool in = kRest && ((s_bits[b >> 5] >> (b & 31)) & 1u);
-    add_one(in ? list : rest, loose_s, c);
+  const bool loose_in = kRest && has_loose && ((s_bits[(loose_v - bit0) >> 5] >> ((loose_v - bit0) & 31)) & 1u);
+  if (has_loose) (loose_in ? s_list : s_rest) += ex2((loose_s - ref) * c);
+  if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // (of the arrival at the top)
+  cg::cluster_group cl = cg::this_cluster();
+  // Adds two values of every thread over the cluster's CTAs; every thread gets the sums.
+  auto cluster_sum = [&](float a, float b) -> float2 {
+    a = warp_sum(a);
+    b = kRest ? warp_sum(b) : 0.0f;
+    if (CS > 1) {
+      if (lane < CS) *cl.map_shared_rank(&part[rank * kNW + warp], lane) = make_float2(a, b);
+      cl.sync();
+    } else {
+      if (lane == 0) part[warp] = make_float2(a, b);
+      __syncthreads();
+    }
+    float2 t = make_float2(0.0f, 0.0f);
+    for (int i = lane; i < kNW * CS; i += 32) {
+      t.x += part[i].x;
+      t.y += part[i].y;
+    }
+    return make_float2(warp_sum(t.x), kRest ? warp_sum(t.y) : 0.0f);
+  };
+  Sum2 list, rest, all;
+  {
+    const float2 t = cluster_sum(s_rest, s_list);
+    rest = Sum2{ref, t.x};
+    list = Sum2{ref, t.y};
+    all = Sum2{ref, t.x + t.y};
   }
-  rest = warp_merge(rest, c);
-  if (kRest) list = warp_merge(list, c);
-  const float4 sums = make_float4(rest.ref, rest.s, list.ref, list.s);
-  if (CS > 1) {
-    cg::cluster_group cl = cg::this_cluster();
-    if (lane < CS) *cl.map_shared_rank(&part[rank * kNW + warp], lane) = sums;
-    cl.sync();  // every CTA holds every part
-  } else {
-    if (lane == 0) part[warp] = sums;
-    __syncthreads();
+  // (!: NaN goes there too; without tokens outside the list their sum is nothing, as it should be)
+  const bool fine = fabsf(ref * c) <= kFastRef && rest.s >= 0x1p-60f && all.s <= 0x1p100f;
+  if (!fine) {
+    // the same in every CTA: the largest logit outside the list first, then its sum against that
+    // (a maximum is a sum here too: of the one warp that holds it)
+    float m = has_loose && !loose_in ? loose_s : -INFINITY;
+    bool nan = has_loose && isnan(loose_s);
+    auto outside = [&](auto&& f) {  // f(logit) for the thread's tokens outside the list
+      for (int i = 0; i < count; ++i) {
+        const uint4 v = mine[i * kNT];
+        const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t bits = kRest ? listed_bits(i) : 0u;
+#pragma unroll
+        for (int e = 0; e < G; ++e) {
+          const float s = kBF16 ? __uint_as_float((e & 1) ? (word[e / 2] & 0xFFFF0000u) : (word[e / 2] << 16))
+                                : __uint_as_float(word[e]);
+          if (!((bits >> e) & 1u)) f(s);
+          else nan |= isnan(s);
+        }
+      }
+    };
+    outside([&](float s) {
+      m = fmaxf(m, s);
+      nan |= isnan(s);
+    });
+    const float2 mine2 = make_float2(warp_max(m), __any_sync(0xffffffffu, nan) ? 1.0f : 0.0f);
+    if (CS > 1) {
+      cl.sync();  // the parts are read
+      if (lane < CS) *cl.map_shared_rank(&part[rank * kNW + warp], lane) = mine2;
+      cl.sync();
+    } else {
+      __syncthreads();
+      if (lane == 0) part[warp] = mine2;
+      __syncthreads();
+    }
+    m = -INFINITY;
+    nan = false;
+    for (int i = 0; i < kNW * CS; ++i) {
+      m = fmaxf(m, part[i].x);
+      nan |= part[i].y != 0.0f;
+    }
+    m = clamp_ref(m);
+    float s = has_loose && !loose_in ? ex2((loose_s - m) * c) : 0.0f;
+    outside([&](float y) { s += ex2((y - m) * c); });
+    if (CS > 1) cl.sync(); else __syncthreads();
+    rest = Sum2{m, cluster_sum(s, 0.0f).x};
+    all = kRest ? merge(list, rest, c) : rest;
+    if (nan) all.s = NAN;
   }
-  rest = Sum2{0.0f, 0.0f};
-  list = rest;
-  for (int i = lane; i < kNW * CS; i += 32) {
-    const float4 p = part[i];
-    rest = merge(rest, Sum2{p.x, p.y}, c);
-    if (kRest) list = merge(list, Sum2{p.z, p.w}, c);
+  float E = 0.0f, W = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kNW; ++i) {
+    E += teacher[i].x;
+    W += teacher[i].y;
   }
-  rest = warp_merge(rest, c);
-  if (kRest) list = warp_merge(list, c);
-  const Sum2 all = kRest ? merge(list, rest, c) : rest;
-  const float E = teacher[0], W = teacher[1], tref = teacher[2], ref = teacher[3];
   const float ur = (r * P.tau - tref) * c;
   const float er = kRest ? ex2(ur) : 0.0f;  // the rest class (0 when there is none)
   if (rank == 0 && threadIdx.x == 0) {
@@ -727,7 +786,7 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, i
   if (F.one && o.head == x.head && fabsf(rc) <= kFastRef) {
     const float fix = ex2(-fmaf(all.ref, c, -rc));  // what rc's rounding left out
     const f32x2 nrc2 = pack2(-rc, -rc), c2 = pack2(c, c), C2 = pack2(F.C * fix, F.C * fix);
-    uint4* ov = const_cast<uint4*>(o.vec) + g0 + threadIdx.x;
+    uint4* ov = const_cast<uint4*>(o.vec) + g;
 #pragma unroll 2
     for (int i = 0; i < count; ++i) __stcs(ov + i * kNT, grad_vec<kBF16>(mine[i * kNT], c2, nrc2, C2));
   } else {
@@ -738,7 +797,7 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, i
       for (int e = 0; e < G; ++e) {
         const float s = kBF16 ? __uint_as_float((e & 1) ? (word[e / 2] & 0xFFFF0000u) : (word[e / 2] << 16))
                               : __uint_as_float(word[e]);
-        put_grad<kBF16>(obase, x.head + (g0 + i * kNT + static_cast<int>(threadIdx.x)) * G + e, F.outside(s, all, rest, c));
+        put_grad<kBF16>(obase, x.head + (g + i * kNT) * G + e, F.outside(s, all, rest, c));
       }
     }
   }
@@ -813,11 +872,11 @@ static kps_status launch_both(const Params& P, cudaStream_t stream) {
   if (!sms) return KPS_ERR_CUDA;
   constexpr int G = kBF16 ? 8 : 4;
   const int64_t bytes = static_cast<int64_t>(P.V) * (kBF16 ? 2 : 4);
-  int cs = 1;
-  while (cs < kMaxCS && bytes > static_cast<int64_t>(kChunkBytes) * cs) cs *= 2;
+  int cs = static_cast<int>((bytes + kChunkBytes - 1) / kChunkBytes);
+  cs = cs < 1 ? 1 : cs > kMaxCS ? kMaxCS : cs;
   if (bytes > static_cast<int64_t>(kMaxChunkBytes) * cs) return launch_t<kBF16, kRest, kBoth>(P, stream);
   // few rows: wider clusters, while every thread keeps a group's worth of vectors
-  while (cs < kMaxCS && P.N * cs * 2 <= 2 * sms && P.V >= 2 * cs * kNT * kGroups * G) cs *= 2;
+  while (2 * cs <= kMaxCS && P.N * cs * 2 <= 2 * sms && P.V >= 2 * cs * kNT * kGroups * G) cs *= 2;
   const int vecs = (static_cast<int>((P.V / G + cs - 1) / cs) + 1 + kNT - 1) / kNT * kNT;  // a whole round for every thread
   const size_t total = static_cast<size_t>(vecs) * 16 + make_layout(P.K, (P.V + cs - 1) / cs + 4 * G, true, kRest).total;
   auto* kernel = distill_resident_kernel<kBF16, kRest>;
