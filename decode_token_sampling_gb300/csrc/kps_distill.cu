@@ -198,6 +198,14 @@ __device__ __forceinline__ bool insert_token(int32_t* hash, int size, int32_t id
   }
 }
 
+// Whether the table holds a token.
+__device__ __forceinline__ bool has_token(const int32_t* hash, int size, int32_t id) {
+  uint32_t h = (static_cast<uint32_t>(id) * 2654435761u) & (size - 1);
+  for (; hash[h] != -1; h = (h + 1) & (size - 1))
+    if (hash[h] == id) return true;
+  return false;
+}
+
 // The gradient's factors: d_v = A 2^((s_v - all.ref) c) - p_v for a token of the list, less
 // B 2^((s_v - rest.ref) c) for any other; C covers both terms of the latter with one exponential
 // unless the two references lie too far apart for fp32 (one false).
@@ -526,17 +534,27 @@ __device__ __forceinline__ float order_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
+// What the host lays out for a launch: `share` vectors of a row for each CTA, and the offsets of
+// the small arrays behind them in shared memory.
+struct Resident {
+  int share, hash_size;
+  int id, e, v, next, head, hash;
+};
+
 template <bool kBF16, bool kRest>
-__global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, int vecs) {
+__global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, const Resident R) {
   constexpr int G = kBF16 ? 8 : 4;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float2 part[kMaxCS * kNW];  // per warp of the cluster: the sums outside the list and in it
-  __shared__ float2 teacher[kNW];        // per warp: E and W
-  __shared__ uint32_t top[2];            // keys of the largest teacher's value and student's logit in the list
+  __shared__ float part[kMaxCS * kNW];  // per warp of the cluster
+  __shared__ float4 teacher[kNW];       // per warp: E, W and the student's sum over the list
+  __shared__ uint32_t top[2];           // keys of the largest teacher's value and student's logit in the list
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int CS = static_cast<int>(cg::this_cluster().num_blocks());
-  const int rank = static_cast<int>(cg::this_cluster().block_rank());
-  const int64_t row = blockIdx.x / CS;
+  cg::cluster_group cl = cg::this_cluster();
+  const int CS = static_cast<int>(cl.num_blocks());
+  const int rank = static_cast<int>(cl.block_rank());
+  uint32_t cluster;
+  asm("mov.u32 %0, %%clusterid.x;" : "=r"(cluster));
+  const int64_t row = cluster;
   const int V = P.V, K = P.K;
   const float c = P.c;
   // every CTA of the cluster runs before any writes into another's shared memory
@@ -545,21 +563,17 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, i
   const float scale = w * P.tau;
 
   const RowView<kBF16> x(P.student, row * P.ld, V);
-  const int g0 = static_cast<int>(static_cast<int64_t>(x.nv) * rank / CS);
-  const int g1 = static_cast<int>(static_cast<int64_t>(x.nv) * (rank + 1) / CS);
+  const int g0 = min(rank * R.share, x.nv), g1 = rank == CS - 1 ? x.nv : min(g0 + R.share, x.nv);
   const int g = g0 + static_cast<int>(threadIdx.x);                  // the thread's vectors: g + i kNT, i < count,
   uint4* const mine = reinterpret_cast<uint4*>(smem) + threadIdx.x;  // kept at mine[i kNT]
   const int count = g < g1 ? (g1 - g - 1) / kNT + 1 : 0;
   const int group = ((g1 - g0 + kNT - 1) / kNT + kGroups - 1) / kGroups;  // vectors waited for together
-  const Layout lay = make_layout(K, (V + CS - 1) / CS + 4 * G, true, kRest);
-  unsigned char* small = smem + static_cast<size_t>(vecs) * 16;
-  int32_t* s_id = reinterpret_cast<int32_t*>(small + lay.id);
-  float* s_e = reinterpret_cast<float*>(small + lay.e);
-  float* s_v = reinterpret_cast<float*>(small + lay.v);
-  int32_t* s_hash = reinterpret_cast<int32_t*>(small + lay.hash);
-  uint32_t* s_bits = reinterpret_cast<uint32_t*>(small + lay.bits);
-  const int bit0 = x.head + g0 * G - G;  // as in distill_kernel
-  const int nbits = (g1 - g0 + 3) * G;
+  int32_t* s_id = reinterpret_cast<int32_t*>(smem + R.id);
+  float* s_e = reinterpret_cast<float*>(smem + R.e);
+  float* s_v = reinterpret_cast<float*>(smem + R.v);
+  int32_t* s_next = reinterpret_cast<int32_t*>(smem + R.next);
+  int32_t* s_head = reinterpret_cast<int32_t*>(smem + R.head);  // per thread: the first of the slots whose tokens
+  int32_t* s_hash = reinterpret_cast<int32_t*>(smem + R.hash);  // lie in its vectors, the others by s_next (kRest)
 
   // ---- the copies, and the teacher's slots while they are under way -----------------------------
   bool any = false;
@@ -574,9 +588,8 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, i
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
     if (threadIdx.x < 2) top[threadIdx.x] = 0u;
-    if (kRest)
-      for (int i = threadIdx.x; i < (nbits + 31) / 32; i += kNT) s_bits[i] = 0u;
-    for (int i = threadIdx.x; i < lay.hash_size; i += kNT) s_hash[i] = -1;
+    if (kRest) s_head[threadIdx.x] = -1;
+    for (int i = threadIdx.x; i < R.hash_size; i += kNT) s_hash[i] = -1;
     for (int k = threadIdx.x; k < K; k += kNT) {
       int32_t id = P.ids[row * K + k];
       const float t = P.values_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(P.values)[row * K + k])
@@ -602,7 +615,7 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, i
     return;
   }
   bool twice = false;
-  if (warp * 32 < K) {  // (a warp's slots: all of them are its own threads')
+  if (warp * 32 < K) {  // (a warp's slots are its own threads')
     uint32_t t = 0, sm = 0;
     for (int k = threadIdx.x; k < K; k += kNT) {
       const int32_t id = s_id[k];
@@ -610,9 +623,11 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, i
       const float tk = s_e[k], sk = s_v[k];
       if (!isnan(tk)) t = max(t, order_key(tk));
       if (!isnan(sk)) sm = max(sm, order_key(sk));
-      twice |= insert_token(s_hash, lay.hash_size, id);
-      const int b = id - bit0;
-      if (kRest && b >= 0 && b < nbits) atomicOr(&s_bits[b >> 5], 1u << (b & 31));
+      twice |= insert_token(s_hash, R.hash_size, id);
+      if (kRest) {
+        const int at = id - x.head, vec = at / G - g0;
+        if (at >= 0 && vec >= 0 && vec < g1 - g0) s_next[k] = atomicExch(&s_head[vec & (kNT - 1)], k);
+      }
     }
     __syncwarp();
     t = __reduce_max_sync(0xffffffffu, t);
@@ -626,36 +641,41 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, i
   const float r = kRest ? P.rest[row] : -INFINITY;
   const float tref = clamp_ref(fmaxf(top[0] ? order_value(top[0]) : -INFINITY, r * P.tau));
   const float ref = clamp_ref(top[1] ? order_value(top[1]) : -INFINITY);  // of the student's sums too
-  if (warp * 32 < K) {
-    float E = 0.0f, W = 0.0f;
-    for (int k = threadIdx.x; k < K; k += kNT) {
-      float e = 0.0f, v = 0.0f;
-      if (s_id[k] >= 0) {
-        const float u = (s_e[k] - tref) * c;
-        v = (s_v[k] - ref) * c;
-        e = ex2(u);
-        E += e;
-        if (e != 0.0f) W += e * (u - v);
+  {
+    float E = 0.0f, W = 0.0f, S = 0.0f;
+    if (warp * 32 < K) {
+      for (int k = threadIdx.x; k < K; k += kNT) {
+        const int32_t id = s_id[k];
+        float e = 0.0f, v = 0.0f;
+        if (id >= 0) {
+          const float u = (s_e[k] - tref) * c;
+          v = (s_v[k] - ref) * c;
+          e = ex2(u);
+          E += e;
+          if (e != 0.0f) W += e * (u - v);
+          bool first = true;  // a token of several slots counts once
+          if (dup)
+            for (int j = 0; j < k; ++j) first = first && s_id[j] != id;
+          if (first) S += ex2(v);
+        }
+        s_e[k] = e;
+        s_v[k] = v;
       }
-      s_e[k] = e;
-      s_v[k] = v;
+      E = warp_sum(E);
+      W = warp_sum(W);
+      S = warp_sum(S);
     }
-    E = warp_sum(E);
-    W = warp_sum(W);
-    if (lane == 0) teacher[warp] = make_float2(E, W);
-  } else if (lane == 0) {
-    teacher[warp] = make_float2(0.0f, 0.0f);
+    if (lane == 0) teacher[warp] = make_float4(E, W, S, 0.0f);
   }
 
-  // ---- the student's sums, as the copies arrive -------------------------------------------------
-  // Against the list's largest student logit, one reference for the whole row, so that the parts
-  // simply add up.  Sums that leave fp32's range (the list far from everything else) are taken
-  // again below, with moving references.
-  float s_list = 0.0f, s_rest;
-  const unsigned char* bytes = reinterpret_cast<const unsigned char*>(s_bits) + (kBF16 ? threadIdx.x + 1 : (threadIdx.x + 1) / 2);
-  const int nibble = kBF16 ? 0 : ((threadIdx.x + 1) & 1) * 4;  // a vector's bits: a byte, or half of one
-  auto listed_bits = [&](int i) -> uint32_t { return kBF16 ? bytes[i * kNT] : (bytes[i * (kNT / 2)] >> nibble) & 15u; };
+  // ---- the student's sum outside the list, as the copies arrive ------------------------------------
+  // With kRest the list's tokens leave the row: each thread overwrites those in its own vectors with
+  // -inf (their logits are in s_v).  Against the list's largest student logit, one reference for
+  // the whole row, so that the parts simply add up; a sum that leaves fp32's range (the list far
+  // from everything else) is taken again below against its own maximum.
+  float s_rest;
   {
+    const int32_t head = kRest ? s_head[threadIdx.x] : -1;
     FastSum<kBF16> fast(fabsf(ref * c) <= kFastRef ? ref : 0.0f, c);
 #pragma unroll
     for (int j = 0, i = 0; j < kGroups; ++j) {
@@ -664,19 +684,16 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, i
       if (j == 2) wait_copies<1>();
       if (j == 3) wait_copies<0>();
       const int end = count < (j + 1) * group ? count : (j + 1) * group;
-#pragma unroll 2
-      for (; i < end; ++i) {
-        uint4 v = mine[i * kNT];
-        if (kRest) {
-          const uint32_t m = listed_bits(i);
-          if (m) {
-            Sum2 l{ref, 0.0f};
-            take_listed<kBF16>(v, m, l, c);
-            s_list += l.s;
-          }
+      if (kRest) {
+        for (int k = head; k >= 0; k = s_next[k]) {
+          const int at = s_id[k] - x.head, step = (at / G - g0) / kNT;
+          if (step < i || step >= end) continue;
+          if (kBF16) reinterpret_cast<uint16_t*>(mine + step * kNT)[at % G] = 0xFF80u;
+          else reinterpret_cast<uint32_t*>(mine + step * kNT)[at % G] = 0xFF800000u;
         }
-        fast.add(v);
       }
+#pragma unroll 2
+      for (; i < end; ++i) fast.add(mine[i * kNT]);
     }
     s_rest = fast.total(ref, c);
   }
@@ -685,89 +702,73 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, i
                          ((x.loose_at(threadIdx.x) < x.head) ? rank == 0 : rank == CS - 1);
   const int loose_v = has_loose ? x.loose_at(threadIdx.x) : 0;
   const float loose_s = has_loose ? x.at(loose_v) : -INFINITY;
-  const bool loose_in = kRest && has_loose && ((s_bits[(loose_v - bit0) >> 5] >> ((loose_v - bit0) & 31)) & 1u);
-  if (has_loose) (loose_in ? s_list : s_rest) += ex2((loose_s - ref) * c);
+  const bool loose_out = has_loose && !(kRest && has_token(s_hash, R.hash_size, loose_v));
+  if (loose_out) s_rest += ex2((loose_s - ref) * c);
   if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // (of the arrival at the top)
-  cg::cluster_group cl = cg::this_cluster();
-  // Adds two values of every thread over the cluster's CTAs; every thread gets the sums.
-  auto cluster_sum = [&](float a, float b) -> float2 {
-    a = warp_sum(a);
-    b = kRest ? warp_sum(b) : 0.0f;
+  // Gives every warp of the cluster's CTAs' values a to all of them, at part[].
+  auto exchange = [&](float a) {
     if (CS > 1) {
-      if (lane < CS) *cl.map_shared_rank(&part[rank * kNW + warp], lane) = make_float2(a, b);
+      if (lane < CS) *cl.map_shared_rank(&part[rank * kNW + warp], lane) = a;
       cl.sync();
     } else {
-      if (lane == 0) part[warp] = make_float2(a, b);
+      if (lane == 0) part[warp] = a;
       __syncthreads();
     }
-    float2 t = make_float2(0.0f, 0.0f);
-    for (int i = lane; i < kNW * CS; i += 32) {
-      t.x += part[i].x;
-      t.y += part[i].y;
-    }
-    return make_float2(warp_sum(t.x), kRest ? warp_sum(t.y) : 0.0f);
   };
-  Sum2 list, rest, all;
-  {
-    const float2 t = cluster_sum(s_rest, s_list);
-    rest = Sum2{ref, t.x};
-    list = Sum2{ref, t.y};
-    all = Sum2{ref, t.x + t.y};
+  auto part_sum = [&]() -> float {
+    float t = lane < kNW * CS ? part[lane] : 0.0f;
+    if (lane + 32 < kNW * CS) t += part[lane + 32];
+    return warp_sum(t);
+  };
+  exchange(warp_sum(s_rest));
+  float E = 0.0f, W = 0.0f, S = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kNW; ++i) {
+    const float4 t = teacher[i];
+    E += t.x;
+    W += t.y;
+    S += t.z;
   }
-  // (!: NaN goes there too; without tokens outside the list their sum is nothing, as it should be)
-  const bool fine = fabsf(ref * c) <= kFastRef && rest.s >= 0x1p-60f && all.s <= 0x1p100f;
-  if (!fine) {
-    // the same in every CTA: the largest logit outside the list first, then its sum against that
-    // (a maximum is a sum here too: of the one warp that holds it)
-    float m = has_loose && !loose_in ? loose_s : -INFINITY;
-    bool nan = has_loose && isnan(loose_s);
-    auto outside = [&](auto&& f) {  // f(logit) for the thread's tokens outside the list
+  const Sum2 list{ref, kRest ? S : 0.0f};
+  Sum2 rest{ref, part_sum()};
+  Sum2 all{ref, rest.s + list.s};
+  // (NaN fails this too)
+  if (!(fabsf(ref * c) <= kFastRef && rest.s >= 0x1p-60f && all.s <= 0x1p100f)) {
+    // the same in every CTA: the largest logit outside the list (NaN: there is one), then the sum
+    // against that
+    float m = loose_out ? loose_s : -INFINITY;
+    bool nan = isnan(m);
+    auto each = [&](auto&& f) {
       for (int i = 0; i < count; ++i) {
         const uint4 v = mine[i * kNT];
         const uint32_t word[4] = {v.x, v.y, v.z, v.w};
-        const uint32_t bits = kRest ? listed_bits(i) : 0u;
 #pragma unroll
-        for (int e = 0; e < G; ++e) {
-          const float s = kBF16 ? __uint_as_float((e & 1) ? (word[e / 2] & 0xFFFF0000u) : (word[e / 2] << 16))
-                                : __uint_as_float(word[e]);
-          if (!((bits >> e) & 1u)) f(s);
-          else nan |= isnan(s);
-        }
+        for (int e = 0; e < G; ++e)
+          f(kBF16 ? __uint_as_float((e & 1) ? (word[e / 2] & 0xFFFF0000u) : (word[e / 2] << 16)) : __uint_as_float(word[e]));
       }
     };
-    outside([&](float s) {
-      m = fmaxf(m, s);
-      nan |= isnan(s);
+    each([&](float y) {
+      m = fmaxf(m, y);
+      nan |= isnan(y);
     });
-    const float2 mine2 = make_float2(warp_max(m), __any_sync(0xffffffffu, nan) ? 1.0f : 0.0f);
-    if (CS > 1) {
-      cl.sync();  // the parts are read
-      if (lane < CS) *cl.map_shared_rank(&part[rank * kNW + warp], lane) = mine2;
-      cl.sync();
-    } else {
-      __syncthreads();
-      if (lane == 0) part[warp] = mine2;
-      __syncthreads();
-    }
+    nan = __any_sync(0xffffffffu, nan);
+    m = nan ? NAN : warp_max(m);
+    if (CS > 1) cl.sync(); else __syncthreads();  // the parts are read
+    exchange(m);
     m = -INFINITY;
     nan = false;
     for (int i = 0; i < kNW * CS; ++i) {
-      m = fmaxf(m, part[i].x);
-      nan |= part[i].y != 0.0f;
+      m = fmaxf(m, part[i]);
+      nan |= isnan(part[i]);
     }
     m = clamp_ref(m);
-    float s = has_loose && !loose_in ? ex2((loose_s - m) * c) : 0.0f;
-    outside([&](float y) { s += ex2((y - m) * c); });
+    float t = loose_out ? ex2((loose_s - m) * c) : 0.0f;
+    each([&](float y) { t += ex2((y - m) * c); });
     if (CS > 1) cl.sync(); else __syncthreads();
-    rest = Sum2{m, cluster_sum(s, 0.0f).x};
+    exchange(warp_sum(t));
+    rest = Sum2{m, part_sum()};
     all = kRest ? merge(list, rest, c) : rest;
     if (nan) all.s = NAN;
-  }
-  float E = 0.0f, W = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kNW; ++i) {
-    E += teacher[i].x;
-    W += teacher[i].y;
   }
   const float ur = (r * P.tau - tref) * c;
   const float er = kRest ? ex2(ur) : 0.0f;  // the rest class (0 when there is none)
@@ -877,8 +878,18 @@ static kps_status launch_both(const Params& P, cudaStream_t stream) {
   if (bytes > static_cast<int64_t>(kMaxChunkBytes) * cs) return launch_t<kBF16, kRest, kBoth>(P, stream);
   // few rows: wider clusters, while every thread keeps a group's worth of vectors
   while (2 * cs <= kMaxCS && P.N * cs * 2 <= 2 * sms && P.V >= 2 * cs * kNT * kGroups * G) cs *= 2;
-  const int vecs = (static_cast<int>((P.V / G + cs - 1) / cs) + 1 + kNT - 1) / kNT * kNT;  // a whole round for every thread
-  const size_t total = static_cast<size_t>(vecs) * 16 + make_layout(P.K, (P.V + cs - 1) / cs + 4 * G, true, kRest).total;
+  Resident R;
+  R.share = (P.V / G + cs - 1) / cs;
+  R.hash_size = 32;
+  while (R.hash_size < 2 * P.K) R.hash_size *= 2;
+  const int k4 = (P.K * 4 + 15) / 16 * 16;
+  R.id = (R.share + kNT - 1) / kNT * kNT * 16;  // a whole round of vectors for every thread
+  R.e = R.id + k4;
+  R.v = R.e + k4;
+  R.next = R.v + k4;
+  R.head = R.next + (kRest ? k4 : 0);
+  R.hash = R.head + (kRest ? kNT * 4 : 0);
+  const size_t total = static_cast<size_t>(R.hash) + R.hash_size * 4;
   auto* kernel = distill_resident_kernel<kBF16, kRest>;
   static std::atomic<bool> done[kMaxDevices];
   if (!allow_shared(kernel, done)) {
@@ -897,7 +908,7 @@ static kps_status launch_both(const Params& P, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  if (cudaLaunchKernelEx(&lc, kernel, P, vecs) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&lc, kernel, P, R) != cudaSuccess) {
     (void)cudaGetLastError();
     return KPS_ERR_CUDA;
   }
