@@ -248,14 +248,16 @@ __device__ __forceinline__ uint4 grad_vec(const uint4& w, f32x2 c2, f32x2 nrc2, 
   }
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
-// The gradient of the list's tokens in [v0, v1), over what is there.  A token of several slots
-// (dup: there are some) takes the sum of their masses in slot order, at its first slot.
-template <bool kBF16>
-__device__ __forceinline__ void put_listed(unsigned char* base, int v0, int v1, bool dup, int K, const int32_t* s_id,
-                                           const float* s_e, const float* s_v, float shift, float A, float unit) {
+// The gradient of the list's tokens, over what is there: at element id of place(id) (nullptr:
+// another CTA's).  A token of several slots (dup: there are some) takes the sum of their masses in
+// slot order, at its first slot.
+template <bool kBF16, class Place>
+__device__ __forceinline__ void put_listed(Place&& place, bool dup, int K, const int32_t* s_id, const float* s_e,
+                                           const float* s_v, float shift, float A, float unit) {
   for (int k = threadIdx.x; k < K; k += kNT) {
     const int32_t id = s_id[k];
-    if (id < v0 || id >= v1) continue;  // empty slots are -1
+    unsigned char* base = id >= 0 ? place(id) : nullptr;  // empty slots are -1
+    if (!base) continue;
     float e = s_e[k];
     if (dup) {
       e = 0.0f;
@@ -496,7 +498,8 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
     }
     // the list's tokens in this CTA's part, over what the pass above wrote
     const bool dup = __syncthreads_or(twice);
-    put_listed<kBF16>(obase, rank == 0 ? 0 : x.head + g0 * G, rank == CS - 1 ? V : x.head + g1 * G, dup, K, s_id, s_e, s_v,
+    const int v0 = rank == 0 ? 0 : x.head + g0 * G, v1 = rank == CS - 1 ? V : x.head + g1 * G;
+    put_listed<kBF16>([&](int32_t id) { return id >= v0 && id < v1 ? obase : nullptr; }, dup, K, s_id, s_e, s_v,
                       (ref - all.ref) * c, F.A, scale * invE);
   }
 }
@@ -505,25 +508,13 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
 // The loss and the gradient with the row in shared memory
 // ------------------------------------------------------------------------------------------
 //
-// Memory bounds the pair: the row is read once, copied asynchronously into the shared memory of
-// a cluster's CTAs (a copy needs no register and every thread reads back only what it copied, so
-// no barrier either), summed as its parts arrive, and turned into the gradient from there.  Read
+// Memory bounds the pair: the row is read once, by bulk copies into the shared memory of a
+// cluster's CTAs, summed there, turned into the gradient in place and copied out.  Read
 // again from global memory it came from DRAM once more (an SM's rows in flight, times 152, are
 // more than the second-level cache holds): 495 us for 4096 rows of 151936 bf16 with a quarter
 // masked, three transfers of the matrix, whatever the number of rows in flight.
-constexpr int kGroups = 4;             // parts of a thread's copies that are waited for in turn
-constexpr int kChunkBytes = 40 * 1024; // of a row per CTA, where the cluster allows: five CTAs an SM
+constexpr int kChunkBytes = 52 * 1024; // of a row per CTA, where the cluster allows: four CTAs an SM
 constexpr int kMaxChunkBytes = 200 * 1024;
-
-__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-               "l"(src)
-               : "memory");
-}
-template <int kLeft>
-__device__ __forceinline__ void wait_copies() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
 
 // Keys of floats that order as they do, for maxima by integer atomics (NaN excluded).
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -548,6 +539,7 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
   __shared__ float part[kMaxCS * kNW];  // per warp of the cluster
   __shared__ float4 teacher[kNW];       // per warp: E, W and the student's sum over the list
   __shared__ uint32_t top[2];           // keys of the largest teacher's value and student's logit in the list
+  __shared__ __align__(8) unsigned long long landed;  // the copy's barrier
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   cg::cluster_group cl = cg::this_cluster();
   const int CS = static_cast<int>(cl.num_blocks());
@@ -567,7 +559,6 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
   const int g = g0 + static_cast<int>(threadIdx.x);                  // the thread's vectors: g + i kNT, i < count,
   uint4* const mine = reinterpret_cast<uint4*>(smem) + threadIdx.x;  // kept at mine[i kNT]
   const int count = g < g1 ? (g1 - g - 1) / kNT + 1 : 0;
-  const int group = ((g1 - g0 + kNT - 1) / kNT + kGroups - 1) / kGroups;  // vectors waited for together
   int32_t* s_id = reinterpret_cast<int32_t*>(smem + R.id);
   float* s_e = reinterpret_cast<float*>(smem + R.e);
   float* s_v = reinterpret_cast<float*>(smem + R.v);
@@ -578,14 +569,9 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
   // ---- the copies, and the teacher's slots while they are under way -----------------------------
   bool any = false;
   if (w != 0.0f) {
-    const uint4* from = x.vec + g;
-    uint4* to = mine;
-#pragma unroll
-    for (int j = 0, i = 0; j < kGroups; ++j) {
-      const int end = count < (j + 1) * group ? count : (j + 1) * group;
-#pragma unroll 4
-      for (; i < end; ++i, from += kNT, to += kNT) copy_async16(to, from);
-      asm volatile("cp.async.commit_group;" ::: "memory");
+    if (threadIdx.x == 0) {
+      copy_barrier_init(&landed);
+      if (g1 > g0) copy_in(smem, x.vec + g0, static_cast<uint32_t>(g1 - g0) * 16u, &landed);
     }
     if (threadIdx.x < 2) top[threadIdx.x] = 0u;
     if (kRest) s_head[threadIdx.x] = -1;
@@ -608,7 +594,7 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
   }
   any = __syncthreads_or(any);
   if (!any) {  // no loss: zeros (the same in every CTA of the row)
-    wait_copies<0>();
+    if (w != 0.0f && g1 > g0) copy_landed(&landed);
     if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (rank == 0 && threadIdx.x == 0) P.loss[row] = 0.0f;
     zero_row<kBF16>(P.grad, row * P.ld_grad, V, rank, CS);
@@ -668,34 +654,26 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
     if (lane == 0) teacher[warp] = make_float4(E, W, S, 0.0f);
   }
 
-  // ---- the student's sum outside the list, as the copies arrive ------------------------------------
+  // ---- the student's sum outside the list -------------------------------------------------------
   // With kRest the list's tokens leave the row: each thread overwrites those in its own vectors with
   // -inf (their logits are in s_v).  Against the list's largest student logit, one reference for
   // the whole row, so that the parts simply add up; a sum that leaves fp32's range (the list far
   // from everything else) is taken again below against its own maximum.
+  const bool late = g1 > g0 && !copy_landed(&landed);
   float s_rest;
   {
-    const int32_t head = kRest ? s_head[threadIdx.x] : -1;
     FastSum<kBF16> fast(fabsf(ref * c) <= kFastRef ? ref : 0.0f, c);
-#pragma unroll
-    for (int j = 0, i = 0; j < kGroups; ++j) {
-      if (j == 0) wait_copies<3>();
-      if (j == 1) wait_copies<2>();
-      if (j == 2) wait_copies<1>();
-      if (j == 3) wait_copies<0>();
-      const int end = count < (j + 1) * group ? count : (j + 1) * group;
-      if (kRest) {
-        for (int k = head; k >= 0; k = s_next[k]) {
-          const int at = s_id[k] - x.head, step = (at / G - g0) / kNT;
-          if (step < i || step >= end) continue;
-          if (kBF16) reinterpret_cast<uint16_t*>(mine + step * kNT)[at % G] = 0xFF80u;
-          else reinterpret_cast<uint32_t*>(mine + step * kNT)[at % G] = 0xFF800000u;
-        }
+    if (kRest) {
+      for (int k = s_head[threadIdx.x]; k >= 0; k = s_next[k]) {
+        const int at = s_id[k] - x.head;
+        uint4* v = mine + (at / G - g);
+        if (kBF16) reinterpret_cast<uint16_t*>(v)[at % G] = 0xFF80u;
+        else reinterpret_cast<uint32_t*>(v)[at % G] = 0xFF800000u;
       }
-#pragma unroll 2
-      for (; i < end; ++i) fast.add(mine[i * kNT]);
     }
-    s_rest = fast.total(ref, c);
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) fast.add(mine[i * kNT]);
+    s_rest = late ? NAN : fast.total(ref, c);  // a row that did not arrive has no result
   }
   // the elements outside the vectors: the head with rank 0, the tail with the last rank
   const bool has_loose = static_cast<int>(threadIdx.x) < x.loose() &&
@@ -737,7 +715,7 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
     // the same in every CTA: the largest logit outside the list (NaN: there is one), then the sum
     // against that
     float m = loose_out ? loose_s : -INFINITY;
-    bool nan = isnan(m);
+    bool nan = late || isnan(m);
     auto each = [&](auto&& f) {
       for (int i = 0; i < count; ++i) {
         const uint4 v = mine[i * kNT];
@@ -779,17 +757,20 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
   }
 
   // ---- the gradient ------------------------------------------------------------------------------
+  // In place in shared memory, the list's tokens last, and out with one copy.
   const float invE = 1.0f / (E + er);
   const Factors F(scale, er, invE, all, rest, c);
   const RowView<kBF16> o(P.grad, row * P.ld_grad, V);
   unsigned char* obase = const_cast<unsigned char*>(o.base);
+  unsigned char* inside = obase;  // where element id of this CTA's vectors goes
+  const int v0 = x.head + g0 * G, v1 = x.head + g1 * G;
   const float rc = all.ref * c;
   if (F.one && o.head == x.head && fabsf(rc) <= kFastRef) {
     const float fix = ex2(-fmaf(all.ref, c, -rc));  // what rc's rounding left out
     const f32x2 nrc2 = pack2(-rc, -rc), c2 = pack2(c, c), C2 = pack2(F.C * fix, F.C * fix);
-    uint4* ov = const_cast<uint4*>(o.vec) + g;
-#pragma unroll 2
-    for (int i = 0; i < count; ++i) __stcs(ov + i * kNT, grad_vec<kBF16>(mine[i * kNT], c2, nrc2, C2));
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) mine[i * kNT] = grad_vec<kBF16>(mine[i * kNT], c2, nrc2, C2);
+    inside = smem - static_cast<int64_t>(v0) * (kBF16 ? 2 : 4);
   } else {
     for (int i = 0; i < count; ++i) {
       const uint4 v = mine[i * kNT];
@@ -798,14 +779,25 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
       for (int e = 0; e < G; ++e) {
         const float s = kBF16 ? __uint_as_float((e & 1) ? (word[e / 2] & 0xFFFF0000u) : (word[e / 2] << 16))
                               : __uint_as_float(word[e]);
-        put_grad<kBF16>(obase, x.head + (g + i * kNT) * G + e, F.outside(s, all, rest, c));
+        put_grad<kBF16>(obase, v0 + (static_cast<int>(threadIdx.x) + i * kNT) * G + e, F.outside(s, all, rest, c));
       }
     }
   }
   if (has_loose) put_grad<kBF16>(obase, loose_v, F.outside(loose_s, all, rest, c));
   __syncthreads();
-  put_listed<kBF16>(obase, rank == 0 ? 0 : x.head + g0 * G, rank == CS - 1 ? V : x.head + g1 * G, dup, K, s_id, s_e, s_v,
-                    (ref - all.ref) * c, F.A, scale * invE);
+  put_listed<kBF16>(
+      [&](int32_t id) -> unsigned char* {
+        if (id >= v0 && id < v1) return inside;
+        return (rank == 0 && id < x.head) || (rank == CS - 1 && id >= v1) ? obase : nullptr;
+      },
+      dup, K, s_id, s_e, s_v, (ref - all.ref) * c, F.A, scale * invE);
+  if (inside != obase) {
+    publish_to_copies();
+    __syncthreads();
+    if (threadIdx.x == 0 && g1 > g0)
+      copy_out(const_cast<uint4*>(o.vec) + g0, smem, static_cast<uint32_t>(g1 - g0) * 16u);
+  }
+  if (late) copy_landed(&landed);  // one more wait before the block leaves
 }
 
 // ------------------------------------------------------------------------------------------
@@ -877,7 +869,7 @@ static kps_status launch_both(const Params& P, cudaStream_t stream) {
   cs = cs < 1 ? 1 : cs > kMaxCS ? kMaxCS : cs;
   if (bytes > static_cast<int64_t>(kMaxChunkBytes) * cs) return launch_t<kBF16, kRest, kBoth>(P, stream);
   // few rows: wider clusters, while every thread keeps a group's worth of vectors
-  while (2 * cs <= kMaxCS && P.N * cs * 2 <= 2 * sms && P.V >= 2 * cs * kNT * kGroups * G) cs *= 2;
+  while (2 * cs <= kMaxCS && P.N * cs * 2 <= 2 * sms && P.V >= 2 * cs * kNT * 4 * G) cs *= 2;
   Resident R;
   R.share = (P.V / G + cs - 1) / cs;
   R.hash_size = 32;

@@ -211,5 +211,45 @@ __device__ __forceinline__ float warp_sum(float v) {
 // A finite reference: differences to it are never inf - inf.
 __device__ __forceinline__ float clamp_ref(float x) { return fminf(fmaxf(x, -FLT_MAX), FLT_MAX); }
 
+// ---- bulk copies between global and shared memory (16-byte addresses and sizes) -----------------
+__device__ __forceinline__ uint32_t shared_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+// A barrier for one copy; visible to the copy engine and, after a block barrier, to the block.
+__device__ __forceinline__ void copy_barrier_init(unsigned long long* bar) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_u32(bar)) : "memory");
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void copy_in(void* dst, const void* src, uint32_t bytes, unsigned long long* bar) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_u32(bar)), "r"(bytes) : "memory");
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   shared_u32(dst)),
+               "l"(src), "r"(bytes), "r"(shared_u32(bar))
+               : "memory");
+}
+// Waits for the copy, for about two seconds at most; false when it has not landed by then.
+__device__ __forceinline__ bool copy_landed(unsigned long long* bar) {
+  const long long t0 = clock64();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], 0;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(shared_u32(bar))
+        : "memory");
+    if (ok) return true;
+    if (clock64() - t0 > 4000000000LL) return false;
+  }
+}
+// Before a block barrier after which one thread stores what the block wrote to shared memory.
+__device__ __forceinline__ void publish_to_copies() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// The store, by one thread, which waits until the shared memory has been read.
+__device__ __forceinline__ void copy_out(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(shared_u32(src)), "r"(bytes)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
 }  // namespace stream
 }  // namespace kps
