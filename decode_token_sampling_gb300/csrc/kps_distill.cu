@@ -85,6 +85,11 @@ __host__ __device__ inline Layout make_layout(int K, int64_t chunk, bool grad, b
   return L;
 }
 
+__device__ __forceinline__ float teacher_value(const Params& P, int64_t i) {
+  return P.values_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(P.values)[i])
+                       : static_cast<const float*>(P.values)[i];
+}
+
 // Block reductions over kNT threads; every thread gets the result.
 __device__ __forceinline__ void block_max2(float& a, float& b, float (*red)[2]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -190,18 +195,19 @@ __device__ __forceinline__ void take_listed(uint4& v, uint32_t m, Sum2& list, fl
 // Inserts a token of the list into a table of its distinct tokens; true when it was there already.
 __device__ __forceinline__ bool insert_token(int32_t* hash, int size, int32_t id) {
   uint32_t h = (static_cast<uint32_t>(id) * 2654435761u) & (size - 1);
-  for (;;) {
+  for (int i = 0; i < size; ++i) {  // at most K of the 2K places are taken: it ends long before
     const int32_t old = atomicCAS(&hash[h], -1, id);
     if (old == -1) return false;
     if (old == id) return true;
-    h = (h + 1) & (size - 1);  // at most K of the 2K places are taken
+    h = (h + 1) & (size - 1);
   }
+  return false;
 }
 
 // Whether the table holds a token.
 __device__ __forceinline__ bool has_token(const int32_t* hash, int size, int32_t id) {
   uint32_t h = (static_cast<uint32_t>(id) * 2654435761u) & (size - 1);
-  for (; hash[h] != -1; h = (h + 1) & (size - 1))
+  for (int i = 0; i < size && hash[h] != -1; ++i, h = (h + 1) & (size - 1))
     if (hash[h] == id) return true;
   return false;
 }
@@ -317,8 +323,7 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
       for (int i = threadIdx.x; i < lay.hash_size; i += kNT) s_hash[i] = -1;
     for (int k = threadIdx.x; k < K; k += kNT) {
       int32_t id = P.ids[row * K + k];
-      const float t = P.values_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(P.values)[row * K + k])
-                                    : static_cast<const float*>(P.values)[row * K + k];
+      const float t = teacher_value(P, row * K + k);
       float s = 0.0f;
       if (id < 0 || id >= V || t == -INFINITY) {
         id = -1;
@@ -539,6 +544,7 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
   __shared__ float part[kMaxCS * kNW];  // per warp of the cluster
   __shared__ float4 teacher[kNW];       // per warp: E, W and the student's sum over the list
   __shared__ uint32_t top[2];           // keys of the largest teacher's value and student's logit in the list
+  __shared__ int flags[2];              // the row has a filled slot; some token has two
   __shared__ __align__(8) unsigned long long landed;  // the copy's barrier
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   cg::cluster_group cl = cg::this_cluster();
@@ -551,9 +557,6 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
   const float c = P.c;
   // every CTA of the cluster runs before any writes into another's shared memory
   if (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  const float w = P.weight ? P.weight[row] : 1.0f;
-  const float scale = w * P.tau;
-
   const RowView<kBF16> x(P.student, row * P.ld, V);
   const int g0 = min(rank * R.share, x.nv), g1 = rank == CS - 1 ? x.nv : min(g0 + R.share, x.nv);
   const int g = g0 + static_cast<int>(threadIdx.x);                  // the thread's vectors: g + i kNT, i < count,
@@ -566,65 +569,65 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
   int32_t* s_head = reinterpret_cast<int32_t*>(smem + R.head);  // per thread: the first of the slots whose tokens
   int32_t* s_hash = reinterpret_cast<int32_t*>(smem + R.hash);  // lie in its vectors, the others by s_next (kRest)
 
-  // ---- the copies, and the teacher's slots while they are under way -----------------------------
-  bool any = false;
+  // ---- the copy, and the teacher's slots while it is under way ------------------------------------
+  if (threadIdx.x == 0) copy_barrier_init(&landed);
+  if (threadIdx.x < 2) {
+    top[threadIdx.x] = 0u;
+    flags[threadIdx.x] = 0;
+  }
+  if (kRest) s_head[threadIdx.x] = -1;
+  for (int i = threadIdx.x; i < R.hash_size; i += kNT) s_hash[i] = -1;
+  // (the slots of a row of weight 0 are read all the same: their loads need not wait for the weight's)
+  int32_t id = threadIdx.x < K ? P.ids[row * K + threadIdx.x] : -1;
+  float t = threadIdx.x < K ? teacher_value(P, row * K + threadIdx.x) : -INFINITY;
+  const float w = P.weight ? P.weight[row] : 1.0f;
+  const float r = kRest ? P.rest[row] : -INFINITY;
+  const float scale = w * P.tau;
+  __syncthreads();
   if (w != 0.0f) {
-    if (threadIdx.x == 0) {
-      copy_barrier_init(&landed);
-      if (g1 > g0) copy_in(smem, x.vec + g0, static_cast<uint32_t>(g1 - g0) * 16u, &landed);
-    }
-    if (threadIdx.x < 2) top[threadIdx.x] = 0u;
-    if (kRest) s_head[threadIdx.x] = -1;
-    for (int i = threadIdx.x; i < R.hash_size; i += kNT) s_hash[i] = -1;
-    for (int k = threadIdx.x; k < K; k += kNT) {
-      int32_t id = P.ids[row * K + k];
-      const float t = P.values_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(P.values)[row * K + k])
-                                    : static_cast<const float*>(P.values)[row * K + k];
-      float s = 0.0f;
-      if (id < 0 || id >= V || t == -INFINITY) {
-        id = -1;
-      } else {
-        s = x.at(id);
-        any = true;
+    if (threadIdx.x == 0 && g1 > g0) copy_in(smem, x.vec + g0, static_cast<uint32_t>(g1 - g0) * 16u, &landed);
+    if (warp * 32 < K) {  // (a warp's slots are its own threads')
+      uint32_t tk = 0, sk = 0;
+      for (int k = threadIdx.x; k < K;) {
+        if (id < 0 || id >= V || t == -INFINITY) id = -1;
+        const float s = id >= 0 ? x.at(id) : 0.0f;
+        s_id[k] = id;
+        s_e[k] = t;
+        s_v[k] = s;
+        if (id >= 0) {
+          flags[0] = 1;
+          if (!isnan(t)) tk = max(tk, order_key(t));
+          if (!isnan(s)) sk = max(sk, order_key(s));
+          if (insert_token(s_hash, R.hash_size, id)) flags[1] = 1;
+          if (kRest) {
+            const int at = id - x.head, vec = at / G - g0;
+            if (at >= 0 && vec >= 0 && vec < g1 - g0) s_next[k] = atomicExch(&s_head[vec & (kNT - 1)], k);
+          }
+        }
+        k += kNT;
+        if (k < K) {
+          id = P.ids[row * K + k];
+          t = teacher_value(P, row * K + k);
+        }
       }
-      s_id[k] = id;
-      s_e[k] = t;
-      s_v[k] = s;
+      __syncwarp();
+      tk = __reduce_max_sync(0xffffffffu, tk);
+      sk = __reduce_max_sync(0xffffffffu, sk);
+      if (lane == 0) {
+        atomicMax(&top[0], tk);
+        atomicMax(&top[1], sk);
+      }
     }
   }
-  any = __syncthreads_or(any);
-  if (!any) {  // no loss: zeros (the same in every CTA of the row)
+  __syncthreads();
+  if (!flags[0]) {  // no loss: zeros (the same in every CTA of the row)
     if (w != 0.0f && g1 > g0) copy_landed(&landed);
     if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (rank == 0 && threadIdx.x == 0) P.loss[row] = 0.0f;
     zero_row<kBF16>(P.grad, row * P.ld_grad, V, rank, CS);
     return;
   }
-  bool twice = false;
-  if (warp * 32 < K) {  // (a warp's slots are its own threads')
-    uint32_t t = 0, sm = 0;
-    for (int k = threadIdx.x; k < K; k += kNT) {
-      const int32_t id = s_id[k];
-      if (id < 0) continue;
-      const float tk = s_e[k], sk = s_v[k];
-      if (!isnan(tk)) t = max(t, order_key(tk));
-      if (!isnan(sk)) sm = max(sm, order_key(sk));
-      twice |= insert_token(s_hash, R.hash_size, id);
-      if (kRest) {
-        const int at = id - x.head, vec = at / G - g0;
-        if (at >= 0 && vec >= 0 && vec < g1 - g0) s_next[k] = atomicExch(&s_head[vec & (kNT - 1)], k);
-      }
-    }
-    __syncwarp();
-    t = __reduce_max_sync(0xffffffffu, t);
-    sm = __reduce_max_sync(0xffffffffu, sm);
-    if (lane == 0) {
-      atomicMax(&top[0], t);
-      atomicMax(&top[1], sm);
-    }
-  }
-  const bool dup = __syncthreads_or(twice);
-  const float r = kRest ? P.rest[row] : -INFINITY;
+  const bool dup = flags[1] != 0;
   const float tref = clamp_ref(fmaxf(top[0] ? order_value(top[0]) : -INFINITY, r * P.tau));
   const float ref = clamp_ref(top[1] ? order_value(top[1]) : -INFINITY);  // of the student's sums too
   {
@@ -750,12 +753,6 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
   }
   const float ur = (r * P.tau - tref) * c;
   const float er = kRest ? ex2(ur) : 0.0f;  // the rest class (0 when there is none)
-  if (rank == 0 && threadIdx.x == 0) {
-    const float kl = divergence<kRest>(E, W, er, ur, ref, list, rest, all, c);
-    const bool ok = all.s > 0.0f && all.s < INFINITY;
-    P.loss[row] = ok ? w * P.tau * P.tau * (kl * kLn2) : NAN;
-  }
-
   // ---- the gradient ------------------------------------------------------------------------------
   // In place in shared memory, the list's tokens last, and out with one copy.
   const float invE = 1.0f / (E + er);
@@ -796,6 +793,11 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
     __syncthreads();
     if (threadIdx.x == 0 && g1 > g0)
       copy_out(const_cast<uint4*>(o.vec) + g0, smem, static_cast<uint32_t>(g1 - g0) * 16u);
+  }
+  if (rank == 0 && threadIdx.x == kNT - 1) {
+    const float kl = divergence<kRest>(E, W, er, ur, ref, list, rest, all, c);
+    const bool ok = all.s > 0.0f && all.s < INFINITY;
+    P.loss[row] = ok ? w * P.tau * P.tau * (kl * kLn2) : NAN;
   }
   if (late) copy_landed(&landed);  // one more wait before the block leaves
 }
