@@ -54,7 +54,7 @@ struct Params {
   int values_bf16;
   const float* rest;     // or nullptr
   const float* weight;   // or nullptr: 1
-  float tau, c;          // c = log2(e) / tau
+  float tau, c, c_lo;    // c + c_lo = log2(e) / tau
   const float* upstream; // gradient modes: the loss's gradient per row, or nullptr: 1
   float* loss;           // [N] (kForward, kBoth)
   float* stats;          // [N, kStats]: written by kForward (may be nullptr), read by kBackward
@@ -62,13 +62,13 @@ struct Params {
   int64_t ld_grad;
 };
 
-// Shared memory: the teacher's slots, the exchange slots, the hash table of the list's ids
-// (gradient modes) and the bitmap of the list's tokens in this CTA's part of the row (rest).
+// Shared memory: the teacher's slots, the hash table of the list's distinct tokens and the bitmap
+// of the list's tokens in this CTA's part of the row (rest).
 struct Layout {
   size_t id, e, v, hash, bits, total;
   int hash_size;
 };
-__host__ __device__ inline Layout make_layout(int K, int64_t chunk, bool grad, bool rest) {
+__host__ __device__ inline Layout make_layout(int K, int64_t chunk, bool distinct, bool rest) {
   Layout L;
   size_t off = 0;
   const size_t k4 = (static_cast<size_t>(K) * 4 + 15) / 16 * 16;
@@ -78,7 +78,7 @@ __host__ __device__ inline Layout make_layout(int K, int64_t chunk, bool grad, b
   L.hash_size = 32;
   while (L.hash_size < 2 * K) L.hash_size *= 2;
   L.hash = off;
-  if (grad) off += static_cast<size_t>(L.hash_size) * 4;
+  if (distinct) off += static_cast<size_t>(L.hash_size) * 4;
   L.bits = off;
   if (rest) off += (static_cast<size_t>(chunk) + 31) / 32 * 4 / 16 * 16 + 32;
   L.total = off;
@@ -139,22 +139,69 @@ __device__ __forceinline__ void add_one(Sum2& sum, float x, float c) {
 // log2(1 + 2^z).
 __device__ __forceinline__ float log2_1p_ex2(float z) { return z > 24.0f ? z : kLog2e * log1pf(ex2(z)); }
 
-// The divergence in base 2, from the teacher's E = sum 2^(u_k), W = sum 2^(u_k) (u_k - v_k) over
-// the list and er = 2^(ur) of the rest, and the student's sums.
+// ---- the list, to more than fp32's rounding of its exponents ----------------------------------
+//
+// The gradient of a list's token is a difference of two masses, and the loss a sum of terms that
+// cancel when the student comes near its teacher: there the rounding of an exponent of 20 or 30
+// would show.  Exponents of the list's tokens and of the rest are therefore carried as two floats
+// (the sum over the row needs none of that: its terms weigh little where their exponents are large).
+
+// h + l = x - y exactly (l = 0 where the difference is not finite).
+__device__ __forceinline__ void two_diff(float x, float y, float& h, float& l) {
+  h = x - y;
+  const float b = h - x;
+  l = (x - (h - b)) + (-y - b);
+  if (!(fabsf(h) < INFINITY)) l = 0.0f;
+}
+// 2^(h + l) for a small l.
+__device__ __forceinline__ float ex2_two(float h, float l) {
+  const float e = ex2(h);
+  return l != 0.0f ? fmaf(e, l * kLn2, e) : e;
+}
+// 2^((x - ref) (c + c_lo)).
+__device__ __forceinline__ float mass(float x, float ref, float c, float c_lo) {
+  float h, l;
+  two_diff(x, ref, h, l);
+  const float z = h * c;
+  const float rest = fmaf(h, c, -z) + fmaf(h, c_lo, l * c);
+  return ex2_two(z, fabsf(z) < 1e30f ? rest : 0.0f);
+}
+
+// The teacher's side of a row against the reference tref: E = sum e_k, W = sum e_k (u_k - v_k), with
+// e_k = 2^(u_k), u_k and v_k the exponents of the teacher's value and the student's logit; the
+// rest's e_r = 2^(uh + ul).
+struct Teacher {
+  float E, W, er, uh, ul;
+  template <bool kRest>
+  __device__ __forceinline__ void rest(float r, float tref, float c, float c_lo) {
+    er = uh = ul = 0.0f;
+    if (!kRest) return;
+    const float a = r * kLog2e, b = tref * c;  // r is in nats at the temperature
+    const float al = fmaf(r, kLog2e, -a) + r * 1.92596303e-8f, bl = fmaf(tref, c, -b) + tref * c_lo;
+    two_diff(a, b, uh, ul);
+    ul = fabsf(uh) < 1e30f ? ul + (al - bl) : 0.0f;
+    er = ex2_two(uh, ul);
+  }
+};
+
+// The divergence in base 2.  list, rest, all: the student's sums.
 template <bool kRest>
-__device__ __forceinline__ float divergence(float E, float W, float er, float ur, float ref, const Sum2& list,
-                                            const Sum2& rest, const Sum2& all, float c) {
-  // ls = log2 S and lr = log2 SR against ref
-  const float ls = log2f(all.s) + (all.ref - ref) * c;
-  if (!kRest || er == 0.0f) return W / E - log2f(E) + ls;
+__device__ __forceinline__ float divergence(const Teacher& t, float ref, const Sum2& list, const Sum2& rest,
+                                            const Sum2& all, float c) {
+  const float moved = (all.ref - ref) * c;
+  if (!kRest || t.er == 0.0f) return t.W / t.E + log2f(all.s / t.E) + moved;
   if (rest.s == 0.0f) return INFINITY;  // the teacher's rest has mass, the student's none
-  const float Et = E + er, pr = er / Et;
-  const float lr = log2f(rest.s) + (rest.ref - ref) * c;
-  if (!(pr >= 0.5f)) return (W + er * (ur - lr)) / Et - log2f(Et) + ls;
+  const float Et = t.E + t.er, pr = t.er / Et;
+  // D = (uh + ul) - log2 of the student's rest against ref, whole powers of two first
+  const uint32_t bits = __float_as_uint(rest.s);
+  const float k = static_cast<float>(static_cast<int>(bits >> 23) - 127);
+  const float m = __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u);
+  const float D = ((t.uh - k) + t.ul) - log2f(m) - (rest.ref - ref) * c;
+  if (!(pr >= 0.5f)) return (t.W + t.er * D) / Et + log2f(all.s / Et) + moved;
   // most mass is the rest's: ln p_r and ln q_r from what they leave, so that two numbers near
   // zero are not differences of large ones
   const float q = list.s > 0.0f ? log2_1p_ex2(log2f(list.s / rest.s) + (list.ref - rest.ref) * c) : 0.0f;
-  return W / Et - E / Et * (ur - lr) - kLog2e * log1pf(E / er) + q;
+  return t.W / Et - t.E / Et * D - kLog2e * log1pf(t.E / t.er) + q;
 }
 
 // Writes zeros to this CTA's part of a row of the gradient.
@@ -172,22 +219,15 @@ __device__ __forceinline__ void zero_row(void* grad, int64_t offset, int V, int 
   }
 }
 
-// Takes the list's tokens (bits m) out of a vector into their own sum.
+// Takes the list's tokens (bits m) out of a vector.
 template <bool kBF16>
-__device__ __forceinline__ void take_listed(uint4& v, uint32_t m, Sum2& list, float c) {
-  constexpr int G = kBF16 ? 8 : 4;
+__device__ __forceinline__ void drop_listed(uint4& v, uint32_t m) {
   uint32_t word[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int e = 0; e < G; ++e) {
+  for (int e = 0; e < (kBF16 ? 8 : 4); ++e) {
     if (!((m >> e) & 1u)) continue;
-    if (kBF16) {
-      const uint32_t h = (e & 1) ? (word[e / 2] & 0xFFFF0000u) : (word[e / 2] << 16);
-      add_one(list, __uint_as_float(h), c);
-      word[e / 2] = (e & 1) ? (word[e / 2] & 0x0000FFFFu) | 0xFF800000u : (word[e / 2] & 0xFFFF0000u) | 0x0000FF80u;
-    } else {
-      add_one(list, __uint_as_float(word[e]), c);
-      word[e] = 0xFF800000u;
-    }
+    if (kBF16) word[e / 2] = (e & 1) ? (word[e / 2] & 0x0000FFFFu) | 0xFF800000u : (word[e / 2] & 0xFFFF0000u) | 0x0000FF80u;
+    else word[e] = 0xFF800000u;
   }
   v = make_uint4(word[0], word[1], word[2], word[3]);
 }
@@ -256,10 +296,11 @@ __device__ __forceinline__ uint4 grad_vec(const uint4& w, f32x2 c2, f32x2 nrc2, 
 }
 // The gradient of the list's tokens, over what is there: at element id of place(id) (nullptr:
 // another CTA's).  A token of several slots (dup: there are some) takes the sum of their masses in
-// slot order, at its first slot.
+// slot order, at its first slot.  s_e, s_v: the teacher's and the student's masses before their
+// factors unit and A.
 template <bool kBF16, class Place>
 __device__ __forceinline__ void put_listed(Place&& place, bool dup, int K, const int32_t* s_id, const float* s_e,
-                                           const float* s_v, float shift, float A, float unit) {
+                                           const float* s_v, float A, float unit) {
   for (int k = threadIdx.x; k < K; k += kNT) {
     const int32_t id = s_id[k];
     unsigned char* base = id >= 0 ? place(id) : nullptr;  // empty slots are -1
@@ -275,7 +316,7 @@ __device__ __forceinline__ void put_listed(Place&& place, bool dup, int K, const
       }
       if (!first) continue;
     }
-    put_grad<kBF16>(base, id, A * ex2(s_v[k] + shift) - unit * e);
+    put_grad<kBF16>(base, id, A * s_v[k] - unit * e);
   }
 }
 
@@ -284,7 +325,8 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
   constexpr int G = kBF16 ? 8 : 4;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float red[kNW][2];
-  __shared__ float part[2 * kMaxCS][2];  // the partial sums of the cluster's CTAs (list, rest)
+  __shared__ float part[kMaxCS][2];  // the partial sums of the cluster's CTAs
+  constexpr bool kDistinct = kMode != kForward || kRest;  // the list's distinct tokens are needed
   const int CS = static_cast<int>(cg::this_cluster().num_blocks());
   const int rank = static_cast<int>(cg::this_cluster().block_rank());
   const int64_t row = blockIdx.x / CS;
@@ -297,7 +339,7 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
   const RowView<kBF16> x(P.student, row * P.ld, V);
   const int g0 = static_cast<int>(static_cast<int64_t>(x.nv) * rank / CS);
   const int g1 = static_cast<int>(static_cast<int64_t>(x.nv) * (rank + 1) / CS);
-  const Layout lay = make_layout(K, (V + CS - 1) / CS + 4 * G, kMode != kForward, kRest);
+  const Layout lay = make_layout(K, (V + CS - 1) / CS + 4 * G, kDistinct, kRest);
   int32_t* s_id = reinterpret_cast<int32_t*>(smem + lay.id);
   float* s_e = reinterpret_cast<float*>(smem + lay.e);
   float* s_v = reinterpret_cast<float*>(smem + lay.v);
@@ -319,7 +361,7 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
   if (w != 0.0f) {
     if (kRest && kMode != kBackward)
       for (int i = threadIdx.x; i < (nbits + 31) / 32; i += kNT) s_bits[i] = 0u;
-    if (kMode != kForward)
+    if (kDistinct)
       for (int i = threadIdx.x; i < lay.hash_size; i += kNT) s_hash[i] = -1;
     for (int k = threadIdx.x; k < K; k += kNT) {
       int32_t id = P.ids[row * K + k];
@@ -363,96 +405,109 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
     rest = Sum2{P.stats[row * kStats + 2], P.stats[row * kStats + 3]};
   }
   const float ref = kMode == kBackward ? all.ref : clamp_ref(smax);
-  // e_k = 2^(u_k), u_k = (t_k - tref) c; v_k = (s_k - ref) c; E = sum e_k, W = sum e_k (u_k - v_k)
-  float E = 0.0f, W = 0.0f;
   bool twice = false;
+  if (kDistinct) {
+    for (int k = threadIdx.x; k < K; k += kNT) {
+      const int32_t id = s_id[k];
+      if (id < 0) continue;
+      twice |= insert_token(s_hash, lay.hash_size, id);
+      const int b = id - bit0;
+      if (kRest && kMode != kBackward && b >= 0 && b < nbits) atomicOr(&s_bits[b >> 5], 1u << (b & 31));
+    }
+  }
+  const bool dup = kDistinct && __syncthreads_or(twice);
+  Teacher T = {};
+  float S = 0.0f;  // the student's sum over the list
   for (int k = threadIdx.x; k < K; k += kNT) {
     const int32_t id = s_id[k];
-    float e = 0.0f, v = 0.0f;
+    float e = 0.0f, q = 0.0f;
     if (id >= 0) {
-      const float u = (s_e[k] - tref) * c;
-      v = (s_v[k] - ref) * c;
-      e = ex2(u);
-      E += e;
-      if (e != 0.0f) W += e * (u - v);  // NaN stays (e is NaN then)
-      if (kRest && kMode != kBackward) {
-        const int b = id - bit0;
-        if (b >= 0 && b < nbits) atomicOr(&s_bits[b >> 5], 1u << (b & 31));
-      }
-      if (kMode != kForward) {
-        twice |= insert_token(s_hash, lay.hash_size, id);
-      }
+      const float t = s_e[k], sv = s_v[k];
+      e = mass(t, tref, c, P.c_lo);
+      q = mass(sv, ref, c, P.c_lo);
+      T.E += e;
+      if (e != 0.0f) T.W += e * (((t - tref) - (sv - ref)) * c);  // NaN stays (e is NaN then)
+      bool first = true;  // a token of several slots counts once
+      if (dup)
+        for (int j = 0; j < k; ++j) first = first && s_id[j] != id;
+      if (first) S += q;
     }
     s_e[k] = e;
-    s_v[k] = v;
+    s_v[k] = q;
   }
-  block_sum2(E, W, red);  // its barriers also publish the bitmap and the slots
-  const float ur = (r * P.tau - tref) * c;
-  const float er = kRest ? ex2(ur) : 0.0f;  // the rest class (0 when there is none)
+  block_sum2(T.E, T.W, red);  // its barriers also publish the bitmap and the slots
+  if (kRest && kMode != kBackward) {
+    float unused = 0.0f;
+    block_sum2(S, unused, red);
+  }
+  T.rest<kRest>(r, tref, c, P.c_lo);
 
-  // ---- the student's sums -------------------------------------------------------------
+  // ---- the student's sum outside the list (kRest; of the whole row else) ----------------------
+  // Against the list's largest logit, one reference for the whole row and near its top.  A sum that
+  // leaves fp32's range (the list far from everything else) is taken again with moving references.
   if (kMode != kBackward) {
-    // without kRest every token counts in `rest`; its reference is a value of the thread's own
-    Sum2 list{ref, 0.0f};
-    rest = Sum2{-FLT_MAX, 0.0f};
-    const float lift = kRaise / c;
     const unsigned char* bytes = reinterpret_cast<const unsigned char*>(s_bits);
-    for (int base = g0; base < g1; base += kNT * kU) {
-      uint4 v[kU];
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int g = base + u * kNT + static_cast<int>(threadIdx.x);
-        v[u] = g < g1 ? ld_stream(x.vec + g) : neg_inf_vec<kBF16>();
-      }
-      if (kRest) {
-        // the list's tokens go to their own sum and leave the vector
+    const Sum2 list{ref, kRest ? S : 0.0f};
+    for (bool moving = !(fabsf(ref * c) <= kFastRef);; moving = true) {
+      FastSum<kBF16> fast(moving ? 0.0f : ref, c);
+      rest = Sum2{-FLT_MAX, 0.0f};
+      for (int base = g0; base < g1; base += kNT * kU) {
+        uint4 v[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const int g = base + u * kNT + static_cast<int>(threadIdx.x);
-          const int b = (g - g0 + 1) * G;
-          uint32_t m = g < g1 ? bytes[b >> 3] : 0u;
-          if (!kBF16) m = (m >> (b & 4)) & 15u;
-          if (m) take_listed<kBF16>(v[u], m, list, c);
+          v[u] = g < g1 ? ld_stream(x.vec + g) : neg_inf_vec<kBF16>();
+        }
+        if (kRest) {
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            const int g = base + u * kNT + static_cast<int>(threadIdx.x);
+            const int b = (g - g0 + 1) * G;
+            uint32_t m = g < g1 ? bytes[b >> 3] : 0u;
+            if (!kBF16) m = (m >> (b & 4)) & 15u;
+            if (m) drop_listed<kBF16>(v[u], m);
+          }
+        }
+        if (!moving) {
+#pragma unroll
+          for (int u = 0; u < kU; ++u) fast.add(v[u]);
+        } else {
+          float m = vec_max<kBF16>(v[0]);
+#pragma unroll
+          for (int u = 1; u < kU; ++u) m = fmaxf(m, vec_max<kBF16>(v[u]));
+          if ((m - rest.ref) * c > kRaise) rest.raise(clamp_ref(m), c);
+#pragma unroll
+          for (int u = 0; u < kU; ++u) add_vec<kBF16>(rest, v[u], c);
         }
       }
-      float m = vec_max<kBF16>(v[0]);
-#pragma unroll
-      for (int u = 1; u < kU; ++u) m = fmaxf(m, vec_max<kBF16>(v[u]));
-      if (m > rest.ref + lift) rest.raise(clamp_ref(m), c);
-#pragma unroll
-      for (int u = 0; u < kU; ++u) add_vec<kBF16>(rest, v[u], c);
-    }
-    // the elements outside the vectors: the head with rank 0, the tail with the last rank
-    if (static_cast<int>(threadIdx.x) < x.loose()) {
-      const int v = x.loose_at(threadIdx.x);
-      if ((v < x.head) ? rank == 0 : rank == CS - 1) {
-        const int b = v - bit0;
-        const bool in = kRest && ((s_bits[b >> 5] >> (b & 31)) & 1u);
-        add_one(in ? list : rest, x.at(v), c);
+      if (!moving) rest = Sum2{ref, fast.total(ref, c)};
+      // the elements outside the vectors: the head with rank 0, the tail with the last rank
+      if (static_cast<int>(threadIdx.x) < x.loose()) {
+        const int v = x.loose_at(threadIdx.x);
+        if ((v < x.head) ? rank == 0 : rank == CS - 1) {
+          const int b = v - bit0;
+          const bool in = kRest && ((s_bits[b >> 5] >> (b & 31)) & 1u);
+          if (!in) add_one(rest, x.at(v), c);
+        }
       }
-    }
-    rest = block_merge(rest, c, red);
-    if (kRest) list = block_merge(list, c, red);
-    if (CS > 1) {
-      cg::cluster_group cl = cg::this_cluster();
-      if (static_cast<int>(threadIdx.x) < CS) {
-        float* to = cl.map_shared_rank(&part[0][0], threadIdx.x);
-        to[2 * rank] = rest.ref;
-        to[2 * rank + 1] = rest.s;
-        to[2 * (kMaxCS + rank)] = list.ref;
-        to[2 * (kMaxCS + rank) + 1] = list.s;
+      rest = block_merge(rest, c, red);
+      if (CS > 1) {
+        cg::cluster_group cl = cg::this_cluster();
+        if (static_cast<int>(threadIdx.x) < CS) {
+          float* to = cl.map_shared_rank(&part[0][0], threadIdx.x);
+          to[2 * rank] = rest.ref;
+          to[2 * rank + 1] = rest.s;
+        }
+        cl.sync();  // every CTA holds every part
+        rest = Sum2{part[0][0], part[0][1]};
+        for (int q = 1; q < CS; ++q) rest = merge(rest, Sum2{part[q][0], part[q][1]}, c);
       }
-      cl.sync();  // every CTA holds every part
-      rest = Sum2{part[0][0], part[0][1]};
-      list = Sum2{part[kMaxCS][0], part[kMaxCS][1]};
-      for (int q = 1; q < CS; ++q) {
-        rest = merge(rest, Sum2{part[q][0], part[q][1]}, c);
-        list = merge(list, Sum2{part[kMaxCS + q][0], part[kMaxCS + q][1]}, c);
-      }
+      all = kRest ? merge(list, rest, c) : rest;
+      if (moving || (rest.s >= 0x1p-60f && all.s <= 0x1p100f)) break;  // the same in every CTA
+      if (CS > 1) cg::this_cluster().sync();  // the parts are read
     }
-    all = kRest ? merge(list, rest, c) : rest;
     if (rank == 0 && threadIdx.x == 0) {
-      const float kl = divergence<kRest>(E, W, er, ur, ref, list, rest, all, c);
+      const float kl = divergence<kRest>(T, ref, list, rest, all, c);
       const bool ok = all.s > 0.0f && all.s < INFINITY;
       P.loss[row] = ok ? w * P.tau * P.tau * (kl * kLn2) : NAN;
       if (kMode == kForward && P.stats) {
@@ -467,8 +522,8 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
 
   // ---- the gradient -------------------------------------------------------------------
   if (kMode != kForward) {
-    const float invE = 1.0f / (E + er);
-    const Factors F(scale, er, invE, all, rest, c);
+    const float invE = 1.0f / (T.E + T.er);
+    const Factors F(scale, T.er, invE, all, rest, c);
     const RowView<kBF16> o(P.grad, row * P.ld_grad, V);
     unsigned char* obase = const_cast<unsigned char*>(o.base);
     const float rc = all.ref * c;
@@ -502,10 +557,10 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
         put_grad<kBF16>(obase, v, F.outside(x.at(v), all, rest, c));
     }
     // the list's tokens in this CTA's part, over what the pass above wrote
-    const bool dup = __syncthreads_or(twice);
+    __syncthreads();
     const int v0 = rank == 0 ? 0 : x.head + g0 * G, v1 = rank == CS - 1 ? V : x.head + g1 * G;
     put_listed<kBF16>([&](int32_t id) { return id >= v0 && id < v1 ? obase : nullptr; }, dup, K, s_id, s_e, s_v,
-                      (ref - all.ref) * c, F.A, scale * invE);
+                      F.A * ex2((ref - all.ref) * c), scale * invE);
   }
 }
 
@@ -635,20 +690,20 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
     if (warp * 32 < K) {
       for (int k = threadIdx.x; k < K; k += kNT) {
         const int32_t id = s_id[k];
-        float e = 0.0f, v = 0.0f;
+        float e = 0.0f, q = 0.0f;
         if (id >= 0) {
-          const float u = (s_e[k] - tref) * c;
-          v = (s_v[k] - ref) * c;
-          e = ex2(u);
+          const float t = s_e[k], sv = s_v[k];
+          e = mass(t, tref, c, P.c_lo);
+          q = mass(sv, ref, c, P.c_lo);
           E += e;
-          if (e != 0.0f) W += e * (u - v);
+          if (e != 0.0f) W += e * (((t - tref) - (sv - ref)) * c);
           bool first = true;  // a token of several slots counts once
           if (dup)
             for (int j = 0; j < k; ++j) first = first && s_id[j] != id;
-          if (first) S += ex2(v);
+          if (first) S += q;
         }
         s_e[k] = e;
-        s_v[k] = v;
+        s_v[k] = q;
       }
       E = warp_sum(E);
       W = warp_sum(W);
@@ -702,14 +757,16 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
     return warp_sum(t);
   };
   exchange(warp_sum(s_rest));
-  float E = 0.0f, W = 0.0f, S = 0.0f;
+  Teacher T = {};
+  float S = 0.0f;
 #pragma unroll
   for (int i = 0; i < kNW; ++i) {
     const float4 t = teacher[i];
-    E += t.x;
-    W += t.y;
+    T.E += t.x;
+    T.W += t.y;
     S += t.z;
   }
+  T.rest<kRest>(r, tref, c, P.c_lo);
   const Sum2 list{ref, kRest ? S : 0.0f};
   Sum2 rest{ref, part_sum()};
   Sum2 all{ref, rest.s + list.s};
@@ -751,12 +808,10 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
     all = kRest ? merge(list, rest, c) : rest;
     if (nan) all.s = NAN;
   }
-  const float ur = (r * P.tau - tref) * c;
-  const float er = kRest ? ex2(ur) : 0.0f;  // the rest class (0 when there is none)
   // ---- the gradient ------------------------------------------------------------------------------
   // In place in shared memory, the list's tokens last, and out with one copy.
-  const float invE = 1.0f / (E + er);
-  const Factors F(scale, er, invE, all, rest, c);
+  const float invE = 1.0f / (T.E + T.er);
+  const Factors F(scale, T.er, invE, all, rest, c);
   const RowView<kBF16> o(P.grad, row * P.ld_grad, V);
   unsigned char* obase = const_cast<unsigned char*>(o.base);
   unsigned char* inside = obase;  // where element id of this CTA's vectors goes
@@ -787,7 +842,7 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
         if (id >= v0 && id < v1) return inside;
         return (rank == 0 && id < x.head) || (rank == CS - 1 && id >= v1) ? obase : nullptr;
       },
-      dup, K, s_id, s_e, s_v, (ref - all.ref) * c, F.A, scale * invE);
+      dup, K, s_id, s_e, s_v, F.A * ex2((ref - all.ref) * c), scale * invE);
   if (inside != obase) {
     publish_to_copies();
     __syncthreads();
@@ -795,7 +850,7 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
       copy_out(const_cast<uint4*>(o.vec) + g0, smem, static_cast<uint32_t>(g1 - g0) * 16u);
   }
   if (rank == 0 && threadIdx.x == kNT - 1) {
-    const float kl = divergence<kRest>(E, W, er, ur, ref, list, rest, all, c);
+    const float kl = divergence<kRest>(T, ref, list, rest, all, c);
     const bool ok = all.s > 0.0f && all.s < INFINITY;
     P.loss[row] = ok ? w * P.tau * P.tau * (kl * kLn2) : NAN;
   }
@@ -835,7 +890,7 @@ static kps_status launch_t(const Params& P, cudaStream_t stream) {
   int cs = 1;
   const int64_t round = static_cast<int64_t>(kNT) * kU * (kBF16 ? 8 : 4);
   while (cs < kMaxCS && P.N * cs * 2 <= 2 * sms && P.V >= 2 * cs * round) cs *= 2;
-  const Layout lay = make_layout(P.K, (P.V + cs - 1) / cs + 4 * (kBF16 ? 8 : 4), kMode != kForward, kRest);
+  const Layout lay = make_layout(P.K, (P.V + cs - 1) / cs + 4 * (kBF16 ? 8 : 4), kMode != kForward || kRest, kRest);
   static std::atomic<bool> done[kMaxDevices];
   if (!allow_shared(distill_kernel<kBF16, kRest, kMode>, done)) {
     (void)cudaGetLastError();
@@ -945,7 +1000,9 @@ static kps_status check(const void* student, kps_dtype dt, int64_t N, int64_t V,
   P->rest = rest;
   P->weight = weight;
   P->tau = temperature;
-  P->c = stream::kLog2e / temperature;
+  const double c = 1.4426950408889634074 / static_cast<double>(temperature);
+  P->c = static_cast<float>(c);
+  P->c_lo = static_cast<float>(c - static_cast<double>(P->c));
   return KPS_OK;
 }
 
