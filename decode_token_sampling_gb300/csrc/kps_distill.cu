@@ -36,7 +36,14 @@ using namespace stream;
 
 constexpr int kNT = 256;  // threads per CTA
 constexpr int kNW = kNT / 32;
-constexpr int kU = 4;         // 16-byte loads each thread keeps in flight
+// 16-byte loads each thread keeps in flight, and the CTAs an SM then holds.  The forward with eight
+// and four took 153 us for 4096 rows of 151936 bf16 (a quarter masked) and 44.2 us for 1024 of
+// 128256, with six and five 152 and 50.2 us, with four and five 154 and 48.4 us; the backward of the
+// latter with six and five 86.2 us, with eight and four 88.1 us, with four and five 92.5 us.
+template <int kMode>
+struct Flight {
+  static constexpr int loads = kMode == 0 ? 8 : 6, ctas = kMode == 0 ? 4 : 5;
+};
 constexpr int kMaxK = 1024;   // teacher slots a row may have (the framework's top-k limit)
 constexpr int64_t kMaxV = 1 << 20;
 constexpr int kMaxCS = 8;     // widest cluster (the portable limit)
@@ -90,33 +97,7 @@ __device__ __forceinline__ float teacher_value(const Params& P, int64_t i) {
                        : static_cast<const float*>(P.values)[i];
 }
 
-// Block reductions over kNT threads; every thread gets the result.
-__device__ __forceinline__ void block_max2(float& a, float& b, float (*red)[2]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  a = warp_max(a);
-  b = warp_max(b);
-  __syncthreads();
-  if (lane == 0) {
-    red[warp][0] = a;
-    red[warp][1] = b;
-  }
-  __syncthreads();
-  a = warp_max(red[lane & (kNW - 1)][0]);
-  b = warp_max(red[lane & (kNW - 1)][1]);
-}
-__device__ __forceinline__ void block_sum2(float& a, float& b, float (*red)[2]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  a = warp_sum(a);
-  b = warp_sum(b);
-  __syncthreads();
-  if (lane == 0) {
-    red[warp][0] = a;
-    red[warp][1] = b;
-  }
-  __syncthreads();
-  a = warp_sum(lane < kNW ? red[lane][0] : 0.0f);
-  b = warp_sum(lane < kNW ? red[lane][1] : 0.0f);
-}
+// The block's sum; every thread gets it.
 __device__ __forceinline__ Sum2 block_merge(Sum2 v, float c, float (*red)[2]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   v = warp_merge(v, c);
@@ -167,11 +148,41 @@ __device__ __forceinline__ float mass(float x, float ref, float c, float c_lo) {
   return ex2_two(z, fabsf(z) < 1e30f ? rest : 0.0f);
 }
 
+// A sum as two floats: h + l.
+struct F2 {
+  float h, l;
+  __device__ __forceinline__ void add(float x) {
+    const float t = h + x, b = t - h;
+    const float e = (h - (t - b)) + (x - b);
+    h = t;
+    l += fabsf(t) < INFINITY ? e : 0.0f;
+  }
+  __device__ __forceinline__ void add(const F2& o) {
+    add(o.h);
+    l += o.l;
+  }
+  __device__ __forceinline__ float value() const { return h + l; }
+};
+__device__ __forceinline__ F2 warp_sum_two(F2 v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v.add(F2{__shfl_xor_sync(0xffffffffu, v.h, o), __shfl_xor_sync(0xffffffffu, v.l, o)});
+  return v;
+}
+// log2((a + b) / (c + d)) without the roundings of the sums and the quotient.
+__device__ __forceinline__ float log2_ratio(F2 a, float b, F2 c, float d) {
+  a.add(b);
+  c.add(d);
+  const float q = a.h / c.h;
+  if (!(q > 0.0f && q < INFINITY)) return log2f(q);
+  return log2f(q) + kLog2e * ((fmaf(-q, c.h, a.h) + a.l) / a.h - c.l / c.h);
+}
+
 // The teacher's side of a row against the reference tref: E = sum e_k, W = sum e_k (u_k - v_k), with
 // e_k = 2^(u_k), u_k and v_k the exponents of the teacher's value and the student's logit; the
 // rest's e_r = 2^(uh + ul).
 struct Teacher {
-  float E, W, er, uh, ul;
+  F2 E, W;
+  float er, uh, ul;
   template <bool kRest>
   __device__ __forceinline__ void rest(float r, float tref, float c, float c_lo) {
     er = uh = ul = 0.0f;
@@ -184,24 +195,29 @@ struct Teacher {
   }
 };
 
-// The divergence in base 2.  list, rest, all: the student's sums.
+// The divergence in base 2.  list (against ref), rest, all: the student's sums.
 template <bool kRest>
-__device__ __forceinline__ float divergence(const Teacher& t, float ref, const Sum2& list, const Sum2& rest,
+__device__ __forceinline__ float divergence(const Teacher& t, float ref, const F2& list, const Sum2& rest,
                                             const Sum2& all, float c) {
-  const float moved = (all.ref - ref) * c;
-  if (!kRest || t.er == 0.0f) return t.W / t.E + log2f(all.s / t.E) + moved;
+  const float moved = (all.ref - ref) * c, E = t.E.value(), W = t.W.value();
+  // (list and rest against one reference: their sum as two floats)
+  const bool same = kRest && rest.ref == ref;
+  const F2 head = same ? list : F2{all.s, 0.0f};
+  const float tail = same ? rest.s : 0.0f;
+  if (!kRest || t.er == 0.0f) return W / E + log2_ratio(head, tail, t.E, 0.0f) + moved;
   if (rest.s == 0.0f) return INFINITY;  // the teacher's rest has mass, the student's none
-  const float Et = t.E + t.er, pr = t.er / Et;
+  const float Et = E + t.er, pr = t.er / Et;
   // D = (uh + ul) - log2 of the student's rest against ref, whole powers of two first
   const uint32_t bits = __float_as_uint(rest.s);
   const float k = static_cast<float>(static_cast<int>(bits >> 23) - 127);
   const float m = __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u);
   const float D = ((t.uh - k) + t.ul) - log2f(m) - (rest.ref - ref) * c;
-  if (!(pr >= 0.5f)) return (t.W + t.er * D) / Et + log2f(all.s / Et) + moved;
+  if (!(pr >= 0.5f)) return (W + t.er * D) / Et + log2_ratio(head, tail, t.E, t.er) + moved;
   // most mass is the rest's: ln p_r and ln q_r from what they leave, so that two numbers near
   // zero are not differences of large ones
-  const float q = list.s > 0.0f ? log2_1p_ex2(log2f(list.s / rest.s) + (list.ref - rest.ref) * c) : 0.0f;
-  return t.W / Et - t.E / Et * D - kLog2e * log1pf(t.E / t.er) + q;
+  const float S = list.value();
+  const float q = S > 0.0f ? log2_1p_ex2(log2f(S / rest.s) + (ref - rest.ref) * c) : 0.0f;
+  return W / Et - E / Et * D - kLog2e * log1pf(E / t.er) + q;
 }
 
 // Writes zeros to this CTA's part of a row of the gradient.
@@ -250,6 +266,117 @@ __device__ __forceinline__ bool has_token(const int32_t* hash, int size, int32_t
   for (int i = 0; i < size && hash[h] != -1; ++i, h = (h + 1) & (size - 1))
     if (hash[h] == id) return true;
   return false;
+}
+
+// Keys of floats that order as they do, for maxima by integer atomics (NaN excluded).
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
+// ---- the teacher's slots of a row ---------------------------------------------------------------
+struct Slot {
+  int32_t id;
+  float t;
+};
+__device__ __forceinline__ Slot read_slot(const Params& P, int64_t row, int k) {
+  return Slot{P.ids[row * P.K + k], teacher_value(P, row * P.K + k)};
+}
+__device__ __forceinline__ Slot first_slot(const Params& P, int64_t row) {
+  return static_cast<int>(threadIdx.x) < P.K ? read_slot(P, row, threadIdx.x) : Slot{-1, -INFINITY};
+}
+// Slots k = threadIdx.x, + kNT, ... (the first of them already loaded): ids (-1: empty), the
+// teacher's values and the student's logits to shared memory, the distinct tokens to the table, the
+// keys of both largest values to top[], flags[0] set where a slot is filled and flags[1] where a
+// token has two; visit(k, id) for the filled ones.  Warps without slots do nothing.
+template <bool kDistinct, class View, class Visit>
+__device__ __forceinline__ void read_slots(const Params& P, int64_t row, const View& x, Slot slot, int32_t* s_id, float* s_e,
+                                           float* s_v, int32_t* s_hash, int hash_size, uint32_t* top, int* flags,
+                                           Visit&& visit) {
+  const int K = P.K;
+  if (static_cast<int>(threadIdx.x & ~31u) >= K) return;
+  uint32_t tk = 0, sk = 0;
+  for (int k = threadIdx.x; k < K;) {
+    const int32_t id = slot.id < 0 || slot.id >= P.V || slot.t == -INFINITY ? -1 : slot.id;
+    const float s = id >= 0 ? x.at(id) : 0.0f;
+    s_id[k] = id;
+    s_e[k] = slot.t;
+    s_v[k] = s;
+    if (id >= 0) {
+      flags[0] = 1;
+      if (!isnan(slot.t)) tk = max(tk, order_key(slot.t));
+      if (!isnan(s)) sk = max(sk, order_key(s));
+      if (kDistinct && insert_token(s_hash, hash_size, id)) flags[1] = 1;
+      visit(k, id);
+    }
+    k += kNT;
+    if (k < K) slot = read_slot(P, row, k);
+  }
+  __syncwarp();
+  tk = __reduce_max_sync(0xffffffffu, tk);
+  sk = __reduce_max_sync(0xffffffffu, sk);
+  if ((threadIdx.x & 31) == 0) {
+    atomicMax(&top[0], tk);
+    atomicMax(&top[1], sk);
+  }
+}
+// The references: the teacher's largest class (its rest in nats at tau included), and the largest
+// student logit among the list's tokens.
+__device__ __forceinline__ float teacher_ref(const uint32_t* top, float r, float tau) {
+  return clamp_ref(fmaxf(top[0] ? order_value(top[0]) : -INFINITY, r * tau));
+}
+__device__ __forceinline__ float student_ref(const uint32_t* top) {
+  return clamp_ref(top[1] ? order_value(top[1]) : -INFINITY);
+}
+// The slots' masses in the place of their values, and each warp's part of E, W and the student's sum
+// over the list (its distinct tokens).
+__device__ __forceinline__ void slot_masses(const Params& P, int K, float tref, float ref, bool dup, const int32_t* s_id,
+                                            float* s_e, float* s_v, F2 (*sums)[3]) {
+  if (static_cast<int>(threadIdx.x & ~31u) >= K) return;
+  F2 E = {}, W = {}, S = {};
+  for (int k = threadIdx.x; k < K; k += kNT) {
+    const int32_t id = s_id[k];
+    float e = 0.0f, q = 0.0f;
+    if (id >= 0) {
+      const float t = s_e[k], sv = s_v[k];
+      e = mass(t, tref, P.c, P.c_lo);
+      q = mass(sv, ref, P.c, P.c_lo);
+      E.add(e);
+      if (e != 0.0f) W.add(e * (((t - tref) - (sv - ref)) * P.c));  // NaN stays (e is NaN then)
+      bool first = true;  // a token of several slots counts once
+      if (dup)
+        for (int j = 0; j < k; ++j) first = first && s_id[j] != id;
+      if (first) S.add(q);
+    }
+    s_e[k] = e;
+    s_v[k] = q;
+  }
+  __syncwarp();
+  E = warp_sum_two(E);
+  W = warp_sum_two(W);
+  S = warp_sum_two(S);
+  if ((threadIdx.x & 31) == 0) {
+    F2* to = sums[threadIdx.x >> 5];
+    to[0] = E;
+    to[1] = W;
+    to[2] = S;
+  }
+}
+// All of that, after a barrier; returns the student's sum over the list.
+template <bool kRest>
+__device__ __forceinline__ F2 collect(const F2 (*sums)[3], int K, float r, float tref, float c, float c_lo, Teacher& T) {
+  T = Teacher{};
+  F2 S = {};
+  for (int i = 0; i < kNW && i * 32 < K; ++i) {
+    T.E.add(sums[i][0]);
+    T.W.add(sums[i][1]);
+    S.add(sums[i][2]);
+  }
+  T.rest<kRest>(r, tref, c, c_lo);
+  return S;
 }
 
 // The gradient's factors: d_v = A 2^((s_v - all.ref) c) - p_v for a token of the list, less
@@ -320,12 +447,38 @@ __device__ __forceinline__ void put_listed(Place&& place, bool dup, int K, const
   }
 }
 
+// The list's tokens among the elements of a CTA's i-th vector (its bitmap starts one vector early).
+template <bool kBF16>
+__device__ __forceinline__ uint32_t listed_bits(const unsigned char* bytes, int i, bool in) {
+  const int b = (i + 1) * (kBF16 ? 8 : 4);
+  const uint32_t m = in ? bytes[b >> 3] : 0u;
+  return kBF16 ? m : (m >> (b & 4)) & 15u;
+}
+// The thread's sum over vectors [g0, g1) of a row, without the list's tokens, and one logit more,
+// with a reference that moves up: for rows whose list lies far from everything else.
+template <bool kBF16, bool kRest>
+__device__ __noinline__ Sum2 moving_sum(const RowView<kBF16>& x, int g0, int g1, const unsigned char* bytes, float one, float c) {
+  Sum2 sum{-FLT_MAX, 0.0f};
+  for (int g = g0 + static_cast<int>(threadIdx.x); g < g1; g += kNT) {
+    uint4 v = ld_stream(x.vec + g);
+    if (kRest) drop_listed<kBF16>(v, listed_bits<kBF16>(bytes, g - g0, true));
+    const float m = vec_max<kBF16>(v);
+    if ((m - sum.ref) * c > kRaise) sum.raise(clamp_ref(m), c);
+    add_vec<kBF16>(sum, v, c);
+  }
+  add_one(sum, one, c);
+  return sum;
+}
+
 template <bool kBF16, bool kRest, int kMode>
-__global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
-  constexpr int G = kBF16 ? 8 : 4;
+__global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const Params P) {
+  constexpr int G = kBF16 ? 8 : 4, kU = Flight<kMode>::loads;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float red[kNW][2];
   __shared__ float part[kMaxCS][2];  // the partial sums of the cluster's CTAs
+  __shared__ F2 sums[kNW][3];        // per warp: E, W and the student's sum over the list
+  __shared__ uint32_t top[2];
+  __shared__ int flags[2];
   constexpr bool kDistinct = kMode != kForward || kRest;  // the list's distinct tokens are needed
   const int CS = static_cast<int>(cg::this_cluster().num_blocks());
   const int rank = static_cast<int>(cg::this_cluster().block_rank());
@@ -350,147 +503,93 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
   const int bit0 = x.head + g0 * G - G;
   const int nbits = (g1 - g0 + 3) * G;
 
+  // ---- the teacher's slots ------------------------------------------------------------
+  if (threadIdx.x < 2) {
+    top[threadIdx.x] = 0u;
+    flags[threadIdx.x] = 0;
+  }
+  if (kRest && kMode != kBackward)
+    for (int i = threadIdx.x; i < (nbits + 31) / 32; i += kNT) s_bits[i] = 0u;
+  if (kDistinct)
+    for (int i = threadIdx.x; i < lay.hash_size; i += kNT) s_hash[i] = -1;
+  // (the slots of a row of weight 0 are read all the same: their loads need not wait for the weight's)
+  Slot slot = first_slot(P, row);
   const float w = P.weight ? P.weight[row] : 1.0f;
+  const float r = kRest ? P.rest[row] : -INFINITY;
   float scale = w;  // of the gradient
   if (kMode != kForward && P.upstream) scale *= P.upstream[row];
   scale *= P.tau;
-
-  // ---- the teacher's slots ------------------------------------------------------------
-  float tmax = -INFINITY, smax = -INFINITY;
-  bool any = false;
-  if (w != 0.0f) {
-    if (kRest && kMode != kBackward)
-      for (int i = threadIdx.x; i < (nbits + 31) / 32; i += kNT) s_bits[i] = 0u;
-    if (kDistinct)
-      for (int i = threadIdx.x; i < lay.hash_size; i += kNT) s_hash[i] = -1;
-    for (int k = threadIdx.x; k < K; k += kNT) {
-      int32_t id = P.ids[row * K + k];
-      const float t = teacher_value(P, row * K + k);
-      float s = 0.0f;
-      if (id < 0 || id >= V || t == -INFINITY) {
-        id = -1;
-      } else {
-        s = x.at(id);
-        any = true;
-        tmax = fmaxf(tmax, t);
-        smax = fmaxf(smax, s);
-      }
-      s_id[k] = id;
-      s_e[k] = t;
-      s_v[k] = s;
-    }
-  }
-  any = __syncthreads_or(any);
+  __syncthreads();
+  if (w != 0.0f)
+    read_slots<kDistinct>(P, row, x, slot, s_id, s_e, s_v, s_hash, lay.hash_size, top, flags, [&](int, int32_t id) {
+      const int b = id - bit0;
+      if (kRest && kMode != kBackward && b >= 0 && b < nbits) atomicOr(&s_bits[b >> 5], 1u << (b & 31));
+    });
+  __syncthreads();
   if (kShare && CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  const bool dead = !any || (kMode == kBackward && scale == 0.0f);
-  if (dead) {  // no loss: zeros, and the student's row is not looked at (the same in every CTA of the row)
+  if (!flags[0] || (kMode == kBackward && scale == 0.0f)) {
+    // no loss: zeros, and the student's row is not looked at (the same in every CTA of the row)
     if (rank == 0 && threadIdx.x == 0) {
       if (kMode != kBackward) P.loss[row] = 0.0f;
       if (kMode == kForward && P.stats)
         for (int i = 0; i < kStats; ++i) P.stats[row * kStats + i] = 0.0f;
     }
-    if (kMode != kForward) {
-      zero_row<kBF16>(P.grad, row * P.ld_grad, V, rank, CS);
-    }
+    if (kMode != kForward) zero_row<kBF16>(P.grad, row * P.ld_grad, V, rank, CS);
     return;
   }
-  block_max2(tmax, smax, red);
-  // the teacher's reference: its largest class, the rest (in nats at tau) included
-  const float r = kRest ? P.rest[row] : -INFINITY;
-  const float tref = clamp_ref(fmaxf(tmax, r * P.tau));
+  const bool dup = flags[1] != 0;
   // the student's sums: over the whole row, and over the tokens outside the list
   Sum2 all, rest;
   if (kMode == kBackward) {
     all = Sum2{P.stats[row * kStats], P.stats[row * kStats + 1]};
     rest = Sum2{P.stats[row * kStats + 2], P.stats[row * kStats + 3]};
   }
-  const float ref = kMode == kBackward ? all.ref : clamp_ref(smax);
-  bool twice = false;
-  if (kDistinct) {
-    for (int k = threadIdx.x; k < K; k += kNT) {
-      const int32_t id = s_id[k];
-      if (id < 0) continue;
-      twice |= insert_token(s_hash, lay.hash_size, id);
-      const int b = id - bit0;
-      if (kRest && kMode != kBackward && b >= 0 && b < nbits) atomicOr(&s_bits[b >> 5], 1u << (b & 31));
-    }
-  }
-  const bool dup = kDistinct && __syncthreads_or(twice);
-  Teacher T = {};
-  float S = 0.0f;  // the student's sum over the list
-  for (int k = threadIdx.x; k < K; k += kNT) {
-    const int32_t id = s_id[k];
-    float e = 0.0f, q = 0.0f;
-    if (id >= 0) {
-      const float t = s_e[k], sv = s_v[k];
-      e = mass(t, tref, c, P.c_lo);
-      q = mass(sv, ref, c, P.c_lo);
-      T.E += e;
-      if (e != 0.0f) T.W += e * (((t - tref) - (sv - ref)) * c);  // NaN stays (e is NaN then)
-      bool first = true;  // a token of several slots counts once
-      if (dup)
-        for (int j = 0; j < k; ++j) first = first && s_id[j] != id;
-      if (first) S += q;
-    }
-    s_e[k] = e;
-    s_v[k] = q;
-  }
-  block_sum2(T.E, T.W, red);  // its barriers also publish the bitmap and the slots
-  if (kRest && kMode != kBackward) {
-    float unused = 0.0f;
-    block_sum2(S, unused, red);
-  }
-  T.rest<kRest>(r, tref, c, P.c_lo);
+  const float tref = teacher_ref(top, r, P.tau);
+  const float ref = kMode == kBackward ? all.ref : student_ref(top);
+  slot_masses(P, K, tref, ref, dup, s_id, s_e, s_v, sums);  // read after the barriers below
 
   // ---- the student's sum outside the list (kRest; of the whole row else) ----------------------
   // Against the list's largest logit, one reference for the whole row and near its top.  A sum that
   // leaves fp32's range (the list far from everything else) is taken again with moving references.
   if (kMode != kBackward) {
     const unsigned char* bytes = reinterpret_cast<const unsigned char*>(s_bits);
-    const Sum2 list{ref, kRest ? S : 0.0f};
-    for (bool moving = !(fabsf(ref * c) <= kFastRef);; moving = true) {
-      FastSum<kBF16> fast(moving ? 0.0f : ref, c);
-      rest = Sum2{-FLT_MAX, 0.0f};
-      for (int base = g0; base < g1; base += kNT * kU) {
-        uint4 v[kU];
+    // the element outside the vectors that is this thread's, if any: the head's with rank 0, the
+    // tail's with the last rank
+    const bool loose = static_cast<int>(threadIdx.x) < x.loose() &&
+                       ((x.loose_at(threadIdx.x) < x.head) ? rank == 0 : rank == CS - 1);
+    const int lv = loose ? x.loose_at(threadIdx.x) : 0;
+    const bool loose_out = loose && !(kRest && ((s_bits[(lv - bit0) >> 5] >> ((lv - bit0) & 31)) & 1u));
+    FastSum<kBF16> fast(fabsf(ref * c) <= kFastRef ? ref : 0.0f, c);
+    for (int base = g0; base < g1; base += kNT * kU) {
+      uint4 v[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int g = base + u * kNT + static_cast<int>(threadIdx.x);
+        v[u] = g < g1 ? ld_stream(x.vec + g) : neg_inf_vec<kBF16>();
+      }
+      if (kRest) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const int g = base + u * kNT + static_cast<int>(threadIdx.x);
-          v[u] = g < g1 ? ld_stream(x.vec + g) : neg_inf_vec<kBF16>();
-        }
-        if (kRest) {
-#pragma unroll
-          for (int u = 0; u < kU; ++u) {
-            const int g = base + u * kNT + static_cast<int>(threadIdx.x);
-            const int b = (g - g0 + 1) * G;
-            uint32_t m = g < g1 ? bytes[b >> 3] : 0u;
-            if (!kBF16) m = (m >> (b & 4)) & 15u;
-            if (m) drop_listed<kBF16>(v[u], m);
-          }
-        }
-        if (!moving) {
-#pragma unroll
-          for (int u = 0; u < kU; ++u) fast.add(v[u]);
-        } else {
-          float m = vec_max<kBF16>(v[0]);
-#pragma unroll
-          for (int u = 1; u < kU; ++u) m = fmaxf(m, vec_max<kBF16>(v[u]));
-          if ((m - rest.ref) * c > kRaise) rest.raise(clamp_ref(m), c);
-#pragma unroll
-          for (int u = 0; u < kU; ++u) add_vec<kBF16>(rest, v[u], c);
+          const uint32_t m = listed_bits<kBF16>(bytes, g - g0, g < g1);
+          if (m) drop_listed<kBF16>(v[u], m);
         }
       }
-      if (!moving) rest = Sum2{ref, fast.total(ref, c)};
-      // the elements outside the vectors: the head with rank 0, the tail with the last rank
-      if (static_cast<int>(threadIdx.x) < x.loose()) {
-        const int v = x.loose_at(threadIdx.x);
-        if ((v < x.head) ? rank == 0 : rank == CS - 1) {
-          const int b = v - bit0;
-          const bool in = kRest && ((s_bits[b >> 5] >> (b & 31)) & 1u);
-          if (!in) add_one(rest, x.at(v), c);
-        }
-      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) fast.add(v[u]);
+    }
+    rest = Sum2{ref, fast.total(ref, c)};
+    if (loose_out) add_one(rest, x.at(lv), c);
+    Teacher T;
+    F2 S;
+    Sum2 list;
+    for (bool moving = false;; moving = true) {
+      if (moving) rest = moving_sum<kBF16, kRest>(x, g0, g1, bytes, loose_out ? x.at(lv) : -INFINITY, c);
       rest = block_merge(rest, c, red);
+      if (!moving) {
+        S = collect<kRest>(sums, K, r, tref, c, P.c_lo, T);
+        list = Sum2{ref, kRest ? S.value() : 0.0f};
+      }
       if (CS > 1) {
         cg::cluster_group cl = cg::this_cluster();
         if (static_cast<int>(threadIdx.x) < CS) {
@@ -503,11 +602,12 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
         for (int q = 1; q < CS; ++q) rest = merge(rest, Sum2{part[q][0], part[q][1]}, c);
       }
       all = kRest ? merge(list, rest, c) : rest;
-      if (moving || (rest.s >= 0x1p-60f && all.s <= 0x1p100f)) break;  // the same in every CTA
+      // the same in every CTA
+      if (moving || (fabsf(ref * c) <= kFastRef && rest.s >= 0x1p-60f && all.s <= 0x1p100f)) break;
       if (CS > 1) cg::this_cluster().sync();  // the parts are read
     }
     if (rank == 0 && threadIdx.x == 0) {
-      const float kl = divergence<kRest>(T, ref, list, rest, all, c);
+      const float kl = divergence<kRest>(T, ref, S, rest, all, c);
       const bool ok = all.s > 0.0f && all.s < INFINITY;
       P.loss[row] = ok ? w * P.tau * P.tau * (kl * kLn2) : NAN;
       if (kMode == kForward && P.stats) {
@@ -518,11 +618,15 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
       }
     }
     if (kMode == kForward) return;
+  } else {
+    __syncthreads();  // the slots' masses
   }
 
   // ---- the gradient -------------------------------------------------------------------
   if (kMode != kForward) {
-    const float invE = 1.0f / (T.E + T.er);
+    Teacher T;
+    (void)collect<kRest>(sums, K, r, tref, c, P.c_lo, T);
+    const float invE = 1.0f / (T.E.value() + T.er);
     const Factors F(scale, T.er, invE, all, rest, c);
     const RowView<kBF16> o(P.grad, row * P.ld_grad, V);
     unsigned char* obase = const_cast<unsigned char*>(o.base);
@@ -576,15 +680,6 @@ __global__ void __launch_bounds__(kNT) distill_kernel(const Params P) {
 constexpr int kChunkBytes = 52 * 1024; // of a row per CTA, where the cluster allows: four CTAs an SM
 constexpr int kMaxChunkBytes = 200 * 1024;
 
-// Keys of floats that order as they do, for maxima by integer atomics (NaN excluded).
-__device__ __forceinline__ uint32_t order_key(float x) {
-  const uint32_t u = __float_as_uint(x);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float order_value(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
-}
-
 // What the host lays out for a launch: `share` vectors of a row for each CTA, and the offsets of
 // the small arrays behind them in shared memory.
 struct Resident {
@@ -597,7 +692,7 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
   constexpr int G = kBF16 ? 8 : 4;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float part[kMaxCS * kNW];  // per warp of the cluster
-  __shared__ float4 teacher[kNW];       // per warp: E, W and the student's sum over the list
+  __shared__ F2 teacher[kNW][3];        // per warp: E, W and the student's sum over the list
   __shared__ uint32_t top[2];           // keys of the largest teacher's value and student's logit in the list
   __shared__ int flags[2];              // the row has a filled slot; some token has two
   __shared__ __align__(8) unsigned long long landed;  // the copy's barrier
@@ -633,46 +728,18 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
   if (kRest) s_head[threadIdx.x] = -1;
   for (int i = threadIdx.x; i < R.hash_size; i += kNT) s_hash[i] = -1;
   // (the slots of a row of weight 0 are read all the same: their loads need not wait for the weight's)
-  int32_t id = threadIdx.x < K ? P.ids[row * K + threadIdx.x] : -1;
-  float t = threadIdx.x < K ? teacher_value(P, row * K + threadIdx.x) : -INFINITY;
+  Slot slot = first_slot(P, row);
   const float w = P.weight ? P.weight[row] : 1.0f;
   const float r = kRest ? P.rest[row] : -INFINITY;
   const float scale = w * P.tau;
   __syncthreads();
   if (w != 0.0f) {
     if (threadIdx.x == 0 && g1 > g0) copy_in(smem, x.vec + g0, static_cast<uint32_t>(g1 - g0) * 16u, &landed);
-    if (warp * 32 < K) {  // (a warp's slots are its own threads')
-      uint32_t tk = 0, sk = 0;
-      for (int k = threadIdx.x; k < K;) {
-        if (id < 0 || id >= V || t == -INFINITY) id = -1;
-        const float s = id >= 0 ? x.at(id) : 0.0f;
-        s_id[k] = id;
-        s_e[k] = t;
-        s_v[k] = s;
-        if (id >= 0) {
-          flags[0] = 1;
-          if (!isnan(t)) tk = max(tk, order_key(t));
-          if (!isnan(s)) sk = max(sk, order_key(s));
-          if (insert_token(s_hash, R.hash_size, id)) flags[1] = 1;
-          if (kRest) {
-            const int at = id - x.head, vec = at / G - g0;
-            if (at >= 0 && vec >= 0 && vec < g1 - g0) s_next[k] = atomicExch(&s_head[vec & (kNT - 1)], k);
-          }
-        }
-        k += kNT;
-        if (k < K) {
-          id = P.ids[row * K + k];
-          t = teacher_value(P, row * K + k);
-        }
-      }
-      __syncwarp();
-      tk = __reduce_max_sync(0xffffffffu, tk);
-      sk = __reduce_max_sync(0xffffffffu, sk);
-      if (lane == 0) {
-        atomicMax(&top[0], tk);
-        atomicMax(&top[1], sk);
-      }
-    }
+    read_slots<true>(P, row, x, slot, s_id, s_e, s_v, s_hash, R.hash_size, top, flags, [&](int k, int32_t id) {
+      if (!kRest) return;
+      const int at = id - x.head, vec = at / G - g0;
+      if (at >= 0 && vec >= 0 && vec < g1 - g0) s_next[k] = atomicExch(&s_head[vec & (kNT - 1)], k);
+    });
   }
   __syncthreads();
   if (!flags[0]) {  // no loss: zeros (the same in every CTA of the row)
@@ -683,34 +750,8 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
     return;
   }
   const bool dup = flags[1] != 0;
-  const float tref = clamp_ref(fmaxf(top[0] ? order_value(top[0]) : -INFINITY, r * P.tau));
-  const float ref = clamp_ref(top[1] ? order_value(top[1]) : -INFINITY);  // of the student's sums too
-  {
-    float E = 0.0f, W = 0.0f, S = 0.0f;
-    if (warp * 32 < K) {
-      for (int k = threadIdx.x; k < K; k += kNT) {
-        const int32_t id = s_id[k];
-        float e = 0.0f, q = 0.0f;
-        if (id >= 0) {
-          const float t = s_e[k], sv = s_v[k];
-          e = mass(t, tref, c, P.c_lo);
-          q = mass(sv, ref, c, P.c_lo);
-          E += e;
-          if (e != 0.0f) W += e * (((t - tref) - (sv - ref)) * c);
-          bool first = true;  // a token of several slots counts once
-          if (dup)
-            for (int j = 0; j < k; ++j) first = first && s_id[j] != id;
-          if (first) S += q;
-        }
-        s_e[k] = e;
-        s_v[k] = q;
-      }
-      E = warp_sum(E);
-      W = warp_sum(W);
-      S = warp_sum(S);
-    }
-    if (lane == 0) teacher[warp] = make_float4(E, W, S, 0.0f);
-  }
+  const float tref = teacher_ref(top, r, P.tau), ref = student_ref(top);  // the latter of the student's sums too
+  slot_masses(P, K, tref, ref, dup, s_id, s_e, s_v, teacher);
 
   // ---- the student's sum outside the list -------------------------------------------------------
   // With kRest the list's tokens leave the row: each thread overwrites those in its own vectors with
@@ -757,17 +798,9 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
     return warp_sum(t);
   };
   exchange(warp_sum(s_rest));
-  Teacher T = {};
-  float S = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kNW; ++i) {
-    const float4 t = teacher[i];
-    T.E += t.x;
-    T.W += t.y;
-    S += t.z;
-  }
-  T.rest<kRest>(r, tref, c, P.c_lo);
-  const Sum2 list{ref, kRest ? S : 0.0f};
+  Teacher T;
+  const F2 S = collect<kRest>(teacher, K, r, tref, c, P.c_lo, T);
+  const Sum2 list{ref, kRest ? S.value() : 0.0f};
   Sum2 rest{ref, part_sum()};
   Sum2 all{ref, rest.s + list.s};
   // (NaN fails this too)
@@ -810,7 +843,7 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
   }
   // ---- the gradient ------------------------------------------------------------------------------
   // In place in shared memory, the list's tokens last, and out with one copy.
-  const float invE = 1.0f / (T.E + T.er);
+  const float invE = 1.0f / (T.E.value() + T.er);
   const Factors F(scale, T.er, invE, all, rest, c);
   const RowView<kBF16> o(P.grad, row * P.ld_grad, V);
   unsigned char* obase = const_cast<unsigned char*>(o.base);
@@ -850,7 +883,7 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
       copy_out(const_cast<uint4*>(o.vec) + g0, smem, static_cast<uint32_t>(g1 - g0) * 16u);
   }
   if (rank == 0 && threadIdx.x == kNT - 1) {
-    const float kl = divergence<kRest>(T, ref, list, rest, all, c);
+    const float kl = divergence<kRest>(T, ref, S, rest, all, c);
     const bool ok = all.s > 0.0f && all.s < INFINITY;
     P.loss[row] = ok ? w * P.tau * P.tau * (kl * kLn2) : NAN;
   }
@@ -886,9 +919,9 @@ template <bool kBF16, bool kRest, int kMode>
 static kps_status launch_t(const Params& P, cudaStream_t stream) {
   const int sms = sm_count();
   if (!sms) return KPS_ERR_CUDA;
-  // few rows: a cluster shares each, as wide as leaves every CTA a full round of loads
+  // few rows: a cluster shares each, as wide as leaves every thread four vectors
   int cs = 1;
-  const int64_t round = static_cast<int64_t>(kNT) * kU * (kBF16 ? 8 : 4);
+  const int64_t round = static_cast<int64_t>(kNT) * 4 * (kBF16 ? 8 : 4);
   while (cs < kMaxCS && P.N * cs * 2 <= 2 * sms && P.V >= 2 * cs * round) cs *= 2;
   const Layout lay = make_layout(P.K, (P.V + cs - 1) / cs + 4 * (kBF16 ? 8 : 4), kMode != kForward || kRest, kRest);
   static std::atomic<bool> done[kMaxDevices];
