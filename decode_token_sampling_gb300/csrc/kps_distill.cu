@@ -672,12 +672,20 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
 // The loss and the gradient with the row in shared memory
 // ------------------------------------------------------------------------------------------
 //
-// Memory bounds the pair: the row is read once, by bulk copies into the shared memory of a
-// cluster's CTAs, summed there, turned into the gradient in place and copied out.  Read
-// again from global memory it came from DRAM once more (an SM's rows in flight, times 152, are
-// more than the second-level cache holds): 495 us for 4096 rows of 151936 bf16 with a quarter
-// masked, three transfers of the matrix, whatever the number of rows in flight.
-constexpr int kChunkBytes = 52 * 1024; // of a row per CTA, where the cluster allows: four CTAs an SM
+// Memory bounds the pair: the row is read once, by a bulk copy into the shared memory of each of a
+// cluster's CTAs, summed there, turned into the gradient in place and copied out.  Read again from
+// global memory instead it came from DRAM once more (an SM's rows in flight, times 152, are more
+// than the second-level cache holds): 495 us for 4096 rows of 151936 bf16 with a quarter masked
+// (321 us at the copy rate), whatever the number of rows in flight.  What it took since: copies by
+// the threads 437 us, bulk copies 409, the cluster's sums sent with stores that count at their
+// receiver's barrier instead of a cluster barrier (whose fence waits for everything) 400, five CTAs'
+// registers 395.  1024 rows of 128256: 94 us (77 at the copy rate).  What bounds it now is the time
+// that a part of a row spends waiting: some 20000 cycles from its slots' loads to its last byte out,
+// of which memory is busy for 80%.
+//
+// Bytes of a row per CTA, where the cluster allows: four CTAs an SM.  40 KB took 415 us, 62 KB 447,
+// 78 KB 499 (fewer CTAs to fill each other's waits).
+constexpr int kChunkBytes = 52 * 1024;
 constexpr int kMaxChunkBytes = 200 * 1024;
 
 // What the host lays out for a launch: `share` vectors of a row for each CTA, and the offsets of
@@ -688,14 +696,14 @@ struct Resident {
 };
 
 template <bool kBF16, bool kRest>
-__global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, const Resident R) {
+__global__ void __launch_bounds__(kNT, 5) distill_resident_kernel(const Params P, const Resident R) {
   constexpr int G = kBF16 ? 8 : 4;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float part[kMaxCS * kNW];  // per warp of the cluster
   __shared__ F2 teacher[kNW][3];        // per warp: E, W and the student's sum over the list
   __shared__ uint32_t top[2];           // keys of the largest teacher's value and student's logit in the list
   __shared__ int flags[2];              // the row has a filled slot; some token has two
-  __shared__ __align__(8) unsigned long long landed;  // the copy's barrier
+  __shared__ __align__(8) unsigned long long landed, gathered;  // the barriers of the copy and of part[]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   cg::cluster_group cl = cg::this_cluster();
   const int CS = static_cast<int>(cl.num_blocks());
@@ -705,7 +713,14 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
   const int64_t row = cluster;
   const int V = P.V, K = P.K;
   const float c = P.c;
-  // every CTA of the cluster runs before any writes into another's shared memory
+  if (threadIdx.x == 0) {
+    copy_barrier_init(&landed);
+    copy_barrier_init(&gathered);
+    if (CS > 1) expect_bytes(&gathered, static_cast<uint32_t>(kNW * CS * sizeof(float)));
+  }
+  __syncwarp();
+  // every CTA of the cluster runs, and has set up its barriers, before any writes into another's
+  // shared memory
   if (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   const RowView<kBF16> x(P.student, row * P.ld, V);
   const int g0 = min(rank * R.share, x.nv), g1 = rank == CS - 1 ? x.nv : min(g0 + R.share, x.nv);
@@ -720,7 +735,6 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
   int32_t* s_hash = reinterpret_cast<int32_t*>(smem + R.hash);  // lie in its vectors, the others by s_next (kRest)
 
   // ---- the copy, and the teacher's slots while it is under way ------------------------------------
-  if (threadIdx.x == 0) copy_barrier_init(&landed);
   if (threadIdx.x < 2) {
     top[threadIdx.x] = 0u;
     flags[threadIdx.x] = 0;
@@ -758,7 +772,7 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
   // -inf (their logits are in s_v).  Against the list's largest student logit, one reference for
   // the whole row, so that the parts simply add up; a sum that leaves fp32's range (the list far
   // from everything else) is taken again below against its own maximum.
-  const bool late = g1 > g0 && !copy_landed(&landed);
+  bool late = g1 > g0 && !copy_landed(&landed);  // a wait ran out
   float s_rest;
   {
     FastSum<kBF16> fast(fabsf(ref * c) <= kFastRef ? ref : 0.0f, c);
@@ -797,11 +811,22 @@ __global__ void __launch_bounds__(kNT) distill_resident_kernel(const Params P, c
     if (lane + 32 < kNW * CS) t += part[lane + 32];
     return warp_sum(t);
   };
-  exchange(warp_sum(s_rest));
+  {
+    // the same with stores that count at the receiver's barrier: no fence, and no CTA waits for
+    // more than the values
+    const float a = warp_sum(s_rest);
+    if (CS > 1) {
+      if (lane < CS) send_float(&part[rank * kNW + warp], a, &gathered, lane);
+      if (!copy_landed(&gathered)) late = true;
+    } else if (lane == 0) {
+      part[warp] = a;
+    }
+    __syncthreads();  // (the slots' sums, too)
+  }
   Teacher T;
   const F2 S = collect<kRest>(teacher, K, r, tref, c, P.c_lo, T);
   const Sum2 list{ref, kRest ? S.value() : 0.0f};
-  Sum2 rest{ref, part_sum()};
+  Sum2 rest{ref, late ? NAN : part_sum()};
   Sum2 all{ref, rest.s + list.s};
   // (NaN fails this too)
   if (!(fabsf(ref * c) <= kFastRef && rest.s >= 0x1p-60f && all.s <= 0x1p100f)) {

@@ -218,11 +218,23 @@ __device__ __forceinline__ void copy_barrier_init(unsigned long long* bar) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_u32(bar)) : "memory");
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
-__device__ __forceinline__ void copy_in(void* dst, const void* src, uint32_t bytes, unsigned long long* bar) {
+__device__ __forceinline__ void expect_bytes(unsigned long long* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_u32(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_in(void* dst, const void* src, uint32_t bytes, unsigned long long* bar) {
+  expect_bytes(bar, bytes);
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                    shared_u32(dst)),
                "l"(src), "r"(bytes), "r"(shared_u32(bar))
+               : "memory");
+}
+// Stores v to *to in the shared memory of the cluster's CTA `cta`, counted at its barrier *bar.
+__device__ __forceinline__ void send_float(float* to, float v, unsigned long long* bar, int cta) {
+  uint32_t ra, rb;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(shared_u32(to)), "r"(cta));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(shared_u32(bar)), "r"(cta));
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(ra), "r"(__float_as_uint(v)),
+               "r"(rb)
                : "memory");
 }
 // Waits for the copy, for about two seconds at most; false when it has not landed by then.
