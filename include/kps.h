@@ -280,6 +280,11 @@ kps_status kps_sample_noalloc(const void* logits, kps_dtype dt, int64_t B, int64
  * element type; rows on 16-byte boundaries are read fastest, any others work.
  * Errors are as for kps_sample: KPS_ERR_INVALID_ARG, KPS_ERR_UNSUPPORTED (a
  * vocabulary or a row count too large), KPS_ERR_CUDA.
+ *
+ * The same call gives the same bits every time.  Sums of exponentials are taken
+ * in fp32 in an order that goes with the shapes, so a row's log-sum-exps, loss
+ * and gradient may differ in their last places between batches of different
+ * sizes; ids and values do not.
  */
 
 /*
@@ -299,7 +304,7 @@ kps_status kps_sample_noalloc(const void* logits, kps_dtype dt, int64_t B, int64
  *
  * temperature is finite and > 0.  A row with +inf has an lse of +inf; in a row
  * of -inf alone lse and rest are -inf.  Log-probabilities of such rows follow
- * IEEE arithmetic.  Results do not depend on the launch shape or on repetition.
+ * IEEE arithmetic.
  */
 kps_status kps_top_logits(const void* logits, kps_dtype dt, int64_t B, int64_t V, int64_t ld, int64_t n,
                           float temperature, const int64_t* tokens, int32_t* out_ids, float* out_values,
@@ -344,7 +349,8 @@ kps_status kps_top_logits(const void* logits, kps_dtype dt, int64_t B, int64_t V
  * (NULL: 1; a row of grad_loss 0 gets zeros).  kps_distill_loss_grad does both
  * in one launch, for programs that have all factors in weight.  out_grad must
  * not overlap the student's rows.  Gradients are computed in fp32 and rounded
- * once.
+ * once.  (kps_distill_loss_grad copies rows into shared memory; a copy that did
+ * not arrive within about two seconds would leave NaN in its row.)
  */
 kps_status kps_distill_forward(const void* student, kps_dtype dt, int64_t N, int64_t V, int64_t ld,
                                const int32_t* ids, const void* values, kps_dtype values_dt, int64_t K,

@@ -151,7 +151,8 @@ def _compare(got, want, tol, what):
 
 
 SIZES = [(1, 1, 1), (3, 2, 1), (2, 7, 9), (5, 31, 4), (1, 1000, 16), (37, 1000, 1), (4, 4099, 33), (2, 8195, 100),
-         (7, 32000, 64), (300, 5003, 20), (3, 50001, 1024), (1, 151936, 64), (160, 8192, 8), (2, 262144, 40)]
+         (7, 32000, 64), (300, 5003, 20), (3, 50001, 1024), (1, 151936, 64), (160, 8192, 8), (2, 262144, 40),
+         (2, 450001, 33), (1, 1 << 20, 300)]  # rows that no cluster's shared memory holds among them
 
 
 @gpu
@@ -410,6 +411,58 @@ def test_more_than_2_to_31_elements():
     _compare(grad[rows].double(), ref, gtol + half * ref.abs() + half * gtol, "grad")
     assert float(loss.double().sum()) == pytest.approx(float(loss[rows].double().sum()))
     assert bool((grad[14000] == 0).all()) and bool((grad[N - 3] == 0).all())
+
+
+@gpu
+@pytest.mark.parametrize("call", ["distill_loss_grad", "distill_forward", "top_logits"])
+def test_first_call_of_a_process_may_be_captured(call):
+    """Nothing is set up by an earlier eager call (a process of its own)."""
+    import os
+    import subprocess
+    import sys
+    code = f"""
+import torch, decode_token_sampling_gb300 as kps
+s = torch.randn(3, 9000, device="cuda"); ids = torch.arange(12, device="cuda", dtype=torch.int32).view(3, 4)
+val = torch.randn(3, 4, device="cuda"); args = (s, 200) if {call!r} == "top_logits" else (s, ids, val)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = kps.{call}(*args)
+g.replay(); torch.cuda.synchronize()
+want = kps.{call}(*args)
+torch.cuda.synchronize()
+assert all(a is b or torch.equal(a, b) for a, b in zip(out, want))
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
+
+
+@gpu
+def test_two_threads_at_once():
+    """Calls of different shapes from two host threads, each on a stream of its own."""
+    import threading
+    import decode_token_sampling_gb300 as kps
+    cases = [_case(30, 20000, 32, torch.bfloat16, "cuda", seed=20), _case(7, 151936, 300, torch.float32, "cuda", seed=21)]
+    want = [kps.distill_loss_grad(s, ids, val, rest=r) for s, ids, val, r in cases]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            s, ids, val, r = cases[i]
+            for _ in range(20):
+                got[i] = kps.distill_loss_grad(s, ids, val, rest=r, stream=stream)
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors
+    for (loss, grad), (l, g) in zip(want, got):
+        assert torch.equal(loss, l) and torch.equal(grad, g)
 
 
 @gpu

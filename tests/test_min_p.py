@@ -197,6 +197,26 @@ def test_rows_that_a_sample_misjudges(V, kernel):
 
 
 @gpu
+@pytest.mark.parametrize("kernel", [0, 1, 2])
+@pytest.mark.parametrize("V,dtype", [(262144, "bf16"), (300001, "bf16"), (262144, "f32")])
+def test_largest_rows(V, dtype, kernel):
+    """The row kernel's largest vocabulary, and one past it (the cluster kernel)."""
+    for seed, kw in ((20, dict(k_range=(0, 0))), (21, dict(k_range=(0, 0), p_range=(1.0, 1.0)))):
+        check(make_random(3, V, seed=seed, dtype=dtype, **kw), [0.02, 0.1, 0.5], kernel, most_near=0.4)
+
+
+@gpu
+@pytest.mark.parametrize("T", [1e-4, 1e-30, 1e30, 3e38])
+def test_extreme_temperatures(T):
+    """Quotients that overflow, meet or fall below the normal numbers."""
+    for kernel in POLICIES:
+        inp = make_random(64, 4096, seed=22, k_range=(0, 0), p_range=(1.0, 1.0))
+        inp.temperature[:] = T
+        inp.top_p[::2] = 0.9
+        check(inp, mixed(64, 22), kernel, most_near=1.0)
+
+
+@gpu
 @pytest.mark.parametrize("kernel", POLICIES)
 def test_border_values(kernel):
     """Elements on both sides of the border by one unit in the last place, for borders that are
