@@ -38,7 +38,10 @@ static_assert(kThreads == 512, "the block helpers of kps_sampler.cuh assume 512 
 
 constexpr int kRT = kThreads;           // threads per CTA
 constexpr int kRW = kRT / 32;
-constexpr int kRU = 4;                  // 16-byte loads each thread keeps in flight
+// 16-byte loads each thread keeps in flight.  The min-p kernels hold more state in the same 64
+// registers: with three loads 256 rows of 151936 fp32 take 108 us and with four 115, 64 rows of
+// 128256 bf16 the same 47 either way (six: 130).  Without min-p four are the faster.
+constexpr int kRU = kMinP ? 3 : 4;
 constexpr int kRCap = 6144;             // candidate / band buffer entries (u64 order words)
 constexpr int kRSeg = kRCap / kRW;      // the part of the buffer each warp appends to
 constexpr int kRKeepAllV = 4096;        // rows this short are taken whole (no sample)
