@@ -400,9 +400,10 @@ def _distill_args(student, ids, values, rest, weight, temperature):
 
 
 def _grad_like(student: torch.Tensor) -> torch.Tensor:
-    """An uninitialised gradient whose rows lie on the same 16-byte phase as the student's."""
+    """An uninitialised gradient whose rows lie on the same 16-byte phase as the student's, at the
+    least distance that allows it (the student may be every hundredth row of something larger)."""
     N, V = student.shape
-    ld = student.stride(0) if N > 1 else V
+    ld = V + (student.stride(0) - V) % (16 // student.element_size()) if N > 1 else V
     grad = torch.empty((N, ld), dtype=student.dtype, device=student.device)
     return grad if ld == V else grad[:, :V]
 

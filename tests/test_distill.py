@@ -481,3 +481,17 @@ def test_binding_refusals():
     with pytest.raises(kps.KpsError):
         kps.distill_loss(s, ids, val, temperature=0.0)
     assert kps.distill_loss(s[:0], ids[:0], val[:0]).shape == (0,)
+
+
+@gpu
+def test_gradient_of_rows_far_apart():
+    """One row out of every 64 of a batch (the last position of each sequence): a gradient of the rows' own size."""
+    import decode_token_sampling_gb300 as kps
+    N, V = 6, 1003
+    s, ids, val, r = _case(N, V, 12, torch.float32, "cuda", seed=9)
+    buf = torch.zeros(N, 64, V, device="cuda")
+    view = buf[:, -1]
+    view.copy_(s)
+    check(view, ids, val, 1.0, r)
+    _, grad = kps.distill_loss_grad(view, ids, val, rest=r)
+    assert grad.untyped_storage().nbytes() <= N * (V + 3) * 4
