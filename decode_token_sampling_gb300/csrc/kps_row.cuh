@@ -39,8 +39,8 @@ static_assert(kThreads == 512, "the block helpers of kps_sampler.cuh assume 512 
 constexpr int kRT = kThreads;           // threads per CTA
 constexpr int kRW = kRT / 32;
 // 16-byte loads each thread keeps in flight.  The min-p kernels hold more state in the same 64
-// registers: with three loads 256 rows of 151936 fp32 take 108 us and with four 115, 64 rows of
-// 128256 bf16 the same 47 either way (six: 130).  Without min-p four are the faster.
+// registers: with three loads 256 rows of 151936 fp32 with a penalty take 100 us and with four 118, 64 rows of
+// 128256 bf16 the same 48 either way.  Without min-p four are the faster.
 constexpr int kRU = kMinP ? 3 : 4;
 constexpr int kRCap = 6144;             // candidate / band buffer entries (u64 order words)
 constexpr int kRSeg = kRCap / kRW;      // the part of the buffer each warp appends to
@@ -1605,14 +1605,44 @@ __device__ __noinline__ int32_t rm_row(const RowCtx& rc, const RowSmem& sm, cons
   if (!rk_gather_team(sm, tm)) return -1;
   if (topp_on) below = tm.sum_of(sm.misc, 1);
   bool over = false;
+  uint32_t n = 0, at = 0;  // what is listed, and where this warp's part of it goes
 #pragma unroll
-  for (int w = 0; w < kRW; ++w) over |= segcnt[w] > static_cast<uint32_t>(kRSeg);
-  unsigned long long top;
-  uint32_t mn;
-  const uint32_t n = rk_normalize(sm.cw, segcnt, 0u, rc.div, rc.identity, sm.red, &top, &mn);
+  for (int w = 0; w < kRW; ++w) {
+    over |= segcnt[w] > static_cast<uint32_t>(kRSeg);
+    at += w < warp ? segcnt[w] : 0u;
+    n += segcnt[w];
+  }
   // a list overflowed, or nothing has a distance to the maximum: the exact selection
   if (over || n == 0u || isinf(M)) return rexact_min_p_row<kBF16>(whole, sm, topp_on, p, mp, eps);
-  Thresh th = with_min_p(kKeepAll, *reinterpret_cast<const float2*>(sm.misc + kMLnMinP), M);
+  const float2 ln_mp = *reinterpret_cast<const float2*>(sm.misc + kMLnMinP);
+  unsigned long long rb = 0, first = 0;
+  if (n <= static_cast<uint32_t>(kTopKMax)) {
+    // all of it fits the survivors' place: divided by T on the way there.  What lies between the
+    // raw bound and the cut takes part in top-p, and the cut is raised to min-p's behind it.
+    unsigned long long S = 0;
+    for (uint32_t i = lane; i < segcnt[warp]; i += 32) {
+      const unsigned long long r = sm.cw[warp * kRSeg + i];
+      const float x = kfloat(static_cast<uint32_t>(r >> 32));
+      const float y = __fadd_rn(rc.identity ? x : rdiv(x, rc.div), 0.0f);
+      sm.wbuf[at + i] = (static_cast<unsigned long long>(fkey(y)) << 32) | (r & 0xFFFFFFFFull);
+      if (topp_on) S += fixed_mass(softmax_weight(y, M));
+    }
+    Thresh th = kKeepAll;
+    if (topp_on) {
+      S = rblock_sum_u64(S, sm.red) + below;
+      if (threadIdx.x == 0) sm.misc[kMRowMass] = S;  // published by the barriers of rk_topp
+      th = rk_topp<true>(sm.wbuf, static_cast<int>(n), M, p, sm.hist, sm.cw, sm.red, sm.misc);
+    } else {
+      __syncthreads();
+    }
+    rlist_race(sm.wbuf, static_cast<int>(n), with_min_p(th, ln_mp, M), M, rc, eps, rb, first);
+    rblock_max2(rb, first, sm.red);
+    return static_cast<int32_t>(~static_cast<uint32_t>(rb ? rb : first));
+  }
+  unsigned long long top;
+  uint32_t mn;
+  (void)rk_normalize(sm.cw, segcnt, 0u, rc.div, rc.identity, sm.red, &top, &mn);
+  Thresh th = with_min_p(kKeepAll, ln_mp, M);
   const unsigned long long* list = sm.cw;
   int len = kRCap;
   if (topp_on) {
@@ -1645,7 +1675,6 @@ __device__ __noinline__ int32_t rm_row(const RowCtx& rc, const RowSmem& sm, cons
       len = nk;
     }
   }
-  unsigned long long rb = 0, first = 0;
   rlist_race(list, len, th, M, rc, eps, rb, first);
   rblock_max2(rb, first, sm.red);
   return static_cast<int32_t>(~static_cast<uint32_t>(rb ? rb : first));
@@ -2719,10 +2748,11 @@ __global__ void __launch_bounds__(kRT, 2) kps_row_kernel(const Params P) {
     const bool kteam = !wide && shared_rows && P.B <= nclusters && P.V > kRKeepAllV;
     const Team& tm = (wide || kteam) ? team : alone;
     RowCtx rc;
-    const bool sample = !wide && !P.exact && P.V > kRKeepAllV && !(kMinP && row_min_p_alone(P, row));
+    const bool min_p_alone = kMinP && row_min_p_alone(P, row);
+    const bool sample = !wide && !P.exact && P.V > kRKeepAllV && !min_p_alone;
     const RowFlags f = row_setup<kBF16>(P, row, sm, tm.rank, tm.C, &rc, sample);
     int32_t chosen;
-    if (kMinP && row_min_p_alone(P, row)) {
+    if (min_p_alone) {
       chosen = rm_row<kBF16>(rc, sm, tm, f.topp_on, f.p, P.eps, P.exact != 0);
     } else if (!wide) {
       chosen = rk_row<kBF16>(rc, sm, tm, f.single ? 1u : static_cast<uint32_t>(f.k), f.single, f.topp_on, f.p, P.eps,
