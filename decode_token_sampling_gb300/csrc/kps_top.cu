@@ -16,6 +16,11 @@
 // are ranked pairwise.  Everything else in the list joins the sum.  So the rest is a sum of
 // its own, never a difference of two large ones.  A list that came out too short or too long (the
 // sample misjudged the row, or ties crowd the threshold) sends the row to an exact selection.
+//
+// 2048 rows of 151936 bf16: 137 us (92 at the copy rate), bound by the instructions of the pass:
+// an exponential for every element, and warps that issue on 60% of the cycles.  256 rows of them:
+// 25.5 us (11.5), where the sample's threshold and the list's selection, about 9 us a row, have too
+// few rows behind them to hide in; one row of 151936 fp32: 9.3 us, a chain of latencies.
 
 #include "kps.h"
 #include "kps_host.h"
