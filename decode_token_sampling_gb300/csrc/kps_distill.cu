@@ -678,13 +678,14 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
 // than the second-level cache holds): 495 us for 4096 rows of 151936 bf16 with a quarter masked
 // (321 us at the copy rate), whatever the number of rows in flight.  What it took since: copies by
 // the threads 437 us, bulk copies 409, the cluster's sums sent with stores that count at their
-// receiver's barrier instead of a cluster barrier (whose fence waits for everything) 400, five CTAs'
-// registers 395.  1024 rows of 128256: 94 us (77 at the copy rate).  What bounds it now is the time
-// that a part of a row spends waiting: some 20000 cycles from its slots' loads to its last byte out,
-// of which memory is busy for 80%.
+// receiver's barrier instead of a cluster barrier (whose fence waits for everything) 395, a first
+// cluster barrier without a fence 368, and four CTAs' registers 363 (five CTAs': 370; shared memory
+// holds four).  1024 rows of 128256: 89 us (77 at the copy rate).  What bounds it now is the time
+// that a part of a row spends waiting between its slots' loads and its last byte out: memory is
+// busy for 88% of it.
 //
-// Bytes of a row per CTA, where the cluster allows: four CTAs an SM.  40 KB took 415 us, 62 KB 447,
-// 78 KB 499 (fewer CTAs to fill each other's waits).
+// Bytes of a row per CTA, where the cluster allows: four CTAs an SM.  40 KB took 386 us, 44 KB 408,
+// 62 KB 403 (fewer CTAs to fill each other's waits).
 constexpr int kChunkBytes = 52 * 1024;
 constexpr int kMaxChunkBytes = 200 * 1024;
 
@@ -696,7 +697,7 @@ struct Resident {
 };
 
 template <bool kBF16, bool kRest>
-__global__ void __launch_bounds__(kNT, 5) distill_resident_kernel(const Params P, const Resident R) {
+__global__ void __launch_bounds__(kNT, 4) distill_resident_kernel(const Params P, const Resident R) {
   constexpr int G = kBF16 ? 8 : 4;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float part[kMaxCS * kNW];  // per warp of the cluster
@@ -720,8 +721,9 @@ __global__ void __launch_bounds__(kNT, 5) distill_resident_kernel(const Params P
   }
   __syncwarp();
   // every CTA of the cluster runs, and has set up its barriers, before any writes into another's
-  // shared memory
-  if (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  // shared memory.  The barriers' own fence is behind their setting up; an arrival that releases
+  // would fence for every thread (394 us against 368).
+  if (CS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const RowView<kBF16> x(P.student, row * P.ld, V);
   const int g0 = min(rank * R.share, x.nv), g1 = rank == CS - 1 ? x.nv : min(g0 + R.share, x.nv);
   const int g = g0 + static_cast<int>(threadIdx.x);                  // the thread's vectors: g + i kNT, i < count,
