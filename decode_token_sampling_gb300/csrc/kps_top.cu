@@ -17,10 +17,12 @@
 // its own, never a difference of two large ones.  A list that came out too short or too long (the
 // sample misjudged the row, or ties crowd the threshold) sends the row to an exact selection.
 //
-// 2048 rows of 151936 bf16: 137 us (92 at the copy rate), bound by the instructions of the pass:
-// an exponential for every element, and warps that issue on 60% of the cycles.  256 rows of them:
-// 25.5 us (11.5), where the sample's threshold and the list's selection, about 9 us a row, have too
-// few rows behind them to hide in; one row of 151936 fp32: 9.3 us, a chain of latencies.
+// 2048 rows of 151936 bf16: 122 us (92 at the copy rate), bound by the instructions of the pass:
+// an exponential for every element.  256 rows of them: 20.5 us (11.5), where the sample's threshold
+// and the list's selection have too
+// few rows behind them to hide in; one row of 151936 fp32: 9.5 us, a chain of latencies.  (The
+// sample's size sets the list's: one element in 37 of a row looked at left 550 vectors of 19000 in
+// the list of the top 64, 137 us; one in nine, read as whole vectors, 122.)
 
 #include "kps.h"
 #include "kps_host.h"
@@ -30,6 +32,7 @@
 
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 namespace cg = cooperative_groups;
 
@@ -40,15 +43,15 @@ using namespace stream;
 
 constexpr int kNT = 256;  // threads per CTA
 constexpr int kNW = kNT / 32;
-// 16-byte loads each thread keeps in flight.  Six with four CTAs an SM (64 registers) took 133 us
-// for 2048 rows of 151936 bf16 and 24.8 us for 256; four with five CTAs 139 and 28.5 us, eight with
-// four 133 and 27.0 us.
+// 16-byte loads each thread keeps in flight.  Six with four CTAs an SM (64 registers) took 122 us
+// for 2048 rows of 151936 bf16 and 20.5 us for 256; five with five CTAs 116 and 21.1 us (22.4 against
+// 21.3 on another board), four with five 118 and 22.2 us, eight with four 123 and 20.6 us.
 constexpr int kU = 6;
 constexpr int kMaxN = 1024;    // the framework's top-k limit
 constexpr int64_t kMaxV = 1 << 20;
 constexpr int kMaxCS = 8;      // widest cluster (the portable limit)
 constexpr int kAllV = 4096;    // rows this short are listed whole
-constexpr int kMaxPer = 16;    // sampled places per thread, at most
+constexpr int kMaxPer = 8;     // sampled vectors per thread, at most (of a quarter million elements)
 constexpr int kMaxRank = 96;   // rank of the threshold among the threads' sample maxima, at most
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
 
@@ -295,32 +298,31 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
   float thr = n > 0 ? -INFINITY : INFINITY;  // n == 0: only +inf is listed
   float ref = 0.0f;                          // of the sum: the threshold; n == 0: the largest of the sample
   if (P.V > kAllV || n == 0) {
-    // kNT * per places in runs of 32 consecutive elements spread over the row, each the largest
-    // of m elements for the longest rows, and a maximum of them per thread.  One element of the
-    // row in `one` is looked at, so of the row's first n about n / one are: fewer than `want`
-    // but for one row in 10^5 (a Poisson tail), so the want-th largest maximum is at most the
-    // n-th largest of the row.
+    // kNT * per vectors (m times as many for the longest rows) in runs of 32 consecutive ones spread
+    // over the row, and a maximum of its own for each thread.  One element of the row in `one` is
+    // looked at, so of the row's first n about n / one are: fewer than `want` but for one row in
+    // 10^5 (a Poisson tail), so the want-th largest maximum is at most the n-th largest of the row.
     const int m = (P.V + (1 << 18) - 1) >> 18;
     int per = P.V > kAllV ? kMaxPer : 1;
     float one, r;
     for (;; per >>= 1) {
-      one = fmaxf(1.0f, static_cast<float>(P.V) / static_cast<float>(kNT * per * m));
+      one = fmaxf(1.0f, static_cast<float>(P.V) / static_cast<float>(kNT * G * per * m));
       r = static_cast<float>(n) / one;
       r += 4.0f * sqrtf(r) + 3.5f;
-      if (r <= static_cast<float>(kMaxRank) || per == 1) break;
+      if ((r <= static_cast<float>(kMaxRank) && kNT * G * per * m <= P.V) || per == 1) break;
     }
-    const int step = P.V >= 32 * m ? (P.V - 32 * m) / (kNW * per - 1) : 0;
-    float place[kMaxPer];  // all loads in flight together
-#pragma unroll
-    for (int i = 0; i < kMaxPer; ++i) {
-      const int v = (i * kNW + warp) * step + lane;
-      place[i] = i < per && v < P.V ? x.at(v) : -INFINITY;
-    }
+    const int step = x.nv >= 32 * m ? (x.nv - 32 * m) / (kNW * per - 1) : 0;
     float y = -INFINITY;
+    for (int j = 0; j < m; ++j) {
+      uint4 place[kMaxPer];  // all loads in flight together
 #pragma unroll
-    for (int i = 0; i < kMaxPer; ++i) y = fmaxf(y, place[i]);  // NaN is ignored
-    for (int j = 1; j < m; ++j)
-      for (int i = 0; i < per; ++i) y = fmaxf(y, x.at((i * kNW + warp) * step + lane + 32 * j));
+      for (int i = 0; i < kMaxPer; ++i) {
+        const int g = (i * kNW + warp) * step + lane + 32 * j;
+        place[i] = i < per && g < x.nv ? x.vec[g] : neg_inf_vec<kBF16>();
+      }
+#pragma unroll
+      for (int i = 0; i < kMaxPer; ++i) y = fmaxf(y, vec_max<kBF16>(place[i]));  // NaN is ignored
+    }
     const uint32_t key = fkey(y + 0.0f);
     const int want = n > 0 ? static_cast<int>(r) : 1;
     uint32_t t = 0;  // the largest key, its low 16 bits zero, that `want` maxima reach
@@ -371,25 +373,31 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
     }
     listed += __popc(who);
   };
-  for (int base = g0; base < g1; base += kNT * kU) {
+  // a round of loads; only the last one has to look where the CTA's part ends
+  auto round = [&](int base, auto full) {
+    constexpr bool kFull = decltype(full)::value;
     uint4 w[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int g = base + u * kNT + static_cast<int>(threadIdx.x);
-      w[u] = g < g1 ? ld_stream(x.vec + g) : neg_inf_vec<kBF16>();
+      w[u] = kFull || g < g1 ? ld_stream(x.vec + g) : neg_inf_vec<kBF16>();
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int g = base + u * kNT + static_cast<int>(threadIdx.x);
       const float m = vec_max<kBF16>(w[u]);
-      const bool hit = m >= thr && g < g1;
+      const bool hit = m >= thr && (kFull || g < g1);
       if (__any_sync(0xffffffffu, hit)) {
         list(hit, w[u], x.head + g * G, m);
         if (hit) w[u] = neg_inf_vec<kBF16>();
       }
       fast.add(w[u]);
     }
-  }
+  };
+  int base = g0;
+#pragma unroll 1
+  for (; base + kNT * kU <= g1; base += kNT * kU) round(base, std::true_type{});
+  if (base < g1) round(base, std::false_type{});
   Sum2 sum{ref, fast.total(ref, c)};  // one reference for all of them
   // the elements outside the vectors, each as the first of a vector of its own (its index
   // complemented): the head with rank 0, the tail with the last rank
