@@ -19,10 +19,9 @@
 //
 // 2048 rows of 151936 bf16: 122 us (92 at the copy rate), bound by the instructions of the pass:
 // an exponential for every element.  256 rows of them: 20.5 us (11.5), where the sample's threshold
-// and the list's selection have too
-// few rows behind them to hide in; one row of 151936 fp32: 9.5 us, a chain of latencies.  (The
-// sample's size sets the list's: one element in 37 of a row looked at left 550 vectors of 19000 in
-// the list of the top 64, 137 us; one in nine, read as whole vectors, 122.)
+// and the list's selection have too few rows behind them to hide in; one row of 151936 fp32: 9.5 us,
+// a chain of latencies.  (The sample's size sets the list's: one element in 37 of a row looked at
+// left 550 vectors of 19000 in the list of the top 64, 137 us; one in nine, whole vectors, 122.)
 
 #include "kps.h"
 #include "kps_host.h"
@@ -298,8 +297,9 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
   float thr = n > 0 ? -INFINITY : INFINITY;  // n == 0: only +inf is listed
   float ref = 0.0f;                          // of the sum: the threshold; n == 0: the largest of the sample
   if (P.V > kAllV || n == 0) {
-    // kNT * per vectors (m times as many for the longest rows) in runs of 32 consecutive ones spread
-    // over the row, and a maximum of its own for each thread.  One element of the row in `one` is
+    // kNT * per vectors (m times as many for the longest rows) in runs of four consecutive ones, 64
+    // bytes, spread over the row, and a maximum of its own for each thread.  (Longer runs see too
+    // much of one place: vocabularies are ordered, and neighbours are likely alike.)  One element of the row in `one` is
     // looked at, so of the row's first n about n / one are: fewer than `want` but for one row in
     // 10^5 (a Poisson tail), so the want-th largest maximum is at most the n-th largest of the row.
     const int m = (P.V + (1 << 18) - 1) >> 18;
@@ -311,13 +311,15 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
       r += 4.0f * sqrtf(r) + 3.5f;
       if ((r <= static_cast<float>(kMaxRank) && kNT * G * per * m <= P.V) || per == 1) break;
     }
-    const int step = x.nv >= 32 * m ? (x.nv - 32 * m) / (kNW * per - 1) : 0;
+    constexpr int kRun = 4;
+    const int step = x.nv >= kRun * m ? (x.nv - kRun * m) / (kNT / kRun * per - 1) : 0;
     float y = -INFINITY;
     for (int j = 0; j < m; ++j) {
       uint4 place[kMaxPer];  // all loads in flight together
 #pragma unroll
       for (int i = 0; i < kMaxPer; ++i) {
-        const int g = (i * kNW + warp) * step + lane + 32 * j;
+        const int v = i * kNT + static_cast<int>(threadIdx.x);
+        const int g = v / kRun * step + v % kRun + kRun * j;
         place[i] = i < per && g < x.nv ? x.vec[g] : neg_inf_vec<kBF16>();
       }
 #pragma unroll
