@@ -17,11 +17,13 @@
 // its own, never a difference of two large ones.  A list that came out too short or too long (the
 // sample misjudged the row, or ties crowd the threshold) sends the row to an exact selection.
 //
-// 2048 rows of 151936 bf16: 122 us (92 at the copy rate), bound by the instructions of the pass:
-// an exponential for every element.  256 rows of them: 20.5 us (11.5), where the sample's threshold
-// and the list's selection have too few rows behind them to hide in; one row of 151936 fp32: 9.5 us,
-// a chain of latencies.  (The sample's size sets the list's: one element in 37 of a row looked at
-// left 550 vectors of 19000 in the list of the top 64, 137 us; one in nine, whole vectors, 122.)
+// 2048 rows of 151936 bf16: 122 us (92 at the copy rate); warps issue on 47% of the cycles, waiting
+// for loads first (an SM's four rows are not always at different phases).  256 rows of them: 20.5 us
+// (11.5), where the sample's threshold and the list's selection have too few rows behind them to
+// hide in; one row of 151936 fp32: 9.8 us, a chain of latencies.  The sample's size sets the list's:
+// one element in 37 of a row looked at left 550 vectors of 19000 in the list of the top 64 and the
+// pass bound by its instructions, 137 us; one in nine, read as whole vectors, 122.
+// Measured slower: the next round's loads issued before this one's sums (125-130 us).
 
 #include "kps.h"
 #include "kps_host.h"
