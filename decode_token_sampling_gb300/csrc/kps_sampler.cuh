@@ -612,7 +612,7 @@ struct Ctx {
   float M;              // row maximum (transformed)
   uint32_t* cand_key;   // candidate list of this CTA (transformed keys)
   int32_t* cand_idx;
-  uint32_t* hist;            // 3072 words: 2048 counts, 1024-bin limb histogram, or radix bins
+  uint32_t* hist;            // 2048 + 1024 words: counts, 1024-bin limb histogram, or radix bins
   uint32_t* fine;            // 3 x kFineBins words: 1024-bin limb histogram
   unsigned long long* sup;   // kLinBins/32 + kFineBins/32 u64 (fallback radix uses two 16-entry halves)
   unsigned long long* small; // [kSmall] own boundary list, [kSmall] gathered list
