@@ -17,12 +17,12 @@
 // its own, never a difference of two large ones.  A list that came out too short or too long (the
 // sample misjudged the row, or ties crowd the threshold) sends the row to an exact selection.
 //
-// 2048 rows of 151936 bf16: 122 us (92 at the copy rate); warps issue on 47% of the cycles, waiting
-// for loads first (an SM's four rows are not always at different phases).  256 rows of them: 20.5 us
+// 2048 rows of 151936 bf16: 121 us (92 at the copy rate); warps issue on 47% of the cycles, waiting
+// for loads first (an SM's four rows are not always at different phases).  256 rows of them: 21 us
 // (11.5), where the sample's threshold and the list's selection have too few rows behind them to
 // hide in; one row of 151936 fp32: 9.8 us, a chain of latencies.  The sample's size sets the list's:
 // one element in 37 of a row looked at left 550 vectors of 19000 in the list of the top 64 and the
-// pass bound by its instructions, 137 us; one in nine, read as whole vectors, 122.
+// pass bound by its instructions, 137 us; one in nine, read as whole vectors, 121.
 // Measured slower: the next round's loads issued before this one's sums (125-130 us).
 
 #include "kps.h"
@@ -44,9 +44,9 @@ using namespace stream;
 
 constexpr int kNT = 256;  // threads per CTA
 constexpr int kNW = kNT / 32;
-// 16-byte loads each thread keeps in flight.  Six with four CTAs an SM (64 registers) took 122 us
-// for 2048 rows of 151936 bf16 and 20.5 us for 256; five with five CTAs 116 and 21.1 us (22.4 against
-// 21.3 on another board), four with five 118 and 22.2 us, eight with four 123 and 20.6 us.
+// 16-byte loads each thread keeps in flight.  Six with four CTAs an SM (64 registers) took 121 us
+// for 2048 rows of 151936 bf16 and 21.3 us for 256; five with five CTAs 118 and 22.4 us, four with
+// five 3% and 8% more than that, eight with four 1% more than six on both.
 constexpr int kU = 6;
 constexpr int kMaxN = 1024;    // the framework's top-k limit
 constexpr int64_t kMaxV = 1 << 20;
@@ -299,9 +299,10 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
   float thr = n > 0 ? -INFINITY : INFINITY;  // n == 0: only +inf is listed
   float ref = 0.0f;                          // of the sum: the threshold; n == 0: the largest of the sample
   if (P.V > kAllV || n == 0) {
-    // kNT * per vectors (m times as many for the longest rows) in runs of four consecutive ones, 64
+    // kNT * per vectors (m times as many for the longest rows) in runs of eight consecutive ones, 128
     // bytes, spread over the row, and a maximum of its own for each thread.  (Longer runs see too
-    // much of one place: vocabularies are ordered, and neighbours are likely alike.)  One element of the row in `one` is
+    // much of one place: vocabularies are ordered, and neighbours are likely alike.  Runs of four
+    // took 125 us for 2048 rows of 151936 bf16, of eight 121.)  One element of the row in `one` is
     // looked at, so of the row's first n about n / one are: fewer than `want` but for one row in
     // 10^5 (a Poisson tail), so the want-th largest maximum is at most the n-th largest of the row.
     const int m = (P.V + (1 << 18) - 1) >> 18;
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
       r += 4.0f * sqrtf(r) + 3.5f;
       if ((r <= static_cast<float>(kMaxRank) && kNT * G * per * m <= P.V) || per == 1) break;
     }
-    constexpr int kRun = 4;
+    constexpr int kRun = 8;
     const int step = x.nv >= kRun * m ? (x.nv - kRun * m) / (kNT / kRun * per - 1) : 0;
     float y = -INFINITY;
     for (int j = 0; j < m; ++j) {
