@@ -195,16 +195,21 @@ struct Teacher {
   }
 };
 
+// Whether the student's sum outside the list holds up: near its reference, or (a teacher whose rest
+// has no mass) nothing beside the list's.
+__device__ __forceinline__ bool precise(const Sum2& rest, const Sum2& list, float er) {
+  return rest.s >= 0x1p-60f || (er == 0.0f && rest.s >= 0.0f && list.s >= 0.5f);
+}
+
 // The divergence in base 2.  list (against ref), rest, all: the student's sums.
-template <bool kRest>
 __device__ __forceinline__ float divergence(const Teacher& t, float ref, const F2& list, const Sum2& rest,
                                             const Sum2& all, float c) {
   const float moved = (all.ref - ref) * c, E = t.E.value(), W = t.W.value();
   // (list and rest against one reference: their sum as two floats)
-  const bool same = kRest && rest.ref == ref;
+  const bool same = rest.ref == ref;
   const F2 head = same ? list : F2{all.s, 0.0f};
   const float tail = same ? rest.s : 0.0f;
-  if (!kRest || t.er == 0.0f) return W / E + log2_ratio(head, tail, t.E, 0.0f) + moved;
+  if (t.er == 0.0f) return W / E + log2_ratio(head, tail, t.E, 0.0f) + moved;
   if (rest.s == 0.0f) return INFINITY;  // the teacher's rest has mass, the student's none
   const float Et = E + t.er, pr = t.er / Et;
   // D = (uh + ul) - log2 of the student's rest against ref, whole powers of two first
@@ -515,7 +520,7 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
   // (the slots of a row of weight 0 are read all the same: their loads need not wait for the weight's)
   Slot slot = first_slot(P, row);
   const float w = P.weight ? P.weight[row] : 1.0f;
-  const float r = kRest ? P.rest[row] : -INFINITY;
+  const float r = kRest && P.rest ? P.rest[row] : -INFINITY;
   float scale = w;  // of the gradient
   if (kMode != kForward && P.upstream) scale *= P.upstream[row];
   scale *= P.tau;
@@ -603,11 +608,11 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
       }
       all = kRest ? merge(list, rest, c) : rest;
       // the same in every CTA
-      if (moving || (fabsf(ref * c) <= kFastRef && rest.s >= 0x1p-60f && all.s <= 0x1p100f)) break;
+      if (moving || (fabsf(ref * c) <= kFastRef && precise(rest, list, T.er) && all.s <= 0x1p100f)) break;
       if (CS > 1) cg::this_cluster().sync();  // the parts are read
     }
     if (rank == 0 && threadIdx.x == 0) {
-      const float kl = divergence<kRest>(T, ref, S, rest, all, c);
+      const float kl = divergence(T, ref, S, rest, all, c);
       const bool ok = all.s > 0.0f && all.s < INFINITY;
       P.loss[row] = ok ? w * P.tau * P.tau * (kl * kLn2) : NAN;
       if (kMode == kForward && P.stats) {
@@ -680,7 +685,7 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
 // the threads 437 us, bulk copies 409, the cluster's sums sent with stores that count at their
 // receiver's barrier instead of a cluster barrier (whose fence waits for everything) 395, a first
 // cluster barrier without a fence 368, and four CTAs' registers 363 (five CTAs': 370; shared memory
-// holds four).  1024 rows of 128256: 89 us (77 at the copy rate).  What bounds it now is the time
+// holds four).  1024 rows of 128256: 91 us (77 at the copy rate).  What bounds it now is the time
 // that a part of a row spends waiting between its slots' loads and its last byte out: memory is
 // busy for 88% of it.
 //
@@ -696,7 +701,7 @@ struct Resident {
   int id, e, v, next, head, hash;
 };
 
-template <bool kBF16, bool kRest>
+template <bool kBF16>
 __global__ void __launch_bounds__(kNT, 4) distill_resident_kernel(const Params P, const Resident R) {
   constexpr int G = kBF16 ? 8 : 4;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -734,25 +739,24 @@ __global__ void __launch_bounds__(kNT, 4) distill_resident_kernel(const Params P
   float* s_v = reinterpret_cast<float*>(smem + R.v);
   int32_t* s_next = reinterpret_cast<int32_t*>(smem + R.next);
   int32_t* s_head = reinterpret_cast<int32_t*>(smem + R.head);  // per thread: the first of the slots whose tokens
-  int32_t* s_hash = reinterpret_cast<int32_t*>(smem + R.hash);  // lie in its vectors, the others by s_next (kRest)
+  int32_t* s_hash = reinterpret_cast<int32_t*>(smem + R.hash);  // lie in its vectors, the others by s_next
 
   // ---- the copy, and the teacher's slots while it is under way ------------------------------------
   if (threadIdx.x < 2) {
     top[threadIdx.x] = 0u;
     flags[threadIdx.x] = 0;
   }
-  if (kRest) s_head[threadIdx.x] = -1;
+  s_head[threadIdx.x] = -1;
   for (int i = threadIdx.x; i < R.hash_size; i += kNT) s_hash[i] = -1;
   // (the slots of a row of weight 0 are read all the same: their loads need not wait for the weight's)
   Slot slot = first_slot(P, row);
   const float w = P.weight ? P.weight[row] : 1.0f;
-  const float r = kRest ? P.rest[row] : -INFINITY;
+  const float r = P.rest ? P.rest[row] : -INFINITY;
   const float scale = w * P.tau;
   __syncthreads();
   if (w != 0.0f) {
     if (threadIdx.x == 0 && g1 > g0) copy_in(smem, x.vec + g0, static_cast<uint32_t>(g1 - g0) * 16u, &landed);
     read_slots<true>(P, row, x, slot, s_id, s_e, s_v, s_hash, R.hash_size, top, flags, [&](int k, int32_t id) {
-      if (!kRest) return;
       const int at = id - x.head, vec = at / G - g0;
       if (at >= 0 && vec >= 0 && vec < g1 - g0) s_next[k] = atomicExch(&s_head[vec & (kNT - 1)], k);
     });
@@ -770,7 +774,7 @@ __global__ void __launch_bounds__(kNT, 4) distill_resident_kernel(const Params P
   slot_masses(P, K, tref, ref, dup, s_id, s_e, s_v, teacher);
 
   // ---- the student's sum outside the list -------------------------------------------------------
-  // With kRest the list's tokens leave the row: each thread overwrites those in its own vectors with
+  // The list's tokens leave the row: each thread overwrites those in its own vectors with
   // -inf (their logits are in s_v).  Against the list's largest student logit, one reference for
   // the whole row, so that the parts simply add up; a sum that leaves fp32's range (the list far
   // from everything else) is taken again below against its own maximum.
@@ -778,13 +782,11 @@ __global__ void __launch_bounds__(kNT, 4) distill_resident_kernel(const Params P
   float s_rest;
   {
     FastSum<kBF16> fast(fabsf(ref * c) <= kFastRef ? ref : 0.0f, c);
-    if (kRest) {
-      for (int k = s_head[threadIdx.x]; k >= 0; k = s_next[k]) {
-        const int at = s_id[k] - x.head;
-        uint4* v = mine + (at / G - g);
-        if (kBF16) reinterpret_cast<uint16_t*>(v)[at % G] = 0xFF80u;
-        else reinterpret_cast<uint32_t*>(v)[at % G] = 0xFF800000u;
-      }
+    for (int k = s_head[threadIdx.x]; k >= 0; k = s_next[k]) {
+      const int at = s_id[k] - x.head;
+      uint4* v = mine + (at / G - g);
+      if (kBF16) reinterpret_cast<uint16_t*>(v)[at % G] = 0xFF80u;
+      else reinterpret_cast<uint32_t*>(v)[at % G] = 0xFF800000u;
     }
 #pragma unroll 4
     for (int i = 0; i < count; ++i) fast.add(mine[i * kNT]);
@@ -795,7 +797,7 @@ __global__ void __launch_bounds__(kNT, 4) distill_resident_kernel(const Params P
                          ((x.loose_at(threadIdx.x) < x.head) ? rank == 0 : rank == CS - 1);
   const int loose_v = has_loose ? x.loose_at(threadIdx.x) : 0;
   const float loose_s = has_loose ? x.at(loose_v) : -INFINITY;
-  const bool loose_out = has_loose && !(kRest && has_token(s_hash, R.hash_size, loose_v));
+  const bool loose_out = has_loose && !has_token(s_hash, R.hash_size, loose_v);
   if (loose_out) s_rest += ex2((loose_s - ref) * c);
   if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // (of the arrival at the top)
   // Gives every warp of the cluster's CTAs' values a to all of them, at part[].
@@ -826,12 +828,12 @@ __global__ void __launch_bounds__(kNT, 4) distill_resident_kernel(const Params P
     __syncthreads();  // (the slots' sums, too)
   }
   Teacher T;
-  const F2 S = collect<kRest>(teacher, K, r, tref, c, P.c_lo, T);
-  const Sum2 list{ref, kRest ? S.value() : 0.0f};
+  const F2 S = collect<true>(teacher, K, r, tref, c, P.c_lo, T);
+  const Sum2 list{ref, S.value()};
   Sum2 rest{ref, late ? NAN : part_sum()};
   Sum2 all{ref, rest.s + list.s};
   // (NaN fails this too)
-  if (!(fabsf(ref * c) <= kFastRef && rest.s >= 0x1p-60f && all.s <= 0x1p100f)) {
+  if (!(fabsf(ref * c) <= kFastRef && precise(rest, list, T.er) && all.s <= 0x1p100f)) {
     // the same in every CTA: the largest logit outside the list (NaN: there is one), then the sum
     // against that
     float m = loose_out ? loose_s : -INFINITY;
@@ -865,7 +867,7 @@ __global__ void __launch_bounds__(kNT, 4) distill_resident_kernel(const Params P
     if (CS > 1) cl.sync(); else __syncthreads();
     exchange(warp_sum(t));
     rest = Sum2{m, part_sum()};
-    all = kRest ? merge(list, rest, c) : rest;
+    all = merge(list, rest, c);
     if (nan) all.s = NAN;
   }
   // ---- the gradient ------------------------------------------------------------------------------
@@ -910,7 +912,7 @@ __global__ void __launch_bounds__(kNT, 4) distill_resident_kernel(const Params P
       copy_out(const_cast<uint4*>(o.vec) + g0, smem, static_cast<uint32_t>(g1 - g0) * 16u);
   }
   if (rank == 0 && threadIdx.x == kNT - 1) {
-    const float kl = divergence<kRest>(T, ref, S, rest, all, c);
+    const float kl = divergence(T, ref, S, rest, all, c);
     const bool ok = all.s > 0.0f && all.s < INFINITY;
     P.loss[row] = ok ? w * P.tau * P.tau * (kl * kLn2) : NAN;
   }
@@ -976,7 +978,7 @@ static kps_status launch_t(const Params& P, cudaStream_t stream) {
 }
 
 // The loss and the gradient: with the row in shared memory where a cluster's holds it.
-template <bool kBF16, bool kRest>
+template <bool kBF16>
 static kps_status launch_both(const Params& P, cudaStream_t stream) {
   const int sms = sm_count();
   if (!sms) return KPS_ERR_CUDA;
@@ -984,7 +986,7 @@ static kps_status launch_both(const Params& P, cudaStream_t stream) {
   const int64_t bytes = static_cast<int64_t>(P.V) * (kBF16 ? 2 : 4);
   int cs = static_cast<int>((bytes + kChunkBytes - 1) / kChunkBytes);
   cs = cs < 1 ? 1 : cs > kMaxCS ? kMaxCS : cs;
-  if (bytes > static_cast<int64_t>(kMaxChunkBytes) * cs) return launch_t<kBF16, kRest, kBoth>(P, stream);
+  if (bytes > static_cast<int64_t>(kMaxChunkBytes) * cs) return launch_t<kBF16, true, kBoth>(P, stream);
   // few rows: wider clusters, while every thread keeps a group's worth of vectors
   while (2 * cs <= kMaxCS && P.N * cs * 2 <= 2 * sms && P.V >= 2 * cs * kNT * 4 * G) cs *= 2;
   Resident R;
@@ -996,10 +998,10 @@ static kps_status launch_both(const Params& P, cudaStream_t stream) {
   R.e = R.id + k4;
   R.v = R.e + k4;
   R.next = R.v + k4;
-  R.head = R.next + (kRest ? k4 : 0);
-  R.hash = R.head + (kRest ? kNT * 4 : 0);
+  R.head = R.next + k4;
+  R.hash = R.head + kNT * 4;
   const size_t total = static_cast<size_t>(R.hash) + R.hash_size * 4;
-  auto* kernel = distill_resident_kernel<kBF16, kRest>;
+  auto* kernel = distill_resident_kernel<kBF16>;
   static std::atomic<bool> done[kMaxDevices];
   if (!allow_shared(kernel, done)) {
     (void)cudaGetLastError();
@@ -1026,12 +1028,14 @@ static kps_status launch_both(const Params& P, cudaStream_t stream) {
 
 template <int kMode>
 static kps_status launch(const Params& P, kps_dtype dt, cudaStream_t stream) {
-  if (kMode == kBoth) {
-    if (dt == KPS_BF16) return P.rest ? launch_both<true, true>(P, stream) : launch_both<true, false>(P, stream);
-    return P.rest ? launch_both<false, true>(P, stream) : launch_both<false, false>(P, stream);
-  }
-  if (dt == KPS_BF16) return P.rest ? launch_t<true, true, kMode>(P, stream) : launch_t<true, false, kMode>(P, stream);
-  return P.rest ? launch_t<false, true, kMode>(P, stream) : launch_t<false, false, kMode>(P, stream);
+  // The loss always takes the list's tokens out of the row's sum, rest or not: they weigh most where
+  // the student is near its teacher, and the loss, a small number there, then comes from sums in two
+  // floats (without a rest its error against 64 bits fell from 1e-6 to 1.2e-7; 1024 rows of 128256
+  // bf16 take 49 us instead of 44).
+  if (kMode == kBoth) return dt == KPS_BF16 ? launch_both<true>(P, stream) : launch_both<false>(P, stream);
+  if (kMode == kForward || P.rest)
+    return dt == KPS_BF16 ? launch_t<true, true, kMode>(P, stream) : launch_t<false, true, kMode>(P, stream);
+  return dt == KPS_BF16 ? launch_t<true, false, kBackward>(P, stream) : launch_t<false, false, kBackward>(P, stream);
 }
 
 // The checks every entry point shares; fills P.  *empty: nothing to do.
