@@ -437,6 +437,9 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
   } else {
     __syncthreads();
   }
+  // every finite element is listed (short rows, and long ones with few finite elements): the pass
+  // summed nothing, and what joins from the list may lie anywhere, far below zero too
+  if (thr <= -FLT_MAX && sum.s == 0.0f) sum.ref = -FLT_MAX;  // (a NaN in the sum stays)
 
   // ---- the listed elements: cut to the n-th largest key's digit --------------------------------
   const int nseg = kNW * CS;

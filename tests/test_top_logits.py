@@ -245,3 +245,25 @@ def test_teacher_to_student():
     got = kps.top_logits(student, 0, tokens=idx).logprob
     want = torch.log_softmax(student.double(), 1).gather(1, idx[:, None])[:, 0]
     assert bool(((got.double() - want).abs() <= 2 * sum_error(V) + 8 * U * 60).all())
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shift", [-100.0, -500.0, -1e4])
+def test_listed_rows_far_below_zero(dtype, shift):
+    """Rows whose sum is taken of listed elements alone (short ones, and masked ones with few finite
+    tokens), far below zero: a log-probability of -12 at temperature 0.1 is an exponent of -120."""
+    for V, n in ((5, 2), (100, 10), (1000, 10), (4096, 300), (4096, 0)):
+        x = (_logits(4, V, torch.float32, seed=V) + shift).to(dtype)
+        check(x, n, 1.0, torch.randint(0, V, (4,), device="cuda"))
+    x = torch.log_softmax(_logits(4, 3000, torch.float32), 1).to(dtype)
+    check(x, 20, 0.1, torch.randint(0, 3000, (4,), device="cuda"))
+    # 40 allowed tokens of a long row, the others -inf or the type's lowest value
+    V = 150001
+    at = torch.randperm(V, device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    x = torch.full((3, V), -math.inf, dtype=dtype, device="cuda")
+    x[1] = torch.finfo(dtype).min
+    x[:2, at[:40]] = (_logits(2, 40, torch.float32) + shift).to(dtype)
+    x[2, at[:3]] = shift
+    for n in (0, 1, 10, 39, 40, 41):
+        check(x, n, 1.0, at[:3])
