@@ -571,9 +571,10 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
     if (P.lse) P.lse[row] = lse;
     if (P.rest) P.rest[row] = ln(sum);
     if (P.logprob) {
-      // relative to the sum's reference: lse and the token's logit are both large
+      // relative to the sum's reference: lse and the token's logit are both large, and lse may have
+      // left fp32 where their difference has not (the type's lowest value over tau < 1)
       const float y = token_logit;
-      float lp = isinf(lse) ? y / P.tau - lse : (y - all.ref) / P.tau - logf(all.s);
+      float lp = all.s > 0.0f && all.s < INFINITY ? (y - all.ref) / P.tau - logf(all.s) : y / P.tau - lse;
       if (isnan(y)) lp = -INFINITY;
       P.logprob[row] = lp;
     }

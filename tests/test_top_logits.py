@@ -267,3 +267,24 @@ def test_listed_rows_far_below_zero(dtype, shift):
     x[2, at[:3]] = shift
     for n in (0, 1, 10, 39, 40, 41):
         check(x, n, 1.0, at[:3])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [1000, 50001])
+def test_logprob_where_the_log_sum_exp_overflows(dtype, V):
+    """Rows of the type's lowest or largest value at a temperature below 1: the log-sum-exp leaves
+    fp32, the token's log-probability does not.  It is -ln of the number of equal tokens."""
+    import decode_token_sampling_gb300 as kps
+    x = torch.full((4, V), torch.finfo(dtype).min, dtype=dtype, device="cuda")
+    x[1] = -x[1]
+    x[2, ::2] = -math.inf
+    x[3] = -x[3]
+    x[3, ::2] = 0.0
+    equal = torch.tensor([V, V, V // 2, V // 2], device="cuda")
+    for n in (0, 5):
+        got = kps.top_logits(x, n, temperature=0.5, tokens=torch.full((4,), 7, device="cuda"))
+        want = -torch.log(equal.double())
+        # the sum's error, ln's last place and the negation
+        assert bool(((got.logprob.double() - want).abs() <= sum_error(V, dtype == torch.bfloat16) + 2 * U * 16).all())
+        assert got.lse.tolist() == [-math.inf, math.inf, -math.inf, math.inf]
