@@ -692,7 +692,6 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
 // Bytes of a row per CTA, where the cluster allows: four CTAs an SM.  40 KB took 386 us, 44 KB 408,
 // 62 KB 403 (fewer CTAs to fill each other's waits).
 constexpr int kChunkBytes = 52 * 1024;
-constexpr int kMaxChunkBytes = 200 * 1024;
 
 // What the host lays out for a launch: `share` vectors of a row for each CTA, and the offsets of
 // the small arrays behind them in shared memory.
@@ -986,7 +985,6 @@ static kps_status launch_both(const Params& P, cudaStream_t stream) {
   const int64_t bytes = static_cast<int64_t>(P.V) * (kBF16 ? 2 : 4);
   int cs = static_cast<int>((bytes + kChunkBytes - 1) / kChunkBytes);
   cs = cs < 1 ? 1 : cs > kMaxCS ? kMaxCS : cs;
-  if (bytes > static_cast<int64_t>(kMaxChunkBytes) * cs) return launch_t<kBF16, true, kBoth>(P, stream);
   // few rows: wider clusters, while every thread keeps a group's worth of vectors
   while (2 * cs <= kMaxCS && P.N * cs * 2 <= 2 * sms && P.V >= 2 * cs * kNT * 4 * G) cs *= 2;
   Resident R;
@@ -1001,6 +999,8 @@ static kps_status launch_both(const Params& P, cudaStream_t stream) {
   R.head = R.next + k4;
   R.hash = R.head + kNT * 4;
   const size_t total = static_cast<size_t>(R.hash) + R.hash_size * 4;
+  // a row's part and the list's arrays have to fit together
+  if (total > kMaxDynamic) return launch_t<kBF16, true, kBoth>(P, stream);
   auto* kernel = distill_resident_kernel<kBF16>;
   static std::atomic<bool> done[kMaxDevices];
   if (!allow_shared(kernel, done)) {

@@ -495,3 +495,13 @@ def test_gradient_of_rows_far_apart():
     check(view, ids, val, 1.0, r)
     _, grad = kps.distill_loss_grad(view, ids, val, rest=r)
     assert grad.untyped_storage().nbytes() <= N * (V + 3) * 4
+
+
+@gpu
+@pytest.mark.parametrize("dtype,edge", [(torch.float32, 401408), (torch.bfloat16, 802816)])
+@pytest.mark.parametrize("K", [960, 961, 1024])
+def test_longest_lists_on_the_longest_rows_in_shared_memory(dtype, edge, K):
+    """Where the row and the arrays of a long list together fill a block's shared memory."""
+    for V in (edge, edge + 8, edge + 3000):
+        s, ids, val, r = _case(2, V, K, dtype, "cuda", seed=K)
+        check(s, ids, val, 1.0, r)
