@@ -92,9 +92,8 @@ __host__ __device__ inline Layout make_layout(int K, int64_t chunk, bool distinc
   return L;
 }
 
-__device__ __forceinline__ float teacher_value(const Params& P, int64_t i) {
-  return P.values_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(P.values)[i])
-                       : static_cast<const float*>(P.values)[i];
+__device__ __forceinline__ float teacher_value(const void* values, bool bf16, int64_t i) {
+  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(values)[i]) : static_cast<const float*>(values)[i];
 }
 
 // The block's sum; every thread gets it.
@@ -225,6 +224,57 @@ __device__ __forceinline__ float divergence(const Teacher& t, float ref, const F
   return W / Et - E / Et * D - kLog2e * log1pf(E / t.er) + q;
 }
 
+// The loss by its definition in 64 bits, by one warp: for rows where the form above meets an infinity.
+// That is a loss of +inf, or one whose parts leave fp32 (or cancel as infinities) while the loss does
+// not: a student of -inf or the type's lowest value all over the list, a list without mass.  As in
+// fp32, a class whose mass is below 2^-126 of the largest has none.
+// (Its arguments go in registers: a reference to the kernel's parameters would cost every row a copy.)
+template <bool kBF16>
+__device__ __noinline__ float plain_loss(const void* student, const int32_t* ids, const void* values, bool values_bf16,
+                                         int V, int K, float temperature, float w, float r, Sum2 all, Sum2 rest) {
+  const RowView<kBF16> x(student, 0, V);
+  const int lane = threadIdx.x & 31;
+  const double tau = temperature;
+  const double L = all.ref / tau + log(static_cast<double>(all.s));
+  double m = r;
+  auto each = [&](auto&& f) {  // f(exponent of the teacher's value, token) of the lane's filled slots
+    for (int k = lane; k < K; k += 32) {
+      const int32_t id = ids[k];
+      const float t = teacher_value(values, values_bf16, k);
+      if (id >= 0 && id < V && t != -INFINITY) f(t / tau, id);
+    }
+  };
+  auto sum = [](double v) {
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  each([&](double u, int32_t) { m = fmax(m, u); });
+  for (int o = 16; o; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+  double Z = 0.0, kl = 0.0;
+  each([&](double u, int32_t) { Z += exp(u - m); });
+  Z = sum(Z) + exp(r - m);
+  auto term = [&](double u, double a) {  // p (ln p - ln q) of a class of the student's log-sum-exp a
+    const double e = exp(u - m);
+    return e < 0x1p-126 ? 0.0 : e / Z * (u - m - log(Z) - a + L);
+  };
+  each([&](double u, int32_t id) { kl += term(u, x.at(id) / tau); });
+  kl = sum(kl) + term(r, rest.ref / tau + log(static_cast<double>(rest.s)));
+  return static_cast<float>(w * tau * tau * kl);
+}
+
+// The row's loss; all 32 lanes of a warp call it with the same arguments.
+template <bool kBF16>
+__device__ __forceinline__ float row_loss(const Params& P, int64_t row, const Teacher& T, float ref, const F2& list,
+                                          const Sum2& rest, const Sum2& all, float w, float r) {
+  if (!(all.s > 0.0f && all.s < INFINITY)) return NAN;
+  const float kl = divergence(T, ref, list, rest, all, P.c);
+  if (fabsf(kl) < INFINITY) return w * P.tau * P.tau * (kl * kLn2);
+  const int64_t slot = row * P.K;
+  return plain_loss<kBF16>(static_cast<const unsigned char*>(P.student) + row * P.ld * (kBF16 ? 2 : 4), P.ids + slot,
+                           static_cast<const unsigned char*>(P.values) + slot * (P.values_bf16 ? 2 : 4), P.values_bf16,
+                           P.V, P.K, P.tau, w, r, all, rest);
+}
+
 // Writes zeros to this CTA's part of a row of the gradient.
 template <bool kBF16>
 __device__ __forceinline__ void zero_row(void* grad, int64_t offset, int V, int rank, int CS) {
@@ -288,7 +338,7 @@ struct Slot {
   float t;
 };
 __device__ __forceinline__ Slot read_slot(const Params& P, int64_t row, int k) {
-  return Slot{P.ids[row * P.K + k], teacher_value(P, row * P.K + k)};
+  return Slot{P.ids[row * P.K + k], teacher_value(P.values, P.values_bf16, row * P.K + k)};
 }
 __device__ __forceinline__ Slot first_slot(const Params& P, int64_t row) {
   return static_cast<int>(threadIdx.x) < P.K ? read_slot(P, row, threadIdx.x) : Slot{-1, -INFINITY};
@@ -611,10 +661,10 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
       if (moving || (fabsf(ref * c) <= kFastRef && precise(rest, list, T.er) && all.s <= 0x1p100f)) break;
       if (CS > 1) cg::this_cluster().sync();  // the parts are read
     }
+    float loss = 0.0f;
+    if (rank == 0 && threadIdx.x < 32) loss = row_loss<kBF16>(P, row, T, ref, S, rest, all, w, r);
     if (rank == 0 && threadIdx.x == 0) {
-      const float kl = divergence(T, ref, S, rest, all, c);
-      const bool ok = all.s > 0.0f && all.s < INFINITY;
-      P.loss[row] = ok ? w * P.tau * P.tau * (kl * kLn2) : NAN;
+      P.loss[row] = loss;
       if (kMode == kForward && P.stats) {
         P.stats[row * kStats] = all.ref;
         P.stats[row * kStats + 1] = all.s;
@@ -910,10 +960,9 @@ __global__ void __launch_bounds__(kNT, 4) distill_resident_kernel(const Params P
     if (threadIdx.x == 0 && g1 > g0)
       copy_out(const_cast<uint4*>(o.vec) + g0, smem, static_cast<uint32_t>(g1 - g0) * 16u);
   }
-  if (rank == 0 && threadIdx.x == kNT - 1) {
-    const float kl = divergence(T, ref, S, rest, all, c);
-    const bool ok = all.s > 0.0f && all.s < INFINITY;
-    P.loss[row] = ok ? w * P.tau * P.tau * (kl * kLn2) : NAN;
+  if (rank == 0 && threadIdx.x >= kNT - 32) {  // not the warp that stores the row
+    const float loss = row_loss<kBF16>(P, row, T, ref, S, rest, all, w, r);
+    if (lane == 0) P.loss[row] = loss;
   }
   if (late) copy_landed(&landed);  // one more wait before the block leaves
 }

@@ -341,7 +341,8 @@ kps_status kps_top_logits(const void* logits, kps_dtype dt, int64_t B, int64_t V
  * (the Kullback-Leibler divergence of the student from the teacher, everything
  * outside the list as one class).  A student row holding NaN or +inf, or
  * nothing above -inf, has a loss and a gradient of NaN; a student that gives
- * no mass to a token or a rest that the teacher gives some has a loss of +inf.
+ * no mass to a token or a rest that the teacher gives some has a loss of +inf
+ * (a mass below 2^-126 of the teacher's largest counts as none).
  *
  * kps_distill_forward writes out_loss [N] and, unless NULL, out_stats [N, 4],
  * which kps_distill_backward takes with the same other arguments: it writes

@@ -505,3 +505,50 @@ def test_longest_lists_on_the_longest_rows_in_shared_memory(dtype, edge, K):
     for V in (edge, edge + 8, edge + 3000):
         s, ids, val, r = _case(2, V, K, dtype, "cuda", seed=K)
         check(s, ids, val, 1.0, r)
+
+
+def _finite_grad(s, ids, val, tau, rest, weight=None):
+    """The fused call and the pair against the formulas where the losses are huge or infinite."""
+    import decode_token_sampling_gb300 as kps
+    kw = dict(temperature=tau, rest=rest, weight=weight)
+    want, ref, _, _ = distill_reference(s, ids, val, tau, rest, weight)
+    loss, stats = kps.distill_forward(s, ids, val, **kw)
+    loss2, grad = kps.distill_loss_grad(s, ids, val, **kw)
+    back = kps.distill_backward(None, s, ids, val, stats, **kw)
+    for got in (loss, loss2):
+        # p's exponentials and their sum, and a few roundings more: all relative, the loss is no difference here
+        lim = (1e-5 * want.abs()).where(torch.isfinite(want), torch.zeros_like(want))
+        _compare(got.double(), want, lim, "loss")
+    half = torch.finfo(s.dtype).eps / 2
+    w = torch.ones_like(want) if weight is None else weight.double()
+    for got in (grad, back):
+        # masses below one in sums off by 1e-5
+        lim = (3e-5 * (w * tau).abs())[:, None] + half * ref.abs()
+        _compare(got.double(), ref, lim, "grad")
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tau", [0.5, 1.0, 2.0])
+@pytest.mark.parametrize("K", [1, 16])
+def test_student_without_the_lists_tokens(dtype, tau, K):
+    """-inf or the type's lowest value at every token of the teacher's list, or at one of them: a loss of
+    +inf, or a huge one; next to no mass in the list: the loss of the rest alone."""
+    s, ids, val, r = _case(6, 3000, K, dtype, "cuda", seed=31)
+    lowest = torch.finfo(dtype).min
+    for value in (-math.inf, lowest, -1e9):
+        x = s.clone()
+        x[:3].scatter_(1, ids[:3].long(), value)
+        x[3:].scatter_(1, ids[3:, :1].long(), value)
+        w = torch.full((6,), 0.25 if value == lowest else 1.0, device="cuda")
+        for rest in (None, r, r + 3.0, r - 3.0):
+            _finite_grad(x, ids, val, tau, rest, w)
+    # the teacher's list has no mass that fp32 holds, the student's list none at all
+    x = s.clone()
+    x.scatter_(1, ids.long(), -math.inf)
+    import decode_token_sampling_gb300 as kps
+    far = torch.full((6,), 2000.0, device="cuda")
+    loss, stats = kps.distill_forward(x, ids, val, temperature=tau, rest=far)
+    loss2, grad = kps.distill_loss_grad(x, ids, val, temperature=tau, rest=far)
+    assert bool((loss.abs() <= 1e-5 * tau * tau).all()) and bool((loss2.abs() <= 1e-5 * tau * tau).all())
+    assert bool((grad.float().abs() <= 1e-5 * tau).all())
