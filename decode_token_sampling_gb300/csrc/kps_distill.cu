@@ -183,9 +183,15 @@ struct Teacher {
   F2 E, W;
   float er, uh, ul;
   template <bool kRest>
-  __device__ __forceinline__ void rest(float r, float tref, float c, float c_lo) {
+  __device__ __forceinline__ void rest(float r, float tref, float tau, float c, float c_lo) {
     er = uh = ul = 0.0f;
-    if (!kRest) return;
+    if (!kRest || r == -INFINITY) return;
+    if (!(fabsf(tref * c) < 0x1p40f)) {
+      // floats this large lie 2^16 apart, and their exponents would overflow: the rest either is the
+      // largest class or has no mass beside it
+      er = r * tau < tref ? 0.0f : fabsf(r) < INFINITY ? 1.0f : NAN;
+      return;
+    }
     const float a = r * kLog2e, b = tref * c;  // r is in nats at the temperature
     const float al = fmaf(r, kLog2e, -a) + r * 1.92596303e-8f, bl = fmaf(tref, c, -b) + tref * c_lo;
     two_diff(a, b, uh, ul);
@@ -422,7 +428,8 @@ __device__ __forceinline__ void slot_masses(const Params& P, int K, float tref, 
 }
 // All of that, after a barrier; returns the student's sum over the list.
 template <bool kRest>
-__device__ __forceinline__ F2 collect(const F2 (*sums)[3], int K, float r, float tref, float c, float c_lo, Teacher& T) {
+__device__ __forceinline__ F2 collect(const F2 (*sums)[3], int K, float r, float tref, float tau, float c, float c_lo,
+                                      Teacher& T) {
   T = Teacher{};
   F2 S = {};
   for (int i = 0; i < kNW && i * 32 < K; ++i) {
@@ -430,7 +437,7 @@ __device__ __forceinline__ F2 collect(const F2 (*sums)[3], int K, float r, float
     T.W.add(sums[i][1]);
     S.add(sums[i][2]);
   }
-  T.rest<kRest>(r, tref, c, c_lo);
+  T.rest<kRest>(r, tref, tau, c, c_lo);
   return S;
 }
 
@@ -642,7 +649,7 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
       if (moving) rest = moving_sum<kBF16, kRest>(x, g0, g1, bytes, loose_out ? x.at(lv) : -INFINITY, c);
       rest = block_merge(rest, c, red);
       if (!moving) {
-        S = collect<kRest>(sums, K, r, tref, c, P.c_lo, T);
+        S = collect<kRest>(sums, K, r, tref, P.tau, c, P.c_lo, T);
         list = Sum2{ref, kRest ? S.value() : 0.0f};
       }
       if (CS > 1) {
@@ -680,7 +687,7 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
   // ---- the gradient -------------------------------------------------------------------
   if (kMode != kForward) {
     Teacher T;
-    (void)collect<kRest>(sums, K, r, tref, c, P.c_lo, T);
+    (void)collect<kRest>(sums, K, r, tref, P.tau, c, P.c_lo, T);
     const float invE = 1.0f / (T.E.value() + T.er);
     const Factors F(scale, T.er, invE, all, rest, c);
     const RowView<kBF16> o(P.grad, row * P.ld_grad, V);
@@ -877,7 +884,7 @@ __global__ void __launch_bounds__(kNT, 4) distill_resident_kernel(const Params P
     __syncthreads();  // (the slots' sums, too)
   }
   Teacher T;
-  const F2 S = collect<true>(teacher, K, r, tref, c, P.c_lo, T);
+  const F2 S = collect<true>(teacher, K, r, tref, P.tau, c, P.c_lo, T);
   const Sum2 list{ref, S.value()};
   Sum2 rest{ref, late ? NAN : part_sum()};
   Sum2 all{ref, rest.s + list.s};

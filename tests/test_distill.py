@@ -552,3 +552,23 @@ def test_student_without_the_lists_tokens(dtype, tau, K):
     loss2, grad = kps.distill_loss_grad(x, ids, val, temperature=tau, rest=far)
     assert bool((loss.abs() <= 1e-5 * tau * tau).all()) and bool((loss2.abs() <= 1e-5 * tau * tau).all())
     assert bool((grad.float().abs() <= 1e-5 * tau).all())
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tau", [0.5, 1.0, 3.0])
+def test_teacher_of_the_types_lowest_values(dtype, tau):
+    """A list of nothing but the lowest value is a uniform one (without a rest, or with one of -inf); with
+    a rest it weighs nothing.  Largest values likewise."""
+    s, ids, val, r = _case(4, 2000, 9, dtype, "cuda", seed=32)
+    for vt in (torch.float32, torch.bfloat16):
+        low = torch.full_like(val, torch.finfo(vt).min, dtype=vt)
+        none = torch.full_like(r, -math.inf)
+        none[1] = torch.finfo(torch.float32).min
+        for v in (low, -low):
+            check(s, ids, v, tau, None)
+            check(s, ids, v, tau, torch.full_like(r, -math.inf) if v is low else none)
+            check(s, ids, v, tau, r)
+        # a teacher's row that is masked all over, as top_logits hands it on at temperature 1: every class alike
+        check(s, ids, low, 1.0, torch.full_like(r, torch.finfo(vt).min))
+        check(s, ids, -low, 1.0, torch.full_like(r, torch.finfo(vt).max))
