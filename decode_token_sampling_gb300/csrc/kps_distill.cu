@@ -24,6 +24,7 @@
 #include <cooperative_groups.h>
 
 #include <atomic>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 
@@ -1101,7 +1102,9 @@ static kps_status check(const void* student, kps_dtype dt, int64_t N, int64_t V,
   if ((dt != KPS_F32 && dt != KPS_BF16) || (values_dt != KPS_F32 && values_dt != KPS_BF16)) return KPS_ERR_INVALID_ARG;
   if (N < 0 || V < 1 || K < 1 || K > kMaxK) return KPS_ERR_INVALID_ARG;
   if (N > 1 && ld < V) return KPS_ERR_INVALID_ARG;
-  if (!(temperature > 0.0f) || std::isinf(temperature) || std::isinf(stream::kLog2e / temperature)) return KPS_ERR_INVALID_ARG;
+  // the loss holds the temperature's square, which has to be a normal number
+  const float tau2 = temperature * temperature;
+  if (!(temperature > 0.0f) || !(tau2 >= FLT_MIN) || std::isinf(tau2)) return KPS_ERR_INVALID_ARG;
   if (V > kMaxV || N > INT32_MAX / kMaxCS) return KPS_ERR_UNSUPPORTED;
   if (N == 0) return KPS_OK;
   if (!student || !ids || !values) return KPS_ERR_INVALID_ARG;

@@ -323,6 +323,7 @@ kps_status kps_top_logits(const void* logits, kps_dtype dt, int64_t B, int64_t V
  *   rest     [N] ln sum of exp(t / temperature) over everything the teacher's
  *            list leaves out (kps_top_logits' out_rest at the same
  *            temperature), or NULL: the list is all there is.
+ *   temperature  above 0, its square a normal fp32 number (1.1e-19 to 1.8e19).
  *   weight   [N] or NULL (1): of each row's loss.  A row of weight 0, or
  *            without a filled slot, has loss 0 and gradient 0, and the
  *            student's logits in it are not looked at.

@@ -572,3 +572,13 @@ def test_teacher_of_the_types_lowest_values(dtype, tau):
         # a teacher's row that is masked all over, as top_logits hands it on at temperature 1: every class alike
         check(s, ids, low, 1.0, torch.full_like(r, torch.finfo(vt).min))
         check(s, ids, -low, 1.0, torch.full_like(r, torch.finfo(vt).max))
+
+
+@pytest.mark.parametrize("call", [_forward, _loss_grad, _backward])
+def test_temperatures_whose_square_is_no_normal_number_are_refused(lib, call):
+    """The loss holds the square of the temperature."""
+    for tau in (2e-20, 1e-30, 2e19, 1e38):
+        assert call(lib, tau=tau) == 1, tau
+    if not torch.cuda.is_available():
+        for tau in (1e-18, 1e18):
+            assert call(lib, tau=tau) == 4, tau
