@@ -400,12 +400,17 @@ def _distill_args(student, ids, values, rest, weight, temperature):
 
 
 def _grad_like(student: torch.Tensor) -> torch.Tensor:
-    """An uninitialised gradient whose rows lie on the same 16-byte phase as the student's, at the
-    least distance that allows it (the student may be every hundredth row of something larger)."""
+    """An uninitialised gradient whose rows lie on the same 16-byte phase as the student's (its first
+    element included), at the least distance that allows it (the student may be every hundredth row
+    of something larger)."""
     N, V = student.shape
-    ld = V + (student.stride(0) - V) % (16 // student.element_size()) if N > 1 else V
-    grad = torch.empty((N, ld), dtype=student.dtype, device=student.device)
-    return grad if ld == V else grad[:, :V]
+    size = student.element_size()
+    ld = V + (student.stride(0) - V) % (16 // size) if N > 1 else V
+    phase = student.data_ptr() % 16 // size
+    if phase == 0 and ld == V:
+        return torch.empty((N, V), dtype=student.dtype, device=student.device)
+    grad = torch.empty(phase + N * ld, dtype=student.dtype, device=student.device)
+    return grad[phase:].view(N, ld)[:, :V]
 
 
 def _distill_forward(student, ids, values, temperature, rest, weight, stream, want_stats):

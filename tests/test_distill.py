@@ -582,3 +582,21 @@ def test_temperatures_whose_square_is_no_normal_number_are_refused(lib, call):
     if not torch.cuda.is_available():
         for tau in (1e-18, 1e18):
             assert call(lib, tau=tau) == 4, tau
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradient_rows_share_the_students_phase(dtype):
+    """Every row of the gradient starts as far behind a 16-byte boundary as the student's, whatever
+    the student's offset and row stride are: only then are rows stored 16 bytes at a time."""
+    import decode_token_sampling_gb300 as kps
+    es = torch.empty(0, dtype=dtype).element_size()
+    for N, V, ld in ((1, 1000, 1000), (3, 1000, 1000), (4, 1001, 1001), (5, 1001, 1100), (2, 7, 5000)):
+        for off in range(16 // es):
+            student = torch.empty(off + N * ld, dtype=dtype)[off:].view(N, ld)[:, :V]
+            grad = kps._grad_like(student)
+            assert grad.shape == student.shape and grad.dtype == dtype and grad.stride(1) == 1
+            assert grad.untyped_storage().nbytes() <= (N * (V + 16 // es) + 16 // es) * es
+            for i in range(N):
+                assert (grad[i].data_ptr() - student[i].data_ptr()) % 16 == 0
+            if ld == V and off == 0:
+                assert grad.is_contiguous()
