@@ -25,7 +25,8 @@
 //   keep-all rows (no top-k, p >= 1): a maximum pass, then the race and write.
 //   min-p rows without top-k: what can be kept lies above the largest value seen so
 //     far plus T ln(min_p), so one streaming pass lists it, thinning the list as that
-//     value grows; with top-p the pass also sums the softmax mass of everything else.
+//     value grows; with top-p the pass also estimates the row's softmax mass, which is summed
+//     exactly where the estimate leaves the cut open.
 //     Top-k rows raise their cut to the min-p bound at the end.
 //
 // The method is the one of the Ascend "torch_npu.npu_top_k_top_p_sample" page
@@ -86,7 +87,7 @@ enum RMisc {
   kMCut = 11, kMBlo = 12, kMBhi = 13,  // list cut, band bounds
   kMLnMinP = 14,                       // float2: ln(min_p) of the row
   kMMinP = 15,                         // float: the row's min-p (0: off)
-  kMRowMass = 17,                      // the whole row's mass (min-p rows with top-p)
+  kMRowLo = 17, kMRowHi = 19,          // bounds of the whole row's mass (min-p rows with top-p)
   kMRunMax = 18,                       // uint32: key of the largest raw value so far (min-p rows)
   kMCnt = 16,                          // uint32 counter
   kMSeg = 20,                          // uint32[kRW]: per-warp segment counts (8 slots)
@@ -955,8 +956,10 @@ __device__ __noinline__ int rlist_topp_cut(const unsigned long long* kl, int n, 
 // Top-p over the survivors kl[0..n) (1 < n <= 1024, maximum M): a fixed-point mass
 // histogram over linear bins of [smallest value, M] finds the bin holding the boundary
 // and that bin's entries are ranked pairwise; a large bin is sorted instead.  Returns
-// the last kept entry.  kRow: p is a share of misc[kMRowMass] instead of the survivors' own
-// sum; every survivor is kept when they do not reach the target.  scratch: 2 * kRRank + 1024 u64.
+// the last kept entry.  kRow: p is a share of a mass between misc[kMRowLo] and misc[kMRowHi]
+// instead of the survivors' own sum; every survivor is kept when they do not reach the target;
+// kUndecided when the two bounds do not lead to the same cut.  scratch: 2 * kRRank + 1024 u64.
+constexpr Thresh kUndecided{0u, 0};
 template <bool kRow = false>
 __device__ __noinline__ Thresh rk_topp(unsigned long long* kl, int n, float M, float p, uint32_t* hist,
                                        unsigned long long* scratch, unsigned long long* red,
@@ -980,9 +983,10 @@ __device__ __noinline__ Thresh rk_topp(unsigned long long* kl, int n, float M, f
     s_cnt = 0u;
   }
   rblock_sum_max2(part, nmn, dummy, red);
-  const unsigned long long S = kRow ? misc[kMRowMass] : part;
-  const unsigned long long tq = rtopp_target(p, S);
+  const unsigned long long tq = rtopp_target(p, kRow ? misc[kMRowLo] : part);
+  const unsigned long long tq_hi = kRow ? rtopp_target(p, misc[kMRowHi]) : tq;
   if (kRow && tq > part) return Thresh{1u, -1};
+  if (kRow && tq_hi > part) return kUndecided;
   const float lo = kfloat(~static_cast<uint32_t>(nmn));
   const float span = __fsub_rn(M, lo);
   const float s = (span > 0.0f && span < INFINITY) ? __fdiv_rn(static_cast<float>(kRSurvBins), span) : 0.0f;
@@ -1037,13 +1041,14 @@ __device__ __noinline__ Thresh rk_topp(unsigned long long* kl, int n, float M, f
         const unsigned long long wi = gw[i];
         unsigned long long exm = above;
         for (int j = 0; j < m; ++j) exm += gw[j] > wi ? gm[j] : 0ull;
-        if (exm < tq && tq <= exm + gm[i]) misc[kMHit] = wi;
+        if (exm < tq && tq <= exm + gm[i]) misc[kMHit] = !kRow || tq_hi <= exm + gm[i] ? wi : ~0ull;
       }
     }
     __syncthreads();
   }
   const unsigned long long hit = misc[kMHit];
   __syncthreads();
+  if (kRow && hit == ~0ull) return kUndecided;
   if (hit != 0ull) return Thresh{static_cast<uint32_t>(hit >> 32), static_cast<int32_t>(~static_cast<uint32_t>(hit))};
   // large boundary bin: sort the survivors and cut the prefix
   int N = 1;
@@ -1052,6 +1057,7 @@ __device__ __noinline__ Thresh rk_topp(unsigned long long* kl, int n, float M, f
   __syncthreads();
   rbitonic_desc(kl, N);
   const int L = rlist_topp_cut(kl, n, M, 0ull, tq, red, misc);
+  if (kRow && tq_hi != tq && rlist_topp_cut(kl, n, M, 0ull, tq_hi, red, misc) != L) return kUndecided;
   const unsigned long long w = kl[(L > 0 ? L : n) - 1];
   return Thresh{static_cast<uint32_t>(w >> 32), static_cast<int32_t>(~static_cast<uint32_t>(w))};
 }
@@ -1389,47 +1395,28 @@ __device__ __forceinline__ int32_t rexact_row(const RowCtx& whole, const RowSmem
 // 20 in the pass (0.7 a round of loads, the rest the exponentials and the list), 6 on the row's
 // maximum and gathering the list, 6 on top-p and the race; rows with top-k and min-p, the
 // longest, take the way of all top-k rows.  256 rows of 151936 fp32 with a penalty: 100 us (23 at
-// the copy rate).  Rows with min-p alone: 30 and 75 us.
+// the copy rate).  Batches of rows with top-p and min-p alone: 38 and 86 us, with min-p alone 30 and 75 us.
 // Measured slower: the first round's largest value before anything is listed (75 -> 79 us), loads
 // issued a round ahead (100 -> 112 us or more: registers), a round looked through first and its few
 // listed vectors taken up in a loop behind (75 -> 88 us), the cluster kernel for whole batches
 // (64 rows: 382 us), a bound from a sample of the row (its list overflows when the sample misses
 // the largest values: 224 us).
 
-// exp(x / T - M) for a raw value x near the maximum: the quotient carried as two floats.
-__device__ __forceinline__ float rscale_to_max(float x, float T, float M) {
-  const float q = __fdiv_rn(x, T);
-  const float ql = __fdiv_rn(__fmaf_rn(-q, T, x), T);
-  const float s = __fsub_rn(q, M);
-  const float b = __fsub_rn(s, q);
-  const float lo = __fadd_rn(__fadd_rn(__fsub_rn(q, __fsub_rn(s, b)), __fsub_rn(-M, b)), ql);
-  const float e = expf(s);
-  return __fmaf_rn(e, lo, e);
-}
-
 // What the warps of a min-p row's pass work with.
 struct MinPScan {
   float reach;   // T ln(min_p): how far under the maximum a kept raw value can lie
   float tiny;    // 1e-30 T: magnitudes whose quotients by T have room above the subnormals
-  float2 c;      // log2(e) / T as two floats: its rounding would scale every exponent of the row alike
+  float c;       // log2(e) / T
   // A raw value below which nothing can be kept once xm has been seen (penalised raw values).
   // The roundings of both quotients and of reach come to less than 2^-20 of |xm| + |reach|.
   __device__ __forceinline__ float floor(float xm) const {
     const float m = fabsf(xm) + fabsf(reach);
     return m >= tiny ? __fsub_rd(__fadd_rd(xm, reach), m * 0x1p-20f) : -INFINITY;
   }
-  // exp((x - ref) / T) for x <= ref; 0 for NaN and -inf.
-  __device__ __forceinline__ float weight(float x, float ref) const {
-    const float d = __fsub_rn(x, ref);
-    return rex2(fmaxf(__fmaf_rn(d, c.x, __fmul_rn(d, c.y)), -200.0f));
-  }
 };
 
-// Drops the entries of seg[0..n) below t, keeping their order; the dropped ones' weights go to
-// *total (kSum).  One warp; returns the count left.
-template <bool kSum>
-__device__ __forceinline__ uint32_t rm_thin(unsigned long long* seg, uint32_t n, float t, float ref, const MinPScan& sc,
-                                            float* total) {
+// Drops the entries of seg[0..n) below t, keeping their order.  One warp; returns the count left.
+__device__ __forceinline__ uint32_t rm_thin(unsigned long long* seg, uint32_t n, float t) {
   const int lane = threadIdx.x & 31;
   const unsigned lt = (1u << lane) - 1u;
   uint32_t kept = 0;
@@ -1439,7 +1426,6 @@ __device__ __forceinline__ uint32_t rm_thin(unsigned long long* seg, uint32_t n,
     const unsigned long long w = in ? seg[i + lane] : 0ull;
     const float x = kfloat(static_cast<uint32_t>(w >> 32));
     const bool keep = in && x >= t;
-    if (kSum && in && !keep) *total += sc.weight(x, ref);
     const unsigned m = __ballot_sync(kFull, keep);  // every lane has read its entry
     if (keep) seg[kept + __popc(m & lt)] = w;       // at or before the entries read
     kept += __popc(m);
@@ -1451,11 +1437,14 @@ __device__ __forceinline__ uint32_t rm_thin(unsigned long long* seg, uint32_t n,
 // The pass of a min-p row: the -inf background of the filtered row, and everything that can
 // still be kept, as (raw key, index), in this warp's segment.  The bound follows the largest
 // value that any warp of the block has seen; a segment that fills up is thinned with the bound
-// as it then stands.  *total: the thread's weights of what is not listed, relative to *cur, the
-// warp's largest value (kSum).  Returns the warp's count (above kRSeg: it overflowed).
+// as it then stands.  Returns the warp's count (above kRSeg: it overflowed).  What is listed
+// depends on when the warps see each other's values, until it is thinned by the row's maximum.
+// kSum: *sum is the thread's sum of 2^(x c - *unit), an estimate (rm_mass_bounds).  The unit is the largest
+// value at the first term and moves only when another lies 2^64 above it, so no term pays for a
+// running maximum.  NaN where a move would have to scale what is summed already, and in rows with NaN.
 template <bool kBF16, bool kSum>
 __device__ __forceinline__ uint32_t rm_stream(const RowCtx& rc, const MinPScan& sc, unsigned long long* seg,
-                                              uint32_t* run_max, unsigned long long pol, float* cur_out, float* total_out) {
+                                              uint32_t* run_max, unsigned long long pol, float* sum, float* unit) {
   constexpr int G = kBF16 ? 8 : 4;
   const int lane = threadIdx.x & 31;
   const unsigned lt = (1u << lane) - 1u;
@@ -1468,22 +1457,31 @@ __device__ __forceinline__ uint32_t rm_stream(const RowCtx& rc, const MinPScan& 
   const float4 ninf = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
   uint32_t wcnt = 0;
   bool over = false;
-  float cur = -INFINITY, t = -INFINITY, total = 0.0f;
+  float cur = -INFINITY, t = -INFINITY;
+  stream::f32x2 acc = 0ull;  // two zeros
+  float total = 0.0f, ref = -INFINITY, rcu = 0.0f;
+  auto raise = [&](float to) {
+    cur = to;
+    t = sc.floor(cur);
+    if (kSum && !((cur - ref) * sc.c <= 64.0f)) {  // the first time as well
+      // what is summed lies 2^64 at most above the unit: nothing beside a new one of 2^128
+      if (total != 0.0f || acc != 0ull) total = (cur - ref) * sc.c >= 128.0f ? 0.0f : NAN;
+      acc = 0ull;
+      ref = cur;
+      rcu = ref * sc.c > -0x1p28f ? ref * sc.c : 0.0f;  // so far below zero every term is 0
+    }
+  };
   for (int base = rc.g0; base < g1; base += kRT * kRU) {
     uint4 w[kRU];
 #pragma unroll
     for (int u = 0; u < kRU; ++u) {
       const int g = base + u * kRT + static_cast<int>(threadIdx.x);
-      w[u] = g < g1 ? ld_row16(xr + g, pol) : make_uint4(0u, 0u, 0u, 0u);
+      w[u] = g < g1 ? ld_row16(xr + g, pol) : stream::neg_inf_vec<kBF16>();
     }
     {
       // what the other warps have seen (NaN before the first)
       const float top = kfloat(__shfl_sync(kFull, *reinterpret_cast<volatile uint32_t*>(run_max), 0));
-      if (top > cur) {
-        if (kSum) total *= sc.weight(cur, top);
-        cur = top;
-        t = sc.floor(cur);
-      }
+      if (top > cur) raise(top);
     }
 #pragma unroll
     for (int u = 0; u < kRU; ++u) {
@@ -1505,32 +1503,27 @@ __device__ __forceinline__ uint32_t rm_stream(const RowCtx& rc, const MinPScan& 
       float mx = -INFINITY;
 #pragma unroll
       for (int e = 0; e < G; ++e) mx = fmaxf(mx, v[e]);  // NaN is ignored (it counts as -inf)
-      if (!in) mx = -INFINITY;
       if (__any_sync(kFull, mx > cur)) {
         // a new largest value: what the block has seen by now, this vector included
         const uint32_t key = __reduce_max_sync(kFull, fkey(mx));
         uint32_t seen = 0;
         if (lane == 0) seen = atomicMax(run_max, key);
         seen = __shfl_sync(kFull, seen, 0);
-        const float top = kfloat(seen > key ? seen : key);
-        if (kSum) total *= sc.weight(cur, top);
-        cur = top;
-        t = sc.floor(cur);
+        raise(kfloat(seen > key ? seen : key));
       }
-      bool pass[G];
-      bool any = false;
+      if (kSum) {
+        const stream::f32x2 c2 = stream::pack2(sc.c, sc.c), n2 = stream::pack2(-rcu, -rcu);
 #pragma unroll
-      for (int e = 0; e < G; ++e) {
-        pass[e] = in && v[e] >= t;
-        any |= pass[e];
+        for (int e = 0; e < G; e += 2) {
+          float a, b;
+          stream::unpack2(stream::fma2(stream::pack2(v[e], v[e + 1]), c2, n2), a, b);
+          acc = stream::add2(acc, stream::pack2(rex2(a), rex2(b)));
+        }
       }
-      if (kSum && in) {
-        float part = 0.0f;
+      if (__any_sync(kFull, in && mx >= t) && !over) {
+        bool pass[G];
 #pragma unroll
-        for (int e = 0; e < G; ++e) part += pass[e] ? 0.0f : sc.weight(v[e], cur);
-        total += part;
-      }
-      if (__any_sync(kFull, any) && !over) {
+        for (int e = 0; e < G; ++e) pass[e] = in && v[e] >= t;
         unsigned m[G];
         uint32_t n = 0;
 #pragma unroll
@@ -1540,11 +1533,8 @@ __device__ __forceinline__ uint32_t rm_stream(const RowCtx& rc, const MinPScan& 
         }
         if (wcnt + n > static_cast<uint32_t>(kRSeg)) {
           // thin with the bound of the whole block; a segment that stays full is given up
-          const float top = fmaxf(cur, kfloat(__shfl_sync(kFull, *reinterpret_cast<volatile uint32_t*>(run_max), 0)));
-          if (kSum) total *= sc.weight(cur, top);
-          cur = top;
-          t = sc.floor(cur);
-          wcnt = rm_thin<kSum>(seg, wcnt, t, cur, sc, &total);
+          raise(fmaxf(cur, kfloat(__shfl_sync(kFull, *reinterpret_cast<volatile uint32_t*>(run_max), 0))));
+          wcnt = rm_thin(seg, wcnt, t);
           over = wcnt > static_cast<uint32_t>(kRSeg * 3 / 4) || wcnt + n > static_cast<uint32_t>(kRSeg);
         }
         if (!over) {
@@ -1556,10 +1546,65 @@ __device__ __forceinline__ uint32_t rm_stream(const RowCtx& rc, const MinPScan& 
         }
       }
     }
+    if (kSum) {
+      float a, b;
+      stream::unpack2(acc, a, b);
+      total += a + b;
+      acc = 0ull;
+    }
   }
-  *cur_out = cur;
-  *total_out = total;
+  *sum = total;
+  *unit = rcu;
   return over ? static_cast<uint32_t>(kRSeg) + 1u : wcnt;
+}
+
+// The softmax mass of a whole row against its maximum M, by one CTA: the sum of fixed-point masses that
+// the exact selection takes.
+template <bool kBF16>
+__device__ __noinline__ unsigned long long rm_mass(const RowCtx& whole, float M, unsigned long long* red) {
+  // w 2^40 to nearest even in two limbs of 20 bits (512 elements a thread at most): the shifts of
+  // fixed_mass would take longer than the exponentials
+  uint32_t high = 0, low = 0;
+  rrow_pass<kBF16>(whole, l2_policy_normal(), [&](bool valid, float y, uint32_t, int) {
+    const float w = valid ? __fmul_rn(softmax_weight(y, M), 0x1p20f) : 0.0f;
+    const float h = __fadd_rd(w, 0x1p23f);  // the integer part, exactly
+    const float l = __fmaf_rn(__fsub_rn(w, __fsub_rn(h, 0x1p23f)), 0x1p20f, 0x1p23f);
+    high += __float_as_uint(h) - 0x4B000000u;
+    low += __float_as_uint(l) - 0x4B000000u;
+  });
+  return rblock_sum_u64((static_cast<unsigned long long>(high) << 20) + low, red);
+}
+
+// Bounds [*lo, *hi] of rm_mass from the estimate S (2^-40 units) that the streaming pass made of it;
+// nothing and everything when it has none.  far: the largest distance, in base-2 exponents, of a thread's unit below the
+// row's maximum; rounds: of loads, each one addition deep.  With u = 2^-24 the estimate is off, relative
+// to the row's mass, by at most
+//   (|M| + 17) u     the definition's rounding of y = x / T.  (Elements 17 nats below M and further weigh
+//                    2^-24 each, 2^-6 all 2^18 of them at most; with what their larger exponents make of
+//                    the terms below, 4 u.)
+//   4 u + 8 u        softmax_weight; ex2.approx (2^-22) of the element and of the unit's factor
+//   0.7 (24 + far) u + 17 u + 0.7 far u      the exponent's rounding, that of c, that of the factor's exponent
+//   (rounds + 8) u   additions
+// and by half a unit of fixed point for every element, twice.
+__device__ __forceinline__ void rm_mass_bounds(unsigned long long S, float far, float M, float T, int rounds, int V,
+                                               unsigned long long* lo, unsigned long long* hi) {
+  const float e = (fabsf(M) + 1.5f * far + static_cast<float>(rounds + 80)) * 0x1p-24f;
+  const bool ok = e < 0x1p-6f && T >= 1e-30f && T <= 1e30f;
+  const unsigned long long off = static_cast<unsigned long long>(__fmul_ru(__ull2float_ru(S), ok ? e : 1.0f)) + static_cast<unsigned>(V) + 1u;
+  *lo = ok && S > off ? S - off : 0ull;
+  *hi = ok ? S + off : 1ull << 62;
+}
+
+// Top-p over the survivors in sm.wbuf[0..n) (rk_topp), with the exact mass where the bounds leave it open.
+template <bool kBF16>
+__device__ __noinline__ Thresh rm_topp(const RowCtx& whole, const RowSmem& sm, int n, float M, float p) {
+  Thresh th = rk_topp<true>(sm.wbuf, n, M, p, sm.hist, sm.cw, sm.red, sm.misc);
+  if (th.key == kUndecided.key) {
+    const unsigned long long S = rm_mass<kBF16>(whole, M, sm.red);
+    if (threadIdx.x == 0) sm.misc[kMRowLo] = sm.misc[kMRowHi] = S;
+    th = rk_topp<true>(sm.wbuf, n, M, p, sm.hist, sm.cw, sm.red, sm.misc);
+  }
+  return th;
 }
 
 // The exact selection out of line: the fallback of the min-p rows.
@@ -1571,11 +1616,15 @@ __device__ __noinline__ int32_t rexact_min_p_row(const RowCtx& whole, const RowS
 
 // A row whose top-k is off and whose min-p is on (mp in (0, 1]); returns the chosen index.
 // Everything that can be kept is at least M + ln(mp): one streaming pass lists what reaches that
-// for the largest value seen so far (the true maximum is always among it).  With top-p the pass
-// also sums the mass of everything it does not list, for p is a share of the whole row's.
-template <bool kBF16>
-__device__ __noinline__ int32_t rm_row(const RowCtx& rc, const RowSmem& sm, const Team& tm, bool topp_on, float p,
-                                       float eps, bool exact) {
+// for the largest value seen so far (the true maximum is always among it).  Top-p takes a share of the
+// whole row's mass.  The pass estimates that mass in fp32; when both bounds of the estimate lead to the
+// same cut, that is the cut, and when they do not (the boundary lies within some 2^-17 of the target: one
+// row in a thousand of usual logits), rank 0 reads the row again for the exact sum.  So the cut is always
+// that of the exact selection, whatever the estimate's last bits were.
+// (kTopP as a run-time choice spilled more registers and took 256 rows of every kind 5% longer.)
+template <bool kBF16, bool kTopP>
+__device__ __noinline__ int32_t rm_row(const RowCtx& rc, const RowSmem& sm, const Team& tm, float p, float eps,
+                                       bool exact) {
   const float mp = *reinterpret_cast<const float*>(sm.misc + kMMinP);
   uint32_t* segcnt = reinterpret_cast<uint32_t*>(sm.misc + kMSeg);
   uint32_t* run_max = reinterpret_cast<uint32_t*>(sm.misc + kMRunMax);
@@ -1583,41 +1632,35 @@ __device__ __noinline__ int32_t rm_row(const RowCtx& rc, const RowSmem& sm, cons
   RowCtx whole = rc;
   whole.g0 = 0;
   whole.g1 = rc.nv;
-  if (exact) return tm.rank == 0 ? rexact_min_p_row<kBF16>(whole, sm, topp_on, p, mp, eps) : -1;
+  if (exact) return tm.rank == 0 ? rexact_min_p_row<kBF16>(whole, sm, kTopP, p, mp, eps) : -1;
   if (threadIdx.x == 0) *run_max = 0u;
-  MinPScan sc;
-  {
-    sc.reach = __fmul_rn(logf(mp), rc.T);
-    sc.tiny = 1e-30f * rc.T;
-    constexpr float kLog2eHi = 1.44269502162933349609f, kLog2eLo = 1.92596299112661746887e-8f;
-    const float hi = __fdiv_rn(kLog2eHi, rc.T);
-    sc.c = make_float2(hi, __fdiv_rn(__fadd_rn(__fmaf_rn(-hi, rc.T, kLog2eHi), kLog2eLo), rc.T));
-  }
+  const MinPScan sc{__fmul_rn(logf(mp), rc.T), 1e-30f * rc.T, __fdiv_rn(kLog2e, rc.T)};
   __syncthreads();
   if (threadIdx.x == kRT - 1) *reinterpret_cast<float2*>(sm.misc + kMLnMinP) = ln_min_p(mp);
-  float cur, total;
   unsigned long long* seg = sm.cw + warp * kRSeg;
-  uint32_t wc = topp_on ? rm_stream<kBF16, true>(rc, sc, seg, run_max, l2_policy_first(), &cur, &total)
-                        : rm_stream<kBF16, false>(rc, sc, seg, run_max, l2_policy_first(), &cur, &total);
+  float sum, unit;
+  uint32_t wc = rm_stream<kBF16, kTopP>(rc, sc, seg, run_max, l2_policy_first(), &sum, &unit);
   __syncthreads();
   // the row's largest value, over every member's part; then every segment against it
   tm.push(sm.misc, 0, *run_max);
   tm.sync();
   const float top_raw = kfloat(static_cast<uint32_t>(tm.max_of(sm.misc, 0)));
   const float M = rmax_transformed(fkey(top_raw), rc);
-  if (topp_on) total *= sc.weight(cur, top_raw);
-  if (wc <= static_cast<uint32_t>(kRSeg))
-    wc = topp_on ? rm_thin<true>(seg, wc, sc.floor(top_raw), top_raw, sc, &total)
-                 : rm_thin<false>(seg, wc, sc.floor(top_raw), top_raw, sc, &total);
-  unsigned long long below = 0;  // the mass of what is not listed, against M
-  if (topp_on) {
-    below = rblock_sum_u64(fixed_mass(__fmul_rn(total, rscale_to_max(top_raw, rc.T, M))), sm.red);
-    tm.push(sm.misc, 1, below);
+  if (wc <= static_cast<uint32_t>(kRSeg)) wc = rm_thin(seg, wc, sc.floor(top_raw));
+  if (kTopP) {  // the part's estimate against the row's maximum
+    const float z = __fmaf_rn(-top_raw, sc.c, unit);
+    const float m = __fdiv_rn(__fmaf_rn(-M, rc.T, top_raw), rc.T);  // what M's rounding left out
+    const float w = sum == 0.0f ? 0.0f : __fmul_rn(sum, __fmaf_rn(rex2(z), m, rex2(z)));
+    const bool ok = w <= 0x1p20f;  // no NaN, no infinity
+    unsigned long long mass = ok ? fixed_mass(w) : 0ull, unused = 0;
+    unsigned long long far = __float_as_uint(!ok ? INFINITY : w > 0.0f ? fmaxf(-z, 0.0f) : 0.0f);
+    rblock_sum_max2(mass, far, unused, sm.red);
+    tm.push(sm.misc, 1, mass);
+    tm.push(sm.misc, 2, far);
   }
   if (lane == 0) segcnt[warp] = wc;
   __syncthreads();
   if (!rk_gather_team(sm, tm)) return -1;
-  if (topp_on) below = tm.sum_of(sm.misc, 1);
   bool over = false;
   uint32_t n = 0, at = 0;  // what is listed, and where this warp's part of it goes
 #pragma unroll
@@ -1627,28 +1670,26 @@ __device__ __noinline__ int32_t rm_row(const RowCtx& rc, const RowSmem& sm, cons
     n += segcnt[w];
   }
   // a list overflowed, or nothing has a distance to the maximum: the exact selection
-  if (over || n == 0u || isinf(M)) return rexact_min_p_row<kBF16>(whole, sm, topp_on, p, mp, eps);
+  if (over || n == 0u || isinf(M)) return rexact_min_p_row<kBF16>(whole, sm, kTopP, p, mp, eps);
   const float2 ln_mp = *reinterpret_cast<const float2*>(sm.misc + kMLnMinP);
+  if (kTopP && threadIdx.x == 0) {  // published by the barriers of rm_topp
+    const int rounds = (rc.g1 - rc.g0) / (kRT * kRU) + 1;
+    rm_mass_bounds(tm.sum_of(sm.misc, 1), __uint_as_float(static_cast<uint32_t>(tm.max_of(sm.misc, 2))), M, rc.T, rounds,
+                   rc.V, sm.misc + kMRowLo, sm.misc + kMRowHi);
+  }
   unsigned long long rb = 0, first = 0;
   if (n <= static_cast<uint32_t>(kTopKMax)) {
     // all of it fits the survivors' place: divided by T on the way there.  What lies between the
     // raw bound and the cut takes part in top-p, and the cut is raised to min-p's behind it.
-    unsigned long long S = 0;
     for (uint32_t i = lane; i < segcnt[warp]; i += 32) {
       const unsigned long long r = sm.cw[warp * kRSeg + i];
       const float x = kfloat(static_cast<uint32_t>(r >> 32));
       const float y = __fadd_rn(rc.identity ? x : rdiv(x, rc.div), 0.0f);
       sm.wbuf[at + i] = (static_cast<unsigned long long>(fkey(y)) << 32) | (r & 0xFFFFFFFFull);
-      if (topp_on) S += fixed_mass(softmax_weight(y, M));
     }
     Thresh th = kKeepAll;
-    if (topp_on) {
-      S = rblock_sum_u64(S, sm.red) + below;
-      if (threadIdx.x == 0) sm.misc[kMRowMass] = S;  // published by the barriers of rk_topp
-      th = rk_topp<true>(sm.wbuf, static_cast<int>(n), M, p, sm.hist, sm.cw, sm.red, sm.misc);
-    } else {
-      __syncthreads();
-    }
+    __syncthreads();
+    if (kTopP) th = rm_topp<kBF16>(whole, sm, static_cast<int>(n), M, p);
     rlist_race(sm.wbuf, static_cast<int>(n), with_min_p(th, ln_mp, M), M, rc, eps, rb, first);
     rblock_max2(rb, first, sm.red);
     return static_cast<int32_t>(~static_cast<uint32_t>(rb ? rb : first));
@@ -1659,17 +1700,10 @@ __device__ __noinline__ int32_t rm_row(const RowCtx& rc, const RowSmem& sm, cons
   Thresh th = with_min_p(kKeepAll, ln_mp, M);
   const unsigned long long* list = sm.cw;
   int len = kRCap;
-  if (topp_on) {
-    unsigned long long S = 0;
-    for (int i = threadIdx.x; i < kRCap; i += kRT) {
-      const uint32_t key = static_cast<uint32_t>(sm.cw[i] >> 32);
-      if (key) S += fixed_mass(softmax_weight(kfloat(key), M));
-    }
-    S = rblock_sum_u64(S, sm.red) + below;
-    if (threadIdx.x == 0) sm.misc[kMRowMass] = S;  // published by the gather's barriers
+  if (kTopP) {
     const int ns = rbuf_gather(sm.cw, kRCap, th, sm.wbuf, kTopKMax, sm.red);
     if (ns < kTopKMax) {
-      th = rk_topp<true>(sm.wbuf, ns, M, p, sm.hist, sm.cw, sm.red, sm.misc);
+      th = rm_topp<kBF16>(whole, sm, ns, M, p);
       list = sm.wbuf;
       len = ns;
     } else {
@@ -1680,10 +1714,11 @@ __device__ __noinline__ int32_t rm_row(const RowCtx& rc, const RowSmem& sm, cons
           sm.cw[i] = 0ull;
       }
       const int nk = rcompact_nonzero(sm.cw, sm.red);
-      if (nk > kRSortMax) return rexact_min_p_row<kBF16>(whole, sm, topp_on, p, mp, eps);
+      if (nk > kRSortMax) return rexact_min_p_row<kBF16>(whole, sm, kTopP, p, mp, eps);
       int N = 1;
       while (N < nk) N <<= 1;
       rbitonic_desc(sm.cw, N);
+      const unsigned long long S = rm_mass<kBF16>(whole, M, sm.red);
       const int L = rlist_topp_cut(sm.cw, nk, M, 0ull, rtopp_target(p, S), sm.red, sm.misc);
       if (L > 0) th = Thresh{static_cast<uint32_t>(sm.cw[L - 1] >> 32), static_cast<int32_t>(~static_cast<uint32_t>(sm.cw[L - 1]))};
       len = nk;
@@ -2767,7 +2802,8 @@ __global__ void __launch_bounds__(kRT, 2) kps_row_kernel(const Params P) {
     const RowFlags f = row_setup<kBF16>(P, row, sm, tm.rank, tm.C, &rc, sample);
     int32_t chosen;
     if (min_p_alone) {
-      chosen = rm_row<kBF16>(rc, sm, tm, f.topp_on, f.p, P.eps, P.exact != 0);
+      chosen = f.topp_on ? rm_row<kBF16, true>(rc, sm, tm, f.p, P.eps, P.exact != 0)
+                         : rm_row<kBF16, false>(rc, sm, tm, f.p, P.eps, P.exact != 0);
     } else if (!wide) {
       chosen = rk_row<kBF16>(rc, sm, tm, f.single ? 1u : static_cast<uint32_t>(f.k), f.single, f.topp_on, f.p, P.eps,
                              P.exact != 0, sample);

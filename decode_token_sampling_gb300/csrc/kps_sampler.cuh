@@ -67,6 +67,7 @@
 #include "kps.h"
 #include "kps_fixed.h"
 #include "kps_div.h"
+#include "kps_stream.cuh"
 #include "kps_weights.cuh"
 #include "kps_host.h"
 

@@ -328,3 +328,37 @@ def test_graph_replay():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("penalty", [None, 1.2])
+def test_top_p_border_repeats_to_the_bit(dtype, penalty):
+    """Rows alike but for top_p, whose values are the floats around the share of a prefix: the target is one
+    sum of fixed-point masses, so every call keeps the same set, and so does the selection over the
+    whole row (KERNEL_ROW_EXACT)."""
+    import torch
+    import decode_token_sampling_gb300 as kps
+    B, V = 96, 32768
+    for seed in range(6):
+        inp = make_random(B, V, seed=40 + seed, dtype=dtype, scale=3.0, k_range=(0, 0), penalty=penalty, n_seen=300)
+        inp.top_k[:] = 0
+        inp.logits[:] = inp.logits[0]
+        inp.temperature[:] = inp.temperature[0]
+        if penalty is not None:
+            inp.seen_ids = np.tile(inp.seen_ids[:300], B)
+        inp.top_p[:] = 0.9
+        t = oracle.row_terms(inp, 0)
+        e = t["e"]
+        n = int((e >= 0.02).sum())
+        # from half a unit in the last place to 2^-13 away on both sides, of a border inside the list and of its end
+        p = np.cumsum(e)[n // 2 if seed % 2 else n - 1] / t["S"]
+        away = np.arange(B) - B / 2 + 0.5
+        inp.top_p[:] = p * (1 + np.sign(away) * 2.0 ** (-25 + 12 * np.abs(away) / (B / 2)))
+        mp = np.full(B, 0.02, np.float32)
+        runs = [run(inp, mp, kernel) for kernel in (kps.KERNEL_ROW_EXACT, kps.KERNEL_ROW, kps.KERNEL_ROW, kps.KERNEL_ROW, kps.KERNEL_AUTO)]
+        for idx, filt in runs[1:]:
+            assert np.array_equal(idx, runs[0][0]) and np.array_equal(filt, runs[0][1])
+        kept = (runs[0][1] > -np.inf).sum(1)
+        border = n // 2 + 1 if seed % 2 else n  # tokens up to the border's
+        assert kept.min() == border and kept.max() == (border + 1 if seed % 2 else n)
