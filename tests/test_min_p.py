@@ -362,3 +362,47 @@ def test_top_p_border_repeats_to_the_bit(dtype, penalty):
         kept = (runs[0][1] > -np.inf).sum(1)
         border = n // 2 + 1 if seed % 2 else n  # tokens up to the border's
         assert kept.min() == border and kept.max() == (border + 1 if seed % 2 else n)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_whose_mass_has_no_estimate(dtype):
+    """Rows that rise by steps, hold NaN, a mask's value almost everywhere, magnitudes whose quotients
+    lose their digits, or an extreme temperature: the kept set is the exact selection's all the same."""
+    import decode_token_sampling_gb300 as kps
+    B, V = 80, 24576
+    inp = make_random(B, V, seed=60, dtype="f32", scale=2.0, k_range=(0, 0), p_range=(0.3, 0.99))
+    inp.top_k[:] = 0
+    r = np.random.default_rng(61)
+    x = inp.logits
+    low = -3.3895314e38
+    for b in range(B):
+        kind = b % 10
+        if kind == 0:
+            x[b] += np.floor(np.arange(V) / V * 6) * (20.0 + b)  # each step past the last one's unit
+        elif kind == 1:
+            x[b, r.integers(0, V, 5)] = np.nan
+        elif kind in (2, 3, 4):
+            keep = r.integers(0, V, 50)
+            kept = x[b, keep].copy()
+            x[b] = (-np.inf, -1e4, low)[kind - 2]
+            x[b, keep] = kept
+        elif kind == 5:
+            x[b] += (1e3, -1e4, 1e5, -3e5)[b // 10 % 4]
+        elif kind == 6:
+            inp.temperature[b] = (1e-30, 1e-20, 1e20, 1e31)[b // 10 % 4]
+        elif kind == 7:
+            x[b] = low
+            x[b, :3] = (5.0, 4.5, 4.0)
+        elif kind == 8:
+            x[b] = 0.001 * x[b]  # thousands of survivors
+        else:
+            x[b, : V // 2] -= 90.0
+    if dtype == "bf16":
+        inp.logits, inp.dtype = f32_to_bf16_bits(x), "bf16"
+    mp = r.uniform(0.01, 0.3, B).astype(np.float32)
+    mp[8::10] = 0.98
+    runs = [run(inp, mp, kernel) for kernel in (kps.KERNEL_ROW_EXACT, kps.KERNEL_ROW, kps.KERNEL_ROW)]
+    for idx, filt in runs[1:]:
+        assert np.array_equal(idx, runs[0][0]) and np.array_equal(filt, runs[0][1])
+    check(inp, mp, kps.KERNEL_ROW, most_near=0.3)
