@@ -600,3 +600,39 @@ def test_gradient_rows_share_the_students_phase(dtype):
                 assert (grad[i].data_ptr() - student[i].data_ptr()) % 16 == 0
             if ld == V and off == 0:
                 assert grad.is_contiguous()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rest", [False, True])
+def test_small_divergence_to_a_hundredth(dtype, rest):
+    """A student next to its teacher, logits on a grid that makes every difference exact: the error left is
+    that of the masses.  With e = 2^-22 + 2^-23 (an exponential and the roundings behind it), a share P
+    of the two rests together, each a sum whose terms of exponent z are off by (2 u z + 2^-22) ln 2 and
+    which adds (V / 2048 + 16) roundings, the loss is off by
+    tau^2 (2 e + e' P + 16 u (1 + sum p |ln p - ln q|)) at most."""
+    import decode_token_sampling_gb300 as kps
+    V, K, N, tau = 4096, 64, 40, 1.0
+    step = 2.0 ** (-8 if dtype == torch.float32 else -4)
+    g = torch.Generator("cuda").manual_seed(33)
+    t = torch.randn(N, V, device="cuda", generator=g) - (0.0 if rest else 9.0)
+    t[:, :K] = 6.0 + 1.5 * torch.randn(N, K, device="cuda", generator=g)
+    t = (t.clamp(-15.0, 12.0) / step).round() * step
+    noise = torch.randint(-6, 7, (N, V), device="cuda", generator=g) * step
+    s = (t + noise).to(dtype)
+    assert torch.equal(s.float(), t + noise)
+    ids = torch.arange(K, device="cuda", dtype=torch.int32).repeat(N, 1)
+    val = t[:, :K].contiguous()
+    r = torch.logsumexp(t[:, K:].double(), 1).float() if rest else None
+    want, _, _, _ = distill_reference(s, ids, val, tau, r)
+    a, b = torch.log_softmax(t.double(), 1), torch.log_softmax(s.double(), 1)
+    P = a[:, K:].exp().sum(1) + b[:, K:].exp().sum(1)
+    e = 2.0 ** -22 + 2.0 ** -23
+    z = 40 * 1.4427  # no logit lies further below the list's largest
+    e_rest = (2 * U * z + 2.0 ** -22) * 0.6932 + (V / 2048 + 16) * U
+    spread = (a[:, :K].exp() * (a - b)[:, :K].abs()).sum(1)
+    tol = tau * tau * (2 * e + e_rest * P + 16 * U * (1 + spread))
+    assert bool((tol <= want / 10).all())  # a bound that a wrong loss would not meet
+    kw = dict(temperature=tau, rest=r)
+    for got in (kps.distill_forward(s, ids, val, **kw)[0], kps.distill_loss_grad(s, ids, val, **kw)[0]):
+        _compare(got.double(), want, tol, "loss")
