@@ -93,8 +93,9 @@ __host__ __device__ inline Layout make_layout(int K, int64_t chunk, bool distinc
   return L;
 }
 
-__device__ __forceinline__ float teacher_value(const void* values, bool bf16, int64_t i) {
-  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(values)[i]) : static_cast<const float*>(values)[i];
+__device__ __forceinline__ float teacher_value(const Params& P, int64_t i) {
+  return P.values_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(P.values)[i])
+                       : static_cast<const float*>(P.values)[i];
 }
 
 // The block's sum; every thread gets it.
@@ -116,9 +117,6 @@ __device__ __forceinline__ void add_one(Sum2& sum, float x, float c) {
   if ((x - sum.ref) * c > kRaise) sum.raise(clamp_ref(x), c);
   sum.s += ex2((x - sum.ref) * c);
 }
-
-// log2(1 + 2^z).
-__device__ __forceinline__ float log2_1p_ex2(float z) { return z > 24.0f ? z : kLog2e * log1pf(ex2(z)); }
 
 // ---- the list, to more than fp32's rounding of its exponents ----------------------------------
 //
@@ -177,9 +175,10 @@ __device__ __forceinline__ float log2_ratio(F2 a, float b, F2 c, float d) {
   return log2f(q) + kLog2e * ((fmaf(-q, c.h, a.h) + a.l) / a.h - c.l / c.h);
 }
 
-// The teacher's side of a row against the reference tref: E = sum e_k, W = sum e_k (u_k - v_k), with
-// e_k = 2^(u_k), u_k and v_k the exponents of the teacher's value and the student's logit; the
-// rest's e_r = 2^(uh + ul).
+// The teacher's side of a row against the reference tref: E = sum e_k, W = sum e_k (t_k - s_k) / kWScale,
+// t_k and s_k the teacher's value and the student's logit from their references (scaled so that no sum
+// of them overflows) and e_k = 2^(t_k c); the rest's e_r = 2^(uh + ul).
+constexpr float kWScale = 4096.0f;
 struct Teacher {
   F2 E, W;
   float er, uh, ul;
@@ -207,79 +206,43 @@ __device__ __forceinline__ bool precise(const Sum2& rest, const Sum2& list, floa
   return rest.s >= 0x1p-60f || (er == 0.0f && rest.s >= 0.0f && list.s >= 0.5f);
 }
 
-// The divergence in base 2.  list (against ref), rest, all: the student's sums.
+// The divergence times the temperature.  list (against ref), rest, all: the student's sums.  Distances
+// between references stay in units of logits: in exponents of 2 those of the type's lowest value (a
+// masked student) would leave fp32 where the loss does not.
 __device__ __forceinline__ float divergence(const Teacher& t, float ref, const F2& list, const Sum2& rest,
-                                            const Sum2& all, float c) {
-  const float moved = (all.ref - ref) * c, E = t.E.value(), W = t.W.value();
+                                            const Sum2& all, float tau, float c) {
+  const float unit = tau * kLn2, moved = all.ref - ref;  // of an exponent of 2
+  const float E = t.E.value(), W = t.W.value();
   // (list and rest against one reference: their sum as two floats)
   const bool same = rest.ref == ref;
   const F2 head = same ? list : F2{all.s, 0.0f};
   const float tail = same ? rest.s : 0.0f;
-  if (t.er == 0.0f) return W / E + log2_ratio(head, tail, t.E, 0.0f) + moved;
+  if (t.er == 0.0f) return W / E * kWScale + unit * log2_ratio(head, tail, t.E, 0.0f) + moved;
   if (rest.s == 0.0f) return INFINITY;  // the teacher's rest has mass, the student's none
   const float Et = E + t.er, pr = t.er / Et;
   // D = (uh + ul) - log2 of the student's rest against ref, whole powers of two first
   const uint32_t bits = __float_as_uint(rest.s);
   const float k = static_cast<float>(static_cast<int>(bits >> 23) - 127);
   const float m = __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u);
-  const float D = ((t.uh - k) + t.ul) - log2f(m) - (rest.ref - ref) * c;
-  if (!(pr >= 0.5f)) return (W + t.er * D) / Et + log2_ratio(head, tail, t.E, t.er) + moved;
+  const float D = unit * (((t.uh - k) + t.ul) - log2f(m)) - (rest.ref - ref);
+  if (!(pr >= 0.5f))
+    return (W + t.er * (D * (1.0f / kWScale))) / Et * kWScale + unit * log2_ratio(head, tail, t.E, t.er) + moved;
   // most mass is the rest's: ln p_r and ln q_r from what they leave, so that two numbers near
   // zero are not differences of large ones
   const float S = list.value();
-  const float q = S > 0.0f ? log2_1p_ex2(log2f(S / rest.s) + (ref - rest.ref) * c) : 0.0f;
-  return W / Et - E / Et * D - kLog2e * log1pf(E / t.er) + q;
+  float q = 0.0f;
+  if (S > 0.0f) {
+    const float s = log2f(S / rest.s), z = s + (ref - rest.ref) * c;
+    q = z > 24.0f ? unit * s + (ref - rest.ref) : tau * log1pf(ex2(z));
+  }
+  return W / Et * kWScale - E / Et * D - tau * log1pf(E / t.er) + q;
 }
 
-// The loss by its definition in 64 bits, by one warp: for rows where the form above meets an infinity.
-// That is a loss of +inf, or one whose parts leave fp32 (or cancel as infinities) while the loss does
-// not: a student of -inf or the type's lowest value all over the list, a list without mass.  As in
-// fp32, a class whose mass is below 2^-126 of the largest has none.
-// (Its arguments go in registers: a reference to the kernel's parameters would cost every row a copy.)
-template <bool kBF16>
-__device__ __noinline__ float plain_loss(const void* student, const int32_t* ids, const void* values, bool values_bf16,
-                                         int V, int K, float temperature, float w, float r, Sum2 all, Sum2 rest) {
-  const RowView<kBF16> x(student, 0, V);
-  const int lane = threadIdx.x & 31;
-  const double tau = temperature;
-  const double L = all.ref / tau + log(static_cast<double>(all.s));
-  double m = r;
-  auto each = [&](auto&& f) {  // f(exponent of the teacher's value, token) of the lane's filled slots
-    for (int k = lane; k < K; k += 32) {
-      const int32_t id = ids[k];
-      const float t = teacher_value(values, values_bf16, k);
-      if (id >= 0 && id < V && t != -INFINITY) f(t / tau, id);
-    }
-  };
-  auto sum = [](double v) {
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-  };
-  each([&](double u, int32_t) { m = fmax(m, u); });
-  for (int o = 16; o; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-  double Z = 0.0, kl = 0.0;
-  each([&](double u, int32_t) { Z += exp(u - m); });
-  Z = sum(Z) + exp(r - m);
-  auto term = [&](double u, double a) {  // p (ln p - ln q) of a class of the student's log-sum-exp a
-    const double e = exp(u - m);
-    return e < 0x1p-126 ? 0.0 : e / Z * (u - m - log(Z) - a + L);
-  };
-  each([&](double u, int32_t id) { kl += term(u, x.at(id) / tau); });
-  kl = sum(kl) + term(r, rest.ref / tau + log(static_cast<double>(rest.s)));
-  return static_cast<float>(w * tau * tau * kl);
-}
-
-// The row's loss; all 32 lanes of a warp call it with the same arguments.
-template <bool kBF16>
-__device__ __forceinline__ float row_loss(const Params& P, int64_t row, const Teacher& T, float ref, const F2& list,
-                                          const Sum2& rest, const Sum2& all, float w, float r) {
-  if (!(all.s > 0.0f && all.s < INFINITY)) return NAN;
-  const float kl = divergence(T, ref, list, rest, all, P.c);
-  if (fabsf(kl) < INFINITY) return w * P.tau * P.tau * (kl * kLn2);
-  const int64_t slot = row * P.K;
-  return plain_loss<kBF16>(static_cast<const unsigned char*>(P.student) + row * P.ld * (kBF16 ? 2 : 4), P.ids + slot,
-                           static_cast<const unsigned char*>(P.values) + slot * (P.values_bf16 ? 2 : 4), P.values_bf16,
-                           P.V, P.K, P.tau, w, r, all, rest);
+// The row's loss.
+__device__ __forceinline__ float row_loss(const Params& P, const Teacher& T, float ref, const F2& list, const Sum2& rest,
+                                          const Sum2& all, float w) {
+  const bool ok = all.s > 0.0f && all.s < INFINITY;
+  return ok ? w * P.tau * divergence(T, ref, list, rest, all, P.tau, P.c) : NAN;
 }
 
 // Writes zeros to this CTA's part of a row of the gradient.
@@ -345,7 +308,7 @@ struct Slot {
   float t;
 };
 __device__ __forceinline__ Slot read_slot(const Params& P, int64_t row, int k) {
-  return Slot{P.ids[row * P.K + k], teacher_value(P.values, P.values_bf16, row * P.K + k)};
+  return Slot{P.ids[row * P.K + k], teacher_value(P, row * P.K + k)};
 }
 __device__ __forceinline__ Slot first_slot(const Params& P, int64_t row) {
   return static_cast<int>(threadIdx.x) < P.K ? read_slot(P, row, threadIdx.x) : Slot{-1, -INFINITY};
@@ -386,12 +349,12 @@ __device__ __forceinline__ void read_slots(const Params& P, int64_t row, const V
   }
 }
 // The references: the teacher's largest class (its rest in nats at tau included), and the largest
-// student logit among the list's tokens.
+// student logit among the list's tokens (0 where all of them are -inf).
 __device__ __forceinline__ float teacher_ref(const uint32_t* top, float r, float tau) {
   return clamp_ref(fmaxf(top[0] ? order_value(top[0]) : -INFINITY, r * tau));
 }
 __device__ __forceinline__ float student_ref(const uint32_t* top) {
-  return clamp_ref(top[1] ? order_value(top[1]) : -INFINITY);
+  return top[1] > order_key(-INFINITY) ? clamp_ref(order_value(top[1])) : 0.0f;
 }
 // The slots' masses in the place of their values, and each warp's part of E, W and the student's sum
 // over the list (its distinct tokens).
@@ -407,7 +370,7 @@ __device__ __forceinline__ void slot_masses(const Params& P, int K, float tref, 
       e = mass(t, tref, P.c, P.c_lo);
       q = mass(sv, ref, P.c, P.c_lo);
       E.add(e);
-      if (e != 0.0f) W.add(e * (((t - tref) - (sv - ref)) * P.c));  // NaN stays (e is NaN then)
+      if (e != 0.0f) W.add(e * (((t - tref) - (sv - ref)) * (1.0f / kWScale)));  // NaN stays (e is NaN then)
       bool first = true;  // a token of several slots counts once
       if (dup)
         for (int j = 0; j < k; ++j) first = first && s_id[j] != id;
@@ -669,10 +632,8 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
       if (moving || (fabsf(ref * c) <= kFastRef && precise(rest, list, T.er) && all.s <= 0x1p100f)) break;
       if (CS > 1) cg::this_cluster().sync();  // the parts are read
     }
-    float loss = 0.0f;
-    if (rank == 0 && threadIdx.x < 32) loss = row_loss<kBF16>(P, row, T, ref, S, rest, all, w, r);
     if (rank == 0 && threadIdx.x == 0) {
-      P.loss[row] = loss;
+      P.loss[row] = row_loss(P, T, ref, S, rest, all, w);
       if (kMode == kForward && P.stats) {
         P.stats[row * kStats] = all.ref;
         P.stats[row * kStats + 1] = all.s;
@@ -968,10 +929,7 @@ __global__ void __launch_bounds__(kNT, 4) distill_resident_kernel(const Params P
     if (threadIdx.x == 0 && g1 > g0)
       copy_out(const_cast<uint4*>(o.vec) + g0, smem, static_cast<uint32_t>(g1 - g0) * 16u);
   }
-  if (rank == 0 && threadIdx.x >= kNT - 32) {  // not the warp that stores the row
-    const float loss = row_loss<kBF16>(P, row, T, ref, S, rest, all, w, r);
-    if (lane == 0) P.loss[row] = loss;
-  }
+  if (rank == 0 && threadIdx.x == kNT - 1) P.loss[row] = row_loss(P, T, ref, S, rest, all, w);
   if (late) copy_landed(&landed);  // one more wait before the block leaves
 }
 

@@ -534,6 +534,7 @@ def _finite_grad(s, ids, val, tau, rest, weight=None):
 def test_student_without_the_lists_tokens(dtype, tau, K):
     """-inf or the type's lowest value at every token of the teacher's list, or at one of them: a loss of
     +inf, or a huge one; next to no mass in the list: the loss of the rest alone."""
+    import decode_token_sampling_gb300 as kps
     s, ids, val, r = _case(6, 3000, K, dtype, "cuda", seed=31)
     lowest = torch.finfo(dtype).min
     for value in (-math.inf, lowest, -1e9):
@@ -543,10 +544,25 @@ def test_student_without_the_lists_tokens(dtype, tau, K):
         w = torch.full((6,), 0.25 if value == lowest else 1.0, device="cuda")
         for rest in (None, r, r + 3.0, r - 3.0):
             _finite_grad(x, ids, val, tau, rest, w)
+    # the lowest value everywhere but in the list: a loss of the rest's share of it, and a gradient that
+    # is that share in equal parts (64 bits lose the logarithm of their number beside the lowest value)
+    x = torch.full_like(s, lowest).scatter_(1, ids.long(), s.gather(1, ids.long()))
+    for rest in (r, r + 3.0, r - 3.0):
+        kw = dict(temperature=tau, rest=rest, weight=torch.full((6,), 0.25, device="cuda"))
+        want, _, _, _ = distill_reference(x, ids, val, tau, rest, kw["weight"])
+        loss, stats = kps.distill_forward(x, ids, val, **kw)
+        loss2, grad = kps.distill_loss_grad(x, ids, val, **kw)
+        back = kps.distill_backward(None, x, ids, val, stats, **kw)
+        for got in (loss, loss2):
+            _compare(got.double(), want, 1e-5 * want.abs(), "loss")
+        p_rest = torch.softmax(torch.cat([val.double() / tau, rest.double()[:, None]], 1), 1)[:, -1]
+        share = (-0.25 * tau * p_rest / (3000 - K))[:, None]
+        for got in (grad, back):
+            outside = got.double().scatter(1, ids.long(), share.expand(6, K))
+            assert bool(((outside - share).abs() <= share.abs() * (1e-5 + torch.finfo(dtype).eps / 2)).all())
     # the teacher's list has no mass that fp32 holds, the student's list none at all
     x = s.clone()
     x.scatter_(1, ids.long(), -math.inf)
-    import decode_token_sampling_gb300 as kps
     far = torch.full((6,), 2000.0, device="cuda")
     loss, stats = kps.distill_forward(x, ids, val, temperature=tau, rest=far)
     loss2, grad = kps.distill_loss_grad(x, ids, val, temperature=tau, rest=far)
