@@ -70,13 +70,13 @@ struct Params {
   int64_t ld_grad;
 };
 
-// Shared memory: the teacher's slots, the hash table of the list's distinct tokens and the bitmap
-// of the list's tokens in this CTA's part of the row (rest).
+// Shared memory: the teacher's slots, the hash table of the list's distinct tokens and, for the
+// student's sum, the bitmap of the list's tokens in this CTA's part of the row.
 struct Layout {
   size_t id, e, v, hash, bits, total;
   int hash_size;
 };
-__host__ __device__ inline Layout make_layout(int K, int64_t chunk, bool distinct, bool rest) {
+__host__ __device__ inline Layout make_layout(int K, int64_t chunk, bool bitmap) {
   Layout L;
   size_t off = 0;
   const size_t k4 = (static_cast<size_t>(K) * 4 + 15) / 16 * 16;
@@ -86,9 +86,9 @@ __host__ __device__ inline Layout make_layout(int K, int64_t chunk, bool distinc
   L.hash_size = 32;
   while (L.hash_size < 2 * K) L.hash_size *= 2;
   L.hash = off;
-  if (distinct) off += static_cast<size_t>(L.hash_size) * 4;
+  off += static_cast<size_t>(L.hash_size) * 4;
   L.bits = off;
-  if (rest) off += (static_cast<size_t>(chunk) + 31) / 32 * 4 / 16 * 16 + 32;
+  if (bitmap) off += (static_cast<size_t>(chunk) + 31) / 32 * 4 / 16 * 16 + 32;
   L.total = off;
   return L;
 }
@@ -317,7 +317,7 @@ __device__ __forceinline__ Slot first_slot(const Params& P, int64_t row) {
 // teacher's values and the student's logits to shared memory, the distinct tokens to the table, the
 // keys of both largest values to top[], flags[0] set where a slot is filled and flags[1] where a
 // token has two; visit(k, id) for the filled ones.  Warps without slots do nothing.
-template <bool kDistinct, class View, class Visit>
+template <class View, class Visit>
 __device__ __forceinline__ void read_slots(const Params& P, int64_t row, const View& x, Slot slot, int32_t* s_id, float* s_e,
                                            float* s_v, int32_t* s_hash, int hash_size, uint32_t* top, int* flags,
                                            Visit&& visit) {
@@ -334,7 +334,7 @@ __device__ __forceinline__ void read_slots(const Params& P, int64_t row, const V
       flags[0] = 1;
       if (!isnan(slot.t)) tk = max(tk, order_key(slot.t));
       if (!isnan(s)) sk = max(sk, order_key(s));
-      if (kDistinct && insert_token(s_hash, hash_size, id)) flags[1] = 1;
+      if (insert_token(s_hash, hash_size, id)) flags[1] = 1;
       visit(k, id);
     }
     k += kNT;
@@ -482,12 +482,12 @@ __device__ __forceinline__ uint32_t listed_bits(const unsigned char* bytes, int 
 }
 // The thread's sum over vectors [g0, g1) of a row, without the list's tokens, and one logit more,
 // with a reference that moves up: for rows whose list lies far from everything else.
-template <bool kBF16, bool kRest>
+template <bool kBF16>
 __device__ __noinline__ Sum2 moving_sum(const RowView<kBF16>& x, int g0, int g1, const unsigned char* bytes, float one, float c) {
   Sum2 sum{-FLT_MAX, 0.0f};
   for (int g = g0 + static_cast<int>(threadIdx.x); g < g1; g += kNT) {
     uint4 v = ld_stream(x.vec + g);
-    if (kRest) drop_listed<kBF16>(v, listed_bits<kBF16>(bytes, g - g0, true));
+    drop_listed<kBF16>(v, listed_bits<kBF16>(bytes, g - g0, true));
     const float m = vec_max<kBF16>(v);
     if ((m - sum.ref) * c > kRaise) sum.raise(clamp_ref(m), c);
     add_vec<kBF16>(sum, v, c);
@@ -496,7 +496,8 @@ __device__ __noinline__ Sum2 moving_sum(const RowView<kBF16>& x, int g0, int g1,
   return sum;
 }
 
-template <bool kBF16, bool kRest, int kMode>
+// kRest (backward): whether the teacher has a rest; the loss's modes always split the row's sum (launch).
+template <bool kBF16, int kMode, bool kRest = true>
 __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const Params P) {
   constexpr int G = kBF16 ? 8 : 4, kU = Flight<kMode>::loads;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -505,7 +506,7 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
   __shared__ F2 sums[kNW][3];        // per warp: E, W and the student's sum over the list
   __shared__ uint32_t top[2];
   __shared__ int flags[2];
-  constexpr bool kDistinct = kMode != kForward || kRest;  // the list's distinct tokens are needed
+  static_assert(kRest || kMode == kBackward);
   const int CS = static_cast<int>(cg::this_cluster().num_blocks());
   const int rank = static_cast<int>(cg::this_cluster().block_rank());
   const int64_t row = blockIdx.x / CS;
@@ -518,7 +519,7 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
   const RowView<kBF16> x(P.student, row * P.ld, V);
   const int g0 = static_cast<int>(static_cast<int64_t>(x.nv) * rank / CS);
   const int g1 = static_cast<int>(static_cast<int64_t>(x.nv) * (rank + 1) / CS);
-  const Layout lay = make_layout(K, (V + CS - 1) / CS + 4 * G, kDistinct, kRest);
+  const Layout lay = make_layout(K, (V + CS - 1) / CS + 4 * G, kMode != kBackward);
   int32_t* s_id = reinterpret_cast<int32_t*>(smem + lay.id);
   float* s_e = reinterpret_cast<float*>(smem + lay.e);
   float* s_v = reinterpret_cast<float*>(smem + lay.v);
@@ -534,10 +535,9 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
     top[threadIdx.x] = 0u;
     flags[threadIdx.x] = 0;
   }
-  if (kRest && kMode != kBackward)
+  if (kMode != kBackward)
     for (int i = threadIdx.x; i < (nbits + 31) / 32; i += kNT) s_bits[i] = 0u;
-  if (kDistinct)
-    for (int i = threadIdx.x; i < lay.hash_size; i += kNT) s_hash[i] = -1;
+  for (int i = threadIdx.x; i < lay.hash_size; i += kNT) s_hash[i] = -1;
   // (the slots of a row of weight 0 are read all the same: their loads need not wait for the weight's)
   Slot slot = first_slot(P, row);
   const float w = P.weight ? P.weight[row] : 1.0f;
@@ -547,9 +547,9 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
   scale *= P.tau;
   __syncthreads();
   if (w != 0.0f)
-    read_slots<kDistinct>(P, row, x, slot, s_id, s_e, s_v, s_hash, lay.hash_size, top, flags, [&](int, int32_t id) {
+    read_slots(P, row, x, slot, s_id, s_e, s_v, s_hash, lay.hash_size, top, flags, [&](int, int32_t id) {
       const int b = id - bit0;
-      if (kRest && kMode != kBackward && b >= 0 && b < nbits) atomicOr(&s_bits[b >> 5], 1u << (b & 31));
+      if (kMode != kBackward && b >= 0 && b < nbits) atomicOr(&s_bits[b >> 5], 1u << (b & 31));
     });
   __syncthreads();
   if (kShare && CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
   const float ref = kMode == kBackward ? all.ref : student_ref(top);
   slot_masses(P, K, tref, ref, dup, s_id, s_e, s_v, sums);  // read after the barriers below
 
-  // ---- the student's sum outside the list (kRest; of the whole row else) ----------------------
+  // ---- the student's sum outside the list --------------------------------------------------------
   // Against the list's largest logit, one reference for the whole row and near its top.  A sum that
   // leaves fp32's range (the list far from everything else) is taken again with moving references.
   if (kMode != kBackward) {
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
     const bool loose = static_cast<int>(threadIdx.x) < x.loose() &&
                        ((x.loose_at(threadIdx.x) < x.head) ? rank == 0 : rank == CS - 1);
     const int lv = loose ? x.loose_at(threadIdx.x) : 0;
-    const bool loose_out = loose && !(kRest && ((s_bits[(lv - bit0) >> 5] >> ((lv - bit0) & 31)) & 1u));
+    const bool loose_out = loose && !((s_bits[(lv - bit0) >> 5] >> ((lv - bit0) & 31)) & 1u);
     FastSum<kBF16> fast(fabsf(ref * c) <= kFastRef ? ref : 0.0f, c);
     for (int base = g0; base < g1; base += kNT * kU) {
       uint4 v[kU];
@@ -593,13 +593,11 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
         const int g = base + u * kNT + static_cast<int>(threadIdx.x);
         v[u] = g < g1 ? ld_stream(x.vec + g) : neg_inf_vec<kBF16>();
       }
-      if (kRest) {
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const int g = base + u * kNT + static_cast<int>(threadIdx.x);
-          const uint32_t m = listed_bits<kBF16>(bytes, g - g0, g < g1);
-          if (m) drop_listed<kBF16>(v[u], m);
-        }
+      for (int u = 0; u < kU; ++u) {
+        const int g = base + u * kNT + static_cast<int>(threadIdx.x);
+        const uint32_t m = listed_bits<kBF16>(bytes, g - g0, g < g1);
+        if (m) drop_listed<kBF16>(v[u], m);
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u) fast.add(v[u]);
@@ -610,11 +608,11 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
     F2 S;
     Sum2 list;
     for (bool moving = false;; moving = true) {
-      if (moving) rest = moving_sum<kBF16, kRest>(x, g0, g1, bytes, loose_out ? x.at(lv) : -INFINITY, c);
+      if (moving) rest = moving_sum<kBF16>(x, g0, g1, bytes, loose_out ? x.at(lv) : -INFINITY, c);
       rest = block_merge(rest, c, red);
       if (!moving) {
-        S = collect<kRest>(sums, K, r, tref, P.tau, c, P.c_lo, T);
-        list = Sum2{ref, kRest ? S.value() : 0.0f};
+        S = collect<true>(sums, K, r, tref, P.tau, c, P.c_lo, T);
+        list = Sum2{ref, S.value()};
       }
       if (CS > 1) {
         cg::cluster_group cl = cg::this_cluster();
@@ -627,7 +625,7 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
         rest = Sum2{part[0][0], part[0][1]};
         for (int q = 1; q < CS; ++q) rest = merge(rest, Sum2{part[q][0], part[q][1]}, c);
       }
-      all = kRest ? merge(list, rest, c) : rest;
+      all = merge(list, rest, c);
       // the same in every CTA
       if (moving || (fabsf(ref * c) <= kFastRef && precise(rest, list, T.er) && all.s <= 0x1p100f)) break;
       if (CS > 1) cg::this_cluster().sync();  // the parts are read
@@ -774,7 +772,7 @@ __global__ void __launch_bounds__(kNT, 4) distill_resident_kernel(const Params P
   __syncthreads();
   if (w != 0.0f) {
     if (threadIdx.x == 0 && g1 > g0) copy_in(smem, x.vec + g0, static_cast<uint32_t>(g1 - g0) * 16u, &landed);
-    read_slots<true>(P, row, x, slot, s_id, s_e, s_v, s_hash, R.hash_size, top, flags, [&](int k, int32_t id) {
+    read_slots(P, row, x, slot, s_id, s_e, s_v, s_hash, R.hash_size, top, flags, [&](int k, int32_t id) {
       const int at = id - x.head, vec = at / G - g0;
       if (at >= 0 && vec >= 0 && vec < g1 - g0) s_next[k] = atomicExch(&s_head[vec & (kNT - 1)], k);
     });
@@ -958,7 +956,7 @@ static bool allow_shared(Kernel* kernel, std::atomic<bool>* done) {
   return true;
 }
 
-template <bool kBF16, bool kRest, int kMode>
+template <bool kBF16, int kMode, bool kRest = true>
 static kps_status launch_t(const Params& P, cudaStream_t stream) {
   const int sms = sm_count();
   if (!sms) return KPS_ERR_CUDA;
@@ -966,9 +964,9 @@ static kps_status launch_t(const Params& P, cudaStream_t stream) {
   int cs = 1;
   const int64_t round = static_cast<int64_t>(kNT) * 4 * (kBF16 ? 8 : 4);
   while (cs < kMaxCS && P.N * cs * 2 <= 2 * sms && P.V >= 2 * cs * round) cs *= 2;
-  const Layout lay = make_layout(P.K, (P.V + cs - 1) / cs + 4 * (kBF16 ? 8 : 4), kMode != kForward || kRest, kRest);
+  const Layout lay = make_layout(P.K, (P.V + cs - 1) / cs + 4 * (kBF16 ? 8 : 4), kMode != kBackward);
   static std::atomic<bool> done[kMaxDevices];
-  if (!allow_shared(distill_kernel<kBF16, kRest, kMode>, done)) {
+  if (!allow_shared(distill_kernel<kBF16, kMode, kRest>, done)) {
     (void)cudaGetLastError();
     return KPS_ERR_CUDA;
   }
@@ -984,7 +982,7 @@ static kps_status launch_t(const Params& P, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  if (cudaLaunchKernelEx(&lc, distill_kernel<kBF16, kRest, kMode>, P) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&lc, distill_kernel<kBF16, kMode, kRest>, P) != cudaSuccess) {
     (void)cudaGetLastError();
     return KPS_ERR_CUDA;
   }
@@ -1015,7 +1013,7 @@ static kps_status launch_both(const Params& P, cudaStream_t stream) {
   R.hash = R.head + kNT * 4;
   const size_t total = static_cast<size_t>(R.hash) + R.hash_size * 4;
   // a row's part and the list's arrays have to fit together
-  if (total > kMaxDynamic) return launch_t<kBF16, true, kBoth>(P, stream);
+  if (total > kMaxDynamic) return launch_t<kBF16, kBoth>(P, stream);
   auto* kernel = distill_resident_kernel<kBF16>;
   static std::atomic<bool> done[kMaxDevices];
   if (!allow_shared(kernel, done)) {
@@ -1049,8 +1047,8 @@ static kps_status launch(const Params& P, kps_dtype dt, cudaStream_t stream) {
   // bf16 take 49 us instead of 44).
   if (kMode == kBoth) return dt == KPS_BF16 ? launch_both<true>(P, stream) : launch_both<false>(P, stream);
   if (kMode == kForward || P.rest)
-    return dt == KPS_BF16 ? launch_t<true, true, kMode>(P, stream) : launch_t<false, true, kMode>(P, stream);
-  return dt == KPS_BF16 ? launch_t<true, false, kBackward>(P, stream) : launch_t<false, false, kBackward>(P, stream);
+    return dt == KPS_BF16 ? launch_t<true, kMode>(P, stream) : launch_t<false, kMode>(P, stream);
+  return dt == KPS_BF16 ? launch_t<true, kBackward, false>(P, stream) : launch_t<false, kBackward, false>(P, stream);
 }
 
 // The checks every entry point shares; fills P.  *empty: nothing to do.
