@@ -1085,6 +1085,8 @@ static kps_status check(const void* student, kps_dtype dt, int64_t N, int64_t V,
   return KPS_OK;
 }
 
+static bool float_aligned(const void* p) { return reinterpret_cast<uintptr_t>(p) % alignof(float) == 0; }
+
 // A gradient buffer of its own: rows of at least V elements, sharing no byte with the student's rows.
 static kps_status check_grad(const Params& P, kps_dtype dt, void* grad, int64_t ld_grad) {
   const uintptr_t esize = dt == KPS_BF16 ? 2 : 4;
@@ -1108,7 +1110,7 @@ kps_status kps_distill_forward(const void* student, kps_dtype dt, int64_t N, int
   kps::distill::Params P = {};
   const kps_status st = kps::distill::check(student, dt, N, V, ld, ids, values, values_dt, K, rest, weight, temperature, &P);
   if (st != KPS_OK || N == 0) return st;
-  if (!out_loss) return KPS_ERR_INVALID_ARG;
+  if (!out_loss || !kps::distill::float_aligned(out_loss) || !kps::distill::float_aligned(out_stats)) return KPS_ERR_INVALID_ARG;
   P.loss = out_loss;
   P.stats = out_stats;
   return kps::distill::launch<kps::distill::kForward>(P, dt, stream);
@@ -1122,7 +1124,7 @@ kps_status kps_distill_backward(const void* student, kps_dtype dt, int64_t N, in
   kps::distill::Params P = {};
   kps_status st = kps::distill::check(student, dt, N, V, ld, ids, values, values_dt, K, rest, weight, temperature, &P);
   if (st != KPS_OK || N == 0) return st;
-  if (!stats) return KPS_ERR_INVALID_ARG;
+  if (!stats || !kps::distill::float_aligned(stats) || !kps::distill::float_aligned(grad_loss)) return KPS_ERR_INVALID_ARG;
   if ((st = kps::distill::check_grad(P, dt, out_grad, ld_grad)) != KPS_OK) return st;
   P.upstream = grad_loss;
   P.stats = const_cast<float*>(stats);
@@ -1139,7 +1141,7 @@ kps_status kps_distill_loss_grad(const void* student, kps_dtype dt, int64_t N, i
   kps::distill::Params P = {};
   kps_status st = kps::distill::check(student, dt, N, V, ld, ids, values, values_dt, K, rest, weight, temperature, &P);
   if (st != KPS_OK || N == 0) return st;
-  if (!out_loss) return KPS_ERR_INVALID_ARG;
+  if (!out_loss || !kps::distill::float_aligned(out_loss)) return KPS_ERR_INVALID_ARG;
   if ((st = kps::distill::check_grad(P, dt, out_grad, ld_grad)) != KPS_OK) return st;
   P.loss = out_loss;
   P.grad = out_grad;

@@ -277,7 +277,8 @@ kps_status kps_sample_noalloc(const void* logits, kps_dtype dt, int64_t B, int64
  * workspace and keep nothing between calls; calls are independent of each
  * other, on one stream or several, and may be captured into CUDA graphs.  The
  * device of the pointers must be current.  Pointers must be aligned to their
- * element type; rows on 16-byte boundaries are read fastest, any others work.
+ * element type (KPS_ERR_INVALID_ARG otherwise); rows on 16-byte boundaries are
+ * read fastest, any others work.
  * Errors are as for kps_sample: KPS_ERR_INVALID_ARG, KPS_ERR_UNSUPPORTED (a
  * vocabulary or a row count too large), KPS_ERR_CUDA.
  *
@@ -349,8 +350,9 @@ kps_status kps_top_logits(const void* logits, kps_dtype dt, int64_t B, int64_t V
  * which kps_distill_backward takes with the same other arguments: it writes
  * out_grad [N, V] (dt, rows ld_grad apart), the gradient times grad_loss [N]
  * (NULL: 1; a row of grad_loss 0 gets zeros).  kps_distill_loss_grad does both
- * in one launch, for programs that have all factors in weight.  out_grad must
- * not overlap the student's rows.  Gradients are computed in fp32 and rounded
+ * in one launch, for programs that have all factors in weight.  out_grad, from
+ * its first element to its last, must lie outside the student's first to last
+ * (rows of the two that take turns in one buffer are refused as well).  Gradients are computed in fp32 and rounded
  * once.  (kps_distill_loss_grad copies rows into shared memory; a copy that did
  * not arrive within about two seconds would leave NaN in its row.)
  */

@@ -652,3 +652,13 @@ def test_small_divergence_to_a_hundredth(dtype, rest):
     kw = dict(temperature=tau, rest=r)
     for got in (kps.distill_forward(s, ids, val, **kw)[0], kps.distill_loss_grad(s, ids, val, **kw)[0]):
         _compare(got.double(), want, tol, "loss")
+
+
+def test_misaligned_results_and_statistics_are_refused(lib):
+    """Addresses that the kernels would read or write as floats."""
+    off = ctypes.c_void_p((1 << 28) + 2)
+    assert _forward(lib, loss=off) == 1
+    assert _forward(lib, stats=off) == 1
+    assert _loss_grad(lib, loss=off) == 1
+    assert _backward(lib, stats=off) == 1
+    assert _backward(lib, grad_loss=off) == 1
