@@ -505,7 +505,9 @@ def distill_loss(student: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
     a value of -inf: an empty slot); rest: float32 [N], the log-sum-exp of what the list leaves out
     at the same temperature (None: nothing); weight: float32 [N] (None: 1; rows of weight 0 are not
     read).  The teacher's side and the weights get no gradient: tensors of theirs that require one
-    are refused.  Runs on the current stream.
+    are refused.  First derivatives in reverse mode only: second derivatives, forward mode and vmap
+    raise.  Runs on the current stream.  A captured backward should make its leaves inside the
+    capture, as any autograd graph's; distill_loss_grad needs none.
     """
     for name, t in (("values", values), ("rest", rest), ("weight", weight)):
         if t is not None and t.requires_grad:

@@ -38,9 +38,9 @@ using namespace stream;
 constexpr int kNT = 256;  // threads per CTA
 constexpr int kNW = kNT / 32;
 // 16-byte loads each thread keeps in flight, and the CTAs an SM then holds.  The forward with eight
-// and four took 153 us for 4096 rows of 151936 bf16 (a quarter masked) and 44.2 us for 1024 of
-// 128256, with six and five 152 and 50.2 us, with four and five 154 and 48.4 us; the backward of the
-// latter with six and five 86.2 us, with eight and four 88.1 us, with four and five 92.5 us.
+// and four takes 151 us for 4096 rows of 151936 bf16 (a quarter masked) and 48.7 us for 1024 of
+// 128256, with six and five 150 and 52.3 us, with four and five 162 and 54.0 us; the backward of the
+// latter with six and five 86.5 us, with eight and four 86.0 us, with four and five 96.9 us.
 template <int kMode>
 struct Flight {
   static constexpr int loads = kMode == 0 ? 8 : 6, ctas = kMode == 0 ? 4 : 5;
@@ -125,7 +125,7 @@ __device__ __forceinline__ void add_one(Sum2& sum, float x, float c) {
 // would show.  Exponents of the list's tokens and of the rest are therefore carried as two floats
 // (the sum over the row needs none of that: its terms weigh little where their exponents are large).
 
-// h + l = x - y exactly (l = 0 where the difference is not finite).
+// h + l = x - y exactly (Knuth's two-sum; l = 0 where the difference is not finite).
 __device__ __forceinline__ void two_diff(float x, float y, float& h, float& l) {
   h = x - y;
   const float b = h - x;
@@ -146,7 +146,7 @@ __device__ __forceinline__ float mass(float x, float ref, float c, float c_lo) {
   return ex2_two(z, fabsf(z) < 1e30f ? rest : 0.0f);
 }
 
-// A sum as two floats: h + l.
+// A sum as two floats: h + l (each addition's rounding error by Knuth's two-sum).
 struct F2 {
   float h, l;
   __device__ __forceinline__ void add(float x) {

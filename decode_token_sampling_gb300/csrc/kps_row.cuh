@@ -953,13 +953,14 @@ __device__ __noinline__ int rlist_topp_cut(const unsigned long long* kl, int n, 
   return L;
 }
 
-// Top-p over the survivors kl[0..n) (1 < n <= 1024, maximum M): a fixed-point mass
+constexpr Thresh kUndecided{0u, 0};  // no real cut: keys of numbers are above 0
+
+// Top-p over the survivors kl[0..n) (n <= 1024, maximum M): a fixed-point mass
 // histogram over linear bins of [smallest value, M] finds the bin holding the boundary
 // and that bin's entries are ranked pairwise; a large bin is sorted instead.  Returns
 // the last kept entry.  kRow: p is a share of a mass between misc[kMRowLo] and misc[kMRowHi]
 // instead of the survivors' own sum; every survivor is kept when they do not reach the target;
 // kUndecided when the two bounds do not lead to the same cut.  scratch: 2 * kRRank + 1024 u64.
-constexpr Thresh kUndecided{0u, 0};
 template <bool kRow = false>
 __device__ __noinline__ Thresh rk_topp(unsigned long long* kl, int n, float M, float p, uint32_t* hist,
                                        unsigned long long* scratch, unsigned long long* red,

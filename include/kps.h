@@ -384,7 +384,8 @@ int kps_last_launch_count(void);
  * call of the calling host thread launched (for the cluster kernel: the CTAs
  * that share one row); 0 = none yet.  Matches the cluster_size that
  * kps_query_launch reports for the same (B, V, dt) under the automatic policy
- * whenever that call took the cluster kernel. */
+ * whenever that call took the cluster kernel (calls without min-p: the kernels
+ * with it are compiled apart). */
 int kps_last_cluster_size(void);
 
 /* Static description of a status code. */
