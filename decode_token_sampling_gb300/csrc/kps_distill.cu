@@ -195,7 +195,14 @@ struct Teacher {
     const float a = r * kLog2e, b = tref * c;  // r is in nats at the temperature
     const float al = fmaf(r, kLog2e, -a) + r * 1.92596303e-8f, bl = fmaf(tref, c, -b) + tref * c_lo;
     two_diff(a, b, uh, ul);
-    ul = fabsf(uh) < 1e30f ? ul + (al - bl) : 0.0f;
+    if (fabsf(uh) < 1e30f) {
+      // large logits leave a and b with coarse last places: the low parts are not small beside uh
+      const float lo = ul + (al - bl), h = uh + lo, back = h - uh;
+      ul = (uh - (h - back)) + (lo - back);
+      uh = h;
+    } else {
+      ul = 0.0f;
+    }
     er = ex2_two(uh, ul);
   }
 };

@@ -662,3 +662,20 @@ def test_misaligned_results_and_statistics_are_refused(lib):
     assert _loss_grad(lib, loss=off) == 1
     assert _backward(lib, stats=off) == 1
     assert _backward(lib, grad_loss=off) == 1
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tau", [0.0625, 1.0, 16.0])
+def test_teacher_with_a_rest_far_from_zero(dtype, tau):
+    """Logits whose quotients by the temperature lie far from zero: the rest, a float of that size, and the
+    list's classes differ by a few nats all the same."""
+    import decode_token_sampling_gb300 as kps
+    s, _, _, _ = _case(6, 3000, 8, torch.float32, "cuda", seed=34)
+    g = torch.Generator("cuda").manual_seed(35)
+    t = (s + torch.randn(s.shape, device="cuda", generator=g)) * tau
+    for shift in (-1e3, 3e4, -3e4, 1e6, -1e9):
+        x = (s * tau + shift).to(dtype)
+        top = kps.top_logits((t + shift).contiguous(), 8, temperature=tau)
+        for nudge in (0.0, 3.0, -3.0):
+            check(x, top.ids, top.values, tau, top.rest + nudge)
