@@ -430,6 +430,11 @@ struct Factors {
     return one ? C * a : A * a - B * ex2((s - rest.ref) * c);
   }
 };
+// From the list's masses, against ref, to the whole row's reference (a list of -inf has none, and a
+// reference that may lie far above the row).
+__device__ __forceinline__ float list_factor(const F2& list, float ref, const Sum2& all, float c) {
+  return list.value() == 0.0f ? 0.0f : ex2((ref - all.ref) * c);
+}
 template <bool kBF16>
 __device__ __forceinline__ void put_grad(unsigned char* base, int v, float d) {
   if (kBF16) reinterpret_cast<__nv_bfloat16*>(base)[v] = __float2bfloat16_rn(d);
@@ -654,7 +659,7 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
   // ---- the gradient -------------------------------------------------------------------
   if (kMode != kForward) {
     Teacher T;
-    (void)collect<kRest>(sums, K, r, tref, P.tau, c, P.c_lo, T);
+    const F2 S = collect<kRest>(sums, K, r, tref, P.tau, c, P.c_lo, T);
     const float invE = 1.0f / (T.E.value() + T.er);
     const Factors F(scale, T.er, invE, all, rest, c);
     const RowView<kBF16> o(P.grad, row * P.ld_grad, V);
@@ -693,7 +698,7 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
     __syncthreads();
     const int v0 = rank == 0 ? 0 : x.head + g0 * G, v1 = rank == CS - 1 ? V : x.head + g1 * G;
     put_listed<kBF16>([&](int32_t id) { return id >= v0 && id < v1 ? obase : nullptr; }, dup, K, s_id, s_e, s_v,
-                      F.A * ex2((ref - all.ref) * c), scale * invE);
+                      F.A * list_factor(S, ref, all, c), scale * invE);
   }
 }
 
@@ -927,7 +932,7 @@ __global__ void __launch_bounds__(kNT, 4) distill_resident_kernel(const Params P
         if (id >= v0 && id < v1) return inside;
         return (rank == 0 && id < x.head) || (rank == CS - 1 && id >= v1) ? obase : nullptr;
       },
-      dup, K, s_id, s_e, s_v, F.A * ex2((ref - all.ref) * c), scale * invE);
+      dup, K, s_id, s_e, s_v, F.A * list_factor(S, ref, all, c), scale * invE);
   if (inside != obase) {
     publish_to_copies();
     __syncthreads();

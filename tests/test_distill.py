@@ -679,3 +679,19 @@ def test_teacher_with_a_rest_far_from_zero(dtype, tau):
         top = kps.top_logits((t + shift).contiguous(), 8, temperature=tau)
         for nudge in (0.0, 3.0, -3.0):
             check(x, top.ids, top.values, tau, top.rest + nudge)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shift", [-3e4, -500.0, 500.0, 3e4])
+def test_gradient_of_a_list_without_student_mass(dtype, shift):
+    """-inf at every token of the list and the rest of the row far from zero: the list's gradient is minus its
+    masses, whatever the loss (+inf)."""
+    for K in (1, 12):
+        for V in (500, 100001):
+            s, ids, val, r = _case(4, V, K, torch.float32, "cuda", seed=36)
+            s = (s + shift).to(dtype)
+            s.scatter_(1, ids.long(), -math.inf)
+            for tau in (0.25, 1.0):
+                for rest in (None, r):
+                    _finite_grad(s, ids, val, tau, rest)
