@@ -615,7 +615,8 @@ __global__ void __launch_bounds__(kNT, Flight<kMode>::ctas) distill_kernel(const
       for (int u = 0; u < kU; ++u) fast.add(v[u]);
     }
     rest = Sum2{ref, fast.total(ref, c)};
-    if (loose_out) add_one(rest, x.at(lv), c);
+    // (against the one reference too: a sum of its own would hide, in the merge, that others overflow)
+    if (loose_out) rest.s += ex2((x.at(lv) - ref) * c);
     Teacher T;
     F2 S;
     Sum2 list;

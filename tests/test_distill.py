@@ -695,3 +695,22 @@ def test_gradient_of_a_list_without_student_mass(dtype, shift):
             for tau in (0.25, 1.0):
                 for rest in (None, r):
                     _finite_grad(s, ids, val, tau, rest)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_list_far_below_a_row_whose_largest_logit_lies_outside_the_vectors(dtype):
+    """The first and last logits of rows off a 16-byte boundary are read apart from the others: neither
+    they nor the others may hide how far above the list the row lies."""
+    N, V = 16, 35
+    g = torch.Generator("cuda").manual_seed(37)
+    for top, rest_of_row in ((89.5, 86.0), (86.0, 89.5), (100.0, 87.0), (300.0, 290.0)):
+        s = rest_of_row + torch.rand(N, V, device="cuda", generator=g)
+        s[:, 0] = top
+        s[:, 34] = top - 0.5
+        s[:, 17] = 0.0
+        s = s.to(dtype)
+        ids = torch.full((N, 1), 17, dtype=torch.int32, device="cuda")
+        val = torch.zeros(N, 1, device="cuda")
+        for r in (None, torch.zeros(N, device="cuda"), torch.full((N,), 2.0, device="cuda")):
+            check(s, ids, val, 1.0, r)
