@@ -213,43 +213,43 @@ __device__ __forceinline__ bool precise(const Sum2& rest, const Sum2& list, floa
   return rest.s >= 0x1p-60f || (er == 0.0f && rest.s >= 0.0f && list.s >= 0.5f);
 }
 
-// The divergence times the temperature.  list (against ref), rest, all: the student's sums.  Distances
-// between references stay in units of logits: in exponents of 2 those of the type's lowest value (a
-// masked student) would leave fp32 where the loss does not.
+// The divergence times the temperature, over kWScale.  list (against ref), rest, all: the student's
+// sums.  Distances between references stay in units of logits, scaled: in exponents of 2, or rounded
+// up, those of the type's lowest value (a masked student) would leave fp32 where the loss does not.
 __device__ __forceinline__ float divergence(const Teacher& t, float ref, const F2& list, const Sum2& rest,
                                             const Sum2& all, float tau, float c) {
-  const float unit = tau * kLn2, moved = all.ref - ref;  // of an exponent of 2
+  constexpr float kDown = 1.0f / kWScale;  // a power of 2: no rounding
+  const float unit = tau * kLn2 * kDown, moved = (all.ref - ref) * kDown;  // of an exponent of 2
   const float E = t.E.value(), W = t.W.value();
   // (list and rest against one reference: their sum as two floats)
   const bool same = rest.ref == ref;
   const F2 head = same ? list : F2{all.s, 0.0f};
   const float tail = same ? rest.s : 0.0f;
-  if (t.er == 0.0f) return W / E * kWScale + unit * log2_ratio(head, tail, t.E, 0.0f) + moved;
+  if (t.er == 0.0f) return W / E + unit * log2_ratio(head, tail, t.E, 0.0f) + moved;
   if (rest.s == 0.0f) return INFINITY;  // the teacher's rest has mass, the student's none
   const float Et = E + t.er, pr = t.er / Et;
   // D = (uh + ul) - log2 of the student's rest against ref, whole powers of two first
   const uint32_t bits = __float_as_uint(rest.s);
   const float k = static_cast<float>(static_cast<int>(bits >> 23) - 127);
   const float m = __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u);
-  const float D = unit * (((t.uh - k) + t.ul) - log2f(m)) - (rest.ref - ref);
-  if (!(pr >= 0.5f))
-    return (W + t.er * (D * (1.0f / kWScale))) / Et * kWScale + unit * log2_ratio(head, tail, t.E, t.er) + moved;
+  const float D = unit * (((t.uh - k) + t.ul) - log2f(m)) - (rest.ref - ref) * kDown;
+  if (!(pr >= 0.5f)) return (W + t.er * D) / Et + unit * log2_ratio(head, tail, t.E, t.er) + moved;
   // most mass is the rest's: ln p_r and ln q_r from what they leave, so that two numbers near
   // zero are not differences of large ones
   const float S = list.value();
   float q = 0.0f;
   if (S > 0.0f) {
     const float s = log2f(S / rest.s), z = s + (ref - rest.ref) * c;
-    q = z > 24.0f ? unit * s + (ref - rest.ref) : tau * log1pf(ex2(z));
+    q = z > 24.0f ? unit * s + (ref - rest.ref) * kDown : tau * kDown * log1pf(ex2(z));
   }
-  return W / Et * kWScale - E / Et * D - tau * log1pf(E / t.er) + q;
+  return W / Et - E / Et * D - tau * kDown * log1pf(E / t.er) + q;
 }
 
 // The row's loss.
 __device__ __forceinline__ float row_loss(const Params& P, const Teacher& T, float ref, const F2& list, const Sum2& rest,
                                           const Sum2& all, float w) {
   const bool ok = all.s > 0.0f && all.s < INFINITY;
-  return ok ? w * P.tau * divergence(T, ref, list, rest, all, P.tau, P.c) : NAN;
+  return ok ? w * P.tau * divergence(T, ref, list, rest, all, P.tau, P.c) * kWScale : NAN;
 }
 
 // Writes zeros to this CTA's part of a row of the gradient.

@@ -714,3 +714,19 @@ def test_list_far_below_a_row_whose_largest_logit_lies_outside_the_vectors(dtype
         val = torch.zeros(N, 1, device="cuda")
         for r in (None, torch.zeros(N, device="cuda"), torch.full((N,), 2.0, device="cuda")):
             check(s, ids, val, 1.0, r)
+
+
+@gpu
+@pytest.mark.parametrize("tau", [0.25, 0.5])
+def test_losses_near_the_largest_number(tau):
+    """fp32's lowest value at all of the teacher's mass but 2^-50: the distance is the largest number there is,
+    the loss a quarter of it or less."""
+    N, V, K = 64, 300, 8
+    g = torch.Generator("cuda").manual_seed(38)
+    s = torch.randn(N, V, device="cuda", generator=g)
+    ids = torch.arange(K, device="cuda", dtype=torch.int32).repeat(N, 1)
+    val = torch.randn(N, K, device="cuda", generator=g) * tau
+    val[:, 7] = -35.0 * tau
+    s[:, :7] = torch.finfo(torch.float32).min
+    _finite_grad(s, ids, val, tau, None, torch.full((N,), 0.5, device="cuda"))
+    _finite_grad(s, ids, val, tau, torch.full((N,), -35.0, device="cuda"), torch.full((N,), 0.5, device="cuda"))
