@@ -38,9 +38,9 @@ using namespace stream;
 constexpr int kNT = 256;  // threads per CTA
 constexpr int kNW = kNT / 32;
 // 16-byte loads each thread keeps in flight, and the CTAs an SM then holds.  The forward with eight
-// and four takes 151 us for 4096 rows of 151936 bf16 (a quarter masked) and 48.7 us for 1024 of
-// 128256, with six and five 150 and 52.3 us, with four and five 162 and 54.0 us; the backward of the
-// latter with six and five 86.5 us, with eight and four 86.0 us, with four and five 96.9 us.
+// and four takes 154 us for 4096 rows of 151936 bf16 (a quarter masked) and 49.4 us for 1024 of
+// 128256, with six and five 153 and 53.2 us, with four and five 164 and 55.9 us; the backward of the
+// latter with six and five 86.8 us, with eight and four 88.6 us, with four and five 87.6 us.
 template <int kMode>
 struct Flight {
   static constexpr int loads = kMode == 0 ? 8 : 6, ctas = kMode == 0 ? 4 : 5;
