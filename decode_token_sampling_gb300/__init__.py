@@ -7,8 +7,11 @@ tensors into that ABI; there is no fallback of any kind: if the library is
 missing or the tensors are not on a CUDA device, calls raise.
 
 Beside the step: top_logits (a row's top logits and log-sum-exps, for
-log-probabilities and for teachers) and distill_loss, distill_loss_grad (the
-distillation loss of a student against a teacher's top logits).
+log-probabilities and for teachers), distill_loss, distill_loss_grad (the
+distillation loss of a student against a teacher's top logits), token_logprobs
+(the log-probabilities and ranks of given tokens with their rows' entropies and
+top alternatives, differentiable) and policy_loss_grad (the clipped policy loss
+of such tokens with its gradient).
 """
 
 from __future__ import annotations
@@ -16,7 +19,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import NamedTuple, Optional, Tuple
+from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
 
@@ -87,6 +90,13 @@ def load_library() -> ctypes.CDLL:
     lib.kps_distill_backward.argtypes = [P, I32, I64, I64, I64, P, P, I32, I64, P, P, F32, P, P, P, I64, P]
     lib.kps_distill_loss_grad.restype = I32
     lib.kps_distill_loss_grad.argtypes = [P, I32, I64, I64, I64, P, P, I32, I64, P, P, F32, P, P, I64, P]
+    lib.kps_token_logprobs.restype = I32
+    lib.kps_token_logprobs.argtypes = [P, I32, I64, I64, I64, P, I64, F32, P, P, P, P, P, P, P, P]
+    lib.kps_token_logprobs_backward.restype = I32
+    lib.kps_token_logprobs_backward.argtypes = [P, I32, I64, I64, I64, P, F32, P, P, P, P, P, I64, P]
+    lib.kps_policy_loss_grad.restype = I32
+    lib.kps_policy_loss_grad.argtypes = [P, I32, I64, I64, I64, P, F32, P, P, P, P, P, F32, F32, F32, F32, P, P, P, P,
+                                         I64, P]
     lib.kps_query_launch.restype = I32
     lib.kps_query_launch.argtypes = [I64, I64, I32, ctypes.POINTER(I32), ctypes.POINTER(I64),
                                      ctypes.POINTER(ctypes.c_size_t)]
@@ -515,3 +525,180 @@ def distill_loss(student: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
     if not (torch.is_grad_enabled() and student.requires_grad):
         return _distill_forward(student, ids, values, temperature, rest, weight, None, False)[0]
     return _DistillLoss.apply(student, ids, values, rest, weight, temperature)
+
+
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs returns (kps_token_logprobs in include/kps.h)."""
+    logprob: torch.Tensor  # float32 [N]
+    entropy: torch.Tensor  # float32 [N]
+    rank: torch.Tensor  # int32 [N]: how many logits of the row are larger than the token's
+    ids: Optional[torch.Tensor]  # int32 [N, n], with n > 0
+    logprobs: Optional[torch.Tensor]  # float32 [N, n], with n > 0
+
+
+def _token_args(logits, tokens, temperature):
+    """Checks the arguments that the calls on given tokens share; returns the ABI's leading arguments and
+    (temperature, temperatures)."""
+    ld = _rows(logits, "logits")
+    dt = _dtype_code(logits)
+    N, V = logits.shape
+    _check(tokens, "tokens", torch.int64, (N,), logits.device)
+    if isinstance(temperature, torch.Tensor):
+        _check(temperature, "temperature", torch.float32, (N,), logits.device)
+        if temperature.requires_grad:
+            raise ValueError("temperature requires a gradient, but there is one for the logits only")
+        scale = (1.0, temperature.data_ptr())
+    else:
+        scale = (temperature, None)
+    return (logits.data_ptr(), dt, N, V, ld, tokens.data_ptr()), scale
+
+
+def _tensor(t):
+    return t if isinstance(t, torch.Tensor) else None
+
+
+def _token_logprobs(logits, tokens, n, temperature, stream, want_stats):
+    lib = load_library()
+    args, scale = _token_args(logits, tokens, temperature)
+    N, V = logits.shape
+    dev = logits.device
+    n = int(n)
+    if not 0 <= n <= min(V, 1024):
+        raise ValueError(f"n must be in 0..min(V, 1024), got {n}")
+
+    def call(handle):
+        out = torch.empty((2, N), dtype=torch.float32, device=dev)
+        rank = torch.empty((N,), dtype=torch.int32, device=dev)
+        ids = torch.empty((N, n), dtype=torch.int32, device=dev) if n else None
+        logprobs = torch.empty((N, n), dtype=torch.float32, device=dev) if n else None
+        stats = torch.empty((3, N), dtype=torch.float32, device=dev) if want_stats else None
+        at = out.data_ptr()
+        st = lib.kps_token_logprobs(*args, n, *scale, at, at + 4 * N, rank.data_ptr(), _addr(ids), _addr(logprobs),
+                                    _addr(stats), handle)
+        if st != 0:
+            raise KpsError(st, "kps_token_logprobs")
+        logprob, entropy = out.unbind(0)
+        return TokenLogprobs(logprob, entropy, rank, ids, logprobs), stats
+
+    return _queue(dev, stream, (logits, tokens, _tensor(temperature)), call)
+
+
+def token_logprobs_forward(logits: torch.Tensor, tokens: torch.Tensor, n: int = 0, *,
+                           temperature: Union[float, torch.Tensor] = 1.0,
+                           stream: Optional[torch.cuda.Stream] = None) -> Tuple[TokenLogprobs, torch.Tensor]:
+    """What token_logprobs returns, and the statistics [3, N] that token_logprobs_backward takes; no
+    autograd."""
+    return _token_logprobs(logits, tokens, n, temperature, stream, True)
+
+
+def token_logprobs_backward(grad_logprob: Optional[torch.Tensor], grad_entropy: Optional[torch.Tensor],
+                            logits: torch.Tensor, tokens: torch.Tensor, stats: torch.Tensor, *,
+                            temperature: Union[float, torch.Tensor] = 1.0,
+                            stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The gradient of the logits, in their type, for the gradients of the log-probabilities and the
+    entropies (float32 [N] each, None: 0) and the statistics of token_logprobs_forward on the same
+    arguments."""
+    lib = load_library()
+    args, scale = _token_args(logits, tokens, temperature)
+    N, dev = logits.shape[0], logits.device
+    _check(grad_logprob, "grad_logprob", torch.float32, (N,), dev)
+    _check(grad_entropy, "grad_entropy", torch.float32, (N,), dev)
+    _check(stats, "stats", torch.float32, (3, N), dev)
+
+    def call(handle):
+        grad = _grad_like(logits)
+        st = lib.kps_token_logprobs_backward(*args, *scale, _addr(grad_logprob), _addr(grad_entropy), stats.data_ptr(),
+                                             grad.data_ptr(), grad.stride(0), handle)
+        if st != 0:
+            raise KpsError(st, "kps_token_logprobs_backward")
+        return grad
+
+    return _queue(dev, stream, (logits, tokens, _tensor(temperature), grad_logprob, grad_entropy, stats), call)
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens, n, temperature):
+        out, stats = _token_logprobs(logits, tokens, n, temperature, None, True)
+        ctx.save_for_backward(logits, tokens, stats, _tensor(temperature))
+        ctx.temperature = None if isinstance(temperature, torch.Tensor) else temperature
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(*(t for t in out[2:] if t is not None))
+        return tuple(out)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_logprob, grad_entropy, *_):
+        logits, tokens, stats, temperatures = ctx.saved_tensors
+        g, h = (None if t is None else t.contiguous() for t in (grad_logprob, grad_entropy))
+        temperature = ctx.temperature if temperatures is None else temperatures
+        return token_logprobs_backward(g, h, logits, tokens, stats, temperature=temperature), None, None, None
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, n: int = 0, *,
+                   temperature: Union[float, torch.Tensor] = 1.0,
+                   stream: Optional[torch.cuda.Stream] = None) -> TokenLogprobs:
+    """The log-probabilities of given tokens (int64 [N]) in their rows of logits [N, V], with the rows'
+    entropies, the tokens' ranks (how many logits are larger) and, for n > 0, the n likeliest tokens with
+    their log-probabilities (include/kps.h has the formulas).  logprob and entropy are differentiable with
+    respect to the logits.
+
+    temperature: a number, or float32 [N] as sample takes it (values that are no positive normal number,
+    its greedy rows, count as 1).  A token outside [0, V) marks a row of padding, which is not read:
+    log-probability and entropy 0, rank -1, ids -1, alternatives of -inf, gradient 0.  Rows may lie apart.
+
+    First derivatives in reverse mode only: second derivatives, forward mode and vmap raise.  A call that
+    autograd records runs on the current stream (no `stream` then).  A captured backward should make its
+    leaves inside the capture, as any autograd graph's; token_logprobs_forward and
+    token_logprobs_backward need none.
+    """
+    if not (torch.is_grad_enabled() and logits.requires_grad):
+        return _token_logprobs(logits, tokens, n, temperature, stream, False)[0]
+    if stream is not None:
+        raise ValueError("a call that autograd records runs on the current stream")
+    return TokenLogprobs(*_TokenLogprobs.apply(logits, tokens, n, temperature))
+
+
+class PolicyLoss(NamedTuple):
+    """What policy_loss_grad returns (kps_policy_loss_grad in include/kps.h)."""
+    loss: torch.Tensor  # float32 [N]
+    grad: torch.Tensor  # the logits' type, [N, V]
+    logprob: torch.Tensor  # float32 [N]
+    entropy: torch.Tensor  # float32 [N]
+
+
+def policy_loss_grad(logits: torch.Tensor, tokens: torch.Tensor, old_logprob: torch.Tensor, advantage: torch.Tensor, *,
+                     clip: Tuple[float, float] = (0.2, 0.2), ref_logprob: Optional[torch.Tensor] = None,
+                     kl_coef: float = 0.0, entropy_coef: float = 0.0, weight: Optional[torch.Tensor] = None,
+                     temperature: Union[float, torch.Tensor] = 1.0,
+                     stream: Optional[torch.cuda.Stream] = None) -> PolicyLoss:
+    """The clipped policy-gradient loss of every row's token and its gradient with respect to the logits
+    (include/kps.h has the formula), for training loops that know every factor of the loss.  No autograd;
+    it may be captured into a CUDA graph.
+
+    old_logprob, advantage: float32 [N]; clip: how far below and above 1 the ratio may go; ref_logprob:
+    float32 [N], with kl_coef; weight: float32 [N] (None: 1).  Rows of weight 0, and rows whose token
+    lies outside [0, V), are not read: loss, log-probability, entropy and gradient 0.  temperature as for
+    token_logprobs.  Any other loss of log-probabilities and entropies: token_logprobs and autograd.
+    """
+    lib = load_library()
+    args, scale = _token_args(logits, tokens, temperature)
+    N, dev = logits.shape[0], logits.device
+    for name, t in (("old_logprob", old_logprob), ("advantage", advantage), ("ref_logprob", ref_logprob), ("weight", weight)):
+        _check(t, name, torch.float32, (N,), dev)
+    if kl_coef != 0 and ref_logprob is None:
+        raise ValueError("kl_coef needs ref_logprob")
+
+    def call(handle):
+        out = torch.empty((3, N), dtype=torch.float32, device=dev)
+        grad = _grad_like(logits)
+        at = out.data_ptr()
+        st = lib.kps_policy_loss_grad(*args, *scale, old_logprob.data_ptr(), advantage.data_ptr(), _addr(ref_logprob),
+                                      _addr(weight), clip[0], clip[1], kl_coef, entropy_coef, at, at + 4 * N, at + 8 * N,
+                                      grad.data_ptr(), grad.stride(0), handle)
+        if st != 0:
+            raise KpsError(st, "kps_policy_loss_grad")
+        loss, logprob, entropy = out.unbind(0)
+        return PolicyLoss(loss, grad, logprob, entropy)
+
+    return _queue(dev, stream, (logits, tokens, _tensor(temperature), old_logprob, advantage, ref_logprob, weight), call)

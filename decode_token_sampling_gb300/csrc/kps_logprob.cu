@@ -1,0 +1,515 @@
+// kps_logprob.cu — the log-probabilities of given tokens with their ranks and the entropies of their
+// rows, the gradient of both, and the clipped policy loss with its gradient.
+//
+// The formulas are in kps_score.cuh.  With g and h the gradients of a row's log-probability and entropy:
+//
+//   d / d x_v = (g (delta_tv - p_v) - h p_v (d_v + Q)) / T
+//
+// and for the policy loss, r = exp(logprob - old), A the advantage, u = ref - logprob:
+//
+//   loss = w (-min(r A, clip(r, 1 - lo, 1 + hi) A) + kl (exp(u) - u - 1) - ent entropy)
+//   g = w (-A r [not clipped] - kl (exp(u) - 1)),  h = -w ent
+//
+// All of it is bound by memory: a row is read (V elements), and written for a gradient.
+
+#include "kps.h"
+#include "kps_host.h"
+#include "kps_score.cuh"
+
+#include <cooperative_groups.h>
+
+#include <climits>
+#include <cmath>
+
+namespace cg = cooperative_groups;
+
+namespace kps {
+namespace score {
+
+constexpr int kNT = 256;  // threads per CTA
+constexpr int kNW = kNT / 32;
+constexpr int kU = 6;         // 16-byte loads each thread keeps in flight
+constexpr int kMaxCS = 8;     // widest cluster (the portable limit)
+
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+// The warp's largest value (NaN as -inf).
+__device__ __forceinline__ float warp_top(float x) {
+  return order_value(__reduce_max_sync(0xffffffffu, order_key(no_nan(x) + 0.0f)));
+}
+
+// ------------------------------------------------------------------------------------------
+// Scoring without alternatives: one pass
+// ------------------------------------------------------------------------------------------
+//
+// A warp's sums are against the largest logit that it has seen, looked for once in a round of loads:
+// it rises some three times in a row's dozen rounds.  The element that holds it stays out of the sums
+// until a larger one takes its place.
+template <bool kBF16>
+__global__ void __launch_bounds__(kNT, 4) score_kernel(const Args A) {
+  __shared__ Part part[kMaxCS * kNW];  // of the cluster's warps (rank 0's are used)
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  cg::cluster_group cl = cg::this_cluster();
+  const int CS = static_cast<int>(cl.num_blocks());
+  const int rank = static_cast<int>(cl.block_rank());
+  const int64_t row = blockIdx.x / CS;
+  // every CTA of the cluster runs before any writes into another's shared memory
+  if (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  const RowView<kBF16> x(A.x, row * A.ld, A.V);
+  const int64_t t = A.tokens[row];
+  const float tau = row_tau(A.taus, A.tau, row);
+  if (t < 0 || t >= A.V) {  // an empty row
+    if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank == 0) put_empty(A, row, kNT);
+    return;
+  }
+  const float token = no_nan(x.at(static_cast<int>(t)));
+  const int g0 = static_cast<int>(static_cast<int64_t>(x.nv) * rank / CS);
+  const int g1 = static_cast<int>(static_cast<int64_t>(x.nv) * (rank + 1) / CS);
+  const float c = kLog2e / tau;
+  const f32x2 c2 = pack2(c, c);
+
+  Moments<kBF16> sum;
+  float top = -INFINITY;  // the warp's largest so far; the sums' reference (0 before there is one)
+  f32x2 nref2 = 0ull;
+  float above = 0.0f;
+  // The reference rises to `to`; the element that held it joins the sums.
+  auto raise = [&](float to) {
+    if (top > -INFINITY) {
+      const float delta = fminf((to - top) * c, -kFloor), f = ex2(-delta);
+      sum.shift(delta, f);
+      if (lane == 0) {
+        sum.s[0] = add2(sum.s[0], pack2(f, 0.0f));
+        sum.w[0] = add2(sum.w[0], pack2(-delta * f, 0.0f));
+      }
+    }
+    top = to;
+    nref2 = pack2(-to, -to);
+  };
+  for (int base = g0; base < g1; base += kNT * kU) {
+    uint4 w[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int g = base + u * kNT + static_cast<int>(threadIdx.x);
+      w[u] = g < g1 ? ld_stream(x.vec + g) : neg_inf_vec<kBF16>();
+    }
+    float m[kU], most = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      m[u] = vec_max<kBF16>(w[u]);
+      most = fmaxf(most, m[u]);
+      if (m[u] > token) above += count_above<kBF16>(w[u], token);
+    }
+    if (__any_sync(0xffffffffu, most > top)) {
+      const float to = warp_top(most);
+      raise(to);
+      const unsigned who = __ballot_sync(0xffffffffu, most == to);
+      if (lane == __ffs(who) - 1) {
+        bool done = false;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          if (done || m[u] != to) continue;
+          strike<kBF16>(w[u], to);
+          done = true;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) sum.add(w[u], nref2, c2);
+  }
+  float s = 0.0f, moment = 0.0f;
+  if (warp == 0) {  // the elements outside the vectors: the head with rank 0, the tail with the last rank
+    const bool in = lane < x.loose() && ((x.loose_at(lane) < x.head) ? rank == 0 : rank == CS - 1);
+    float y = in ? x.at(x.loose_at(lane)) : -INFINITY;
+    if (y > token) above += 1.0f;
+    if (__any_sync(0xffffffffu, y > top)) {
+      const float to = warp_top(y);
+      raise(to);
+      const unsigned who = __ballot_sync(0xffffffffu, y == to);
+      if (lane == __ffs(who) - 1) y = -INFINITY;
+    }
+    const float z = exponent(y, top == -INFINITY ? 0.0f : top, c);
+    s = ex2(z);
+    moment = s * z;
+  }
+  s = warp_sum(s + sum.sum());
+  moment = warp_sum(moment + sum.moment());
+  above = warp_sum(above);
+  Part* to = CS > 1 ? cl.map_shared_rank(&part[0], 0) : part;
+  if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (lane == 0) to[rank * kNW + warp] = Part{top, s, moment, above};
+  if (CS > 1) {
+    cl.sync();
+    if (rank != 0) return;
+  } else {
+    __syncthreads();
+  }
+  if (warp != 0) return;
+  // the parts' sums against the row's largest logit; the first part that holds it keeps it out
+  static_assert(kMaxCS * kNW <= 64);
+  const Part none{-INFINITY, 0.0f, 0.0f, 0.0f};
+  const Part p0 = lane < kNW * CS ? part[lane] : none, p1 = lane + 32 < kNW * CS ? part[lane + 32] : none;
+  const float m = warp_top(fmaxf(p0.m, p1.m));
+  const unsigned w0 = __ballot_sync(0xffffffffu, p0.m == m), w1 = __ballot_sync(0xffffffffu, p1.m == m);
+  const int owner = w0 ? __ffs(w0) - 1 : 32 + __ffs(w1) - 1;
+  float s0, s1, m0, m1;
+  part_to_row(p0, lane == owner, m, c, s0, m0);
+  part_to_row(p1, lane + 32 == owner, m, c, s1, m1);
+  const Row r(m, warp_sum(s0 + s1), warp_sum(m0 + m1));
+  above = warp_sum(p0.above + p1.above);
+  if (lane == 0) put_row(A, row, r, token, tau, above);
+}
+
+// ------------------------------------------------------------------------------------------
+// The gradient
+// ------------------------------------------------------------------------------------------
+struct Grad {
+  Args a;             // max, eps, q are read
+  const float* g;     // the gradients of the log-probability and the entropy, or nullptr: 0
+  const float* h;
+  void* out;
+  int64_t ld_out;
+  // the policy loss (kPolicy): a.max, a.eps, a.q lie in loss, a.logprob, a.entropy, which are written last
+  const float *old, *advantage, *ref, *weight;  // ref, weight: or nullptr
+  float lo, hi, kl, ent;
+  float* loss;
+};
+
+// exp(u) - u - 1 for all u: near 0 by its series, u^2/2! + u^3/3! + ...
+__device__ __forceinline__ float expm1_minus(float u) {
+  if (!(fabsf(u) < 0.5f)) return u == INFINITY ? INFINITY : expm1f(u) - u;
+  float t = 1.0f;  // 1 + u/3 (1 + u/4 (... (1 + u/11))): the next factor is below 2^-28 of the sum
+#pragma unroll
+  for (int i = 11; i >= 3; --i) t = fmaf(t * u, 1.0f / static_cast<float>(i), 1.0f);
+  return 0.5f * u * u * t;
+}
+
+// A row's loss and the gradients of its log-probability and entropy.
+struct PolicyTerm {
+  float loss, g, h;
+  __device__ __forceinline__ PolicyTerm(const Grad& P, int64_t row, float w, float logprob, float entropy) {
+    const float A = P.advantage[row], r = expf(logprob - P.old[row]);
+    const float kept = fminf(fmaxf(r, 1.0f - P.lo), 1.0f + P.hi);
+    const bool clipped = A >= 0.0f ? r > 1.0f + P.hi : r < 1.0f - P.lo;
+    float v = 0.0f, d = 0.0f;
+    if (A != 0.0f) {  // (an infinite ratio times an advantage of 0 is 0)
+      v = -(clipped ? kept : r) * A;
+      d = clipped ? 0.0f : -A * r;
+    }
+    if (P.kl != 0.0f) {
+      const float u = P.ref[row] - logprob;
+      v += P.kl * expm1_minus(u);
+      d -= P.kl * expm1f(u);
+    }
+    if (P.ent != 0.0f) v -= P.ent * entropy;
+    if (isnan(logprob)) v = NAN;
+    loss = w * v;
+    g = w * d;
+    h = -w * P.ent;
+  }
+};
+
+// A row's gradient: e_v (A + B z_v) with e_v = 2^z_v, z_v = (x_v - m) c; the token's apart.
+struct Slope {
+  float a, b, token;
+  __device__ __forceinline__ Slope(const Row& r, float x_token, float tau, float c, float g, float h) {
+    const float inv = 1.0f / (1.0f + r.eps);
+    const float gt = g / tau, ht = h / tau;
+    a = r.ok ? -(gt + ht * r.q) * inv : NAN;
+    b = h == 0.0f ? 0.0f : -ht * kLn2 * inv;
+    // the token's: 1 - p without the difference of two ones where it is the largest
+    const float z = exponent(x_token, r.m, c), e = ex2(z);
+    const float rest = z == 0.0f ? r.eps * inv : 1.0f - e * inv;
+    token = r.ok ? gt * rest + (h == 0.0f ? 0.0f : -ht * (e * inv) * (r.q + kLn2 * z)) : NAN;
+  }
+  __device__ __forceinline__ float at(float x, float m, float c) const {
+    const float z = exponent(x, m, c), e = ex2(z);
+    return e == 0.0f ? 0.0f : e * fmaf(b, z, a);
+  }
+  // Whether a + b z is finite for every z from kFloor on: at the smallest temperatures only at() is.
+  __device__ __forceinline__ bool tame() const { return fabsf(a) < 0x1p110f && fabsf(b) < 0x1p110f; }
+};
+template <bool kBF16>
+__device__ __forceinline__ void put_elem(void* base, int64_t v, float d) {
+  if (kBF16) static_cast<__nv_bfloat16*>(base)[v] = __float2bfloat16_rn(d);
+  else static_cast<float*>(base)[v] = d;
+}
+template <bool kBF16>
+__device__ __forceinline__ uint4 slope_vec(const uint4& w, f32x2 nm2, f32x2 c2, f32x2 a2, f32x2 b2) {
+  uint32_t out[4];
+#pragma unroll
+  for (int i = 0; i < (kBF16 ? 4 : 2); ++i) {
+    float p, q;
+    unpack2(mul2(add2(pair_of<kBF16>(w, i), nm2), c2), p, q);
+    p = max_nan(p, kFloor);
+    q = max_nan(q, kFloor);
+    unpack2(mul2(pack2(ex2(p), ex2(q)), fma2(b2, pack2(p, q), a2)), p, q);
+    if (kBF16) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(p, q);  // the gradient's one rounding
+      out[i] = reinterpret_cast<const uint32_t&>(h);
+    } else {
+      out[2 * i] = __float_as_uint(p);
+      out[2 * i + 1] = __float_as_uint(q);
+    }
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+template <bool kBF16, bool kPolicy>
+__global__ void __launch_bounds__(kNT, 4) slope_kernel(const Grad P) {
+  constexpr int G = kBF16 ? 8 : 4;
+  const Args& A = P.a;
+  cg::cluster_group cl = cg::this_cluster();
+  const int CS = static_cast<int>(cl.num_blocks());
+  const int rank = static_cast<int>(cl.block_rank());
+  const int64_t row = blockIdx.x / CS;
+  const RowView<kBF16> x(A.x, row * A.ld, A.V), o(P.out, row * P.ld_out, A.V);
+  unsigned char* const obase = const_cast<unsigned char*>(o.base);
+  const int64_t t = A.tokens[row];
+  const float tau = row_tau(A.taus, A.tau, row), c = kLog2e / tau;
+  float g = 0.0f, h = 0.0f, w = 1.0f;
+  bool live = t >= 0 && t < A.V;
+  if constexpr (kPolicy) {
+    if (P.weight) w = P.weight[row];
+    live = live && w != 0.0f;
+  } else {
+    if (P.g) g = P.g[row];
+    if (P.h) h = P.h[row];
+    live = live && (g != 0.0f || h != 0.0f);
+  }
+  if (!live) {  // zeros; the row is not looked at (the same in every CTA of the row)
+    const int o0 = static_cast<int>(static_cast<int64_t>(o.nv) * rank / CS);
+    const int o1 = static_cast<int>(static_cast<int64_t>(o.nv) * (rank + 1) / CS);
+    uint4* ov = const_cast<uint4*>(o.vec);
+    for (int i = o0 + static_cast<int>(threadIdx.x); i < o1; i += kNT) __stcs(ov + i, make_uint4(0u, 0u, 0u, 0u));
+    if (rank == 0 && static_cast<int>(threadIdx.x) < o.loose()) put_elem<kBF16>(obase, o.loose_at(threadIdx.x), 0.0f);
+    if (kPolicy && rank == 0 && threadIdx.x == 0) P.loss[row] = A.logprob[row] = A.entropy[row] = 0.0f;
+    return;
+  }
+  const Row r(A.max, A.eps, A.q, row);
+  const float x_token = x.at(static_cast<int>(t));
+  if constexpr (kPolicy) {
+    const float logprob = r.logprob(x_token, tau), entropy = r.entropy();
+    const PolicyTerm term(P, row, w, logprob, entropy);
+    g = term.g;
+    h = term.h;
+    if (CS > 1) cl.sync(); else __syncthreads();  // every thread of the row has read its statistics
+    if (rank == 0 && threadIdx.x == 0) {
+      P.loss[row] = term.loss;
+      A.logprob[row] = logprob;
+      A.entropy[row] = entropy;
+    }
+  }
+  const Slope slope(r, x_token, tau, c, g, h);
+  const int g0 = static_cast<int>(static_cast<int64_t>(x.nv) * rank / CS);
+  const int g1 = static_cast<int>(static_cast<int64_t>(x.nv) * (rank + 1) / CS);
+  const int at = static_cast<int>(t) - x.head;  // the token's vector, if it is in one
+  const int tv = at >= 0 && at < x.nv * G ? at / G : -1;
+  if (o.head == x.head && slope.tame()) {
+    const f32x2 nm2 = pack2(-r.m, -r.m), c2 = pack2(c, c), a2 = pack2(slope.a, slope.a), b2 = pack2(slope.b, slope.b);
+    uint4* ov = const_cast<uint4*>(o.vec);
+    for (int base = g0; base < g1; base += kNT * kU) {
+      uint4 v[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int i = base + u * kNT + static_cast<int>(threadIdx.x);
+        v[u] = i < g1 ? ld_stream(x.vec + i) : neg_inf_vec<kBF16>();
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int i = base + u * kNT + static_cast<int>(threadIdx.x);
+        if (i >= g1) continue;
+        __stcs(ov + i, slope_vec<kBF16>(v[u], nm2, c2, a2, b2));
+        if (i == tv) put_elem<kBF16>(obase, t, slope.token);  // by the thread that wrote the vector, behind it
+      }
+    }
+    if (static_cast<int>(threadIdx.x) < x.loose()) {
+      const int v = x.loose_at(threadIdx.x);
+      if ((v < x.head) ? rank == 0 : rank == CS - 1) put_elem<kBF16>(obase, v, v == t ? slope.token : slope.at(x.at(v), r.m, c));
+    }
+  } else {
+    // the two rows do not share their 16-byte boundaries, or the numbers are extreme: one element at a time
+    const int v0 = rank == 0 ? 0 : x.head + g0 * G, v1 = rank == CS - 1 ? A.V : x.head + g1 * G;
+    for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kNT)
+      put_elem<kBF16>(obase, v, v == t ? slope.token : slope.at(x.at(v), r.m, c));
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// Host side
+// ------------------------------------------------------------------------------------------
+// Launches a kernel of a cluster a row: one CTA, or for few rows up to kMaxCS while every thread keeps
+// four vectors.
+template <class Kernel, class P>
+static kps_status launch_rows(Kernel* kernel, const P& params, int64_t N, int64_t V, bool bf16, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return KPS_ERR_CUDA;
+  }
+  int cs = 1;
+  const int64_t round = static_cast<int64_t>(kNT) * 4 * (bf16 ? 8 : 4);
+  while (cs < kMaxCS && N * cs * 2 <= 2 * sms && V >= 2 * cs * round) cs *= 2;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(static_cast<unsigned>(N * cs));
+  lc.blockDim = dim3(kNT);
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  if (cudaLaunchKernelEx(&lc, kernel, params) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return KPS_ERR_CUDA;
+  }
+  return KPS_OK;
+}
+static kps_status launch_score(const Args& a, kps_dtype dt, cudaStream_t stream) {
+  if (a.n > 0) return launch_alternatives(a, dt, stream);
+  return dt == KPS_BF16 ? launch_rows(score_kernel<true>, a, a.N, a.V, true, stream)
+                        : launch_rows(score_kernel<false>, a, a.N, a.V, false, stream);
+}
+template <bool kPolicy>
+static kps_status launch_slope(const Grad& P, kps_dtype dt, cudaStream_t stream) {
+  return dt == KPS_BF16 ? launch_rows(slope_kernel<true, kPolicy>, P, P.a.N, P.a.V, true, stream)
+                        : launch_rows(slope_kernel<false, kPolicy>, P, P.a.N, P.a.V, false, stream);
+}
+
+static bool misaligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+// The checks that every entry point shares; fills a.
+static kps_status check(const void* logits, kps_dtype dt, int64_t N, int64_t V, int64_t ld, const int64_t* tokens,
+                        float temperature, const float* temperatures, Args* a) {
+  if (dt != KPS_F32 && dt != KPS_BF16) return KPS_ERR_INVALID_ARG;
+  if (N < 0 || V < 1 || (N > 1 && ld < V)) return KPS_ERR_INVALID_ARG;
+  if (!temperatures && (!(temperature > 0.0f) || std::isinf(temperature) || std::isinf(kLog2e / temperature))) return KPS_ERR_INVALID_ARG;
+  if (V > kMaxV || N > INT32_MAX / kMaxCS) return KPS_ERR_UNSUPPORTED;
+  if (N == 0) return KPS_OK;
+  if (!logits || !tokens || misaligned(logits, dt == KPS_BF16 ? 2 : 4) || misaligned(tokens, 8) || misaligned(temperatures, 4))
+    return KPS_ERR_INVALID_ARG;
+  a->x = logits;
+  a->N = N;
+  a->ld = ld;
+  a->V = static_cast<int>(V);
+  a->tau = temperature;
+  a->taus = temperatures;
+  a->tokens = tokens;
+  return KPS_OK;
+}
+
+// A gradient buffer of its own: rows of at least V elements, sharing no byte with the logits' rows.
+static kps_status check_grad(const Args& a, kps_dtype dt, void* grad, int64_t ld_grad) {
+  const uintptr_t esize = dt == KPS_BF16 ? 2 : 4;
+  if (!grad || misaligned(grad, esize) || (a.N > 1 && ld_grad < a.V)) return KPS_ERR_INVALID_ARG;
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.x), q = reinterpret_cast<uintptr_t>(grad);
+  const uintptr_t pn = ((a.N - 1) * a.ld + a.V) * esize, qn = ((a.N - 1) * ld_grad + a.V) * esize;
+  return p < q + qn && q < p + pn ? KPS_ERR_INVALID_ARG : KPS_OK;
+}
+
+}  // namespace score
+}  // namespace kps
+
+extern "C" {
+
+kps_status kps_token_logprobs(const void* logits, kps_dtype dt, int64_t N, int64_t V, int64_t ld, const int64_t* tokens,
+                              int64_t n, float temperature, const float* temperatures, float* out_logprob,
+                              float* out_entropy, int32_t* out_rank, int32_t* out_ids, float* out_logprobs,
+                              float* out_stats, cudaStream_t stream) {
+  namespace ks = kps::score;
+  const kps::NvtxRange range("kps_token_logprobs");
+  ks::Args a = {};
+  const kps_status st = ks::check(logits, dt, N, V, ld, tokens, temperature, temperatures, &a);
+  if (st != KPS_OK) return st;
+  if (n < 0 || n > 1024 || n > V) return KPS_ERR_INVALID_ARG;
+  if (N == 0) return KPS_OK;
+  if (n > 0 && (!out_ids || !out_logprobs)) return KPS_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(out_logprob), static_cast<const void*>(out_entropy),
+                        static_cast<const void*>(out_rank), static_cast<const void*>(out_ids),
+                        static_cast<const void*>(out_logprobs), static_cast<const void*>(out_stats)})
+    if (ks::misaligned(p, 4)) return KPS_ERR_INVALID_ARG;
+  a.n = static_cast<int>(n);
+  a.logprob = out_logprob;
+  a.entropy = out_entropy;
+  a.rank = out_rank;
+  a.ids = out_ids;
+  a.logprobs = out_logprobs;
+  if (out_stats) {
+    a.max = out_stats;
+    a.eps = out_stats + N;
+    a.q = out_stats + 2 * N;
+  }
+  return ks::launch_score(a, dt, stream);
+}
+
+kps_status kps_token_logprobs_backward(const void* logits, kps_dtype dt, int64_t N, int64_t V, int64_t ld,
+                                       const int64_t* tokens, float temperature, const float* temperatures,
+                                       const float* grad_logprob, const float* grad_entropy, const float* stats,
+                                       void* out_grad, int64_t ld_grad, cudaStream_t stream) {
+  namespace ks = kps::score;
+  const kps::NvtxRange range("kps_token_logprobs_backward");
+  ks::Grad P = {};
+  kps_status st = ks::check(logits, dt, N, V, ld, tokens, temperature, temperatures, &P.a);
+  if (st != KPS_OK || N == 0) return st;
+  if (!stats || ks::misaligned(stats, 4) || ks::misaligned(grad_logprob, 4) || ks::misaligned(grad_entropy, 4))
+    return KPS_ERR_INVALID_ARG;
+  if ((st = ks::check_grad(P.a, dt, out_grad, ld_grad)) != KPS_OK) return st;
+  P.a.max = const_cast<float*>(stats);
+  P.a.eps = P.a.max + N;
+  P.a.q = P.a.max + 2 * N;
+  P.g = grad_logprob;
+  P.h = grad_entropy;
+  P.out = out_grad;
+  P.ld_out = ld_grad;
+  return ks::launch_slope<false>(P, dt, stream);
+}
+
+kps_status kps_policy_loss_grad(const void* logits, kps_dtype dt, int64_t N, int64_t V, int64_t ld, const int64_t* tokens,
+                                float temperature, const float* temperatures, const float* old_logprob,
+                                const float* advantage, const float* ref_logprob, const float* weight, float clip_low,
+                                float clip_high, float kl_coef, float entropy_coef, float* out_loss, float* out_logprob,
+                                float* out_entropy, void* out_grad, int64_t ld_grad, cudaStream_t stream) {
+  namespace ks = kps::score;
+  const kps::NvtxRange range("kps_policy_loss_grad");
+  ks::Grad P = {};
+  kps_status st = ks::check(logits, dt, N, V, ld, tokens, temperature, temperatures, &P.a);
+  if (st != KPS_OK) return st;
+  if (!(clip_low >= 0.0f) || !(clip_high >= 0.0f) || !std::isfinite(kl_coef) || !std::isfinite(entropy_coef)) return KPS_ERR_INVALID_ARG;
+  if (N == 0) return KPS_OK;
+  if (!old_logprob || !advantage || (kl_coef != 0.0f && !ref_logprob) || !out_loss || !out_logprob || !out_entropy)
+    return KPS_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(old_logprob), static_cast<const void*>(advantage),
+                        static_cast<const void*>(ref_logprob), static_cast<const void*>(weight),
+                        static_cast<const void*>(out_loss), static_cast<const void*>(out_logprob),
+                        static_cast<const void*>(out_entropy)})
+    if (ks::misaligned(p, 4)) return KPS_ERR_INVALID_ARG;
+  if ((st = ks::check_grad(P.a, dt, out_grad, ld_grad)) != KPS_OK) return st;
+  // the statistics of the first launch lie where the second leaves the results
+  P.a.max = out_loss;
+  P.a.eps = out_logprob;
+  P.a.q = out_entropy;
+  if ((st = ks::launch_score(P.a, dt, stream)) != KPS_OK) return st;
+  P.a.logprob = out_logprob;
+  P.a.entropy = out_entropy;
+  P.old = old_logprob;
+  P.advantage = advantage;
+  P.ref = ref_logprob;
+  P.weight = weight;
+  P.lo = clip_low;
+  P.hi = clip_high;
+  P.kl = kl_coef;
+  P.ent = entropy_coef;
+  P.loss = out_loss;
+  P.out = out_grad;
+  P.ld_out = ld_grad;
+  return ks::launch_slope<true>(P, dt, stream);
+}
+
+}  // extern "C"

@@ -27,6 +27,7 @@
 
 #include "kps.h"
 #include "kps_host.h"
+#include "kps_score.cuh"
 #include "kps_stream.cuh"
 
 #include <cooperative_groups.h>
@@ -77,6 +78,7 @@ struct Params {
   float* lse;      // or nullptr
   float* rest;     // or nullptr
   float* logprob;  // or nullptr
+  score::Args sc;  // scoring
 };
 
 // Keys order as the values do (-0 first made +0); an element's word orders by (value desc, index asc).
@@ -94,8 +96,16 @@ __device__ __forceinline__ unsigned long long word_of(uint32_t key, int v) {
 __device__ __forceinline__ float word_value(unsigned long long w) { return kfloat(static_cast<uint32_t>(w >> 32)); }
 __device__ __forceinline__ int word_index(unsigned long long w) { return static_cast<int>(~static_cast<uint32_t>(w)); }
 
-template <bool kSmall>
-struct Smem {
+// What scoring exchanges beside the list: per warp of the cluster, the moment and the count.
+template <bool kScore>
+struct ScoreSmem {
+  float w[kScore ? kMaxCS * kNW : 1], larger[kScore ? kMaxCS * kNW : 1];
+};
+template <>
+struct ScoreSmem<false> {};
+
+template <bool kSmall, bool kScore = false>
+struct Smem : ScoreSmem<kScore> {
   unsigned long long words[Caps<kSmall>::words];  // the survivors
   uint4 vec[Caps<kSmall>::list];                  // the listed vectors, by warp
   int32_t at[Caps<kSmall>::list];                 // index of each one's first element (~: its only one)
@@ -183,9 +193,9 @@ __device__ __forceinline__ float elem(const uint4& w, int e) {
   return __uint_as_float(word[e]);
 }
 
-// Every element of the row, with the warp converged: f(valid, value with NaN -> -inf, index).
+// Every element of the row, with the warp converged: f(valid, value, index).
 template <bool kBF16, class F>
-__device__ __forceinline__ void each(const RowView<kBF16>& x, F&& f) {
+__device__ __forceinline__ void each_raw(const RowView<kBF16>& x, F&& f) {
   constexpr int G = kBF16 ? 8 : 4;
   for (int base = 0; base < x.nv; base += kNT * kU) {
     uint4 w[kU];
@@ -198,12 +208,17 @@ __device__ __forceinline__ void each(const RowView<kBF16>& x, F&& f) {
     for (int u = 0; u < kU; ++u) {
       const int g = base + u * kNT + static_cast<int>(threadIdx.x);
 #pragma unroll
-      for (int e = 0; e < G; ++e) f(g < x.nv, clean(elem<kBF16>(w[u], e)), x.head + g * G + e);
+      for (int e = 0; e < G; ++e) f(g < x.nv, elem<kBF16>(w[u], e), x.head + g * G + e);
     }
   }
   const bool in = static_cast<int>(threadIdx.x) < x.loose();
   const int v = in ? x.loose_at(threadIdx.x) : 0;
-  f(in, in ? clean(x.at(v)) : -INFINITY, v);
+  f(in, in ? x.at(v) : -INFINITY, v);
+}
+// The same with NaN as -inf.
+template <bool kBF16, class F>
+__device__ __forceinline__ void each(const RowView<kBF16>& x, F&& f) {
+  each_raw<kBF16>(x, [&](bool valid, float y, int v) { f(valid, clean(y), v); });
 }
 
 // The exact selection, by one CTA, for rows whose list came out too short or too long: the n-th
@@ -265,19 +280,23 @@ __device__ __noinline__ Sum2 exact_select(const RowView<kBF16>& x, int n, uint32
   return sum;
 }
 
-template <bool kBF16, bool kSmall>
+// kScore: the tokens' log-probabilities, ranks, the entropy and the list's log-probabilities instead of
+// values and log-sum-exps (kps_score.cuh): the pass also takes the sum's first moment and counts what is
+// larger than the token; the list's part is summed against the row's largest logit, which stays out.
+template <bool kBF16, bool kSmall, bool kScore>
 __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P) {
   constexpr int G = kBF16 ? 8 : 4;
   constexpr int kWords = Caps<kSmall>::words;
   extern __shared__ __align__(16) unsigned char smem[];
-  Smem<kSmall>& sm = *reinterpret_cast<Smem<kSmall>*>(smem);
+  Smem<kSmall, kScore>& sm = *reinterpret_cast<Smem<kSmall, kScore>*>(smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned lt = (1u << lane) - 1u;
   const int CS = static_cast<int>(cg::this_cluster().num_blocks());
   const int rank = static_cast<int>(cg::this_cluster().block_rank());
   const int64_t row = blockIdx.x / CS;
   const int n = P.n;
-  const float c = P.c;
+  const float tau = kScore ? score::row_tau(P.sc.taus, P.tau, row) : P.tau;
+  const float c = kScore ? kLog2e / tau : P.c;
   const RowView<kBF16> x(P.x, row * P.ld, P.V);
   const int g0 = static_cast<int>(static_cast<int64_t>(x.nv) * rank / CS);
   const int g1 = static_cast<int>(static_cast<int64_t>(x.nv) * (rank + 1) / CS);
@@ -288,7 +307,15 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
   }
   // every CTA of the cluster runs, and has set these, before any writes into another's shared memory
   if (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  if (threadIdx.x == 0) {
+  if constexpr (kScore) {
+    const int64_t t = P.tokens[row];
+    if (t < 0 || t >= P.V) {  // an empty row (the same in every CTA)
+      if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      if (rank == 0) score::put_empty(P.sc, row, kNT);
+      return;
+    }
+    token_logit = clean(x.at(static_cast<int>(t)));
+  } else if (threadIdx.x == 0) {
     if (P.logprob && rank == 0) {
       const int64_t t = P.tokens[row];
       token_logit = t >= 0 && t < P.V ? clean(x.at(static_cast<int>(t))) : NAN;  // NaN: no such token
@@ -346,7 +373,7 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
     if (t > kKeyNegInf) {
       ref = kfloat(t);
       if (n > 0) thr = ref;
-      if (fabsf(ref * c) > kFastRef) ref = 0.0f;  // far below zero: what is not listed weighs nothing against it
+      if (!kScore && fabsf(ref * c) > kFastRef) ref = 0.0f;  // far below zero: what is not listed weighs nothing against it
     } else if (n > 0) {
       thr = -FLT_MAX;  // a row of -inf but for a few: everything finite
     }
@@ -357,9 +384,12 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
   // ---- the pass -----------------------------------------------------------------------------
   // everything summed here is below the threshold, the sum's reference
   FastSum<kBF16> fast(ref, c);
+  score::Moments<kBF16> fine;  // scoring: in the place of `fast`
+  const f32x2 nref2 = pack2(-ref, -ref), c2 = pack2(c, c);
+  float larger = 0.0f;  // of this thread's elements, those above the token's
   // the list lives with rank 0: every warp of the cluster writes to a segment of its own there
   cg::cluster_group cl = cg::this_cluster();
-  Smem<kSmall>& home = CS > 1 ? *cl.map_shared_rank(&sm, 0) : sm;
+  Smem<kSmall, kScore>& home = CS > 1 ? *cl.map_shared_rank(&sm, 0) : sm;
   const uint32_t seg_cap = static_cast<uint32_t>(Caps<kSmall>::list / (kNW * CS));
   const int seg = rank * kNW + warp;
   uint32_t listed = 0;  // this warp's
@@ -392,18 +422,21 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
       const int g = base + u * kNT + static_cast<int>(threadIdx.x);
       const float m = vec_max<kBF16>(w[u]);
       const bool hit = m >= thr && (kFull || g < g1);
+      if (kScore && m > token_logit) larger += score::count_above<kBF16>(w[u], token_logit);
       if (__any_sync(0xffffffffu, hit)) {
         list(hit, w[u], x.head + g * G, m);
         if (hit) w[u] = neg_inf_vec<kBF16>();
       }
-      fast.add(w[u]);
+      if constexpr (kScore) fine.add(w[u], nref2, c2);
+      else fast.add(w[u]);
     }
   };
   int base = g0;
 #pragma unroll 1
   for (; base + kNT * kU <= g1; base += kNT * kU) round(base, std::true_type{});
   if (base < g1) round(base, std::false_type{});
-  Sum2 sum{ref, fast.total(ref, c)};  // one reference for all of them
+  Sum2 sum{ref, kScore ? fine.sum() : fast.total(ref, c)};  // one reference for all of them
+  float moment = kScore ? fine.moment() : 0.0f;
   // the elements outside the vectors, each as the first of a vector of its own (its index
   // complemented): the head with rank 0, the tail with the last rank
   if (warp == 0) {
@@ -413,7 +446,16 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
     uint4 w = neg_inf_vec<kBF16>();
     w.x = kBF16 ? (0xFF800000u | (__float_as_uint(y) >> 16)) : __float_as_uint(y);
     list(hit, w, ~x.loose_at(lane), y);
-    if (in && !hit) sum.s += ex2((y - ref) * c);
+    if (kScore && y > token_logit) larger += 1.0f;
+    if (in && !hit) {
+      if constexpr (kScore) {
+        const float z = score::exponent(y, ref, c), e = ex2(z);
+        sum.s += e;
+        moment += e * z;
+      } else {
+        sum.s += ex2((y - ref) * c);
+      }
+    }
   }
   {
     const uint32_t k = __reduce_max_sync(0xffffffffu, fkey(mx + 0.0f));
@@ -425,6 +467,13 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
   if (CS > 1) {
     const float s = warp_sum(sum.s);
     if (lane == 0) home.part[seg] = s;
+  }
+  if constexpr (kScore) {
+    const float a = warp_sum(larger), w = warp_sum(moment);
+    if (lane == 0) {
+      home.larger[seg] = a;
+      home.w[seg] = w;
+    }
   }
   for (int i = threadIdx.x; i < 256; i += kNT) {
     sm.hist[i] = 0u;
@@ -449,7 +498,15 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
   const bool over = __syncthreads_or(most > seg_cap);
   const bool bad = over || !(sum.s < 0x1p100f);
   bool exact = __syncthreads_or(bad);
-  const bool weak = !__syncthreads_or(sum.s >= 0x1p-60f) && thr > -FLT_MAX;
+  const bool weak = !kScore && !__syncthreads_or(sum.s >= 0x1p-60f) && thr > -FLT_MAX;
+  // scoring: the listed elements but the largest, against that
+  Sum2 near{kfloat(sm.top_key), 0.0f};
+  float near_w = 0.0f;
+  auto add_near = [&](float y) {
+    const float z = score::exponent(y, near.ref, c), e = ex2(z);
+    near.s += e;
+    near_w += e * z;
+  };
   uint32_t cut = 0xFFFFFFFFu;  // keys from here on survive
   int count = 0, digit = 0;    // the survivors, and the shift of their first digit
   const uint32_t tkey = thr == -INFINITY ? kKeyNegInf : fkey(thr + 0.0f);
@@ -508,6 +565,20 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
     count = n;
   } else {
     vectors([&](const uint4& w, int v0, int elems) {
+      if constexpr (kScore) {
+#pragma unroll
+        for (int e = 0; e < G; ++e) {
+          if (e >= elems) continue;
+          const float raw = elem<kBF16>(w, e);
+          const uint32_t k = fkey(clean(raw));
+          if (k < cut || isnan(raw)) add_near(raw);
+          if (k >= cut) {
+            const uint32_t d = (k - tkey) >> digit;
+            sm.words[sm.offset[d] + atomicAdd(&sm.filled[d], 1u)] = word_of(k, v0 + e);
+          }
+        }
+        return;
+      }
       float y[G];
       float m = -INFINITY;
 #pragma unroll
@@ -550,6 +621,44 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
     sorted[r] = w;
   }
   __syncthreads();
+  if constexpr (kScore) {
+    const unsigned long long best = sorted[0];
+    near.ref = word_value(best);
+    if (exact) {  // the whole row again (what the list and the pass gave is left out)
+      near.s = near_w = 0.0f;
+      each_raw<kBF16>(x, [&](bool valid, float y, int v) {
+        if (valid && v != word_index(best)) add_near(y);
+      });
+    } else {
+      for (int i = threadIdx.x; i < count; i += kNT)
+        if (i > 0) add_near(word_value(sorted[i]));
+      // the pass's sums: of the cluster's warps, or this thread's own, from their reference to the largest
+      if (CS > 1) moment = static_cast<int>(threadIdx.x) < kNW * CS ? sm.w[threadIdx.x] : 0.0f;
+      const float delta = fminf((near.ref - sum.ref) * c, -score::kFloor), f = ex2(-delta);
+      if (thr > -FLT_MAX || sum.s != 0.0f) {
+        near.s += f * sum.s;
+        near_w += f * (moment - delta * sum.s);
+      }
+    }
+    const float s1 = warp_sum(near.s), w1 = warp_sum(near_w);
+    if (lane == 0) {
+      sm.red[warp][0] = s1;
+      sm.red[warp][1] = w1;
+    }
+    __syncthreads();
+    const score::Row r(near.ref, warp_sum(lane < kNW ? sm.red[lane][0] : 0.0f), warp_sum(lane < kNW ? sm.red[lane][1] : 0.0f));
+    for (int i = threadIdx.x; i < n; i += kNT) {
+      P.ids[row * n + i] = word_index(sorted[i]);
+      P.sc.logprobs[row * n + i] = r.logprob(word_value(sorted[i]), tau);
+    }
+    if (warp == 0) {
+      float a = 0.0f;
+      for (int i = lane; i < kNW * CS; i += 32) a += sm.larger[i];
+      a = warp_sum(a);
+      if (lane == 0) score::put_row(P.sc, row, r, token_logit, tau, a);
+    }
+    return;
+  }
   Sum2 lead{-FLT_MAX, 0.0f};
   for (int i = threadIdx.x; i < count; i += kNT) {
     const unsigned long long w = sorted[i];
@@ -566,7 +675,7 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
   if (threadIdx.x == 0) {
     const Sum2 all = merge(lead, sum, c);
     // a sum of nothing is -inf; a sum with +inf in it is +inf
-    auto ln = [&](const Sum2& s) { return s.s == 0.0f ? -INFINITY : logf(s.s) + s.ref / P.tau; };
+    auto ln = [&](const Sum2& s) { return s.s == 0.0f ? -INFINITY : logf(s.s) + s.ref / tau; };
     const float lse = ln(all);
     if (P.lse) P.lse[row] = lse;
     if (P.rest) P.rest[row] = ln(sum);
@@ -574,7 +683,7 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
       // relative to the sum's reference: lse and the token's logit are both large, and lse may have
       // left fp32 where their difference has not (the type's lowest value over tau < 1)
       const float y = token_logit;
-      float lp = all.s > 0.0f && all.s < INFINITY ? (y - all.ref) / P.tau - logf(all.s) : y / P.tau - lse;
+      float lp = all.s > 0.0f && all.s < INFINITY ? (y - all.ref) / tau - logf(all.s) : y / tau - lse;
       if (isnan(y)) lp = -INFINITY;
       P.logprob[row] = lp;
     }
@@ -584,12 +693,12 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
 // ------------------------------------------------------------------------------------------
 // Host side
 // ------------------------------------------------------------------------------------------
-template <bool kBF16, bool kSmall>
+template <bool kBF16, bool kSmall, bool kScore>
 static kps_status launch_t(const Params& P, cudaStream_t stream) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      (sizeof(Smem<kSmall>) > 48 * 1024 &&
-       cudaFuncSetAttribute(top_kernel<kBF16, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem<kSmall>)) !=
+      (sizeof(Smem<kSmall, kScore>) > 48 * 1024 &&
+       cudaFuncSetAttribute(top_kernel<kBF16, kSmall, kScore>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem<kSmall, kScore>)) !=
            cudaSuccess)) {
     (void)cudaGetLastError();
     return KPS_ERR_CUDA;
@@ -601,7 +710,7 @@ static kps_status launch_t(const Params& P, cudaStream_t stream) {
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(static_cast<unsigned>(P.B * cs));
   lc.blockDim = dim3(kNT);
-  lc.dynamicSmemBytes = sizeof(Smem<kSmall>);
+  lc.dynamicSmemBytes = sizeof(Smem<kSmall, kScore>);
   lc.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -610,18 +719,32 @@ static kps_status launch_t(const Params& P, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  if (cudaLaunchKernelEx(&lc, top_kernel<kBF16, kSmall>, P) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&lc, top_kernel<kBF16, kSmall, kScore>, P) != cudaSuccess) {
     (void)cudaGetLastError();
     return KPS_ERR_CUDA;
   }
   return KPS_OK;
 }
-template <bool kBF16>
+template <bool kBF16, bool kScore>
 static kps_status launch(const Params& P, cudaStream_t stream) {
-  return P.n <= kSmallN ? launch_t<kBF16, true>(P, stream) : launch_t<kBF16, false>(P, stream);
+  return P.n <= kSmallN ? launch_t<kBF16, true, kScore>(P, stream) : launch_t<kBF16, false, kScore>(P, stream);
 }
 
 }  // namespace top
+
+kps_status score::launch_alternatives(const score::Args& a, kps_dtype dt, cudaStream_t stream) {
+  top::Params P = {};
+  P.x = a.x;
+  P.B = a.N;
+  P.ld = a.ld;
+  P.V = a.V;
+  P.n = a.n;
+  P.tau = a.tau;
+  P.tokens = a.tokens;
+  P.ids = a.ids;
+  P.sc = a;
+  return dt == KPS_BF16 ? top::launch<true, true>(P, stream) : top::launch<false, true>(P, stream);
+}
 }  // namespace kps
 
 extern "C" kps_status kps_top_logits(const void* logits, kps_dtype dt, int64_t B, int64_t V, int64_t ld, int64_t n,
@@ -653,5 +776,5 @@ extern "C" kps_status kps_top_logits(const void* logits, kps_dtype dt, int64_t B
   P.lse = out_lse;
   P.rest = out_rest;
   P.logprob = out_logprob;
-  return dt == KPS_BF16 ? kt::launch<true>(P, stream) : kt::launch<false>(P, stream);
+  return dt == KPS_BF16 ? kt::launch<true, false>(P, stream) : kt::launch<false, false>(P, stream);
 }

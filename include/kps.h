@@ -270,7 +270,7 @@ kps_status kps_sample_noalloc(const void* logits, kps_dtype dt, int64_t B, int64
 
 
 /*
- * Rows of logits beside the sampling step.  The three operators below read
+ * Rows of logits beside the sampling step.  The operators below read
  * [rows, V] logits whose rows start ld elements apart (ld >= V when there is
  * more than one row; what lies between a row's end and the next row's start is
  * neither read nor written).  They take V <= 1048576, allocate nothing, need no
@@ -368,6 +368,86 @@ kps_status kps_distill_loss_grad(const void* student, kps_dtype dt, int64_t N, i
                                  const int32_t* ids, const void* values, kps_dtype values_dt, int64_t K,
                                  const float* rest, const float* weight, float temperature, float* out_loss,
                                  void* out_grad, int64_t ld_grad, cudaStream_t stream);
+
+/*
+ * kps_token_logprobs, kps_token_logprobs_backward — the log-probabilities of
+ * given tokens (those that were sampled, a prompt's, a rollout's) with their
+ * ranks, the entropies of their rows and the top alternatives; and the gradient
+ * of log-probabilities and entropies.
+ *
+ *   logits  [N, V] (dt), rows ld apart
+ *   tokens  [N] int64.  A token outside [0, V) marks an empty row (padding): its
+ *           logits are not looked at.
+ *   n       alternatives, 0..min(V, 1024)
+ *   temperatures  [N] fp32, as kps_sample takes them, or NULL: `temperature` for
+ *           every row, finite and > 0.  One that is no positive normal number
+ *           (kps_sample's greedy rows) counts as 1.
+ *
+ * With a = x / temperature and p = softmax(a) over the row:
+ *
+ *   out_logprob  [N]  ln p[token]
+ *   out_entropy  [N]  -sum_v p_v ln p_v (a p of 0 adds nothing)
+ *   out_rank     [N]  how many logits of the row are larger than the token's
+ *   out_ids, out_logprobs [N, n]  the first n of kps_sample's order (value
+ *                     descending, index ascending; NaN counts as -inf) and their
+ *                     ln p; NULL allowed for n == 0
+ *   out_stats    [3 N]  for the backward pass
+ *
+ * Outputs that are NULL are not written.  An empty row has log-probability 0,
+ * entropy 0, rank -1, ids -1 and log-probabilities of -inf.  A row without a
+ * distribution (one holding NaN or +inf, or nothing above -inf) has NaN for the
+ * log-probabilities and the entropy.  Sums leave the row's largest element out, so
+ * the log-probability and the entropy of a row that is all but certain are right
+ * to their own size.
+ *
+ * kps_token_logprobs_backward takes the same arguments with the statistics and
+ * writes out_grad [N, V] (dt, rows ld_grad apart), for grad_logprob and
+ * grad_entropy [N] (NULL: 0):
+ *
+ *   (grad_logprob (delta_{v, token} - p_v)
+ *    - grad_entropy p_v (ln p_v + entropy)) / temperature
+ *
+ * Empty rows, and rows where both factors are 0, get zeros.  out_grad must lie
+ * outside the logits, as for kps_distill_backward.  Gradients are computed in
+ * fp32 and rounded once.
+ */
+kps_status kps_token_logprobs(const void* logits, kps_dtype dt, int64_t N, int64_t V, int64_t ld, const int64_t* tokens,
+                              int64_t n, float temperature, const float* temperatures, float* out_logprob,
+                              float* out_entropy, int32_t* out_rank, int32_t* out_ids, float* out_logprobs,
+                              float* out_stats, cudaStream_t stream);
+kps_status kps_token_logprobs_backward(const void* logits, kps_dtype dt, int64_t N, int64_t V, int64_t ld,
+                                       const int64_t* tokens, float temperature, const float* temperatures,
+                                       const float* grad_logprob, const float* grad_entropy, const float* stats,
+                                       void* out_grad, int64_t ld_grad, cudaStream_t stream);
+
+/*
+ * kps_policy_loss_grad — the clipped policy-gradient loss of the rows' tokens,
+ * with its gradient, for programs that know every factor of the loss.  logits,
+ * tokens and temperatures are as for kps_token_logprobs; with lp and H the
+ * token's log-probability and the row's entropy, r = exp(lp - old_logprob) and
+ * u = ref_logprob - lp:
+ *
+ *   out_loss [N] = weight (-min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *                          + kl_coef (exp(u) - u - 1) - entropy_coef H)
+ *   out_logprob, out_entropy [N] = lp, H
+ *   out_grad [N, V] (dt, rows ld_grad apart) = d out_loss / d logits
+ *
+ *   old_logprob, advantage (A), ref_logprob, weight  [N] fp32; ref_logprob may be
+ *            NULL where kl_coef is 0, weight NULL: 1
+ *   clip_low, clip_high >= 0 (infinity: no bound); kl_coef, entropy_coef finite
+ *
+ * A row whose token lies outside [0, V) or whose weight is 0 is empty: its logits
+ * are not looked at, and loss, lp, H and gradient are 0.  The clipped branch has
+ * no gradient where it is the smaller one (r > 1 + clip_high with A >= 0, r < 1 -
+ * clip_low with A < 0).  A row without a distribution has NaN everywhere; ratios
+ * and penalties that leave fp32 follow IEEE arithmetic.  out_grad must lie
+ * outside the logits; the outputs must not overlap each other or the inputs.
+ */
+kps_status kps_policy_loss_grad(const void* logits, kps_dtype dt, int64_t N, int64_t V, int64_t ld, const int64_t* tokens,
+                                float temperature, const float* temperatures, const float* old_logprob,
+                                const float* advantage, const float* ref_logprob, const float* weight, float clip_low,
+                                float clip_high, float kl_coef, float entropy_coef, float* out_loss, float* out_logprob,
+                                float* out_entropy, void* out_grad, int64_t ld_grad, cudaStream_t stream);
 
 /* Which kernel the most recent kps_sample call of the calling host thread
  * that launched one used: 1 = the cluster kernel (kps_sample_kernel),
