@@ -18,6 +18,7 @@
 
 #include <cooperative_groups.h>
 
+#include <atomic>
 #include <climits>
 #include <cmath>
 
@@ -63,7 +64,7 @@ __global__ void __launch_bounds__(kNT, 4) score_kernel(const Args A) {
   const RowView<kBF16> x(A.x, row * A.ld, A.V);
   const int64_t t = A.tokens[row];
   const float tau = row_tau(A.taus, A.tau, row);
-  if (t < 0 || t >= A.V) {  // an empty row
+  if (t < 0 || t >= A.V || (A.weight && A.weight[row] == 0.0f)) {  // an empty row
     if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (rank == 0) put_empty(A, row, kNT);
     return;
@@ -175,7 +176,7 @@ struct Grad {
   void* out;
   int64_t ld_out;
   // the policy loss (kPolicy): a.max, a.eps, a.q lie in loss, a.logprob, a.entropy, which are written last
-  const float *old, *advantage, *ref, *weight;  // ref, weight: or nullptr
+  const float *old, *advantage, *ref;  // ref: or nullptr
   float lo, hi, kl, ent;
   float* loss;
 };
@@ -217,6 +218,7 @@ struct PolicyTerm {
 // A row's gradient: e_v (A + B z_v) with e_v = 2^z_v, z_v = (x_v - m) c; the token's apart.
 struct Slope {
   float a, b, token;
+  __device__ __forceinline__ Slope(float a_, float b_, float token_) : a(a_), b(b_), token(token_) {}
   __device__ __forceinline__ Slope(const Row& r, float x_token, float tau, float c, float g, float h) {
     const float inv = 1.0f / (1.0f + r.eps);
     const float gt = g / tau, ht = h / tau;
@@ -238,6 +240,16 @@ template <bool kBF16>
 __device__ __forceinline__ void put_elem(void* base, int64_t v, float d) {
   if (kBF16) static_cast<__nv_bfloat16*>(base)[v] = __float2bfloat16_rn(d);
   else static_cast<float*>(base)[v] = d;
+}
+// Zeros to a CTA's part of a row of the gradient.
+template <bool kBF16>
+__device__ __forceinline__ void zero_part(const RowView<kBF16>& o, int rank, int CS) {
+  const int o0 = static_cast<int>(static_cast<int64_t>(o.nv) * rank / CS);
+  const int o1 = static_cast<int>(static_cast<int64_t>(o.nv) * (rank + 1) / CS);
+  uint4* ov = const_cast<uint4*>(o.vec);
+  for (int i = o0 + static_cast<int>(threadIdx.x); i < o1; i += kNT) __stcs(ov + i, make_uint4(0u, 0u, 0u, 0u));
+  if (rank == 0 && static_cast<int>(threadIdx.x) < o.loose())
+    put_elem<kBF16>(const_cast<unsigned char*>(o.base), o.loose_at(threadIdx.x), 0.0f);
 }
 template <bool kBF16>
 __device__ __forceinline__ uint4 slope_vec(const uint4& w, f32x2 nm2, f32x2 c2, f32x2 a2, f32x2 b2) {
@@ -275,7 +287,7 @@ __global__ void __launch_bounds__(kNT, 4) slope_kernel(const Grad P) {
   float g = 0.0f, h = 0.0f, w = 1.0f;
   bool live = t >= 0 && t < A.V;
   if constexpr (kPolicy) {
-    if (P.weight) w = P.weight[row];
+    if (A.weight) w = A.weight[row];
     live = live && w != 0.0f;
   } else {
     if (P.g) g = P.g[row];
@@ -283,11 +295,7 @@ __global__ void __launch_bounds__(kNT, 4) slope_kernel(const Grad P) {
     live = live && (g != 0.0f || h != 0.0f);
   }
   if (!live) {  // zeros; the row is not looked at (the same in every CTA of the row)
-    const int o0 = static_cast<int>(static_cast<int64_t>(o.nv) * rank / CS);
-    const int o1 = static_cast<int>(static_cast<int64_t>(o.nv) * (rank + 1) / CS);
-    uint4* ov = const_cast<uint4*>(o.vec);
-    for (int i = o0 + static_cast<int>(threadIdx.x); i < o1; i += kNT) __stcs(ov + i, make_uint4(0u, 0u, 0u, 0u));
-    if (rank == 0 && static_cast<int>(threadIdx.x) < o.loose()) put_elem<kBF16>(obase, o.loose_at(threadIdx.x), 0.0f);
+    zero_part<kBF16>(o, rank, CS);
     if (kPolicy && rank == 0 && threadIdx.x == 0) P.loss[row] = A.logprob[row] = A.entropy[row] = 0.0f;
     return;
   }
@@ -341,23 +349,181 @@ __global__ void __launch_bounds__(kNT, 4) slope_kernel(const Grad P) {
 }
 
 // ------------------------------------------------------------------------------------------
+// The policy loss with the row in shared memory
+// ------------------------------------------------------------------------------------------
+//
+// The row is read once, by a bulk copy into the shared memory of each of a cluster's CTAs, summed
+// there against the CTA's largest logit, turned into the gradient in place and copied out.
+constexpr int kChunkBytes = 52 * 1024;  // of a row per CTA, where the cluster allows: four CTAs an SM
+
+template <bool kBF16>
+__global__ void __launch_bounds__(kNT, 4) policy_kernel(const Grad P, const int share) {
+  constexpr int G = kBF16 ? 8 : 4;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float sums[kMaxCS * kNW][2];  // S and W of the cluster's warps
+  __shared__ float tops[kMaxCS];           // the CTAs' largest logits
+  __shared__ uint32_t keys[kNW];
+  __shared__ float factors[4];             // m, a, b and the token's gradient
+  __shared__ __align__(8) unsigned long long landed, gathered;  // the barriers of the copy and of sums and tops
+  const Args& A = P.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  cg::cluster_group cl = cg::this_cluster();
+  const int CS = static_cast<int>(cl.num_blocks());
+  const int rank = static_cast<int>(cl.block_rank());
+  uint32_t cluster;
+  asm("mov.u32 %0, %%clusterid.x;" : "=r"(cluster));
+  const int64_t row = cluster;
+  if (threadIdx.x == 0) {
+    copy_barrier_init(&landed);
+    copy_barrier_init(&gathered);
+    expect_bytes(&gathered, static_cast<uint32_t>(CS * (2 * kNW + 1) * sizeof(float)));
+  }
+  __syncwarp();
+  // every CTA of the cluster runs, and has set up its barriers, before any writes into another's
+  // shared memory (the barriers' own fence is behind their setting up)
+  if (CS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const RowView<kBF16> x(A.x, row * A.ld, A.V), o(P.out, row * P.ld_out, A.V);
+  unsigned char* const obase = const_cast<unsigned char*>(o.base);
+  const int g0 = min(rank * share, x.nv), g1 = rank == CS - 1 ? x.nv : min(g0 + share, x.nv);
+  uint4* const mine = reinterpret_cast<uint4*>(smem) + threadIdx.x;  // the thread's vectors: mine[i kNT], i < count
+  const int first = g0 + static_cast<int>(threadIdx.x), count = first < g1 ? (g1 - first - 1) / kNT + 1 : 0;
+  const int64_t t = A.tokens[row];
+  const float w = A.weight ? A.weight[row] : 1.0f;
+  if (t < 0 || t >= A.V || w == 0.0f) {  // an empty row: zeros (the same in every CTA of the row)
+    if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    zero_part<kBF16>(o, rank, CS);
+    if (rank == 0 && threadIdx.x == 0) P.loss[row] = A.logprob[row] = A.entropy[row] = 0.0f;
+    return;
+  }
+  if (threadIdx.x == 0 && g1 > g0) copy_in(smem, x.vec + g0, static_cast<uint32_t>(g1 - g0) * 16u, &landed);
+  const float tau = row_tau(A.taus, A.tau, row), c = kLog2e / tau;
+  const float x_token = x.at(static_cast<int>(t));
+  // the elements outside the vectors: the head with rank 0, the tail with the last rank
+  const bool has_loose = static_cast<int>(threadIdx.x) < x.loose() &&
+                         ((x.loose_at(threadIdx.x) < x.head) ? rank == 0 : rank == CS - 1);
+  const int loose_v = has_loose ? x.loose_at(threadIdx.x) : 0;
+  const float loose_x = has_loose ? x.at(loose_v) : -INFINITY;
+  __syncthreads();  // the barriers are set up
+  const bool late = __any_sync(0xffffffffu, g1 > g0 && !copy_landed(&landed));  // the wait ran out
+
+  // ---- the CTA's largest logit, and the thread that holds it ---------------------------------------
+  float most = no_nan(loose_x);
+  int at = -1;  // its vector (-1: the element outside)
+#pragma unroll 4
+  for (int i = 0; i < count; ++i) {
+    const float m = vec_max<kBF16>(mine[i * kNT]);
+    if (m > most) {
+      most = m;
+      at = i;
+    }
+  }
+  const uint32_t key = order_key(most + 0.0f), warp_key = __reduce_max_sync(0xffffffffu, key);
+  if (lane == 0) keys[warp] = warp_key;
+  __syncthreads();
+  const uint32_t other = keys[lane & (kNW - 1)], top_key = __reduce_max_sync(0xffffffffu, other);
+  const float top = order_value(top_key);
+  const bool holds = warp == __ffs(__ballot_sync(0xffffffffu, other == top_key)) - 1 &&
+                     lane == __ffs(__ballot_sync(0xffffffffu, key == top_key)) - 1;
+
+  // ---- the sums of everything else -----------------------------------------------------------------
+  const float ref = top > -INFINITY ? top : 0.0f;
+  {
+    Moments<kBF16> sum;
+    const f32x2 nref2 = pack2(-ref, -ref), c2 = pack2(c, c);
+    const int skip = holds ? at : -2;
+#pragma unroll 2
+    for (int i = 0; i < count; ++i) {
+      uint4 v = mine[i * kNT];
+      if (i == skip) strike<kBF16>(v, top);
+      sum.add(v, nref2, c2);
+    }
+    const float z = exponent(skip == -1 ? -INFINITY : loose_x, ref, c), e = ex2(z);
+    float s = warp_sum(sum.sum() + e);
+    const float m1 = warp_sum(sum.moment() + e * z);
+    if (late) s = NAN;  // a part that did not arrive leaves its row without a result
+    if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // (of the arrival at the top)
+    if (lane < CS) {
+      send_float(&sums[rank * kNW + warp][0], s, &gathered, lane);
+      send_float(&sums[rank * kNW + warp][1], m1, &gathered, lane);
+      if (warp == 0) send_float(&tops[rank], top, &gathered, lane);
+    }
+  }
+
+  // ---- the row's statistics, its loss and the gradient's factors, by one warp ------------------------
+  if (warp == 0) {
+    const bool lost = !copy_landed(&gathered);
+    float m = lane < CS ? tops[lane] : -INFINITY;
+    m = warp_top(m);
+    const int owner = __ffs(__ballot_sync(0xffffffffu, lane < CS && tops[lane & (kMaxCS - 1)] == m)) - 1;
+    float s = 0.0f, m1 = 0.0f;
+    for (int i = lane; i < kNW * CS; i += 32) {
+      const int cta = i / kNW;
+      float a, b;  // (a CTA's largest element enters with its first warp)
+      part_to_row(Part{tops[cta], sums[i][0], sums[i][1], 0.0f}, i % kNW != 0 || cta == owner, m, c, a, b);
+      s += a;
+      m1 += b;
+    }
+    s = warp_sum(s);
+    m1 = warp_sum(m1);
+    const Row r(m, lost ? NAN : s, m1);
+    const float logprob = r.logprob(x_token, tau), entropy = r.entropy();
+    const PolicyTerm term(P, row, w, logprob, entropy);
+    const Slope slope(r, x_token, tau, c, term.g, term.h);
+    if (lane == 0) {
+      factors[0] = r.m;
+      factors[1] = slope.a;
+      factors[2] = slope.b;
+      factors[3] = slope.token;
+      if (rank == 0) {
+        P.loss[row] = term.loss;
+        A.logprob[row] = logprob;
+        A.entropy[row] = entropy;
+      }
+    }
+  }
+  __syncthreads();
+
+  // ---- the gradient: in place in shared memory, and out with one copy --------------------------------
+  const float m = factors[0];
+  const Slope slope(factors[1], factors[2], factors[3]);
+  const int v0 = x.head + g0 * G, v1 = x.head + g1 * G;  // this CTA's vectors
+  const bool inside = t >= v0 && t < v1;
+  if (o.head == x.head && slope.tame()) {
+    const f32x2 nm2 = pack2(-m, -m), c2 = pack2(c, c), a2 = pack2(slope.a, slope.a), b2 = pack2(slope.b, slope.b);
+#pragma unroll 2
+    for (int i = 0; i < count; ++i) mine[i * kNT] = slope_vec<kBF16>(mine[i * kNT], nm2, c2, a2, b2);
+    if (inside && (static_cast<int>(t) - v0) / G % kNT == static_cast<int>(threadIdx.x))  // behind the vector, by the same thread
+      put_elem<kBF16>(smem, t - v0, slope.token);
+    publish_to_copies();
+    __syncthreads();
+    if (threadIdx.x == 0 && g1 > g0) copy_out(const_cast<uint4*>(o.vec) + g0, smem, static_cast<uint32_t>(g1 - g0) * 16u);
+  } else {
+    // the two rows do not share their 16-byte boundaries, or the numbers are extreme: one element at a time
+    for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kNT) {
+      const float y = kBF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(smem)[v - v0]) : reinterpret_cast<const float*>(smem)[v - v0];
+      put_elem<kBF16>(obase, v, v == t ? slope.token : slope.at(y, m, c));
+    }
+  }
+  if (has_loose) put_elem<kBF16>(obase, loose_v, loose_v == t ? slope.token : slope.at(loose_x, m, c));
+  if (late) copy_landed(&landed);  // one more wait before the block leaves
+}
+
+// ------------------------------------------------------------------------------------------
 // Host side
 // ------------------------------------------------------------------------------------------
-// Launches a kernel of a cluster a row: one CTA, or for few rows up to kMaxCS while every thread keeps
-// four vectors.
-template <class Kernel, class P>
-static kps_status launch_rows(Kernel* kernel, const P& params, int64_t N, int64_t V, bool bf16, cudaStream_t stream) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return KPS_ERR_CUDA;
-  }
-  int cs = 1;
-  const int64_t round = static_cast<int64_t>(kNT) * 4 * (bf16 ? 8 : 4);
-  while (cs < kMaxCS && N * cs * 2 <= 2 * sms && V >= 2 * cs * round) cs *= 2;
+static int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) return n;
+  (void)cudaGetLastError();
+  return 0;
+}
+// Launches a kernel with a cluster of cs CTAs a row.
+template <class... Params, class... Values>
+static kps_status launch_clusters(void (*kernel)(Params...), int64_t N, int cs, size_t shared, cudaStream_t stream, const Values&... values) {
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(static_cast<unsigned>(N * cs));
   lc.blockDim = dim3(kNT);
+  lc.dynamicSmemBytes = shared;
   lc.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -366,21 +532,69 @@ static kps_status launch_rows(Kernel* kernel, const P& params, int64_t N, int64_
   attr[0].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  if (cudaLaunchKernelEx(&lc, kernel, params) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return KPS_ERR_CUDA;
-  }
-  return KPS_OK;
+  if (cudaLaunchKernelEx(&lc, kernel, values...) == cudaSuccess) return KPS_OK;
+  (void)cudaGetLastError();
+  return KPS_ERR_CUDA;
+}
+// A streaming kernel: one CTA a row, or for few rows up to kMaxCS while every thread keeps four vectors.
+template <class P>
+static kps_status launch_rows(void (*kernel)(P), const Args& a, kps_dtype dt, const P& params, cudaStream_t stream) {
+  const int sms = sm_count();
+  if (!sms) return KPS_ERR_CUDA;
+  int cs = 1;
+  const int64_t round = static_cast<int64_t>(kNT) * 4 * (dt == KPS_BF16 ? 8 : 4);
+  while (cs < kMaxCS && a.N * cs * 2 <= 2 * sms && a.V >= 2 * cs * round) cs *= 2;
+  return launch_clusters(kernel, a.N, cs, 0, stream, params);
 }
 static kps_status launch_score(const Args& a, kps_dtype dt, cudaStream_t stream) {
   if (a.n > 0) return launch_alternatives(a, dt, stream);
-  return dt == KPS_BF16 ? launch_rows(score_kernel<true>, a, a.N, a.V, true, stream)
-                        : launch_rows(score_kernel<false>, a, a.N, a.V, false, stream);
+  return launch_rows<Args>(dt == KPS_BF16 ? score_kernel<true> : score_kernel<false>, a, dt, a, stream);
 }
 template <bool kPolicy>
 static kps_status launch_slope(const Grad& P, kps_dtype dt, cudaStream_t stream) {
-  return dt == KPS_BF16 ? launch_rows(slope_kernel<true, kPolicy>, P, P.a.N, P.a.V, true, stream)
-                        : launch_rows(slope_kernel<false, kPolicy>, P, P.a.N, P.a.V, false, stream);
+  return launch_rows<Grad>(dt == KPS_BF16 ? slope_kernel<true, kPolicy> : slope_kernel<false, kPolicy>, P.a, dt, P, stream);
+}
+
+// The policy loss: with the row in shared memory where a cluster's holds it (up to 1.8 MB); longer rows
+// are read twice, in two launches, and their statistics lie where the second leaves the results.
+constexpr int kMaxDynamic = 224 * 1024;
+constexpr int kMaxDevices = 64;
+template <bool kBF16>
+static kps_status launch_policy(const Grad& P, cudaStream_t stream) {
+  constexpr int G = kBF16 ? 8 : 4;
+  const int64_t bytes = static_cast<int64_t>(P.a.V) * (kBF16 ? 2 : 4);
+  const int sms = sm_count();
+  if (!sms) return KPS_ERR_CUDA;
+  int cs = static_cast<int>((bytes + kChunkBytes - 1) / kChunkBytes);
+  cs = cs < 1 ? 1 : cs > kMaxCS ? kMaxCS : cs;
+  // few rows: wider clusters, while every thread keeps four vectors
+  while (2 * cs <= kMaxCS && P.a.N * cs * 2 <= 2 * sms && P.a.V >= 2 * cs * kNT * 4 * G) cs *= 2;
+  const int share = (P.a.V / G + cs - 1) / cs;
+  const size_t total = static_cast<size_t>(share) * 16;
+  if (total > kMaxDynamic) {
+    const kps_dtype dt = kBF16 ? KPS_BF16 : KPS_F32;
+    Grad two = P;
+    two.a.max = P.loss;
+    two.a.eps = P.a.logprob;
+    two.a.q = P.a.entropy;
+    Args a = two.a;
+    a.logprob = a.entropy = nullptr;
+    const kps_status st = launch_score(a, dt, stream);
+    return st != KPS_OK ? st : launch_slope<true>(two, dt, stream);
+  }
+  // as much dynamic shared memory as a block can have, once for each device: the same for every call,
+  // so that calls side by side do not undo each other's
+  static std::atomic<bool> done[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return KPS_ERR_CUDA;
+  if (!done[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(policy_kernel<kBF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return KPS_ERR_CUDA;
+    }
+    done[dev].store(true, std::memory_order_release);
+  }
+  return launch_clusters(policy_kernel<kBF16>, P.a.N, cs, total, stream, P, share);
 }
 
 static bool misaligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
@@ -491,17 +705,10 @@ kps_status kps_policy_loss_grad(const void* logits, kps_dtype dt, int64_t N, int
                         static_cast<const void*>(out_entropy)})
     if (ks::misaligned(p, 4)) return KPS_ERR_INVALID_ARG;
   if ((st = ks::check_grad(P.a, dt, out_grad, ld_grad)) != KPS_OK) return st;
-  // the statistics of the first launch lie where the second leaves the results
-  P.a.max = out_loss;
-  P.a.eps = out_logprob;
-  P.a.q = out_entropy;
-  if ((st = ks::launch_score(P.a, dt, stream)) != KPS_OK) return st;
-  P.a.logprob = out_logprob;
-  P.a.entropy = out_entropy;
+  P.a.weight = weight;
   P.old = old_logprob;
   P.advantage = advantage;
   P.ref = ref_logprob;
-  P.weight = weight;
   P.lo = clip_low;
   P.hi = clip_high;
   P.kl = kl_coef;
@@ -509,7 +716,9 @@ kps_status kps_policy_loss_grad(const void* logits, kps_dtype dt, int64_t N, int
   P.loss = out_loss;
   P.out = out_grad;
   P.ld_out = ld_grad;
-  return ks::launch_slope<true>(P, dt, stream);
+  P.a.logprob = out_logprob;
+  P.a.entropy = out_entropy;
+  return dt == KPS_BF16 ? ks::launch_policy<true>(P, stream) : ks::launch_policy<false>(P, stream);
 }
 
 }  // extern "C"

@@ -35,6 +35,7 @@ struct Args {
   float tau;           // where taus is nullptr
   const float* taus;
   const int64_t* tokens;
+  const float* weight;  // a row of weight 0 is empty, or nullptr (without alternatives only)
   float* logprob;
   float* entropy;
   int32_t* rank;
