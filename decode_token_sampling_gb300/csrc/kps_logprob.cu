@@ -21,6 +21,7 @@
 #include <atomic>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 namespace cg = cooperative_groups;
 
@@ -29,7 +30,6 @@ namespace score {
 
 constexpr int kNT = 256;  // threads per CTA
 constexpr int kNW = kNT / 32;
-constexpr int kU = 6;         // 16-byte loads each thread keeps in flight
 constexpr int kMaxCS = 8;     // widest cluster (the portable limit)
 
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -51,8 +51,14 @@ __device__ __forceinline__ float warp_top(float x) {
 // A warp's sums are against the largest logit that it has seen, looked for once in a round of loads:
 // it rises some three times in a row's dozen rounds.  The element that holds it stays out of the sums
 // until a larger one takes its place.
+//
+// 4096 rows of 151936 bf16, a quarter of them empty: 147 us (140 at the copy rate) with five loads in flight
+// and five CTAs an SM; six and four 153, four and five 151, eight and four 153, eight and three 165; four and
+// six 147, but 16.4 instead of 15.0 us for 333 rows of 50001 fp32, whose CTAs are few.  Rounds that all look
+// where the row ends took 160 with six and four.
 template <bool kBF16>
-__global__ void __launch_bounds__(kNT, 4) score_kernel(const Args A) {
+__global__ void __launch_bounds__(kNT, 5) score_kernel(const Args A) {
+  constexpr int kU = 5;  // 16-byte loads each thread keeps in flight
   __shared__ Part part[kMaxCS * kNW];  // of the cluster's warps (rank 0's are used)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   cg::cluster_group cl = cg::this_cluster();
@@ -73,31 +79,34 @@ __global__ void __launch_bounds__(kNT, 4) score_kernel(const Args A) {
   const int g0 = static_cast<int>(static_cast<int64_t>(x.nv) * rank / CS);
   const int g1 = static_cast<int>(static_cast<int64_t>(x.nv) * (rank + 1) / CS);
   const float c = kLog2e / tau;
-  const f32x2 c2 = pack2(c, c);
 
   Moments<kBF16> sum;
   float top = -INFINITY;  // the warp's largest so far; the sums' reference (0 before there is one)
+  const f32x2 c2 = pack2(c, c);
   f32x2 nref2 = 0ull;
   float above = 0.0f;
   // The reference rises to `to`; the element that held it joins the sums.
   auto raise = [&](float to) {
     if (top > -INFINITY) {
-      const float delta = fminf((to - top) * c, -kFloor), f = ex2(-delta);
-      sum.shift(delta, f);
+      const float delta = fminf((to - top) * c, -kFloor);
+      sum.shift(delta);
       if (lane == 0) {
-        sum.s[0] = add2(sum.s[0], pack2(f, 0.0f));
-        sum.w[0] = add2(sum.w[0], pack2(-delta * f, 0.0f));
+        const float e = ex2(-delta);
+        sum.s[0] = add2(sum.s[0], pack2(e, 0.0f));
+        sum.w[0] = add2(sum.w[0], pack2(-delta * e, 0.0f));
       }
     }
     top = to;
     nref2 = pack2(-to, -to);
   };
-  for (int base = g0; base < g1; base += kNT * kU) {
+  // a round of loads; only the last one has to look where the CTA's part ends
+  auto round = [&](int base, auto full) {
+    constexpr bool kFull = decltype(full)::value;
     uint4 w[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int g = base + u * kNT + static_cast<int>(threadIdx.x);
-      w[u] = g < g1 ? ld_stream(x.vec + g) : neg_inf_vec<kBF16>();
+      w[u] = kFull || g < g1 ? ld_stream(x.vec + g) : neg_inf_vec<kBF16>();
     }
     float m[kU], most = -INFINITY;
 #pragma unroll
@@ -122,8 +131,12 @@ __global__ void __launch_bounds__(kNT, 4) score_kernel(const Args A) {
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) sum.add(w[u], nref2, c2);
-  }
-  float s = 0.0f, moment = 0.0f;
+  };
+  int base = g0;
+#pragma unroll 1
+  for (; base + kNT * kU <= g1; base += kNT * kU) round(base, std::true_type{});
+  if (base < g1) round(base, std::false_type{});
+  float extra = 0.0f, extra_w = 0.0f;
   if (warp == 0) {  // the elements outside the vectors: the head with rank 0, the tail with the last rank
     const bool in = lane < x.loose() && ((x.loose_at(lane) < x.head) ? rank == 0 : rank == CS - 1);
     float y = in ? x.at(x.loose_at(lane)) : -INFINITY;
@@ -135,11 +148,10 @@ __global__ void __launch_bounds__(kNT, 4) score_kernel(const Args A) {
       if (lane == __ffs(who) - 1) y = -INFINITY;
     }
     const float z = exponent(y, top == -INFINITY ? 0.0f : top, c);
-    s = ex2(z);
-    moment = s * z;
+    extra = ex2(z);
+    extra_w = extra * z;
   }
-  s = warp_sum(s + sum.sum());
-  moment = warp_sum(moment + sum.moment());
+  const float s = warp_sum(extra + sum.sum()), moment = warp_sum(extra_w + sum.moment());
   above = warp_sum(above);
   Part* to = CS > 1 ? cl.map_shared_rank(&part[0], 0) : part;
   if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -190,11 +202,22 @@ __device__ __forceinline__ float expm1_minus(float u) {
   return 0.5f * u * u * t;
 }
 
+// What a row's loss needs beside its logits.
+struct PolicyRow {
+  float w, A, old, ref;
+  PolicyRow() = default;
+  __device__ __forceinline__ PolicyRow(const Grad& P, int64_t row) {
+    w = P.a.weight ? P.a.weight[row] : 1.0f;
+    A = P.advantage[row];
+    old = P.old[row];
+    ref = P.kl != 0.0f ? P.ref[row] : 0.0f;
+  }
+};
 // A row's loss and the gradients of its log-probability and entropy.
 struct PolicyTerm {
   float loss, g, h;
-  __device__ __forceinline__ PolicyTerm(const Grad& P, int64_t row, float w, float logprob, float entropy) {
-    const float A = P.advantage[row], r = expf(logprob - P.old[row]);
+  __device__ __forceinline__ PolicyTerm(const Grad& P, const PolicyRow& in, float logprob, float entropy) {
+    const float A = in.A, w = in.w, r = expf(logprob - in.old);
     const float kept = fminf(fmaxf(r, 1.0f - P.lo), 1.0f + P.hi);
     const bool clipped = A >= 0.0f ? r > 1.0f + P.hi : r < 1.0f - P.lo;
     float v = 0.0f, d = 0.0f;
@@ -203,7 +226,7 @@ struct PolicyTerm {
       d = clipped ? 0.0f : -A * r;
     }
     if (P.kl != 0.0f) {
-      const float u = P.ref[row] - logprob;
+      const float u = in.ref - logprob;
       v += P.kl * expm1_minus(u);
       d -= P.kl * expm1f(u);
     }
@@ -251,16 +274,23 @@ __device__ __forceinline__ void zero_part(const RowView<kBF16>& o, int rank, int
   if (rank == 0 && static_cast<int>(threadIdx.x) < o.loose())
     put_elem<kBF16>(const_cast<unsigned char*>(o.base), o.loose_at(threadIdx.x), 0.0f);
 }
+// The gradient of a vector's elements.  Without b one multiply-add an exponent does, as nothing cancels:
+// x c - rc with rc the rounded product of m and c, put right in a.
 template <bool kBF16>
-__device__ __forceinline__ uint4 slope_vec(const uint4& w, f32x2 nm2, f32x2 c2, f32x2 a2, f32x2 b2) {
-  uint32_t out[4];
-#pragma unroll
-  for (int i = 0; i < (kBF16 ? 4 : 2); ++i) {
-    float p, q;
-    unpack2(mul2(add2(pair_of<kBF16>(w, i), nm2), c2), p, q);
-    p = max_nan(p, kFloor);
-    q = max_nan(q, kFloor);
-    unpack2(mul2(pack2(ex2(p), ex2(q)), fma2(b2, pack2(p, q), a2)), p, q);
+struct SlopeVec {
+  f32x2 c2, n2, a2, b2;
+  bool flat, usable;  // b is 0; the vectors' way does for this row
+  __device__ __forceinline__ SlopeVec(const Slope& s, float m, float c) {
+    const float rc = m * c;
+    flat = s.b == 0.0f && fabsf(rc) <= kFastRef;
+    const float a = flat ? s.a * ex2(-fmaf(m, c, -rc)) : s.a, n = flat ? -rc : -m;
+    c2 = pack2(c, c);
+    n2 = pack2(n, n);
+    a2 = pack2(a, a);
+    b2 = pack2(s.b, s.b);
+    usable = s.tame();
+  }
+  static __device__ __forceinline__ void put(uint32_t* out, int i, float p, float q) {
     if (kBF16) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(p, q);  // the gradient's one rounding
       out[i] = reinterpret_cast<const uint32_t&>(h);
@@ -269,11 +299,35 @@ __device__ __forceinline__ uint4 slope_vec(const uint4& w, f32x2 nm2, f32x2 c2, 
       out[2 * i + 1] = __float_as_uint(q);
     }
   }
-  return make_uint4(out[0], out[1], out[2], out[3]);
-}
+  template <bool kFlat, bool kFree = false>
+  __device__ __forceinline__ uint4 of(const uint4& v) const {
+    uint32_t out[4];
+#pragma unroll
+    for (int i = 0; i < (kBF16 ? 4 : 2); ++i) {
+      const f32x2 x = pair_of<kBF16>(v, i);
+      float p, q;
+      if (kFlat) {
+        unpack2(fma2(x, c2, n2), p, q);
+        unpack2(mul2(pack2(ex2(p), ex2(q)), a2), p, q);
+      } else {
+        unpack2(mul2(add2(x, n2), c2), p, q);
+        if (!kFree) {
+          p = max_nan(p, kFloor);
+          q = max_nan(q, kFloor);
+        }
+        unpack2(mul2(pack2(ex2(p), ex2(q)), fma2(b2, pack2(p, q), a2)), p, q);
+      }
+      put(out, i, p, q);
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+  }
+};
 
+// 2048 rows of 128256 bf16, a quarter of them empty: 141 us (138 at the copy rate) with six loads in flight
+// and four CTAs an SM; four and four 142, five and five 145; of 333 rows of 50001 fp32 23.6, 26.0 and 24.6.
 template <bool kBF16, bool kPolicy>
 __global__ void __launch_bounds__(kNT, 4) slope_kernel(const Grad P) {
+  constexpr int kU = 6;  // 16-byte loads each thread keeps in flight
   constexpr int G = kBF16 ? 8 : 4;
   const Args& A = P.a;
   cg::cluster_group cl = cg::this_cluster();
@@ -284,11 +338,10 @@ __global__ void __launch_bounds__(kNT, 4) slope_kernel(const Grad P) {
   unsigned char* const obase = const_cast<unsigned char*>(o.base);
   const int64_t t = A.tokens[row];
   const float tau = row_tau(A.taus, A.tau, row), c = kLog2e / tau;
-  float g = 0.0f, h = 0.0f, w = 1.0f;
+  float g = 0.0f, h = 0.0f;
   bool live = t >= 0 && t < A.V;
   if constexpr (kPolicy) {
-    if (A.weight) w = A.weight[row];
-    live = live && w != 0.0f;
+    live = live && !(A.weight && A.weight[row] == 0.0f);
   } else {
     if (P.g) g = P.g[row];
     if (P.h) h = P.h[row];
@@ -303,7 +356,7 @@ __global__ void __launch_bounds__(kNT, 4) slope_kernel(const Grad P) {
   const float x_token = x.at(static_cast<int>(t));
   if constexpr (kPolicy) {
     const float logprob = r.logprob(x_token, tau), entropy = r.entropy();
-    const PolicyTerm term(P, row, w, logprob, entropy);
+    const PolicyTerm term(P, PolicyRow(P, row), logprob, entropy);
     g = term.g;
     h = term.h;
     if (CS > 1) cl.sync(); else __syncthreads();  // every thread of the row has read its statistics
@@ -318,24 +371,32 @@ __global__ void __launch_bounds__(kNT, 4) slope_kernel(const Grad P) {
   const int g1 = static_cast<int>(static_cast<int64_t>(x.nv) * (rank + 1) / CS);
   const int at = static_cast<int>(t) - x.head;  // the token's vector, if it is in one
   const int tv = at >= 0 && at < x.nv * G ? at / G : -1;
-  if (o.head == x.head && slope.tame()) {
-    const f32x2 nm2 = pack2(-r.m, -r.m), c2 = pack2(c, c), a2 = pack2(slope.a, slope.a), b2 = pack2(slope.b, slope.b);
+  const SlopeVec<kBF16> vec(slope, r.m, c);
+  if (o.head == x.head && vec.usable) {
     uint4* ov = const_cast<uint4*>(o.vec);
-    for (int base = g0; base < g1; base += kNT * kU) {
+    auto round = [&](int base, auto flat, auto full) {
+      constexpr bool kFull = decltype(full)::value;
       uint4 v[kU];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int i = base + u * kNT + static_cast<int>(threadIdx.x);
-        v[u] = i < g1 ? ld_stream(x.vec + i) : neg_inf_vec<kBF16>();
+        v[u] = kFull || i < g1 ? ld_stream(x.vec + i) : neg_inf_vec<kBF16>();
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int i = base + u * kNT + static_cast<int>(threadIdx.x);
-        if (i >= g1) continue;
-        __stcs(ov + i, slope_vec<kBF16>(v[u], nm2, c2, a2, b2));
-        if (i == tv) put_elem<kBF16>(obase, t, slope.token);  // by the thread that wrote the vector, behind it
+        if (kFull || i < g1) __stcs(ov + i, vec.template of<decltype(flat)::value>(v[u]));
+        if (i == tv && i < g1) put_elem<kBF16>(obase, t, slope.token);  // by the thread that wrote the vector, behind it
       }
-    }
+    };
+    auto pass = [&](auto flat) {
+      int base = g0;
+#pragma unroll 1
+      for (; base + kNT * kU <= g1; base += kNT * kU) round(base, flat, std::true_type{});
+      if (base < g1) round(base, flat, std::false_type{});
+    };
+    if (vec.flat) pass(std::true_type{});
+    else pass(std::false_type{});
     if (static_cast<int>(threadIdx.x) < x.loose()) {
       const int v = x.loose_at(threadIdx.x);
       if ((v < x.head) ? rank == 0 : rank == CS - 1) put_elem<kBF16>(obase, v, v == t ? slope.token : slope.at(x.at(v), r.m, c));
@@ -354,15 +415,20 @@ __global__ void __launch_bounds__(kNT, 4) slope_kernel(const Grad P) {
 //
 // The row is read once, by a bulk copy into the shared memory of each of a cluster's CTAs, summed
 // there against the CTA's largest logit, turned into the gradient in place and copied out.
-constexpr int kChunkBytes = 52 * 1024;  // of a row per CTA, where the cluster allows: four CTAs an SM
+// Bytes of a row per CTA, where the cluster allows: five CTAs an SM (48 registers).  4096 rows of 151936
+// bf16 with a quarter empty: 366 us (326 at the copy rate); 52 KB and four CTAs 371, 62 KB and three 427
+// at the time.
+constexpr int kChunkBytes = 43 * 1024;
 
 template <bool kBF16>
-__global__ void __launch_bounds__(kNT, 4) policy_kernel(const Grad P, const int share) {
+__global__ void __launch_bounds__(kNT, 5) policy_kernel(const Grad P, const int share) {
   constexpr int G = kBF16 ? 8 : 4;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float sums[kMaxCS * kNW][2];  // S and W of the cluster's warps
   __shared__ float tops[kMaxCS];           // the CTAs' largest logits
   __shared__ uint32_t keys[kNW];
+  __shared__ PolicyRow inputs;
+  __shared__ float x_token;
   __shared__ float factors[4];             // m, a, b and the token's gradient
   __shared__ __align__(8) unsigned long long landed, gathered;  // the barriers of the copy and of sums and tops
   const Args& A = P.a;
@@ -388,58 +454,73 @@ __global__ void __launch_bounds__(kNT, 4) policy_kernel(const Grad P, const int 
   uint4* const mine = reinterpret_cast<uint4*>(smem) + threadIdx.x;  // the thread's vectors: mine[i kNT], i < count
   const int first = g0 + static_cast<int>(threadIdx.x), count = first < g1 ? (g1 - first - 1) / kNT + 1 : 0;
   const int64_t t = A.tokens[row];
-  const float w = A.weight ? A.weight[row] : 1.0f;
-  if (t < 0 || t >= A.V || w == 0.0f) {  // an empty row: zeros (the same in every CTA of the row)
+  if (t < 0 || t >= A.V || (A.weight && A.weight[row] == 0.0f)) {  // an empty row: zeros (the same in every CTA of the row)
     if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     zero_part<kBF16>(o, rank, CS);
     if (rank == 0 && threadIdx.x == 0) P.loss[row] = A.logprob[row] = A.entropy[row] = 0.0f;
     return;
   }
   if (threadIdx.x == 0 && g1 > g0) copy_in(smem, x.vec + g0, static_cast<uint32_t>(g1 - g0) * 16u, &landed);
-  const float tau = row_tau(A.taus, A.tau, row), c = kLog2e / tau;
-  const float x_token = x.at(static_cast<int>(t));
+  const float c = kLog2e / row_tau(A.taus, A.tau, row);
+  if (threadIdx.x == 0) {  // what the loss needs, so that nothing waits for it later
+    inputs = PolicyRow(P, row);
+    x_token = x.at(static_cast<int>(t));
+  }
   // the elements outside the vectors: the head with rank 0, the tail with the last rank
   const bool has_loose = static_cast<int>(threadIdx.x) < x.loose() &&
                          ((x.loose_at(threadIdx.x) < x.head) ? rank == 0 : rank == CS - 1);
   const int loose_v = has_loose ? x.loose_at(threadIdx.x) : 0;
-  const float loose_x = has_loose ? x.at(loose_v) : -INFINITY;
+  float loose_x = has_loose ? x.at(loose_v) : -INFINITY;
   __syncthreads();  // the barriers are set up
   const bool late = __any_sync(0xffffffffu, g1 > g0 && !copy_landed(&landed));  // the wait ran out
 
   // ---- the CTA's largest logit, and the thread that holds it ---------------------------------------
-  float most = no_nan(loose_x);
-  int at = -1;  // its vector (-1: the element outside)
+  uint4 best = neg_inf_vec<kBF16>(), least = make_uint4(0u, 0u, 0u, 0u);  // (no smallest above 0 is needed)
 #pragma unroll 4
   for (int i = 0; i < count; ++i) {
-    const float m = vec_max<kBF16>(mine[i * kNT]);
-    if (m > most) {
-      most = m;
-      at = i;
-    }
+    const uint4 v = mine[i * kNT];
+    best = vec_extreme<kBF16>(best, v);
+    least = vec_extreme<kBF16, true>(least, v);
   }
+  const float bottom = vec_min<kBF16>(least);
+  const float own = vec_max<kBF16>(best), most = fmaxf(no_nan(loose_x), no_nan(own));
   const uint32_t key = order_key(most + 0.0f), warp_key = __reduce_max_sync(0xffffffffu, key);
   if (lane == 0) keys[warp] = warp_key;
   __syncthreads();
   const uint32_t other = keys[lane & (kNW - 1)], top_key = __reduce_max_sync(0xffffffffu, other);
   const float top = order_value(top_key);
-  const bool holds = warp == __ffs(__ballot_sync(0xffffffffu, other == top_key)) - 1 &&
-                     lane == __ffs(__ballot_sync(0xffffffffu, key == top_key)) - 1;
+  const bool here = warp == __ffs(__ballot_sync(0xffffffffu, other == top_key)) - 1;
+  const bool holds = here && lane == __ffs(__ballot_sync(0xffffffffu, key == top_key)) - 1;
 
   // ---- the sums of everything else -----------------------------------------------------------------
   const float ref = top > -INFINITY ? top : 0.0f;
   {
     Moments<kBF16> sum;
     const f32x2 nref2 = pack2(-ref, -ref), c2 = pack2(c, c);
-    const int skip = holds ? at : -2;
-#pragma unroll 2
-    for (int i = 0; i < count; ++i) {
-      uint4 v = mine[i * kNT];
-      if (i == skip) strike<kBF16>(v, top);
-      sum.add(v, nref2, c2);
+    bool skip = holds;  // the element that stays out is still to come
+    if (skip && loose_x == top) {
+      loose_x = -INFINITY;
+      skip = false;
     }
-    const float z = exponent(skip == -1 ? -INFINITY : loose_x, ref, c), e = ex2(z);
-    float s = warp_sum(sum.sum() + e);
-    const float m1 = warp_sum(sum.moment() + e * z);
+    if (here) {
+#pragma unroll 4
+      for (int i = 0; i < count; ++i) {
+        uint4 v = mine[i * kNT];
+        if (skip && vec_max<kBF16>(v) == top) {
+          strike<kBF16>(v, top);
+          skip = false;
+        }
+        sum.add(v, nref2, c2);
+      }
+    } else if (__all_sync(0xffffffffu, (bottom - ref) * c >= kFloor)) {
+#pragma unroll 4
+      for (int i = 0; i < count; ++i) sum.template add<true>(mine[i * kNT], nref2, c2);
+    } else {
+      for (int i = 0; i < count; ++i) sum.add(mine[i * kNT], nref2, c2);
+    }
+    const float z = exponent(loose_x, ref, c), e = ex2(z);
+    float s = warp_sum(e + sum.sum());
+    const float m1 = warp_sum(e * z + sum.moment());
     if (late) s = NAN;  // a part that did not arrive leaves its row without a result
     if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // (of the arrival at the top)
     if (lane < CS) {
@@ -466,8 +547,9 @@ __global__ void __launch_bounds__(kNT, 4) policy_kernel(const Grad P, const int 
     s = warp_sum(s);
     m1 = warp_sum(m1);
     const Row r(m, lost ? NAN : s, m1);
+    const float tau = row_tau(A.taus, A.tau, row);
     const float logprob = r.logprob(x_token, tau), entropy = r.entropy();
-    const PolicyTerm term(P, row, w, logprob, entropy);
+    const PolicyTerm term(P, inputs, logprob, entropy);
     const Slope slope(r, x_token, tau, c, term.g, term.h);
     if (lane == 0) {
       factors[0] = r.m;
@@ -488,12 +570,19 @@ __global__ void __launch_bounds__(kNT, 4) policy_kernel(const Grad P, const int 
   const Slope slope(factors[1], factors[2], factors[3]);
   const int v0 = x.head + g0 * G, v1 = x.head + g1 * G;  // this CTA's vectors
   const bool inside = t >= v0 && t < v1;
-  if (o.head == x.head && slope.tame()) {
-    const f32x2 nm2 = pack2(-m, -m), c2 = pack2(c, c), a2 = pack2(slope.a, slope.a), b2 = pack2(slope.b, slope.b);
-#pragma unroll 2
-    for (int i = 0; i < count; ++i) mine[i * kNT] = slope_vec<kBF16>(mine[i * kNT], nm2, c2, a2, b2);
-    if (inside && (static_cast<int>(t) - v0) / G % kNT == static_cast<int>(threadIdx.x))  // behind the vector, by the same thread
-      put_elem<kBF16>(smem, t - v0, slope.token);
+  const SlopeVec<kBF16> vec(slope, m, c);
+  if (o.head == x.head && vec.usable) {
+    if (vec.flat) {
+#pragma unroll 4
+      for (int i = 0; i < count; ++i) mine[i * kNT] = vec.template of<true>(mine[i * kNT]);
+    } else if (__all_sync(0xffffffffu, (bottom - m) * c >= kFloor)) {
+#pragma unroll 4
+      for (int i = 0; i < count; ++i) mine[i * kNT] = vec.template of<false, true>(mine[i * kNT]);
+    } else {
+      for (int i = 0; i < count; ++i) mine[i * kNT] = vec.template of<false>(mine[i * kNT]);
+    }
+    if (inside && (static_cast<int>(t) - v0) / G % kNT == static_cast<int>(threadIdx.x))
+      put_elem<kBF16>(smem, t - v0, slope.token);  // behind the vector, by the same thread
     publish_to_copies();
     __syncthreads();
     if (threadIdx.x == 0 && g1 > g0) copy_out(const_cast<uint4*>(o.vec) + g0, smem, static_cast<uint32_t>(g1 - g0) * 16u);
@@ -504,7 +593,7 @@ __global__ void __launch_bounds__(kNT, 4) policy_kernel(const Grad P, const int 
       put_elem<kBF16>(obase, v, v == t ? slope.token : slope.at(y, m, c));
     }
   }
-  if (has_loose) put_elem<kBF16>(obase, loose_v, loose_v == t ? slope.token : slope.at(loose_x, m, c));
+  if (has_loose) put_elem<kBF16>(obase, loose_v, loose_v == t ? slope.token : slope.at(x.at(loose_v), m, c));
   if (late) copy_landed(&landed);  // one more wait before the block leaves
 }
 

@@ -72,24 +72,31 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 constexpr float kFloor = -1024.0f;
 __device__ __forceinline__ float exponent(float x, float ref, float c) { return max_nan((x - ref) * c, kFloor); }
 
-// S = sum 2^z and W = sum 2^z z over elements with z = (x - ref) c <= 0.
+// S = sum 2^z and W = sum 2^z z over elements with z = (x - ref) c <= 0.  The difference comes first, so that
+// equal logits have equal exponents and small ones their own precision (a multiply-add of x would leave the
+// rounding of ref c in them).  (Clamping bf16 logits two at a time instead of exponents: 2% slower.)
+// kFree: no exponent is below kFloor.
 template <bool kBF16>
 struct Moments {
   f32x2 s[2] = {0ull, 0ull}, w[2] = {0ull, 0ull};
+  template <bool kFree = false>
   __device__ __forceinline__ void add(const uint4& v, f32x2 nref2, f32x2 c2) {
 #pragma unroll
     for (int i = 0; i < (kBF16 ? 4 : 2); ++i) {
       float a, b;
       unpack2(mul2(add2(pair_of<kBF16>(v, i), nref2), c2), a, b);
-      a = max_nan(a, kFloor);
-      b = max_nan(b, kFloor);
+      if (!kFree) {
+        a = max_nan(a, kFloor);
+        b = max_nan(b, kFloor);
+      }
       const f32x2 e = pack2(ex2(a), ex2(b));
       s[i & 1] = add2(s[i & 1], e);
       w[i & 1] = fma2(e, pack2(a, b), w[i & 1]);
     }
   }
-  // The reference moves up by delta exponents, 2^-delta = f.
-  __device__ __forceinline__ void shift(float delta, float f) {
+  // The reference moves up by delta exponents.
+  __device__ __forceinline__ void shift(float delta) {
+    const float f = ex2(-delta);
     const f32x2 nd = pack2(-delta, -delta), f2 = pack2(f, f);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -108,6 +115,27 @@ struct Moments {
     return a + b;
   }
 };
+
+// The larger, or the smaller, of two vectors element by element (NaN ignored).
+template <bool kBF16, bool kMin = false>
+__device__ __forceinline__ uint4 vec_extreme(const uint4& v, const uint4& w) {
+  auto of = [](uint32_t a, uint32_t b) -> uint32_t {
+    if (kBF16) {
+      const __nv_bfloat162 x = reinterpret_cast<const __nv_bfloat162&>(a), y = reinterpret_cast<const __nv_bfloat162&>(b);
+      const __nv_bfloat162 m = kMin ? __hmin2(x, y) : __hmax2(x, y);
+      return reinterpret_cast<const uint32_t&>(m);
+    }
+    const float x = __uint_as_float(a), y = __uint_as_float(b);
+    return __float_as_uint(kMin ? fminf(x, y) : fmaxf(x, y));
+  };
+  return make_uint4(of(v.x, w.x), of(v.y, w.y), of(v.z, w.z), of(v.w, w.w));
+}
+// The smallest element of a vector (NaN ignored).
+template <bool kBF16>
+__device__ __forceinline__ float vec_min(const uint4& w) {
+  const uint32_t sign = kBF16 ? 0x80008000u : 0x80000000u;
+  return -vec_max<kBF16>(make_uint4(w.x ^ sign, w.y ^ sign, w.z ^ sign, w.w ^ sign));
+}
 
 // Takes the first element equal to m out of a vector.
 template <bool kBF16>
