@@ -567,17 +567,16 @@ def _token_logprobs(logits, tokens, n, temperature, stream, want_stats):
         raise ValueError(f"n must be in 0..min(V, 1024), got {n}")
 
     def call(handle):
-        out = torch.empty((2, N), dtype=torch.float32, device=dev)
+        logprob = torch.empty((N,), dtype=torch.float32, device=dev)
+        entropy = torch.empty((N,), dtype=torch.float32, device=dev)
         rank = torch.empty((N,), dtype=torch.int32, device=dev)
         ids = torch.empty((N, n), dtype=torch.int32, device=dev) if n else None
         logprobs = torch.empty((N, n), dtype=torch.float32, device=dev) if n else None
         stats = torch.empty((3, N), dtype=torch.float32, device=dev) if want_stats else None
-        at = out.data_ptr()
-        st = lib.kps_token_logprobs(*args, n, *scale, at, at + 4 * N, rank.data_ptr(), _addr(ids), _addr(logprobs),
-                                    _addr(stats), handle)
+        st = lib.kps_token_logprobs(*args, n, *scale, logprob.data_ptr(), entropy.data_ptr(), rank.data_ptr(), _addr(ids),
+                                    _addr(logprobs), _addr(stats), handle)
         if st != 0:
             raise KpsError(st, "kps_token_logprobs")
-        logprob, entropy = out.unbind(0)
         return TokenLogprobs(logprob, entropy, rank, ids, logprobs), stats
 
     return _queue(dev, stream, (logits, tokens, _tensor(temperature)), call)
@@ -616,6 +615,17 @@ def token_logprobs_backward(grad_logprob: Optional[torch.Tensor], grad_entropy: 
     return _queue(dev, stream, (logits, tokens, _tensor(temperature), grad_logprob, grad_entropy, stats), call)
 
 
+def _token_logprobs_grad(ctx, grad_logprob, grad_entropy, *_):
+    logits, tokens, stats, temperatures = ctx.saved_tensors
+    g = None if grad_logprob is None else grad_logprob.contiguous()
+    h = None if grad_entropy is None else grad_entropy.contiguous()
+    temperature = ctx.temperature if temperatures is None else temperatures
+    return token_logprobs_backward(g, h, logits, tokens, stats, temperature=temperature), None, None, None
+
+
+_token_logprobs_grad_once = torch.autograd.function.once_differentiable(_token_logprobs_grad)
+
+
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens, n, temperature):
@@ -623,16 +633,16 @@ class _TokenLogprobs(torch.autograd.Function):
         ctx.save_for_backward(logits, tokens, stats, _tensor(temperature))
         ctx.temperature = None if isinstance(temperature, torch.Tensor) else temperature
         ctx.set_materialize_grads(False)
-        ctx.mark_non_differentiable(*(t for t in out[2:] if t is not None))
+        if n:
+            ctx.mark_non_differentiable(out.rank, out.ids, out.logprobs)
+        else:
+            ctx.mark_non_differentiable(out.rank)
         return tuple(out)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, grad_logprob, grad_entropy, *_):
-        logits, tokens, stats, temperatures = ctx.saved_tensors
-        g, h = (None if t is None else t.contiguous() for t in (grad_logprob, grad_entropy))
-        temperature = ctx.temperature if temperatures is None else temperatures
-        return token_logprobs_backward(g, h, logits, tokens, stats, temperature=temperature), None, None, None
+    def backward(ctx, *grads):
+        # (the wrapper that refuses second derivatives costs microseconds: only where they could be asked for)
+        return (_token_logprobs_grad_once if torch.is_grad_enabled() else _token_logprobs_grad)(ctx, *grads)
 
 
 def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, n: int = 0, *,
@@ -690,15 +700,15 @@ def policy_loss_grad(logits: torch.Tensor, tokens: torch.Tensor, old_logprob: to
         raise ValueError("kl_coef needs ref_logprob")
 
     def call(handle):
-        out = torch.empty((3, N), dtype=torch.float32, device=dev)
+        loss = torch.empty((N,), dtype=torch.float32, device=dev)
+        logprob = torch.empty((N,), dtype=torch.float32, device=dev)
+        entropy = torch.empty((N,), dtype=torch.float32, device=dev)
         grad = _grad_like(logits)
-        at = out.data_ptr()
         st = lib.kps_policy_loss_grad(*args, *scale, old_logprob.data_ptr(), advantage.data_ptr(), _addr(ref_logprob),
-                                      _addr(weight), clip[0], clip[1], kl_coef, entropy_coef, at, at + 4 * N, at + 8 * N,
-                                      grad.data_ptr(), grad.stride(0), handle)
+                                      _addr(weight), clip[0], clip[1], kl_coef, entropy_coef, loss.data_ptr(),
+                                      logprob.data_ptr(), entropy.data_ptr(), grad.data_ptr(), grad.stride(0), handle)
         if st != 0:
             raise KpsError(st, "kps_policy_loss_grad")
-        loss, logprob, entropy = out.unbind(0)
         return PolicyLoss(loss, grad, logprob, entropy)
 
     return _queue(dev, stream, (logits, tokens, _tensor(temperature), old_logprob, advantage, ref_logprob, weight), call)

@@ -15,6 +15,7 @@
 #include "kps.h"
 #include "kps_host.h"
 #include "kps_score.cuh"
+#include "kps_select.cuh"
 
 #include <cooperative_groups.h>
 
@@ -28,43 +29,185 @@ namespace cg = cooperative_groups;
 namespace kps {
 namespace score {
 
-constexpr int kNT = 256;  // threads per CTA
-constexpr int kNW = kNT / 32;
-constexpr int kMaxCS = 8;     // widest cluster (the portable limit)
+using namespace select;
 
-__device__ __forceinline__ uint32_t order_key(float x) {
-  const uint32_t u = __float_as_uint(x);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float order_value(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
-}
+constexpr int kMaxCS = 8;  // widest cluster (the portable limit)
+
 // The warp's largest value (NaN as -inf).
-__device__ __forceinline__ float warp_top(float x) {
-  return order_value(__reduce_max_sync(0xffffffffu, order_key(no_nan(x) + 0.0f)));
-}
+__device__ __forceinline__ float warp_top(float x) { return kfloat(__reduce_max_sync(0xffffffffu, fkey(no_nan(x) + 0.0f))); }
 
 // ------------------------------------------------------------------------------------------
-// Scoring without alternatives: one pass
+// Scoring with none or few alternatives: one pass
 // ------------------------------------------------------------------------------------------
 //
 // A warp's sums are against the largest logit that it has seen, looked for once in a round of loads:
 // it rises some three times in a row's dozen rounds.  The element that holds it stays out of the sums
 // until a larger one takes its place.
 //
-// 4096 rows of 151936 bf16, a quarter of them empty: 147 us (140 at the copy rate) with five loads in flight
-// and five CTAs an SM; six and four 153, four and five 151, eight and four 153, eight and three 165; four and
-// six 147, but 16.4 instead of 15.0 us for 333 rows of 50001 fp32, whose CTAs are few.  Rounds that all look
-// where the row ends took 160 with six and four.
+// Alternatives, up to 32 of them: each thread keeps the round of its vectors that holds its largest value, in
+// shared memory, and the largest value of its other rounds.  The n-th largest of the four largest of each of the
+// block's eight warps bounds the n-th largest of its part of the row from below, and what reaches it lies in the kept
+// rounds, or (the other value reaches it too: a thread in some rows) in vectors that are read once more: little
+// more than n elements, ranked pairwise.
+//
+// 4096 rows of 151936 bf16, a quarter of them empty, without alternatives: 147 us (140 at the copy rate) with
+// five loads in flight and five CTAs an SM; six and four 153, four and five 151, eight and four 153, eight and
+// three 165; four and six 147, but 16.4 instead of 15.0 us for 333 rows of 50001 fp32, whose CTAs are few.
+// Rounds that all look where the row ends took 160 with six and four.
+constexpr int kU = 5;        // 16-byte loads each thread keeps in flight
+constexpr int kFew = 32;     // alternatives
+constexpr int kWords = 512;  // elements that are ranked
+template <bool kList>
+struct Few {
+  unsigned long long words[kWords + kFew];
+  unsigned long long lists[kMaxCS][kFew];  // rank 0's: what each CTA found
+  unsigned long long best[kFew];
+  uint32_t sizes[kMaxCS];                  // and how many; ~0: more than there is room for
+  uint32_t tops[kFew];                     // the keys of four threads' largest values of each warp
+  uint4 kept[kU][kNT];                     // each thread's round of vectors
+  int32_t at[kNT];                         // and its first vector
+  uint16_t who[2][kNT];                    // the threads whose kept vectors count, and those whose all are read again
+  uint32_t n_who[2], ties[kNW];
+  uint32_t hist[256], bin, above, inside, n_words;  // for the exact selection
+  uint32_t* offset;                                 // (not asked for)
+};
+template <>
+struct Few<false> {};
+
+// The warp's keys in descending order.
+__device__ __forceinline__ uint32_t sort_warp(uint32_t k) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1) {
+#pragma unroll
+    for (int j = size >> 1; j > 0; j >>= 1) {
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, k, j);
+      k = ((lane & size) == 0) == ((lane & j) == 0) ? max(k, o) : min(k, o);
+    }
+  }
+  return k;
+}
+
+// Elements [v0, v1) of a row whose key is k, the first `want` of them in the order of their indexes, to the
+// block's words.
 template <bool kBF16>
+__device__ __noinline__ void first_equal(const RowView<kBF16>& x, int v0, int v1, uint32_t k, uint32_t want, Few<true>& sm) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int base = v0; base < v1 && want > 0; base += kNT) {
+    const int v = base + static_cast<int>(threadIdx.x);
+    const bool is = v < v1 && fkey(clean(x.at(v))) == k;
+    const unsigned who = __ballot_sync(0xffffffffu, is);
+    __syncthreads();
+    if (lane == 0) sm.ties[warp] = __popc(who);
+    __syncthreads();
+    uint32_t before = 0, all = 0;
+    for (int i = 0; i < kNW; ++i) {
+      before += i < warp ? sm.ties[i] : 0u;
+      all += sm.ties[i];
+    }
+    before += __popc(who & ((1u << lane) - 1u));
+    if (is && before < want) sm.words[atomicAdd(&sm.n_words, 1u)] = word_of(k, v);
+    want -= min(want, all);
+  }
+}
+
+// The first n of the block's part of a row, in any order and with others perhaps, to words: vectors [g0, g1),
+// of which the thread's largest element is `most`, in its round that starts at vector `at`, and the largest of its
+// other rounds `next`; and `loose`, its element outside the vectors (index loose_v; -inf: none).  [v0, v1) is all
+// of the part.  False where there is no room for them.  Ends with a barrier.
+template <bool kBF16>
+__device__ __forceinline__ bool gather_words(const RowView<kBF16>& x, int g0, int g1, int v0, int v1, float most, int at, float next,
+                                             float loose, int loose_v, int n, Few<true>& sm) {
+  constexpr int G = kBF16 ? 8 : 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  static_assert(kFew == 4 * kNW);
+  const uint32_t mine = fkey(most + 0.0f);
+  {
+    uint32_t k = mine;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t top = __reduce_max_sync(0xffffffffu, k);
+      if (lane == 0) sm.tops[4 * warp + i] = top;
+      if (lane == __ffs(__ballot_sync(0xffffffffu, k == top)) - 1) k = 0u;
+    }
+  }
+  if (threadIdx.x == 0) sm.n_words = sm.n_who[0] = sm.n_who[1] = 0u;
+  __syncthreads();
+  const uint32_t bound = __shfl_sync(0xffffffffu, sort_warp(sm.tops[lane]), n - 1);
+  auto collect = [&](uint32_t from) {
+    auto take = [&](const uint4& v, int g) {
+      if (fkey(no_nan(vec_max<kBF16>(v)) + 0.0f) < from) return;
+#pragma unroll
+      for (int e = 0; e < G; ++e) {
+        const uint32_t k = fkey(clean(elem<kBF16>(v, e)));
+        if (k < from) continue;
+        const uint32_t pos = atomicAdd(&sm.n_words, 1u);
+        if (pos < static_cast<uint32_t>(kWords)) sm.words[pos] = word_of(k, x.head + g * G + e);
+      }
+    };
+    if (mine >= from) {
+      const int which = fkey(next + 0.0f) >= from ? 1 : 0;
+      sm.who[which][atomicAdd(&sm.n_who[which], 1u)] = static_cast<uint16_t>(threadIdx.x);
+      sm.at[threadIdx.x] = at;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < static_cast<int>(sm.n_who[0]) * kU; i += kNT) {
+      const int who = sm.who[0][i / kU], u = i % kU;
+      take(sm.kept[u][who], sm.at[who] + u * kNT + who);
+    }
+    const int rounds = (g1 - g0 + kNT - 1) / kNT, items = static_cast<int>(sm.n_who[1]) * rounds;
+    const float each = 1.0f / static_cast<float>(rounds);  // (i + 1/2 over rounds: whole parts are right below 2^22)
+    for (int i = threadIdx.x; i < items; i += kNT) {
+      const int h = static_cast<int>((static_cast<float>(i) + 0.5f) * each), g = g0 + (i - h * rounds) * kNT + sm.who[1][h];
+      if (g < g1) take(x.vec[g], g);
+    }
+    const uint32_t k = fkey(clean(loose));
+    if (k >= from) {
+      const uint32_t pos = atomicAdd(&sm.n_words, 1u);
+      if (pos < static_cast<uint32_t>(kWords)) sm.words[pos] = word_of(k, loose_v);
+    }
+    __syncthreads();
+  };
+  // (of a bound of -inf: everything above; what else is needed is found below)
+  uint32_t tie = kKeyNegInf;
+  collect(max(bound, kKeyNegInf + 1u));
+  if (sm.n_words > static_cast<uint32_t>(kWords) && bound > kKeyNegInf) {
+    // many elements that equal the bound: only larger ones
+    __syncthreads();
+    if (threadIdx.x == 0) sm.n_words = sm.n_who[0] = sm.n_who[1] = 0u;
+    __syncthreads();
+    tie = bound;
+    collect(bound + 1u);
+  }
+  const uint32_t have = sm.n_words;
+  if (have > static_cast<uint32_t>(kWords)) return false;
+  if (have < static_cast<uint32_t>(n)) first_equal<kBF16>(x, v0, v1, tie, static_cast<uint32_t>(n) - have, sm);
+  __syncthreads();
+  return true;
+}
+
+// The first n of count words in their order, to out (distinct; by the whole block).
+__device__ __forceinline__ void rank_words(const unsigned long long* words, int count, int n, unsigned long long* out) {
+  for (int i = threadIdx.x; i < count; i += kNT) {
+    const unsigned long long w = words[i];
+    int r = 0;
+#pragma unroll 4
+    for (int j = 0; j < count; ++j) r += words[j] > w ? 1 : 0;
+    if (r < n) out[r] = w;
+  }
+}
+
+template <bool kBF16, bool kList>
 __global__ void __launch_bounds__(kNT, 5) score_kernel(const Args A) {
-  constexpr int kU = 5;  // 16-byte loads each thread keeps in flight
-  __shared__ Part part[kMaxCS * kNW];  // of the cluster's warps (rank 0's are used)
+  constexpr int G = kBF16 ? 8 : 4;
+  __shared__ Part part[kMaxCS * kNW];       // of the cluster's warps (rank 0's are used)
+  __shared__ Few<kList> sm;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   cg::cluster_group cl = cg::this_cluster();
   const int CS = static_cast<int>(cl.num_blocks());
   const int rank = static_cast<int>(cl.block_rank());
   const int64_t row = blockIdx.x / CS;
+  const int n = A.n;
   // every CTA of the cluster runs before any writes into another's shared memory
   if (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   const RowView<kBF16> x(A.x, row * A.ld, A.V);
@@ -99,6 +242,13 @@ __global__ void __launch_bounds__(kNT, 5) score_kernel(const Args A) {
     top = to;
     nref2 = pack2(-to, -to);
   };
+  // the elements outside the vectors, by one warp: the head with rank 0, the tail with the last rank
+  const bool in = warp == 0 && lane < x.loose() && ((x.loose_at(lane) < x.head) ? rank == 0 : rank == CS - 1);
+  float loose = in ? x.at(x.loose_at(lane)) : -INFINITY;
+  const float outside = loose;
+
+  float thread_top = -INFINITY, thread_next = -INFINITY;  // of this thread's rounds, and of all but that one
+  int top_at = g0;
   // a round of loads; only the last one has to look where the CTA's part ends
   auto round = [&](int base, auto full) {
     constexpr bool kFull = decltype(full)::value;
@@ -114,6 +264,15 @@ __global__ void __launch_bounds__(kNT, 5) score_kernel(const Args A) {
       m[u] = vec_max<kBF16>(w[u]);
       most = fmaxf(most, m[u]);
       if (m[u] > token) above += count_above<kBF16>(w[u], token);
+    }
+    if constexpr (kList) {
+      thread_next = fmaxf(thread_next, fminf(thread_top, most));
+      if (most > thread_top) {
+        thread_top = most;
+        top_at = base;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) sm.kept[u][threadIdx.x] = w[u];
+      }
     }
     if (__any_sync(0xffffffffu, most > top)) {
       const float to = warp_top(most);
@@ -137,17 +296,15 @@ __global__ void __launch_bounds__(kNT, 5) score_kernel(const Args A) {
   for (; base + kNT * kU <= g1; base += kNT * kU) round(base, std::true_type{});
   if (base < g1) round(base, std::false_type{});
   float extra = 0.0f, extra_w = 0.0f;
-  if (warp == 0) {  // the elements outside the vectors: the head with rank 0, the tail with the last rank
-    const bool in = lane < x.loose() && ((x.loose_at(lane) < x.head) ? rank == 0 : rank == CS - 1);
-    float y = in ? x.at(x.loose_at(lane)) : -INFINITY;
-    if (y > token) above += 1.0f;
-    if (__any_sync(0xffffffffu, y > top)) {
-      const float to = warp_top(y);
+  if (warp == 0) {
+    if (loose > token) above += 1.0f;
+    if (__any_sync(0xffffffffu, loose > top)) {
+      const float to = warp_top(loose);
       raise(to);
-      const unsigned who = __ballot_sync(0xffffffffu, y == to);
-      if (lane == __ffs(who) - 1) y = -INFINITY;
+      const unsigned who = __ballot_sync(0xffffffffu, loose == to);
+      if (lane == __ffs(who) - 1) loose = -INFINITY;
     }
-    const float z = exponent(y, top == -INFINITY ? 0.0f : top, c);
+    const float z = exponent(loose, top == -INFINITY ? 0.0f : top, c);
     extra = ex2(z);
     extra_w = extra * z;
   }
@@ -156,10 +313,38 @@ __global__ void __launch_bounds__(kNT, 5) score_kernel(const Args A) {
   Part* to = CS > 1 ? cl.map_shared_rank(&part[0], 0) : part;
   if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (lane == 0) to[rank * kNW + warp] = Part{top, s, moment, above};
+  if constexpr (kList) {
+    const int v0 = rank == 0 ? 0 : x.head + g0 * G, v1 = rank == CS - 1 ? A.V : x.head + g1 * G;
+    const bool whole = gather_words<kBF16>(x, g0, g1, v0, v1, thread_top, top_at, thread_next, outside, x.loose_at(lane), n, sm);
+    unsigned long long* best = CS > 1 ? cl.map_shared_rank(&sm.lists[0][0], 0) + rank * kFew : sm.best;
+    if (whole) rank_words(sm.words, static_cast<int>(sm.n_words), n, best);
+    if (threadIdx.x == 0)
+      *(CS > 1 ? cl.map_shared_rank(&sm.sizes[0], 0) + rank : &sm.sizes[0]) = whole ? min(sm.n_words, static_cast<uint32_t>(n)) : ~0u;
+  }
   if (CS > 1) {
     cl.sync();
     if (rank != 0) return;
   } else {
+    __syncthreads();
+  }
+  if constexpr (kList) {
+    bool whole = true;
+    for (int i = 0; i < CS; ++i) whole = whole && sm.sizes[i] != ~0u;
+    if (!whole) {
+      exact_select<kBF16>(x, n, 0u, c, sm);  // (its sum is not needed)
+      __syncthreads();
+      rank_words(sm.words, n, n, sm.best);
+    } else if (CS > 1) {
+      // the CTAs' lists one behind the other
+      int at = 0;
+      for (int i = 0; i < CS; ++i) {
+        const int size = static_cast<int>(sm.sizes[i]);
+        if (static_cast<int>(threadIdx.x) < size) sm.words[at + threadIdx.x] = sm.lists[i][threadIdx.x];
+        at += size;
+      }
+      __syncthreads();
+      rank_words(sm.words, at, n, sm.best);
+    }
     __syncthreads();
   }
   if (warp != 0) return;
@@ -176,6 +361,12 @@ __global__ void __launch_bounds__(kNT, 5) score_kernel(const Args A) {
   const Row r(m, warp_sum(s0 + s1), warp_sum(m0 + m1));
   above = warp_sum(p0.above + p1.above);
   if (lane == 0) put_row(A, row, r, token, tau, above);
+  if constexpr (kList) {
+    if (lane < n) {
+      A.ids[row * n + lane] = word_index(sm.best[lane]);
+      A.logprobs[row * n + lane] = r.logprob(word_value(sm.best[lane]), tau);
+    }
+  }
 }
 
 // ------------------------------------------------------------------------------------------
@@ -327,7 +518,7 @@ struct SlopeVec {
 // and four CTAs an SM; four and four 142, five and five 145; of 333 rows of 50001 fp32 23.6, 26.0 and 24.6.
 template <bool kBF16, bool kPolicy>
 __global__ void __launch_bounds__(kNT, 4) slope_kernel(const Grad P) {
-  constexpr int kU = 6;  // 16-byte loads each thread keeps in flight
+  constexpr int kU = 6;  // loads in flight
   constexpr int G = kBF16 ? 8 : 4;
   const Args& A = P.a;
   cg::cluster_group cl = cg::this_cluster();
@@ -484,11 +675,11 @@ __global__ void __launch_bounds__(kNT, 5) policy_kernel(const Grad P, const int 
   }
   const float bottom = vec_min<kBF16>(least);
   const float own = vec_max<kBF16>(best), most = fmaxf(no_nan(loose_x), no_nan(own));
-  const uint32_t key = order_key(most + 0.0f), warp_key = __reduce_max_sync(0xffffffffu, key);
+  const uint32_t key = fkey(most + 0.0f), warp_key = __reduce_max_sync(0xffffffffu, key);
   if (lane == 0) keys[warp] = warp_key;
   __syncthreads();
   const uint32_t other = keys[lane & (kNW - 1)], top_key = __reduce_max_sync(0xffffffffu, other);
-  const float top = order_value(top_key);
+  const float top = kfloat(top_key);
   const bool here = warp == __ffs(__ballot_sync(0xffffffffu, other == top_key)) - 1;
   const bool holds = here && lane == __ffs(__ballot_sync(0xffffffffu, key == top_key)) - 1;
 
@@ -625,23 +816,26 @@ static kps_status launch_clusters(void (*kernel)(Params...), int64_t N, int cs, 
   (void)cudaGetLastError();
   return KPS_ERR_CUDA;
 }
-// A streaming kernel: one CTA a row, or for few rows up to kMaxCS while every thread keeps four vectors.
+// A streaming kernel: one CTA a row, or for few rows up to kMaxCS while there are no more than `fill` an SM and
+// every thread keeps four vectors.  Four an SM without alternatives (256 rows of 151936 bf16: 21.6 us, 23.9 with two
+// an SM), two with them (27.8 and 25.8: a row's parts each rank their own).
 template <class P>
-static kps_status launch_rows(void (*kernel)(P), const Args& a, kps_dtype dt, const P& params, cudaStream_t stream) {
+static kps_status launch_rows(void (*kernel)(P), const Args& a, kps_dtype dt, int fill, const P& params, cudaStream_t stream) {
   const int sms = sm_count();
   if (!sms) return KPS_ERR_CUDA;
   int cs = 1;
   const int64_t round = static_cast<int64_t>(kNT) * 4 * (dt == KPS_BF16 ? 8 : 4);
-  while (cs < kMaxCS && a.N * cs * 2 <= 2 * sms && a.V >= 2 * cs * round) cs *= 2;
+    while (cs < kMaxCS && a.N * cs * 2 <= fill * sms && a.V >= 2 * cs * round) cs *= 2;
   return launch_clusters(kernel, a.N, cs, 0, stream, params);
 }
 static kps_status launch_score(const Args& a, kps_dtype dt, cudaStream_t stream) {
-  if (a.n > 0) return launch_alternatives(a, dt, stream);
-  return launch_rows<Args>(dt == KPS_BF16 ? score_kernel<true> : score_kernel<false>, a, dt, a, stream);
+  if (a.n > kFew) return launch_alternatives(a, dt, stream);
+  if (a.n > 0) return launch_rows<Args>(dt == KPS_BF16 ? score_kernel<true, true> : score_kernel<false, true>, a, dt, 2, a, stream);
+  return launch_rows<Args>(dt == KPS_BF16 ? score_kernel<true, false> : score_kernel<false, false>, a, dt, 4, a, stream);
 }
 template <bool kPolicy>
 static kps_status launch_slope(const Grad& P, kps_dtype dt, cudaStream_t stream) {
-  return launch_rows<Grad>(dt == KPS_BF16 ? slope_kernel<true, kPolicy> : slope_kernel<false, kPolicy>, P.a, dt, P, stream);
+  return launch_rows<Grad>(dt == KPS_BF16 ? slope_kernel<true, kPolicy> : slope_kernel<false, kPolicy>, P.a, dt, 4, P, stream);
 }
 
 // The policy loss: with the row in shared memory where a cluster's holds it (up to 1.8 MB); longer rows

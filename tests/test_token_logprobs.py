@@ -235,6 +235,40 @@ def test_hard_rows(n, V, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [1, 5, 20, 31, 32, 33])
+@pytest.mark.parametrize("copies,V", [(1, 1000), (1, 50003), (1, 151936), (40, 20011)])
+def test_alternatives_of_rows_that_bounds_misjudge(n, copies, V, dtype):
+    """Vocabularies in order, plateaus that begin late, masks with fewer tokens than alternatives, the largest
+    logits in few of a warp's lanes."""
+    low = torch.finfo(dtype).min
+    x, _ = make(12, V, dtype, seed=V + n)
+    at = torch.randperm(V, device="cuda", generator=torch.Generator("cuda").manual_seed(n))
+    i = torch.arange(V, device="cuda")
+    x[0] = (i * (60.0 / V)).to(dtype)
+    x[1] = (-i * (60.0 / V)).to(dtype)
+    x[2] = 0.0
+    x[2, V // 2:] = 1.0
+    x[3] = -math.inf
+    x[3, at[:7]] = x[4, at[:7]]
+    x[4] = low
+    x[4, at[:7]] = x[5, at[:7]]
+    x[5] = -math.inf
+    x[5, at[:300]] = x[6, at[:300]]
+    x[6] = low
+    x[6, at[:300]] = x[7, at[:300]]
+    x[7] = torch.where(i // (8 if dtype == torch.bfloat16 else 4) % 32 < 3, 30.0 + x[7].float(), x[7].float()).to(dtype)
+    x[8, at[:3]] = math.nan
+    x[9] = (i % 977).to(dtype)  # values in cycles, each many times
+    x[10] = -math.inf
+    x[10, at[0]] = 3.0
+    x[11, V // 3:] += 20.0
+    x = x.repeat(copies, 1)
+    tokens = at[:1].expand(len(x)).contiguous()
+    check(x, tokens, n)
+
+
+@gpu
 @pytest.mark.parametrize("n", [0, 3])
 @pytest.mark.parametrize("N", [1, 500])
 def test_hard_rows_of_long_vocabularies(n, N):
