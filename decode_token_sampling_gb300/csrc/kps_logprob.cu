@@ -168,16 +168,18 @@ __device__ __forceinline__ bool gather_words(const RowView<kBF16>& x, int g0, in
     }
     __syncthreads();
   };
-  // (of a bound of -inf: everything above; what else is needed is found below)
-  uint32_t tie = kKeyNegInf;
-  collect(max(bound, kKeyNegInf + 1u));
-  if (sm.n_words > static_cast<uint32_t>(kWords) && bound > kKeyNegInf) {
-    // many elements that equal the bound: only larger ones
+  // (of a bound of -inf: everything above; what else is needed is found below.)  Where many elements equal the
+  // bound, only larger ones.
+  uint32_t tie = kKeyNegInf, from = max(bound, kKeyNegInf + 1u);
+#pragma unroll 1
+  for (int again = 0; again < 2; ++again) {
+    collect(from);
+    if (sm.n_words <= static_cast<uint32_t>(kWords) || bound == kKeyNegInf || again) break;
     __syncthreads();
     if (threadIdx.x == 0) sm.n_words = sm.n_who[0] = sm.n_who[1] = 0u;
     __syncthreads();
     tie = bound;
-    collect(bound + 1u);
+    from = bound + 1u;
   }
   const uint32_t have = sm.n_words;
   if (have > static_cast<uint32_t>(kWords)) return false;
@@ -606,9 +608,10 @@ __global__ void __launch_bounds__(kNT, 4) slope_kernel(const Grad P) {
 //
 // The row is read once, by a bulk copy into the shared memory of each of a cluster's CTAs, summed
 // there against the CTA's largest logit, turned into the gradient in place and copied out.
-// Bytes of a row per CTA, where the cluster allows: five CTAs an SM (48 registers).  4096 rows of 151936
-// bf16 with a quarter empty: 366 us (326 at the copy rate); 52 KB and four CTAs 371, 62 KB and three 427
-// at the time.
+// Bytes of a row per CTA, where the cluster allows: five CTAs an SM (48 registers).  4096 rows of 151936 bf16
+// with a quarter empty take 363 us (326 at the copy rate), 2048 of 128256 179 (157); with 52 KB and four CTAs 371
+// and 184, with 62 KB and three 427 and 224 at the time.  Loops unrolled more than twice cost 2% (instructions
+// are fetched anew by every block), parts copied in and out in two slices 1%, in four 5%.
 constexpr int kChunkBytes = 43 * 1024;
 
 template <bool kBF16>
@@ -618,8 +621,6 @@ __global__ void __launch_bounds__(kNT, 5) policy_kernel(const Grad P, const int 
   __shared__ float sums[kMaxCS * kNW][2];  // S and W of the cluster's warps
   __shared__ float tops[kMaxCS];           // the CTAs' largest logits
   __shared__ uint32_t keys[kNW];
-  __shared__ PolicyRow inputs;
-  __shared__ float x_token;
   __shared__ float factors[4];             // m, a, b and the token's gradient
   __shared__ __align__(8) unsigned long long landed, gathered;  // the barriers of the copy and of sums and tops
   const Args& A = P.a;
@@ -653,10 +654,8 @@ __global__ void __launch_bounds__(kNT, 5) policy_kernel(const Grad P, const int 
   }
   if (threadIdx.x == 0 && g1 > g0) copy_in(smem, x.vec + g0, static_cast<uint32_t>(g1 - g0) * 16u, &landed);
   const float c = kLog2e / row_tau(A.taus, A.tau, row);
-  if (threadIdx.x == 0) {  // what the loss needs, so that nothing waits for it later
-    inputs = PolicyRow(P, row);
-    x_token = x.at(static_cast<int>(t));
-  }
+  const PolicyRow inputs(P, row);
+  const float x_token = x.at(static_cast<int>(t));
   // the elements outside the vectors: the head with rank 0, the tail with the last rank
   const bool has_loose = static_cast<int>(threadIdx.x) < x.loose() &&
                          ((x.loose_at(threadIdx.x) < x.head) ? rank == 0 : rank == CS - 1);
@@ -667,7 +666,7 @@ __global__ void __launch_bounds__(kNT, 5) policy_kernel(const Grad P, const int 
 
   // ---- the CTA's largest logit, and the thread that holds it ---------------------------------------
   uint4 best = neg_inf_vec<kBF16>(), least = make_uint4(0u, 0u, 0u, 0u);  // (no smallest above 0 is needed)
-#pragma unroll 4
+#pragma unroll 2
   for (int i = 0; i < count; ++i) {
     const uint4 v = mine[i * kNT];
     best = vec_extreme<kBF16>(best, v);
@@ -693,8 +692,11 @@ __global__ void __launch_bounds__(kNT, 5) policy_kernel(const Grad P, const int 
       loose_x = -INFINITY;
       skip = false;
     }
-    if (here) {
-#pragma unroll 4
+    if (!here && __all_sync(0xffffffffu, (bottom - ref) * c >= kFloor)) {
+#pragma unroll 2
+      for (int i = 0; i < count; ++i) sum.template add<true>(mine[i * kNT], nref2, c2);
+    } else {
+#pragma unroll 2
       for (int i = 0; i < count; ++i) {
         uint4 v = mine[i * kNT];
         if (skip && vec_max<kBF16>(v) == top) {
@@ -703,11 +705,6 @@ __global__ void __launch_bounds__(kNT, 5) policy_kernel(const Grad P, const int 
         }
         sum.add(v, nref2, c2);
       }
-    } else if (__all_sync(0xffffffffu, (bottom - ref) * c >= kFloor)) {
-#pragma unroll 4
-      for (int i = 0; i < count; ++i) sum.template add<true>(mine[i * kNT], nref2, c2);
-    } else {
-      for (int i = 0; i < count; ++i) sum.add(mine[i * kNT], nref2, c2);
     }
     const float z = exponent(loose_x, ref, c), e = ex2(z);
     float s = warp_sum(e + sum.sum());
@@ -764,10 +761,10 @@ __global__ void __launch_bounds__(kNT, 5) policy_kernel(const Grad P, const int 
   const SlopeVec<kBF16> vec(slope, m, c);
   if (o.head == x.head && vec.usable) {
     if (vec.flat) {
-#pragma unroll 4
+#pragma unroll 2
       for (int i = 0; i < count; ++i) mine[i * kNT] = vec.template of<true>(mine[i * kNT]);
     } else if (__all_sync(0xffffffffu, (bottom - m) * c >= kFloor)) {
-#pragma unroll 4
+#pragma unroll 2
       for (int i = 0; i < count; ++i) mine[i * kNT] = vec.template of<false, true>(mine[i * kNT]);
     } else {
       for (int i = 0; i < count; ++i) mine[i * kNT] = vec.template of<false>(mine[i * kNT]);
@@ -817,8 +814,8 @@ static kps_status launch_clusters(void (*kernel)(Params...), int64_t N, int cs, 
   return KPS_ERR_CUDA;
 }
 // A streaming kernel: one CTA a row, or for few rows up to kMaxCS while there are no more than `fill` an SM and
-// every thread keeps four vectors.  Four an SM without alternatives (256 rows of 151936 bf16: 21.6 us, 23.9 with two
-// an SM), two with them (27.8 and 25.8: a row's parts each rank their own).
+// every thread keeps four vectors.  Five an SM without alternatives (256 rows of 151936 bf16: 21.6 us, 23.9 with two
+// an SM; 333 of 50001 fp32 13.7 and 15.1, their gradient 23.0 and 23.7), two with them (27.8 and 25.8: a row's parts each rank their own).
 template <class P>
 static kps_status launch_rows(void (*kernel)(P), const Args& a, kps_dtype dt, int fill, const P& params, cudaStream_t stream) {
   const int sms = sm_count();
@@ -831,11 +828,11 @@ static kps_status launch_rows(void (*kernel)(P), const Args& a, kps_dtype dt, in
 static kps_status launch_score(const Args& a, kps_dtype dt, cudaStream_t stream) {
   if (a.n > kFew) return launch_alternatives(a, dt, stream);
   if (a.n > 0) return launch_rows<Args>(dt == KPS_BF16 ? score_kernel<true, true> : score_kernel<false, true>, a, dt, 2, a, stream);
-  return launch_rows<Args>(dt == KPS_BF16 ? score_kernel<true, false> : score_kernel<false, false>, a, dt, 4, a, stream);
+  return launch_rows<Args>(dt == KPS_BF16 ? score_kernel<true, false> : score_kernel<false, false>, a, dt, 5, a, stream);
 }
 template <bool kPolicy>
 static kps_status launch_slope(const Grad& P, kps_dtype dt, cudaStream_t stream) {
-  return launch_rows<Grad>(dt == KPS_BF16 ? slope_kernel<true, kPolicy> : slope_kernel<false, kPolicy>, P.a, dt, 4, P, stream);
+  return launch_rows<Grad>(dt == KPS_BF16 ? slope_kernel<true, kPolicy> : slope_kernel<false, kPolicy>, P.a, dt, 5, P, stream);
 }
 
 // The policy loss: with the row in shared memory where a cluster's holds it (up to 1.8 MB); longer rows
