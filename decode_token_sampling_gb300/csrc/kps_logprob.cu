@@ -45,7 +45,7 @@ __device__ __forceinline__ float warp_top(float x) { return kfloat(__reduce_max_
 // until a larger one takes its place.
 //
 // Alternatives, up to 32 of them: each thread keeps the round of its vectors that holds its largest value, in
-// shared memory, and the largest value of its other rounds.  The n-th largest of the four largest of each of the
+// shared memory, and the largest value of its other rounds.  The n-th largest of 32 of them, the largest few of each of the
 // block's eight warps bounds the n-th largest of its part of the row from below, and what reaches it lies in the kept
 // rounds, or (the other value reaches it too: a thread in some rows) in vectors that are read once more: little
 // more than n elements, ranked pairwise.
@@ -57,22 +57,22 @@ __device__ __forceinline__ float warp_top(float x) { return kfloat(__reduce_max_
 constexpr int kU = 5;        // 16-byte loads each thread keeps in flight
 constexpr int kFew = 32;     // alternatives
 constexpr int kWords = 512;  // elements that are ranked
-template <bool kList>
+template <bool kList, int NT>
 struct Few {
   unsigned long long words[kWords + kFew];
   unsigned long long lists[kMaxCS][kFew];  // rank 0's: what each CTA found
   unsigned long long best[kFew];
   uint32_t sizes[kMaxCS];                  // and how many; ~0: more than there is room for
-  uint32_t tops[kFew];                     // the keys of four threads' largest values of each warp
-  uint4 kept[kU][kNT];                     // each thread's round of vectors
-  int32_t at[kNT];                         // and its first vector
-  uint16_t who[2][kNT];                    // the threads whose kept vectors count, and those whose all are read again
-  uint32_t n_who[2], ties[kNW];
+  uint32_t tops[kFew];                     // the keys of some threads' largest values of each warp
+  uint4 kept[kU][NT];                     // each thread's round of vectors
+  int32_t at[NT];                         // and its first vector
+  uint16_t who[2][NT];                    // the threads whose kept vectors count, and those whose all are read again
+  uint32_t n_who[2], ties[NT / 32];
   uint32_t hist[256], bin, above, inside, n_words;  // for the exact selection
   uint32_t* offset;                                 // (not asked for)
 };
-template <>
-struct Few<false> {};
+template <int NT>
+struct Few<false, NT> {};
 
 // The warp's keys in descending order.
 __device__ __forceinline__ uint32_t sort_warp(uint32_t k) {
@@ -90,10 +90,10 @@ __device__ __forceinline__ uint32_t sort_warp(uint32_t k) {
 
 // Elements [v0, v1) of a row whose key is k, the first `want` of them in the order of their indexes, to the
 // block's words.
-template <bool kBF16>
-__device__ __noinline__ void first_equal(const RowView<kBF16>& x, int v0, int v1, uint32_t k, uint32_t want, Few<true>& sm) {
+template <bool kBF16, int NT>
+__device__ __noinline__ void first_equal(const RowView<kBF16>& x, int v0, int v1, uint32_t k, uint32_t want, Few<true, NT>& sm) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int base = v0; base < v1 && want > 0; base += kNT) {
+  for (int base = v0; base < v1 && want > 0; base += NT) {
     const int v = base + static_cast<int>(threadIdx.x);
     const bool is = v < v1 && fkey(clean(x.at(v))) == k;
     const unsigned who = __ballot_sync(0xffffffffu, is);
@@ -101,7 +101,7 @@ __device__ __noinline__ void first_equal(const RowView<kBF16>& x, int v0, int v1
     if (lane == 0) sm.ties[warp] = __popc(who);
     __syncthreads();
     uint32_t before = 0, all = 0;
-    for (int i = 0; i < kNW; ++i) {
+    for (int i = 0; i < NT / 32; ++i) {
       before += i < warp ? sm.ties[i] : 0u;
       all += sm.ties[i];
     }
@@ -115,19 +115,19 @@ __device__ __noinline__ void first_equal(const RowView<kBF16>& x, int v0, int v1
 // of which the thread's largest element is `most`, in its round that starts at vector `at`, and the largest of its
 // other rounds `next`; and `loose`, its element outside the vectors (index loose_v; -inf: none).  [v0, v1) is all
 // of the part.  False where there is no room for them.  Ends with a barrier.
-template <bool kBF16>
+template <bool kBF16, int NT>
 __device__ __forceinline__ bool gather_words(const RowView<kBF16>& x, int g0, int g1, int v0, int v1, float most, int at, float next,
-                                             float loose, int loose_v, int n, Few<true>& sm) {
+                                             float loose, int loose_v, int n, Few<true, NT>& sm) {
   constexpr int G = kBF16 ? 8 : 4;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  static_assert(kFew == 4 * kNW);
+  constexpr int kPer = kFew / (NT / 32);
   const uint32_t mine = fkey(most + 0.0f);
   {
     uint32_t k = mine;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kPer; ++i) {
       const uint32_t top = __reduce_max_sync(0xffffffffu, k);
-      if (lane == 0) sm.tops[4 * warp + i] = top;
+      if (lane == 0) sm.tops[kPer * warp + i] = top;
       if (lane == __ffs(__ballot_sync(0xffffffffu, k == top)) - 1) k = 0u;
     }
   }
@@ -151,14 +151,14 @@ __device__ __forceinline__ bool gather_words(const RowView<kBF16>& x, int g0, in
       sm.at[threadIdx.x] = at;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < static_cast<int>(sm.n_who[0]) * kU; i += kNT) {
+    for (int i = threadIdx.x; i < static_cast<int>(sm.n_who[0]) * kU; i += NT) {
       const int who = sm.who[0][i / kU], u = i % kU;
-      take(sm.kept[u][who], sm.at[who] + u * kNT + who);
+      take(sm.kept[u][who], sm.at[who] + u * NT + who);
     }
-    const int rounds = (g1 - g0 + kNT - 1) / kNT, items = static_cast<int>(sm.n_who[1]) * rounds;
+    const int rounds = (g1 - g0 + NT - 1) / NT, items = static_cast<int>(sm.n_who[1]) * rounds;
     const float each = 1.0f / static_cast<float>(rounds);  // (i + 1/2 over rounds: whole parts are right below 2^22)
-    for (int i = threadIdx.x; i < items; i += kNT) {
-      const int h = static_cast<int>((static_cast<float>(i) + 0.5f) * each), g = g0 + (i - h * rounds) * kNT + sm.who[1][h];
+    for (int i = threadIdx.x; i < items; i += NT) {
+      const int h = static_cast<int>((static_cast<float>(i) + 0.5f) * each), g = g0 + (i - h * rounds) * NT + sm.who[1][h];
       if (g < g1) take(x.vec[g], g);
     }
     const uint32_t k = fkey(clean(loose));
@@ -183,14 +183,15 @@ __device__ __forceinline__ bool gather_words(const RowView<kBF16>& x, int g0, in
   }
   const uint32_t have = sm.n_words;
   if (have > static_cast<uint32_t>(kWords)) return false;
-  if (have < static_cast<uint32_t>(n)) first_equal<kBF16>(x, v0, v1, tie, static_cast<uint32_t>(n) - have, sm);
+  if (have < static_cast<uint32_t>(n)) first_equal<kBF16, NT>(x, v0, v1, tie, static_cast<uint32_t>(n) - have, sm);
   __syncthreads();
   return true;
 }
 
 // The first n of count words in their order, to out (distinct; by the whole block).
+template <int NT>
 __device__ __forceinline__ void rank_words(const unsigned long long* words, int count, int n, unsigned long long* out) {
-  for (int i = threadIdx.x; i < count; i += kNT) {
+  for (int i = threadIdx.x; i < count; i += NT) {
     const unsigned long long w = words[i];
     int r = 0;
 #pragma unroll 4
@@ -199,11 +200,11 @@ __device__ __forceinline__ void rank_words(const unsigned long long* words, int 
   }
 }
 
-template <bool kBF16, bool kList>
-__global__ void __launch_bounds__(kNT, 5) score_kernel(const Args A) {
-  constexpr int G = kBF16 ? 8 : 4;
-  __shared__ Part part[kMaxCS * kNW];       // of the cluster's warps (rank 0's are used)
-  __shared__ Few<kList> sm;
+template <bool kBF16, bool kList, int NT>
+__global__ void __launch_bounds__(NT, 5 * 256 / NT) score_kernel(const Args A) {
+  constexpr int G = kBF16 ? 8 : 4, NW = NT / 32;
+  __shared__ Part part[kMaxCS * NW];       // of the cluster's warps (rank 0's are used)
+  __shared__ Few<kList, NT> sm;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   cg::cluster_group cl = cg::this_cluster();
   const int CS = static_cast<int>(cl.num_blocks());
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kNT, 5) score_kernel(const Args A) {
   const float tau = row_tau(A.taus, A.tau, row);
   if (t < 0 || t >= A.V || (A.weight && A.weight[row] == 0.0f)) {  // an empty row
     if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (rank == 0) put_empty(A, row, kNT);
+    if (rank == 0) put_empty(A, row, NT);
     return;
   }
   const float token = no_nan(x.at(static_cast<int>(t)));
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(kNT, 5) score_kernel(const Args A) {
     uint4 w[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int g = base + u * kNT + static_cast<int>(threadIdx.x);
+      const int g = base + u * NT + static_cast<int>(threadIdx.x);
       w[u] = kFull || g < g1 ? ld_stream(x.vec + g) : neg_inf_vec<kBF16>();
     }
     float m[kU], most = -INFINITY;
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kNT, 5) score_kernel(const Args A) {
   };
   int base = g0;
 #pragma unroll 1
-  for (; base + kNT * kU <= g1; base += kNT * kU) round(base, std::true_type{});
+  for (; base + NT * kU <= g1; base += NT * kU) round(base, std::true_type{});
   if (base < g1) round(base, std::false_type{});
   float extra = 0.0f, extra_w = 0.0f;
   if (warp == 0) {
@@ -314,12 +315,12 @@ __global__ void __launch_bounds__(kNT, 5) score_kernel(const Args A) {
   above = warp_sum(above);
   Part* to = CS > 1 ? cl.map_shared_rank(&part[0], 0) : part;
   if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (lane == 0) to[rank * kNW + warp] = Part{top, s, moment, above};
+  if (lane == 0) to[rank * NW + warp] = Part{top, s, moment, above};
   if constexpr (kList) {
     const int v0 = rank == 0 ? 0 : x.head + g0 * G, v1 = rank == CS - 1 ? A.V : x.head + g1 * G;
-    const bool whole = gather_words<kBF16>(x, g0, g1, v0, v1, thread_top, top_at, thread_next, outside, x.loose_at(lane), n, sm);
+    const bool whole = gather_words<kBF16, NT>(x, g0, g1, v0, v1, thread_top, top_at, thread_next, outside, x.loose_at(lane), n, sm);
     unsigned long long* best = CS > 1 ? cl.map_shared_rank(&sm.lists[0][0], 0) + rank * kFew : sm.best;
-    if (whole) rank_words(sm.words, static_cast<int>(sm.n_words), n, best);
+    if (whole) rank_words<NT>(sm.words, static_cast<int>(sm.n_words), n, best);
     if (threadIdx.x == 0)
       *(CS > 1 ? cl.map_shared_rank(&sm.sizes[0], 0) + rank : &sm.sizes[0]) = whole ? min(sm.n_words, static_cast<uint32_t>(n)) : ~0u;
   }
@@ -333,9 +334,9 @@ __global__ void __launch_bounds__(kNT, 5) score_kernel(const Args A) {
     bool whole = true;
     for (int i = 0; i < CS; ++i) whole = whole && sm.sizes[i] != ~0u;
     if (!whole) {
-      exact_select<kBF16>(x, n, 0u, c, sm);  // (its sum is not needed)
+      exact_select<kBF16, NT>(x, n, 0u, c, sm);  // (its sum is not needed)
       __syncthreads();
-      rank_words(sm.words, n, n, sm.best);
+      rank_words<NT>(sm.words, n, n, sm.best);
     } else if (CS > 1) {
       // the CTAs' lists one behind the other
       int at = 0;
@@ -345,15 +346,15 @@ __global__ void __launch_bounds__(kNT, 5) score_kernel(const Args A) {
         at += size;
       }
       __syncthreads();
-      rank_words(sm.words, at, n, sm.best);
+      rank_words<NT>(sm.words, at, n, sm.best);
     }
     __syncthreads();
   }
   if (warp != 0) return;
   // the parts' sums against the row's largest logit; the first part that holds it keeps it out
-  static_assert(kMaxCS * kNW <= 64);
+  static_assert(kMaxCS * NW <= 64);
   const Part none{-INFINITY, 0.0f, 0.0f, 0.0f};
-  const Part p0 = lane < kNW * CS ? part[lane] : none, p1 = lane + 32 < kNW * CS ? part[lane + 32] : none;
+  const Part p0 = lane < NW * CS ? part[lane] : none, p1 = lane + 32 < NW * CS ? part[lane + 32] : none;
   const float m = warp_top(fmaxf(p0.m, p1.m));
   const unsigned w0 = __ballot_sync(0xffffffffu, p0.m == m), w1 = __ballot_sync(0xffffffffu, p1.m == m);
   const int owner = w0 ? __ffs(w0) - 1 : 32 + __ffs(w1) - 1;
@@ -516,11 +517,12 @@ struct SlopeVec {
   }
 };
 
-// 2048 rows of 128256 bf16, a quarter of them empty: 141 us (138 at the copy rate) with six loads in flight
-// and four CTAs an SM; four and four 142, five and five 145; of 333 rows of 50001 fp32 23.6, 26.0 and 24.6.
+// 2048 rows of 128256 bf16, a quarter of them empty: 134 us (138 at the copy rate) in up to eight CTAs a row, with
+// four loads in flight and six CTAs an SM; six and four 147, three and eight 138, two and eight 136; six and four
+// with one CTA a row 141.  333 rows of 50001 fp32: 21.9 us, and 24.0, 21.9, 22.7, 23.3.
 template <bool kBF16, bool kPolicy>
-__global__ void __launch_bounds__(kNT, 4) slope_kernel(const Grad P) {
-  constexpr int kU = 6;  // loads in flight
+__global__ void __launch_bounds__(kNT, 6) slope_kernel(const Grad P) {
+  constexpr int kU = 4;  // loads in flight
   constexpr int G = kBF16 ? 8 : 4;
   const Args& A = P.a;
   cg::cluster_group cl = cg::this_cluster();
@@ -795,11 +797,11 @@ static int sm_count() {
   return 0;
 }
 // Launches a kernel with a cluster of cs CTAs a row.
-template <class... Params, class... Values>
+template <int NT = kNT, class... Params, class... Values>
 static kps_status launch_clusters(void (*kernel)(Params...), int64_t N, int cs, size_t shared, cudaStream_t stream, const Values&... values) {
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(static_cast<unsigned>(N * cs));
-  lc.blockDim = dim3(kNT);
+  lc.blockDim = dim3(NT);
   lc.dynamicSmemBytes = shared;
   lc.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -813,26 +815,40 @@ static kps_status launch_clusters(void (*kernel)(Params...), int64_t N, int cs, 
   (void)cudaGetLastError();
   return KPS_ERR_CUDA;
 }
-// A streaming kernel: one CTA a row, or for few rows up to kMaxCS while there are no more than `fill` an SM and
-// every thread keeps four vectors.  Five an SM without alternatives (256 rows of 151936 bf16: 21.6 us, 23.9 with two
-// an SM; 333 of 50001 fp32 13.7 and 15.1, their gradient 23.0 and 23.7), two with them (27.8 and 25.8: a row's parts each rank their own).
+// A streaming kernel: one CTA a row, or up to kMaxCS while there are no more than `fill` an SM (0: any number) and every thread keeps
+// four vectors.  Five an SM for scoring without alternatives (256 rows of 151936 bf16: 21.6 us, 23.9 with two an SM;
+// 333 of 50001 fp32 13.7 and 15.1), two with them (27.8 and 25.8: a row's parts each rank their own).  The
+// gradient's CTAs have nothing in common, so there it is as many as there can be.
 template <class P>
-static kps_status launch_rows(void (*kernel)(P), const Args& a, kps_dtype dt, int fill, const P& params, cudaStream_t stream) {
-  const int sms = sm_count();
-  if (!sms) return KPS_ERR_CUDA;
+static kps_status launch_rows(void (*kernel)(P), const Args& a, kps_dtype dt, int fill, int sms, const P& params, cudaStream_t stream) {
   int cs = 1;
   const int64_t round = static_cast<int64_t>(kNT) * 4 * (dt == KPS_BF16 ? 8 : 4);
-    while (cs < kMaxCS && a.N * cs * 2 <= fill * sms && a.V >= 2 * cs * round) cs *= 2;
+    while (cs < kMaxCS && (fill == 0 || a.N * cs * 2 <= static_cast<int64_t>(fill) * sms) && a.V >= 2 * cs * round) cs *= 2;
   return launch_clusters(kernel, a.N, cs, 0, stream, params);
 }
+// Scoring: many short rows go to blocks of 128 threads, twice as many an SM, as a block spends some 3.5 us on
+// its start and its end whatever its row is (8192 rows of 5000 bf16: 27.8 us, 44.5 with 256 threads; with five
+// alternatives 55 and 85; 2048 of 32000 bf16 30.9 and 33.7).  Rows above 64 KB are faster with 256 (2048 of
+// 32000 fp32 with five alternatives 62 and 58.6, of 128256 bf16 125 and 109).
+constexpr int kShortBytes = 64 * 1024, kShortThreads = 128;
 static kps_status launch_score(const Args& a, kps_dtype dt, cudaStream_t stream) {
   if (a.n > kFew) return launch_alternatives(a, dt, stream);
-  if (a.n > 0) return launch_rows<Args>(dt == KPS_BF16 ? score_kernel<true, true> : score_kernel<false, true>, a, dt, 2, a, stream);
-  return launch_rows<Args>(dt == KPS_BF16 ? score_kernel<true, false> : score_kernel<false, false>, a, dt, 5, a, stream);
+  const int sms = sm_count();
+  if (!sms) return KPS_ERR_CUDA;
+  const bool bf16 = dt == KPS_BF16, list = a.n > 0;
+  if (a.N > 2 * sms && static_cast<int64_t>(a.V) * (bf16 ? 2 : 4) <= kShortBytes) {
+    constexpr int NT = kShortThreads;
+    auto* kernel = bf16 ? (list ? score_kernel<true, true, NT> : score_kernel<true, false, NT>)
+                        : (list ? score_kernel<false, true, NT> : score_kernel<false, false, NT>);
+    return launch_clusters<NT>(kernel, a.N, 1, 0, stream, a);
+  }
+  auto* kernel = bf16 ? (list ? score_kernel<true, true, kNT> : score_kernel<true, false, kNT>)
+                      : (list ? score_kernel<false, true, kNT> : score_kernel<false, false, kNT>);
+  return launch_rows<Args>(kernel, a, dt, list ? 2 : 5, sms, a, stream);
 }
 template <bool kPolicy>
 static kps_status launch_slope(const Grad& P, kps_dtype dt, cudaStream_t stream) {
-  return launch_rows<Grad>(dt == KPS_BF16 ? slope_kernel<true, kPolicy> : slope_kernel<false, kPolicy>, P.a, dt, 5, P, stream);
+  return launch_rows<Grad>(dt == KPS_BF16 ? slope_kernel<true, kPolicy> : slope_kernel<false, kPolicy>, P.a, dt, 0, 0, P, stream);
 }
 
 // The policy loss: with the row in shared memory where a cluster's holds it (up to 1.8 MB); longer rows

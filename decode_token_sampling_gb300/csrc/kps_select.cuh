@@ -10,7 +10,7 @@ namespace select {
 
 using namespace stream;
 
-constexpr int kNT = 256;  // threads per CTA
+constexpr int kNT = 256;  // threads per CTA, unless a template says otherwise (NT)
 constexpr int kNW = kNT / 32;
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
 
@@ -87,19 +87,19 @@ __device__ __forceinline__ float elem(const uint4& w, int e) {
 }
 
 // Every element of the row, with the warp converged: f(valid, value, index).
-template <bool kBF16, class F>
+template <bool kBF16, int NT = kNT, class F>
 __device__ __forceinline__ void each_raw(const RowView<kBF16>& x, F&& f) {
   constexpr int G = kBF16 ? 8 : 4, kU = 6;  // loads in flight
-  for (int base = 0; base < x.nv; base += kNT * kU) {
+  for (int base = 0; base < x.nv; base += NT * kU) {
     uint4 w[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int g = base + u * kNT + static_cast<int>(threadIdx.x);
+      const int g = base + u * NT + static_cast<int>(threadIdx.x);
       w[u] = g < x.nv ? ld_stream(x.vec + g) : neg_inf_vec<kBF16>();
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int g = base + u * kNT + static_cast<int>(threadIdx.x);
+      const int g = base + u * NT + static_cast<int>(threadIdx.x);
 #pragma unroll
       for (int e = 0; e < G; ++e) f(g < x.nv, elem<kBF16>(w[u], e), x.head + g * G + e);
     }
@@ -109,16 +109,16 @@ __device__ __forceinline__ void each_raw(const RowView<kBF16>& x, F&& f) {
   f(in, in ? x.at(v) : -INFINITY, v);
 }
 // The same with NaN as -inf.
-template <bool kBF16, class F>
+template <bool kBF16, int NT = kNT, class F>
 __device__ __forceinline__ void each(const RowView<kBF16>& x, F&& f) {
-  each_raw<kBF16>(x, [&](bool valid, float y, int v) { f(valid, clean(y), v); });
+  each_raw<kBF16, NT>(x, [&](bool valid, float y, int v) { f(valid, clean(y), v); });
 }
 
 // The exact selection, by one CTA, for rows whose list came out too short or too long: the n-th
 // element of the order by 8-bit digits of its key and, among equal keys, of its index; then the n
 // elements as survivors and the thread's sum of all others.  At least n elements have a key of
 // floor or more.
-template <bool kBF16, class S>
+template <bool kBF16, int NT = kNT, class S>
 __device__ __noinline__ Sum2 exact_select(const RowView<kBF16>& x, int n, uint32_t floor, float c, S& sm) {
   uint32_t need = static_cast<uint32_t>(n);
   unsigned long long at = 0;  // the digits found so far, from the top of the 64-bit word
@@ -135,9 +135,9 @@ __device__ __noinline__ Sum2 exact_select(const RowView<kBF16>& x, int n, uint32
         at |= 0xFFull << 24;
         continue;
       }
-      for (int i = threadIdx.x; i < 256; i += kNT) sm.hist[i] = 0u;
+      for (int i = threadIdx.x; i < 256; i += NT) sm.hist[i] = 0u;
       __syncthreads();
-      each<kBF16>(x, [&](bool valid, float y, int v) {
+      each<kBF16, NT>(x, [&](bool valid, float y, int v) {
         const unsigned long long w = word_of(fkey(y), v);
         const bool ok = valid && (w >> 32) >= floor && (shift == 56 || (w >> (shift + 8)) == (at >> (shift + 8)));
         const int d = static_cast<int>((w >> shift) & 255u);
@@ -162,7 +162,7 @@ __device__ __noinline__ Sum2 exact_select(const RowView<kBF16>& x, int n, uint32
   if (threadIdx.x == 0) sm.n_words = 0u;
   __syncthreads();
   Sum2 sum{-FLT_MAX, 0.0f};
-  each<kBF16>(x, [&](bool valid, float y, int v) {
+  each<kBF16, NT>(x, [&](bool valid, float y, int v) {
     const unsigned long long w = word_of(fkey(y), v);
     if (valid && n > 0 && w >= at) {
       sm.words[atomicAdd(&sm.n_words, 1u)] = w;  // n of them
