@@ -417,10 +417,10 @@ def _grad_like(student: torch.Tensor) -> torch.Tensor:
     size = student.element_size()
     ld = V + (student.stride(0) - V) % (16 // size) if N > 1 else V
     phase = student.data_ptr() % 16 // size
-    if phase == 0 and ld == V:
-        return torch.empty((N, V), dtype=student.dtype, device=student.device)
+    if phase == 0:
+        return torch.empty_strided((N, V), (ld, 1), dtype=student.dtype, device=student.device)
     grad = torch.empty(phase + N * ld, dtype=student.dtype, device=student.device)
-    return grad[phase:].view(N, ld)[:, :V]
+    return grad.as_strided((N, V), (ld, 1), phase)  # (one view: three cost 8 us)
 
 
 def _distill_forward(student, ids, values, temperature, rest, weight, stream, want_stats):
