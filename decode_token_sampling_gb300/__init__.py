@@ -619,8 +619,21 @@ def _token_logprobs_grad(ctx, grad_logprob, grad_entropy, *_):
     logits, tokens, stats, temperatures = ctx.saved_tensors
     g = None if grad_logprob is None else grad_logprob.contiguous()
     h = None if grad_entropy is None else grad_entropy.contiguous()
-    temperature = ctx.temperature if temperatures is None else temperatures
-    return token_logprobs_backward(g, h, logits, tokens, stats, temperature=temperature), None, None, None
+    N, V = logits.shape
+    index = logits.device.index
+    if V > 1 and logits.stride(1) != 1 or N > 1 and logits.stride(0) < V or index != torch.cuda.current_device():
+        # (saved elsewhere by a hook, or another device's turn: the call that looks at its arguments)
+        temperature = ctx.temperature if temperatures is None else temperatures
+        return token_logprobs_backward(g, h, logits, tokens, stats, temperature=temperature), None, None, None
+    # everything was checked by the forward pass, and autograd has checked the gradients
+    grad = _grad_like(logits)
+    st = load_library().kps_token_logprobs_backward(
+        logits.data_ptr(), KPS_F32 if logits.dtype is torch.float32 else KPS_BF16, N, V, logits.stride(0) if N > 1 else V,
+        tokens.data_ptr(), 1.0 if temperatures is not None else ctx.temperature, _addr(temperatures), _addr(g), _addr(h),
+        stats.data_ptr(), grad.data_ptr(), grad.stride(0), torch._C._cuda_getCurrentRawStream(index))
+    if st != 0:
+        raise KpsError(st, "kps_token_logprobs_backward")
+    return grad, None, None, None
 
 
 _token_logprobs_grad_once = torch.autograd.function.once_differentiable(_token_logprobs_grad)

@@ -301,6 +301,26 @@ def test_more_than_2_to_31_elements():
 
 
 @gpu
+def test_many_short_rows():
+    s = _case(70001, 5, torch.bfloat16, seed=2, empty=1000)
+    one, two = check(s), own(s)
+    assert all(torch.equal(a, b) for a, b in zip(one, two))
+
+
+@gpu
+def test_a_token_of_probability_zero():
+    """Without a penalty it has a ratio of 0; with one the loss is infinite, as its formula."""
+    s = _case(4, 3000, seed=1)
+    s["logits"][torch.arange(4), s["tokens"]] = -math.inf
+    s["old"].fill_(-2.0)
+    s["ref"].fill_(-2.0)
+    s["advantage"] = torch.tensor([1.0, -1.0, 0.0, 2.0], device="cuda")
+    got = check(s, kl=0.0)
+    assert bool(torch.isfinite(got.loss).all()) and bool(torch.isfinite(got.grad).all())
+    assert own(s, kl=0.1).loss.tolist() == [math.inf] * 4
+
+
+@gpu
 def test_binding_refusals():
     import decode_token_sampling_gb300 as kps
     s = _case(4, 100)

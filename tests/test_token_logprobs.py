@@ -414,7 +414,7 @@ def test_against_differences_of_the_kernel_itself():
 
 
 @gpu
-@pytest.mark.parametrize("n", [0, 30])
+@pytest.mark.parametrize("n", [0, 30, 200])
 def test_streams_graphs_and_repetition(n):
     import decode_token_sampling_gb300 as kps
     x, tokens = make(20, 32000, torch.bfloat16)
@@ -448,6 +448,68 @@ def test_streams_graphs_and_repetition(n):
     for got in runs:
         assert all(torch.equal(a, b) for a, b in zip(got, want) if a is not None)
     assert all(torch.equal(a, want_grad) for a in grads)
+
+
+@gpu
+@pytest.mark.parametrize("n", [0, 2, 40])
+def test_many_short_rows(n):
+    """More rows than a grid's other dimensions could hold; the same bits from call to call."""
+    for N, V in ((70001, 3 if n < 40 else 50), (2000, 4003)):
+        x, tokens = make(N, V, torch.bfloat16, seed=n)
+        m = min(n, V)
+        one, two = check(x, tokens, m), check(x, tokens, m)
+        assert all(torch.equal(a, b) for a, b in zip(one, two) if a is not None)
+        check_grad(x, tokens, *upstream(N))
+
+
+@gpu
+def test_two_host_threads():
+    import threading
+    import decode_token_sampling_gb300 as kps
+    cases = [make(30, 20011, torch.bfloat16, seed=i) for i in range(2)]
+    g, h = upstream(30)
+
+    def job(x, tokens):
+        t, stats = kps.token_logprobs_forward(x, tokens, 25)
+        leaf = x.clone().requires_grad_()
+        r = kps.token_logprobs(leaf, tokens)
+        grad, = torch.autograd.grad([r.logprob, r.entropy], leaf, [g, h])
+        p = kps.policy_loss_grad(x, tokens, g, h)
+        return [*t, kps.token_logprobs_backward(g, h, x, tokens, stats), grad, *p]
+
+    want = [job(*c) for c in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got[i].append(job(*cases[i]))
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 20
+        for run in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(run, want[i]))
+
+
+@gpu
+def test_logits_changed_before_the_backward_are_refused():
+    import decode_token_sampling_gb300 as kps
+    x, tokens = make(3, 100)
+    leaf = x.clone().requires_grad_()
+    y = leaf * 1.0
+    t = kps.token_logprobs(y, tokens)
+    with torch.no_grad():
+        y.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        t.logprob.sum().backward()
 
 
 @gpu
