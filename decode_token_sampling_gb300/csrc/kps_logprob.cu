@@ -54,13 +54,19 @@ __device__ __forceinline__ float warp_top(float x) { return kfloat(__reduce_max_
 // five loads in flight and five CTAs an SM; six and four 153, four and five 151, eight and four 153, eight and
 // three 165; four and six 147, but 16.4 instead of 15.0 us for 333 rows of 50001 fp32, whose CTAs are few.
 // Rounds that all look where the row ends took 160 with six and four.
-constexpr int kU = 5;        // 16-byte loads each thread keeps in flight
+// 16-byte loads each thread keeps in flight (of 512 threads four: the kept rounds fit 48 KB), and the widest cluster
+// of blocks of NT threads.
+template <int NT>
+constexpr int kLoads = NT == 512 ? 4 : 5;
+template <int NT>
+constexpr int kWidest = NT == 256 ? kMaxCS : 1;
 constexpr int kFew = 32;     // alternatives
 constexpr int kWords = 512;  // elements that are ranked
 template <bool kList, int NT>
 struct Few {
+  static constexpr int kU = kLoads<NT>;
   unsigned long long words[kWords + kFew];
-  unsigned long long lists[kMaxCS][kFew];  // rank 0's: what each CTA found
+  unsigned long long lists[kWidest<NT>][kFew];  // rank 0's: what each CTA found
   unsigned long long best[kFew];
   uint32_t sizes[kMaxCS];                  // and how many; ~0: more than there is room for
   uint32_t tops[kFew];                     // the keys of some threads' largest values of each warp
@@ -120,7 +126,7 @@ __device__ __forceinline__ bool gather_words(const RowView<kBF16>& x, int g0, in
                                              float loose, int loose_v, int n, Few<true, NT>& sm) {
   constexpr int G = kBF16 ? 8 : 4;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kPer = kFew / (NT / 32);
+  constexpr int kPer = kFew / (NT / 32), kU = kLoads<NT>;
   const uint32_t mine = fkey(most + 0.0f);
   {
     uint32_t k = mine;
@@ -201,9 +207,9 @@ __device__ __forceinline__ void rank_words(const unsigned long long* words, int 
 }
 
 template <bool kBF16, bool kList, int NT>
-__global__ void __launch_bounds__(NT, 5 * 256 / NT) score_kernel(const Args A) {
-  constexpr int G = kBF16 ? 8 : 4, NW = NT / 32;
-  __shared__ Part part[kMaxCS * NW];       // of the cluster's warps (rank 0's are used)
+__global__ void __launch_bounds__(NT, NT == 512 ? 2 : 5 * 256 / NT) score_kernel(const Args A) {
+  constexpr int G = kBF16 ? 8 : 4, NW = NT / 32, kU = kLoads<NT>;
+  __shared__ Part part[kWidest<NT> * NW];  // of the cluster's warps (rank 0's are used)
   __shared__ Few<kList, NT> sm;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   cg::cluster_group cl = cg::this_cluster();
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(NT, 5 * 256 / NT) score_kernel(const Args A) {
   }
   if (warp != 0) return;
   // the parts' sums against the row's largest logit; the first part that holds it keeps it out
-  static_assert(kMaxCS * NW <= 64);
+  static_assert(kWidest<NT> * NW <= 64);
   const Part none{-INFINITY, 0.0f, 0.0f, 0.0f};
   const Part p0 = lane < NW * CS ? part[lane] : none, p1 = lane + 32 < NW * CS ? part[lane + 32] : none;
   const float m = warp_top(fmaxf(p0.m, p1.m));
@@ -817,8 +823,8 @@ static kps_status launch_clusters(void (*kernel)(Params...), int64_t N, int cs, 
 }
 // A streaming kernel: one CTA a row, or up to kMaxCS while there are no more than `fill` an SM (0: any number) and every thread keeps
 // four vectors.  Five an SM for scoring without alternatives (256 rows of 151936 bf16: 21.6 us, 23.9 with two an SM;
-// 333 of 50001 fp32 13.7 and 15.1), two with them (27.8 and 25.8: a row's parts each rank their own).  The
-// gradient's CTAs have nothing in common, so there it is as many as there can be.
+// 333 of 50001 fp32 13.7 and 15.1), four with them (128 rows of 151936 bf16 19.2 and 19.8, 100 of 50001 fp32 12.3
+// and 13.1).  The gradient's CTAs have nothing in common, so there it is as many as there can be.
 template <class P>
 static kps_status launch_rows(void (*kernel)(P), const Args& a, kps_dtype dt, int fill, int sms, const P& params, cudaStream_t stream) {
   int cs = 1;
@@ -826,11 +832,13 @@ static kps_status launch_rows(void (*kernel)(P), const Args& a, kps_dtype dt, in
     while (cs < kMaxCS && (fill == 0 || a.N * cs * 2 <= static_cast<int64_t>(fill) * sms) && a.V >= 2 * cs * round) cs *= 2;
   return launch_clusters(kernel, a.N, cs, 0, stream, params);
 }
-// Scoring: many short rows go to blocks of 128 threads, twice as many an SM, as a block spends some 3.5 us on
+// Scoring.  Many short rows go to blocks of 128 threads, twice as many an SM, as a block spends some 3.5 us on
 // its start and its end whatever its row is (8192 rows of 5000 bf16: 27.8 us, 44.5 with 256 threads; with five
 // alternatives 55 and 85; 2048 of 32000 bf16 30.9 and 33.7).  Rows above 64 KB are faster with 256 (2048 of
-// 32000 fp32 with five alternatives 62 and 58.6, of 128256 bf16 125 and 109).
-constexpr int kShortBytes = 64 * 1024, kShortThreads = 128;
+// 32000 fp32 with five alternatives 62 and 58.6, of 128256 bf16 125 and 109).  With alternatives, one or two long
+// rows an SM go to blocks of 512 (256 of 151936 bf16, twenty alternatives: 26.5 us, 29.2 with 256 threads; 300 of 128256
+// 24.2 and 27.0; 200 of 50001 fp32 16.2 and 17.8): clusters of two of 256 take 28.7, 26.7 and 16.3.
+constexpr int kShortBytes = 64 * 1024, kShortThreads = 128, kLongThreads = 512;
 static kps_status launch_score(const Args& a, kps_dtype dt, cudaStream_t stream) {
   if (a.n > kFew) return launch_alternatives(a, dt, stream);
   const int sms = sm_count();
@@ -842,9 +850,13 @@ static kps_status launch_score(const Args& a, kps_dtype dt, cudaStream_t stream)
                         : (list ? score_kernel<false, true, NT> : score_kernel<false, false, NT>);
     return launch_clusters<NT>(kernel, a.N, 1, 0, stream, a);
   }
+  if (list && a.N > sms && a.N <= 2 * sms && static_cast<int64_t>(a.V) * (bf16 ? 2 : 4) > kShortBytes) {
+    constexpr int NT = kLongThreads;
+    return launch_clusters<NT>(bf16 ? score_kernel<true, true, NT> : score_kernel<false, true, NT>, a.N, 1, 0, stream, a);
+  }
   auto* kernel = bf16 ? (list ? score_kernel<true, true, kNT> : score_kernel<true, false, kNT>)
                       : (list ? score_kernel<false, true, kNT> : score_kernel<false, false, kNT>);
-  return launch_rows<Args>(kernel, a, dt, list ? 2 : 5, sms, a, stream);
+  return launch_rows<Args>(kernel, a, dt, list ? 4 : 5, sms, a, stream);
 }
 template <bool kPolicy>
 static kps_status launch_slope(const Grad& P, kps_dtype dt, cudaStream_t stream) {
