@@ -88,9 +88,11 @@ class Rows:
         size = torch.where(p > 0, d.abs(), 0.0)
         rel = EX2 + 4 * U * size + self.share[:, None] + 8 * U
         ga, ha = g.abs()[:, None], h.abs()[:, None]
-        tol = p * (ga + ha * (size + Q)) * rel + p * ha * Q * (self.r1 + self.r2)[:, None] + 4 * U * p * ha * size
-        # the token's own: eps / S where it is the largest, else 1 - p of a p of at most 1/2
-        own = torch.where(self.at_max, (self.eps / self.S) * (self.r1 + 6 * U), 2 * U + p.gather(1, self.at)[:, 0] * rel.gather(1, self.at)[:, 0])
+        # (Q's terms below 2^-126 are zero too: at most 2^20 of 2^-126 times an exponent of 88, 1.1e-30)
+        tol = p * (ga + ha * (size + Q)) * rel + p * ha * (Q * (self.r1 + self.r2)[:, None] + 2 * TINY) + 4 * U * p * ha * size
+        # the token's own: eps / S where it is the largest (its terms below 2^-126 are zero: at most 2^20 of them,
+        # 1.3e-32), else 1 - p of a p of at most 1/2
+        own = torch.where(self.at_max, (self.eps / self.S) * (self.r1 + 6 * U) + TINY, 2 * U + p.gather(1, self.at)[:, 0] * rel.gather(1, self.at)[:, 0])
         tol = tol + delta * ga * own[:, None] + 4 * U * (ga * one_less.abs() + ha * info.abs())
         if g_tol is not None:
             tol = tol + g_tol[:, None] * one_less.abs()
