@@ -48,14 +48,14 @@ __device__ __forceinline__ float warp_top(float x) { return kfloat(__reduce_max_
 // shared memory, and the largest value of its other rounds.  Of the threads' largest values 32, the first few of
 // each warp, are put in order: the n-th of them bounds the n-th of the block's part of the row from below.  What reaches it
 // lies in the kept rounds, or (the other value reaches it too: a thread in some rows) in vectors that are
-// read once more: little more than n elements, ranked pairwise.  2048 rows of 128256 bf16 take 109 us with five
-// alternatives, 112 with twenty, 90 without (79 at the copy rate): a block's end takes some 7 us, the first, last and
-// ranking phases of a chain that five blocks an SM do not hide.  Slower: every vector above a rising bound listed during the
-// pass (139 us), the kept round read again instead of kept (118), all vectors of the threads read again (108, but 147
-// with twenty), the largest vector of each of a thread's five streams kept (131).
+// read once more: little more than n elements, ranked pairwise.  2048 rows of 128256 bf16 take 106 us with five
+// alternatives, 109 with twenty, 88 without (79 at the copy rate): a block's end takes some 7 us, the last sums and
+// the ranking in a chain that five blocks an SM do not hide.  Slower (when it took 111 and 112): every vector above a
+// rising bound listed during the pass (139), the kept round read again instead of kept (118 and 127), all vectors of
+// those threads read again (108 and 147), the largest vector of each of a thread's five streams kept (131).
 //
 // 4096 rows of 151936 bf16, a quarter of them empty, without alternatives: 147 us (140 at the copy rate) with
-// five loads in flight and five CTAs an SM; six and four 153, four and five 151, eight and four 153, eight and
+// five loads in flight and five CTAs an SM (146 since the first round is fetched ahead); six and four 153, four and five 151, eight and four 153, eight and
 // three 165; four and six 147, but 16.4 instead of 15.0 us for 333 rows of 50001 fp32, whose CTAs are few.
 // Rounds that all look where the row ends took 160 with six and four.  Blocks that go on to rows of blocks not yet
 // started (cluster launch control), their warps independent of each other: 165, for the registers that it takes and
