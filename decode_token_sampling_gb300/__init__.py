@@ -542,6 +542,8 @@ def _token_args(logits, tokens, temperature):
     ld = _rows(logits, "logits")
     dt = _dtype_code(logits)
     N, V = logits.shape
+    if tokens is None:
+        raise TypeError("tokens must be a tensor")
     _check(tokens, "tokens", torch.int64, (N,), logits.device)
     if isinstance(temperature, torch.Tensor):
         _check(temperature, "temperature", torch.float32, (N,), logits.device)
@@ -602,6 +604,8 @@ def token_logprobs_backward(grad_logprob: Optional[torch.Tensor], grad_entropy: 
     N, dev = logits.shape[0], logits.device
     _check(grad_logprob, "grad_logprob", torch.float32, (N,), dev)
     _check(grad_entropy, "grad_entropy", torch.float32, (N,), dev)
+    if stats is None:
+        raise TypeError("stats must be a tensor")
     _check(stats, "stats", torch.float32, (3, N), dev)
 
     def call(handle):
@@ -707,6 +711,8 @@ def policy_loss_grad(logits: torch.Tensor, tokens: torch.Tensor, old_logprob: to
     lib = load_library()
     args, scale = _token_args(logits, tokens, temperature)
     N, dev = logits.shape[0], logits.device
+    if old_logprob is None or advantage is None:
+        raise TypeError("old_logprob and advantage must be tensors")
     for name, t in (("old_logprob", old_logprob), ("advantage", advantage), ("ref_logprob", ref_logprob), ("weight", weight)):
         _check(t, name, torch.float32, (N,), dev)
     if kl_coef != 0 and ref_logprob is None:

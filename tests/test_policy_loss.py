@@ -325,7 +325,8 @@ def test_binding_refusals():
     import decode_token_sampling_gb300 as kps
     s = _case(4, 100)
     for bad in (dict(logits=s["logits"].half()), dict(tokens=s["tokens"].int()), dict(old=s["old"].double()), dict(advantage=s["advantage"][:3]),
-                dict(ref=s["ref"].cpu()), dict(weight=s["weight"][:, None]), dict(ref=None)):
+                dict(ref=s["ref"].cpu()), dict(weight=s["weight"][:, None]), dict(ref=None),
+                dict(tokens=None), dict(old=None), dict(advantage=None)):
         with pytest.raises((TypeError, ValueError)):
             own(dict(s, **bad))
     for kw in (dict(clip=(-0.1, 0.2)), dict(clip=(0.2, math.nan)), dict(kl=math.inf), dict(ent=math.nan), dict(temperature=0.0)):

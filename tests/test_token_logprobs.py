@@ -557,7 +557,7 @@ def test_binding_refusals():
     x, tokens = make(4, 100)
     T = torch.ones(4, device="cuda")
     for bad in (dict(logits=x.half()), dict(logits=x[0]), dict(logits=x.t()), dict(logits=x[:1].expand(4, 100)), dict(n=101), dict(n=-1),
-                dict(tokens=tokens.int()), dict(tokens=tokens.cpu()), dict(tokens=tokens[:3]), dict(tokens=tokens[:, None]),
+                dict(tokens=tokens.int()), dict(tokens=tokens.cpu()), dict(tokens=None), dict(tokens=tokens[:3]), dict(tokens=tokens[:, None]),
                 dict(temperature=T.double()), dict(temperature=T[:3]), dict(temperature=T.cpu()),
                 dict(temperature=T.clone().requires_grad_()), dict(logits=x.clone().requires_grad_(), stream=torch.cuda.Stream())):
         kw = dict(logits=x, tokens=tokens, n=5)
@@ -570,7 +570,7 @@ def test_binding_refusals():
     _, stats = kps.token_logprobs_forward(x, tokens)
     one = torch.ones(4, device="cuda")
     for args in ((one.double(), None, x, tokens, stats), (None, one[:3], x, tokens, stats), (one, one, x, tokens, stats.t()),
-                 (one, one, x, tokens, stats[:2])):
+                 (one, one, x, tokens, stats[:2]), (one, one, x, tokens, None)):
         with pytest.raises((TypeError, ValueError)):
             kps.token_logprobs_backward(*args)
 
