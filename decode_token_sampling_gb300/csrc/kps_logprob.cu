@@ -55,7 +55,7 @@ __device__ __forceinline__ float warp_top(float x) { return kfloat(__reduce_max_
 // those threads read again (108 and 147), the largest vector of each of a thread's five streams kept (131).
 //
 // 4096 rows of 151936 bf16, a quarter of them empty, without alternatives: 147 us (140 at the copy rate) with
-// five loads in flight and five CTAs an SM (146 since the first round is fetched ahead); six and four 153, four and five 151, eight and four 153, eight and
+// five loads in flight and five CTAs an SM; six and four 153, four and five 151, eight and four 153, eight and
 // three 165; four and six 147, but 16.4 instead of 15.0 us for 333 rows of 50001 fp32, whose CTAs are few.
 // Rounds that all look where the row ends took 160 with six and four.  Blocks that go on to rows of blocks not yet
 // started (cluster launch control), their warps independent of each other: 165, for the registers that it takes and
@@ -228,13 +228,17 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 5 * 256 / NT) score_kernel
   const RowView<kBF16> x(A.x, row * A.ld, A.V);
   const int g0 = static_cast<int>(static_cast<int64_t>(x.nv) * rank / CS);
   const int g1 = static_cast<int>(static_cast<int64_t>(x.nv) * (rank + 1) / CS);
-  // the first round is on its way to the second-level cache before the token says that the row counts (an empty
-  // row costs its first round; 2048 rows of 128256 bf16 with five alternatives 110 -> 106 us, 4096 of 32000 fp32
-  // without 85 -> 78; two rounds: 106, 75, but rollouts with a quarter of padding 147 -> 148)
+  // The first round is on its way to the second-level cache before the token says that the row counts.  A row of
+  // padding costs its first round, so not for bf16 without alternatives, a training batch's case (rollouts with a quarter
+  // of padding 150.4 us, 152.0 so).  With alternatives 2048 rows of 128256 bf16 take 107.3 instead of 108.2 us, with a
+  // quarter of padding 86.8 and 89.3; 4096 rows of 32000 fp32 without alternatives 82 and 85, with a quarter 65.5
+  // either way, with half 48.4 and 45.4; 1024 of 128256 83 and 85.
+  if (kList || !kBF16) {
 #pragma unroll
-  for (int u = 0; u < kU; ++u) {
-    const int g = g0 + u * NT + static_cast<int>(threadIdx.x);
-    if (g < g1) asm volatile("prefetch.global.L2 [%0];" ::"l"(x.vec + g));
+    for (int u = 0; u < kU; ++u) {
+      const int g = g0 + u * NT + static_cast<int>(threadIdx.x);
+      if (g < g1) asm volatile("prefetch.global.L2 [%0];" ::"l"(x.vec + g));
+    }
   }
   const int64_t t = A.tokens[row];
   const float tau = row_tau(A.taus, A.tau, row);
