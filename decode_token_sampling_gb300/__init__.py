@@ -423,6 +423,25 @@ def _grad_like(student: torch.Tensor) -> torch.Tensor:
     return grad.as_strided((N, V), (ld, 1), phase)  # (one view: three cost 8 us)
 
 
+class _FirstOnly(torch.autograd.Function):
+    """A gradient as it is, tied to what it was computed from: a derivative of it raises."""
+
+    @staticmethod
+    def forward(ctx, grad, *sources):
+        return grad.detach()
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("second derivatives are not available: the gradient was computed by a kernel that has none")
+
+
+def _first_only(grad, ctx, *upstream):
+    """What a recorded backward returns for its first saved tensor.  Where the backward is recorded in turn
+    (create_graph), the gradient depends on that tensor even if no gradient from above requires one, and must not pass
+    for a constant."""
+    return _FirstOnly.apply(grad, ctx.saved_tensors[0], *upstream) if torch.is_grad_enabled() else grad
+
+
 def _distill_forward(student, ids, values, temperature, rest, weight, stream, want_stats):
     lib = load_library()
     args = _distill_args(student, ids, values, rest, weight, temperature)
@@ -619,7 +638,7 @@ def token_logprobs_backward(grad_logprob: Optional[torch.Tensor], grad_entropy: 
     return _queue(dev, stream, (logits, tokens, _tensor(temperature), grad_logprob, grad_entropy, stats), call)
 
 
-def _token_logprobs_grad(ctx, grad_logprob, grad_entropy, *_):
+def _token_logprobs_grad(ctx, grad_logprob, grad_entropy):
     logits, tokens, stats, temperatures = ctx.saved_tensors
     g = None if grad_logprob is None else grad_logprob.contiguous()
     h = None if grad_entropy is None else grad_entropy.contiguous()
@@ -628,7 +647,7 @@ def _token_logprobs_grad(ctx, grad_logprob, grad_entropy, *_):
     if V > 1 and logits.stride(1) != 1 or N > 1 and logits.stride(0) < V or index != torch.cuda.current_device():
         # (saved elsewhere by a hook, or another device's turn: the call that looks at its arguments)
         temperature = ctx.temperature if temperatures is None else temperatures
-        return token_logprobs_backward(g, h, logits, tokens, stats, temperature=temperature), None, None, None
+        return token_logprobs_backward(g, h, logits, tokens, stats, temperature=temperature)
     # everything was checked by the forward pass, and autograd has checked the gradients
     grad = _grad_like(logits)
     st = load_library().kps_token_logprobs_backward(
@@ -637,10 +656,7 @@ def _token_logprobs_grad(ctx, grad_logprob, grad_entropy, *_):
         stats.data_ptr(), grad.data_ptr(), grad.stride(0), torch._C._cuda_getCurrentRawStream(index))
     if st != 0:
         raise KpsError(st, "kps_token_logprobs_backward")
-    return grad, None, None, None
-
-
-_token_logprobs_grad_once = torch.autograd.function.once_differentiable(_token_logprobs_grad)
+    return grad
 
 
 class _TokenLogprobs(torch.autograd.Function):
@@ -657,9 +673,8 @@ class _TokenLogprobs(torch.autograd.Function):
         return tuple(out)
 
     @staticmethod
-    def backward(ctx, *grads):
-        # (the wrapper that refuses second derivatives costs microseconds: only where they could be asked for)
-        return (_token_logprobs_grad_once if torch.is_grad_enabled() else _token_logprobs_grad)(ctx, *grads)
+    def backward(ctx, grad_logprob, grad_entropy, *_):
+        return _first_only(_token_logprobs_grad(ctx, grad_logprob, grad_entropy), ctx, grad_logprob, grad_entropy), None, None, None
 
 
 def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, n: int = 0, *,

@@ -1,0 +1,89 @@
+"""What the differentiable operators refuse: second derivatives, forward mode, vmap.
+
+Without a GPU the binding runs against a library that computes nothing and CPU tensors that say they are CUDA ones: what
+autograd records and what reaches the library is the binding's own.
+"""
+
+import pytest
+import torch
+from torch.autograd import forward_ad
+
+import decode_token_sampling_gb300 as kps
+
+
+class _Device(torch.Tensor):
+    """A CPU tensor that passes for a CUDA one."""
+    is_cuda = property(lambda self: True)
+
+
+def _device(t):
+    return t.detach().as_subclass(_Device).requires_grad_(t.requires_grad)
+
+
+class _Library:
+    """Takes every call and counts it."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        if not name.startswith("kps_"):
+            raise AttributeError(name)
+
+        def call(*args):
+            self.calls.append(name)
+            return 0
+        return call
+
+
+@pytest.fixture
+def library(monkeypatch):
+    lib = _Library()
+    monkeypatch.setattr(kps, "load_library", lambda: lib)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0, raising=False)
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t, lambda t: _device(t) if t.device.type == "cpu" else t):
+        yield lib
+
+
+def _logprobs(x):
+    n = x.shape[0]
+    t = kps.token_logprobs(x, _tokens(n, x))
+    return t.logprob.sum() + t.entropy.sum()
+
+
+def _tokens(n, like):
+    t = torch.zeros(n, dtype=torch.int64, device=like.device)
+    return t if like.device.type == "cuda" else _device(t)
+
+
+def _second_derivatives(call, x):
+    """The gradient alone is given; what would go on through it raises, beside a term that has a second derivative too."""
+    u, = torch.autograd.grad(call(x), x, create_graph=True)
+    assert u.shape == x.shape
+    with torch.no_grad():
+        u.mul_(2.0)  # (a tensor of its own)
+    with pytest.raises(RuntimeError, match="second derivatives"):
+        (u.pow(2).sum() + (x ** 2).sum()).backward()
+    assert x.grad is None
+    # with respect to what comes from above, too
+    w = torch.ones((), device=x.device, requires_grad=True)
+    u, = torch.autograd.grad(call(x) * w, x, create_graph=True)
+    with pytest.raises(RuntimeError, match="second derivatives"):
+        torch.autograd.grad(u.sum() + w * w, w)
+    # and not where nothing is asked of it
+    y, = torch.autograd.grad(call(x) + (x ** 2).sum(), x)
+    assert not y.requires_grad
+
+
+def test_second_derivatives_of_logprobs(library):
+    _second_derivatives(_logprobs, _device(torch.randn(3, 10)).requires_grad_())
+    assert library.calls.count("kps_token_logprobs_backward") == 3
+
+
+gpu = pytest.mark.gpu
+
+
+@gpu
+def test_second_derivatives_of_logprobs_on_the_gpu():
+    _second_derivatives(_logprobs, torch.randn(3, 10, device="cuda", requires_grad=True))
