@@ -517,12 +517,11 @@ class _DistillLoss(torch.autograd.Function):
         return loss
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, grad_loss):
         student, ids, values, rest, weight, stats = ctx.saved_tensors
         grad = distill_backward(grad_loss.contiguous(), student, ids, values, stats, temperature=ctx.temperature,
                                 rest=rest, weight=weight)
-        return grad, None, None, None, None, None
+        return _first_only(grad, ctx, grad_loss), None, None, None, None, None
 
 
 def distill_loss(student: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, *, temperature: float = 1.0,

@@ -81,9 +81,28 @@ def test_second_derivatives_of_logprobs(library):
     assert library.calls.count("kps_token_logprobs_backward") == 3
 
 
+def _distill(x):
+    n = x.shape[0]
+    ids = torch.arange(3 * n, dtype=torch.int32, device=x.device).view(n, 3)
+    values = torch.zeros(n, 3, device=x.device)
+    if x.device.type != "cuda":
+        ids, values = _device(ids), _device(values)
+    return kps.distill_loss(x, ids, values).sum()
+
+
+def test_second_derivatives_of_the_distillation(library):
+    _second_derivatives(_distill, _device(torch.randn(3, 10)).requires_grad_())
+    assert library.calls.count("kps_distill_backward") == 3
+
+
 gpu = pytest.mark.gpu
 
 
 @gpu
 def test_second_derivatives_of_logprobs_on_the_gpu():
     _second_derivatives(_logprobs, torch.randn(3, 10, device="cuda", requires_grad=True))
+
+
+@gpu
+def test_second_derivatives_of_the_distillation_on_the_gpu():
+    _second_derivatives(_distill, torch.randn(3, 10, device="cuda", requires_grad=True))
