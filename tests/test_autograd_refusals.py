@@ -1,23 +1,13 @@
 """What the differentiable operators refuse: second derivatives, forward mode, vmap.
 
-Without a GPU the binding runs against a library that computes nothing and CPU tensors that say they are CUDA ones: what
-autograd records and what reaches the library is the binding's own.
+Without a GPU the binding runs against a library that computes nothing, on CPU tensors that say they are CUDA ones: what autograd
+records and what reaches the library is the binding's own.
 """
 
 import pytest
 import torch
-from torch.autograd import forward_ad
 
 import decode_token_sampling_gb300 as kps
-
-
-class _Device(torch.Tensor):
-    """A CPU tensor that passes for a CUDA one."""
-    is_cuda = property(lambda self: True)
-
-
-def _device(t):
-    return t.detach().as_subclass(_Device).requires_grad_(t.requires_grad)
 
 
 class _Library:
@@ -42,19 +32,13 @@ def library(monkeypatch):
     monkeypatch.setattr(kps, "load_library", lambda: lib)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0, raising=False)
-    with torch.autograd.graph.saved_tensors_hooks(lambda t: t, lambda t: _device(t) if t.device.type == "cpu" else t):
-        yield lib
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda self: True), raising=False)
+    return lib
 
 
 def _logprobs(x):
-    n = x.shape[0]
-    t = kps.token_logprobs(x, _tokens(n, x))
+    t = kps.token_logprobs(x, torch.zeros(x.shape[0], dtype=torch.int64, device=x.device))
     return t.logprob.sum() + t.entropy.sum()
-
-
-def _tokens(n, like):
-    t = torch.zeros(n, dtype=torch.int64, device=like.device)
-    return t if like.device.type == "cuda" else _device(t)
 
 
 def _second_derivatives(call, x):
@@ -77,21 +61,18 @@ def _second_derivatives(call, x):
 
 
 def test_second_derivatives_of_logprobs(library):
-    _second_derivatives(_logprobs, _device(torch.randn(3, 10)).requires_grad_())
+    _second_derivatives(_logprobs, torch.randn(3, 10, requires_grad=True))
     assert library.calls.count("kps_token_logprobs_backward") == 3
 
 
 def _distill(x):
     n = x.shape[0]
     ids = torch.arange(3 * n, dtype=torch.int32, device=x.device).view(n, 3)
-    values = torch.zeros(n, 3, device=x.device)
-    if x.device.type != "cuda":
-        ids, values = _device(ids), _device(values)
-    return kps.distill_loss(x, ids, values).sum()
+    return kps.distill_loss(x, ids, torch.zeros(n, 3, device=x.device)).sum()
 
 
 def test_second_derivatives_of_the_distillation(library):
-    _second_derivatives(_distill, _device(torch.randn(3, 10)).requires_grad_())
+    _second_derivatives(_distill, torch.randn(3, 10, requires_grad=True))
     assert library.calls.count("kps_distill_backward") == 3
 
 
