@@ -22,6 +22,7 @@ import threading
 from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
+from torch.autograd import forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkps.so")
@@ -423,6 +424,15 @@ def _grad_like(student: torch.Tensor) -> torch.Tensor:
     return grad.as_strided((N, V), (ld, 1), phase)  # (one view: three cost 8 us)
 
 
+def _no_tangents(what: str, *inputs) -> None:
+    """Refuses forward mode: the results would lack their tangents without a word."""
+    if forward_ad._current_level < 0:  # no dual level is open (looking at every input costs 0.3 us each)
+        return
+    for t in inputs:
+        if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError(f"{what} has no forward mode, but an input carries a tangent")
+
+
 class _FirstOnly(torch.autograd.Function):
     """A gradient as it is, tied to what it was computed from: a derivative of it raises."""
 
@@ -518,6 +528,7 @@ class _DistillLoss(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_loss):
+        _no_tangents("the gradient of distill_loss", grad_loss)
         student, ids, values, rest, weight, stats = ctx.saved_tensors
         grad = distill_backward(grad_loss.contiguous(), student, ids, values, stats, temperature=ctx.temperature,
                                 rest=rest, weight=weight)
@@ -537,6 +548,7 @@ def distill_loss(student: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
     raise.  Runs on the current stream.  A captured backward should make its leaves inside the
     capture, as any autograd graph's; distill_loss_grad needs none.
     """
+    _no_tangents("distill_loss", student, values, rest, weight)
     for name, t in (("values", values), ("rest", rest), ("weight", weight)):
         if t is not None and t.requires_grad:
             raise ValueError(f"{name} requires a gradient, but distill_loss has one for the student only")
@@ -607,6 +619,7 @@ def token_logprobs_forward(logits: torch.Tensor, tokens: torch.Tensor, n: int = 
                            stream: Optional[torch.cuda.Stream] = None) -> Tuple[TokenLogprobs, torch.Tensor]:
     """What token_logprobs returns, and the statistics [3, N] that token_logprobs_backward takes; no
     autograd."""
+    _no_tangents("token_logprobs_forward", logits, temperature)
     return _token_logprobs(logits, tokens, n, temperature, stream, True)
 
 
@@ -617,6 +630,7 @@ def token_logprobs_backward(grad_logprob: Optional[torch.Tensor], grad_entropy: 
     """The gradient of the logits, in their type, for the gradients of the log-probabilities and the
     entropies (float32 [N] each, None: 0) and the statistics of token_logprobs_forward on the same
     arguments."""
+    _no_tangents("token_logprobs_backward", grad_logprob, grad_entropy, logits, stats, temperature)
     lib = load_library()
     args, scale = _token_args(logits, tokens, temperature)
     N, dev = logits.shape[0], logits.device
@@ -673,6 +687,7 @@ class _TokenLogprobs(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_logprob, grad_entropy, *_):
+        _no_tangents("the gradient of token_logprobs", grad_logprob, grad_entropy)
         return _first_only(_token_logprobs_grad(ctx, grad_logprob, grad_entropy), ctx, grad_logprob, grad_entropy), None, None, None
 
 
@@ -693,6 +708,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, n: int = 0, *,
     leaves inside the capture, as any autograd graph's; token_logprobs_forward and
     token_logprobs_backward need none.
     """
+    _no_tangents("token_logprobs", logits, temperature)
     if not (torch.is_grad_enabled() and logits.requires_grad):
         return _token_logprobs(logits, tokens, n, temperature, stream, False)[0]
     if stream is not None:
@@ -722,6 +738,7 @@ def policy_loss_grad(logits: torch.Tensor, tokens: torch.Tensor, old_logprob: to
     lies outside [0, V), are not read: loss, log-probability, entropy and gradient 0.  temperature as for
     token_logprobs.  Any other loss of log-probabilities and entropies: token_logprobs and autograd.
     """
+    _no_tangents("policy_loss_grad", logits, old_logprob, advantage, ref_logprob, weight, temperature)
     lib = load_library()
     args, scale = _token_args(logits, tokens, temperature)
     N, dev = logits.shape[0], logits.device

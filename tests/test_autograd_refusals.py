@@ -6,6 +6,7 @@ records and what reaches the library is the binding's own.
 
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 import decode_token_sampling_gb300 as kps
 
@@ -76,6 +77,81 @@ def test_second_derivatives_of_the_distillation(library):
     assert library.calls.count("kps_distill_backward") == 3
 
 
+def _calls(device):
+    """(call, its arguments that may carry a tangent) for every operator that says what it is not differentiated by."""
+    n = 3
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn(n, 10, generator=g).to(device)
+    tokens = torch.zeros(n, dtype=torch.int64, device=device)
+    ids = torch.arange(3, dtype=torch.int32, device=device).repeat(n, 1)
+    row = torch.rand(n, generator=g).to(device) + 0.5
+    return {
+        "token_logprobs": (lambda x, T: kps.token_logprobs(x, tokens, temperature=T), (x, row)),
+        "token_logprobs_forward": (lambda x, T: kps.token_logprobs_forward(x, tokens, temperature=T), (x, row)),
+        "token_logprobs_backward": (lambda g, h, x, stats, T: kps.token_logprobs_backward(g, h, x, tokens, stats, temperature=T),
+                                    (row, row, x, torch.ones(3, n, device=device), row)),
+        "policy_loss_grad": (lambda x, old, A, ref, w, T: kps.policy_loss_grad(x, tokens, old, A, ref_logprob=ref, kl_coef=0.1, weight=w,
+                                                                               temperature=T), (x, row, row, row, row, row)),
+        "distill_loss": (lambda x, values, rest, w: kps.distill_loss(x, ids, values, rest=rest, weight=w), (x, torch.zeros(n, 3, device=device), row, row)),
+    }
+
+
+NAMES = ["token_logprobs", "token_logprobs_forward", "token_logprobs_backward", "policy_loss_grad", "distill_loss"]
+
+
+def _forward_mode(name, device):
+    """A tangent in any argument is refused before anything runs; none is needed to be refused for the others."""
+    call, args = _calls(device)[name]
+    call(*args)
+    with forward_ad.dual_level():
+        call(*args)  # (no tangent among them)
+        for i in range(len(args)):
+            dual = [forward_ad.make_dual(a, torch.ones_like(a)) if j == i else a for j, a in enumerate(args)]
+            with pytest.raises(NotImplementedError, match="forward mode"):
+                call(*dual)
+        for i in range(len(args)):
+            dual = [forward_ad.make_dual(a.clone().requires_grad_(), torch.ones_like(a)) if j == i else a for j, a in enumerate(args)]
+            with pytest.raises((NotImplementedError, ValueError)):
+                call(*dual)
+    with pytest.raises(NotImplementedError, match="forward mode"):
+        torch.func.jvp(lambda a: call(a, *args[1:])[0], args[:1], (torch.ones_like(args[0]),))
+
+
+def _forward_over_reverse(call, x):
+    """A tangent that comes from above reaches the recorded backward only."""
+    with forward_ad.dual_level():
+        w = forward_ad.make_dual(torch.tensor(2.0, device=x.device), torch.tensor(1.0, device=x.device))
+        out = call(x) * w
+        with pytest.raises(NotImplementedError, match="forward mode"):
+            torch.autograd.grad(out, x)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_forward_mode(name, library):
+    _forward_mode(name, "cpu")
+    assert len(library.calls) == 2
+
+
+def test_forward_mode_from_above(library):
+    _forward_over_reverse(_logprobs, torch.randn(3, 10, requires_grad=True))
+    _forward_over_reverse(_distill, torch.randn(3, 10, requires_grad=True))
+    assert not any("backward" in c for c in library.calls)
+
+
+def _vmap(name, device):
+    call, args = _calls(device)[name]
+    for i in range(len(args)):
+        many = [torch.stack([a, a]) if j == i else a for j, a in enumerate(args)]
+        with pytest.raises(RuntimeError):
+            torch.vmap(call, in_dims=tuple(0 if j == i else None for j in range(len(args))))(*many)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_vmap(name, library):
+    _vmap(name, "cpu")
+    assert library.calls == []
+
+
 gpu = pytest.mark.gpu
 
 
@@ -87,3 +163,16 @@ def test_second_derivatives_of_logprobs_on_the_gpu():
 @gpu
 def test_second_derivatives_of_the_distillation_on_the_gpu():
     _second_derivatives(_distill, torch.randn(3, 10, device="cuda", requires_grad=True))
+
+
+@gpu
+@pytest.mark.parametrize("name", NAMES)
+def test_forward_mode_and_vmap_on_the_gpu(name):
+    _forward_mode(name, "cuda")
+    _vmap(name, "cuda")
+
+
+@gpu
+def test_forward_mode_from_above_on_the_gpu():
+    _forward_over_reverse(_logprobs, torch.randn(3, 10, device="cuda", requires_grad=True))
+    _forward_over_reverse(_distill, torch.randn(3, 10, device="cuda", requires_grad=True))
