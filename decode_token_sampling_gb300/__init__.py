@@ -653,20 +653,25 @@ def token_logprobs_backward(grad_logprob: Optional[torch.Tensor], grad_entropy: 
 
 def _token_logprobs_grad(ctx, grad_logprob, grad_entropy):
     logits, tokens, stats, temperatures = ctx.saved_tensors
+    if logits.dtype is not ctx.dtype or logits.shape != ctx.shape:
+        raise ValueError(f"logits were saved as {ctx.dtype} {tuple(ctx.shape)} and came back as {logits.dtype} {tuple(logits.shape)}")
     g = None if grad_logprob is None else grad_logprob.contiguous()
     h = None if grad_entropy is None else grad_entropy.contiguous()
-    N, V = logits.shape
-    index = logits.device.index
-    if V > 1 and logits.stride(1) != 1 or N > 1 and logits.stride(0) < V or index != torch.cuda.current_device():
-        # (saved elsewhere by a hook, or another device's turn: the call that looks at its arguments)
+    N, V = ctx.shape
+    device = logits.device
+    if V > 1 and logits.stride(1) != 1 or N > 1 and logits.stride(0) < V or device.index != torch.cuda.current_device():
         temperature = ctx.temperature if temperatures is None else temperatures
         return token_logprobs_backward(g, h, logits, tokens, stats, temperature=temperature)
-    # everything was checked by the forward pass, and autograd has checked the gradients
+    # Autograd has checked the gradients; hooks may have given back other tensors than those that were saved.  (The call
+    # above, which looks at everything once more, takes 6 us longer.)
+    _check(tokens, "tokens", torch.int64, (N,), device)
+    _check(stats, "stats", torch.float32, (3, N), device)
+    _check(temperatures, "temperature", torch.float32, (N,), device)
     grad = _grad_like(logits)
     st = load_library().kps_token_logprobs_backward(
-        logits.data_ptr(), KPS_F32 if logits.dtype is torch.float32 else KPS_BF16, N, V, logits.stride(0) if N > 1 else V,
-        tokens.data_ptr(), 1.0 if temperatures is not None else ctx.temperature, _addr(temperatures), _addr(g), _addr(h),
-        stats.data_ptr(), grad.data_ptr(), grad.stride(0), torch._C._cuda_getCurrentRawStream(index))
+        logits.data_ptr(), _dtype_code(logits), N, V, logits.stride(0) if N > 1 else V, tokens.data_ptr(),
+        1.0 if temperatures is not None else ctx.temperature, _addr(temperatures), _addr(g), _addr(h), stats.data_ptr(),
+        grad.data_ptr(), grad.stride(0), torch._C._cuda_getCurrentRawStream(device.index))
     if st != 0:
         raise KpsError(st, "kps_token_logprobs_backward")
     return grad
@@ -678,6 +683,7 @@ class _TokenLogprobs(torch.autograd.Function):
         out, stats = _token_logprobs(logits, tokens, n, temperature, None, True)
         ctx.save_for_backward(logits, tokens, stats, _tensor(temperature))
         ctx.temperature = None if isinstance(temperature, torch.Tensor) else temperature
+        ctx.dtype, ctx.shape = logits.dtype, logits.shape
         ctx.set_materialize_grads(False)
         if n:
             ctx.mark_non_differentiable(out.rank, out.ids, out.logprobs)
