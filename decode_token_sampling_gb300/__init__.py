@@ -706,7 +706,8 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, n: int = 0, *,
     respect to the logits.
 
     temperature: a number, or float32 [N] as sample takes it (values that are no positive normal number,
-    its greedy rows, count as 1).  A token outside [0, V) marks a row of padding, which is not read:
+    its greedy rows, count as 1).  A token outside [0, V) marks a row of padding, whose logits may be
+    anything (they may be fetched, but enter nothing):
     log-probability and entropy 0, rank -1, ids -1, alternatives of -inf, gradient 0.  Rows may lie apart.
 
     First derivatives in reverse mode only: second derivatives, forward mode and vmap raise.  A call that
@@ -741,7 +742,7 @@ def policy_loss_grad(logits: torch.Tensor, tokens: torch.Tensor, old_logprob: to
 
     old_logprob, advantage: float32 [N]; clip: how far below and above 1 the ratio may go; ref_logprob:
     float32 [N], with kl_coef; weight: float32 [N] (None: 1).  Rows of weight 0, and rows whose token
-    lies outside [0, V), are not read: loss, log-probability, entropy and gradient 0.  temperature as for
+    lies outside [0, V), enter nothing: loss, log-probability, entropy and gradient 0.  temperature as for
     token_logprobs.  Any other loss of log-probabilities and entropies: token_logprobs and autograd.
     """
     _no_tangents("policy_loss_grad", logits, old_logprob, advantage, ref_logprob, weight, temperature)

@@ -228,17 +228,17 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 5 * 256 / NT) score_kernel
   const RowView<kBF16> x(A.x, row * A.ld, A.V);
   const int g0 = static_cast<int>(static_cast<int64_t>(x.nv) * rank / CS);
   const int g1 = static_cast<int>(static_cast<int64_t>(x.nv) * (rank + 1) / CS);
-  // The first round is on its way to the second-level cache before the token says that the row counts.  A row of
-  // padding costs its first round, so not for bf16 without alternatives, a training batch's case (rollouts with a quarter
-  // of padding 150.4 us, 152.0 so).  With alternatives 2048 rows of 128256 bf16 take 107.3 instead of 108.2 us, with a
-  // quarter of padding 86.8 and 89.3; 4096 rows of 32000 fp32 without alternatives 82 and 85, with a quarter 65.5
-  // either way, with half 48.4 and 45.4; 1024 of 128256 83 and 85.
-  if (kList || !kBF16) {
+  // The first round is on its way to the second-level cache before the token says that the row counts; a row of
+  // padding costs its first round (at most 20 KB a block), which is fetched but not looked at.  Graph replays with and
+  // without, us: rows of fp32 without alternatives, 4096 x 32000 79.1 and 84.1, 1024 x 128256 82.8 and 84.2, 333 x 50001
+  // 13.4 and 14.9; of bf16, 4096 x 151936 187.0 and 189.3, 2048 x 128256 87.8 and 89.2, 333 x 50001 13.1 and 13.6; with
+  // five alternatives 2048 x 128256 bf16 105.7 and 109.3, 2048 x 32000 fp32 54.0 and 58.8; 8192 x 5000 is the same to 1%.
+  // With a quarter of padding: 4096 x 151936 bf16 145.1 and 147.3 (as calls, other inputs each, 151.9 and 150.5), 4096 x
+  // 32000 fp32 65.7 and 64.8; with half 47.6 and 44.8, and 2048 x 128256 bf16 with five alternatives 66.0 and 67.5.
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int g = g0 + u * NT + static_cast<int>(threadIdx.x);
-      if (g < g1) asm volatile("prefetch.global.L2 [%0];" ::"l"(x.vec + g));
-    }
+  for (int u = 0; u < kU; ++u) {
+    const int g = g0 + u * NT + static_cast<int>(threadIdx.x);
+    if (g < g1) asm volatile("prefetch.global.L2 [%0];" ::"l"(x.vec + g));
   }
   const int64_t t = A.tokens[row];
   const float tau = row_tau(A.taus, A.tau, row);

@@ -377,7 +377,8 @@ kps_status kps_distill_loss_grad(const void* student, kps_dtype dt, int64_t N, i
  *
  *   logits  [N, V] (dt), rows ld apart
  *   tokens  [N] int64.  A token outside [0, V) marks an empty row (padding): its
- *           logits are not looked at.
+ *           logits do not enter anything (some may be fetched: they are the caller's
+ *           memory all the same).
  *   n       alternatives, 0..min(V, 1024)
  *   temperatures  [N] fp32, as kps_sample takes them, or NULL: `temperature` for
  *           every row, finite and > 0.  One that is no positive normal number
@@ -437,7 +438,7 @@ kps_status kps_token_logprobs_backward(const void* logits, kps_dtype dt, int64_t
  *   clip_low, clip_high >= 0 (infinity: no bound); kl_coef, entropy_coef finite
  *
  * A row whose token lies outside [0, V) or whose weight is 0 is empty: its logits
- * are not looked at, and loss, lp, H and gradient are 0.  The clipped branch has
+ * enter nothing, and loss, lp, H and gradient are 0.  The clipped branch has
  * no gradient where it is the smaller one (r > 1 + clip_high with A >= 0, r < 1 -
  * clip_low with A < 0).  A row without a distribution has NaN everywhere; ratios
  * and penalties that leave fp32 follow IEEE arithmetic.  out_grad must lie
