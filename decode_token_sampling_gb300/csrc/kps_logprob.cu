@@ -436,9 +436,9 @@ struct PolicyTerm {
   __device__ __forceinline__ PolicyTerm(const Grad& P, const PolicyRow& in, float logprob, float entropy) {
     const float A = in.A, w = in.w, r = expf(logprob - in.old);
     const float kept = fminf(fmaxf(r, 1.0f - P.lo), 1.0f + P.hi);
-    const bool clipped = A >= 0.0f ? r > 1.0f + P.hi : r < 1.0f - P.lo;
+    const bool clipped = A >= 0.0f ? r > 1.0f + P.hi : A < 0.0f && r < 1.0f - P.lo;  // (NaN: not)
     float v = 0.0f, d = 0.0f;
-    if (A != 0.0f) {  // (an infinite ratio times an advantage of 0 is 0)
+    if (A != 0.0f || isnan(r)) {  // (an infinite ratio times an advantage of 0 is 0; a NaN in either stays)
       v = -(clipped ? kept : r) * A;
       d = clipped ? 0.0f : -A * r;
     }
