@@ -455,25 +455,32 @@ struct PolicyTerm {
   }
 };
 
-// A row's gradient: e_v (A + B z_v) with e_v = 2^z_v, z_v = (x_v - m) c; the token's apart.
+// At temperatures below 2^-60 g / tau and h / tau may leave fp32 while the gradient does not: between equal logits, of
+// which there are up to 2^20, it is that part of them, and beside a certain token 0.  So a slope is held 2^-20 down
+// there, for g and h below 2^22 at least, and its elements are taken one at a time.  (At every temperature it would cost the
+// smallest gradients their last bits.)
+__device__ __forceinline__ bool is_tiny(float c) { return c > kLog2e * 0x1p60f; }
+__device__ __forceinline__ float slope_up(float c) { return is_tiny(c) ? 0x1p20f : 1.0f; }
+
+// A row's gradient: up e_v (A + B z_v) with e_v = 2^z_v, z_v = (x_v - m) c; the token's apart.
 struct Slope {
   float a, b, token;
   __device__ __forceinline__ Slope(float a_, float b_, float token_) : a(a_), b(b_), token(token_) {}
   __device__ __forceinline__ Slope(const Row& r, float x_token, float tau, float c, float g, float h) {
     const float inv = 1.0f / (1.0f + r.eps);
-    const float gt = g / tau, ht = h / tau;
+    const float down = is_tiny(c) ? 0x1p-20f : 1.0f, gt = g * down / tau, ht = h * down / tau;
     a = r.ok ? -(gt + ht * r.q) * inv : NAN;
     b = h == 0.0f ? 0.0f : -ht * kLn2 * inv;
     // the token's: 1 - p without the difference of two ones where it is the largest
     const float z = exponent(x_token, r.m, c), e = ex2(z);
     const float rest = z == 0.0f ? r.eps * inv : 1.0f - e * inv;
-    token = r.ok ? gt * rest + (h == 0.0f ? 0.0f : -ht * (e * inv) * (r.q + kLn2 * z)) : NAN;
+    token = r.ok ? (gt * rest + (h == 0.0f ? 0.0f : -ht * (e * inv) * (r.q + kLn2 * z))) * slope_up(c) : NAN;
   }
   __device__ __forceinline__ float at(float x, float m, float c) const {
     const float z = exponent(x, m, c), e = ex2(z);
-    return e == 0.0f ? 0.0f : e * fmaf(b, z, a);
+    return e == 0.0f ? 0.0f : e * fmaf(b, z, a) * slope_up(c);
   }
-  // Whether a + b z is finite for every z from kFloor on: at the smallest temperatures only at() is.
+  // Whether a + b z is finite for every z from kFloor on; else only at() is.
   __device__ __forceinline__ bool tame() const { return fabsf(a) < 0x1p110f && fabsf(b) < 0x1p110f; }
 };
 template <bool kBF16>
@@ -505,7 +512,7 @@ struct SlopeVec {
     n2 = pack2(n, n);
     a2 = pack2(a, a);
     b2 = pack2(s.b, s.b);
-    usable = s.tame();
+    usable = s.tame() && !is_tiny(c);
   }
   static __device__ __forceinline__ void put(uint32_t* out, int i, float p, float q) {
     if (kBF16) {
