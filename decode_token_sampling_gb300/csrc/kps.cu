@@ -123,7 +123,6 @@ kps_status kps_last_device_status(void* workspace, cudaStream_t stream, int* out
 // ------------------------------------------------------------------------------------------
 namespace kps {
 constexpr size_t kNoallocScratchBytes = 4096;
-constexpr int kMaxDevices = 64;
 // File-scope scratch for kps_sample_noalloc.  In host code this name is only a
 // stand-in for the symbol: its device address comes from cudaGetSymbolAddress.
 static __device__ __align__(256) unsigned char g_noalloc_scratch[kNoallocScratchBytes];

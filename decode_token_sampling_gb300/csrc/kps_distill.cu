@@ -48,7 +48,6 @@ struct Flight {
 constexpr int kMaxK = 1024;   // teacher slots a row may have (the framework's top-k limit)
 constexpr int64_t kMaxV = 1 << 20;
 constexpr int kMaxCS = 8;     // widest cluster (the portable limit)
-constexpr int kMaxDevices = 64;
 constexpr int kStats = 4;     // floats of statistics per row
 
 enum Mode { kForward = 0, kBackward = 1, kBoth = 2 };
@@ -947,28 +946,6 @@ __global__ void __launch_bounds__(kNT, 4) distill_resident_kernel(const Params P
 // ------------------------------------------------------------------------------------------
 // Host side
 // ------------------------------------------------------------------------------------------
-static int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return 0;
-  }
-  return n;
-}
-
-// Lets a kernel take as much dynamic shared memory as a block can have: the same for every call,
-// so that calls side by side do not undo each other's; once for each device.
-constexpr int kMaxDynamic = 224 * 1024;
-template <class Kernel>
-static bool allow_shared(Kernel* kernel, std::atomic<bool>* done) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
-  if (done[dev].load(std::memory_order_acquire)) return true;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic) != cudaSuccess) return false;
-  done[dev].store(true, std::memory_order_release);
-  return true;
-}
-
 template <bool kBF16, int kMode, bool kRest = true>
 static kps_status launch_t(const Params& P, cudaStream_t stream) {
   const int sms = sm_count();
@@ -979,10 +956,7 @@ static kps_status launch_t(const Params& P, cudaStream_t stream) {
   while (cs < kMaxCS && P.N * cs * 2 <= 2 * sms && P.V >= 2 * cs * round) cs *= 2;
   const Layout lay = make_layout(P.K, (P.V + cs - 1) / cs + 4 * (kBF16 ? 8 : 4), kMode != kBackward);
   static std::atomic<bool> done[kMaxDevices];
-  if (!allow_shared(distill_kernel<kBF16, kMode, kRest>, done)) {
-    (void)cudaGetLastError();
-    return KPS_ERR_CUDA;
-  }
+  if (!allow_shared(distill_kernel<kBF16, kMode, kRest>, done)) return KPS_ERR_CUDA;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(static_cast<unsigned>(P.N * cs));
   lc.blockDim = dim3(kNT);
@@ -1100,16 +1074,6 @@ static kps_status check(const void* student, kps_dtype dt, int64_t N, int64_t V,
 
 static bool float_aligned(const void* p) { return reinterpret_cast<uintptr_t>(p) % alignof(float) == 0; }
 
-// A gradient buffer of its own: rows of at least V elements, sharing no byte with the student's rows.
-static kps_status check_grad(const Params& P, kps_dtype dt, void* grad, int64_t ld_grad) {
-  const uintptr_t esize = dt == KPS_BF16 ? 2 : 4;
-  if (!grad || reinterpret_cast<uintptr_t>(grad) % esize || (P.N > 1 && ld_grad < P.V)) return KPS_ERR_INVALID_ARG;
-  const uintptr_t a = reinterpret_cast<uintptr_t>(P.student), b = reinterpret_cast<uintptr_t>(grad);
-  const uintptr_t an = ((P.N - 1) * P.ld + P.V) * esize, bn = ((P.N - 1) * ld_grad + P.V) * esize;
-  if (a < b + bn && b < a + an) return KPS_ERR_INVALID_ARG;
-  return KPS_OK;
-}
-
 }  // namespace distill
 }  // namespace kps
 
@@ -1138,7 +1102,7 @@ kps_status kps_distill_backward(const void* student, kps_dtype dt, int64_t N, in
   kps_status st = kps::distill::check(student, dt, N, V, ld, ids, values, values_dt, K, rest, weight, temperature, &P);
   if (st != KPS_OK || N == 0) return st;
   if (!stats || !kps::distill::float_aligned(stats) || !kps::distill::float_aligned(grad_loss)) return KPS_ERR_INVALID_ARG;
-  if ((st = kps::distill::check_grad(P, dt, out_grad, ld_grad)) != KPS_OK) return st;
+  if ((st = kps::check_grad(student, N, V, ld, dt, out_grad, ld_grad)) != KPS_OK) return st;
   P.upstream = grad_loss;
   P.stats = const_cast<float*>(stats);
   P.grad = out_grad;
@@ -1155,7 +1119,7 @@ kps_status kps_distill_loss_grad(const void* student, kps_dtype dt, int64_t N, i
   kps_status st = kps::distill::check(student, dt, N, V, ld, ids, values, values_dt, K, rest, weight, temperature, &P);
   if (st != KPS_OK || N == 0) return st;
   if (!out_loss || !kps::distill::float_aligned(out_loss)) return KPS_ERR_INVALID_ARG;
-  if ((st = kps::distill::check_grad(P, dt, out_grad, ld_grad)) != KPS_OK) return st;
+  if ((st = kps::check_grad(student, N, V, ld, dt, out_grad, ld_grad)) != KPS_OK) return st;
   P.loss = out_loss;
   P.grad = out_grad;
   P.ld_grad = ld_grad;

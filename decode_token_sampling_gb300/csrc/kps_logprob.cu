@@ -820,12 +820,6 @@ __global__ void __launch_bounds__(kNT, 5) policy_kernel(const Grad P, const int 
 // ------------------------------------------------------------------------------------------
 // Host side
 // ------------------------------------------------------------------------------------------
-static int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) return n;
-  (void)cudaGetLastError();
-  return 0;
-}
 // Launches a kernel with a cluster of cs CTAs a row.
 template <int NT = kNT, class... Params, class... Values>
 static kps_status launch_clusters(void (*kernel)(Params...), int64_t N, int cs, size_t shared, cudaStream_t stream, const Values&... values) {
@@ -853,7 +847,7 @@ template <class P>
 static kps_status launch_rows(void (*kernel)(P), const Args& a, kps_dtype dt, int fill, int sms, const P& params, cudaStream_t stream) {
   int cs = 1;
   const int64_t round = static_cast<int64_t>(kNT) * 4 * (dt == KPS_BF16 ? 8 : 4);
-    while (cs < kMaxCS && (fill == 0 || a.N * cs * 2 <= static_cast<int64_t>(fill) * sms) && a.V >= 2 * cs * round) cs *= 2;
+  while (cs < kMaxCS && (fill == 0 || a.N * cs * 2 <= static_cast<int64_t>(fill) * sms) && a.V >= 2 * cs * round) cs *= 2;
   return launch_clusters(kernel, a.N, cs, 0, stream, params);
 }
 // Scoring.  Many short rows go to blocks of 128 threads, twice as many an SM, as a block spends some 3.5 us on
@@ -889,8 +883,6 @@ static kps_status launch_slope(const Grad& P, kps_dtype dt, cudaStream_t stream)
 
 // The policy loss: with the row in shared memory where a cluster's holds it (up to 1.8 MB); longer rows
 // are read twice, in two launches, and their statistics lie where the second leaves the results.
-constexpr int kMaxDynamic = 224 * 1024;
-constexpr int kMaxDevices = 64;
 template <bool kBF16>
 static kps_status launch_policy(const Grad& P, cudaStream_t stream) {
   constexpr int G = kBF16 ? 8 : 4;
@@ -914,18 +906,8 @@ static kps_status launch_policy(const Grad& P, cudaStream_t stream) {
     const kps_status st = launch_score(a, dt, stream);
     return st != KPS_OK ? st : launch_slope<true>(two, dt, stream);
   }
-  // as much dynamic shared memory as a block can have, once for each device: the same for every call,
-  // so that calls side by side do not undo each other's
   static std::atomic<bool> done[kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return KPS_ERR_CUDA;
-  if (!done[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(policy_kernel<kBF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return KPS_ERR_CUDA;
-    }
-    done[dev].store(true, std::memory_order_release);
-  }
+  if (!allow_shared(policy_kernel<kBF16>, done)) return KPS_ERR_CUDA;
   return launch_clusters(policy_kernel<kBF16>, P.a.N, cs, total, stream, P, share);
 }
 
@@ -949,15 +931,6 @@ static kps_status check(const void* logits, kps_dtype dt, int64_t N, int64_t V, 
   a->taus = temperatures;
   a->tokens = tokens;
   return KPS_OK;
-}
-
-// A gradient buffer of its own: rows of at least V elements, sharing no byte with the logits' rows.
-static kps_status check_grad(const Args& a, kps_dtype dt, void* grad, int64_t ld_grad) {
-  const uintptr_t esize = dt == KPS_BF16 ? 2 : 4;
-  if (!grad || misaligned(grad, esize) || (a.N > 1 && ld_grad < a.V)) return KPS_ERR_INVALID_ARG;
-  const uintptr_t p = reinterpret_cast<uintptr_t>(a.x), q = reinterpret_cast<uintptr_t>(grad);
-  const uintptr_t pn = ((a.N - 1) * a.ld + a.V) * esize, qn = ((a.N - 1) * ld_grad + a.V) * esize;
-  return p < q + qn && q < p + pn ? KPS_ERR_INVALID_ARG : KPS_OK;
 }
 
 }  // namespace score
@@ -1006,7 +979,7 @@ kps_status kps_token_logprobs_backward(const void* logits, kps_dtype dt, int64_t
   if (st != KPS_OK || N == 0) return st;
   if (!stats || ks::misaligned(stats, 4) || ks::misaligned(grad_logprob, 4) || ks::misaligned(grad_entropy, 4))
     return KPS_ERR_INVALID_ARG;
-  if ((st = ks::check_grad(P.a, dt, out_grad, ld_grad)) != KPS_OK) return st;
+  if ((st = kps::check_grad(logits, N, V, ld, dt, out_grad, ld_grad)) != KPS_OK) return st;
   P.a.max = const_cast<float*>(stats);
   P.a.eps = P.a.max + N;
   P.a.q = P.a.max + 2 * N;
@@ -1036,7 +1009,7 @@ kps_status kps_policy_loss_grad(const void* logits, kps_dtype dt, int64_t N, int
                         static_cast<const void*>(out_loss), static_cast<const void*>(out_logprob),
                         static_cast<const void*>(out_entropy)})
     if (ks::misaligned(p, 4)) return KPS_ERR_INVALID_ARG;
-  if ((st = ks::check_grad(P.a, dt, out_grad, ld_grad)) != KPS_OK) return st;
+  if ((st = kps::check_grad(logits, N, V, ld, dt, out_grad, ld_grad)) != KPS_OK) return st;
   P.a.weight = weight;
   P.old = old_logprob;
   P.advantage = advantage;
