@@ -50,13 +50,16 @@ __device__ __forceinline__ float warp_top(float x) { return kfloat(__reduce_max_
 // lies in the kept rounds, or (the other value reaches it too: a thread in some rows) in vectors that are
 // read once more: little more than n elements, ranked pairwise.  2048 rows of 128256 bf16 take 106 us with five
 // alternatives, 109 with twenty, 88 without (79 at the copy rate): a block's end takes some 7 us, the last sums and
-// the ranking in a chain that five blocks an SM do not hide.  Slower (when it took 111 and 112): every vector above a
-// rising bound listed during the pass (139), the kept round read again instead of kept (118 and 127), all vectors of
+// the ranking in a chain that five blocks an SM do not hide.  The 48 registers that these leave a thread do not hold the
+// pass with the kept round: 20 to 28 bytes a thread are stored to local memory and 52 to 60 loaded, up to 44 and 92 in
+// first_equal, which few rows call (blocks of 512 threads have 64 registers and keep all there).  Slower (when it took
+// 111 and 112): every vector above a rising bound listed during the pass (139), the kept round read again instead of kept (118 and 127), all vectors of
 // those threads read again (108 and 147), the largest vector of each of a thread's five streams kept (131).
 //
 // 4096 rows of 151936 bf16, a quarter of them empty, without alternatives: 147 us (140 at the copy rate) with
 // five loads in flight and five CTAs an SM; six and four 153, four and five 151, eight and four 153, eight and
-// three 165; four and six 147, but 16.4 instead of 15.0 us for 333 rows of 50001 fp32, whose CTAs are few.
+// three 165; four and six 147, but 16.4 instead of 15.0 us for 333 rows of 50001 fp32, whose CTAs are few
+// (13.4 with the first round fetched ahead).
 // Rounds that all look where the row ends took 160 with six and four.  Blocks that go on to rows of blocks not yet
 // started (cluster launch control), their warps independent of each other: 165, for the registers that it takes and
 // the wait for the next row's number behind empty ones.
@@ -66,7 +69,10 @@ template <int NT>
 constexpr int kLoads = NT == 512 ? 4 : 5;
 template <int NT>
 constexpr int kWidest = NT == 256 ? kMaxCS : 1;
-constexpr int kFew = 32;     // alternatives
+// The alternatives that the kept rounds do for; more go to the top logits' kernel.  2048 rows of 128256 bf16: 32 take 124
+// us, 33 there 133, 64 140, 128 149, 129 (its larger lists, two CTAs an SM instead of four) 201, 256 221, 1000 302; 256
+// rows of 151936 bf16 29, 32, 34 with 32, 33, 64, and 38 with 256.
+constexpr int kFew = 32;
 constexpr int kWords = 512;  // elements that are ranked
 template <bool kList, int NT>
 struct Few {
@@ -547,7 +553,7 @@ struct SlopeVec {
   }
 };
 
-// 2048 rows of 128256 bf16, a quarter of them empty: 134 us (138 at the copy rate) in up to eight CTAs a row, with
+// 2048 rows of 128256 bf16, a quarter of them empty: 135 us (138 at the copy rate) in up to eight CTAs a row, with
 // four loads in flight and six CTAs an SM; six and four 147, three and eight 138, two and eight 136; six and four
 // with one CTA a row 141.  333 rows of 50001 fp32: 21.9 us, and 24.0, 21.9, 22.7, 23.3.
 template <bool kBF16, bool kPolicy>
@@ -641,7 +647,8 @@ __global__ void __launch_bounds__(kNT, 6) slope_kernel(const Grad P) {
 // The row is read once, by a bulk copy into the shared memory of each of a cluster's CTAs, summed
 // there against the CTA's largest logit, turned into the gradient in place and copied out.
 // Bytes of a row per CTA, where the cluster allows: five CTAs an SM (48 registers).  4096 rows of 151936 bf16
-// with a quarter empty take 363 us (326 at the copy rate), 2048 of 128256 179 (157); with 52 KB and four CTAs 371
+// with a quarter empty take 366 us (326 at the copy rate), 2048 of 128256 181 (157); 363 and 179 before
+// the smallest temperatures had a scale of their own; with 52 KB and four CTAs 371
 // and 184, with 62 KB and three 427 and 224 at the time.  Loops unrolled more than twice cost 2% (instructions
 // are fetched anew by every block), parts copied in and out in two slices 1%, in four 5%.
 constexpr int kChunkBytes = 43 * 1024;
@@ -851,8 +858,8 @@ static kps_status launch_rows(void (*kernel)(P), const Args& a, kps_dtype dt, in
   return launch_clusters(kernel, a.N, cs, 0, stream, params);
 }
 // Scoring.  Many short rows go to blocks of 128 threads, twice as many an SM, as a block spends some 3.5 us on
-// its start and its end whatever its row is (8192 rows of 5000 bf16: 27.8 us, 44.5 with 256 threads; with five
-// alternatives 55 and 85; 2048 of 32000 bf16 30.9 and 33.7).  Rows above 64 KB are faster with 256 (2048 of
+// its start and its end whatever its row is (8192 rows of 5000 bf16: 29.6 us; 27.8 and, with 256
+// threads, 44.5 when they were compared; with five alternatives 55 and 85; 2048 of 32000 bf16 30.9 and 33.7).  Rows above 64 KB are faster with 256 (2048 of
 // 32000 fp32 with five alternatives 62 and 58.6, of 128256 bf16 125 and 109).  With alternatives, one or two long
 // rows an SM go to blocks of 512 (256 of 151936 bf16, twenty alternatives: 26.5 us, 29.2 with 256 threads; 300 of 128256
 // 24.2 and 27.0; 200 of 50001 fp32 16.2 and 17.8): clusters of two of 256 take 28.7, 26.7 and 16.3.

@@ -535,11 +535,11 @@ __global__ void __launch_bounds__(kNT, kSmall ? 4 : 2) top_kernel(const Params P
 // ------------------------------------------------------------------------------------------
 template <bool kBF16, bool kSmall, bool kScore>
 static kps_status launch_t(const Params& P, cudaStream_t stream) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      (sizeof(Smem<kSmall, kScore>) > 48 * 1024 &&
-       cudaFuncSetAttribute(top_kernel<kBF16, kSmall, kScore>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem<kSmall, kScore>)) !=
-           cudaSuccess)) {
+  const int sms = sm_count();
+  if (!sms) return KPS_ERR_CUDA;
+  if (sizeof(Smem<kSmall, kScore>) > 48 * 1024 &&
+      cudaFuncSetAttribute(top_kernel<kBF16, kSmall, kScore>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem<kSmall, kScore>)) !=
+          cudaSuccess) {
     (void)cudaGetLastError();
     return KPS_ERR_CUDA;
   }
