@@ -381,8 +381,9 @@ kps_status kps_distill_loss_grad(const void* student, kps_dtype dt, int64_t N, i
  *           memory all the same).
  *   n       alternatives, 0..min(V, 1024)
  *   temperatures  [N] fp32, as kps_sample takes them, or NULL: `temperature` for
- *           every row, finite and > 0.  One that is no positive normal number
- *           (kps_sample's greedy rows) counts as 1.
+ *           every row, finite and above 4.3e-39 (log2(e) over it is finite).  One of
+ *           the rows' that is no positive normal number (kps_sample's greedy rows)
+ *           counts as 1.
  *
  * With a = x / temperature and p = softmax(a) over the row:
  *
@@ -441,8 +442,8 @@ kps_status kps_token_logprobs_backward(const void* logits, kps_dtype dt, int64_t
  * enter nothing, and loss, lp, H and gradient are 0.  The clipped branch has
  * no gradient where it is the smaller one (r > 1 + clip_high with A >= 0, r < 1 -
  * clip_low with A < 0).  A row without a distribution has NaN everywhere, and so
- * has one whose advantage, old_logprob or (with a penalty) ref_logprob is NaN, in
- * its loss and gradient.  Ratios and penalties that leave fp32 follow IEEE
+ * has one whose advantage, old_logprob, weight or (with a penalty) ref_logprob is
+ * NaN, in its loss and, where p is not 0, its gradient.  Ratios and penalties that leave fp32 follow IEEE
  * arithmetic, but that an infinite ratio times an advantage of 0 is 0.  out_grad
  * must lie outside the logits; the outputs must not overlap each other or the
  * inputs.

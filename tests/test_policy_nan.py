@@ -57,3 +57,22 @@ def test_nan_of_the_reference_policy(V):
     want = torch.arange(10, device="cuda") == 3
     assert torch.equal(torch.isnan(got.loss), want) and torch.equal(torch.isnan(got.grad).all(1), want)
     assert torch.equal(torch.isnan(got.grad).any(1), want)
+
+
+@gpu
+@pytest.mark.parametrize("V", [50, 5003, 500001])
+def test_nan_weights_and_masked_tokens(V):
+    """A NaN weight is not 0: its row is read.  A token of probability 0 has a gradient of 0 whatever the loss."""
+    import decode_token_sampling_gb300 as kps
+    x, tokens, old, A, weight, _ = _rows(torch.float32, V)
+    x[:, V // 2:] = -math.inf
+    tokens %= V // 2
+    lp = kps.token_logprobs(x, tokens).logprob
+    A, weight = torch.ones_like(A), torch.ones_like(weight)
+    weight[2] = NAN
+    A[5] = NAN
+    nan = torch.tensor([i in (2, 5) for i in range(10)], device="cuda")
+    got = kps.policy_loss_grad(x, tokens, lp, A, weight=weight, entropy_coef=0.1)
+    assert torch.equal(torch.isnan(got.loss), nan)
+    assert torch.equal(torch.isnan(got.grad[:, :V // 2]).all(1), nan) and torch.equal(torch.isnan(got.grad).any(1), nan)
+    assert bool((got.grad[:, V // 2:] == 0).all())
