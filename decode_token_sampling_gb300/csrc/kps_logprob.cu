@@ -463,28 +463,28 @@ struct PolicyTerm {
 
 // At temperatures below 2^-60 g / tau and h / tau may leave fp32 while the gradient does not: between equal logits, of
 // which there are up to 2^20, it is that part of them, and beside a certain token 0.  So a slope is held 2^-20 down
-// there, for g and h below 2^22 at least, and its elements are taken one at a time.  (At every temperature it would cost the
-// smallest gradients their last bits.)
+// there, for g and h below 2^22 at least, and its elements are taken one at a time and brought up by whoever writes them.
+// (At every temperature it would cost the smallest gradients their last bits.)
 __device__ __forceinline__ bool is_tiny(float c) { return c > kLog2e * 0x1p60f; }
 __device__ __forceinline__ float slope_up(float c) { return is_tiny(c) ? 0x1p20f : 1.0f; }
 
-// A row's gradient: up e_v (A + B z_v) with e_v = 2^z_v, z_v = (x_v - m) c; the token's apart.
+// A row's gradient over slope_up: e_v (A + B z_v) with e_v = 2^z_v, z_v = (x_v - m) c; the token's apart.
 struct Slope {
   float a, b, token;
   __device__ __forceinline__ Slope(float a_, float b_, float token_) : a(a_), b(b_), token(token_) {}
   __device__ __forceinline__ Slope(const Row& r, float x_token, float tau, float c, float g, float h) {
     const float inv = 1.0f / (1.0f + r.eps);
-    const float down = is_tiny(c) ? 0x1p-20f : 1.0f, gt = g * down / tau, ht = h * down / tau;
+    const float by = tau * slope_up(c), gt = g / by, ht = h / by;
     a = r.ok ? -(gt + ht * r.q) * inv : NAN;
     b = h == 0.0f ? 0.0f : -ht * kLn2 * inv;
     // the token's: 1 - p without the difference of two ones where it is the largest
     const float z = exponent(x_token, r.m, c), e = ex2(z);
     const float rest = z == 0.0f ? r.eps * inv : 1.0f - e * inv;
-    token = r.ok ? (gt * rest + (h == 0.0f ? 0.0f : -ht * (e * inv) * (r.q + kLn2 * z))) * slope_up(c) : NAN;
+    token = r.ok ? gt * rest + (h == 0.0f ? 0.0f : -ht * (e * inv) * (r.q + kLn2 * z)) : NAN;
   }
   __device__ __forceinline__ float at(float x, float m, float c) const {
     const float z = exponent(x, m, c), e = ex2(z);
-    return e == 0.0f ? 0.0f : e * fmaf(b, z, a) * slope_up(c);
+    return e == 0.0f ? 0.0f : fmaf(b, z, a) * e;
   }
   // Whether a + b z is finite for every z from kFloor on; else only at() is.
   __device__ __forceinline__ bool tame() const { return fabsf(a) < 0x1p110f && fabsf(b) < 0x1p110f; }
@@ -553,7 +553,7 @@ struct SlopeVec {
   }
 };
 
-// 2048 rows of 128256 bf16, a quarter of them empty: 135 us (138 at the copy rate) in up to eight CTAs a row, with
+// 2048 rows of 128256 bf16, a quarter of them empty: 134 us (138 at the copy rate) in up to eight CTAs a row, with
 // four loads in flight and six CTAs an SM; six and four 147, three and eight 138, two and eight 136; six and four
 // with one CTA a row 141.  333 rows of 50001 fp32: 21.9 us, and 24.0, 21.9, 22.7, 23.3.
 template <bool kBF16, bool kPolicy>
@@ -630,13 +630,13 @@ __global__ void __launch_bounds__(kNT, 6) slope_kernel(const Grad P) {
     else pass(std::false_type{});
     if (static_cast<int>(threadIdx.x) < x.loose()) {
       const int v = x.loose_at(threadIdx.x);
-      if ((v < x.head) ? rank == 0 : rank == CS - 1) put_elem<kBF16>(obase, v, v == t ? slope.token : slope.at(x.at(v), r.m, c));
+      if ((v < x.head) ? rank == 0 : rank == CS - 1) put_elem<kBF16>(obase, v, slope_up(c) * (v == t ? slope.token : slope.at(x.at(v), r.m, c)));
     }
   } else {
     // the two rows do not share their 16-byte boundaries, or the numbers are extreme: one element at a time
     const int v0 = rank == 0 ? 0 : x.head + g0 * G, v1 = rank == CS - 1 ? A.V : x.head + g1 * G;
     for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kNT)
-      put_elem<kBF16>(obase, v, v == t ? slope.token : slope.at(x.at(v), r.m, c));
+      put_elem<kBF16>(obase, v, slope_up(c) * (v == t ? slope.token : slope.at(x.at(v), r.m, c)));
   }
 }
 
@@ -647,8 +647,7 @@ __global__ void __launch_bounds__(kNT, 6) slope_kernel(const Grad P) {
 // The row is read once, by a bulk copy into the shared memory of each of a cluster's CTAs, summed
 // there against the CTA's largest logit, turned into the gradient in place and copied out.
 // Bytes of a row per CTA, where the cluster allows: five CTAs an SM (48 registers).  4096 rows of 151936 bf16
-// with a quarter empty take 366 us (326 at the copy rate), 2048 of 128256 181 (157); 363 and 179 before
-// the smallest temperatures had a scale of their own; with 52 KB and four CTAs 371
+// with a quarter empty take 365 us (326 at the copy rate), 2048 of 128256 180 (157); with 52 KB and four CTAs 371
 // and 184, with 62 KB and three 427 and 224 at the time.  Loops unrolled more than twice cost 2% (instructions
 // are fetched anew by every block), parts copied in and out in two slices 1%, in four 5%.
 constexpr int kChunkBytes = 43 * 1024;
@@ -814,13 +813,15 @@ __global__ void __launch_bounds__(kNT, 5) policy_kernel(const Grad P, const int 
     __syncthreads();
     if (threadIdx.x == 0 && g1 > g0) copy_out(const_cast<uint4*>(o.vec) + g0, smem, static_cast<uint32_t>(g1 - g0) * 16u);
   } else {
-    // the two rows do not share their 16-byte boundaries, or the numbers are extreme: one element at a time
+    // the two rows do not share their 16-byte boundaries, or the numbers are extreme: one element at a time (unrolled,
+    // its instructions cost every block 0.4%)
+#pragma unroll 1
     for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kNT) {
       const float y = kBF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(smem)[v - v0]) : reinterpret_cast<const float*>(smem)[v - v0];
-      put_elem<kBF16>(obase, v, v == t ? slope.token : slope.at(y, m, c));
+      put_elem<kBF16>(obase, v, slope_up(c) * (v == t ? slope.token : slope.at(y, m, c)));
     }
   }
-  if (has_loose) put_elem<kBF16>(obase, loose_v, loose_v == t ? slope.token : slope.at(x.at(loose_v), m, c));
+  if (has_loose) put_elem<kBF16>(obase, loose_v, slope_up(c) * (loose_v == t ? slope.token : slope.at(x.at(loose_v), m, c)));
   if (late) copy_landed(&landed);  // one more wait before the block leaves
 }
 
