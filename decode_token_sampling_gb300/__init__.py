@@ -659,7 +659,8 @@ def _token_logprobs_grad(ctx, grad_logprob, grad_entropy):
     h = None if grad_entropy is None else grad_entropy.contiguous()
     N, V = ctx.shape
     device = logits.device
-    if V > 1 and logits.stride(1) != 1 or N > 1 and logits.stride(0) < V or device.index != torch.cuda.current_device():
+    if (not logits.is_cuda or V > 1 and logits.stride(1) != 1 or N > 1 and logits.stride(0) < V or
+            device.index != torch.cuda.current_device()):
         temperature = ctx.temperature if temperatures is None else temperatures
         return token_logprobs_backward(g, h, logits, tokens, stats, temperature=temperature)
     # Autograd has checked the gradients; hooks may have given back other tensors than those that were saved.  (The call

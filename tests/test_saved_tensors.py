@@ -73,6 +73,29 @@ def test_changed_tensors_never_reach_the_library(which, change, library):
     assert [name for name, _ in library.calls] == ["kps_token_logprobs"]
 
 
+def test_logits_in_host_memory_never_reach_it(library, monkeypatch):
+    """Wherever they say that they lie: a device index alone is no CUDA device."""
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda self: not self.__dict__.get("host")), raising=False)
+
+    def host(t):
+        t = t.clone()
+        t.host = True
+        return t
+
+    x = torch.randn(4, 10).requires_grad_()
+    t = kps.token_logprobs(x, torch.zeros(4, dtype=torch.int64))
+    ctx = t.logprob.grad_fn
+    saved = ctx.saved_tensors
+
+    class Context:
+        saved_tensors = (host(saved[0].detach()), *saved[1:])
+        dtype, shape, temperature = ctx.dtype, ctx.shape, ctx.temperature
+
+    with pytest.raises(ValueError, match="CUDA"):
+        kps._token_logprobs_grad(Context, torch.ones(4), None)
+    assert [name for name, _ in library.calls] == ["kps_token_logprobs"]
+
+
 def test_tensors_as_they_were_saved_reach_it(library):
     _recorded("cpu", lambda t: t, 0)
     _recorded("cpu", lambda t: t.clone(), 0)
