@@ -53,8 +53,9 @@ __device__ __forceinline__ float warp_top(float x) { return kfloat(__reduce_max_
 // the ranking in a chain that five blocks an SM do not hide.  The 48 registers that these leave a thread do not hold the
 // pass with the kept round: 20 to 28 bytes a thread are stored to local memory and 52 to 60 loaded, up to 44 and 92 in
 // first_equal, which few rows call (blocks of 512 threads have 64 registers and keep all there).  Slower (when it took
-// 111 and 112): every vector above a rising bound listed during the pass (139), the kept round read again instead of kept (118 and 127), all vectors of
-// those threads read again (108 and 147), the largest vector of each of a thread's five streams kept (131).
+// 111 and 112): every vector above a rising bound listed during the pass (139), the kept round read again instead of kept
+// (118 and 127), all vectors of those threads read again (108 and 147), the largest vector of each of a thread's five
+// streams kept (131).
 //
 // 4096 rows of 151936 bf16, a quarter of them empty, without alternatives: 147 us (140 at the copy rate) with
 // five loads in flight and five CTAs an SM; six and four 153, four and five 151, eight and four 153, eight and
@@ -859,11 +860,11 @@ static kps_status launch_rows(void (*kernel)(P), const Args& a, kps_dtype dt, in
   return launch_clusters(kernel, a.N, cs, 0, stream, params);
 }
 // Scoring.  Many short rows go to blocks of 128 threads, twice as many an SM, as a block spends some 3.5 us on
-// its start and its end whatever its row is (8192 rows of 5000 bf16: 29.6 us; 27.8 and, with 256
-// threads, 44.5 when they were compared; with five alternatives 55 and 85; 2048 of 32000 bf16 30.9 and 33.7).  Rows above 64 KB are faster with 256 (2048 of
-// 32000 fp32 with five alternatives 62 and 58.6, of 128256 bf16 125 and 109).  With alternatives, one or two long
-// rows an SM go to blocks of 512 (256 of 151936 bf16, twenty alternatives: 26.5 us, 29.2 with 256 threads; 300 of 128256
-// 24.2 and 27.0; 200 of 50001 fp32 16.2 and 17.8): clusters of two of 256 take 28.7, 26.7 and 16.3.
+// its start and its end whatever its row is (8192 rows of 5000 bf16: 29.6 us; 27.8 and, with 256 threads, 44.5 when they
+// were compared; with five alternatives 55 and 85; 2048 of 32000 bf16 30.9 and 33.7).  Rows above 64 KB are faster with
+// 256 (2048 of 32000 fp32 with five alternatives 62 and 58.6, of 128256 bf16 125 and 109).  With alternatives, one or
+// two long rows an SM go to blocks of 512 (256 of 151936 bf16, twenty alternatives: 26.5 us, 29.2 with 256 threads; 300
+// of 128256 24.2 and 27.0; 200 of 50001 fp32 16.2 and 17.8): clusters of two of 256 take 28.7, 26.7 and 16.3.
 constexpr int kShortBytes = 64 * 1024, kShortThreads = 128, kLongThreads = 512;
 static kps_status launch_score(const Args& a, kps_dtype dt, cudaStream_t stream) {
   if (a.n > kFew) return launch_alternatives(a, dt, stream);

@@ -443,10 +443,10 @@ kps_status kps_token_logprobs_backward(const void* logits, kps_dtype dt, int64_t
  * no gradient where it is the smaller one (r > 1 + clip_high with A >= 0, r < 1 -
  * clip_low with A < 0).  A row without a distribution has NaN everywhere, and so
  * has one whose advantage, old_logprob, weight or (with a penalty) ref_logprob is
- * NaN, in its loss and, where p is not 0, its gradient.  Ratios and penalties that leave fp32 follow IEEE
- * arithmetic, but that an infinite ratio times an advantage of 0 is 0.  out_grad
- * must lie outside the logits; the outputs must not overlap each other or the
- * inputs.
+ * NaN, in its loss and, where p is not 0, its gradient.  Ratios and penalties that
+ * leave fp32 follow IEEE arithmetic, but that an infinite ratio times an advantage
+ * of 0 is 0.  out_grad must lie outside the logits; the outputs must not overlap
+ * each other or the inputs.
  */
 kps_status kps_policy_loss_grad(const void* logits, kps_dtype dt, int64_t N, int64_t V, int64_t ld, const int64_t* tokens,
                                 float temperature, const float* temperatures, const float* old_logprob,
